@@ -379,6 +379,65 @@ KDA_API kda_status kda_short_conv_bwd(int64_t n_tok, int C, int dtype, int activ
                    const int32_t* cu_seqlens, int n_docs, const void* x, const float* w, const void* dy,
                    void* dx, float* dw, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* Linear attention with one decay per head (no delta rule, no gate input):
+ * per document and head, tokens in order, a = exp(A_log[h]),
+ *   S_t = exp(-a) S_{t-1} + k_t v_t^T,    o_t = scale S_t^T q_t
+ * q and k enter as they are (no L2 norm).  Sizes, layouts, dtypes, documents
+ * (rows or cu_seqlens), h0 / h_final and statuses are those of kda_fwd; the
+ * problem's gate must be KDA_GATE_CHANNEL (it is not used).  A_log : [H] fp32;
+ * A_log = -inf is no decay.  Inputs are finite: a chunk's pairs are formed as
+ * matrix products, so an infinity or NaN at one token also reaches its
+ * document's other tokens, up to 63 before it (never another document's).
+ * The workspace (kda_linear_workspace_size(p, for_backward) bytes, 256-byte
+ * aligned) holds the error word (kda_device_status), the table of the packed
+ * documents' units and the states of a long document's segments; with
+ * save_for_backward = 1 it must be passed to kda_linear_bwd unmodified, with
+ * the same inputs.  Documents longer than about the tokens that one of two
+ * chains per SM would get are cut into segments whose states are formed in
+ * parallel and folded onto h0 (the segment length depends on B * T, H, dv and
+ * the dtype: a document's last bits can differ between batches of other
+ * sizes). */
+KDA_API size_t kda_linear_workspace_size(const kda_problem* p, int for_backward);
+KDA_API kda_status kda_linear_fwd(const kda_problem* p, const void* q, const void* k, const void* v,
+                   const float* A_log, const float* h0, void* o, float* h_final,
+                   int save_for_backward, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Backward of sum(o * dO) + sum(h_final * dh_final) for kda_linear_fwd with
+ * save_for_backward = 1 (another workspace is refused by the device:
+ * KDA_ERR_WORKSPACE from kda_device_status).  Writes dq, dk, dv (dtype),
+ * dA_log [H] and dh0 (fp32; either may be NULL: not returned; without dA_log
+ * its extra products are skipped).  Sums run in a fixed order: deterministic.
+ * The workspace may be used by several backwards of one forward, one at a
+ * time. */
+KDA_API kda_status kda_linear_bwd(const kda_problem* p, const void* q, const void* k, const void* v,
+                   const float* A_log, const float* h0, const void* dO, const float* dh_final,
+                   void* dq, void* dk, void* dv, float* dA_log, float* dh0,
+                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Single-token step of kda_linear_fwd for n_seq sequences, states in place:
+ * q, k : [n_seq, H, dk], v, o : [n_seq, H, dv] in dtype, A_log [H] fp32, state
+ * [n_seq, H, dk, dv] fp32.  Arguments, limits and statuses as kda_decode. */
+KDA_API kda_status kda_linear_decode(int n_seq, int H, int dk, int dv, int dtype, float scale,
+                   const void* q, const void* k, const void* v, const float* A_log, float* state, void* o,
+                   cudaStream_t stream);
+
+/* Layer norm of n_rows rows of D values (any D from 1 to 2^24):
+ *   mu = mean_j x_j,  r = 1 / sqrt(mean_j (x_j - mu)^2 + eps),
+ *   y_j = (x_j - mu) r w_j + bias_j
+ * x, y, dy, dx : [n_rows, D] contiguous in dtype (KDA_BF16 or KDA_F32); w, bias,
+ * dw, dbias : [D] fp32 (bias and dbias may be NULL); mean, rstd : [n_rows] fp32,
+ * written by the forward for the backward (both NULL: not wanted).  eps <= 0
+ * selects 1e-6.  Device pointers, 16-byte aligned.  The backward overwrites dx,
+ * dw and dbias; its scratch (per-CTA partials of dw and dbias, summed in a
+ * fixed order) is kda_layer_norm_workspace_size(n_rows, D, dtype) bytes (0 for
+ * invalid sizes). */
+KDA_API size_t kda_layer_norm_workspace_size(int64_t n_rows, int D, int dtype);
+KDA_API kda_status kda_layer_norm_fwd(int64_t n_rows, int D, int dtype, float eps, const void* x, const float* w,
+                   const float* bias, void* y, float* mean, float* rstd, cudaStream_t stream);
+KDA_API kda_status kda_layer_norm_bwd(int64_t n_rows, int D, int dtype, const void* x, const float* w,
+                   const void* dy, const float* mean, const float* rstd, void* dx, float* dw, float* dbias,
+                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

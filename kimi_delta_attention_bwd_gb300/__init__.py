@@ -15,6 +15,12 @@ libkda_gb300.so through its C ABI, include/kda.h):
   do, dgate, dweight = kda_norm_gate_backward(o, gate, weight, dy)
   o = kda_attention(q, k, v, f, b, A_log, dt_bias)             # the same as a torch.autograd op
   x = short_conv(x_raw, conv_w); y = gated_norm(o, gate, weight)  # likewise
+  o, h_final, ctx = kda_linear_forward(q, k, v, A_log, ...)    # linear attention, one decay per head
+  grads = kda_linear_backward(ctx, dO, dh_final=None)          # dq, dk, dv, dA_log, dh0
+  o = kda_linear_decode_step(q, k, v, A_log, state)            # one token, state in place
+  y = kda_layer_norm(x, weight, bias)                          # layer norm over the last axis
+  dx, dw, db = kda_layer_norm_backward(x, weight, dy, mean, rstd)
+  o = linear_attention(q, k, v, A_log); y = layer_norm(x, weight, bias)  # as torch.autograd ops
 
 Layouts: q, k, f [B, T, H, dk]; v [B, T, H, dv]; b [B, T, H] (bf16 or fp32);
 A_log [H], dt_bias [H, dk] fp32 (scalar-gated variant: f [B, T, H], dt_bias [H]); optional cu_seqlens int32 [n_docs + 1] over
@@ -33,7 +39,9 @@ from ._lib import KdaError, kda_device_status, kda_strerror_text  # noqa: F401
 __all__ = ["kda_forward", "kda_backward", "kda_forward_norm_gate", "kda_backward_norm_gate", "kda_forward_conv",
            "kda_backward_conv", "kda_decode_step", "kda_norm_gate", "kda_norm_gate_backward",
            "kda_short_conv", "kda_short_conv_backward", "KdaContext", "KdaError", "kda_device_status",
-           "kda_attention", "short_conv", "gated_norm"]
+           "kda_attention", "short_conv", "gated_norm", "kda_linear_forward", "kda_linear_backward",
+           "kda_linear_decode_step", "LinearContext", "kda_layer_norm", "kda_layer_norm_backward",
+           "linear_attention", "layer_norm"]
 
 
 @dataclass
@@ -73,6 +81,16 @@ def _shape(t, name, shape):
 def _dims(t, name, n):
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+
+
+def _same_device(first, **others):
+    """The library launches on the current device and stream: every tensor
+    must live there."""
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {first.device}, the current device is {torch.cuda.current_device()}")
+    for n, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{n} is on {t.device}, not on {first.device}")
 
 
 def _gate_of(f, dt_bias, qshape):
@@ -466,4 +484,6 @@ def kda_short_conv_backward(x, w, dy, cu_seqlens=None, activation: str = "silu",
     return dx, dw
 
 
-from .autograd import gated_norm, kda_attention, short_conv  # noqa: E402  (differentiable forms)
+from .linear import LinearContext, kda_linear_backward, kda_linear_decode_step, kda_linear_forward  # noqa: E402
+from .layer_norm import kda_layer_norm, kda_layer_norm_backward  # noqa: E402
+from .autograd import gated_norm, kda_attention, layer_norm, linear_attention, short_conv  # noqa: E402  (differentiable forms)

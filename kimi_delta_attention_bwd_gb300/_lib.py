@@ -104,6 +104,20 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.kda_short_conv_fwd.restype = I
         lib.kda_short_conv_bwd.argtypes = [I64, I, I, I, P, I, P, P, P, P, P, P, SZ, P]
         lib.kda_short_conv_bwd.restype = I
+        lib.kda_linear_workspace_size.argtypes = [PP, I]
+        lib.kda_linear_workspace_size.restype = SZ
+        lib.kda_linear_fwd.argtypes = [PP] + [P] * 7 + [I, P, SZ, P]
+        lib.kda_linear_fwd.restype = I
+        lib.kda_linear_bwd.argtypes = [PP] + [P] * 13 + [SZ, P]
+        lib.kda_linear_bwd.restype = I
+        lib.kda_linear_decode.argtypes = [I, I, I, I, I, F] + [P] * 7
+        lib.kda_linear_decode.restype = I
+        lib.kda_layer_norm_workspace_size.argtypes = [I64, I, I]
+        lib.kda_layer_norm_workspace_size.restype = SZ
+        lib.kda_layer_norm_fwd.argtypes = [I64, I, I, F] + [P] * 7
+        lib.kda_layer_norm_fwd.restype = I
+        lib.kda_layer_norm_bwd.argtypes = [I64, I, I] + [P] * 9 + [SZ, P]
+        lib.kda_layer_norm_bwd.restype = I
         _lib = lib
         return lib
 
@@ -271,6 +285,50 @@ def kda_short_conv_bwd(n_tok, C, dtype, activation, cu_seqlens, x, w, dy, dx, dw
 
 def kda_short_conv_workspace_size(n_tok, C) -> int:
     return int(load().kda_short_conv_workspace_size(int(n_tok), int(C)))
+
+
+def kda_linear_workspace_size(problem, for_backward) -> int:
+    return int(load().kda_linear_workspace_size(ctypes.byref(problem), 1 if for_backward else 0))
+
+
+def kda_linear_fwd(problem, q, k, v, A_log, h0, o, h_final, save_for_backward, workspace):
+    st = load().kda_linear_fwd(ctypes.byref(problem), _p(q), _p(k), _p(v), _p(A_log), _p(h0), _p(o), _p(h_final),
+                               1 if save_for_backward else 0, _p(workspace), workspace.numel(), _stream())
+    if st != 0:
+        raise KdaError(st, "kda_linear_fwd")
+
+
+def kda_linear_bwd(problem, q, k, v, A_log, h0, dO, dh_final, dq, dk, dv, dA_log, dh0, workspace):
+    st = load().kda_linear_bwd(ctypes.byref(problem), _p(q), _p(k), _p(v), _p(A_log), _p(h0), _p(dO), _p(dh_final),
+                               _p(dq), _p(dk), _p(dv), _p(dA_log), _p(dh0), _p(workspace), workspace.numel(),
+                               _stream())
+    if st != 0:
+        raise KdaError(st, "kda_linear_bwd")
+
+
+def kda_linear_decode(n_seq, H, dk, dv, dtype, scale, q, k, v, A_log, state, o):
+    st = load().kda_linear_decode(int(n_seq), int(H), int(dk), int(dv), _dt(dtype), float(scale or 0.0), _p(q), _p(k),
+                                  _p(v), _p(A_log), _p(state), _p(o), _stream())
+    if st != 0:
+        raise KdaError(st, "kda_linear_decode")
+
+
+def kda_layer_norm_workspace_size(n_rows, D, dtype) -> int:
+    return int(load().kda_layer_norm_workspace_size(int(n_rows), int(D), _dt(dtype)))
+
+
+def kda_layer_norm_fwd(n_rows, D, dtype, eps, x, w, bias, y, mean, rstd):
+    st = load().kda_layer_norm_fwd(int(n_rows), int(D), _dt(dtype), float(eps or 0.0), _p(x), _p(w), _p(bias), _p(y),
+                                   _p(mean), _p(rstd), _stream())
+    if st != 0:
+        raise KdaError(st, "kda_layer_norm_fwd")
+
+
+def kda_layer_norm_bwd(n_rows, D, dtype, x, w, dy, mean, rstd, dx, dw, dbias, workspace):
+    st = load().kda_layer_norm_bwd(int(n_rows), int(D), _dt(dtype), _p(x), _p(w), _p(dy), _p(mean), _p(rstd), _p(dx),
+                                   _p(dw), _p(dbias), _p(workspace), workspace.numel(), _stream())
+    if st != 0:
+        raise KdaError(st, "kda_layer_norm_bwd")
 
 
 def kda_device_status(workspace) -> int:

@@ -6,9 +6,11 @@ points), wrapped so that a model can use them like any differentiable op.
   o, h_final = kda_attention(..., h0=h0, output_final_state=True)     # and the final states
   x = short_conv(x_raw, conv_w, cu_seqlens)                           # causal conv (k=4) + silu
   y = gated_norm(o, gate, weight)                                     # gated RMSNorm epilogue
+  o = linear_attention(q, k, v, A_log)                                # linear attention, one decay per head
+  y = layer_norm(x, weight, bias)                                     # layer norm over the last axis
 
 Gradients flow to q, k, v, f, b, A_log, dt_bias and h0 (and to the
-convolution's input and taps, the norm's input, gate and weight).  Each
+convolution's input and taps, the norms' input, gate, weight and bias).  Each
 backward runs the library's backward kernels once; a second derivative is
 not provided.
 """
@@ -18,9 +20,10 @@ from typing import Optional
 
 import torch
 
-from . import kda_backward, kda_forward, kda_norm_gate, kda_norm_gate_backward, kda_short_conv, kda_short_conv_backward
+from . import (LinearContext, kda_backward, kda_forward, kda_layer_norm, kda_layer_norm_backward, kda_linear_backward,
+               kda_linear_forward, kda_norm_gate, kda_norm_gate_backward, kda_short_conv, kda_short_conv_backward)
 
-__all__ = ["kda_attention", "short_conv", "gated_norm"]
+__all__ = ["kda_attention", "short_conv", "gated_norm", "linear_attention", "layer_norm"]
 
 
 class _KdaAttention(torch.autograd.Function):
@@ -93,3 +96,58 @@ class _GatedNorm(torch.autograd.Function):
 def gated_norm(x, g, w, eps: Optional[float] = None):
     """Differentiable gated RMSNorm epilogue (kda_norm_gate)."""
     return _GatedNorm.apply(x, g, w, eps)
+
+
+class _LinearAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(fctx, q, k, v, A_log, h0, scale, cu_seqlens, cu_seqlens_host, want_final):
+        fctx.set_materialize_grads(False)
+        o, hf, lctx = kda_linear_forward(q, k, v, A_log, scale=scale, h0=h0, cu_seqlens=cu_seqlens,
+                                         cu_seqlens_host=cu_seqlens_host,
+                                         save_for_backward=any(fctx.needs_input_grad), want_final_state=want_final)
+        fctx.save_for_backward(q, k, v, A_log, h0, cu_seqlens)
+        fctx.rest = (lctx.problem, lctx.cu_seqlens_host, lctx.workspace, lctx.n_docs, lctx.saved)
+        return (o, hf) if want_final else o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(fctx, dO, dhf=None):
+        q, k, v, A_log, h0, cu_seqlens = fctx.saved_tensors
+        problem, cu_host, workspace, n_docs, saved = fctx.rest
+        lctx = LinearContext(problem, q, k, v, A_log, h0, cu_seqlens, cu_host, workspace, n_docs, saved)
+        dO = torch.zeros_like(v) if dO is None else dO.contiguous()
+        g = kda_linear_backward(lctx, dO, None if dhf is None else dhf.contiguous(),
+                                want_dA_log=fctx.needs_input_grad[3],
+                                want_dh0=h0 is not None and fctx.needs_input_grad[4])
+        return g["dq"], g["dk"], g["dv"], g["dA_log"], g["dh0"], None, None, None, None
+
+
+def linear_attention(q, k, v, A_log, scale: Optional[float] = None, h0=None, cu_seqlens=None, cu_seqlens_host=None,
+                     output_final_state: bool = False):
+    """Differentiable linear attention: o (and h_final when
+    output_final_state) from the layouts of kda_linear_forward; gradients to q,
+    k, v, A_log and h0 through kda_linear_backward."""
+    return _LinearAttention.apply(q, k, v, A_log, h0, scale, cu_seqlens, cu_seqlens_host, output_final_state)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(fctx, x, w, bias, eps):
+        if not any(fctx.needs_input_grad):
+            return kda_layer_norm(x, w, bias, eps)
+        y, mean, rstd = kda_layer_norm(x, w, bias, eps, return_stats=True)
+        fctx.save_for_backward(x, w, mean, rstd)
+        fctx.has_bias = bias is not None
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(fctx, dy):
+        x, w, mean, rstd = fctx.saved_tensors
+        dx, dw, db = kda_layer_norm_backward(x, w, dy.contiguous(), mean, rstd, want_dbias=fctx.has_bias)
+        return dx, dw, db, None
+
+
+def layer_norm(x, w, bias=None, eps: Optional[float] = None):
+    """Differentiable layer norm over the last axis (kda_layer_norm)."""
+    return _LayerNorm.apply(x, w, bias, eps)

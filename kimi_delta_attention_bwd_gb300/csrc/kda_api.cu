@@ -414,7 +414,7 @@ static bool supported(int dk, int dv) {
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // Validates the problem and fills the dims.  Pure host code: no CUDA call.
-static kda_status check_problem(const kda_problem* p, Dims* d) {
+kda_status check_problem(const kda_problem* p, Dims* d) {
   if (!p) return KDA_ERR_INVALID_ARG;
   if (p->B <= 0 || p->T <= 0 || p->H <= 0 || p->dk <= 0 || p->dv <= 0) return KDA_ERR_INVALID_ARG;
   if (p->dtype != KDA_BF16 && p->dtype != KDA_F32) return KDA_ERR_INVALID_ARG;
@@ -748,7 +748,9 @@ static const char* const k_names[K_COUNT] = {"chunk_table", "fwd_intra", "fwd_sc
                                              "fwd_state", "bwd_grad",  "bwd_gate",   "decode",
                                              "norm_gate_fwd", "norm_gate_bwd", "norm_gate_reduce",
                                              "conv_fwd",  "conv_bwd",  "conv_reduce",
-                                             "fwd_state_norm", "bwd_scan_norm", "fwd_seg", "bwd_seg"};
+                                             "fwd_state_norm", "bwd_scan_norm", "fwd_seg", "bwd_seg",
+                                             "linear_chain", "linear_seg", "linear_decay", "linear_decode",
+                                             "layer_norm_fwd", "layer_norm_bwd", "layer_norm_reduce"};
 
 const char* kda_prof_kernel_name(int i) { return (i >= 0 && i < K_COUNT) ? k_names[i] : nullptr; }
 

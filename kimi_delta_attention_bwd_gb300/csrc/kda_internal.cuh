@@ -36,6 +36,13 @@ enum KernelId {
   K_BWD_SCAN_NORM,
   K_FWD_SEG,
   K_BWD_SEG,
+  K_LIN_CHAIN,
+  K_LIN_SEG,
+  K_LIN_DECAY,
+  K_LIN_DECODE,
+  K_LN_FWD,
+  K_LN_BWD,
+  K_LN_RED,
   K_COUNT
 };
 

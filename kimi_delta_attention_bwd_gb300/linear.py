@@ -1,0 +1,149 @@
+"""Linear attention with one decay per head (kda_linear_*):
+
+  S_t = exp(-a) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   a = exp(A_log[h])
+
+per document and head; q and k enter as they are.  Shapes, dtypes and
+documents as kda_forward: q, k [B, T, H, dk]; v, o [B, T, H, dv] (bf16 or fp32;
+(dk, dv) = (32, 64), (64, 64), (64, 128), (128, 128)); A_log [H] fp32; states
+[n_docs, H, dk, dv] fp32; optional cu_seqlens int32 [n_docs + 1].
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import _check, _dims, _lib, _same_device, _shape
+from ._lib import KdaError
+
+
+@dataclass
+class LinearContext:
+    """What kda_linear_backward needs from kda_linear_forward."""
+    problem: object
+    q: torch.Tensor
+    k: torch.Tensor
+    v: torch.Tensor
+    A_log: torch.Tensor
+    h0: Optional[torch.Tensor]
+    cu_seqlens: Optional[torch.Tensor]
+    cu_seqlens_host: object
+    workspace: torch.Tensor
+    n_docs: int
+    saved: bool
+
+
+def _host_offsets(cu_seqlens_host, cu_seqlens):
+    """cu_seqlens_host as the int32 host array the library reads (a tensor or
+    a numpy array of cu_seqlens' length)."""
+    if cu_seqlens_host is None:
+        return None
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens_host comes with cu_seqlens")
+    c = cu_seqlens_host
+    if isinstance(c, torch.Tensor):
+        if c.is_cuda or c.dtype != torch.int32 or not c.is_contiguous():
+            raise ValueError("cu_seqlens_host must be a contiguous int32 tensor on the host")
+        n = c.numel()
+    else:
+        if str(c.dtype) != "int32" or not c.flags["C_CONTIGUOUS"]:
+            raise ValueError("cu_seqlens_host must be a contiguous int32 array")
+        n = c.size
+    if n != cu_seqlens.numel():
+        raise ValueError(f"cu_seqlens_host has {n} offsets, cu_seqlens {cu_seqlens.numel()}")
+    return c
+
+
+def kda_linear_forward(q, k, v, A_log, scale: Optional[float] = None, h0=None, cu_seqlens=None, cu_seqlens_host=None,
+                       save_for_backward: bool = True, workspace: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, want_final_state: bool = True,
+                       final_state: Optional[torch.Tensor] = None):
+    """Forward pass.  Returns (o, h_final or None, ctx); ctx feeds
+    kda_linear_backward when save_for_backward is set.  scale: 1/sqrt(dk)
+    unless given (> 0).  out / final_state: optional preallocated outputs."""
+    _dims(q, "q", 4)
+    _dims(v, "v", 4)
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    _shape(k, "k", q.shape)
+    _shape(v, "v", (B, T, H, dv))
+    _shape(A_log, "A_log", (H,))
+    if cu_seqlens is not None:
+        _dims(cu_seqlens, "cu_seqlens", 1)
+        if cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must hold at least two offsets")
+    cu_seqlens_host = _host_offsets(cu_seqlens_host, cu_seqlens)
+    n_docs = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    states = (n_docs, H, dk, dv)
+    for t, n, shape, dt in ((q, "q", q.shape, q.dtype), (k, "k", q.shape, q.dtype), (v, "v", v.shape, q.dtype),
+                            (A_log, "A_log", (H,), torch.float32), (h0, "h0", states, torch.float32),
+                            (out, "out", (B, T, H, dv), q.dtype), (final_state, "final_state", states, torch.float32),
+                            (cu_seqlens, "cu_seqlens", None, torch.int32)):
+        if t is not None:
+            if shape is not None:
+                _shape(t, n, shape)
+            _check(t, n, dt)
+    _same_device(q, k=k, v=v, A_log=A_log, h0=h0, cu_seqlens=cu_seqlens, out=out, final_state=final_state,
+                 workspace=workspace)
+    prob = _lib.make_problem(B, T, H, dk, dv, q.dtype, scale, cu_seqlens, cu_seqlens_host)
+    if workspace is None:
+        n = _lib.kda_linear_workspace_size(prob, save_for_backward)
+        # (0 for a problem that the call below refuses with its own status)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    else:
+        _check(workspace, "workspace", torch.uint8)
+    o = out if out is not None else torch.empty(B, T, H, dv, dtype=q.dtype, device=q.device)
+    hf = None
+    if want_final_state:
+        hf = final_state if final_state is not None else torch.empty(*states, dtype=torch.float32, device=q.device)
+    _lib.kda_linear_fwd(prob, q, k, v, A_log, h0, o, hf, save_for_backward, workspace)
+    return o, hf, LinearContext(prob, q, k, v, A_log, h0, cu_seqlens, cu_seqlens_host, workspace, n_docs,
+                                bool(save_for_backward))
+
+
+def kda_linear_backward(ctx: LinearContext, dO, dh_final=None, want_dA_log: bool = True, want_dh0: bool = True):
+    """Backward of sum(o * dO) + sum(h_final * dh_final).  Returns a dict with
+    dq, dk, dv (io dtype), dA_log and dh0 (fp32; None where not wanted:
+    without dA_log, e.g. for fixed decays, its products are skipped)."""
+    if not ctx.saved:
+        raise ValueError("the forward saved nothing: call kda_linear_forward with save_for_backward=True")
+    q, v = ctx.q, ctx.v
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    _shape(dO, "dO", (B, T, H, dv))
+    _check(dO, "dO", q.dtype)
+    if dh_final is not None:
+        _shape(dh_final, "dh_final", (ctx.n_docs, H, dk, dv))
+        _check(dh_final, "dh_final", torch.float32)
+    _same_device(q, dO=dO, dh_final=dh_final)
+    gr = {"dq": torch.empty_like(q), "dk": torch.empty_like(ctx.k), "dv": torch.empty_like(v),
+          "dA_log": torch.empty(H, dtype=torch.float32, device=q.device) if want_dA_log else None,
+          "dh0": torch.empty(ctx.n_docs, H, dk, dv, dtype=torch.float32, device=q.device) if want_dh0 else None}
+    _lib.kda_linear_bwd(ctx.problem, q, ctx.k, v, ctx.A_log, ctx.h0, dO, dh_final, gr["dq"], gr["dk"], gr["dv"],
+                        gr["dA_log"], gr["dh0"], ctx.workspace)
+    return gr
+
+
+def kda_linear_decode_step(q, k, v, A_log, state, scale: Optional[float] = None,
+                           out: Optional[torch.Tensor] = None):
+    """One token for each of n sequences: q, k [n, H, dk], v [n, H, dv] (bf16 or
+    fp32), A_log [H] and state [n, H, dk, dv] fp32, the state updated in place.
+    Returns o [n, H, dv] in the io dtype."""
+    _dims(q, "q", 3)
+    _dims(v, "v", 3)
+    n, H, dk = q.shape
+    dv = v.shape[-1]
+    for t, nm, shape, dt in ((q, "q", q.shape, q.dtype), (k, "k", q.shape, q.dtype), (v, "v", (n, H, dv), q.dtype),
+                             (A_log, "A_log", (H,), torch.float32), (state, "state", (n, H, dk, dv), torch.float32),
+                             (out, "out", (n, H, dv), q.dtype)):
+        if t is not None:
+            _shape(t, nm, shape)
+            _check(t, nm, dt)
+    _same_device(q, k=k, v=v, A_log=A_log, state=state, out=out)
+    o = out if out is not None else torch.empty(n, H, dv, dtype=q.dtype, device=q.device)
+    _lib.kda_linear_decode(n, H, dk, dv, q.dtype, scale, q, k, v, A_log, state, o)
+    return o
+
+
+__all__ = ["LinearContext", "kda_linear_forward", "kda_linear_backward", "kda_linear_decode_step", "KdaError"]

@@ -1,0 +1,353 @@
+"""Linear attention with one decay per head (kda_linear_*) against its oracle.
+
+Tolerances, per element, from M, the oracle on the absolute values of the
+inputs (the sum of the magnitudes of the terms of each output):
+ - bf16 io.  A computed operand (weighted pairs, state, weighted values) is two
+   bf16 parts, off by at most 2^-16 of itself; a term passes at most two of
+   them, and the fp32 sums of at most 64 + 16 products per chunk add at most
+   as much again (80 * 2^-23 < 2^-16): 2^-14 M.  A bf16 output adds its own
+   rounding, 2^-8 of the value.
+ - fp32 io.  Three parts (2^-24) per operand, six products: below 100 sums per
+   chunk and product, 100 * 2^-23 < 2^-16, M; plus 2^-24 of the value.
+The decays add a few 2^-23 of a term times a m e^-am <= 1/e, well inside both.
+"""
+import numpy as np
+import pytest
+import torch
+
+import kimi_delta_attention_bwd_gb300 as kda
+from kimi_delta_attention_bwd_gb300 import _lib
+from oracle import linear_attention as ola
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+REL = {"bf16": 2.0 ** -14, "f32": 2.0 ** -16}
+ROUND = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+SHAPES = [(32, 64), (64, 64), (64, 128), (128, 128)]
+
+
+def make(seed, docs, H, dk, dv, dt, rows=False, A=None):
+    g = torch.Generator().manual_seed(seed)
+    N = sum(docs)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    B = len(docs) if rows else 1
+    x = dict(q=r(B, N // B, H, dk).to(DT[dt]), k=r(B, N // B, H, dk).to(DT[dt]), v=r(B, N // B, H, dv).to(DT[dt]),
+             A_log=(torch.linspace(-6.0, 1.0, H) if A is None else torch.tensor(A)).float(),
+             h0=r(len(docs), H, dk, dv), dO=r(B, N // B, H, dv).to(DT[dt]), dh=r(len(docs), H, dk, dv))
+    x["cu"] = None if rows else torch.tensor([0] + list(np.cumsum(docs)), dtype=torch.int32)
+    x["docs"] = docs
+    return x
+
+
+def oracle(x, backward=True, h0=True, dh=True, scale=None):
+    H, dk = x["q"].shape[2:]
+    cu = [0] + list(np.cumsum(x["docs"]))
+    scale = scale or dk ** -0.5
+    f = lambda t: t.double().numpy().reshape(-1, *t.shape[2:])  # noqa: E731
+    res = {}
+    for key, fn in (("ref", lambda t: t), ("mag", np.abs)):
+        q, k, v, dO = (fn(f(x[n])) for n in ("q", "k", "v", "dO"))
+        a = dict(q=q, k=k, v=v, A_log=x["A_log"].double().numpy(), cu=cu, scale=scale,
+                 h0=fn(x["h0"].double().numpy()) if h0 else None)
+        o, hf = ola.forward(**a)
+        out = dict(o=o, h_final=hf)
+        if backward:
+            out.update(ola.backward(**a, dO=dO, dh_final=fn(x["dh"].double().numpy()) if dh else None))
+        res[key] = out
+    return res
+
+
+def check(got, res, dt, names=None):
+    for n, r in res["ref"].items():
+        if names is not None and n not in names:
+            continue
+        g = got[n].detach().double().cpu().numpy().reshape(r.shape)
+        lim = REL[dt] * np.abs(res["mag"][n])
+        if n in ("o", "dq", "dk", "dv"):
+            lim = lim + ROUND[dt] * np.abs(r) * (1 + REL[dt])
+        bad = ~(np.abs(g - r) <= lim + 1e-30)
+        assert not bad.any(), (n, int(bad.sum()), g[bad][:4], r[bad][:4], lim[bad][:4])
+
+
+def run(x, backward=True, h0=True, dh=True, host=True, **kw):
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    o, hf, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=d["h0"] if h0 else None,
+                                        cu_seqlens=d["cu"], cu_seqlens_host=x["cu"] if host else None,
+                                        save_for_backward=backward, **kw)
+    got = dict(o=o, h_final=hf)
+    if backward:
+        got.update(kda.kda_linear_backward(ctx, d["dO"], d["dh"] if dh else None))
+    torch.cuda.synchronize()
+    assert kda.kda_device_status(ctx.workspace) == 0
+    return got
+
+
+@pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 130])
+def test_rows(T):
+    x = make(T, [T, T], 3, 32, 64, "bf16", rows=True)
+    check(run(x), oracle(x), "bf16")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_packed_documents(dk, dv, dt):
+    # an empty document, single tokens, chunk borders; 300 and 700 tokens are cut into segments of 256
+    x = make(dk + dv, [5, 0, 300, 1, 64, 1, 700, 0], 2, dk, dv, dt)
+    check(run(x), oracle(x), dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_rows_cut_into_segments(dk, dv, dt):
+    x = make(7 + dk, [577, 577], 2, dk, dv, dt, rows=True)
+    check(run(x), oracle(x), dt)
+
+
+def test_without_states_and_with_a_scale():
+    x = make(11, [90, 0, 333], 2, 64, 64, "bf16")
+    res = oracle(x, h0=False, dh=False, scale=0.75)
+    check(run(x, h0=False, dh=False, scale=0.75), res, "bf16")
+
+
+def test_offsets_known_on_the_device_alone():
+    x = make(12, [10, 500, 0, 33], 2, 32, 64, "bf16")
+    a, b = run(x, host=True), run(x, host=False)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("A", [[-np.inf, -30.0], [3.0, 60.0]])
+def test_no_decay_and_total_decay(A):
+    # no decay: a running sum; a = e^3, e^60: nothing of the token before is left
+    x = make(13, [200, 1, 270], 2, 32, 64, "bf16", A=A)
+    res = oracle(x)
+    if np.isinf(A[0]):  # 0 times the (finite) derivative
+        for r in res.values():
+            r["dA_log"][0] = 0.0
+    check(run(x), res, "bf16")
+
+
+def test_a_document_does_not_see_its_neighbours():
+    docs = [70, 129, 1, 300]
+    x = make(14, docs, 2, 64, 128, "bf16")
+    y = dict(x)
+    for n in ("q", "k", "v", "dO"):  # the neighbours of document 1 hold infinities and NaN
+        t = x[n].clone()
+        t[:, :70] = float("inf")
+        t[:, 199:] = float("nan")
+        y[n] = t
+    a, b = run(x), run(y)
+    for n in ("o", "dq", "dk", "dv"):
+        assert torch.equal(a[n][:, 70:199], b[n][:, 70:199]), n
+    for n in ("h_final", "dh0"):
+        assert torch.equal(a[n][1], b[n][1]), n
+
+
+def test_gradients_that_are_not_wanted():
+    x = make(15, [400, 3], 2, 128, 128, "bf16")
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    _, _, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=d["h0"], cu_seqlens=d["cu"])
+    a = kda.kda_linear_backward(ctx, d["dO"], d["dh"])
+    b = kda.kda_linear_backward(ctx, d["dO"], d["dh"], want_dA_log=False, want_dh0=False)
+    c = kda.kda_linear_backward(ctx, d["dO"], d["dh"])  # the workspace serves again
+    assert b["dA_log"] is None and b["dh0"] is None
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(a[n], b[n]), n
+    for n in a:
+        assert torch.equal(a[n], c[n]), n
+
+
+def test_given_outputs_and_states_left_alone():
+    x = make(16, [100, 20], 2, 32, 64, "bf16")
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    out, fin = torch.empty_like(d["v"]), torch.empty_like(d["h0"])
+    ref = run(x, backward=False)
+    o, hf, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=d["h0"], cu_seqlens=d["cu"], out=out,
+                                        final_state=fin, save_for_backward=False)
+    assert o is out and hf is fin and torch.equal(o, ref["o"]) and torch.equal(hf, ref["h_final"])
+    assert torch.equal(d["h0"].cpu(), x["h0"])
+    with pytest.raises(ValueError, match="saved nothing"):
+        kda.kda_linear_backward(ctx, d["dO"])
+    _, none, _ = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], cu_seqlens=d["cu"],
+                                        want_final_state=False)
+    assert none is None
+
+
+def test_bad_offsets_on_the_device_do_no_work():
+    x = make(17, [60, 60], 2, 32, 64, "bf16")
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    for bad in ([0, 130, 120], [0, 60, 119], [3, 60, 120]):
+        out = torch.full_like(d["v"], 7.0)
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        _, _, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], cu_seqlens=cu, out=out)
+        assert kda.kda_device_status(ctx.workspace) == -4
+        assert bool((out == 7.0).all())
+        kda.kda_linear_backward(ctx, d["dO"])
+        assert kda.kda_device_status(ctx.workspace) in (-4, -5)
+
+
+def test_a_workspace_that_nothing_saved_is_refused():
+    x = make(18, [60, 60], 2, 32, 64, "bf16")
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    _, _, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], cu_seqlens=d["cu"])
+    ctx.workspace.zero_()
+    kda.kda_linear_backward(ctx, d["dO"])
+    assert kda.kda_device_status(ctx.workspace) == -5
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_decode_continues_a_prompt(dk, dv, dt):
+    # the prompt's state, then four single tokens, against one document of all of them
+    n, T, H = 3, 70, 2
+    x = make(19 + dk, [T + 4] * n, H, dk, dv, dt, rows=True)
+    res = oracle(x, backward=False)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    cut = lambda t, s: t[:, s].contiguous()  # noqa: E731
+    _, state, _ = kda.kda_linear_forward(cut(d["q"], slice(0, T)), cut(d["k"], slice(0, T)),
+                                         cut(d["v"], slice(0, T)), d["A_log"], h0=d["h0"], save_for_backward=False)
+    outs = [kda.kda_linear_decode_step(cut(d["q"], T + i), cut(d["k"], T + i), cut(d["v"], T + i), d["A_log"], state)
+            for i in range(4)]
+    o = torch.stack(outs, 1)
+    sel = {k: {"o": r["o"].reshape(n, T + 4, H, dv)[:, T:], "h_final": r["h_final"]} for k, r in res.items()}
+    check(dict(o=o, h_final=state), sel, dt)
+
+
+def test_on_another_stream_and_as_a_graph():
+    x = make(20, [300, 0, 45], 2, 32, 64, "bf16")
+    ref = run(x)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        o, hf, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=d["h0"], cu_seqlens=d["cu"],
+                                            cu_seqlens_host=x["cu"])
+        return dict(o=o, h_final=hf, **kda.kda_linear_backward(ctx, d["dO"], d["dh"]))
+
+    with torch.cuda.stream(s):
+        a = step()
+    s.synchronize()
+    for n in ref:
+        assert torch.equal(ref[n], a[n]), n
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b = step()
+    keep = d["q"].clone()
+    d["q"].zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert not bool(b["o"].any())
+    d["q"].copy_(keep)
+    g.replay()
+    torch.cuda.synchronize()
+    for n in ref:
+        assert torch.equal(ref[n], b[n]), n
+
+
+def test_autograd_matches_the_direct_calls():
+    x = make(21, [130, 1, 300], 2, 64, 64, "bf16")
+    ref = run(x)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    leaves = [d[n].clone().requires_grad_() for n in ("q", "k", "v", "A_log", "h0")]
+    o, hf = kda.linear_attention(*leaves[:4], h0=leaves[4], cu_seqlens=d["cu"], output_final_state=True)
+    torch.autograd.backward([o, hf], [d["dO"], d["dh"]])
+    assert torch.equal(o, ref["o"]) and torch.equal(hf, ref["h_final"])
+    for t, n in zip(leaves, ("dq", "dk", "dv", "dA_log", "dh0")):
+        assert torch.equal(t.grad, ref[n]), n
+    # the state alone: dO is zero
+    fixed = kda.linear_attention(leaves[0].detach(), leaves[1], leaves[2].detach(), d["A_log"], cu_seqlens=d["cu"],
+                                 output_final_state=True)[1]
+    gk, = torch.autograd.grad(fixed.sum(), [leaves[1]])
+    assert bool(torch.isfinite(gk).all()) and bool(gk.any())
+    with torch.no_grad():
+        assert torch.equal(kda.linear_attention(*leaves[:4], h0=leaves[4], cu_seqlens=d["cu"]), ref["o"])
+
+
+def test_gradients_against_differences():
+    # fp32, a direction per leaf: (L(x + e u) - L(x - e u)) / 2e for the loss in 64 bits
+    x = make(22, [100, 30], 2, 32, 64, "f32")
+    got = run(x)
+    g = torch.Generator().manual_seed(5)
+
+    def loss(**kw):
+        y = {**x, **kw}
+        r = run(y, backward=False)
+        return float((r["o"].double().cpu() * x["dO"].double()).sum() + (r["h_final"].double().cpu() * x["dh"].double()).sum())
+
+    # the loss's own error: 2^-16 of the sum of magnitudes over 2e; both are far below the directional derivative
+    mag = oracle(x, backward=False)["mag"]
+    noise = 2.0 ** -16 * float((mag["o"] * np.abs(x["dO"].double().numpy().reshape(mag["o"].shape))).sum()
+                               + (mag["h_final"] * np.abs(x["dh"].double().numpy())).sum())
+    for leaf, grad in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("A_log", "dA_log"), ("h0", "dh0")):
+        ref = got[grad].double().cpu().reshape(x[leaf].shape)
+        u = ref / ref.norm() + 0.1 * torch.randn(x[leaf].shape, generator=g, dtype=torch.float64) / ref.numel() ** 0.5
+        e = 0.25 if leaf != "A_log" else 0.01
+        p, m = (x[leaf].double() + s * e * u for s in (1, -1))
+        fd = (loss(**{leaf: p.float()}) - loss(**{leaf: m.float()})) / (2 * e)
+        want = float((ref * u).sum())
+        # the loss is linear in q, v, h0 and k; in A_log the third derivative leaves e^2 / 6 of its size
+        lim = noise / e + (2e-3 * abs(want) if leaf == "A_log" else 1e-4 * abs(want))
+        assert abs(fd - want) <= lim, (leaf, fd, want, lim)
+
+
+def test_layer_norm_linear_attention_layer_norm():
+    # a block as it would be used: norm of the hidden states, heads, per-head norm of the output
+    B, T, H, dk, dv = 2, 90, 2, 32, 64
+    g = torch.Generator().manual_seed(23)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    hid = r(B, T, H * (2 * dk + dv)).to(torch.bfloat16)
+    w1, b1, w2, dy = 1 + 0.1 * r(hid.shape[-1]), 0.1 * r(hid.shape[-1]), 1 + 0.1 * r(dv), r(B, T, H, dv)
+    A = torch.tensor([-3.0, -0.5])
+
+    def block(hid, w1, b1, A, w2, ln, attn):
+        y = ln(hid, w1, b1)
+        q, k, v = (t.reshape(B, T, H, -1).contiguous() for t in y.split([H * dk, H * dk, H * dv], -1))
+        return ln(attn(q, k, v, A), w2, None)
+
+    own = [t.cuda().requires_grad_() for t in (hid, w1, b1, A, w2)]
+    out = block(*own, kda.layer_norm, kda.linear_attention)
+    got = torch.autograd.grad(out, own, dy.cuda().to(torch.bfloat16))
+
+    def ln64(x, w, b):
+        z = (x - x.mean(-1, keepdim=True)) / (x.var(-1, unbiased=False, keepdim=True) + 1e-6).sqrt() * w
+        return z if b is None else z + b
+
+    def attn64(q, k, v, A):
+        i = torch.arange(T)
+        w = torch.exp(-torch.exp(A)[:, None, None] * (i[:, None] - i).clamp(min=0)) * (i[:, None] >= i)
+        return torch.einsum("bthd,bshd,hts,bshe->bthe", q, k, w, v) * dk ** -0.5
+
+    leaves = [t.double().requires_grad_() for t in (hid, w1, b1, A, w2)]
+    ref = block(*leaves, ln64, attn64)
+    want = torch.autograd.grad(ref, leaves, dy.to(torch.bfloat16).double())
+    # three bf16 roundings lie between the input and an output, six to a gradient, each 2^-8 of its tensor at most
+    # and independent from value to value; in the 2-norm: 6 * 2^-8, doubled for the norms' Jacobians
+    for a, b in zip([out, *got], [ref, *want]):
+        e = (a.double().cpu() - b).norm() / b.norm()
+        assert e <= 12 * 2.0 ** -8, float(e)
+
+
+def test_python_refusals_on_the_device():
+    x = make(24, [40], 2, 32, 64, "bf16", rows=True)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    f = kda.kda_linear_forward
+    with pytest.raises(ValueError, match="contiguous"):
+        f(d["q"].transpose(1, 2).contiguous().transpose(1, 2), d["k"], d["v"], d["A_log"])
+    with pytest.raises(ValueError, match="v must be torch.bfloat16"):
+        f(d["q"], d["k"], d["v"].float(), d["A_log"])
+    with pytest.raises(kda.KdaError, match="INVALID_ARG"):
+        f(d["q"].half(), d["k"].half(), d["v"].half(), d["A_log"])
+    with pytest.raises(kda.KdaError, match="UNSUPPORTED"):
+        f(d["q"], d["k"], torch.zeros(1, 40, 2, 32, dtype=torch.bfloat16, device="cuda"), d["A_log"])
+    with pytest.raises(kda.KdaError, match="WORKSPACE"):
+        f(d["q"], d["k"], d["v"], d["A_log"], workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(kda.KdaError, match="BAD_SEQLENS"):
+        bad = torch.tensor([0, 50], dtype=torch.int32)
+        f(d["q"], d["k"], d["v"], d["A_log"], cu_seqlens=bad.cuda(), cu_seqlens_host=bad)
+    with pytest.raises(kda.KdaError, match="INVALID_ARG"):
+        z = torch.zeros(0, 2, 32, dtype=torch.bfloat16, device="cuda")
+        kda.kda_linear_decode_step(z, z, torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda"), d["A_log"],
+                                   torch.zeros(0, 2, 32, 64, device="cuda"))
+    assert _lib.load() is not None
