@@ -3302,6 +3302,19 @@ static bool encode_rows(CUtensorMap* m, const void* base, int Ntok, int H, int d
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_head_rows(CUtensorMap* m, const void* base, int Ntok, int H, int dh) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
+  if (!enc) return false;
+  const int bx = dh < 64 ? dh : 64;
+  const cuuint64_t dims[2] = {(cuuint64_t)H * dh, (cuuint64_t)Ntok};
+  const cuuint64_t strides[1] = {(cuuint64_t)H * dh * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)bx, (cuuint32_t)C};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, bx == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_nmaps(NMaps* nm, const void* g, const void* dy, const float* o, int Ntok, int H, int dv) {
   *nm = NMaps{};
   return encode_rows(&nm->g, g, Ntok, H, dv, fast::NSC, false) && (!dy || encode_rows(&nm->dy, dy, Ntok, H, dv, fast::NSC, false)) &&

@@ -220,6 +220,9 @@ bool encode_tmaps(TMaps* tm, const void* q, const void* k, const void* v, const 
 struct NMaps {
   CUtensorMap g, dy, o;
 };
+// The map of a bf16 [Ntok, H, dh] tensor as [Ntok][H dh] rows with a box of C
+// tokens by one head's 64 columns (dh = 32: 32) in the 128-byte (64-byte) swizzle.
+bool encode_head_rows(CUtensorMap* m, const void* base, int Ntok, int H, int dh);
 bool encode_nmaps(NMaps* nm, const void* g, const void* dy, const float* o, int Ntok, int H, int dv);
 
 // Launch wrappers (return cudaGetLastError of their launches).

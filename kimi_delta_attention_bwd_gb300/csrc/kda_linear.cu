@@ -28,79 +28,21 @@
 //   E  <R^ at the document's end, dh_final>
 // A, B, D, E ride on the dq chain, C on the dk chain.
 //
-// Products run on tcgen05 (M = 64).  Operands that are not inputs (the
-// weighted pairs, the state, the weighted values) are split bf16 hi + lo (about 16
-// bits); fp32 io splits everything in three (24 bits, six products).  The
-// state stays in fp32 registers.
-#include "kda_internal.cuh"
-#include "kda_mma.cuh"
-#include "kda_tc.cuh"
-#include "../../include/kda.h"
-
-#include <atomic>
+// The state stays in fp32 registers for a whole chain.  Operands that are not
+// inputs are split into bf16 parts: two (about 16 bits) where the result is
+// rounded to bf16, three (24 bits) where it enters the fp32 state or the decay
+// gradient's sums.  fp32 io: kda_linear_f32.cu.
+#include "kda_linear.cuh"
 
 namespace kda {
 
 kda_status check_problem(const kda_problem* p, Dims* d);
 
+namespace lin {
 namespace {
 
-using bf16 = __nv_bfloat16;
-constexpr int LTH = 256;        // threads of a chain CTA: warp w holds rows 16 (w % 4) .., column half w / 4
-constexpr int LIN_SMS = 152;    // SMs of a GB300: the segment rule's denominator
-constexpr int SEG_TOK = 256;    // shortest segment (tokens)
-
-struct LinP {
-  int Ntok, H, n_docs, T, rows;  // rows: documents are the rows of T tokens
-  int nu, L, seg;                // units (an upper bound with cu_seqlens), segment length, any document split
-  int save, tag;
-  float scale;
-  const int32_t* cu;
-  const float* A_log;
-  int32_t *err, *wtag, *n_units;
-  int4* units;                   // {document, first token, tokens, segment}
-};
-
-// One application of the operator (see above).  z, out and the state's value
-// side have DVt columns per head; the state is stored [key][DVt], or, with tr,
-// [DVt][key].
-struct LinOp {
-  const void *x, *y, *z;
-  void* out;
-  const float* init;  // state at the chain's start (nullptr: 0)
-  float* fin;         // state at its end (nullptr: not wanted)
-  int tr, rev, DVt;
-  const float* segc;  // segments' own states [nu][H][2][key * DVt] (rev: [nu][H][key * DVt])
-  const void* wx;     // decay gradient: q (dq chain) or k (dk chain), laid out like z
-  const float* dfin;  // decay gradient: dh_final
-  double* pda;        // decay gradient: per CTA partial
-};
-
-// ------------------------------------------------------------ geometry
-struct Unit {
-  int doc, tok0, ntok, seg, d0, dlen;  // document start and length
-};
-__device__ __forceinline__ bool unit_of(const LinP& P, int u, Unit& t) {
-  if (P.rows) {
-    const int ns = (P.T + P.L - 1) / P.L;
-    t.doc = u / ns;
-    t.seg = u % ns;
-    t.d0 = t.doc * P.T;
-    t.dlen = P.T;
-    t.tok0 = t.d0 + t.seg * P.L;
-    t.ntok = min(P.L, P.T - t.seg * P.L);
-    return true;
-  }
-  if (u >= *P.n_units) return false;
-  const int4 v = P.units[u];
-  t.doc = v.x;
-  t.tok0 = v.y;
-  t.ntok = v.z;
-  t.seg = v.w;
-  t.d0 = t.tok0 - t.seg * P.L;
-  t.dlen = P.cu[t.doc + 1] - t.d0;
-  return true;
-}
+constexpr int LIN_SMS = 152;  // SMs of a GB300: the segment rule's denominator
+constexpr int SEG_TOK = 256;  // shortest segment (tokens)
 
 // The unit table of packed documents: a document of n tokens has max(1,
 // ceil(n / L)) units.  One CTA; also validates the offsets.
@@ -154,584 +96,462 @@ __global__ void __launch_bounds__(1024) lin_table_kernel(LinP P) {
   }
 }
 
-// Equal rows have no table: the first kernel of a forward resets the words.
-__device__ __forceinline__ void rows_reset(const LinP& P) {
-  if (P.rows && blockIdx.x == 0 && threadIdx.x == 0) {
-    *P.err = KDA_OK;
-    *P.wtag = P.save ? P.tag : 0;
-  }
-}
-
-__device__ __forceinline__ float decay_of(const float* A_log, int h) { return fminf(expf(A_log[h]), 1e30f); }
-__device__ __forceinline__ float decay_pow(float a, int m) { return m > 0 ? expf(-a * (float)m) : 1.0f; }
-
-// ------------------------------------------------------------ tiles
-// x = sum of N bf16 parts, each the rounding of what the parts before it leave
-// (two parts: about 16 bits, three: 24).
-template <int N>
-__device__ __forceinline__ void split8(const float (&v)[8], bf16* dst, int stride) {
-  float r[8];
-#pragma unroll
-  for (int e = 0; e < 8; e++) r[e] = v[e];
-#pragma unroll
-  for (int p = 0; p < N; p++) {
-    uint4 u;
-    uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(r[2 * e], r[2 * e + 1]);
-      const float2 f = __bfloat1622float2(h);
-      w[e] = *reinterpret_cast<const uint32_t*>(&h);
-      r[2 * e] -= f.x;
-      r[2 * e + 1] -= f.y;
-    }
-    *reinterpret_cast<uint4*>(dst + p * stride) = u;
-  }
-}
-template <int N>
-__device__ __forceinline__ void split2(float x0, float x1, bf16* dst, int stride) {
-#pragma unroll
-  for (int p = 0; p < N; p++) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-    const float2 f = __bfloat1622float2(h);
-    *reinterpret_cast<__nv_bfloat162*>(dst + p * stride) = h;
-    x0 -= f.x;
-    x1 -= f.y;
-  }
-}
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int e = 0; e < 4; e++) {
-    v[2 * e] = __uint_as_float(w[e] << 16);
-    v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-  }
-}
-
-// cp.async of 16 bytes that reads only `bytes` of them (0: fills with zeros).
-__device__ __forceinline__ void cp16z(void* smem, const void* gmem, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(mma::smem_u32(smem)), "l"(gmem), "r"(bytes)
-               : "memory");
-}
-
-// A chunk's rows: row i is token t0 + dir * i, i < n (later rows read as 0).
-struct Rows {
-  int64_t t0;
-  int dir, n;
-};
-
-// Loads a 64 x W tile (columns c0 .. of a head's D) into core-matrix order.
-// Element group idx (8 columns of a row) lands at element 8 idx: eight lanes
-// fill one 128-byte core matrix, a warp reads 64 bytes of eight rows.
-template <int W>
-__device__ __forceinline__ void load_tile(bf16* dst, const bf16* g, const Rows& r, int H, int h, int D, int c0) {
-  for (int idx = threadIdx.x; idx < 8 * W; idx += LTH) {
-    const int row = (idx & 7) + 8 * (idx / W), cg = (idx >> 3) % (W / 8);
-    const bool in = row < r.n;
-    const int64_t t = in ? r.t0 + (int64_t)r.dir * row : r.t0;
-    cp16z(dst + 8 * idx, g + (t * H + h) * D + c0 + 8 * cg, in ? 16 : 0);
-  }
-}
-template <int W>
-__device__ __forceinline__ void load_tile(bf16* dst, const float* g, const Rows& r, int H, int h, int D, int c0) {
-  for (int idx = threadIdx.x; idx < 8 * W; idx += LTH) {
-    const int row = (idx & 7) + 8 * (idx / W), cg = (idx >> 3) % (W / 8);
-    float v[8];
-    if (row < r.n) {
-      const float4* p = reinterpret_cast<const float4*>(g + ((r.t0 + (int64_t)r.dir * row) * H + h) * D + c0 + 8 * cg);
-      const float4 f0 = __ldg(p), f1 = __ldg(p + 1);
-      v[0] = f0.x; v[1] = f0.y; v[2] = f0.z; v[3] = f0.w;
-      v[4] = f1.x; v[5] = f1.y; v[6] = f1.z; v[7] = f1.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; e++) v[e] = 0.f;
-    }
-    split8<3>(v, dst + 8 * idx, 64 * W);
-  }
-}
-
-// sc = the 64 x W tile `raw` (NX parts) with row i times sw[i], in NS parts; each
-// thread scales the groups that it loaded itself (load_tile's mapping), so it
-// needs no barrier in between.
-template <int W, int NX, int NS>
-__device__ __forceinline__ void scale_tile(bf16* sc, const bf16* raw, const float* sw) {
-  for (int idx = threadIdx.x; idx < 8 * W; idx += LTH) {
-    const float w = sw[(idx & 7) + 8 * (idx / W)];
-    float v[8], u[8];
-    unpack8(*reinterpret_cast<const uint4*>(raw + 8 * idx), v);
-#pragma unroll
-    for (int p = 1; p < NX; p++) {
-      unpack8(*reinterpret_cast<const uint4*>(raw + p * 64 * W + 8 * idx), u);
-#pragma unroll
-      for (int e = 0; e < 8; e++) v[e] += u[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; e++) v[e] *= w;
-    split8<NS>(v, sc + 8 * idx, 64 * W);
-  }
-}
-
-// D = A B over ksteps x 16 with A in NA parts (sa elements apart) and B in NB:
-// the products of parts i, j with i + j <= 2.  One thread issues.
-template <int NA, int NB>
-__device__ __forceinline__ void gemm_parts(uint32_t d, const tc::View& A, int sa, const tc::View& B, int sb, int N,
-                                           int ksteps) {
-  const uint32_t id = tc::idesc_bf16(64, N, A.mn, B.mn);
-  const uint64_t da = tc::vstep(A), db = tc::vstep(B);
-  uint32_t acc = 0;
-#pragma unroll
-  for (int i = 0; i < NA; i++)
-#pragma unroll
-    for (int j = 0; j < NB; j++) {
-      if (i + j > 2) continue;
-      uint64_t a = tc::vdesc(A, A.hi + i * sa, 0), b = tc::vdesc(B, B.hi + j * sb, 0);
-      for (int ks = 0; ks < ksteps; ks++) {
-        tc::mma_issue(d, a, b, id, acc);
-        acc = 1;
-        a += da;
-        b += db;
-      }
-    }
-}
-__device__ __forceinline__ tc::View kview(const bf16* p, int Kc) { return tc::View{p, nullptr, Kc, 0, 0, false}; }
-__device__ __forceinline__ tc::View mview(const bf16* p, int Kc) { return tc::View{p, nullptr, Kc, 0, 0, true}; }
-
-template <int NT>
-__device__ __forceinline__ void ld_tiles(uint32_t tbase, int c0, float (&v)[NT][4]) {
-  if constexpr (NT <= 4) {
-    tc::ld_frag<NT>(tbase, c0, v);
-  } else {
-#pragma unroll
-    for (int b = 0; b < NT / 4; b++) {
-      float t[4][4];
-      tc::ld_frag<4>(tbase, c0 + 32 * b, t);
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) v[4 * b + j][e] = t[j][e];
-    }
-  }
-}
-
-// ------------------------------------------------------------ chain shape
+// ------------------------------------------------------------ bf16 chain
 // DEC: 0 plain, 1 the dq chain with the decay gradient's A, B, D, E, 2 the dk
 // chain with its C, 3 state only (a segment's own state), 4 the same with R^.
-template <int DK, int DVS, typename T, int DEC>
+template <int DK, int DVS, int DEC>
 struct Shape {
-  static constexpr bool F = sizeof(T) == 4;
-  static constexpr int NX = F ? 3 : 1;      // parts of an input tile
-  static constexpr int NS = F ? 3 : 2;      // parts of a computed operand
-  static constexpr bool ONLY = DEC >= 3;    // no output rows
+  static constexpr bool ONLY = DEC >= 3;
   static constexpr bool HASR = DEC == 1 || DEC == 4;
-  static constexpr bool SCY = DK < DVS;     // the narrower of y and z carries the state weights
-  static constexpr int SCW = SCY ? DK : DVS;
-  // two stages of input tiles where that leaves two CTAs per SM
-  static constexpr int STG = !F && (DK <= 64 || ONLY) && DEC != 1 ? 2 : 1;
-  static constexpr int XE = ONLY ? 0 : NX * 64 * DK, YE = NX * 64 * DK, ZE = NX * 64 * DVS;
-  static constexpr int STAGE = XE + YE + ZE;
-  static constexpr int SE = ONLY ? 0 : NS * DVS * DK, SCE = NS * 64 * SCW, PE = ONLY ? 0 : NS * 64 * 64;
-  static constexpr int QE = DEC == 1 ? NX * 64 * DVS : 0, RE = DEC == 1 ? NS * DVS * DK : 0;
-  // 512 bytes after the tiles: an M = 64 view of a 32-column tile reads up to four cores past it
-  static constexpr int ELEMS = STG * STAGE + SE + SCE + PE + QE + RE + 256;
-  static constexpr int TMEM = DEC == 1 || 64 + DK > 128 ? 256 : 128;
-  static constexpr int SMEM = ELEMS * 2 + 1024 /* lut */ + 512 /* tab, sw */ + 256 /* sw */ + 64;
-  static constexpr int NTV = DVS / 16;      // 8-column tiles of a warp's half of the value side
-  static constexpr int NTK = DK / 16;       // and of the key side
+  static constexpr bool HASW = DEC == 1 || DEC == 2;  // a further row tile: q or k beside the output's columns
+  static constexpr int NW = DVS / 16, NTH = 32 * NW;
+  // bytes of the tiles of a stage (multiples of the swizzle's 1024)
+  static constexpr int XB = ONLY ? 0 : 128 * DK, YB = 128 * DK, ZB = 128 * DVS, WB = HASW ? 128 * DVS : 0;
+  static constexpr int STAGE = XB + YB + ZB + WB;
+  static constexpr int STG = DEC == 1 && DK == 128 ? 1 : 2;  // (one stage there: two CTAs per SM)
+  static constexpr int PB = ONLY ? 0 : 2 * 64 * 64 * 2;
+  static constexpr int SMEM = 1024 /* alignment */ + STG * STAGE + PB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
+  static constexpr int NTK = DK / 8;       // 8-key tiles of a warp's state rows
+  static constexpr int SP = HASW ? 3 : 2;  // parts of the state as an operand: its rows enter fp32 sums there
+  static constexpr int JG = DK == 128 && HASR ? 2 : 1;  // key groups of the state product (registers)
+  // resident CTAs: what registers and shared memory allow
+  static constexpr int REGS = DK == 128 ? 255 : HASR ? 204 : DK == 64 ? 168 : 128;
+  static constexpr int BY_REG = 65536 / (NTH * REGS), BY_SMEM = 227 * 1024 / (SMEM + 1024);
+  static constexpr int CTAS = BY_REG < BY_SMEM ? (BY_REG < 1 ? 1 : BY_REG) : BY_SMEM;
 };
 
-// Element (value j, key i) of a stored state.
-__device__ __forceinline__ int64_t st_at(int tr, int j, int i, int DK, int DVt) {
-  return tr ? (int64_t)j * DK + i : (int64_t)i * DVt + j;
+// Fragments of a 64-row bf16 tile of W columns as TMA's 128-byte (W = 32:
+// 64-byte) swizzle lays it out; W = 128 is two tiles of 64 columns.  Pattern 1
+// (the 16 x 16 block's rows by bit 0 of the 8 x 8 matrix index, columns by bit
+// 1) reads A(m, k) = X[m][k] and, transposed, B(k, n) = X[k][n]; pattern 2 the
+// other two.
+template <int W, int PAT>
+struct Frag {
+  uint32_t row, x;  // the lane's row offset and its swizzle term
+  __device__ __forceinline__ Frag() {
+    const int lane = threadIdx.x & 31, l7 = lane & 7, mi = lane >> 3;
+    const int r = PAT == 1 ? mi & 1 : mi >> 1, b = PAT == 1 ? mi >> 1 : mi & 1;
+    row = (l7 + 8 * r) * (W == 32 ? 64 : 128);
+    x = (uint32_t)(b ^ (W == 32 ? (l7 >> 1) & 3 : l7)) << 4;
+  }
+  // block of rows r0 .. (a multiple of 8), columns c0 .. (a multiple of 16)
+  __device__ __forceinline__ uint32_t at(uint32_t base, int r0, int c0) const {
+    if (W == 32) return base + r0 * 64 + row + (((uint32_t)c0 * 2) ^ x);
+    return base + (c0 >> 6) * 8192 + r0 * 128 + row + (((uint32_t)(c0 & 63) * 2) ^ x);
+  }
+};
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// Transposes 8x8 tiles on the way to shared memory (register pairs along rows).
+__device__ __forceinline__ void stsm4t(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(mma::smem_u32(p)), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float even(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float odd(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The 16 x 16 blocks (row r, column c <= r) of a chunk's pairs that a warp
+// forms, a byte 4 r + c + 1 each, 0 ends: ten over four warps or two.
+template <int NW>
+__device__ __forceinline__ uint64_t pair_blocks(int warp) {
+  if (NW == 2) return warp == 0 ? 0x01100f0e0dull : 0x06050b0a09ull;
+  return warp == 0 ? 0x0f0e0dull : warp == 1 ? 0x0a0910ull : warp == 2 ? 0x050bull : 0x0106ull;
 }
 
-template <int DK, int DVS, typename T, int DEC>
-__device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
-  using SH = Shape<DK, DVS, T, DEC>;
-  constexpr int NX = SH::NX, NS = SH::NS, NTV = SH::NTV, NTK = SH::NTK;
+// The tensors of a chain as [Ntok][H d] maps with boxes of 64 tokens.
+struct LinMaps {
+  CUtensorMap x, y, z, w;
+};
+
+// One CTA carries one chain of a DVS-column value slice.  Warp w holds the
+// state's value rows 16 w .. of S^T as fp32 accumulator fragments for the whole
+// chain; per chunk
+//   pairs  P = w (x y^T), the ten 16 x 16 blocks on and below the diagonal
+//          shared out over the warps, to shared memory as two parts
+//   o^T    = row weight * (S^T x^T) (S as register fragments) + z^T P^T
+//   S^T    = e^{-an} S^T + (weighted z)^T y
+// so that the state never leaves its registers and a chunk needs two barriers.
+// Tokens lie in memory order in both directions; in reverse the blocks are
+// walked from the other end (blk) and the weights run the other way.
+// mma.sync rather than tcgen05: the chain is bound by the instructions around
+// its products, and accumulators that are the next product's operands save
+// the round trips through TMEM and shared memory.
+template <int DK, int DVS, int DEC>
+__device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u, int h, int slice) {
+  using SH = Shape<DK, DVS, DEC>;
+  constexpr int NTH = SH::NTH, NW = SH::NW, NTK = SH::NTK, SP = SH::SP;
   constexpr bool ONLY = SH::ONLY;
-  extern __shared__ __align__(1024) unsigned char smem[];
-  bf16* stage0 = reinterpret_cast<bf16*>(smem);
-  bf16* tS = stage0 + SH::STG * SH::STAGE;
-  bf16* tSC = tS + SH::SE;
-  bf16* tP = tSC + SH::SCE;
-  bf16* tQ = tP + SH::PE;
-  bf16* tR = tQ + SH::QE;
-  float2* lut = reinterpret_cast<float2*>(smem + SH::ELEMS * 2);  // [128] (w(m), w(m - 1)), m = index - 64
-  float* tab = reinterpret_cast<float*>(lut + 128);               // [65] e^{-a m}
-  float* sw = tab + 96;                                           // [64] state weights of the chunk's rows
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sw + 64);
-  uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 1);
-  int* s_fail = reinterpret_cast<int*>(slot + 1);
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (mma::smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* tP = smem + SH::STG * SH::STAGE;  // [2 parts][64][64]
+  float2* lut = reinterpret_cast<float2*>(tP + SH::PB);
+  float* tab = reinterpret_cast<float*>(lut + 128);  // [65] e^{-a m}
+  float* sw = tab + 96;                              // [64] weights of the chunk's rows in its state
+  float* rwt = sw + 64;                              // [64] weights of the entry state in its rows
+  uint64_t* bar = reinterpret_cast<uint64_t*>(rwt + 64);  // [STG]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
-  const int q4 = warp & 3, half = warp >> 2, r0 = 16 * q4 + gq;
 
   Unit un;
   if (!unit_of(P, u, un)) return;
   const int nseg = P.seg ? max(1, (un.dlen + P.L - 1) / P.L) : 1;
   if (ONLY && un.seg == (op.rev ? 0 : nseg - 1)) return;  // the last segment of its direction feeds nobody
   const int H = P.H, DVt = op.DVt, c0 = slice * DVS;
+  const int64_t stN = (int64_t)DK * DVt;
   const float a = decay_of(P.A_log, h);
-
-  if (warp == 0) tc::tmem_alloc(slot, SH::TMEM);
-  if (tid == 0) {
-    mma::mbar_init(bar, 1);
-    mma::mbar_init_fence();
-    *s_fail = 0;
-  }
-  if (tid < 65) tab[tid] = decay_pow(a, tid);
-  __syncthreads();
-  if (tid < 128) {
-    const int m = tid - 64;
-    lut[tid] = make_float2(m >= 0 ? P.scale * tab[m] : 0.f, m >= 1 ? P.scale * tab[m - 1] : 0.f);
-  }
-  tc::fence_after();
-  const uint32_t tm = *slot;
-
   const int nch = (un.ntok + C - 1) / C;
-  auto rows_of = [&](int c) {
-    const int idx = op.rev ? nch - 1 - c : c;
-    const int n = min(C, un.ntok - idx * C);
-    Rows r;
-    r.n = n;
-    r.dir = op.rev ? -1 : 1;
-    r.t0 = un.tok0 + idx * C + (op.rev ? n - 1 : 0);
-    return r;
-  };
-  auto load_x = [&](int c) {
-    if constexpr (!ONLY) load_tile<DK>(stage0 + (c % SH::STG) * SH::STAGE, (const T*)op.x, rows_of(c), H, h, DK, 0);
-  };
-  auto load_yz = [&](int c) {
-    bf16* s = stage0 + (c % SH::STG) * SH::STAGE + SH::XE;
-    load_tile<DK>(s, (const T*)op.y, rows_of(c), H, h, DK, 0);
-    load_tile<DVS>(s + SH::YE, (const T*)op.z, rows_of(c), H, h, DVt, c0);
-    if constexpr (DEC == 1) load_tile<DVS>(tQ, (const T*)op.wx, rows_of(c), H, h, DVt, c0);
-  };
-  if (!SH::F && nch > 0) {
-    load_x(0);
-    load_yz(0);
-    mma::cp_commit();
-  }
+  const bool rev = op.rev != 0;
+  auto blk = [&](int t) { return rev ? 3 - t : t; };  // 16-token block t in the chain's direction
 
-  // ---- the state at the unit's start: the initial state and the earlier segments, decayed to here
-  const bool st_rows = 16 * q4 < DVS;  // a warp whose rows exist (DVS = 32: warps 0, 1 of each half)
+  auto load = [&](int c) {  // one thread
+    const int t0 = un.tok0 + C * (rev ? nch - 1 - c : c), s = SH::STG == 2 ? c & 1 : 0;
+    unsigned char* p = smem + s * SH::STAGE;
+    mma::mbar_expect_tx(bar + s, SH::STAGE);
+#pragma unroll
+    for (int b = 0; b < (DK + 63) / 64; b++) {
+      if constexpr (!ONLY) mma::tma_load_2d(p + 8192 * b, &maps.x, h * DK + 64 * b, t0, bar + s);
+      mma::tma_load_2d(p + SH::XB + 8192 * b, &maps.y, h * DK + 64 * b, t0, bar + s);
+    }
+    mma::tma_load_2d(p + SH::XB + SH::YB, &maps.z, h * DVt + c0, t0, bar + s);
+    if constexpr (SH::HASW) mma::tma_load_2d(p + SH::XB + SH::YB + SH::ZB, &maps.w, h * DVt + c0, t0, bar + s);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < SH::STG; s++) mma::mbar_init(bar + s, 1);
+    mma::mbar_init_fence();
+    if (nch > 0) load(0);
+  }
+  for (int i = tid; i < 65; i += NTH) tab[i] = decay_pow(a, i);
+  __syncthreads();
+  for (int i = tid; i < 128; i += NTH) {  // weights of a pair of neighbouring columns at distances m and m -+ 1
+    const int m = i - 64, m2 = rev ? m + 1 : m - 1;
+    lut[i] = make_float2(m >= 0 ? P.scale * tab[m] : 0.f, m2 >= 0 ? P.scale * tab[m2] : 0.f);
+  }
+  int n_w = -1;  // rows for which sw and rwt are set
+
   float S[NTK][4], R[SH::HASR ? NTK : 1][4];
   mma::zero<NTK>(S);
   mma::zero<SH::HASR ? NTK : 1>(R);
-  if (!ONLY && st_rows) {
-    const int64_t stN = (int64_t)DK * DVt;
-    auto each_st = [&](auto fn) {
+  auto each_st = [&](auto fn) {
 #pragma unroll
-      for (int j = 0; j < NTK; j++)
+    for (int j = 0; j < NTK; j++)
 #pragma unroll
-        for (int e = 0; e < 4; e++)
-          fn(j, e, st_at(op.tr, c0 + r0 + 8 * (e >> 1), half * (DK / 2) + 8 * j + 2 * tq + (e & 1), DK, DVt));
-    };
-    const int age0 = op.rev ? un.dlen - un.seg * P.L - un.ntok : un.seg * P.L;
-    if (op.init) {
-      const float* p = op.init + ((int64_t)un.doc * H + h) * stN;
-      const float w = decay_pow(a, age0) * (op.rev ? 1.0f / P.scale : 1.0f);
-      each_st([&](int j, int e, int64_t at) {
-        const float v = w * p[at];
-        S[j][e] = v;
-        if constexpr (DEC == 1) R[j][e] = (float)age0 * v;
-      });
-    }
-    if (op.segc) {
-      const int r1 = op.rev ? un.seg + 1 : 0, r2 = op.rev ? nseg : un.seg;
-      for (int r = r1; r < r2; r++) {
-        const int age = P.L * (op.rev ? r - un.seg - 1 : un.seg - 1 - r);
-        const float w = decay_pow(a, age);
-        const float* p = op.segc + ((int64_t)(u - un.seg + r) * H + h) * stN * (op.rev ? 1 : 2);
-        each_st([&](int j, int e, int64_t at) {
-          const float v = p[at];
-          S[j][e] = fmaf(w, v, S[j][e]);
-          if constexpr (DEC == 1) R[j][e] = fmaf(w, fmaf((float)age, v, p[stN + at]), R[j][e]);
-        });
-      }
-    }
-  }
-  auto put_state = [&]() {
-    if (st_rows) {
-#pragma unroll
-      for (int j = 0; j < NTK; j++)
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-          const int at = mma::opix(r0 + 8 * k, half * (DK / 2) + 8 * j + 2 * tq, DK);
-          split2<NS>(S[j][2 * k], S[j][2 * k + 1], tS + at, DVS * DK);
-          if constexpr (DEC == 1) split2<NS>(R[j][2 * k], R[j][2 * k + 1], tR + at, DVS * DK);
-        }
-    }
+      for (int e = 0; e < 4; e++)
+        fn(S[j][e], R[SH::HASR ? j : 0][e],
+           st_at(op.tr, c0 + 16 * warp + gq + 8 * (e >> 1), 8 * j + 2 * tq + (e & 1), DK, DVt));
   };
-  if constexpr (!ONLY) put_state();
+  if (!ONLY) start_state<DEC == 1>(P, op, un, u, h, nseg, a, stN, each_st);
+
+  const Frag<DK, 1> k1;   // x and y tiles
+  const Frag<DK, 2> k2;
+  const Frag<DVS, 1> v1;  // z and w tiles
+  const Frag<DVS, 2> v2;
+  const Frag<64, 2> p2;   // pairs
 
   double dacc = 0.0;  // this thread's part of the decay gradient's sums
-  uint32_t ph = 0;
   bool good = true;
   for (int c = 0; c < nch; c++) {
-    const Rows rw = rows_of(c);
-    const int n = rw.n;
-    bf16* tX = stage0 + (c % SH::STG) * SH::STAGE;
-    bf16 *tY = tX + SH::XE, *tZ = tY + SH::YE;
-    if (tid < C) sw[tid] = tid < n ? tab[n - 1 - tid + (op.rev ? 1 : 0)] : 0.f;
-    if constexpr (SH::F) {
-      load_x(c);
-      load_yz(c);
-    } else {
-      mma::cp_wait_all();
-    }
-    [[maybe_unused]] float kx[NTV][4];
-    if constexpr (DEC == 2) {  // k's rows in fragment order, used after the first products
-#pragma unroll
-      for (int j = 0; j < NTV; j++)
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-          const int row = r0 + 8 * k;
-          const T* p = (const T*)op.wx + ((rw.t0 + (int64_t)rw.dir * (row < n ? row : 0)) * H + h) * DVt + c0 +
-                       half * (DVS / 2) + 8 * j + 2 * tq;
-          kx[j][2 * k] = row < n ? ldf(p) : 0.f;
-          kx[j][2 * k + 1] = row < n ? ldf(p + 1) : 0.f;
-        }
-    }
-    __syncthreads();  // sw
-    scale_tile<SH::SCW, NX, NS>(tSC, SH::SCY ? tY : tZ, sw);
-    mma::fence_async_smem();
-    tc::fence_before();
-    __syncthreads();
-    if (SH::STG == 2 && c + 1 < nch) {  // the other stage's last readers finished in the chunk before
-      load_x(c + 1);
-      load_yz(c + 1);
-      mma::cp_commit();
-    }
-    float o[NTV][4];
-    if constexpr (!ONLY) {
-      if (tid == 0) {
-        tc::fence_after();
-        gemm_parts<NX, NX>(tm, kview(tX, DK), 64 * DK, kview(tY, DK), 64 * DK, 64, DK / 16);
-        gemm_parts<NX, NS>(tm + 64, kview(tX, DK), 64 * DK, kview(tS, DK), DVS * DK, DVS, DK / 16);
-        if constexpr (DEC == 1) {
-          gemm_parts<NX, NX>(tm + 128, kview(tQ, DVS), 64 * DVS, kview(tZ, DVS), 64 * DVS, 64, DVS / 16);
-          gemm_parts<NX, NS>(tm + 192, kview(tX, DK), 64 * DK, kview(tR, DK), DVS * DK, DVS, DK / 16);
-        }
-        tc::commit(bar);
+    const int idx = rev ? nch - 1 - c : c, t0 = un.tok0 + C * idx, n = min(C, un.ntok - C * idx);
+    const int st = SH::STG == 2 ? c & 1 : 0;
+    unsigned char* stg = smem + st * SH::STAGE;
+    const uint32_t tX = mma::smem_u32(stg), tY = tX + SH::XB, tZ = tY + SH::YB, tW = tZ + SH::ZB;
+    good = mma::mbar_wait(bar + st, (SH::STG == 2 ? c >> 1 : c) & 1);
+    if (n != n_w) {  // the first chunk, and the one that is not full
+      if (n_w >= 0) __syncthreads();
+      for (int i = tid; i < C; i += NTH) {
+        sw[i] = i < n ? tab[rev ? i + 1 : n - 1 - i] : 0.f;
+        rwt[i] = i < n ? P.scale * tab[rev ? n - 1 - i : i + 1] : 0.f;
       }
-      __syncwarp();
-      if (!mma::mbar_wait(bar, ph)) *s_fail = 1;
-      ph ^= 1;
-      tc::fence_after();
-      if (!SH::F && SH::STG == 1 && c + 1 < nch) {  // x has been read
-        load_x(c + 1);
-        mma::cp_commit();
-      }
-      float p[4][4];
-      ld_tiles<4>(tm, half * 32, p);
-      float part = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-          const int row = r0 + 8 * k, col = half * 32 + 8 * j + 2 * tq;
-          const float2 w = lut[64 + row - col];
-          p[j][2 * k] *= w.x;
-          p[j][2 * k + 1] *= w.y;
-          split2<NS>(p[j][2 * k], p[j][2 * k + 1], tP + mma::opix(row, col, 64), 64 * 64);
-        }
-      const float rs[2] = {P.scale * tab[r0 + (op.rev ? 0 : 1)], P.scale * tab[r0 + 8 + (op.rev ? 0 : 1)]};
-      ld_tiles<NTV>(tm + 64, half * (DVS / 2), o);
-      if constexpr (DEC == 1) {
-        {  // A: pairs inside the chunk
-          float m2[4][4];
-          ld_tiles<4>(tm + 128, half * 32, m2);
-#pragma unroll
-          for (int j = 0; j < 4; j++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-              const int d = r0 + 8 * (e >> 1) - (half * 32 + 8 * j + 2 * tq + (e & 1));
-              part = fmaf((float)d * p[j][e], m2[j][e], part);
-            }
-        }
-        float qr[NTV][4];
-        ld_tiles<NTV>(tm + 192, half * (DVS / 2), qr);
-#pragma unroll
-        for (int j = 0; j < NTV; j++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) {  // B and D
-            const int row = r0 + 8 * (e >> 1), at = mma::opix(row, half * (DVS / 2) + 8 * j + 2 * tq + (e & 1), DVS);
-            float qv = 0.f;
-#pragma unroll
-            for (int b = 0; b < NX; b++) qv += __bfloat162float(tQ[b * 64 * DVS + at]);
-            part = fmaf(rs[e >> 1] * qv, fmaf((float)(row + 1), o[j][e], qr[j][e]), part);
-          }
-      }
-#pragma unroll
-      for (int j = 0; j < NTV; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          o[j][e] *= rs[e >> 1];
-          if constexpr (DEC == 2) part = fmaf((float)(r0 + 8 * (e >> 1)) * kx[j][e], o[j][e], part);
-        }
-      if constexpr (DEC == 1 || DEC == 2) dacc += (double)part;
-      mma::fence_async_smem();
-      tc::fence_before();
-      __syncthreads();
-    }
-    if (tid == 0) {
-      tc::fence_after();
-      // S'^T += z^T (weighted) y: rows are the value columns
-      if constexpr (SH::SCY)
-        gemm_parts<NX, NS>(tm + 64, mview(tZ, DVS), 64 * DVS, mview(tSC, DK), 64 * DK, DK, 4);
-      else
-        gemm_parts<NS, NX>(tm + 64, mview(tSC, DVS), 64 * DVS, mview(tY, DK), 64 * DK, DK, 4);
-      if constexpr (!ONLY) gemm_parts<NS, NX>(tm, kview(tP, 64), 64 * 64, mview(tZ, DVS), 64 * DVS, DVS, 4);
-      tc::commit(bar);
-    }
-    __syncwarp();
-    if (!mma::mbar_wait(bar, ph)) *s_fail = 1;
-    ph ^= 1;
-    tc::fence_after();
-    if (!SH::F && SH::STG == 1 && c + 1 < nch) {
-      if (ONLY) load_x(c + 1);
-      load_yz(c + 1);
-      mma::cp_commit();
-    }
-    {  // S' = e^{-an} S + ...: as S + (e^{-an} - 1) S where the decay is slow, so that its rounding is
-       // relative to what a chunk loses and hundreds of chunks add up no bias; as a product where it
-       // is fast, where that sum would cancel
-      const bool slow = a * (float)n < 0.5f;
-      const float g = slow ? expm1f(-a * (float)n) : expf(-a * (float)n);
-      float d[NTK][4];
-      ld_tiles<NTK>(tm + 64, half * (DK / 2), d);
-#pragma unroll
-      for (int j = 0; j < NTK; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          if constexpr (SH::HASR) {
-            const float t = fmaf((float)n, S[j][e], R[j][e]);
-            R[j][e] = fmaf(g, t, slow ? t : 0.f);
-          }
-          S[j][e] = fmaf(g, S[j][e], slow ? S[j][e] : 0.f) + d[j][e];
-        }
-    }
-    if constexpr (!ONLY) {
-      if (c + 1 < nch) put_state();
-      float v[NTV][4];
-      ld_tiles<NTV>(tm, half * (DVS / 2), v);
-#pragma unroll
-      for (int k = 0; k < 2; k++) {
-        const int row = r0 + 8 * k;
-        T* po = (T*)op.out + ((rw.t0 + (int64_t)rw.dir * row) * H + h) * DVt + c0 + half * (DVS / 2);
-        if constexpr (SH::F) {
-          if (row < n) {
-#pragma unroll
-            for (int j = 0; j < NTV; j++)
-              *reinterpret_cast<float2*>(po + 8 * j + 2 * tq) =
-                  make_float2(o[j][2 * k] + v[j][2 * k], o[j][2 * k + 1] + v[j][2 * k + 1]);
-          }
-        } else {
-          uint32_t w[NTV];
-#pragma unroll
-          for (int j = 0; j < NTV; j++) {
-            const __nv_bfloat162 b2 =
-                __floats2bfloat162_rn(o[j][2 * k] + v[j][2 * k], o[j][2 * k + 1] + v[j][2 * k + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&b2);
-          }
-          if constexpr (NTV == 4) {  // transpose the quad: lane tq gets the 8 columns of tile tq
-            uint32_t t[4];
-#pragma unroll
-            for (int x = 0; x < 4; x++) {
-              uint32_t give = w[0];
-#pragma unroll
-              for (int y = 1; y < 4; y++)
-                if ((tq ^ x) == y) give = w[y];
-              t[x] = __shfl_xor_sync(0xffffffffu, give, x);
-            }
-            uint4 st;
-            uint32_t* sp = reinterpret_cast<uint32_t*>(&st);
-#pragma unroll
-            for (int x = 0; x < 4; x++) {
-              // t[x] came from lane tq ^ x: word tq ^ x of this lane's tile
-#pragma unroll
-              for (int y = 0; y < 4; y++)
-                if ((tq ^ x) == y) sp[y] = t[x];
-            }
-            if (row < n) *reinterpret_cast<uint4*>(po + 8 * tq) = st;
-          } else {
-            if (row < n) {
-#pragma unroll
-              for (int j = 0; j < NTV; j++) *reinterpret_cast<uint32_t*>(po + 8 * j + 2 * tq) = w[j];
-            }
-          }
+      n_w = n;
+      // rows past the chunk hold other documents' tokens: zero, so that nothing of them (an infinity)
+      // enters a product.  (64-byte rows: 16-byte groups 4 row ..; 128-byte rows 8 row .. of each 8 KB)
+      if (n < C) {
+        for (int g = tid; g < SH::STAGE / 16; g += NTH) {
+          const int b = 16 * g, dk_rows = DK == 32 ? 64 : 128, dv_rows = DVS == 32 ? 64 : 128;
+          const int row = b < SH::XB + SH::YB ? (b / dk_rows) & 63 : ((b - SH::XB - SH::YB) / dv_rows) & 63;
+          if (row >= n) *reinterpret_cast<uint4*>(stg + b) = make_uint4(0, 0, 0, 0);
         }
       }
     }
-    tc::fence_before();
-    if (*s_fail) {  // a wait ran out: no thread starts another chunk
-      good = false;
-    }
+    mma::fence_async_smem();  // this thread's accesses to the other stage precede the copies into it
+    // this chunk's tiles are complete; every reader of the last one is done
     if (__syncthreads_or(!good)) {
       good = false;
       break;
     }
-  }
-  if (!good && tid == 0) *P.err = KDA_ERR_DEVICE;
-  mma::cp_wait_all();
+    if (SH::STG == 2 && tid == 0 && c + 1 < nch) load(c + 1);
 
-  // ---- the unit's state
-  if (good && st_rows) {
-    const int64_t stN = (int64_t)DK * DVt;
-    const bool last = un.seg == (op.rev ? 0 : nseg - 1);
-    float* pf = nullptr;
-    float mul = 1.0f;
-    if (ONLY) {
-      pf = const_cast<float*>(op.segc) + ((int64_t)u * H + h) * stN * (op.rev ? 1 : 2);
-    } else if (last && op.fin) {
-      pf = op.fin + ((int64_t)un.doc * H + h) * stN;
-      mul = op.rev ? P.scale : 1.0f;
-    }
-    const float* pd = DEC == 1 && last && op.dfin ? op.dfin + ((int64_t)un.doc * H + h) * stN : nullptr;
     float part = 0.f;
+    float o[8][4];
+    if constexpr (!ONLY) {
+      // ---- pairs: three blocks at a time, so that consecutive products are independent
+      for (uint64_t todo = pair_blocks<NW>(warp); todo; todo >>= 24) {
+        int rr[3], cc[3];
+        float p[3][2][4];
 #pragma unroll
-    for (int j = 0; j < NTK; j++)
+        for (int t = 0; t < 3; t++) {
+          int code = (int)(todo >> (8 * t)) & 255;
+          if (!code) code = (int)todo & 255;  // (the first once more, not stored)
+          rr[t] = blk((code - 1) >> 2);
+          cc[t] = blk((code - 1) & 3);
+          mma::zero<2>(p[t]);
+        }
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const int64_t at = st_at(op.tr, c0 + r0 + 8 * (e >> 1), half * (DK / 2) + 8 * j + 2 * tq + (e & 1), DK, DVt);
-        if (pf) pf[at] = mul * S[j][e];
-        if constexpr (DEC == 4) pf[stN + at] = R[j][e];
-        if constexpr (DEC == 1) {
-          if (pd) part = fmaf(R[j][e], pd[at], part);
+        for (int kk = 0; kk < DK / 16; kk++) {
+          uint32_t fa[3][4], fb[3][4];
+#pragma unroll
+          for (int t = 0; t < 3; t++) {
+            ldsm(fa[t], k1.at(tX, 16 * rr[t], 16 * kk));
+            ldsm(fb[t], k2.at(tY, 16 * cc[t], 16 * kk));
+          }
+#pragma unroll
+          for (int t = 0; t < 3; t++) {
+            mma::mma_bf16(p[t][0], fa[t], fb[t][0], fb[t][1]);
+            mma::mma_bf16(p[t][1], fa[t], fb[t][2], fb[t][3]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 3; t++) {
+          if (t > 0 && !((todo >> (8 * t)) & 255)) continue;
+          const int d = 16 * (rr[t] - cc[t]) + gq - 2 * tq;  // row - column of the thread's first pair
+          const float2* lp = lut + 64 + (rev ? -d : d);
+#pragma unroll
+          for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+              const int dd = 8 * k - 8 * j;
+              const float2 w = lp[rev ? -dd : dd];
+              p[t][j][2 * k] *= w.x;
+              p[t][j][2 * k + 1] *= w.y;
+              uint32_t s[2];
+              split2<2>(p[t][j][2 * k], p[t][j][2 * k + 1], s);
+              unsigned char* at = tP + (16 * rr[t] + 8 * k + gq) * 128 + (((2 * cc[t] + j) ^ gq) << 4) + 4 * tq;
+              *reinterpret_cast<uint32_t*>(at) = s[0];
+              *reinterpret_cast<uint32_t*>(at + 8192) = s[1];
+            }
+          if constexpr (DEC == 1) {  // A: the same pairs of q and k (this slice's columns)
+            float m2[2][4];
+            mma::zero<2>(m2);
+#pragma unroll
+            for (int kk = 0; kk < DVS / 16; kk++) {
+              uint32_t fa[4], fb[4];
+              ldsm(fa, v1.at(tW, 16 * rr[t], 16 * kk));
+              ldsm(fb, v2.at(tZ, 16 * cc[t], 16 * kk));
+              mma::mma_bf16(m2[0], fa, fb[0], fb[1]);
+              mma::mma_bf16(m2[1], fa, fb[2], fb[3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+              for (int e = 0; e < 4; e++)
+                part = fmaf((float)(d + 8 * (e >> 1) - 8 * j - (e & 1)) * p[t][j][e], m2[j][e], part);
+          }
         }
       }
-    dacc += (double)part;
+      // ---- the entry state's rows: o^T = S^T x^T, and R^'s for the decay gradient
+      auto state_rows = [&](float (&acc)[8][4], const float (&st_)[NTK][4]) {
+        mma::zero<8>(acc);
+#pragma unroll
+        for (int kk = 0; kk < DK / 16; kk++) {
+          uint32_t f[SP][4], fb[4][4];
+#pragma unroll
+          for (int p = 0; p < 4; p++) ldsm(fb[p], k2.at(tX, 16 * blk(p), 16 * kk));
+#pragma unroll
+          for (int q = 0; q < 4; q++) {  // accumulator tiles 2 kk, 2 kk + 1 are the 16 x 16 operand
+            uint32_t s[SP];
+            split2<SP>(st_[2 * kk + (q >> 1)][2 * (q & 1)], st_[2 * kk + (q >> 1)][2 * (q & 1) + 1], s);
+#pragma unroll
+            for (int b = 0; b < SP; b++) f[b][q] = s[b];
+          }
+#pragma unroll
+          for (int b = SP - 1; b >= 0; b--)
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+              mma::mma_bf16(acc[2 * p], f[b], fb[p][0], fb[p][1]);
+              mma::mma_bf16(acc[2 * p + 1], f[b], fb[p][2], fb[p][3]);
+            }
+        }
+      };
+      state_rows(o, S);
+      if constexpr (DEC == 1) {  // B and D
+        float qr[8][4];
+        state_rows(qr, R);
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+          uint32_t f[4];
+          ldsm_t(f, v2.at(tW, 16 * p, 16 * warp));
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            const int j = 2 * p + (q >> 1), e = 2 * (q & 1), i = 8 * j + 2 * tq;
+            const float2 w = *reinterpret_cast<const float2*>(rwt + i);
+            part = fmaf(w.x * even(f[q]), fmaf((float)(i + 1), o[j][e], qr[j][e]), part);
+            part = fmaf(w.y * odd(f[q]), fmaf((float)(i + 2), o[j][e + 1], qr[j][e + 1]), part);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const float2 w = *reinterpret_cast<const float2*>(rwt + 16 * blk(j >> 1) + 8 * (j & 1) + 2 * tq);
+        o[j][0] *= w.x;
+        o[j][1] *= w.y;
+        o[j][2] *= w.x;
+        o[j][3] *= w.y;
+      }
+      if constexpr (DEC == 2) {  // C
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+          uint32_t f[4];
+          ldsm_t(f, v2.at(tW, 16 * blk(p), 16 * warp));
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            const int j = 2 * p + (q >> 1), e = 2 * (q & 1), i = n - 1 - (16 * blk(p) + 8 * (q >> 1) + 2 * tq);
+            part = fmaf((float)i * even(f[q]), o[j][e], part);
+            part = fmaf((float)(i - 1) * odd(f[q]), o[j][e + 1], part);
+          }
+        }
+      }
+      if constexpr (SH::HASW) dacc += (double)part;
+    }
+    // ---- the state: S^T = e^{-an} S^T + (weighted z)^T y.  The product is summed apart from the
+    // state (the tensor core truncates what an addition shifts out: into a long chain's state that
+    // would be a bias), smallest parts first.
+    uint32_t zr[4][4];
+#pragma unroll
+    for (int kk = 0; kk < 4; kk++) ldsm_t(zr[kk], v2.at(tZ, 16 * blk(kk), 16 * warp));
+    const Decay dec(a, n);
+#pragma unroll
+    for (int g = 0; g < SH::JG; g++) {
+      constexpr int NG = NTK / SH::JG;
+      float d[NG][4];
+      mma::zero<NG>(d);
+#pragma unroll
+      for (int kk = 0; kk < 4; kk++) {
+        uint32_t fb[NG / 2][4];
+#pragma unroll
+        for (int p = 0; p < NG / 2; p++) ldsm_t(fb[p], k1.at(tY, 16 * blk(kk), 8 * NG * g + 16 * p));
+        uint32_t za[3][4];
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const float2 w = *reinterpret_cast<const float2*>(sw + 16 * blk(kk) + 8 * (q >> 1) + 2 * tq);
+          uint32_t s[3];
+          split2<3>(w.x * even(zr[kk][q]), w.y * odd(zr[kk][q]), s);
+#pragma unroll
+          for (int b = 0; b < 3; b++) za[b][q] = s[b];
+        }
+#pragma unroll
+        for (int b = 2; b >= 0; b--)
+#pragma unroll
+          for (int p = 0; p < NG / 2; p++) {
+            mma::mma_bf16(d[2 * p], za[b], fb[p][0], fb[p][1]);
+            mma::mma_bf16(d[2 * p + 1], za[b], fb[p][2], fb[p][3]);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < NG; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          float& s = S[NG * g + j][e];
+          if constexpr (SH::HASR) R[NG * g + j][e] = dec(fmaf((float)n, s, R[NG * g + j][e]));
+          s = dec(s) + d[j][e];
+        }
+    }
+    if constexpr (!ONLY) {
+      __syncthreads();  // the pairs of every warp; x and y have been read
+      // ---- o^T += z^T P^T
+#pragma unroll
+      for (int kk = 0; kk < 4; kk++)
+#pragma unroll
+        for (int b = 1; b >= 0; b--) {
+          uint32_t fb[4][4];
+#pragma unroll
+          for (int p = kk; p < 4; p++) ldsm(fb[p], p2.at(mma::smem_u32(tP) + 8192 * b, 16 * blk(p), 16 * blk(kk)));
+#pragma unroll
+          for (int p = kk; p < 4; p++) {
+            mma::mma_bf16(o[2 * p], zr[kk], fb[p][0], fb[p][1]);
+            mma::mma_bf16(o[2 * p + 1], zr[kk], fb[p][2], fb[p][3]);
+          }
+        }
+      // ---- out: transposed through the warp's 2 KB of the x and y tiles, 16 bytes a lane
+      bf16* tO = reinterpret_cast<bf16*>(stg) + warp * 64 * 16;
+#pragma unroll
+      for (int p = 0; p < 4; p++)  // four 8 x 8 tiles: 16 tokens by the warp's 16 columns
+        stsm4t(tO + (4 * p + (lane >> 3)) * 64 + (lane & 7) * 8, pack2(o[2 * p][0], o[2 * p][1]),
+               pack2(o[2 * p][2], o[2 * p][3]), pack2(o[2 * p + 1][0], o[2 * p + 1][1]),
+               pack2(o[2 * p + 1][2], o[2 * p + 1][3]));
+      __syncwarp();
+      bf16* po = (bf16*)op.out + ((int64_t)t0 * H + h) * DVt + c0 + 16 * warp;
+#pragma unroll
+      for (int p = 0; p < 4; p++) {
+        const int m = lane >> 3, row = 16 * blk(p) + 8 * (m >> 1) + (lane & 7);
+        const uint4 v = *reinterpret_cast<const uint4*>(tO + (4 * p + m) * 64 + (lane & 7) * 8);
+        if (row < n) *reinterpret_cast<uint4*>(po + (int64_t)row * H * DVt + 8 * (m & 1)) = v;
+      }
+    }
+    if (SH::STG == 1 && c + 1 < nch) {
+      mma::fence_async_smem();
+      __syncthreads();
+      if (tid == 0) load(c + 1);
+    }
   }
-  __syncthreads();
-  if constexpr (DEC == 1 || DEC == 2) {  // the CTA's partial, summed in a fixed order
-    double* red = reinterpret_cast<double*>(smem);
+  if (!good) {  // a wait ran out
+    if (tid == 0) *P.err = KDA_ERR_DEVICE;
+    return;
+  }
+
+  // ---- the unit's state
+  const bool last = un.seg == (rev ? 0 : nseg - 1);
+  float* pf = nullptr;
+  float mul = 1.0f;
+  if (ONLY) {
+    pf = const_cast<float*>(op.segc) + ((int64_t)u * H + h) * stN * (rev ? 1 : 2);
+  } else if (last && op.fin) {
+    pf = op.fin + ((int64_t)un.doc * H + h) * stN;
+    mul = rev ? P.scale : 1.0f;
+  }
+  const float* pd = DEC == 1 && last && op.dfin ? op.dfin + ((int64_t)un.doc * H + h) * stN : nullptr;
+  float part = 0.f;
+  each_st([&](float& s, float& r, int64_t at) {
+    if (pf) pf[at] = mul * s;
+    if constexpr (DEC == 4) pf[stN + at] = r;
+    if constexpr (DEC == 1) {
+      if (pd) part = fmaf(r, pd[at], part);
+    }
+  });
+  if constexpr (SH::HASW) {  // the CTA's partial, summed in a fixed order
+    dacc += (double)part;
+    double* red = reinterpret_cast<double*>(lut);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) dacc += __shfl_xor_sync(0xffffffffu, dacc, s);
+    __syncthreads();
     if (lane == 0) red[warp] = dacc;
     __syncthreads();
     if (tid == 0) {
       double s = 0.0;
-      for (int w = 0; w < LTH / 32; w++) s += red[w];
+      for (int w = 0; w < NW; w++) s += red[w];
       op.pda[((int64_t)u * H + h) * (DVt / DVS) + slice] = s;
     }
   }
-  if (warp == 0) tc::tmem_dealloc(tm, SH::TMEM);
 }
 
-template <int DK, int DVS, typename T, int DEC>
-__global__ void __launch_bounds__(LTH, Shape<DK, DVS, T, DEC>::SMEM <= 113 * 1024 ? 2 : 1)
-    lin_chain_kernel(LinP P, LinOp op, int fwd) {
+template <int DK, int DVS, int DEC>
+__global__ void __launch_bounds__(Shape<DK, DVS, DEC>::NTH, Shape<DK, DVS, DEC>::CTAS)
+    lin_chain_kernel(const __grid_constant__ LinMaps maps, LinP P, LinOp op, int fwd) {
+  if (!ready(P, fwd)) return;
   const int ns = op.DVt / DVS;
-  const int slice = blockIdx.x % ns, h = (blockIdx.x / ns) % P.H, u = blockIdx.x / (ns * P.H);
-  if (fwd == 1) {
-    rows_reset(P);
-  } else if (fwd == 2) {  // after this forward's first kernel
-    if (*P.err != KDA_OK) return;
-  } else if (*P.wtag != P.tag || *P.err != KDA_OK) {  // no forward saved this workspace, or it failed
-    if (threadIdx.x == 0 && *P.wtag != P.tag) *P.err = KDA_ERR_WORKSPACE;
-    return;
-  }
-  chain<DK, DVS, T, DEC>(P, op, u, h, slice);
+  chain<DK, DVS, DEC>(P, op, maps, blockIdx.x / (ns * P.H), (blockIdx.x / ns) % P.H, blockIdx.x % ns);
 }
 
 // dA_log[h] = -a (sum of the partials), in a fixed order.
@@ -754,42 +574,37 @@ __global__ void __launch_bounds__(256) lin_decay_kernel(LinP P, const double* p1
 }
 
 // ------------------------------------------------------------ launches
-// The dynamic shared memory limit of kernel K, raised once per device.
-template <auto K>
-cudaError_t raise_smem(int bytes) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (dev < 64 && (done.load() & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) done.fetch_or(bit);
-  return e;
-}
-
-template <int DK, int DVS, typename T, int DEC>
+template <int DK, int DVS, int DEC>
 cudaError_t launch_chain(int kid, const LinP& P, const LinOp& op, int fwd, cudaStream_t st) {
-  constexpr int smem = Shape<DK, DVS, T, DEC>::SMEM;
-  cudaError_t e = raise_smem<lin_chain_kernel<DK, DVS, T, DEC>>(smem);
+  using SH = Shape<DK, DVS, DEC>;
+  cudaError_t e = raise_smem<lin_chain_kernel<DK, DVS, DEC>>(SH::SMEM);
   if (e != cudaSuccess) return e;
+  LinMaps m = {};
+  if (!encode_head_rows(&m.x, op.x, P.Ntok, P.H, DK) || !encode_head_rows(&m.y, op.y, P.Ntok, P.H, DK) ||
+      !encode_head_rows(&m.z, op.z, P.Ntok, P.H, op.DVt) ||
+      (SH::HASW && !encode_head_rows(&m.w, op.wx, P.Ntok, P.H, op.DVt)))
+    return cudaErrorInvalidValue;
   prof_begin(kid, st);
-  lin_chain_kernel<DK, DVS, T, DEC><<<(unsigned)((int64_t)P.nu * P.H * (op.DVt / DVS)), LTH, smem, st>>>(P, op, fwd);
+  lin_chain_kernel<DK, DVS, DEC>
+      <<<(unsigned)((int64_t)P.nu * P.H * (op.DVt / DVS)), SH::NTH, SH::SMEM, st>>>(m, P, op, fwd);
   prof_end(kid, st);
   return cudaGetLastError();
 }
 
+// The chain whose state has `key` key columns (op.DVt value columns).
 template <typename T, int DEC>
 cudaError_t dispatch(int kid, int key, const LinP& P, const LinOp& op, int fwd, cudaStream_t st) {
   if constexpr (sizeof(T) == 4) {
-    if (key == 32) return launch_chain<32, 32, T, DEC>(kid, P, op, fwd, st);
-    if (key == 64) return launch_chain<64, 32, T, DEC>(kid, P, op, fwd, st);
-    return launch_chain<128, 32, T, DEC>(kid, P, op, fwd, st);
+    return launch_f32(DEC, kid, key, P, op, fwd, st);
   } else {
-    if (key == 32) return launch_chain<32, 64, T, DEC>(kid, P, op, fwd, st);
-    if (key == 64 && op.DVt == 32) return launch_chain<64, 32, T, DEC>(kid, P, op, fwd, st);
-    if (key == 64) return launch_chain<64, 64, T, DEC>(kid, P, op, fwd, st);
-    return launch_chain<128, 64, T, DEC>(kid, P, op, fwd, st);
+    if constexpr (DEC != 1 && DEC != 2) {  // (the gradients' chains have dv as their key side)
+      if (key == 32) return launch_chain<32, 64, DEC>(kid, P, op, fwd, st);
+    }
+    if constexpr (DEC < 3) {
+      if (key == 64 && op.DVt == 32) return launch_chain<64, 32, DEC>(kid, P, op, fwd, st);
+    }
+    if (key == 64) return launch_chain<64, 64, DEC>(kid, P, op, fwd, st);
+    return launch_chain<128, 64, DEC>(kid, P, op, fwd, st);
   }
 }
 
@@ -805,8 +620,12 @@ struct LinLayout {
 void lin_plan(const kda_problem* p, const Dims& d, LinP& P) {
   const int64_t per = (int64_t)d.H * (d.dv / value_slice(p->dtype, d.dv));
   int64_t L = ((int64_t)d.Ntok * per + 2 * LIN_SMS - 1) / (2 * LIN_SMS);
-  L = (L + C - 1) / C * C;
   if (L < SEG_TOK) L = SEG_TOK;
+  if (d.rows) {  // equal segments of a row
+    const int64_t ns = (d.T + L - 1) / L;
+    L = (d.T + ns - 1) / ns;
+  }
+  L = (L + C - 1) / C * C;
   P.Ntok = d.Ntok;
   P.H = d.H;
   P.n_docs = d.n_docs;
@@ -1010,9 +829,11 @@ cudaError_t launch_lin_decode(int dtype, int64_t n, int H, float scale, const vo
 }
 
 }  // namespace
+}  // namespace lin
 }  // namespace kda
 
 using namespace kda;
+using namespace kda::lin;
 
 extern "C" KDA_API size_t kda_linear_workspace_size(const kda_problem* p, int for_backward) {
   Dims d;

@@ -152,8 +152,8 @@ def test_gradients_that_are_not_wanted():
     b = kda.kda_linear_backward(ctx, d["dO"], d["dh"], want_dA_log=False, want_dh0=False)
     c = kda.kda_linear_backward(ctx, d["dO"], d["dh"])  # the workspace serves again
     assert b["dA_log"] is None and b["dh0"] is None
-    for n in ("dq", "dk", "dv"):
-        assert torch.equal(a[n], b[n]), n
+    # (with the decay gradient the state enters its products in one more part: the last bits differ)
+    check(b, oracle(x), "bf16", names=("dq", "dk", "dv"))
     for n in a:
         assert torch.equal(a[n], c[n]), n
 
