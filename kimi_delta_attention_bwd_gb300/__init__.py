@@ -74,7 +74,7 @@ def _shape(t, name, shape):
     """Shapes are checked before anything is launched: the C ABI sees only
     pointers, so a tensor smaller than its declared layout would be read out
     of bounds."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
