@@ -16,9 +16,10 @@
 // a thread meets the same s, hence the same columns, in all its rows: it keeps
 // their w and b, and the backward their dw and db sums, in registers.  The two
 // vectors that a row shares with its neighbours are read and written value by
-// value.  Eight columns a thread, so that 1024 threads fit an SM; two rows at a
-// time share the sums' barriers, and the next rows are under way to the
-// thread's own slots of shared memory (cp.async, no barrier) meanwhile.  The
+// value.  Sixteen columns a thread: with eight, the shuffles of the row sums and
+// the bookkeeping took the larger part of the issue slots (bf16 32768 x 2048
+// forward: 68 us at 76% of them).  The next rows are under way to the thread's
+// own slots of shared memory (cp.async, no barrier) while a row is summed.  The
 // backward's per-CTA partials are added in a fixed order (deterministic).
 #include "kda_internal.cuh"
 #include "../../include/kda.h"
@@ -27,11 +28,10 @@ namespace kda {
 namespace {
 
 constexpr int LN_NTHR = 256;     // threads per CTA where a row takes at most a warp
-constexpr int LN_CTAS = 3;       // and resident CTAs per SM of those
-constexpr int LN_PER = 8;        // values of a row per thread (16 in rows past LN_WIDE)
-constexpr int LN_WIDE = 8184;    // widest row of 1024 threads at eight values each (and a vector of offset)
-constexpr int LN_REG_D = 16368;  // and at sixteen; wider rows are read once per pass
+constexpr int LN_CTHR = 512;     // most threads of a one-row CTA (128 registers each)
+constexpr int LN_PER = 16;       // values of a row per thread, twice that in rows that LN_CTHR threads do not hold
 constexpr int LN_SMS = 152;      // the grids: what the SMs hold at once
+constexpr int LN_FWD_THR = 640, LN_BWD_THR = 512;  // resident threads per SM (their registers)
 constexpr int LN_MAX_D = 1 << 24;
 
 // 16 bytes as loaded (half the registers for bf16) until they are used.
@@ -64,15 +64,27 @@ struct Pack {
 };
 
 // A thread's vector: columns c .. c + V - 1 of its rows, of which those in
-// [0, D) exist.
-template <typename T>
+// [0, D) exist.  EDGE: rows may share vectors with their neighbours (else a
+// vector is a row's or nobody's).
+template <typename T, bool EDGE>
 struct Cols {
   static constexpr int V = Pack<T>::V;
   int c, D;
-  __device__ __forceinline__ Cols(int first, int D_) : c(first), D(D_) {}
-  __device__ __forceinline__ bool full() const { return c >= 0 && c + V <= D; }
-  __device__ __forceinline__ bool any() const { return c < D && c + V > 0; }
-  __device__ __forceinline__ bool in(int e) const { return (unsigned)(c + e) < (unsigned)D; }
+  __device__ __forceinline__ bool full() const { return EDGE ? c >= 0 && c + V <= D : c < D; }
+  __device__ __forceinline__ bool any() const { return EDGE ? c < D && c + V > 0 : c < D; }
+  __device__ __forceinline__ bool in(int e) const { return EDGE ? (unsigned)(c + e) < (unsigned)D : c < D; }
+  // The whole aligned vector to shared memory, its neighbours' columns included, but nothing at or
+  // past `end` (the tensor's).
+  __device__ __forceinline__ void copy(uint4* slot, const T* row, const T* end) const {
+    int bytes = 16;
+    if constexpr (EDGE) {
+      const int64_t left = (const char*)end - (const char*)(row + c);
+      if (left < 16) bytes = (int)left;
+    }
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"((uint32_t)__cvta_generic_to_shared(slot)),
+                 "l"(row + c), "r"(bytes)
+                 : "memory");
+  }
   __device__ __forceinline__ Pack<T> load(const T* row) const {  // missing columns read as 0
     Pack<T> p;
     if (full()) {
@@ -84,15 +96,6 @@ struct Cols {
       p.set(v);
     }
     return p;
-  }
-  // The whole aligned vector to shared memory, its neighbours' columns included, but nothing at or
-  // past `end` (the tensor's).
-  __device__ __forceinline__ void copy(uint4* slot, const T* row, const T* end) const {
-    const int64_t left = (const char*)end - (const char*)(row + c);
-    const int bytes = left < 16 ? (int)left : 16;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"((uint32_t)__cvta_generic_to_shared(slot)),
-                 "l"(row + c), "r"(bytes)
-                 : "memory");
   }
   __device__ __forceinline__ void clear(float* v) const {  // the columns that are not this row's
     if (!full()) {
@@ -106,21 +109,29 @@ struct Cols {
       Pack<T> p;
       p.set(v);
       *reinterpret_cast<uint4*>(row + c) = p.u;
-    } else {
+    } else if (EDGE) {
 #pragma unroll
       for (int e = 0; e < V; e++)
         if (in(e)) stf(row + c + e, v[e]);
     }
   }
   __device__ __forceinline__ void param(const float* w, float* v) const {
+    if (!EDGE && w && full()) {
 #pragma unroll
-    for (int e = 0; e < V; e++) v[e] = w && in(e) ? __ldg(w + c + e) : 0.f;
+      for (int e = 0; e < V; e += 4) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(w + c + e));
+        v[e] = f.x; v[e + 1] = f.y; v[e + 2] = f.z; v[e + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; e++) v[e] = w && in(e) ? __ldg(w + c + e) : 0.f;
+    }
   }
 };
 
-// Sums of NS values over the G threads of a row at once: the whole CTA (BLK;
-// red: NS x 32 floats, free again after the CTA's next barrier but one), or an
-// aligned group of G lanes.
+// Sums of NS values over the G threads of a row at once: the whole CTA (BLK; up
+// to 16 warps; red: NS x 32 floats, free again after the CTA's next barrier but
+// one), or an aligned group of G lanes.
 template <bool BLK, int NS>
 __device__ __forceinline__ void row_sums(float (&x)[NS], int G, float (*red)[32]) {
   if constexpr (!BLK) {
@@ -137,7 +148,11 @@ __device__ __forceinline__ void row_sums(float (&x)[NS], int G, float (*red)[32]
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < NS; k++) x[k] = warp_sum(lane < nw ? red[k][lane] : 0.f);
+    for (int k = 0; k < NS; k++) {
+      x[k] = (lane & 15) < nw ? red[k][lane & 15] : 0.f;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) x[k] += __shfl_xor_sync(0xffffffffu, x[k], o);
+    }
   }
 }
 
@@ -156,36 +171,39 @@ struct Ahead {
   __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group 1;\n" ::: "memory"); }
 };
 
-// KEEP: w and b in registers and NR rows at a time (eight columns a thread);
-// else (sixteen columns) neither.
-template <typename T, int NCH, bool BLK, bool KEEP, int NR>
-__global__ void __launch_bounds__(BLK ? 1024 : LN_NTHR, BLK ? 1 : LN_CTAS)
+// KEEP: w and b in registers and the next rows under way; else (32 columns a
+// thread) both are read as they are needed.
+template <typename T, bool BLK, bool EDGE, bool KEEP, int NR>
+__global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_FWD_THR / LN_NTHR)
     ln_fwd_kernel(int64_t n, int D, int G, float eps, const T* __restrict__ x, const float* __restrict__ w,
                   const float* __restrict__ b, T* __restrict__ y, float* __restrict__ mean,
                   float* __restrict__ rstd) {
-  constexpr int V = Pack<T>::V, E = NCH * V;
+  constexpr int V = Pack<T>::V, E = KEEP ? LN_PER : 2 * LN_PER, NCH = E / V;
   __shared__ float red[4][NR][32];
   extern __shared__ __align__(16) unsigned char smem[];
   const Ahead<T, 1, NR, NCH> q = {reinterpret_cast<uint4*>(smem)};
   const int gid = BLK ? 0 : threadIdx.x / G, lane = BLK ? threadIdx.x : threadIdx.x % G, rpc = BLK ? 1 : LN_NTHR / G;
-  const int64_t row0 = (int64_t)blockIdx.x * rpc + gid, step = (int64_t)gridDim.x * rpc;
-  const int s = (int)((row0 % V) * (D % V) % V);
+  const int64_t row0 = (int64_t)blockIdx.x * rpc + gid, step = (int64_t)gridDim.x * rpc, stepD = step * D;
+  const int s = EDGE ? (int)((row0 % V) * (D % V) % V) : 0;
   const float inv = 1.0f / (float)D;
   const T* end = x + n * D;
-  auto cols = [&](int i) { return Cols<T>((i * G + lane) * V - s, D); };
-  auto fetch = [&](int g) {
+  auto cols = [&](int i) { return Cols<T, EDGE>{(i * G + lane) * V - s, D}; };
+  auto fetch = [&](int g, int64_t row, const T* p) {
 #pragma unroll
     for (int k = 0; k < NR; k++) {
-      const int64_t row = row0 + ((int64_t)g * NR + k) * step;
+      if (row + k * step < n) {
 #pragma unroll
-      for (int i = 0; i < NCH; i++)
-        if (row < n && cols(i).any()) cols(i).copy(q.slot(g, 0, k, i), x + row * D, end);
+        for (int i = 0; i < NCH; i++)
+          if (cols(i).any()) cols(i).copy(q.slot(g, 0, k, i), p + k * stepD, end);
+      }
     }
     q.commit();
   };
-  if constexpr (KEEP) fetch(0);
-  float wv[KEEP ? E : 1], bv[KEEP ? E : 1];
+  const T* px = x + row0 * D;
+  T* py = y + row0 * D;
+  float wv[KEEP ? E : V], bv[KEEP ? E : V];
   if constexpr (KEEP) {
+    fetch(0, row0, px);
 #pragma unroll
     for (int i = 0; i < NCH; i++) {
       cols(i).param(w, wv + i * V);
@@ -194,11 +212,12 @@ __global__ void __launch_bounds__(BLK ? 1024 : LN_NTHR, BLK ? 1 : LN_CTAS)
   }
   int flip = 0;
   // (the trip count is the CTA's: a group past the last row takes part in the shuffles)
-  for (int g = 0; row0 - gid + (int64_t)g * NR * step < n; g++) {
-    const int64_t row = row0 + (int64_t)g * NR * step;
+  int64_t row = row0;
+  for (int g = 0; row - gid < n; g++) {
     float v[NR][E], m[NR], var[NR];
     if constexpr (KEEP) {
-      fetch(g + 1);
+      px += NR * stepD;
+      fetch(g + 1, row + NR * step, px);
       q.wait();
     }
 #pragma unroll
@@ -208,12 +227,12 @@ __global__ void __launch_bounds__(BLK ? 1024 : LN_NTHR, BLK ? 1 : LN_CTAS)
       for (int i = 0; i < NCH; i++) {
         Pack<T> p;
         p.u = make_uint4(0, 0, 0, 0);
-        if (row + k * step < n && cols(i).any()) {
+        if (cols(i).any()) {  // (a row past the last: whatever the slot held, not stored)
           if constexpr (KEEP) p.u = *q.slot(g, 0, k, i);
-          else p = cols(i).load(x + (row + k * step) * D);
+          else p = cols(i).load(px);
         }
         p.get(v[k] + i * V);
-        if constexpr (KEEP) cols(i).clear(v[k] + i * V);
+        if constexpr (EDGE && KEEP) cols(i).clear(v[k] + i * V);
 #pragma unroll
         for (int e = 0; e < V; e++) m[k] += v[k][i * V + e];
       }
@@ -235,67 +254,70 @@ __global__ void __launch_bounds__(BLK ? 1024 : LN_NTHR, BLK ? 1 : LN_CTAS)
     flip ^= 2;
 #pragma unroll
     for (int k = 0; k < NR; k++) {
-      const int64_t rk = row + k * step;
       const float r = 1.0f / sqrtf(var[k] * inv + eps);
-      if (rk >= n) continue;
+      if (row + k * step >= n) continue;
       if (mean && lane == 0) {
-        mean[rk] = m[k];
-        rstd[rk] = r;
+        mean[row + k * step] = m[k];
+        rstd[row + k * step] = r;
       }
 #pragma unroll
       for (int i = 0; i < NCH; i++) {
         if (!cols(i).any()) continue;
-        float o[V], pw[V], pb[V];
+        const int at = KEEP ? i * V : 0;
         if constexpr (!KEEP) {
-          cols(i).param(w, pw);
-          cols(i).param(b, pb);
+          cols(i).param(w, wv);
+          cols(i).param(b, bv);
         }
+        float o[V];
 #pragma unroll
-        for (int e = 0; e < V; e++)
-          o[e] = KEEP ? v[k][i * V + e] * r * wv[KEEP ? i * V + e : 0] + bv[KEEP ? i * V + e : 0]
-                      : v[k][i * V + e] * r * pw[e] + pb[e];
-        cols(i).store(y + rk * D, o);
+        for (int e = 0; e < V; e++) o[e] = v[k][i * V + e] * r * wv[at + e] + bv[at + e];
+        cols(i).store(py + k * stepD, o);
       }
     }
+    row += NR * step;
+    py += NR * stepD;
+    if constexpr (!KEEP) px += NR * stepD;
   }
 }
 
-// KEEP: the dw / db sums and w in registers; else (sixteen columns a thread)
-// the sums in shared memory, in slots of the thread's own.
-template <typename T, int NCH, bool BLK, bool KEEP, int NR>
-__global__ void __launch_bounds__(BLK ? 1024 : LN_NTHR, BLK ? 1 : LN_CTAS)
+// KEEP as in the forward; without it the dw / db sums are in shared memory, in
+// slots of the thread's own.
+template <typename T, bool BLK, bool EDGE, bool KEEP>
+__global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_BWD_THR / LN_NTHR)
     ln_bwd_kernel(int64_t n, int D, int G, const T* __restrict__ x, const float* __restrict__ w,
                   const T* __restrict__ dy, const float* __restrict__ mean, const float* __restrict__ rstd,
                   T* __restrict__ dx, float* __restrict__ part) {
-  constexpr int V = Pack<T>::V, E = NCH * V;
-  __shared__ float red[2][2 * NR][32];
+  constexpr int V = Pack<T>::V, E = KEEP ? LN_PER : 2 * LN_PER, NCH = E / V;
+  __shared__ float red[2][2][32];
   extern __shared__ __align__(16) unsigned char smem[];
-  const Ahead<T, 2, NR, NCH> q = {reinterpret_cast<uint4*>(smem)};
+  const Ahead<T, 2, 1, NCH> q = {reinterpret_cast<uint4*>(smem)};
   float* acc = reinterpret_cast<float*>(smem);  // !KEEP: [2][E][blockDim.x]; !BLK, at the end: [256 / G][D]
   pdl_release();
   const int gid = BLK ? 0 : threadIdx.x / G, lane = BLK ? threadIdx.x : threadIdx.x % G;
   const int rpc = BLK ? 1 : LN_NTHR / G;
-  const int64_t row0 = (int64_t)blockIdx.x * rpc + gid, step = (int64_t)gridDim.x * rpc;
-  const int s = (int)((row0 % V) * (D % V) % V);
+  const int64_t row0 = (int64_t)blockIdx.x * rpc + gid, step = (int64_t)gridDim.x * rpc, stepD = step * D;
+  const int s = EDGE ? (int)((row0 % V) * (D % V) % V) : 0;
   const float inv = 1.0f / (float)D;
   const T *xend = x + n * D, *dend = dy + n * D;
-  auto cols = [&](int i) { return Cols<T>((i * G + lane) * V - s, D); };
-  auto fetch = [&](int g) {
-#pragma unroll
-    for (int k = 0; k < NR; k++) {
-      const int64_t row = row0 + ((int64_t)g * NR + k) * step;
+  auto cols = [&](int i) { return Cols<T, EDGE>{(i * G + lane) * V - s, D}; };
+  float nmu = 0.f, nr = 0.f;
+  auto fetch = [&](int g, int64_t row, int64_t at) {
+    if (row < n) {
+      nmu = __ldg(mean + row);
+      nr = __ldg(rstd + row);
 #pragma unroll
       for (int i = 0; i < NCH; i++)
-        if (row < n && cols(i).any()) {
-          cols(i).copy(q.slot(g, 0, k, i), x + row * D, xend);
-          cols(i).copy(q.slot(g, 1, k, i), dy + row * D, dend);
+        if (cols(i).any()) {
+          cols(i).copy(q.slot(g, 0, 0, i), x + at, xend);
+          cols(i).copy(q.slot(g, 1, 0, i), dy + at, dend);
         }
     }
     q.commit();
   };
-  float aw[KEEP ? E : 1], ab[KEEP ? E : 1], wv[KEEP ? E : 1];
+  int64_t at = row0 * D, row = row0;
+  float aw[KEEP ? E : 1], ab[KEEP ? E : 1], wv[KEEP ? E : V];
   if constexpr (KEEP) {
-    fetch(0);
+    fetch(0, row, at);
 #pragma unroll
     for (int i = 0; i < NCH; i++) cols(i).param(w, wv + i * V);
 #pragma unroll
@@ -305,86 +327,77 @@ __global__ void __launch_bounds__(BLK ? 1024 : LN_NTHR, BLK ? 1 : LN_CTAS)
     for (int e = 0; e < 2 * E; e++) acc[e * blockDim.x + threadIdx.x] = 0.f;
   }
   int flip = 0;
-  for (int g = 0; row0 - gid + (int64_t)g * NR * step < n; g++) {
-    const int64_t row = row0 + (int64_t)g * NR * step;
-    float xh[NR][E], dd[NR][E], m[2 * NR], r[NR];
-    if constexpr (KEEP) fetch(g + 1);
-#pragma unroll
-    for (int k = 0; k < NR; k++) {
-      const int64_t rk = row + k * step;
-      m[k] = rk < n ? __ldg(mean + rk) : 0.f;
-      r[k] = rk < n ? __ldg(rstd + rk) : 0.f;
+  for (int g = 0; row - gid < n; g++) {
+    const bool ok = row < n;
+    if (!KEEP && ok) {
+      nmu = mean[row];
+      nr = rstd[row];
     }
-    if constexpr (KEEP) q.wait();
+    const float mu = nmu, r = nr;
+    if constexpr (KEEP) {
+      fetch(g + 1, row + step, at + stepD);
+      q.wait();
+    }
+    float xh[E], dd[E], m[2] = {0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < NR; k++) {
-      const int64_t rk = row + k * step;
-      const float mu = m[k];
-      float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-      for (int i = 0; i < NCH; i++) {
-        Pack<T> px, pd;
-        px.u = pd.u = make_uint4(0, 0, 0, 0);
-        if (rk < n && cols(i).any()) {
-          if constexpr (KEEP) {
-            px.u = *q.slot(g, 0, k, i);
-            pd.u = *q.slot(g, 1, k, i);
-          } else {
-            px = cols(i).load(x + rk * D);
-            pd = cols(i).load(dy + rk * D);
-          }
-        }
-        px.get(xh[k] + i * V);
-        pd.get(dd[k] + i * V);
-        if constexpr (KEEP) {  // (a missing column then has dy = 0, and h finite: nothing enters a sum)
-          cols(i).clear(xh[k] + i * V);
-          cols(i).clear(dd[k] + i * V);
-        }
-        float wl[V];
-        if constexpr (!KEEP) cols(i).param(w, wl);
-#pragma unroll
-        for (int e = 0; e < V; e++) {
-          const int j = i * V + e;
-          const float h = (xh[k][j] - mu) * r[k], d = dd[k][j];
-          xh[k][j] = h;
-          if constexpr (KEEP) {
-            aw[j] += d * h;
-            ab[j] += d;
-            dd[k][j] = d * wv[j];
-          } else {
-            acc[j * blockDim.x + threadIdx.x] += d * h;
-            acc[(E + j) * blockDim.x + threadIdx.x] += d;
-            dd[k][j] = d * wl[e];
-          }
-          s1 += dd[k][j];
-          s2 += dd[k][j] * h;
+    for (int i = 0; i < NCH; i++) {
+      Pack<T> px, pd;
+      px.u = pd.u = make_uint4(0, 0, 0, 0);
+      if (ok && cols(i).any()) {
+        if constexpr (KEEP) {
+          px.u = *q.slot(g, 0, 0, i);
+          pd.u = *q.slot(g, 1, 0, i);
+        } else {
+          px = cols(i).load(x + at);
+          pd = cols(i).load(dy + at);
         }
       }
-      m[k] = s1;
-      m[NR + k] = s2;
-    }
-    row_sums<BLK, 2 * NR>(m, G, red[flip]);
-    flip ^= 1;
+      px.get(xh + i * V);
+      pd.get(dd + i * V);
+      if constexpr (!KEEP) cols(i).param(w, wv);
+      if constexpr (EDGE && KEEP) {
+        cols(i).clear(xh + i * V);
+        cols(i).clear(dd + i * V);
+      }
 #pragma unroll
-    for (int k = 0; k < NR; k++) {
-      const int64_t rk = row + k * step;
-      if (rk >= n) continue;
-      const float m1 = m[k] * inv, m2 = m[NR + k] * inv;
+      for (int e = 0; e < V; e++) {  // (a missing column or row has dy = 0, and h finite: nothing enters a sum)
+        const int j = i * V + e;
+        const float h = (xh[j] - mu) * r, d = dd[j];
+        xh[j] = h;
+        if constexpr (KEEP) {
+          aw[j] += d * h;
+          ab[j] += d;
+        } else {
+          acc[j * blockDim.x + threadIdx.x] += d * h;
+          acc[(E + j) * blockDim.x + threadIdx.x] += d;
+        }
+        dd[j] = d * wv[KEEP ? j : e];
+        m[0] += dd[j];
+        m[1] += dd[j] * h;
+      }
+    }
+    row_sums<BLK, 2>(m, G, red[flip]);
+    flip ^= 1;
+    if (ok) {
+      m[0] *= inv;
+      m[1] *= inv;
 #pragma unroll
       for (int i = 0; i < NCH; i++) {
         if (!cols(i).any()) continue;
         float o[V];
 #pragma unroll
-        for (int e = 0; e < V; e++) o[e] = r[k] * (dd[k][i * V + e] - m1 - xh[k][i * V + e] * m2);
-        cols(i).store(dx + rk * D, o);
+        for (int e = 0; e < V; e++) o[e] = r * (dd[i * V + e] - m[0] - xh[i * V + e] * m[1]);
+        cols(i).store(dx + at, o);
       }
     }
-  }
-  if constexpr (KEEP && !BLK) {
-    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
-    __syncthreads();  // the slots are free: acc takes their place
+    row += step;
+    at += stepD;
   }
   float* pw = part + (int64_t)blockIdx.x * 2 * D;
+  if constexpr (!BLK) {  // acc takes the slots' place
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    __syncthreads();
+  }
 #pragma unroll
   for (int k = 0; k < 2; k++) {  // dw, then db
 #pragma unroll
@@ -409,7 +422,7 @@ __global__ void __launch_bounds__(BLK ? 1024 : LN_NTHR, BLK ? 1 : LN_CTAS)
   }
 }
 
-// Rows wider than LN_REG_D: a CTA per row, the row read once per pass (its
+// Rows wider than 32 columns for each of LN_CTHR threads: a CTA per row, the row read once per pass (its
 // later passes hit L2), the backward's column sums in its partial row.
 __device__ __forceinline__ float one_sum(float x, float (*red)[32]) {
   float v[1] = {x};
@@ -418,7 +431,7 @@ __device__ __forceinline__ float one_sum(float x, float (*red)[32]) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(int64_t n, int D, float eps, const T* __restrict__ x,
+__global__ void __launch_bounds__(LN_CTHR) ln_fwd_wide_kernel(int64_t n, int D, float eps, const T* __restrict__ x,
                                                            const float* __restrict__ w, const float* __restrict__ b,
                                                            T* __restrict__ y, float* __restrict__ mean,
                                                            float* __restrict__ rstd) {
@@ -446,7 +459,7 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(int64_t n, int D, flo
 }
 
 template <typename T>
-__global__ void __launch_bounds__(1024) ln_bwd_wide_kernel(int64_t n, int D, const T* __restrict__ x,
+__global__ void __launch_bounds__(LN_CTHR) ln_bwd_wide_kernel(int64_t n, int D, const T* __restrict__ x,
                                                            const float* __restrict__ w, const T* __restrict__ dy,
                                                            const float* __restrict__ mean,
                                                            const float* __restrict__ rstd, T* __restrict__ dx,
@@ -503,32 +516,32 @@ __global__ void __launch_bounds__(1024) ln_reduce_kernel(const float* __restrict
   }
 }
 
-// How a row is laid over threads: G threads of `per` values each, blk: a CTA a row.
+// How a row is laid over threads: G threads of LN_PER values each (twice that
+// without keep), blk: a CTA a row.  wide: not held in registers.
 struct LnShape {
-  int G, per;
-  bool blk;
+  int G;
+  bool blk, edge, keep, wide;
 };
 LnShape ln_shape(int D, int dtype) {
   const int V = dtype == KDA_BF16 ? 8 : 4, span = D % V ? D + V - 1 : D;  // with the offset of a row's start
-  LnShape s = {1, LN_PER, false};
-  while (s.G < 32 && s.G * s.per < span) s.G *= 2;
-  if (s.G * s.per < span) {
+  LnShape s = {1, false, D % V != 0, span <= LN_CTHR * LN_PER, span > 2 * LN_CTHR * LN_PER};
+  while (s.G < 32 && s.G * LN_PER < span) s.G *= 2;
+  if (s.G * LN_PER < span) {
+    const int per = s.keep ? LN_PER : 2 * LN_PER;
     s.blk = true;
-    if (D > LN_WIDE) s.per = 2 * LN_PER;
-    s.G = ((span + s.per - 1) / s.per + 31) / 32 * 32;
+    s.G = ((span + per - 1) / per + 31) / 32 * 32;
   }
   return s;
 }
 
-// Persistent CTAs: no more than the rows need or than the SMs hold at once (a
-// thread of the one-row CTAs has 64 registers), in a number that makes the row
-// step a multiple of a vector's values.
-int ln_blocks(int64_t n, int D, int dtype) {
-  if (D > LN_REG_D) return (int)(n < LN_SMS ? n : LN_SMS);
+// Persistent CTAs: no more than the rows need or than the SMs hold at once, in
+// a number that makes the row step a multiple of a vector's values.
+int ln_blocks(int64_t n, int D, int dtype, int thr) {
   const LnShape s = ln_shape(D, dtype);
-  const int rpc = s.blk ? 1 : LN_NTHR / s.G, per = s.blk ? 1024 / s.G : LN_CTAS;
+  if (s.wide) return (int)(n < LN_SMS ? n : LN_SMS);
+  const int rpc = s.blk ? 1 : LN_NTHR / s.G, per = thr / (s.blk ? s.G : LN_NTHR);
   const int64_t need = (n + rpc - 1) / rpc;
-  const int64_t most = (int64_t)LN_SMS * per;  // a multiple of 8
+  const int64_t most = (int64_t)LN_SMS * (per < 1 ? 1 : per);  // a multiple of 8
   return (int)(need < most ? (need + 7) / 8 * 8 : most);
 }
 
@@ -556,31 +569,29 @@ cudaError_t ln_run(void (*k)(KA...), int nblk, int thr, size_t smem, cudaStream_
 
 template <typename T>
 cudaError_t ln_fwd_launch(const LnShape& s, const LnArgs& a, int nblk) {
-  constexpr int NCH = LN_PER * (int)sizeof(T) / 16, NR = 2;
-  auto run = [&](auto* kernel, int thr, size_t slots) {
-    return ln_run(kernel, nblk, thr, slots * 32 * thr, a.st, a.n, a.D, s.G, a.eps, (const T*)a.x, a.w, a.b, (T*)a.y,
-                  a.mean, a.rstd);
+  constexpr int NR = 2;
+  const int thr = s.blk ? s.G : LN_NTHR;
+  auto run = [&](auto* kernel) {
+    return ln_run(kernel, nblk, thr, s.keep ? 2 * NR * LN_PER * sizeof(T) * thr : 0, a.st, a.n, a.D, s.G, a.eps, (const T*)a.x, a.w,
+                  a.b, (T*)a.y, a.mean, a.rstd);
   };
-  if (!s.blk) return run(ln_fwd_kernel<T, NCH, false, true, NR>, LN_NTHR, NR * NCH);
-  if (s.per == LN_PER) return run(ln_fwd_kernel<T, NCH, true, true, NR>, s.G, NR * NCH);
-  return run(ln_fwd_kernel<T, 2 * NCH, true, false, 1>, s.G, 0);
+  if (!s.keep) return s.edge ? run(ln_fwd_kernel<T, true, true, false, 1>) : run(ln_fwd_kernel<T, true, false, false, 1>);
+  if (s.blk) return s.edge ? run(ln_fwd_kernel<T, true, true, true, NR>) : run(ln_fwd_kernel<T, true, false, true, NR>);
+  return s.edge ? run(ln_fwd_kernel<T, false, true, true, NR>) : run(ln_fwd_kernel<T, false, false, true, NR>);
 }
 
 template <typename T>
 cudaError_t ln_bwd_launch(const LnShape& s, const LnArgs& a, int nblk) {
-  // (two fp32 rows at a time would take 256 KB of slots)
-  constexpr int NCH = LN_PER * (int)sizeof(T) / 16, NR = sizeof(T) == 4 ? 1 : 2;
-  auto run = [&](auto* kernel, int thr, size_t smem) {
-    return ln_run(kernel, nblk, thr, smem, a.st, a.n, a.D, s.G, (const T*)a.x, a.w, (const T*)a.dy,
-                  (const float*)a.mean, (const float*)a.rstd, (T*)a.dx, a.part);
+  const int thr = s.blk ? s.G : LN_NTHR;
+  const size_t slots = s.keep ? 2 * 2 * LN_PER * sizeof(T) * thr : 0;
+  const size_t acc = !s.keep ? 4 * LN_PER * sizeof(float) * thr : s.blk ? 0 : (size_t)(LN_NTHR / s.G) * a.D * 4;
+  auto run = [&](auto* kernel) {
+    return ln_run(kernel, nblk, thr, acc > slots ? acc : slots, a.st, a.n, a.D, s.G, (const T*)a.x, a.w,
+                  (const T*)a.dy, (const float*)a.mean, (const float*)a.rstd, (T*)a.dx, a.part);
   };
-  const size_t slots = 2 * NR * NCH * 32;  // bytes a thread
-  if (!s.blk) {  // at most 256 x 8 floats at the end
-    const size_t acc = (size_t)(LN_NTHR / s.G) * a.D * sizeof(float);
-    return run(ln_bwd_kernel<T, NCH, false, true, NR>, LN_NTHR, acc > slots * LN_NTHR ? acc : slots * LN_NTHR);
-  }
-  if (s.per == LN_PER) return run(ln_bwd_kernel<T, NCH, true, true, NR>, s.G, slots * s.G);
-  return run(ln_bwd_kernel<T, 2 * NCH, true, false, 1>, s.G, 4 * LN_PER * (size_t)s.G * sizeof(float));
+  if (!s.keep) return s.edge ? run(ln_bwd_kernel<T, true, true, false>) : run(ln_bwd_kernel<T, true, false, false>);
+  if (s.blk) return s.edge ? run(ln_bwd_kernel<T, true, true, true>) : run(ln_bwd_kernel<T, true, false, true>);
+  return s.edge ? run(ln_bwd_kernel<T, false, true, true>) : run(ln_bwd_kernel<T, false, false, true>);
 }
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
@@ -599,7 +610,7 @@ using namespace kda;
 
 extern "C" KDA_API size_t kda_layer_norm_workspace_size(int64_t n_rows, int D, int dtype) {
   if (ln_check(n_rows, D, dtype) != KDA_OK) return 0;
-  return (size_t)ln_blocks(n_rows, D, dtype) * 2 * (size_t)D * sizeof(float);
+  return (size_t)ln_blocks(n_rows, D, dtype, LN_BWD_THR) * 2 * (size_t)D * sizeof(float);
 }
 
 extern "C" KDA_API kda_status kda_layer_norm_fwd(int64_t n_rows, int D, int dtype, float eps, const void* x,
@@ -612,18 +623,18 @@ extern "C" KDA_API kda_status kda_layer_norm_fwd(int64_t n_rows, int D, int dtyp
   for (const void* p : ptrs)
     if (!aligned16(p)) return KDA_ERR_ALIGNMENT;
   const LnShape s = ln_shape(D, dtype);
-  const int nblk = ln_blocks(n_rows, D, dtype);
+  const int nblk = ln_blocks(n_rows, D, dtype, LN_FWD_THR);
   LnArgs a = {};
   a.n = n_rows; a.D = D; a.eps = eps > 0.f ? eps : 1e-6f;
   a.x = x; a.w = w; a.b = bias; a.y = y; a.mean = mean; a.rstd = rstd; a.st = st;
   typedef __nv_bfloat16 B;
   cudaError_t e;
   prof_begin(K_LN_FWD, st);
-  if (D > LN_REG_D) {
+  if (s.wide) {
     if (dtype == KDA_BF16)
-      ln_fwd_wide_kernel<B><<<nblk, 1024, 0, st>>>(n_rows, D, a.eps, (const B*)x, w, bias, (B*)y, mean, rstd);
+      ln_fwd_wide_kernel<B><<<nblk, LN_CTHR, 0, st>>>(n_rows, D, a.eps, (const B*)x, w, bias, (B*)y, mean, rstd);
     else
-      ln_fwd_wide_kernel<float><<<nblk, 1024, 0, st>>>(n_rows, D, a.eps, (const float*)x, w, bias, (float*)y, mean,
+      ln_fwd_wide_kernel<float><<<nblk, LN_CTHR, 0, st>>>(n_rows, D, a.eps, (const float*)x, w, bias, (float*)y, mean,
                                                        rstd);
     e = cudaGetLastError();
   } else {
@@ -646,7 +657,7 @@ extern "C" KDA_API kda_status kda_layer_norm_bwd(int64_t n_rows, int D, int dtyp
   if (!workspace || workspace_bytes < kda_layer_norm_workspace_size(n_rows, D, dtype)) return KDA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return KDA_ERR_ALIGNMENT;
   const LnShape s = ln_shape(D, dtype);
-  const int nblk = ln_blocks(n_rows, D, dtype);
+  const int nblk = ln_blocks(n_rows, D, dtype, LN_BWD_THR);
   LnArgs a = {};
   a.n = n_rows; a.D = D;
   a.x = x; a.w = w; a.dy = dy; a.dx = dx; a.mean = (float*)mean; a.rstd = (float*)rstd; a.part = (float*)workspace;
@@ -654,11 +665,11 @@ extern "C" KDA_API kda_status kda_layer_norm_bwd(int64_t n_rows, int D, int dtyp
   typedef __nv_bfloat16 B;
   cudaError_t e;
   prof_begin(K_LN_BWD, st);
-  if (D > LN_REG_D) {
+  if (s.wide) {
     if (dtype == KDA_BF16)
-      ln_bwd_wide_kernel<B><<<nblk, 1024, 0, st>>>(n_rows, D, (const B*)x, w, (const B*)dy, mean, rstd, (B*)dx, a.part);
+      ln_bwd_wide_kernel<B><<<nblk, LN_CTHR, 0, st>>>(n_rows, D, (const B*)x, w, (const B*)dy, mean, rstd, (B*)dx, a.part);
     else
-      ln_bwd_wide_kernel<float><<<nblk, 1024, 0, st>>>(n_rows, D, (const float*)x, w, (const float*)dy, mean, rstd,
+      ln_bwd_wide_kernel<float><<<nblk, LN_CTHR, 0, st>>>(n_rows, D, (const float*)x, w, (const float*)dy, mean, rstd,
                                                        (float*)dx, a.part);
     e = cudaGetLastError();
   } else {
