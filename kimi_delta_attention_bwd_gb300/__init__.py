@@ -83,14 +83,31 @@ def _dims(t, name, n):
         raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
 
 
-def _same_device(first, **others):
-    """The library launches on the current device and stream: every tensor
-    must live there."""
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {first.device}, the current device is {torch.cuda.current_device()}")
-    for n, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{n} is on {t.device}, not on {first.device}")
+def _all_well(*specs):
+    """Whether every (tensor, shape, dtype) is a contiguous tensor of that
+    shape and type on the current CUDA device (the library launches there).
+    One pass over what the named checks of _require look at, for the calls
+    whose time is the host's."""
+    if not specs[0][0].is_cuda:
+        return False
+    device = torch._C._cuda_getDevice()
+    for t, shape, dtype in specs:
+        if t.get_device() != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            return False
+    return True
+
+
+def _require(**specs):
+    """The named checks of (tensor, shape, dtype); tensors that are None are
+    left out.  The library launches on the current device and stream: every
+    tensor must live there."""
+    specs = {name: spec for name, spec in specs.items() if spec[0] is not None}
+    for name, (t, shape, _) in specs.items():
+        _shape(t, name, shape)
+    for name, (t, _, dtype) in specs.items():
+        _check(t, name, dtype)
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is {torch.cuda.current_device()}")
 
 
 def _gate_of(f, dt_bias, qshape):
@@ -485,5 +502,5 @@ def kda_short_conv_backward(x, w, dy, cu_seqlens=None, activation: str = "silu",
 
 
 from .linear import LinearContext, kda_linear_backward, kda_linear_decode_step, kda_linear_forward  # noqa: E402
-from .layer_norm import kda_layer_norm, kda_layer_norm_backward  # noqa: E402
+from .layernorm import kda_layer_norm, kda_layer_norm_backward  # noqa: E402
 from .autograd import gated_norm, kda_attention, layer_norm, linear_attention, short_conv  # noqa: E402  (differentiable forms)

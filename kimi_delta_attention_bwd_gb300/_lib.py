@@ -48,6 +48,8 @@ def exported_names() -> list[str]:
 
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     global _lib
+    if _lib is not None:  # (set once, complete)
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -140,7 +142,7 @@ def _p(t):
 def _stream():
     """The current stream's handle (torch.cuda.current_stream() builds a Stream
     object on the way, a third of a small call's host time)."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def make_problem(B, T, H, dk, dv, dtype, scale=None, cu_seqlens=None, cu_seqlens_host=None, gate=KDA_GATE_CHANNEL):
@@ -309,8 +311,8 @@ def kda_linear_bwd(problem, q, k, v, A_log, h0, dO, dh_final, dq, dk, dv, dA_log
 
 
 def kda_linear_decode(n_seq, H, dk, dv, dtype, scale, q, k, v, A_log, state, o):
-    st = load().kda_linear_decode(int(n_seq), int(H), int(dk), int(dv), _dt(dtype), float(scale or 0.0), _p(q), _p(k),
-                                  _p(v), _p(A_log), _p(state), _p(o), _stream())
+    st = load().kda_linear_decode(n_seq, H, dk, dv, _dt(dtype), scale or 0.0, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                  A_log.data_ptr(), state.data_ptr(), o.data_ptr(), _stream())
     if st != 0:
         raise KdaError(st, "kda_linear_decode")
 
@@ -320,8 +322,8 @@ def kda_layer_norm_workspace_size(n_rows, D, dtype) -> int:
 
 
 def kda_layer_norm_fwd(n_rows, D, dtype, eps, x, w, bias, y, mean, rstd):
-    st = load().kda_layer_norm_fwd(int(n_rows), int(D), _dt(dtype), float(eps or 0.0), _p(x), _p(w), _p(bias), _p(y),
-                                   _p(mean), _p(rstd), _stream())
+    st = load().kda_layer_norm_fwd(n_rows, D, _dt(dtype), eps or 0.0, x.data_ptr(), w.data_ptr(), _p(bias),
+                                   y.data_ptr(), _p(mean), _p(rstd), _stream())
     if st != 0:
         raise KdaError(st, "kda_layer_norm_fwd")
 

@@ -31,7 +31,7 @@ constexpr int LN_NTHR = 256;     // threads per CTA where a row takes at most a 
 constexpr int LN_CTHR = 512;     // most threads of a one-row CTA (128 registers each)
 constexpr int LN_PER = 16;       // values of a row per thread, twice that in rows that LN_CTHR threads do not hold
 constexpr int LN_SMS = 152;      // the grids: what the SMs hold at once
-constexpr int LN_FWD_THR = 640, LN_BWD_THR = 512;  // resident threads per SM (their registers)
+constexpr int LN_FWD_THR = 512, LN_BWD_THR = 512;  // resident threads per SM (their registers)
 constexpr int LN_MAX_D = 1 << 24;
 
 // 16 bytes as loaded (half the registers for bf16) until they are used.

@@ -11,19 +11,19 @@ from typing import Optional
 
 import torch
 
-from . import _check, _lib, _same_device, _shape
+from . import _all_well, _lib, _require
 
 
-def _args(x, w, bias=None):
-    if x.dim() < 1 or x.shape[-1] == 0:
+def _rows(x, w, bias=None):
+    """(rows, D) of x [..., D], with x and the fp32 [D] parameters checked."""
+    D = x.shape[-1] if x.dim() else 0
+    if D == 0:
         raise ValueError(f"x must have a last axis of at least one value, got shape {tuple(x.shape)}")
-    D = x.shape[-1]
-    _check(x, "x")
-    _shape(w, "w", (D,))
-    _check(w, "w", torch.float32)
-    if bias is not None:
-        _shape(bias, "bias", (D,))
-        _check(bias, "bias", torch.float32)
+    f32 = torch.float32
+    specs = ((x, x.shape, x.dtype), (w, (D,), f32)) if bias is None else ((x, x.shape, x.dtype), (w, (D,), f32),
+                                                                         (bias, (D,), f32))
+    if not _all_well(*specs):
+        _require(**dict(zip(("x", "w", "bias"), specs)))
     return x.numel() // D, D
 
 
@@ -32,12 +32,12 @@ def kda_layer_norm(x, w, bias=None, eps: Optional[float] = None, out: Optional[t
     """Layer norm of x [..., D]; eps 1e-6 unless given (> 0).  With
     return_stats returns (y, mean, rstd), the rows' statistics [...] in fp32
     that the backward takes."""
-    n, D = _args(x, w, bias)
-    if out is not None:
-        _shape(out, "out", x.shape)
-        _check(out, "out", x.dtype)
-    _same_device(x, w=w, bias=bias, out=out)
-    y = out if out is not None else torch.empty_like(x)
+    n, D = _rows(x, w, bias)
+    if out is None:
+        y = torch.empty_like(x)
+    else:
+        _require(out=(out, x.shape, x.dtype))
+        y = out
     mean = rstd = None
     if return_stats:
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
@@ -49,18 +49,14 @@ def kda_layer_norm(x, w, bias=None, eps: Optional[float] = None, out: Optional[t
 def kda_layer_norm_backward(x, w, dy, mean, rstd, want_dbias: bool = True, workspace: Optional[torch.Tensor] = None):
     """Backward of kda_layer_norm from its inputs and statistics: returns
     (dx, dw, dbias); dbias is None unless wanted."""
-    n, D = _args(x, w)
-    _shape(dy, "dy", x.shape)
-    _check(dy, "dy", x.dtype)
-    for t, nm in ((mean, "mean"), (rstd, "rstd")):
-        _shape(t, nm, x.shape[:-1])
-        _check(t, nm, torch.float32)
-    _same_device(x, w=w, dy=dy, mean=mean, rstd=rstd, workspace=workspace)
+    n, D = _rows(x, w)
+    _require(dy=(dy, x.shape, x.dtype), mean=(mean, x.shape[:-1], torch.float32),
+             rstd=(rstd, x.shape[:-1], torch.float32))
     if workspace is None:
-        workspace = torch.empty(max(1, _lib.kda_layer_norm_workspace_size(n, D, x.dtype)), dtype=torch.uint8,
+        workspace = torch.empty(_lib.kda_layer_norm_workspace_size(n, D, x.dtype) or 1, dtype=torch.uint8,
                                 device=x.device)
     else:
-        _check(workspace, "workspace", torch.uint8)
+        _require(workspace=(workspace, workspace.shape, torch.uint8))
     dx, dw = torch.empty_like(x), torch.empty_like(w)
     db = torch.empty_like(w) if want_dbias else None
     _lib.kda_layer_norm_bwd(n, D, x.dtype, x, w, dy, mean, rstd, dx, dw, db, workspace)

@@ -14,8 +14,7 @@ from typing import Optional
 
 import torch
 
-from . import _check, _dims, _lib, _same_device, _shape
-from ._lib import KdaError
+from . import _all_well, _dims, _lib, _require
 
 
 @dataclass
@@ -66,37 +65,32 @@ def kda_linear_forward(q, k, v, A_log, scale: Optional[float] = None, h0=None, c
     _dims(v, "v", 4)
     B, T, H, dk = q.shape
     dv = v.shape[-1]
-    _shape(k, "k", q.shape)
-    _shape(v, "v", (B, T, H, dv))
-    _shape(A_log, "A_log", (H,))
+    io, f32 = q.dtype, torch.float32
+    n_docs = B
     if cu_seqlens is not None:
         _dims(cu_seqlens, "cu_seqlens", 1)
         if cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must hold at least two offsets")
+        n_docs = cu_seqlens.numel() - 1
     cu_seqlens_host = _host_offsets(cu_seqlens_host, cu_seqlens)
-    n_docs = B if cu_seqlens is None else cu_seqlens.numel() - 1
     states = (n_docs, H, dk, dv)
-    for t, n, shape, dt in ((q, "q", q.shape, q.dtype), (k, "k", q.shape, q.dtype), (v, "v", v.shape, q.dtype),
-                            (A_log, "A_log", (H,), torch.float32), (h0, "h0", states, torch.float32),
-                            (out, "out", (B, T, H, dv), q.dtype), (final_state, "final_state", states, torch.float32),
-                            (cu_seqlens, "cu_seqlens", None, torch.int32)):
-        if t is not None:
-            if shape is not None:
-                _shape(t, n, shape)
-            _check(t, n, dt)
-    _same_device(q, k=k, v=v, A_log=A_log, h0=h0, cu_seqlens=cu_seqlens, out=out, final_state=final_state,
-                 workspace=workspace)
-    prob = _lib.make_problem(B, T, H, dk, dv, q.dtype, scale, cu_seqlens, cu_seqlens_host)
+    more = [s for s in ((h0, states, f32), (out, v.shape, io), (final_state, states, f32),
+                        (cu_seqlens, (n_docs + 1,), torch.int32)) if s[0] is not None]
+    if not _all_well((q, q.shape, io), (k, q.shape, io), (v, (B, T, H, dv), io), (A_log, (H,), f32), *more):
+        _require(q=(q, q.shape, io), k=(k, q.shape, io), v=(v, (B, T, H, dv), io), A_log=(A_log, (H,), f32),
+                 h0=(h0, states, f32), out=(out, (B, T, H, dv), io), final_state=(final_state, states, f32),
+                 cu_seqlens=(cu_seqlens, (n_docs + 1,), torch.int32))
+    prob = _lib.make_problem(B, T, H, dk, dv, io, scale, cu_seqlens, cu_seqlens_host)
     if workspace is None:
-        n = _lib.kda_linear_workspace_size(prob, save_for_backward)
-        # (0 for a problem that the call below refuses with its own status)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        # (size 0 for a problem that the call below refuses with its own status)
+        workspace = torch.empty(_lib.kda_linear_workspace_size(prob, save_for_backward) or 1, dtype=torch.uint8,
+                                device=q.device)
     else:
-        _check(workspace, "workspace", torch.uint8)
-    o = out if out is not None else torch.empty(B, T, H, dv, dtype=q.dtype, device=q.device)
+        _require(workspace=(workspace, workspace.shape, torch.uint8))
+    o = out if out is not None else torch.empty_like(v)
     hf = None
     if want_final_state:
-        hf = final_state if final_state is not None else torch.empty(*states, dtype=torch.float32, device=q.device)
+        hf = final_state if final_state is not None else torch.empty(states, dtype=f32, device=q.device)
     _lib.kda_linear_fwd(prob, q, k, v, A_log, h0, o, hf, save_for_backward, workspace)
     return o, hf, LinearContext(prob, q, k, v, A_log, h0, cu_seqlens, cu_seqlens_host, workspace, n_docs,
                                 bool(save_for_backward))
@@ -111,15 +105,11 @@ def kda_linear_backward(ctx: LinearContext, dO, dh_final=None, want_dA_log: bool
     q, v = ctx.q, ctx.v
     B, T, H, dk = q.shape
     dv = v.shape[-1]
-    _shape(dO, "dO", (B, T, H, dv))
-    _check(dO, "dO", q.dtype)
-    if dh_final is not None:
-        _shape(dh_final, "dh_final", (ctx.n_docs, H, dk, dv))
-        _check(dh_final, "dh_final", torch.float32)
-    _same_device(q, dO=dO, dh_final=dh_final)
-    gr = {"dq": torch.empty_like(q), "dk": torch.empty_like(ctx.k), "dv": torch.empty_like(v),
-          "dA_log": torch.empty(H, dtype=torch.float32, device=q.device) if want_dA_log else None,
-          "dh0": torch.empty(ctx.n_docs, H, dk, dv, dtype=torch.float32, device=q.device) if want_dh0 else None}
+    states = (ctx.n_docs, H, dk, dv)
+    _require(dO=(dO, (B, T, H, dv), q.dtype), dh_final=(dh_final, states, torch.float32))
+    gr = {"dq": torch.empty_like(q), "dk": torch.empty_like(q), "dv": torch.empty_like(v),
+          "dA_log": torch.empty_like(ctx.A_log) if want_dA_log else None,
+          "dh0": torch.empty(states, dtype=torch.float32, device=q.device) if want_dh0 else None}
     _lib.kda_linear_bwd(ctx.problem, q, ctx.k, v, ctx.A_log, ctx.h0, dO, dh_final, gr["dq"], gr["dk"], gr["dv"],
                         gr["dA_log"], gr["dh0"], ctx.workspace)
     return gr
@@ -134,16 +124,15 @@ def kda_linear_decode_step(q, k, v, A_log, state, scale: Optional[float] = None,
     _dims(v, "v", 3)
     n, H, dk = q.shape
     dv = v.shape[-1]
-    for t, nm, shape, dt in ((q, "q", q.shape, q.dtype), (k, "k", q.shape, q.dtype), (v, "v", (n, H, dv), q.dtype),
-                             (A_log, "A_log", (H,), torch.float32), (state, "state", (n, H, dk, dv), torch.float32),
-                             (out, "out", (n, H, dv), q.dtype)):
-        if t is not None:
-            _shape(t, nm, shape)
-            _check(t, nm, dt)
-    _same_device(q, k=k, v=v, A_log=A_log, state=state, out=out)
-    o = out if out is not None else torch.empty(n, H, dv, dtype=q.dtype, device=q.device)
-    _lib.kda_linear_decode(n, H, dk, dv, q.dtype, scale, q, k, v, A_log, state, o)
+    io, f32 = q.dtype, torch.float32
+    specs = ((q, q.shape, io), (k, q.shape, io), (v, (n, H, dv), io), (A_log, (H,), f32), (state, (n, H, dk, dv), f32))
+    if out is not None:
+        specs += ((out, v.shape, io),)
+    if not _all_well(*specs):
+        _require(**dict(zip(("q", "k", "v", "A_log", "state", "out"), specs)))
+    o = out if out is not None else torch.empty_like(v)
+    _lib.kda_linear_decode(n, H, dk, dv, io, scale, q, k, v, A_log, state, o)
     return o
 
 
-__all__ = ["LinearContext", "kda_linear_forward", "kda_linear_backward", "kda_linear_decode_step", "KdaError"]
+__all__ = ["LinearContext", "kda_linear_forward", "kda_linear_backward", "kda_linear_decode_step"]
