@@ -749,7 +749,7 @@ static const char* const k_names[K_COUNT] = {"chunk_table", "fwd_intra", "fwd_sc
                                              "norm_gate_fwd", "norm_gate_bwd", "norm_gate_reduce",
                                              "conv_fwd",  "conv_bwd",  "conv_reduce",
                                              "fwd_state_norm", "bwd_scan_norm", "fwd_seg", "bwd_seg",
-                                             "linear_chain", "linear_seg", "linear_decay", "linear_decode",
+                                             "linear_chain", "linear_seg", "linear_fold", "linear_dqk", "linear_decay", "linear_decode",
                                              "layer_norm_fwd", "layer_norm_bwd", "layer_norm_reduce"};
 
 const char* kda_prof_kernel_name(int i) { return (i >= 0 && i < K_COUNT) ? k_names[i] : nullptr; }

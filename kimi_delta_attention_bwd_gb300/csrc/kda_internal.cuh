@@ -38,6 +38,8 @@ enum KernelId {
   K_BWD_SEG,
   K_LIN_CHAIN,
   K_LIN_SEG,
+  K_LIN_FOLD,
+  K_LIN_DQK,
   K_LIN_DECAY,
   K_LIN_DECODE,
   K_LN_FWD,

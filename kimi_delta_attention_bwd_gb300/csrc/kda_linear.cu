@@ -14,19 +14,19 @@
 // (out_i = scale (row_i x_i . S + sum_j e^{-a|i-j|} (x_i . y_j) z_j)).  In reverse
 // the chain carries R / scale; a token's own contribution reaches R after its
 // decay step, so the row weight is e^{-a i} and the state weight e^{-a(n-j)}.
-// One kernel body (chain) therefore serves the forward and the three gradients.
+//
+// bf16: the forward's chain keeps every chunk's entry state S and the dv chain
+// its exit state's gradient R, so that dq and dk need no chain of their own:
+// one kernel over all chunks at once forms both from the pairs
+// P = scale e^{-a(i-j)} (dO_i . v_j) that they share (lin_dqk).
 //
 // Decay gradient: with a exponent per token distance,
-//   dL/da = -(A + B + D + C + E), all sums of products of one sign pattern (no
+//   dL/da = -(A + B + C + D), all sums of products of one sign pattern (no
 //   difference of large position sums):
 //   A  pairs inside a chunk, sum_{j<i} (i-j) e^{-a(i-j)} scale (dO_i . v_j)(q_i . k_j)
 //   B  entry state to row, sum_i (i+1) e^{-a(i+1)} scale q_i . S dO_i
-//   D  the same with S replaced by R^ (the state weighted by the tokens that
-//      passed since the end of the chunk each term came from):
-//      R^' = e^{-an} (R^ + n S)
-//   C  a chunk's terms to its exit state's gradient, sum_i i (k_i . dk_i^state)
-//   E  <R^ at the document's end, dh_final>
-// A, B, D, E ride on the dq chain, C on the dk chain.
+//   C  row to exit state, sum_j (n-1-j) e^{-a(n-1-j)} k_j . R v_j
+//   D  entry state to exit state, n e^{-an} <S, R>
 //
 // The state stays in fp32 registers for a whole chain.  Operands that are not
 // inputs are split into bf16 parts: two (about 16 bits) where the result is
@@ -44,78 +44,139 @@ namespace {
 constexpr int LIN_SMS = 152;  // SMs of a GB300: the segment rule's denominator
 constexpr int SEG_TOK = 256;  // shortest segment (tokens)
 
+// Inclusive scan of x over the 1024-thread block; the block's sum in *total.
+__device__ __forceinline__ int block_scan(int x, int* s_w, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_w[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int y = s_w[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    s_w[lane] = y;
+  }
+  __syncthreads();
+  x += warp ? s_w[warp - 1] : 0;
+  *total = s_w[31];
+  __syncthreads();
+  return x;
+}
+
 // The unit table of packed documents: a document of n tokens has max(1,
-// ceil(n / L)) units.  One CTA; also validates the offsets.
+// ceil(n / L)) units and ceil(n / C) chunks.  One CTA; also validates the
+// offsets.
 __global__ void __launch_bounds__(1024) lin_table_kernel(LinP P) {
-  __shared__ int s_bad, s_carry, s_w[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = P.n_docs;
+  __shared__ int s_bad, s_long, s_w[32];
+  const int tid = threadIdx.x, n = P.n_docs;
+  pdl_release();
   if (tid == 0) {
     s_bad = P.cu[0] != 0 || P.cu[n] != P.Ntok;
-    s_carry = 0;
+    s_long = 0;
   }
   __syncthreads();
   for (int i = tid; i < n; i += 1024)
     if (P.cu[i + 1] < P.cu[i]) s_bad = 1;
   __syncthreads();
   if (s_bad) {
-    if (tid == 0) { *P.err = KDA_ERR_BAD_SEQLENS; *P.n_units = 0; *P.wtag = 0; }
+    if (tid == 0) {
+      *P.err = KDA_ERR_BAD_SEQLENS;
+      *P.wtag = 0;
+      P.counts[0] = P.counts[1] = P.counts[2] = 0;
+    }
     return;
   }
+  int units = 0, chunks = 0;
   for (int base = 0; base < n; base += 1024) {
     const int i = base + tid;
     const int t0 = i < n ? P.cu[i] : 0, len = i < n ? P.cu[i + 1] - t0 : 0;
-    const int ns = i < n ? max(1, (len + P.L - 1) / P.L) : 0;
-    int x = ns;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+    const int ns = i < n ? max(1, (len + P.L - 1) / P.L) : 0, nc = (len + C - 1) / C;
+    int all;
+    const int u0 = units + block_scan(ns, s_w, &all) - ns;
+    units += all;
+    const int c0 = chunks + block_scan(nc, s_w, &all) - nc;
+    chunks += all;
+    for (int s = 0; s < ns; s++) {
+      P.units[u0 + s] = make_int4(i, t0 + s * P.L, min(P.L, len - s * P.L), s);
+      P.unit_ch0[u0 + s] = c0 + s * (P.L / C);
     }
-    if (lane == 31) s_w[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-      int y = s_w[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-      }
-      s_w[lane] = y;
-    }
-    __syncthreads();
-    const int u0 = s_carry + x - ns + (warp ? s_w[warp - 1] : 0);
-    for (int s = 0; s < ns; s++) P.units[u0 + s] = make_int4(i, t0 + s * P.L, min(P.L, len - s * P.L), s);
-    __syncthreads();
-    if (tid == 0) s_carry += s_w[31];
-    __syncthreads();
+    if (ns > 1) P.longs[atomicAdd(&s_long, 1)] = make_int2(u0, ns);  // (in any order: they are independent)
   }
-  if (tid == 0) {
-    *P.n_units = s_carry;  // <= n + Ntok / L = nu
+  __syncthreads();
+  if (tid == 0) {  // units <= n + Ntok / L, chunks <= (Ntok + (C - 1) n) / C, split documents <= Ntok / L
+    P.counts[0] = units;
+    P.counts[1] = chunks;
+    P.counts[2] = s_long;
     *P.err = KDA_OK;
     *P.wtag = P.save ? P.tag : 0;
   }
 }
 
+// Turns the segments' own states into their start states, in the chain's
+// direction: start_0 = init, start_{s+1} = e^{-a len_s} start_s + own_s.  A
+// thread per element of a (split document, head)'s state; four segments' loads
+// in flight.
+__global__ void __launch_bounds__(256) lin_fold_kernel(LinP P, float* segc, const float* init, int rev, int N, int fwd) {
+  pdl_wait();
+  pdl_release();
+  if (!ready(P, fwd)) return;
+  const int d = blockIdx.x / P.H, h = blockIdx.x % P.H, at = blockIdx.y * 256 + threadIdx.x;
+  int u0, ns, doc, last;
+  if (P.rows) {
+    ns = (P.T + P.L - 1) / P.L;
+    u0 = d * ns;
+    doc = d;
+    last = P.T - (ns - 1) * P.L;
+  } else {
+    if (d >= P.counts[2]) return;
+    u0 = P.longs[d].x;
+    ns = P.longs[d].y;
+    doc = P.units[u0].x;
+    last = P.units[u0 + ns - 1].z;
+  }
+  const float a = decay_of(P.A_log, h), full = decay_pow(a, P.L);
+  float st = init ? init[((int64_t)doc * P.H + h) * N + at] * (rev ? 1.0f / P.scale : 1.0f) : 0.f;
+  auto own = [&](int k) -> float* {  // k-th segment in the chain's direction
+    return segc + ((int64_t)(u0 + (rev ? ns - 1 - k : k)) * P.H + h) * N + at;
+  };
+  float v[4], nx[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) v[e] = e < ns - 1 ? *own(e) : 0.f;
+  for (int k = 0; k < ns - 1; k += 4) {
+    // (start k + 4 goes where own state k + 4 was: the next four are read first)
+#pragma unroll
+    for (int e = 0; e < 4; e++) nx[e] = k + 4 + e < ns - 1 ? *own(k + 4 + e) : 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (k + e < ns - 1) {
+        st = fmaf(rev && k + e == 0 ? decay_pow(a, last) : full, st, v[e]);
+        *own(k + e + 1) = st;
+      }
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[e] = nx[e];
+  }
+}
+
 // ------------------------------------------------------------ bf16 chain
-// DEC: 0 plain, 1 the dq chain with the decay gradient's A, B, D, E, 2 the dk
-// chain with its C, 3 state only (a segment's own state), 4 the same with R^.
-template <int DK, int DVS, int DEC>
+// ONLY: state only (a segment's own state), no output rows.
+template <int DK, int DVS, bool ONLY>
 struct Shape {
-  static constexpr bool ONLY = DEC >= 3;
-  static constexpr bool HASR = DEC == 1 || DEC == 4;
-  static constexpr bool HASW = DEC == 1 || DEC == 2;  // a further row tile: q or k beside the output's columns
   static constexpr int NW = DVS / 16, NTH = 32 * NW;
   // bytes of the tiles of a stage (multiples of the swizzle's 1024)
-  static constexpr int XB = ONLY ? 0 : 128 * DK, YB = 128 * DK, ZB = 128 * DVS, WB = HASW ? 128 * DVS : 0;
-  static constexpr int STAGE = XB + YB + ZB + WB;
-  static constexpr int STG = DEC == 1 && DK == 128 ? 1 : 2;  // (one stage there: two CTAs per SM)
+  static constexpr int XB = ONLY ? 0 : 128 * DK, YB = 128 * DK, ZB = 128 * DVS;
+  static constexpr int STAGE = XB + YB + ZB, STG = 2;
   static constexpr int PB = ONLY ? 0 : 2 * 64 * 64 * 2;
   static constexpr int SMEM = 1024 /* alignment */ + STG * STAGE + PB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
-  static constexpr int NTK = DK / 8;       // 8-key tiles of a warp's state rows
-  static constexpr int SP = HASW ? 3 : 2;  // parts of the state as an operand: its rows enter fp32 sums there
-  static constexpr int JG = DK == 128 && HASR ? 2 : 1;  // key groups of the state product (registers)
+  static constexpr int NTK = DK / 8;  // 8-key tiles of a warp's state rows
   // resident CTAs: what registers and shared memory allow
-  static constexpr int REGS = DK == 128 ? 255 : HASR ? 204 : DK == 64 ? 168 : 128;
+  static constexpr int REGS = DK == 128 ? 255 : DK == 64 ? 168 : 128;
   static constexpr int BY_REG = 65536 / (NTH * REGS), BY_SMEM = 227 * 1024 / (SMEM + 1024);
   static constexpr int CTAS = BY_REG < BY_SMEM ? (BY_REG < 1 ? 1 : BY_REG) : BY_SMEM;
 };
@@ -175,8 +236,39 @@ __device__ __forceinline__ uint64_t pair_blocks(int warp) {
 
 // The tensors of a chain as [Ntok][H d] maps with boxes of 64 tokens.
 struct LinMaps {
-  CUtensorMap x, y, z, w;
+  CUtensorMap x, y, z;
 };
+
+// Rows n .. of a stage's tiles hold other documents' tokens: zero them, so that
+// nothing of them (an infinity) enters a product.  The first A bytes are rows of
+// RA bytes, the others of RB; a tile (or 64-column half of one) has 64 rows.
+template <int BYTES, int A, int RA, int RB, int NTH>
+__device__ __forceinline__ void zero_rows(unsigned char* stg, int n) {
+  if (n == C) return;
+  for (int b = 16 * threadIdx.x; b < BYTES; b += 16 * NTH) {
+    const int row = b < A ? (b / RA) & 63 : ((b - A) / RB) & 63;
+    if (row >= n) *reinterpret_cast<uint4*>(stg + b) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// A warp's 16 columns x 64 tokens of an output (accumulator fragments of its
+// transpose, token block t at 16 blk(t)) to rows of `ld` elements, transposed
+// through 2 KB of shared memory, 16 bytes a lane; tokens < n.
+__device__ __forceinline__ void store_rows(bf16* buf, const float (&o)[8][4], bf16* out, int64_t ld, int n, bool rev) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int p = 0; p < 4; p++)  // four 8 x 8 tiles
+    stsm4t(buf + (4 * p + (lane >> 3)) * 64 + (lane & 7) * 8, pack2(o[2 * p][0], o[2 * p][1]),
+           pack2(o[2 * p][2], o[2 * p][3]), pack2(o[2 * p + 1][0], o[2 * p + 1][1]),
+           pack2(o[2 * p + 1][2], o[2 * p + 1][3]));
+  __syncwarp();
+#pragma unroll
+  for (int p = 0; p < 4; p++) {
+    const int m = lane >> 3, row = 16 * (rev ? 3 - p : p) + 8 * (m >> 1) + (lane & 7);
+    const uint4 v = *reinterpret_cast<const uint4*>(buf + (4 * p + m) * 64 + (lane & 7) * 8);
+    if (row < n) *reinterpret_cast<uint4*>(out + row * ld + 8 * (m & 1)) = v;
+  }
+}
 
 // One CTA carries one chain of a DVS-column value slice.  Warp w holds the
 // state's value rows 16 w .. of S^T as fp32 accumulator fragments for the whole
@@ -191,11 +283,10 @@ struct LinMaps {
 // mma.sync rather than tcgen05: the chain is bound by the instructions around
 // its products, and accumulators that are the next product's operands save
 // the round trips through TMEM and shared memory.
-template <int DK, int DVS, int DEC>
+template <int DK, int DVS, bool ONLY>
 __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u, int h, int slice) {
-  using SH = Shape<DK, DVS, DEC>;
-  constexpr int NTH = SH::NTH, NW = SH::NW, NTK = SH::NTK, SP = SH::SP;
-  constexpr bool ONLY = SH::ONLY;
+  using SH = Shape<DK, DVS, ONLY>;
+  constexpr int NTH = SH::NTH, NW = SH::NW, NTK = SH::NTK;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (mma::smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char* tP = smem + SH::STG * SH::STAGE;  // [2 parts][64][64]
@@ -208,8 +299,7 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
 
   Unit un;
   if (!unit_of(P, u, un)) return;
-  const int nseg = P.seg ? max(1, (un.dlen + P.L - 1) / P.L) : 1;
-  if (ONLY && un.seg == (op.rev ? 0 : nseg - 1)) return;  // the last segment of its direction feeds nobody
+  if (ONLY && un.seg == (op.rev ? 0 : un.nseg - 1)) return;  // the last segment of its direction feeds nobody
   const int H = P.H, DVt = op.DVt, c0 = slice * DVS;
   const int64_t stN = (int64_t)DK * DVt;
   const float a = decay_of(P.A_log, h);
@@ -218,7 +308,7 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
   auto blk = [&](int t) { return rev ? 3 - t : t; };  // 16-token block t in the chain's direction
 
   auto load = [&](int c) {  // one thread
-    const int t0 = un.tok0 + C * (rev ? nch - 1 - c : c), s = SH::STG == 2 ? c & 1 : 0;
+    const int t0 = un.tok0 + C * (rev ? nch - 1 - c : c), s = c & 1;
     unsigned char* p = smem + s * SH::STAGE;
     mma::mbar_expect_tx(bar + s, SH::STAGE);
 #pragma unroll
@@ -227,7 +317,6 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
       mma::tma_load_2d(p + SH::XB + 8192 * b, &maps.y, h * DK + 64 * b, t0, bar + s);
     }
     mma::tma_load_2d(p + SH::XB + SH::YB, &maps.z, h * DVt + c0, t0, bar + s);
-    if constexpr (SH::HASW) mma::tma_load_2d(p + SH::XB + SH::YB + SH::ZB, &maps.w, h * DVt + c0, t0, bar + s);
   };
   if (tid == 0) {
     for (int s = 0; s < SH::STG; s++) mma::mbar_init(bar + s, 1);
@@ -242,33 +331,39 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
   }
   int n_w = -1;  // rows for which sw and rwt are set
 
-  float S[NTK][4], R[SH::HASR ? NTK : 1][4];
+  float S[NTK][4];
   mma::zero<NTK>(S);
-  mma::zero<SH::HASR ? NTK : 1>(R);
-  auto each_st = [&](auto fn) {
+  auto each_at = [&](int tr, auto fn) {
 #pragma unroll
     for (int j = 0; j < NTK; j++)
 #pragma unroll
       for (int e = 0; e < 4; e++)
-        fn(S[j][e], R[SH::HASR ? j : 0][e],
-           st_at(op.tr, c0 + 16 * warp + gq + 8 * (e >> 1), 8 * j + 2 * tq + (e & 1), DK, DVt));
+        fn(S[j][e], st_at(tr, c0 + 16 * warp + gq + 8 * (e >> 1), 8 * j + 2 * tq + (e & 1), DK, DVt));
   };
-  if (!ONLY) start_state<DEC == 1>(P, op, un, u, h, nseg, a, stN, each_st);
+  if (!ONLY) start_state(P, op, un, u, h, stN, [&](auto fn) { each_at(0, fn); });
 
   const Frag<DK, 1> k1;   // x and y tiles
   const Frag<DK, 2> k2;
-  const Frag<DVS, 1> v1;  // z and w tiles
-  const Frag<DVS, 2> v2;
+  const Frag<DVS, 2> v2;  // z tile
   const Frag<64, 2> p2;   // pairs
 
-  double dacc = 0.0;  // this thread's part of the decay gradient's sums
   bool good = true;
   for (int c = 0; c < nch; c++) {
     const int idx = rev ? nch - 1 - c : c, t0 = un.tok0 + C * idx, n = min(C, un.ntok - C * idx);
-    const int st = SH::STG == 2 ? c & 1 : 0;
+    const int st = c & 1;
     unsigned char* stg = smem + st * SH::STAGE;
-    const uint32_t tX = mma::smem_u32(stg), tY = tX + SH::XB, tZ = tY + SH::YB, tW = tZ + SH::ZB;
-    good = mma::mbar_wait(bar + st, (SH::STG == 2 ? c >> 1 : c) & 1);
+    const uint32_t tX = mma::smem_u32(stg), tY = tX + SH::XB, tZ = tY + SH::YB;
+    if (!ONLY && op.states) {  // the state where the chain enters the chunk, [dv][dk]
+      float* p = op.states + ((int64_t)(un.ch0 + idx) * H + h) * stN + (int64_t)(c0 + 16 * warp + gq) * DK + 2 * tq;
+      const float m = rev ? P.scale : 1.0f;
+#pragma unroll
+      for (int j = 0; j < NTK; j++)
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+          *reinterpret_cast<float2*>(p + 8 * k * DK + 8 * j) = make_float2(m * S[j][2 * k], m * S[j][2 * k + 1]);
+      if (!rev && h == 0 && slice == 0 && tid == 0) P.chunks[un.ch0 + idx] = make_int2(t0, n);
+    }
+    good = mma::mbar_wait(bar + st, (c >> 1) & 1);
     if (n != n_w) {  // the first chunk, and the one that is not full
       if (n_w >= 0) __syncthreads();
       for (int i = tid; i < C; i += NTH) {
@@ -276,25 +371,16 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
         rwt[i] = i < n ? P.scale * tab[rev ? n - 1 - i : i + 1] : 0.f;
       }
       n_w = n;
-      // rows past the chunk hold other documents' tokens: zero, so that nothing of them (an infinity)
-      // enters a product.  (64-byte rows: 16-byte groups 4 row ..; 128-byte rows 8 row .. of each 8 KB)
-      if (n < C) {
-        for (int g = tid; g < SH::STAGE / 16; g += NTH) {
-          const int b = 16 * g, dk_rows = DK == 32 ? 64 : 128, dv_rows = DVS == 32 ? 64 : 128;
-          const int row = b < SH::XB + SH::YB ? (b / dk_rows) & 63 : ((b - SH::XB - SH::YB) / dv_rows) & 63;
-          if (row >= n) *reinterpret_cast<uint4*>(stg + b) = make_uint4(0, 0, 0, 0);
-        }
-      }
     }
+    zero_rows<SH::STAGE, SH::XB + SH::YB, DK == 32 ? 64 : 128, DVS == 32 ? 64 : 128, NTH>(stg, n);
     mma::fence_async_smem();  // this thread's accesses to the other stage precede the copies into it
     // this chunk's tiles are complete; every reader of the last one is done
     if (__syncthreads_or(!good)) {
       good = false;
       break;
     }
-    if (SH::STG == 2 && tid == 0 && c + 1 < nch) load(c + 1);
+    if (tid == 0 && c + 1 < nch) load(c + 1);
 
-    float part = 0.f;
     float o[8][4];
     if constexpr (!ONLY) {
       // ---- pairs: three blocks at a time, so that consecutive products are independent
@@ -342,65 +428,29 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
               *reinterpret_cast<uint32_t*>(at) = s[0];
               *reinterpret_cast<uint32_t*>(at + 8192) = s[1];
             }
-          if constexpr (DEC == 1) {  // A: the same pairs of q and k (this slice's columns)
-            float m2[2][4];
-            mma::zero<2>(m2);
-#pragma unroll
-            for (int kk = 0; kk < DVS / 16; kk++) {
-              uint32_t fa[4], fb[4];
-              ldsm(fa, v1.at(tW, 16 * rr[t], 16 * kk));
-              ldsm(fb, v2.at(tZ, 16 * cc[t], 16 * kk));
-              mma::mma_bf16(m2[0], fa, fb[0], fb[1]);
-              mma::mma_bf16(m2[1], fa, fb[2], fb[3]);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; j++)
-#pragma unroll
-              for (int e = 0; e < 4; e++)
-                part = fmaf((float)(d + 8 * (e >> 1) - 8 * j - (e & 1)) * p[t][j][e], m2[j][e], part);
-          }
         }
       }
-      // ---- the entry state's rows: o^T = S^T x^T, and R^'s for the decay gradient
-      auto state_rows = [&](float (&acc)[8][4], const float (&st_)[NTK][4]) {
-        mma::zero<8>(acc);
+      // ---- the entry state's rows: o^T = S^T x^T
+      mma::zero<8>(o);
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; kk++) {
-          uint32_t f[SP][4], fb[4][4];
+      for (int kk = 0; kk < DK / 16; kk++) {
+        uint32_t f[2][4], fb[4][4];
 #pragma unroll
-          for (int p = 0; p < 4; p++) ldsm(fb[p], k2.at(tX, 16 * blk(p), 16 * kk));
+        for (int p = 0; p < 4; p++) ldsm(fb[p], k2.at(tX, 16 * blk(p), 16 * kk));
 #pragma unroll
-          for (int q = 0; q < 4; q++) {  // accumulator tiles 2 kk, 2 kk + 1 are the 16 x 16 operand
-            uint32_t s[SP];
-            split2<SP>(st_[2 * kk + (q >> 1)][2 * (q & 1)], st_[2 * kk + (q >> 1)][2 * (q & 1) + 1], s);
-#pragma unroll
-            for (int b = 0; b < SP; b++) f[b][q] = s[b];
-          }
-#pragma unroll
-          for (int b = SP - 1; b >= 0; b--)
-#pragma unroll
-            for (int p = 0; p < 4; p++) {
-              mma::mma_bf16(acc[2 * p], f[b], fb[p][0], fb[p][1]);
-              mma::mma_bf16(acc[2 * p + 1], f[b], fb[p][2], fb[p][3]);
-            }
+        for (int q = 0; q < 4; q++) {  // accumulator tiles 2 kk, 2 kk + 1 are the 16 x 16 operand
+          uint32_t s[2];
+          split2<2>(S[2 * kk + (q >> 1)][2 * (q & 1)], S[2 * kk + (q >> 1)][2 * (q & 1) + 1], s);
+          f[0][q] = s[0];
+          f[1][q] = s[1];
         }
-      };
-      state_rows(o, S);
-      if constexpr (DEC == 1) {  // B and D
-        float qr[8][4];
-        state_rows(qr, R);
 #pragma unroll
-        for (int p = 0; p < 4; p++) {
-          uint32_t f[4];
-          ldsm_t(f, v2.at(tW, 16 * p, 16 * warp));
+        for (int b = 1; b >= 0; b--)
 #pragma unroll
-          for (int q = 0; q < 4; q++) {
-            const int j = 2 * p + (q >> 1), e = 2 * (q & 1), i = 8 * j + 2 * tq;
-            const float2 w = *reinterpret_cast<const float2*>(rwt + i);
-            part = fmaf(w.x * even(f[q]), fmaf((float)(i + 1), o[j][e], qr[j][e]), part);
-            part = fmaf(w.y * odd(f[q]), fmaf((float)(i + 2), o[j][e + 1], qr[j][e + 1]), part);
+          for (int p = 0; p < 4; p++) {
+            mma::mma_bf16(o[2 * p], f[b], fb[p][0], fb[p][1]);
+            mma::mma_bf16(o[2 * p + 1], f[b], fb[p][2], fb[p][3]);
           }
-        }
       }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
@@ -410,20 +460,6 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
         o[j][2] *= w.x;
         o[j][3] *= w.y;
       }
-      if constexpr (DEC == 2) {  // C
-#pragma unroll
-        for (int p = 0; p < 4; p++) {
-          uint32_t f[4];
-          ldsm_t(f, v2.at(tW, 16 * blk(p), 16 * warp));
-#pragma unroll
-          for (int q = 0; q < 4; q++) {
-            const int j = 2 * p + (q >> 1), e = 2 * (q & 1), i = n - 1 - (16 * blk(p) + 8 * (q >> 1) + 2 * tq);
-            part = fmaf((float)i * even(f[q]), o[j][e], part);
-            part = fmaf((float)(i - 1) * odd(f[q]), o[j][e + 1], part);
-          }
-        }
-      }
-      if constexpr (SH::HASW) dacc += (double)part;
     }
     // ---- the state: S^T = e^{-an} S^T + (weighted z)^T y.  The product is summed apart from the
     // state (the tensor core truncates what an addition shifts out: into a long chain's state that
@@ -432,16 +468,14 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
 #pragma unroll
     for (int kk = 0; kk < 4; kk++) ldsm_t(zr[kk], v2.at(tZ, 16 * blk(kk), 16 * warp));
     const Decay dec(a, n);
-#pragma unroll
-    for (int g = 0; g < SH::JG; g++) {
-      constexpr int NG = NTK / SH::JG;
-      float d[NG][4];
-      mma::zero<NG>(d);
+    {
+      float d[NTK][4];
+      mma::zero<NTK>(d);
 #pragma unroll
       for (int kk = 0; kk < 4; kk++) {
-        uint32_t fb[NG / 2][4];
+        uint32_t fb[NTK / 2][4];
 #pragma unroll
-        for (int p = 0; p < NG / 2; p++) ldsm_t(fb[p], k1.at(tY, 16 * blk(kk), 8 * NG * g + 16 * p));
+        for (int p = 0; p < NTK / 2; p++) ldsm_t(fb[p], k1.at(tY, 16 * blk(kk), 16 * p));
         uint32_t za[3][4];
 #pragma unroll
         for (int q = 0; q < 4; q++) {
@@ -454,19 +488,15 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
 #pragma unroll
         for (int b = 2; b >= 0; b--)
 #pragma unroll
-          for (int p = 0; p < NG / 2; p++) {
+          for (int p = 0; p < NTK / 2; p++) {
             mma::mma_bf16(d[2 * p], za[b], fb[p][0], fb[p][1]);
             mma::mma_bf16(d[2 * p + 1], za[b], fb[p][2], fb[p][3]);
           }
       }
 #pragma unroll
-      for (int j = 0; j < NG; j++)
+      for (int j = 0; j < NTK; j++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          float& s = S[NG * g + j][e];
-          if constexpr (SH::HASR) R[NG * g + j][e] = dec(fmaf((float)n, s, R[NG * g + j][e]));
-          s = dec(s) + d[j][e];
-        }
+        for (int e = 0; e < 4; e++) S[j][e] = dec(S[j][e]) + d[j][e];
     }
     if constexpr (!ONLY) {
       __syncthreads();  // the pairs of every warp; x and y have been read
@@ -484,22 +514,302 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
             mma::mma_bf16(o[2 * p + 1], zr[kk], fb[p][2], fb[p][3]);
           }
         }
-      // ---- out: transposed through the warp's 2 KB of the x and y tiles, 16 bytes a lane
-      bf16* tO = reinterpret_cast<bf16*>(stg) + warp * 64 * 16;
+      // ---- out, through the warp's 2 KB of the x and y tiles
+      store_rows(reinterpret_cast<bf16*>(stg) + warp * 1024, o, (bf16*)op.out + ((int64_t)t0 * H + h) * DVt + c0 + 16 * warp,
+                 (int64_t)H * DVt, n, rev);
+    }
+  }
+  if (!good) {  // a wait ran out
+    if (tid == 0) *P.err = KDA_ERR_DEVICE;
+    return;
+  }
+
+  // ---- the unit's state
+  if (ONLY) {
+    float* p = op.segc + ((int64_t)u * H + h) * stN;
+    each_at(0, [&](float& s, int64_t at) { p[at] = s; });
+  } else if (op.fin && un.seg == (rev ? 0 : un.nseg - 1)) {
+    float* p = op.fin + ((int64_t)un.doc * H + h) * stN;
+    const float mul = rev ? P.scale : 1.0f;
+    each_at(0, [&](float& s, int64_t at) { p[at] = mul * s; });
+  }
+}
+
+template <int DK, int DVS, bool ONLY>
+__global__ void __launch_bounds__(Shape<DK, DVS, ONLY>::NTH, Shape<DK, DVS, ONLY>::CTAS)
+    lin_chain_kernel(const __grid_constant__ LinMaps maps, LinP P, LinOp op, int fwd) {
+  if (!ready(P, fwd)) return;
+  const int ns = op.DVt / DVS;
+  chain<DK, DVS, ONLY>(P, op, maps, blockIdx.x / (ns * P.H), (blockIdx.x / ns) % P.H, blockIdx.x % ns);
+}
+
+// ------------------------------------------------------------ dq and dk, bf16
+// Every chunk by itself, from its entry state S and its exit state's gradient
+// R (fp32, [dv][dk]): with P = scale e^{-a(i-j)} (dO_i . v_j), i >= j,
+//   dq_i = sum_j P_ij k_j + scale e^{-a(i+1)} S dO_i
+//   dk_j = sum_i P_ij q_i + e^{-a(n-1-j)} R v_j
+// and, with DA, the decay gradient's A, B, C, D.  A CTA takes CPB chunks of a
+// head and a DVS-column slice of dk; warp w forms rows 16 w .. of dq^T and dk^T
+// and reads its rows of S and R from memory as operand fragments, once.
+constexpr int CPB = 4;
+
+template <int DV, int DVS, bool DA>
+struct DShape {
+  static constexpr int NW = DVS / 16, NTH = 32 * NW;
+  static constexpr int OB = 128 * DV, QB = 128 * DVS;  // bytes of the dO and v, the q and k tiles
+  static constexpr int STAGE = 2 * OB + 2 * QB;
+  static constexpr int STG = DV == 128 ? 1 : 2;        // (one stage there: three CTAs per SM)
+  static constexpr int PB = 2 * 64 * 64 * 2;
+  static constexpr int SMEM = 1024 + STG * STAGE + PB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
+  static constexpr int SP = DA ? 3 : 2;  // parts of the states as operands: fp32 sums need the third
+  static constexpr int BY_REG = 65536 / (NTH * 168), BY_SMEM = 227 * 1024 / (SMEM + 1024);
+  static constexpr int CTAS = BY_REG < BY_SMEM ? BY_REG : BY_SMEM;
+};
+
+struct DqkMaps {
+  CUtensorMap q, k, v, dO;
+};
+struct DqkOp {
+  void *dq, *dk;
+  const float *S, *R;
+  double* pda;
+};
+
+template <int DV, int DVS, bool DA>
+__global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>::CTAS)
+    lin_dqk_kernel(const __grid_constant__ DqkMaps maps, LinP P, DqkOp op, int DKt) {
+  using SH = DShape<DV, DVS, DA>;
+  constexpr int NTH = SH::NTH, NW = SH::NW, SP = SH::SP;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (mma::smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* tP = smem + SH::STG * SH::STAGE;  // [2 parts][64][64]
+  float2* lut = reinterpret_cast<float2*>(tP + SH::PB);
+  float* tab = reinterpret_cast<float*>(lut + 128);
+  float* rq = tab + 96;  // [64] scale e^{-a(i+1)}
+  float* rk = rq + 64;   // [64] e^{-a(n-1-j)}
+  uint64_t* bar = reinterpret_cast<uint64_t*>(rk + 64);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
+  const int ns = DKt / DVS, slice = blockIdx.x % ns, h = (blockIdx.x / ns) % P.H, g0 = blockIdx.x / (ns * P.H) * CPB;
+  if (!ready(P, 0)) return;
+  const int nchunks = P.rows ? P.nc : P.counts[1], nch = min(CPB, nchunks - g0);
+  if (nch <= 0) {
+    if (DA && tid == 0) op.pda[blockIdx.x] = 0.0;
+    return;
+  }
+  const int H = P.H, c0 = slice * DVS;
+  const float a = decay_of(P.A_log, h);
+  auto chunk = [&](int c) -> int2 {  // {first token, tokens}
+    const int g = g0 + c;
+    if (!P.rows) return P.chunks[g];
+    const int cpr = (P.T + C - 1) / C, r = g / cpr, i = g % cpr;
+    return make_int2(r * P.T + i * C, min(C, P.T - i * C));
+  };
+  auto load = [&](int c) {  // one thread
+    const int t0 = chunk(c).x, s = SH::STG == 2 ? c & 1 : 0;
+    unsigned char* p = smem + s * SH::STAGE;
+    mma::mbar_expect_tx(bar + s, SH::STAGE);
 #pragma unroll
-      for (int p = 0; p < 4; p++)  // four 8 x 8 tiles: 16 tokens by the warp's 16 columns
-        stsm4t(tO + (4 * p + (lane >> 3)) * 64 + (lane & 7) * 8, pack2(o[2 * p][0], o[2 * p][1]),
-               pack2(o[2 * p][2], o[2 * p][3]), pack2(o[2 * p + 1][0], o[2 * p + 1][1]),
-               pack2(o[2 * p + 1][2], o[2 * p + 1][3]));
-      __syncwarp();
-      bf16* po = (bf16*)op.out + ((int64_t)t0 * H + h) * DVt + c0 + 16 * warp;
+    for (int b = 0; b < (DV + 63) / 64; b++) {
+      mma::tma_load_2d(p + 8192 * b, &maps.dO, h * DV + 64 * b, t0, bar + s);
+      mma::tma_load_2d(p + SH::OB + 8192 * b, &maps.v, h * DV + 64 * b, t0, bar + s);
+    }
+    mma::tma_load_2d(p + 2 * SH::OB, &maps.q, h * DKt + c0, t0, bar + s);
+    mma::tma_load_2d(p + 2 * SH::OB + SH::QB, &maps.k, h * DKt + c0, t0, bar + s);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < SH::STG; s++) mma::mbar_init(bar + s, 1);
+    mma::mbar_init_fence();
+    load(0);
+  }
+  for (int i = tid; i < 65; i += NTH) tab[i] = decay_pow(a, i);
+  __syncthreads();
+  for (int i = tid; i < 128; i += NTH) {
+    const int m = i - 64;
+    lut[i] = make_float2(m >= 0 ? P.scale * tab[m] : 0.f, m >= 1 ? P.scale * tab[m - 1] : 0.f);
+  }
+  for (int i = tid; i < C; i += NTH) rq[i] = P.scale * tab[i + 1];
+  int n_w = -1;  // rows for which rk is set
+
+  const Frag<DV, 1> o1;   // dO and v tiles
+  const Frag<DV, 2> o2;
+  const Frag<DVS, 1> v1;  // q and k tiles
+  const Frag<DVS, 2> v2;
+  const Frag<64, 1> p1;   // pairs
+  const Frag<64, 2> p2;
+
+  double dacc = 0.0;
+  bool good = true;
+  for (int c = 0; c < nch; c++) {
+    const int2 ck = chunk(c);
+    const int t0 = ck.x, n = ck.y, st = SH::STG == 2 ? c & 1 : 0;
+    unsigned char* stg = smem + st * SH::STAGE;
+    const uint32_t tO = mma::smem_u32(stg), tV = tO + SH::OB, tQ = tV + SH::OB, tK = tQ + SH::QB;
+    good = mma::mbar_wait(bar + st, (SH::STG == 2 ? c >> 1 : c) & 1);
+    if (n != n_w) {
+      if (n_w >= 0) __syncthreads();
+      for (int i = tid; i < C; i += NTH) rk[i] = i < n ? tab[n - 1 - i] : 0.f;
+      n_w = n;
+    }
+    zero_rows<SH::STAGE, 2 * SH::OB, 128, DVS == 32 ? 64 : 128, NTH>(stg, n);
+    mma::fence_async_smem();  // this thread's accesses to the other stage precede the copies into it
+    if (__syncthreads_or(!good)) {
+      good = false;
+      break;
+    }
+    if (SH::STG == 2 && tid == 0 && c + 1 < nch) load(c + 1);
+
+    float part = 0.f;
+    // ---- pairs, three blocks at a time
+    for (uint64_t todo = pair_blocks<NW>(warp); todo; todo >>= 24) {
+      int rr[3], cc[3];
+      float p[3][2][4];
 #pragma unroll
-      for (int p = 0; p < 4; p++) {
-        const int m = lane >> 3, row = 16 * blk(p) + 8 * (m >> 1) + (lane & 7);
-        const uint4 v = *reinterpret_cast<const uint4*>(tO + (4 * p + m) * 64 + (lane & 7) * 8);
-        if (row < n) *reinterpret_cast<uint4*>(po + (int64_t)row * H * DVt + 8 * (m & 1)) = v;
+      for (int t = 0; t < 3; t++) {
+        int code = (int)(todo >> (8 * t)) & 255;
+        if (!code) code = (int)todo & 255;  // (the first once more, not stored)
+        rr[t] = (code - 1) >> 2;
+        cc[t] = (code - 1) & 3;
+        mma::zero<2>(p[t]);
+      }
+#pragma unroll
+      for (int kk = 0; kk < DV / 16; kk++) {
+        uint32_t fa[3][4], fb[3][4];
+#pragma unroll
+        for (int t = 0; t < 3; t++) {
+          ldsm(fa[t], o1.at(tO, 16 * rr[t], 16 * kk));
+          ldsm(fb[t], o2.at(tV, 16 * cc[t], 16 * kk));
+        }
+#pragma unroll
+        for (int t = 0; t < 3; t++) {
+          mma::mma_bf16(p[t][0], fa[t], fb[t][0], fb[t][1]);
+          mma::mma_bf16(p[t][1], fa[t], fb[t][2], fb[t][3]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 3; t++) {
+        if (t > 0 && !((todo >> (8 * t)) & 255)) continue;
+        const int d = 16 * (rr[t] - cc[t]) + gq - 2 * tq;  // row - column of the thread's first pair
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+          for (int k = 0; k < 2; k++) {
+            const float2 w = lut[64 + d + 8 * k - 8 * j];
+            p[t][j][2 * k] *= w.x;
+            p[t][j][2 * k + 1] *= w.y;
+            uint32_t s[2];
+            split2<2>(p[t][j][2 * k], p[t][j][2 * k + 1], s);
+            unsigned char* at = tP + (16 * rr[t] + 8 * k + gq) * 128 + (((2 * cc[t] + j) ^ gq) << 4) + 4 * tq;
+            *reinterpret_cast<uint32_t*>(at) = s[0];
+            *reinterpret_cast<uint32_t*>(at + 8192) = s[1];
+          }
+        if constexpr (DA) {  // A: the same pairs of q and k (this slice's columns)
+          float m2[2][4];
+          mma::zero<2>(m2);
+#pragma unroll
+          for (int kk = 0; kk < DVS / 16; kk++) {
+            uint32_t fa[4], fb[4];
+            ldsm(fa, v1.at(tQ, 16 * rr[t], 16 * kk));
+            ldsm(fb, v2.at(tK, 16 * cc[t], 16 * kk));
+            mma::mma_bf16(m2[0], fa, fb[0], fb[1]);
+            mma::mma_bf16(m2[1], fa, fb[2], fb[3]);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              part = fmaf((float)(d + 8 * (e >> 1) - 8 * j - (e & 1)) * p[t][j][e], m2[j][e], part);
+        }
       }
     }
+    // ---- the states' rows: gq^T = S dO^T, gk^T = R v^T
+    float dq[8][4], dk[8][4];
+    mma::zero<8>(dq);
+    mma::zero<8>(dk);
+    const int64_t sat = ((int64_t)(g0 + c) * H + h) * DV * DKt + c0 + 16 * warp + gq;
+    const float *pS = op.S + sat, *pR = op.R + sat;
+    float dot = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < DV / 16; kk++) {
+      uint32_t fs[SP][4], fr[SP][4];
+#pragma unroll
+      for (int q = 0; q < 4; q++) {  // rows (dk) gq + 8 (q & 1), columns (dv) 16 kk + 8 (q >> 1) + 2 tq, + 1
+        const int64_t at = (int64_t)(16 * kk + 8 * (q >> 1) + 2 * tq) * DKt + 8 * (q & 1);
+        const float s0 = __ldg(pS + at), s1 = __ldg(pS + at + DKt), r0 = __ldg(pR + at), r1 = __ldg(pR + at + DKt);
+        if constexpr (DA) dot = fmaf(s0, r0, fmaf(s1, r1, dot));
+        uint32_t w[SP];
+        split2<SP>(s0, s1, w);
+#pragma unroll
+        for (int b = 0; b < SP; b++) fs[b][q] = w[b];
+        split2<SP>(r0, r1, w);
+#pragma unroll
+        for (int b = 0; b < SP; b++) fr[b][q] = w[b];
+      }
+      uint32_t fo[4][4], fv[4][4];
+#pragma unroll
+      for (int p = 0; p < 4; p++) {
+        ldsm(fo[p], o2.at(tO, 16 * p, 16 * kk));
+        ldsm(fv[p], o2.at(tV, 16 * p, 16 * kk));
+      }
+#pragma unroll
+      for (int b = SP - 1; b >= 0; b--)
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+          mma::mma_bf16(dq[2 * p], fs[b], fo[p][0], fo[p][1]);
+          mma::mma_bf16(dq[2 * p + 1], fs[b], fo[p][2], fo[p][3]);
+          mma::mma_bf16(dk[2 * p], fr[b], fv[p][0], fv[p][1]);
+          mma::mma_bf16(dk[2 * p + 1], fr[b], fv[p][2], fv[p][3]);
+        }
+    }
+    uint32_t fq[4][4], fk[4][4];  // q^T and k^T, rows 16 warp ..
+#pragma unroll
+    for (int p = 0; p < 4; p++) {
+      ldsm_t(fq[p], v2.at(tQ, 16 * p, 16 * warp));
+      ldsm_t(fk[p], v2.at(tK, 16 * p, 16 * warp));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const int i = 8 * j + 2 * tq;
+      const float2 wq = *reinterpret_cast<const float2*>(rq + i), wk = *reinterpret_cast<const float2*>(rk + i);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        dq[j][e] *= e & 1 ? wq.y : wq.x;
+        dk[j][e] *= e & 1 ? wk.y : wk.x;
+        if constexpr (DA) {  // B and C (the fragments' rows and tokens are the accumulators')
+          const uint32_t uq = fq[j >> 1][2 * (j & 1) + (e >> 1)], uk = fk[j >> 1][2 * (j & 1) + (e >> 1)];
+          part = fmaf((float)(i + (e & 1) + 1) * (e & 1 ? odd(uq) : even(uq)), dq[j][e], part);
+          part = fmaf((float)(n - 1 - i - (e & 1)) * (e & 1 ? odd(uk) : even(uk)), dk[j][e], part);
+        }
+      }
+    }
+    if constexpr (DA) dacc += (double)part + (double)(dot * (float)n * tab[n]);
+    __syncthreads();  // the pairs of every warp; dO and v have been read
+    // ---- dq^T += k^T P^T, dk^T += q^T P
+#pragma unroll
+    for (int kk = 0; kk < 4; kk++)
+#pragma unroll
+      for (int b = 1; b >= 0; b--) {
+        const uint32_t tp = mma::smem_u32(tP) + 8192 * b;
+        uint32_t fp[4][4];
+#pragma unroll
+        for (int p = kk; p < 4; p++) ldsm(fp[p], p2.at(tp, 16 * p, 16 * kk));  // tokens i of block p, j of kk
+#pragma unroll
+        for (int p = kk; p < 4; p++) {
+          mma::mma_bf16(dq[2 * p], fk[kk], fp[p][0], fp[p][1]);
+          mma::mma_bf16(dq[2 * p + 1], fk[kk], fp[p][2], fp[p][3]);
+        }
+#pragma unroll
+        for (int p = 0; p <= kk; p++) ldsm_t(fp[p], p1.at(tp, 16 * kk, 16 * p));  // tokens i of block kk, j of p
+#pragma unroll
+        for (int p = 0; p <= kk; p++) {
+          mma::mma_bf16(dk[2 * p], fq[kk], fp[p][0], fp[p][1]);
+          mma::mma_bf16(dk[2 * p + 1], fq[kk], fp[p][2], fp[p][3]);
+        }
+      }
+    // ---- out, through the warp's 4 KB of the dO and v tiles
+    store_rows(reinterpret_cast<bf16*>(stg) + warp * 2048, dq, (bf16*)op.dq + ((int64_t)t0 * H + h) * DKt + c0 + 16 * warp,
+               (int64_t)H * DKt, n, false);
+    store_rows(reinterpret_cast<bf16*>(stg) + warp * 2048 + 1024, dk,
+               (bf16*)op.dk + ((int64_t)t0 * H + h) * DKt + c0 + 16 * warp, (int64_t)H * DKt, n, false);
     if (SH::STG == 1 && c + 1 < nch) {
       mma::fence_async_smem();
       __syncthreads();
@@ -510,28 +820,7 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
     if (tid == 0) *P.err = KDA_ERR_DEVICE;
     return;
   }
-
-  // ---- the unit's state
-  const bool last = un.seg == (rev ? 0 : nseg - 1);
-  float* pf = nullptr;
-  float mul = 1.0f;
-  if (ONLY) {
-    pf = const_cast<float*>(op.segc) + ((int64_t)u * H + h) * stN * (rev ? 1 : 2);
-  } else if (last && op.fin) {
-    pf = op.fin + ((int64_t)un.doc * H + h) * stN;
-    mul = rev ? P.scale : 1.0f;
-  }
-  const float* pd = DEC == 1 && last && op.dfin ? op.dfin + ((int64_t)un.doc * H + h) * stN : nullptr;
-  float part = 0.f;
-  each_st([&](float& s, float& r, int64_t at) {
-    if (pf) pf[at] = mul * s;
-    if constexpr (DEC == 4) pf[stN + at] = r;
-    if constexpr (DEC == 1) {
-      if (pd) part = fmaf(r, pd[at], part);
-    }
-  });
-  if constexpr (SH::HASW) {  // the CTA's partial, summed in a fixed order
-    dacc += (double)part;
+  if constexpr (DA) {  // the CTA's partial, summed in a fixed order
     double* red = reinterpret_cast<double*>(lut);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) dacc += __shfl_xor_sync(0xffffffffu, dacc, s);
@@ -541,29 +830,22 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
     if (tid == 0) {
       double s = 0.0;
       for (int w = 0; w < NW; w++) s += red[w];
-      op.pda[((int64_t)u * H + h) * (DVt / DVS) + slice] = s;
+      op.pda[blockIdx.x] = s;
     }
   }
 }
 
-template <int DK, int DVS, int DEC>
-__global__ void __launch_bounds__(Shape<DK, DVS, DEC>::NTH, Shape<DK, DVS, DEC>::CTAS)
-    lin_chain_kernel(const __grid_constant__ LinMaps maps, LinP P, LinOp op, int fwd) {
-  if (!ready(P, fwd)) return;
-  const int ns = op.DVt / DVS;
-  chain<DK, DVS, DEC>(P, op, maps, blockIdx.x / (ns * P.H), (blockIdx.x / ns) % P.H, blockIdx.x % ns);
-}
-
-// dA_log[h] = -a (sum of the partials), in a fixed order.
-__global__ void __launch_bounds__(256) lin_decay_kernel(LinP P, const double* p1, int n1, const double* p2, int n2,
-                                                        float* dA) {
+// dA_log[h] = -a (sum of the partials), in a fixed order: per head n1 of each of
+// cnt1 groups, n2 of each of cnt2.
+__global__ void __launch_bounds__(256) lin_decay_kernel(LinP P, const double* p1, int64_t cnt1, int n1,
+                                                        const double* p2, int64_t cnt2, int n2, float* dA) {
   __shared__ double red[256];
   const int h = blockIdx.x;
+  pdl_wait();
   if (*P.wtag != P.tag || *P.err != KDA_OK) return;
-  const int nu = P.rows ? P.nu : *P.n_units;
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < (int64_t)nu * n1; i += 256) s += p1[((i / n1) * P.H + h) * n1 + i % n1];
-  for (int64_t i = threadIdx.x; i < (int64_t)nu * n2; i += 256) s += p2[((i / n2) * P.H + h) * n2 + i % n2];
+  for (int64_t i = threadIdx.x; i < cnt1 * n1; i += 256) s += p1[((i / n1) * P.H + h) * n1 + i % n1];
+  for (int64_t i = threadIdx.x; i < cnt2 * n2; i += 256) s += p2[((i / n2) * P.H + h) * n2 + i % n2];
   red[threadIdx.x] = s;
   __syncthreads();
   for (int o = 128; o > 0; o >>= 1) {
@@ -574,45 +856,66 @@ __global__ void __launch_bounds__(256) lin_decay_kernel(LinP P, const double* p1
 }
 
 // ------------------------------------------------------------ launches
-template <int DK, int DVS, int DEC>
+template <int DK, int DVS, bool ONLY>
 cudaError_t launch_chain(int kid, const LinP& P, const LinOp& op, int fwd, cudaStream_t st) {
-  using SH = Shape<DK, DVS, DEC>;
-  cudaError_t e = raise_smem<lin_chain_kernel<DK, DVS, DEC>>(SH::SMEM);
+  using SH = Shape<DK, DVS, ONLY>;
+  cudaError_t e = raise_smem<lin_chain_kernel<DK, DVS, ONLY>>(SH::SMEM);
   if (e != cudaSuccess) return e;
   LinMaps m = {};
-  if (!encode_head_rows(&m.x, op.x, P.Ntok, P.H, DK) || !encode_head_rows(&m.y, op.y, P.Ntok, P.H, DK) ||
-      !encode_head_rows(&m.z, op.z, P.Ntok, P.H, op.DVt) ||
-      (SH::HASW && !encode_head_rows(&m.w, op.wx, P.Ntok, P.H, op.DVt)))
+  if ((!ONLY && !encode_head_rows(&m.x, op.x, P.Ntok, P.H, DK)) || !encode_head_rows(&m.y, op.y, P.Ntok, P.H, DK) ||
+      !encode_head_rows(&m.z, op.z, P.Ntok, P.H, op.DVt))
     return cudaErrorInvalidValue;
   prof_begin(kid, st);
-  lin_chain_kernel<DK, DVS, DEC>
+  lin_chain_kernel<DK, DVS, ONLY>
       <<<(unsigned)((int64_t)P.nu * P.H * (op.DVt / DVS)), SH::NTH, SH::SMEM, st>>>(m, P, op, fwd);
   prof_end(kid, st);
   return cudaGetLastError();
 }
 
-// The chain whose state has `key` key columns (op.DVt value columns).
-template <typename T, int DEC>
-cudaError_t dispatch(int kid, int key, const LinP& P, const LinOp& op, int fwd, cudaStream_t st) {
-  if constexpr (sizeof(T) == 4) {
-    return launch_f32(DEC, kid, key, P, op, fwd, st);
-  } else {
-    if constexpr (DEC != 1 && DEC != 2) {  // (the gradients' chains have dv as their key side)
-      if (key == 32) return launch_chain<32, 64, DEC>(kid, P, op, fwd, st);
-    }
-    if constexpr (DEC < 3) {
-      if (key == 64 && op.DVt == 32) return launch_chain<64, 32, DEC>(kid, P, op, fwd, st);
-    }
-    if (key == 64) return launch_chain<64, 64, DEC>(kid, P, op, fwd, st);
-    return launch_chain<128, 64, DEC>(kid, P, op, fwd, st);
-  }
+template <bool ONLY>
+cudaError_t launch_bf16(int kid, int key, const LinP& P, const LinOp& op, int fwd, cudaStream_t st) {
+  if (key == 32) return launch_chain<32, 64, ONLY>(kid, P, op, fwd, st);
+  if (key == 64) return launch_chain<64, 64, ONLY>(kid, P, op, fwd, st);
+  return launch_chain<128, 64, ONLY>(kid, P, op, fwd, st);
+}
+
+struct LinGrads {
+  const void *q, *k, *v, *dO;
+  const float *h0, *dhf;
+  void *dq, *dk, *dv;
+  float *dA, *dh0;
+};
+
+int64_t dqk_groups(const LinP& P) { return (P.nc + CPB - 1) / CPB; }
+
+template <int DV, int DVS, bool DA>
+cudaError_t launch_dqk(const LinP& P, const LinGrads& g, const DqkOp& op, int dk, cudaStream_t st) {
+  using SH = DShape<DV, DVS, DA>;
+  cudaError_t e = raise_smem<lin_dqk_kernel<DV, DVS, DA>>(SH::SMEM);
+  if (e != cudaSuccess) return e;
+  DqkMaps m = {};
+  if (!encode_head_rows(&m.q, g.q, P.Ntok, P.H, dk) || !encode_head_rows(&m.k, g.k, P.Ntok, P.H, dk) ||
+      !encode_head_rows(&m.v, g.v, P.Ntok, P.H, DV) || !encode_head_rows(&m.dO, g.dO, P.Ntok, P.H, DV))
+    return cudaErrorInvalidValue;
+  prof_begin(K_LIN_DQK, st);
+  lin_dqk_kernel<DV, DVS, DA>
+      <<<(unsigned)(dqk_groups(P) * P.H * (dk / DVS)), SH::NTH, SH::SMEM, st>>>(m, P, op, dk);
+  prof_end(K_LIN_DQK, st);
+  return cudaGetLastError();
+}
+
+template <bool DA>
+cudaError_t dqk(const LinP& P, const Dims& d, const LinGrads& g, const DqkOp& op, cudaStream_t st) {
+  if (d.dk == 32) return launch_dqk<64, 32, DA>(P, g, op, 32, st);
+  if (d.dv == 64) return launch_dqk<64, 64, DA>(P, g, op, 64, st);
+  return launch_dqk<128, 64, DA>(P, g, op, d.dk, st);
 }
 
 int value_slice(int dtype, int DVt) { return dtype == KDA_F32 || DVt == 32 ? 32 : 64; }
 
 // ------------------------------------------------------------ plan, workspace
 struct LinLayout {
-  size_t off_nu, off_units, off_segf, off_segr, off_p1, off_p2, total;
+  size_t off_counts, off_units, off_ch0, off_longs, off_chunks, off_segf, off_segr, off_S, off_R, off_p1, off_p2, total;
 };
 
 // Segment length: long documents are cut so that about two chain CTAs per SM
@@ -632,13 +935,16 @@ void lin_plan(const kda_problem* p, const Dims& d, LinP& P) {
   P.T = d.T;
   P.rows = d.rows;
   P.L = (int)L;
+  P.nc = d.nc_max;
   P.scale = d.scale;
   P.cu = p->cu_seqlens;
   if (P.rows) {
     P.seg = d.T > L;
     P.nu = d.B * (int)((d.T + L - 1) / L);
+    P.n_long = d.B;
   } else {
     P.nu = d.n_docs + (int)(d.Ntok / L);
+    P.n_long = (int)(d.Ntok / L);
     P.seg = d.Ntok > L;
     if (p->cu_seqlens_host && P.seg) {
       P.seg = 0;
@@ -648,20 +954,31 @@ void lin_plan(const kda_problem* p, const Dims& d, LinP& P) {
   P.tag = d.tag ^ 0x4c696e;
 }
 
-LinLayout lin_layout(const Dims& d, const LinP& P, int for_bwd) {
+LinLayout lin_layout(const kda_problem* p, const Dims& d, const LinP& P, int for_bwd) {
   LinLayout L = {};
   size_t o = 256;  // error word, saved-problem tag
   auto take = [&](size_t bytes) { const size_t r = o; o = (o + bytes + 255) & ~(size_t)255; return r; };
-  const size_t st = (size_t)P.nu * d.H * d.dk * d.dv * 4;
-  L.off_nu = take(4);
-  L.off_units = take(P.rows ? 0 : 16 * (size_t)P.nu);
+  const size_t st = (size_t)d.H * d.dk * d.dv * 4;
+  if (!P.rows) {
+    L.off_counts = take(12);
+    L.off_units = take(16 * (size_t)P.nu);
+    L.off_ch0 = take(4 * (size_t)P.nu);
+    L.off_longs = take(8 * (size_t)(P.n_long + 1));
+  }
   // sized as if every long document were cut: whether any is may be known on the device alone
   const bool seg = P.rows ? P.seg : d.Ntok > P.L;
-  L.off_segf = take(seg ? 2 * st : 0);
+  L.off_segf = take(seg ? P.nu * st : 0);
   if (for_bwd) {
-    L.off_segr = take(seg ? st : 0);
-    L.off_p1 = take(8 * (size_t)P.nu * d.H * (d.dk / 32));
-    L.off_p2 = take(8 * (size_t)P.nu * d.H * (d.dk / 32));
+    L.off_chunks = take(8 * (size_t)P.nc);
+    L.off_segr = take(seg ? P.nu * st : 0);
+    L.off_S = take(P.nc * st);
+    if (p->dtype == KDA_F32) {
+      L.off_p1 = take(8 * (size_t)P.nu * d.H * (d.dk / 32));
+      L.off_p2 = take(8 * (size_t)P.nu * d.H * (d.dk / 32));
+    } else {
+      L.off_R = take(P.nc * st);
+      L.off_p1 = take(8 * (size_t)dqk_groups(P) * d.H * (d.dk / value_slice(p->dtype, d.dk)));
+    }
   }
   L.total = o;
   return L;
@@ -674,38 +991,50 @@ kda_status lin_setup(const kda_problem* p, int for_bwd, void* ws, size_t bytes, 
   const kda_status s = check_problem(p, &d);
   if (s != KDA_OK) return s;
   lin_plan(p, d, P);
-  L = lin_layout(d, P, for_bwd);
-  if ((int64_t)P.nu * d.H * 4 > 2147483647LL) return KDA_ERR_INVALID_ARG;  // one CTA per unit, head and slice
+  L = lin_layout(p, d, P, for_bwd);
+  // one CTA per unit (chunk group, split document), head and slice on one grid axis
+  if ((int64_t)P.nu * d.H * 4 > 2147483647LL || (int64_t)P.nc * d.H * 4 > 2147483647LL) return KDA_ERR_INVALID_ARG;
   if (!ws) return KDA_ERR_WORKSPACE;
   if (!al(ws, 256)) return KDA_ERR_ALIGNMENT;
   if (bytes < L.total) return KDA_ERR_WORKSPACE;
   char* w = (char*)ws;
   P.err = (int32_t*)w;
   P.wtag = (int32_t*)(w + 4);
-  P.n_units = (int32_t*)(w + L.off_nu);
+  P.counts = (int32_t*)(w + L.off_counts);
   P.units = (int4*)(w + L.off_units);
+  P.unit_ch0 = (int32_t*)(w + L.off_ch0);
+  P.longs = (int2*)(w + L.off_longs);
+  P.chunks = (int2*)(w + L.off_chunks);
   P.A_log = A_log;
   P.save = for_bwd;
   return KDA_OK;
 }
 
-// The segments' own states of one direction.
+// The segments' start states of one direction (y, z: k, v, or in reverse q, dO).
 template <typename T>
-cudaError_t run_seg(const LinP& P, const Dims& d, const void* y, const void* z, float* segc, int rev, int want_r,
+cudaError_t run_seg(const LinP& P, const Dims& d, const void* y, const void* z, const float* init, float* segc, int rev,
                     int fwd, cudaStream_t st) {
   LinOp op = {};
-  op.x = y;
   op.y = y;
   op.z = z;
+  op.x = y;
   op.rev = rev;
   op.DVt = d.dv;
   op.segc = segc;
-  return want_r ? dispatch<T, 4>(K_LIN_SEG, d.dk, P, op, fwd, st) : dispatch<T, 3>(K_LIN_SEG, d.dk, P, op, fwd, st);
+  cudaError_t e = sizeof(T) == 4 ? launch_f32(3, K_LIN_SEG, d.dk, P, op, fwd, st)
+                                 : launch_bf16<true>(K_LIN_SEG, d.dk, P, op, fwd, st);
+  if (e != cudaSuccess) return e;
+  const int N = d.dk * d.dv;
+  prof_begin(K_LIN_FOLD, st);
+  e = launch_pdl(lin_fold_kernel, dim3((unsigned)P.n_long * d.H, N / 256), dim3(256), 0, st, P, segc, init, rev, N,
+                 fwd == 1 ? 2 : fwd);
+  prof_end(K_LIN_FOLD, st);
+  return e;
 }
 
 template <typename T>
 cudaError_t lin_forward(const LinP& P, const Dims& d, const void* q, const void* k, const void* v, const float* h0,
-                        void* o, float* hf, float* segf, cudaStream_t st) {
+                        void* o, float* hf, float* segf, float* S, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (!P.rows) {
     prof_begin(K_TABLE, st);
@@ -713,7 +1042,7 @@ cudaError_t lin_forward(const LinP& P, const Dims& d, const void* q, const void*
     prof_end(K_TABLE, st);
     e = cudaGetLastError();
   }
-  if (e == cudaSuccess && P.seg) e = run_seg<T>(P, d, k, v, segf, 0, P.save, P.rows ? 1 : 2, st);
+  if (e == cudaSuccess && P.seg) e = run_seg<T>(P, d, k, v, h0, segf, 0, P.rows ? 1 : 2, st);
   if (e != cudaSuccess) return e;
   LinOp op = {};
   op.x = q;
@@ -724,42 +1053,51 @@ cudaError_t lin_forward(const LinP& P, const Dims& d, const void* q, const void*
   op.fin = hf;
   op.DVt = d.dv;
   op.segc = P.seg ? segf : nullptr;
-  return dispatch<T, 0>(K_LIN_CHAIN, d.dk, P, op, P.rows && !P.seg ? 1 : 2, st);
+  op.states = P.save ? S : nullptr;
+  const int fwd = P.rows && !P.seg ? 1 : 2;
+  return sizeof(T) == 4 ? launch_f32(0, K_LIN_CHAIN, d.dk, P, op, fwd, st)
+                        : launch_bf16<false>(K_LIN_CHAIN, d.dk, P, op, fwd, st);
 }
 
-struct LinGrads {
-  const void *q, *k, *v, *dO;
-  const float *h0, *dhf;
-  void *dq, *dk, *dv;
-  float *dA, *dh0;
+struct LinBwdWs {
+  float *segf, *segr, *S, *R;
+  double *p1, *p2;
 };
 
 template <typename T>
-cudaError_t lin_backward(const LinP& P, const Dims& d, const LinGrads& g, float* segf, float* segr, double* p1,
-                         double* p2, int dtype, cudaStream_t st) {
+cudaError_t lin_backward(const LinP& P, const Dims& d, const LinGrads& g, const LinBwdWs& w, cudaStream_t st) {
+  constexpr bool F = sizeof(T) == 4;
   cudaError_t e = cudaSuccess;
-  if (P.seg) e = run_seg<T>(P, d, g.q, g.dO, segr, 1, 0, 0, st);
+  if (P.seg) e = run_seg<T>(P, d, g.q, g.dO, g.dhf, w.segr, 1, 0, st);
   if (e != cudaSuccess) return e;
   LinOp op = {};
-  op.x = g.dO; op.y = g.v; op.z = g.k; op.out = g.dq; op.init = g.h0; op.tr = 1; op.DVt = d.dk;
-  op.segc = P.seg ? segf : nullptr; op.wx = g.q; op.dfin = g.dhf; op.pda = p1;
-  e = g.dA ? dispatch<T, 1>(K_LIN_CHAIN, d.dv, P, op, 0, st) : dispatch<T, 0>(K_LIN_CHAIN, d.dv, P, op, 0, st);
-  if (e != cudaSuccess) return e;
-  op = LinOp{};
-  op.x = g.v; op.y = g.dO; op.z = g.q; op.out = g.dk; op.init = g.dhf; op.tr = 1; op.rev = 1; op.DVt = d.dk;
-  op.segc = P.seg ? segr : nullptr; op.wx = g.k; op.pda = p2;
-  e = g.dA ? dispatch<T, 2>(K_LIN_CHAIN, d.dv, P, op, 0, st) : dispatch<T, 0>(K_LIN_CHAIN, d.dv, P, op, 0, st);
-  if (e != cudaSuccess) return e;
-  op = LinOp{};
   op.x = g.k; op.y = g.q; op.z = g.dO; op.out = g.dv; op.init = g.dhf; op.fin = g.dh0; op.rev = 1; op.DVt = d.dv;
-  op.segc = P.seg ? segr : nullptr;
-  e = dispatch<T, 0>(K_LIN_CHAIN, d.dk, P, op, 0, st);
+  op.segc = P.seg ? w.segr : nullptr;
+  if (!F) op.states = w.R;
+  e = F ? launch_f32(0, K_LIN_CHAIN, d.dk, P, op, 0, st) : launch_bf16<false>(K_LIN_CHAIN, d.dk, P, op, 0, st);
+  if (e != cudaSuccess) return e;
+  const int ns = d.dk / value_slice(F ? KDA_F32 : KDA_BF16, d.dk);
+  if constexpr (!F) {
+    const DqkOp dop{g.dq, g.dk, w.S, w.R, w.p1};
+    e = g.dA ? dqk<true>(P, d, g, dop, st) : dqk<false>(P, d, g, dop, st);
+  } else {
+    op = LinOp{};
+    op.x = g.dO; op.y = g.v; op.z = g.k; op.out = g.dq; op.init = g.h0; op.tr = 1; op.DVt = d.dk;
+    op.segc = P.seg ? w.segf : nullptr; op.wx = g.q; op.pda = w.p1;
+    e = launch_f32(g.dA ? 1 : 0, K_LIN_CHAIN, d.dv, P, op, 0, st);
+    if (e != cudaSuccess) return e;
+    op = LinOp{};
+    op.x = g.v; op.y = g.dO; op.z = g.q; op.out = g.dk; op.init = g.dhf; op.tr = 1; op.rev = 1; op.DVt = d.dk;
+    op.segc = P.seg ? w.segr : nullptr; op.wx = g.k; op.ent = w.S; op.pda = w.p2;
+    e = launch_f32(g.dA ? 2 : 0, K_LIN_CHAIN, d.dv, P, op, 0, st);
+  }
   if (e != cudaSuccess || !g.dA) return e;
-  const int ns = d.dk / value_slice(dtype, d.dk);
+  const int64_t cnt = F ? P.nu : dqk_groups(P);
   prof_begin(K_LIN_DECAY, st);
-  lin_decay_kernel<<<d.H, 256, 0, st>>>(P, p1, ns, p2, ns, g.dA);
+  e = launch_pdl(lin_decay_kernel, dim3(d.H), dim3(256), 0, st, P, (const double*)w.p1, cnt, ns, (const double*)w.p2,
+                 F ? cnt : (int64_t)0, ns, g.dA);
   prof_end(K_LIN_DECAY, st);
-  return cudaGetLastError();
+  return e;
 }
 
 // ------------------------------------------------------------ single-token step
@@ -840,7 +1178,7 @@ extern "C" KDA_API size_t kda_linear_workspace_size(const kda_problem* p, int fo
   if (check_problem(p, &d) != KDA_OK) return 0;
   LinP P = {};
   lin_plan(p, d, P);
-  return lin_layout(d, P, for_backward ? 1 : 0).total;
+  return lin_layout(p, d, P, for_backward ? 1 : 0).total;
 }
 
 extern "C" KDA_API kda_status kda_linear_fwd(const kda_problem* p, const void* q, const void* k, const void* v,
@@ -858,9 +1196,9 @@ extern "C" KDA_API kda_status kda_linear_fwd(const kda_problem* p, const void* q
     if (!al(x, 16)) return KDA_ERR_ALIGNMENT;
   const kda_status s = lin_setup(p, save_for_backward ? 1 : 0, workspace, workspace_bytes, A_log, d, P, L);
   if (s != KDA_OK) return s;
-  float* segf = (float*)((char*)workspace + L.off_segf);
-  const cudaError_t e = p->dtype == KDA_F32 ? lin_forward<float>(P, d, q, k, v, h0, o, h_final, segf, stream)
-                                            : lin_forward<bf16>(P, d, q, k, v, h0, o, h_final, segf, stream);
+  float *segf = (float*)((char*)workspace + L.off_segf), *S = (float*)((char*)workspace + L.off_S);
+  const cudaError_t e = p->dtype == KDA_F32 ? lin_forward<float>(P, d, q, k, v, h0, o, h_final, segf, S, stream)
+                                            : lin_forward<bf16>(P, d, q, k, v, h0, o, h_final, segf, S, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -882,11 +1220,10 @@ extern "C" KDA_API kda_status kda_linear_bwd(const kda_problem* p, const void* q
   if (s != KDA_OK) return s;
   char* w = (char*)workspace;
   const LinGrads g{q, k, v, dO, h0, dh_final, dq, dk, dv, dA_log, dh0};
-  float *segf = (float*)(w + L.off_segf), *segr = (float*)(w + L.off_segr);
-  double *p1 = (double*)(w + L.off_p1), *p2 = (double*)(w + L.off_p2);
-  const cudaError_t e = p->dtype == KDA_F32
-                            ? lin_backward<float>(P, d, g, segf, segr, p1, p2, p->dtype, stream)
-                            : lin_backward<bf16>(P, d, g, segf, segr, p1, p2, p->dtype, stream);
+  const LinBwdWs bw{(float*)(w + L.off_segf), (float*)(w + L.off_segr), (float*)(w + L.off_S), (float*)(w + L.off_R),
+                    (double*)(w + L.off_p1), (double*)(w + L.off_p2)};
+  const cudaError_t e = p->dtype == KDA_F32 ? lin_backward<float>(P, d, g, bw, stream)
+                                            : lin_backward<bf16>(P, d, g, bw, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

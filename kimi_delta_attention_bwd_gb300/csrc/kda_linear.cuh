@@ -15,12 +15,16 @@ using bf16 = __nv_bfloat16;
 struct LinP {
   int Ntok, H, n_docs, T, rows;  // rows: documents are the rows of T tokens
   int nu, L, seg;                // units (an upper bound with cu_seqlens), segment length, any document split
+  int nc, n_long;                // upper bounds: chunks, split documents
   int save, tag;
   float scale;
   const int32_t* cu;
   const float* A_log;
-  int32_t *err, *wtag, *n_units;
+  int32_t *err, *wtag, *counts;  // counts: units, chunks, split documents (cu_seqlens)
   int4* units;                   // {document, first token, tokens, segment}
+  int32_t* unit_ch0;             // first chunk
+  int2* longs;                   // split documents: {first unit, segments}
+  int2* chunks;                  // {first token, tokens}, written by the saving forward's chains
 };
 
 // One application of the operator (see above).  z, out and the state's value
@@ -32,34 +36,35 @@ struct LinOp {
   const float* init;  // state at the chain's start (nullptr: 0)
   float* fin;         // state at its end (nullptr: not wanted)
   int tr, rev, DVt;
-  const float* segc;  // segments' own states [nu][H][2][key * DVt] (rev: [nu][H][key * DVt])
-  const void* wx;     // decay gradient: q (dq chain) or k (dk chain), laid out like z
-  const float* dfin;  // decay gradient: dh_final
-  double* pda;        // decay gradient: per CTA partial
+  float* segc;        // per unit [nu][H][key * DVt]: a segment's own state, then (lin_fold) its start state
+  float* states;      // per chunk [nc][H][dv][dk]: the state where the chain enters it (nullptr: not kept)
+  const void* wx;     // fp32 decay gradient: q (dq chain) or k (dk chain), laid out like z
+  const float* ent;   // fp32 decay gradient, dk chain: the forward's states
+  double* pda;        // fp32 decay gradient: per CTA partial
 };
 
 struct Unit {
-  int doc, tok0, ntok, seg, d0, dlen;  // document start and length
+  int doc, tok0, ntok, seg, nseg, ch0;
 };
 __device__ __forceinline__ bool unit_of(const LinP& P, int u, Unit& t) {
   if (P.rows) {
     const int ns = (P.T + P.L - 1) / P.L;
     t.doc = u / ns;
     t.seg = u % ns;
-    t.d0 = t.doc * P.T;
-    t.dlen = P.T;
-    t.tok0 = t.d0 + t.seg * P.L;
+    t.nseg = ns;
+    t.tok0 = t.doc * P.T + t.seg * P.L;
     t.ntok = min(P.L, P.T - t.seg * P.L);
+    t.ch0 = t.doc * ((P.T + C - 1) / C) + t.seg * (P.L / C);
     return true;
   }
-  if (u >= *P.n_units) return false;
+  if (u >= P.counts[0]) return false;
   const int4 v = P.units[u];
   t.doc = v.x;
   t.tok0 = v.y;
   t.ntok = v.z;
   t.seg = v.w;
-  t.d0 = t.tok0 - t.seg * P.L;
-  t.dlen = P.cu[t.doc + 1] - t.d0;
+  t.nseg = max(1, (P.cu[t.doc + 1] - t.tok0 + P.L - 1) / P.L + t.seg);
+  t.ch0 = P.unit_ch0[u];
   return true;
 }
 
@@ -110,33 +115,20 @@ __device__ __forceinline__ Rows rows_of(const Unit& un, int rev, int c) {
   return r;
 }
 
-// The state at a unit's start: the initial state and the earlier segments' own
-// states, decayed to here; R (decay gradient): each weighted by its age in
-// tokens.  each(fn) calls fn(s, r, at) for every state element a thread holds.
-template <bool WITH_R, class EACH>
-__device__ __forceinline__ void start_state(const LinP& P, const LinOp& op, const Unit& un, int u, int h, int nseg,
-                                            float a, int64_t stN, EACH each) {
-  const int age0 = op.rev ? un.dlen - un.seg * P.L - un.ntok : un.seg * P.L;
-  if (op.init) {
-    const float* p = op.init + ((int64_t)un.doc * P.H + h) * stN;
-    const float w = decay_pow(a, age0) * (op.rev ? 1.0f / P.scale : 1.0f);
-    each([&](float& s, float& r, int64_t at) {
-      s = w * p[at];
-      if (WITH_R) r = (float)age0 * s;
-    });
+// The state at a unit's start.  each(fn) calls fn(s, at) for every state
+// element a thread holds.
+template <class EACH>
+__device__ __forceinline__ void start_state(const LinP& P, const LinOp& op, const Unit& un, int u, int h, int64_t stN,
+                                            EACH each) {
+  const float *p = nullptr;
+  float w = 1.0f;
+  if (op.segc && un.seg != (op.rev ? un.nseg - 1 : 0)) {
+    p = op.segc + ((int64_t)u * P.H + h) * stN;
+  } else if (op.init) {
+    p = op.init + ((int64_t)un.doc * P.H + h) * stN;
+    if (op.rev) w = 1.0f / P.scale;
   }
-  if (!op.segc) return;
-  const int r1 = op.rev ? un.seg + 1 : 0, r2 = op.rev ? nseg : un.seg;
-  for (int g = r1; g < r2; g++) {
-    const int age = P.L * (op.rev ? g - un.seg - 1 : un.seg - 1 - g);
-    const float w = decay_pow(a, age);
-    const float* p = op.segc + ((int64_t)(u - un.seg + g) * P.H + h) * stN * (op.rev ? 1 : 2);
-    each([&](float& s, float& r, int64_t at) {
-      const float v = p[at];
-      s = fmaf(w, v, s);
-      if (WITH_R) r = fmaf(w, fmaf((float)age, v, p[stN + at]), r);
-    });
-  }
+  if (p) each([&](float& s, int64_t at) { s = w * p[at]; });
 }
 
 // The state after n tokens of decay, S' = e^{-an} S: as S + (e^{-an} - 1) S where

@@ -126,13 +126,12 @@ __device__ __forceinline__ void ld_tiles(uint32_t tbase, int c0, float (&v)[NT][
 template <int DK, int DEC>
 struct Shape {
   static constexpr bool ONLY = DEC >= 3;  // a segment's own state: no output rows
-  static constexpr bool HASR = DEC == 1 || DEC == 4;
   static constexpr int XE = ONLY ? 0 : NP * 64 * DK, YE = NP * 64 * DK, ZE = NP * 64 * DVS;
   static constexpr int SE = ONLY ? 0 : NP * DVS * DK, SCE = ZE, PE = ONLY ? 0 : NP * 64 * 64;
-  static constexpr int QE = DEC == 1 ? ZE : 0, RE = DEC == 1 ? NP * DVS * DK : 0;
+  static constexpr int QE = DEC == 1 ? ZE : 0;
   // 512 bytes after the tiles: an M = 64 view of a 32-column tile reads up to four cores past it
-  static constexpr int ELEMS = XE + YE + ZE + SE + SCE + PE + QE + RE + 256;
-  static constexpr int TMEM = DEC == 1 || 64 + DK > 128 ? 256 : 128;
+  static constexpr int ELEMS = XE + YE + ZE + SE + SCE + PE + QE + 256;
+  static constexpr int TMEM = DEC == 1 || 64 + DK > 128 ? 256 : 128;  // (DEC 1: 64 more for the pairs of q and k)
   static constexpr int SMEM = ELEMS * 2 + 1024 /* lut */ + 384 /* tab */ + 256 /* sw */ + 64;
   static constexpr int NTV = DVS / 16;  // 8-column tiles of a warp's half of the value side
   static constexpr int NTK = DK / 16;   // and of the key side
@@ -151,7 +150,6 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
   bf16* tSC = tS + SH::SE;
   bf16* tP = tSC + SH::SCE;
   bf16* tQ = tP + SH::PE;
-  bf16* tR = tQ + SH::QE;
   float2* lut = reinterpret_cast<float2*>(smem + SH::ELEMS * 2);  // [128] (w(m), w(m - 1)), m = index - 64
   float* tab = reinterpret_cast<float*>(lut + 128);               // [65] e^{-a m}
   float* sw = tab + 96;                                           // [64] state weights of the chunk's rows
@@ -162,9 +160,11 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
   const int q4 = warp & 3, half = warp >> 2, r0 = 16 * q4 + gq;
 
   Unit un;
-  if (!unit_of(P, u, un)) return;
-  const int nseg = P.seg ? max(1, (un.dlen + P.L - 1) / P.L) : 1;
-  if (ONLY && un.seg == (op.rev ? 0 : nseg - 1)) return;  // the last segment of its direction feeds nobody
+  if (!unit_of(P, u, un)) {
+    if ((DEC == 1 || DEC == 2) && tid == 0) op.pda[((int64_t)u * P.H + h) * (op.DVt / DVS) + slice] = 0.0;
+    return;
+  }
+  if (ONLY && un.seg == (op.rev ? 0 : un.nseg - 1)) return;  // the last segment of its direction feeds nobody
   const int H = P.H, DVt = op.DVt, c0 = slice * DVS;
   const int64_t stN = (int64_t)DK * DVt;
   const float a = decay_of(P.A_log, h);
@@ -185,18 +185,18 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
   const uint32_t tm = *slot;
 
   const bool st_rows = 16 * q4 < DVS;  // a warp whose state rows exist (warps 0, 1 of each half)
-  float S[NTK][4], R[SH::HASR ? NTK : 1][4];
+  float S[NTK][4];
   mma::zero<NTK>(S);
-  mma::zero<SH::HASR ? NTK : 1>(R);
-  auto each_st = [&](auto fn) {
+  auto each_at = [&](int tr, auto fn) {
 #pragma unroll
     for (int j = 0; j < NTK; j++)
 #pragma unroll
       for (int e = 0; e < 4; e++)
-        fn(S[j][e], R[SH::HASR ? j : 0][e],
-           st_at(op.tr, c0 + r0 + 8 * (e >> 1), half * (DK / 2) + 8 * j + 2 * tq + (e & 1), DK, DVt));
+        fn(S[j][e],
+           st_at(tr, c0 + r0 + 8 * (e >> 1), half * (DK / 2) + 8 * j + 2 * tq + (e & 1), DK, DVt));
   };
-  if (!ONLY && st_rows) start_state<DEC == 1>(P, op, un, u, h, nseg, a, stN, each_st);
+  auto each_st = [&](auto fn) { each_at(op.tr, fn); };
+  if (!ONLY && st_rows) start_state(P, op, un, u, h, stN, each_st);
   auto put_state = [&]() {
     if (st_rows) {
 #pragma unroll
@@ -205,7 +205,6 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
         for (int k = 0; k < 2; k++) {
           const int at = mma::opix(r0 + 8 * k, half * (DK / 2) + 8 * j + 2 * tq, DK);
           put2(S[j][2 * k], S[j][2 * k + 1], tS + at, DVS * DK);
-          if constexpr (DEC == 1) put2(R[j][2 * k], R[j][2 * k + 1], tR + at, DVS * DK);
         }
     }
   };
@@ -217,7 +216,19 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
   const int nch = (un.ntok + C - 1) / C;
   for (int c = 0; c < nch; c++) {
     const Rows rw = rows_of(un, op.rev, c);
-    const int n = rw.n;
+    const int n = rw.n, idx = op.rev ? nch - 1 - c : c;
+    if (!ONLY && st_rows) {
+      const int64_t at0 = ((int64_t)(un.ch0 + idx) * H + h) * stN;
+      if (op.states) {  // the saving forward: [dv][dk]
+        each_at(1, [&](float& s, int64_t at) { op.states[at0 + at] = s; });
+        if (h == 0 && slice == 0 && tid == 0) P.chunks[un.ch0 + idx] = make_int2((int)rw.t0, n);
+      }
+      if constexpr (DEC == 2) {  // D: n e^{-an} <the chunk's exit gradient, its entry state>
+        float part = 0.f;
+        each_at(0, [&](float& s, int64_t at) { part = fmaf(s, op.ent[at0 + at], part); });
+        dacc += (double)(part * P.scale * (float)n * tab[n]);
+      }
+    }
     if (tid < C) sw[tid] = tid < n ? tab[n - 1 - tid + (op.rev ? 1 : 0)] : 0.f;
     if constexpr (!ONLY) load_tile<DK>(tX, (const float*)op.x, rw, H, h, DK, 0);
     load_tile<DK>(tY, (const float*)op.y, rw, H, h, DK, 0);
@@ -250,10 +261,8 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
         tc::fence_after();
         gemm_parts(tm, kview(tX, DK), 64 * DK, kview(tY, DK), 64 * DK, 64, DK / 16);
         gemm_parts(tm + 64, kview(tX, DK), 64 * DK, kview(tS, DK), DVS * DK, DVS, DK / 16);
-        if constexpr (DEC == 1) {
+        if constexpr (DEC == 1)
           gemm_parts(tm + 128, kview(tQ, DVS), 64 * DVS, kview(tZ, DVS), 64 * DVS, 64, DVS / 16);
-          gemm_parts(tm + 192, kview(tX, DK), 64 * DK, kview(tR, DK), DVS * DK, DVS, DK / 16);
-        }
         tc::commit(bar);
       }
       __syncwarp();
@@ -287,17 +296,15 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
               part = fmaf((float)d * p[j][e], m2[j][e], part);
             }
         }
-        float qr[NTV][4];
-        ld_tiles<NTV>(tm + 192, half * (DVS / 2), qr);
 #pragma unroll
         for (int j = 0; j < NTV; j++)
 #pragma unroll
-          for (int e = 0; e < 4; e++) {  // B and D
+          for (int e = 0; e < 4; e++) {  // B
             const int row = r0 + 8 * (e >> 1), at = mma::opix(row, half * (DVS / 2) + 8 * j + 2 * tq + (e & 1), DVS);
             float qv = 0.f;
 #pragma unroll
             for (int b = 0; b < NP; b++) qv += __bfloat162float(tQ[b * 64 * DVS + at]);
-            part = fmaf(rs[e >> 1] * qv, fmaf((float)(row + 1), o[j][e], qr[j][e]), part);
+            part = fmaf(rs[e >> 1] * qv * (float)(row + 1), o[j][e], part);
           }
       }
 #pragma unroll
@@ -331,7 +338,6 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
       for (int j = 0; j < NTK; j++)
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          if constexpr (SH::HASR) R[j][e] = dec(fmaf((float)n, S[j][e], R[j][e]));
           S[j][e] = dec(S[j][e]) + d[j][e];
         }
     }
@@ -361,25 +367,16 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
   if (!good && tid == 0) *P.err = KDA_ERR_DEVICE;
 
   if (good && st_rows) {  // the unit's state
-    const bool last = un.seg == (op.rev ? 0 : nseg - 1);
+    const bool last = un.seg == (op.rev ? 0 : un.nseg - 1);
     float* pf = nullptr;
     float mul = 1.0f;
     if (ONLY) {
-      pf = const_cast<float*>(op.segc) + ((int64_t)u * H + h) * stN * (op.rev ? 1 : 2);
+      pf = op.segc + ((int64_t)u * H + h) * stN;
     } else if (last && op.fin) {
       pf = op.fin + ((int64_t)un.doc * H + h) * stN;
       mul = op.rev ? P.scale : 1.0f;
     }
-    const float* pd = DEC == 1 && last && op.dfin ? op.dfin + ((int64_t)un.doc * H + h) * stN : nullptr;
-    float part = 0.f;
-    each_st([&](float& s, float& r, int64_t at) {
-      if (pf) pf[at] = mul * s;
-      if constexpr (DEC == 4) pf[stN + at] = r;
-      if constexpr (DEC == 1) {
-        if (pd) part = fmaf(r, pd[at], part);
-      }
-    });
-    dacc += (double)part;
+    if (pf) each_st([&](float& s, int64_t at) { pf[at] = mul * s; });
   }
   __syncthreads();
   if constexpr (DEC == 1 || DEC == 2) {  // the CTA's partial, summed in a fixed order
@@ -433,8 +430,7 @@ cudaError_t launch_f32(int dec, int kid, int key, const LinP& P, const LinOp& op
     case 0: return by_key<0>(kid, key, P, op, fwd, st);
     case 1: return by_key<1>(kid, key, P, op, fwd, st);
     case 2: return by_key<2>(kid, key, P, op, fwd, st);
-    case 3: return by_key<3>(kid, key, P, op, fwd, st);
-    default: return by_key<4>(kid, key, P, op, fwd, st);
+    default: return by_key<3>(kid, key, P, op, fwd, st);
   }
 }
 
