@@ -171,12 +171,14 @@ struct Shape {
   static constexpr int NW = DVS / 16, NTH = 32 * NW;
   // bytes of the tiles of a stage (multiples of the swizzle's 1024)
   static constexpr int XB = ONLY ? 0 : 128 * DK, YB = 128 * DK, ZB = 128 * DVS;
-  static constexpr int STAGE = XB + YB + ZB, STG = 2;
-  static constexpr int PB = ONLY ? 0 : 2 * 64 * 64 * 2;
-  static constexpr int SMEM = 1024 /* alignment */ + STG * STAGE + PB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
+  static constexpr int STAGE = XB + YB + ZB;
+  static constexpr int STG = 2;
+  static constexpr int PB = ONLY ? 0 : 2 * 64 * 64 * 2, OB = ONLY ? 0 : 128 * DVS;
+  static constexpr int SMEM = 1024 /* alignment */ + STG * STAGE + PB + OB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
   static constexpr int NTK = DK / 8;  // 8-key tiles of a warp's state rows
+  static constexpr int NG = ONLY || NTK < 8 ? NTK : 8;  // and of a pass of the state's product
   // resident CTAs: what registers and shared memory allow
-  static constexpr int REGS = DK == 128 ? 255 : DK == 64 ? 168 : 128;
+  static constexpr int REGS = DK == 128 ? 255 : 168;
   static constexpr int BY_REG = 65536 / (NTH * REGS), BY_SMEM = 227 * 1024 / (SMEM + 1024);
   static constexpr int CTAS = BY_REG < BY_SMEM ? (BY_REG < 1 ? 1 : BY_REG) : BY_SMEM;
 };
@@ -277,7 +279,8 @@ __device__ __forceinline__ void store_rows(bf16* buf, const float (&o)[8][4], bf
 //          shared out over the warps, to shared memory as two parts
 //   o^T    = row weight * (S^T x^T) (S as register fragments) + z^T P^T
 //   S^T    = e^{-an} S^T + (weighted z)^T y
-// so that the state never leaves its registers and a chunk needs two barriers.
+// so that the state never leaves its registers and a chunk needs two barriers;
+// the state's product comes last, when the output's registers are free.
 // Tokens lie in memory order in both directions; in reverse the blocks are
 // walked from the other end (blk) and the weights run the other way.
 // mma.sync rather than tcgen05: the chain is bound by the instructions around
@@ -290,7 +293,8 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (mma::smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char* tP = smem + SH::STG * SH::STAGE;  // [2 parts][64][64]
-  float2* lut = reinterpret_cast<float2*>(tP + SH::PB);
+  unsigned char* tO = tP + SH::PB;                 // 2 KB a warp
+  float2* lut = reinterpret_cast<float2*>(tO + SH::OB);
   float* tab = reinterpret_cast<float*>(lut + 128);  // [65] e^{-a m}
   float* sw = tab + 96;                              // [64] weights of the chunk's rows in its state
   float* rwt = sw + 64;                              // [64] weights of the entry state in its rows
@@ -308,7 +312,7 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
   auto blk = [&](int t) { return rev ? 3 - t : t; };  // 16-token block t in the chain's direction
 
   auto load = [&](int c) {  // one thread
-    const int t0 = un.tok0 + C * (rev ? nch - 1 - c : c), s = c & 1;
+    const int t0 = un.tok0 + C * (rev ? nch - 1 - c : c), s = SH::STG == 2 ? c & 1 : 0;
     unsigned char* p = smem + s * SH::STAGE;
     mma::mbar_expect_tx(bar + s, SH::STAGE);
 #pragma unroll
@@ -350,7 +354,7 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
   bool good = true;
   for (int c = 0; c < nch; c++) {
     const int idx = rev ? nch - 1 - c : c, t0 = un.tok0 + C * idx, n = min(C, un.ntok - C * idx);
-    const int st = c & 1;
+    const int st = SH::STG == 2 ? c & 1 : 0;
     unsigned char* stg = smem + st * SH::STAGE;
     const uint32_t tX = mma::smem_u32(stg), tY = tX + SH::XB, tZ = tY + SH::YB;
     if (!ONLY && op.states) {  // the state where the chain enters the chunk, [dv][dk]
@@ -363,7 +367,7 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
           *reinterpret_cast<float2*>(p + 8 * k * DK + 8 * j) = make_float2(m * S[j][2 * k], m * S[j][2 * k + 1]);
       if (!rev && h == 0 && slice == 0 && tid == 0) P.chunks[un.ch0 + idx] = make_int2(t0, n);
     }
-    good = mma::mbar_wait(bar + st, (c >> 1) & 1);
+    good = mma::mbar_wait(bar + st, (SH::STG == 2 ? c >> 1 : c) & 1);
     if (n != n_w) {  // the first chunk, and the one that is not full
       if (n_w >= 0) __syncthreads();
       for (int i = tid; i < C; i += NTH) {
@@ -379,9 +383,8 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
       good = false;
       break;
     }
-    if (tid == 0 && c + 1 < nch) load(c + 1);
+    if (SH::STG == 2 && tid == 0 && c + 1 < nch) load(c + 1);
 
-    float o[8][4];
     if constexpr (!ONLY) {
       // ---- pairs: three blocks at a time, so that consecutive products are independent
       for (uint64_t todo = pair_blocks<NW>(warp); todo; todo >>= 24) {
@@ -430,7 +433,9 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
             }
         }
       }
+      __syncthreads();  // the pairs of every warp
       // ---- the entry state's rows: o^T = S^T x^T
+      float o[8][4];
       mma::zero<8>(o);
 #pragma unroll
       for (int kk = 0; kk < DK / 16; kk++) {
@@ -460,49 +465,11 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
         o[j][2] *= w.x;
         o[j][3] *= w.y;
       }
-    }
-    // ---- the state: S^T = e^{-an} S^T + (weighted z)^T y.  The product is summed apart from the
-    // state (the tensor core truncates what an addition shifts out: into a long chain's state that
-    // would be a bias), smallest parts first.
-    uint32_t zr[4][4];
-#pragma unroll
-    for (int kk = 0; kk < 4; kk++) ldsm_t(zr[kk], v2.at(tZ, 16 * blk(kk), 16 * warp));
-    const Decay dec(a, n);
-    {
-      float d[NTK][4];
-      mma::zero<NTK>(d);
-#pragma unroll
-      for (int kk = 0; kk < 4; kk++) {
-        uint32_t fb[NTK / 2][4];
-#pragma unroll
-        for (int p = 0; p < NTK / 2; p++) ldsm_t(fb[p], k1.at(tY, 16 * blk(kk), 16 * p));
-        uint32_t za[3][4];
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const float2 w = *reinterpret_cast<const float2*>(sw + 16 * blk(kk) + 8 * (q >> 1) + 2 * tq);
-          uint32_t s[3];
-          split2<3>(w.x * even(zr[kk][q]), w.y * odd(zr[kk][q]), s);
-#pragma unroll
-          for (int b = 0; b < 3; b++) za[b][q] = s[b];
-        }
-#pragma unroll
-        for (int b = 2; b >= 0; b--)
-#pragma unroll
-          for (int p = 0; p < NTK / 2; p++) {
-            mma::mma_bf16(d[2 * p], za[b], fb[p][0], fb[p][1]);
-            mma::mma_bf16(d[2 * p + 1], za[b], fb[p][2], fb[p][3]);
-          }
-      }
-#pragma unroll
-      for (int j = 0; j < NTK; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) S[j][e] = dec(S[j][e]) + d[j][e];
-    }
-    if constexpr (!ONLY) {
-      __syncthreads();  // the pairs of every warp; x and y have been read
       // ---- o^T += z^T P^T
 #pragma unroll
-      for (int kk = 0; kk < 4; kk++)
+      for (int kk = 0; kk < 4; kk++) {
+        uint32_t zr[4];
+        ldsm_t(zr, v2.at(tZ, 16 * blk(kk), 16 * warp));
 #pragma unroll
         for (int b = 1; b >= 0; b--) {
           uint32_t fb[4][4];
@@ -510,13 +477,60 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
           for (int p = kk; p < 4; p++) ldsm(fb[p], p2.at(mma::smem_u32(tP) + 8192 * b, 16 * blk(p), 16 * blk(kk)));
 #pragma unroll
           for (int p = kk; p < 4; p++) {
-            mma::mma_bf16(o[2 * p], zr[kk], fb[p][0], fb[p][1]);
-            mma::mma_bf16(o[2 * p + 1], zr[kk], fb[p][2], fb[p][3]);
+            mma::mma_bf16(o[2 * p], zr, fb[p][0], fb[p][1]);
+            mma::mma_bf16(o[2 * p + 1], zr, fb[p][2], fb[p][3]);
           }
         }
-      // ---- out, through the warp's 2 KB of the x and y tiles
-      store_rows(reinterpret_cast<bf16*>(stg) + warp * 1024, o, (bf16*)op.out + ((int64_t)t0 * H + h) * DVt + c0 + 16 * warp,
+      }
+      // ---- out
+      store_rows(reinterpret_cast<bf16*>(tO) + warp * 1024, o, (bf16*)op.out + ((int64_t)t0 * H + h) * DVt + c0 + 16 * warp,
                  (int64_t)H * DVt, n, rev);
+    }
+    // ---- the state: S^T = e^{-an} S^T + (weighted z)^T y.  The product is summed apart from the
+    // state (the tensor core truncates what an addition shifts out: into a long chain's state that
+    // would be a bias), smallest parts first.
+    uint32_t za[4][3][4];
+#pragma unroll
+    for (int kk = 0; kk < 4; kk++) {
+      uint32_t zr[4];
+      ldsm_t(zr, v2.at(tZ, 16 * blk(kk), 16 * warp));
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const float2 w = *reinterpret_cast<const float2*>(sw + 16 * blk(kk) + 8 * (q >> 1) + 2 * tq);
+        uint32_t s[3];
+        split2<3>(w.x * even(zr[q]), w.y * odd(zr[q]), s);
+#pragma unroll
+        for (int b = 0; b < 3; b++) za[kk][b][q] = s[b];
+      }
+    }
+    const Decay dec(a, n);
+#pragma unroll
+    for (int g = 0; g < NTK / SH::NG; g++) {
+      constexpr int NG = SH::NG;
+      float d[NG][4];
+      mma::zero<NG>(d);
+#pragma unroll
+      for (int kk = 0; kk < 4; kk++) {
+        uint32_t fb[NG / 2][4];
+#pragma unroll
+        for (int p = 0; p < NG / 2; p++) ldsm_t(fb[p], k1.at(tY, 16 * blk(kk), 8 * NG * g + 16 * p));
+#pragma unroll
+        for (int b = 2; b >= 0; b--)
+#pragma unroll
+          for (int p = 0; p < NG / 2; p++) {
+            mma::mma_bf16(d[2 * p], za[kk][b], fb[p][0], fb[p][1]);
+            mma::mma_bf16(d[2 * p + 1], za[kk][b], fb[p][2], fb[p][3]);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < NG; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) S[NG * g + j][e] = dec(S[NG * g + j][e]) + d[j][e];
+    }
+    if (SH::STG == 1 && c + 1 < nch) {
+      mma::fence_async_smem();
+      __syncthreads();
+      if (tid == 0) load(c + 1);
     }
   }
   if (!good) {  // a wait ran out
