@@ -71,7 +71,7 @@ __device__ __forceinline__ int block_scan(int x, int* s_w, int* total) {
 }
 
 // The unit table of packed documents: a document of n tokens has max(1,
-// ceil(n / L)) units and ceil(n / C) chunks.  One CTA; also validates the
+// ceil(n / L)) units, of equal length but for the last, and ceil(n / C) chunks.  One CTA; also validates the
 // offsets.
 __global__ void __launch_bounds__(1024) lin_table_kernel(LinP P) {
   __shared__ int s_bad, s_long, s_w[32];
@@ -97,15 +97,16 @@ __global__ void __launch_bounds__(1024) lin_table_kernel(LinP P) {
   for (int base = 0; base < n; base += 1024) {
     const int i = base + tid;
     const int t0 = i < n ? P.cu[i] : 0, len = i < n ? P.cu[i + 1] - t0 : 0;
-    const int ns = i < n ? max(1, (len + P.L - 1) / P.L) : 0, nc = (len + C - 1) / C;
+    const int L = seg_tokens(P.L, len);
+    const int ns = i < n ? max(1, (len + L - 1) / L) : 0, nc = (len + C - 1) / C;
     int all;
     const int u0 = units + block_scan(ns, s_w, &all) - ns;
     units += all;
     const int c0 = chunks + block_scan(nc, s_w, &all) - nc;
     chunks += all;
     for (int s = 0; s < ns; s++) {
-      P.units[u0 + s] = make_int4(i, t0 + s * P.L, min(P.L, len - s * P.L), s);
-      P.unit_ch0[u0 + s] = c0 + s * (P.L / C);
+      P.units[u0 + s] = make_int4(i, t0 + s * L, min(L, len - s * L), s);
+      P.unit_at[u0 + s] = make_int2(c0 + s * (L / C), ns);
     }
     if (ns > 1) P.longs[atomicAdd(&s_long, 1)] = make_int2(u0, ns);  // (in any order: they are independent)
   }
@@ -121,42 +122,56 @@ __global__ void __launch_bounds__(1024) lin_table_kernel(LinP P) {
 
 // Turns the segments' own states into their start states, in the chain's
 // direction: start_0 = init, start_{s+1} = e^{-a len_s} start_s + own_s.  A
-// thread per element of a (split document, head)'s state; four segments' loads
-// in flight.
+// thread per four elements of a (split document, head)'s state; four segments'
+// loads in flight.
 __global__ void __launch_bounds__(256) lin_fold_kernel(LinP P, float* segc, const float* init, int rev, int N, int fwd) {
   pdl_wait();
   pdl_release();
   if (!ready(P, fwd)) return;
-  const int d = blockIdx.x / P.H, h = blockIdx.x % P.H, at = blockIdx.y * 256 + threadIdx.x;
-  int u0, ns, doc, last;
+  const int d = blockIdx.x / P.H, h = blockIdx.x % P.H, at = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (at >= N) return;
+  int u0, ns, doc, len, last;
   if (P.rows) {
     ns = (P.T + P.L - 1) / P.L;
     u0 = d * ns;
     doc = d;
+    len = P.L;
     last = P.T - (ns - 1) * P.L;
   } else {
     if (d >= P.counts[2]) return;
     u0 = P.longs[d].x;
     ns = P.longs[d].y;
     doc = P.units[u0].x;
+    len = P.units[u0].z;
     last = P.units[u0 + ns - 1].z;
   }
-  const float a = decay_of(P.A_log, h), full = decay_pow(a, P.L);
-  float st = init ? init[((int64_t)doc * P.H + h) * N + at] * (rev ? 1.0f / P.scale : 1.0f) : 0.f;
-  auto own = [&](int k) -> float* {  // k-th segment in the chain's direction
-    return segc + ((int64_t)(u0 + (rev ? ns - 1 - k : k)) * P.H + h) * N + at;
+  const float a = decay_of(P.A_log, h), full = decay_pow(a, len), first = rev ? decay_pow(a, last) : full;
+  float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (init) {
+    st = *reinterpret_cast<const float4*>(init + ((int64_t)doc * P.H + h) * N + at);
+    const float m = rev ? 1.0f / P.scale : 1.0f;
+    st.x *= m; st.y *= m; st.z *= m; st.w *= m;
+  }
+  auto own = [&](int k) -> float4* {  // k-th segment in the chain's direction
+    return reinterpret_cast<float4*>(segc + ((int64_t)(u0 + (rev ? ns - 1 - k : k)) * P.H + h) * N + at);
   };
-  float v[4], nx[4];
+  float4 v[4], nx[4];
 #pragma unroll
-  for (int e = 0; e < 4; e++) v[e] = e < ns - 1 ? *own(e) : 0.f;
+  for (int e = 0; e < 4; e++)
+    if (e < ns - 1) v[e] = *own(e);
   for (int k = 0; k < ns - 1; k += 4) {
     // (start k + 4 goes where own state k + 4 was: the next four are read first)
 #pragma unroll
-    for (int e = 0; e < 4; e++) nx[e] = k + 4 + e < ns - 1 ? *own(k + 4 + e) : 0.f;
+    for (int e = 0; e < 4; e++)
+      if (k + 4 + e < ns - 1) nx[e] = *own(k + 4 + e);
 #pragma unroll
     for (int e = 0; e < 4; e++)
       if (k + e < ns - 1) {
-        st = fmaf(rev && k + e == 0 ? decay_pow(a, last) : full, st, v[e]);
+        const float g = k + e == 0 ? first : full;
+        st.x = fmaf(g, st.x, v[e].x);
+        st.y = fmaf(g, st.y, v[e].y);
+        st.z = fmaf(g, st.z, v[e].z);
+        st.w = fmaf(g, st.w, v[e].w);
         *own(k + e + 1) = st;
       }
 #pragma unroll
@@ -644,6 +659,16 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
   for (int i = tid; i < C; i += NTH) rq[i] = P.scale * tab[i + 1];
   int n_w = -1;  // rows for which rk is set
 
+  // this warp's 64 bytes of every dv row of a chunk's S and R, on their way to L2 a chunk ahead
+  auto prefetch = [&](int c) {
+    const int64_t at = ((int64_t)(g0 + c) * H + h) * DV * DKt + c0 + 16 * warp;
+    for (int r = lane; r < DV; r += 32) {
+      mma::prefetch_l2(op.S + at + (int64_t)r * DKt);
+      mma::prefetch_l2(op.R + at + (int64_t)r * DKt);
+    }
+  };
+  prefetch(0);
+
   const Frag<DV, 1> o1;   // dO and v tiles
   const Frag<DV, 2> o2;
   const Frag<DVS, 1> v1;  // q and k tiles
@@ -671,6 +696,7 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
       break;
     }
     if (SH::STG == 2 && tid == 0 && c + 1 < nch) load(c + 1);
+    if (c + 1 < nch) prefetch(c + 1);
 
     float part = 0.f;
     // ---- pairs, three blocks at a time
@@ -932,17 +958,17 @@ struct LinLayout {
   size_t off_counts, off_units, off_ch0, off_longs, off_chunks, off_segf, off_segr, off_S, off_R, off_p1, off_p2, total;
 };
 
-// Segment length: long documents are cut so that about two chain CTAs per SM
-// exist, in whole chunks and at least SEG_TOK tokens.
+// Segment length: long documents are cut into equal pieces of at most L tokens
+// (whole chunks, at least SEG_TOK tokens), L chosen so that about eight chain
+// CTAs per SM exist: two or three run at once, and uneven documents then even
+// out.  Whole rows of 2048 tokens (300M) take 77 us, two CTAs per SM 51, eight
+// 45; more pieces cost more in the fold than they give.
 void lin_plan(const kda_problem* p, const Dims& d, LinP& P) {
   const int64_t per = (int64_t)d.H * (d.dv / value_slice(p->dtype, d.dv));
-  int64_t L = ((int64_t)d.Ntok * per + 2 * LIN_SMS - 1) / (2 * LIN_SMS);
+  int64_t L = ((int64_t)d.Ntok * per + 8 * LIN_SMS - 1) / (8 * LIN_SMS);
   if (L < SEG_TOK) L = SEG_TOK;
-  if (d.rows) {  // equal segments of a row
-    const int64_t ns = (d.T + L - 1) / L;
-    L = (d.T + ns - 1) / ns;
-  }
   L = (L + C - 1) / C * C;
+  if (d.rows) L = seg_tokens((int)L, d.T);
   P.Ntok = d.Ntok;
   P.H = d.H;
   P.n_docs = d.n_docs;
@@ -976,7 +1002,7 @@ LinLayout lin_layout(const kda_problem* p, const Dims& d, const LinP& P, int for
   if (!P.rows) {
     L.off_counts = take(12);
     L.off_units = take(16 * (size_t)P.nu);
-    L.off_ch0 = take(4 * (size_t)P.nu);
+    L.off_ch0 = take(8 * (size_t)P.nu);
     L.off_longs = take(8 * (size_t)(P.n_long + 1));
   }
   // sized as if every long document were cut: whether any is may be known on the device alone
@@ -1016,7 +1042,7 @@ kda_status lin_setup(const kda_problem* p, int for_bwd, void* ws, size_t bytes, 
   P.wtag = (int32_t*)(w + 4);
   P.counts = (int32_t*)(w + L.off_counts);
   P.units = (int4*)(w + L.off_units);
-  P.unit_ch0 = (int32_t*)(w + L.off_ch0);
+  P.unit_at = (int2*)(w + L.off_ch0);
   P.longs = (int2*)(w + L.off_longs);
   P.chunks = (int2*)(w + L.off_chunks);
   P.A_log = A_log;
@@ -1040,7 +1066,7 @@ cudaError_t run_seg(const LinP& P, const Dims& d, const void* y, const void* z, 
   if (e != cudaSuccess) return e;
   const int N = d.dk * d.dv;
   prof_begin(K_LIN_FOLD, st);
-  e = launch_pdl(lin_fold_kernel, dim3((unsigned)P.n_long * d.H, N / 256), dim3(256), 0, st, P, segc, init, rev, N,
+  e = launch_pdl(lin_fold_kernel, dim3((unsigned)P.n_long * d.H, (N + 1023) / 1024), dim3(256), 0, st, P, segc, init, rev, N,
                  fwd == 1 ? 2 : fwd);
   prof_end(K_LIN_FOLD, st);
   return e;

@@ -22,7 +22,7 @@ struct LinP {
   const float* A_log;
   int32_t *err, *wtag, *counts;  // counts: units, chunks, split documents (cu_seqlens)
   int4* units;                   // {document, first token, tokens, segment}
-  int32_t* unit_ch0;             // first chunk
+  int2* unit_at;                 // {first chunk, segments of the document}
   int2* longs;                   // split documents: {first unit, segments}
   int2* chunks;                  // {first token, tokens}, written by the saving forward's chains
 };
@@ -42,6 +42,13 @@ struct LinOp {
   const float* ent;   // fp32 decay gradient, dk chain: the forward's states
   double* pda;        // fp32 decay gradient: per CTA partial
 };
+
+// Tokens of the equal pieces (whole chunks) of a document of len tokens, at most
+// L (a multiple of C).
+__host__ __device__ inline int seg_tokens(int L, int len) {
+  const int ns = (len + L - 1) / L;
+  return ns <= 1 ? L : ((len + ns - 1) / ns + C - 1) / C * C;
+}
 
 struct Unit {
   int doc, tok0, ntok, seg, nseg, ch0;
@@ -63,8 +70,9 @@ __device__ __forceinline__ bool unit_of(const LinP& P, int u, Unit& t) {
   t.tok0 = v.y;
   t.ntok = v.z;
   t.seg = v.w;
-  t.nseg = max(1, (P.cu[t.doc + 1] - t.tok0 + P.L - 1) / P.L + t.seg);
-  t.ch0 = P.unit_ch0[u];
+  const int2 at = P.unit_at[u];
+  t.ch0 = at.x;
+  t.nseg = at.y;
   return true;
 }
 
