@@ -659,16 +659,6 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
   for (int i = tid; i < C; i += NTH) rq[i] = P.scale * tab[i + 1];
   int n_w = -1;  // rows for which rk is set
 
-  // this warp's 64 bytes of every dv row of a chunk's S and R, on their way to L2 a chunk ahead
-  auto prefetch = [&](int c) {
-    const int64_t at = ((int64_t)(g0 + c) * H + h) * DV * DKt + c0 + 16 * warp;
-    for (int r = lane; r < DV; r += 32) {
-      mma::prefetch_l2(op.S + at + (int64_t)r * DKt);
-      mma::prefetch_l2(op.R + at + (int64_t)r * DKt);
-    }
-  };
-  prefetch(0);
-
   const Frag<DV, 1> o1;   // dO and v tiles
   const Frag<DV, 2> o2;
   const Frag<DVS, 1> v1;  // q and k tiles
@@ -696,7 +686,6 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
       break;
     }
     if (SH::STG == 2 && tid == 0 && c + 1 < nch) load(c + 1);
-    if (c + 1 < nch) prefetch(c + 1);
 
     float part = 0.f;
     // ---- pairs, three blocks at a time
