@@ -183,17 +183,19 @@ __global__ void __launch_bounds__(256) lin_fold_kernel(LinP P, float* segc, cons
 // ONLY: state only (a segment's own state), no output rows.
 template <int DK, int DVS, bool ONLY>
 struct Shape {
-  static constexpr int NW = DVS / 16, NTH = 32 * NW;
+  // 16-row tiles of the state per warp: two where the registers hold them, so that every operand
+  // fragment read from shared memory serves two products
+  static constexpr int MT = DK == 128 ? 1 : 2;
+  static constexpr int NW = DVS / (16 * MT), NTH = 32 * NW;
   // bytes of the tiles of a stage (multiples of the swizzle's 1024)
   static constexpr int XB = ONLY ? 0 : 128 * DK, YB = 128 * DK, ZB = 128 * DVS;
   static constexpr int STAGE = XB + YB + ZB;
-  static constexpr int STG = 2;
+  static constexpr int STG = DK == 128 || ONLY ? 2 : 1;
   static constexpr int PB = ONLY ? 0 : 2 * 64 * 64 * 2, OB = ONLY ? 0 : 128 * DVS;
   static constexpr int SMEM = 1024 /* alignment */ + STG * STAGE + PB + OB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
   static constexpr int NTK = DK / 8;  // 8-key tiles of a warp's state rows
-  static constexpr int NG = ONLY || NTK < 8 ? NTK : 8;  // and of a pass of the state's product
   // resident CTAs: what registers and shared memory allow
-  static constexpr int REGS = DK == 128 ? 255 : 168;
+  static constexpr int REGS = DK == 32 ? 200 : 255;
   static constexpr int BY_REG = 65536 / (NTH * REGS), BY_SMEM = 227 * 1024 / (SMEM + 1024);
   static constexpr int CTAS = BY_REG < BY_SMEM ? (BY_REG < 1 ? 1 : BY_REG) : BY_SMEM;
 };
@@ -253,8 +255,15 @@ __device__ __forceinline__ uint64_t pair_blocks(int warp) {
 
 // The tensors of a chain as [Ntok][H d] maps with boxes of 64 tokens.
 struct LinMaps {
-  CUtensorMap x, y, z;
+  CUtensorMap x, y, z, o;
 };
+
+// A 64-token x box tile of shared memory (in the map's swizzle) to a tensor.
+__device__ __forceinline__ void tma_store_2d(const void* map, int x0, int y0, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(x0),
+               "r"(y0), "r"(mma::smem_u32(src))
+               : "memory");
+}
 
 // Rows n .. of a stage's tiles hold other documents' tokens: zero them, so that
 // nothing of them (an infinity) enters a product.  The first A bytes are rows of
@@ -287,8 +296,8 @@ __device__ __forceinline__ void store_rows(bf16* buf, const float (&o)[8][4], bf
   }
 }
 
-// One CTA carries one chain of a DVS-column value slice.  Warp w holds the
-// state's value rows 16 w .. of S^T as fp32 accumulator fragments for the whole
+// One CTA carries one chain of a DVS-column value slice.  Warp w holds MT x 16
+// value rows of S^T as fp32 accumulator fragments for the whole
 // chain; per chunk
 //   pairs  P = w (x y^T), the ten 16 x 16 blocks on and below the diagonal
 //          shared out over the warps, to shared memory as two parts
@@ -304,11 +313,11 @@ __device__ __forceinline__ void store_rows(bf16* buf, const float (&o)[8][4], bf
 template <int DK, int DVS, bool ONLY>
 __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u, int h, int slice) {
   using SH = Shape<DK, DVS, ONLY>;
-  constexpr int NTH = SH::NTH, NW = SH::NW, NTK = SH::NTK;
+  constexpr int NTH = SH::NTH, NW = SH::NW, NTK = SH::NTK, MT = SH::MT;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (mma::smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char* tP = smem + SH::STG * SH::STAGE;  // [2 parts][64][64]
-  unsigned char* tO = tP + SH::PB;                 // 2 KB a warp
+  unsigned char* tO = tP + SH::PB;                 // [64][DVS], the output's rows
   float2* lut = reinterpret_cast<float2*>(tO + SH::OB);
   float* tab = reinterpret_cast<float*>(lut + 128);  // [65] e^{-a m}
   float* sw = tab + 96;                              // [64] weights of the chunk's rows in its state
@@ -350,14 +359,18 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
   }
   int n_w = -1;  // rows for which sw and rwt are set
 
-  float S[NTK][4];
-  mma::zero<NTK>(S);
+  float S[MT][NTK][4];
+#pragma unroll
+  for (int m = 0; m < MT; m++) mma::zero<NTK>(S[m]);
+  const int r0 = 16 * MT * warp;  // this warp's first value row
   auto each_at = [&](int tr, auto fn) {
 #pragma unroll
-    for (int j = 0; j < NTK; j++)
+    for (int m = 0; m < MT; m++)
 #pragma unroll
-      for (int e = 0; e < 4; e++)
-        fn(S[j][e], st_at(tr, c0 + 16 * warp + gq + 8 * (e >> 1), 8 * j + 2 * tq + (e & 1), DK, DVt));
+      for (int j = 0; j < NTK; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          fn(S[m][j][e], st_at(tr, c0 + r0 + 16 * m + gq + 8 * (e >> 1), 8 * j + 2 * tq + (e & 1), DK, DVt));
   };
   if (!ONLY) start_state(P, op, un, u, h, stN, [&](auto fn) { each_at(0, fn); });
 
@@ -367,19 +380,23 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
   const Frag<64, 2> p2;   // pairs
 
   bool good = true;
+  int out_t0 = -1;  // first token of the output tile that waits in tO
   for (int c = 0; c < nch; c++) {
     const int idx = rev ? nch - 1 - c : c, t0 = un.tok0 + C * idx, n = min(C, un.ntok - C * idx);
     const int st = SH::STG == 2 ? c & 1 : 0;
     unsigned char* stg = smem + st * SH::STAGE;
     const uint32_t tX = mma::smem_u32(stg), tY = tX + SH::XB, tZ = tY + SH::YB;
     if (!ONLY && op.states) {  // the state where the chain enters the chunk, [dv][dk]
-      float* p = op.states + ((int64_t)(un.ch0 + idx) * H + h) * stN + (int64_t)(c0 + 16 * warp + gq) * DK + 2 * tq;
-      const float m = rev ? P.scale : 1.0f;
+      float* p = op.states + ((int64_t)(un.ch0 + idx) * H + h) * stN + (int64_t)(c0 + r0 + gq) * DK + 2 * tq;
+      const float w = rev ? P.scale : 1.0f;
 #pragma unroll
-      for (int j = 0; j < NTK; j++)
+      for (int m = 0; m < MT; m++)
 #pragma unroll
-        for (int k = 0; k < 2; k++)
-          *reinterpret_cast<float2*>(p + 8 * k * DK + 8 * j) = make_float2(m * S[j][2 * k], m * S[j][2 * k + 1]);
+        for (int j = 0; j < NTK; j++)
+#pragma unroll
+          for (int k = 0; k < 2; k++)
+            *reinterpret_cast<float2*>(p + (16 * m + 8 * k) * DK + 8 * j) =
+                make_float2(w * S[m][j][2 * k], w * S[m][j][2 * k + 1]);
       if (!rev && h == 0 && slice == 0 && tid == 0) P.chunks[un.ch0 + idx] = make_int2(t0, n);
     }
     good = mma::mbar_wait(bar + st, (SH::STG == 2 ? c >> 1 : c) & 1);
@@ -401,6 +418,10 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
     if (SH::STG == 2 && tid == 0 && c + 1 < nch) load(c + 1);
 
     if constexpr (!ONLY) {
+      if (tid == 0 && out_t0 >= 0) {
+        tma_store_2d(&maps.o, h * DVt + c0, out_t0, tO);
+        mma::bulk_commit();
+      }
       // ---- pairs: three blocks at a time, so that consecutive products are independent
       for (uint64_t todo = pair_blocks<NW>(warp); todo; todo >>= 24) {
         int rr[3], cc[3];
@@ -448,104 +469,146 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
             }
         }
       }
-      __syncthreads();  // the pairs of every warp
+      if (tid == 0) mma::bulk_wait_read();  // tO is free again
+      __syncthreads();                      // the pairs of every warp
       // ---- the entry state's rows: o^T = S^T x^T
-      float o[8][4];
-      mma::zero<8>(o);
+      float o[MT][8][4];
+#pragma unroll
+      for (int m = 0; m < MT; m++) mma::zero<8>(o[m]);
 #pragma unroll
       for (int kk = 0; kk < DK / 16; kk++) {
-        uint32_t f[2][4], fb[4][4];
+        uint32_t f[MT][2][4], fb[4][4];
 #pragma unroll
         for (int p = 0; p < 4; p++) ldsm(fb[p], k2.at(tX, 16 * blk(p), 16 * kk));
 #pragma unroll
-        for (int q = 0; q < 4; q++) {  // accumulator tiles 2 kk, 2 kk + 1 are the 16 x 16 operand
-          uint32_t s[2];
-          split2<2>(S[2 * kk + (q >> 1)][2 * (q & 1)], S[2 * kk + (q >> 1)][2 * (q & 1) + 1], s);
-          f[0][q] = s[0];
-          f[1][q] = s[1];
-        }
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+          for (int q = 0; q < 4; q++) {  // accumulator tiles 2 kk, 2 kk + 1 are the 16 x 16 operand
+            const float* st2 = &S[m][2 * kk + (q >> 1)][2 * (q & 1)];
+            uint32_t s[2];
+            split2<2>(st2[0], st2[1], s);
+            f[m][0][q] = s[0];
+            f[m][1][q] = s[1];
+          }
 #pragma unroll
         for (int b = 1; b >= 0; b--)
 #pragma unroll
-          for (int p = 0; p < 4; p++) {
-            mma::mma_bf16(o[2 * p], f[b], fb[p][0], fb[p][1]);
-            mma::mma_bf16(o[2 * p + 1], f[b], fb[p][2], fb[p][3]);
-          }
+          for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+              mma::mma_bf16(o[m][2 * p], f[m][b], fb[p][0], fb[p][1]);
+              mma::mma_bf16(o[m][2 * p + 1], f[m][b], fb[p][2], fb[p][3]);
+            }
       }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         const float2 w = *reinterpret_cast<const float2*>(rwt + 16 * blk(j >> 1) + 8 * (j & 1) + 2 * tq);
-        o[j][0] *= w.x;
-        o[j][1] *= w.y;
-        o[j][2] *= w.x;
-        o[j][3] *= w.y;
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+          o[m][j][0] *= w.x;
+          o[m][j][1] *= w.y;
+          o[m][j][2] *= w.x;
+          o[m][j][3] *= w.y;
+        }
       }
       // ---- o^T += z^T P^T
 #pragma unroll
       for (int kk = 0; kk < 4; kk++) {
-        uint32_t zr[4];
-        ldsm_t(zr, v2.at(tZ, 16 * blk(kk), 16 * warp));
+        uint32_t zr[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; m++) ldsm_t(zr[m], v2.at(tZ, 16 * blk(kk), r0 + 16 * m));
 #pragma unroll
         for (int b = 1; b >= 0; b--) {
           uint32_t fb[4][4];
 #pragma unroll
           for (int p = kk; p < 4; p++) ldsm(fb[p], p2.at(mma::smem_u32(tP) + 8192 * b, 16 * blk(p), 16 * blk(kk)));
 #pragma unroll
-          for (int p = kk; p < 4; p++) {
-            mma::mma_bf16(o[2 * p], zr, fb[p][0], fb[p][1]);
-            mma::mma_bf16(o[2 * p + 1], zr, fb[p][2], fb[p][3]);
-          }
+          for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int p = kk; p < 4; p++) {
+              mma::mma_bf16(o[m][2 * p], zr[m], fb[p][0], fb[p][1]);
+              mma::mma_bf16(o[m][2 * p + 1], zr[m], fb[p][2], fb[p][3]);
+            }
         }
       }
-      // ---- out
-      store_rows(reinterpret_cast<bf16*>(tO) + warp * 1024, o, (bf16*)op.out + ((int64_t)t0 * H + h) * DVt + c0 + 16 * warp,
-                 (int64_t)H * DVt, n, rev);
+      // ---- out: transposed into tO, and from there as a tile (a chunk that is not full: row by row)
+#pragma unroll
+      for (int m = 0; m < MT; m++)
+#pragma unroll
+        for (int p = 0; p < 4; p++) {  // four 8 x 8 tiles: 16 tokens by 16 columns
+          const int row = 16 * blk(p) + 8 * (lane >> 4) + (lane & 7), cg = (r0 + 16 * m) / 8 + ((lane >> 3) & 1);
+          stsm4t(tO + row * 128 + ((cg ^ (row & 7)) << 4), pack2(o[m][2 * p][0], o[m][2 * p][1]),
+                 pack2(o[m][2 * p][2], o[m][2 * p][3]), pack2(o[m][2 * p + 1][0], o[m][2 * p + 1][1]),
+                 pack2(o[m][2 * p + 1][2], o[m][2 * p + 1][3]));
+        }
+      out_t0 = n == C ? t0 : -1;
+      if (n < C) {
+        __syncwarp();
+        for (int g = lane; g < n * 2 * MT; g += 32) {
+          const int row = g / (2 * MT), cg = r0 / 8 + g % (2 * MT);
+          *reinterpret_cast<uint4*>((bf16*)op.out + ((int64_t)(t0 + row) * H + h) * DVt + c0 + 8 * cg) =
+              *reinterpret_cast<const uint4*>(tO + row * 128 + ((cg ^ (row & 7)) << 4));
+        }
+      }
     }
     // ---- the state: S^T = e^{-an} S^T + (weighted z)^T y.  The product is summed apart from the
     // state (the tensor core truncates what an addition shifts out: into a long chain's state that
     // would be a bias), smallest parts first.
-    uint32_t za[4][3][4];
+    float d[MT][NTK][4];
+#pragma unroll
+    for (int m = 0; m < MT; m++) mma::zero<NTK>(d[m]);
 #pragma unroll
     for (int kk = 0; kk < 4; kk++) {
-      uint32_t zr[4];
-      ldsm_t(zr, v2.at(tZ, 16 * blk(kk), 16 * warp));
+      uint32_t za[MT][3][4], fb[NTK / 2][4];
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const float2 w = *reinterpret_cast<const float2*>(sw + 16 * blk(kk) + 8 * (q >> 1) + 2 * tq);
-        uint32_t s[3];
-        split2<3>(w.x * even(zr[q]), w.y * odd(zr[q]), s);
+      for (int p = 0; p < NTK / 2; p++) ldsm_t(fb[p], k1.at(tY, 16 * blk(kk), 16 * p));
+      const float2 w0 = *reinterpret_cast<const float2*>(sw + 16 * blk(kk) + 2 * tq);
+      const float2 w1 = *reinterpret_cast<const float2*>(sw + 16 * blk(kk) + 2 * tq + 8);
 #pragma unroll
-        for (int b = 0; b < 3; b++) za[kk][b][q] = s[b];
+      for (int m = 0; m < MT; m++) {
+        uint32_t zr[4];
+        ldsm_t(zr, v2.at(tZ, 16 * blk(kk), r0 + 16 * m));
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const float2 w = q >> 1 ? w1 : w0;
+          uint32_t s[3];
+          split2<3>(w.x * even(zr[q]), w.y * odd(zr[q]), s);
+#pragma unroll
+          for (int b = 0; b < 3; b++) za[m][b][q] = s[b];
+        }
       }
+#pragma unroll
+      for (int b = 2; b >= 0; b--)
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+          for (int p = 0; p < NTK / 2; p++) {
+            mma::mma_bf16(d[m][2 * p], za[m][b], fb[p][0], fb[p][1]);
+            mma::mma_bf16(d[m][2 * p + 1], za[m][b], fb[p][2], fb[p][3]);
+          }
     }
     const Decay dec(a, n);
 #pragma unroll
-    for (int g = 0; g < NTK / SH::NG; g++) {
-      constexpr int NG = SH::NG;
-      float d[NG][4];
-      mma::zero<NG>(d);
+    for (int m = 0; m < MT; m++)
 #pragma unroll
-      for (int kk = 0; kk < 4; kk++) {
-        uint32_t fb[NG / 2][4];
+      for (int j = 0; j < NTK; j++)
 #pragma unroll
-        for (int p = 0; p < NG / 2; p++) ldsm_t(fb[p], k1.at(tY, 16 * blk(kk), 8 * NG * g + 16 * p));
-#pragma unroll
-        for (int b = 2; b >= 0; b--)
-#pragma unroll
-          for (int p = 0; p < NG / 2; p++) {
-            mma::mma_bf16(d[2 * p], za[kk][b], fb[p][0], fb[p][1]);
-            mma::mma_bf16(d[2 * p + 1], za[kk][b], fb[p][2], fb[p][3]);
-          }
-      }
-#pragma unroll
-      for (int j = 0; j < NG; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) S[NG * g + j][e] = dec(S[NG * g + j][e]) + d[j][e];
-    }
+        for (int e = 0; e < 4; e++) S[m][j][e] = dec(S[m][j][e]) + d[m][j][e];
     if (SH::STG == 1 && c + 1 < nch) {
       mma::fence_async_smem();
       __syncthreads();
       if (tid == 0) load(c + 1);
+    }
+  }
+  if (!ONLY && nch > 0) {  // the last output tile, and every tile's reads before the CTA ends
+    mma::fence_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      if (good && out_t0 >= 0) {
+        tma_store_2d(&maps.o, h * DVt + c0, out_t0, tO);
+        mma::bulk_commit();
+      }
+      mma::bulk_wait_all();
     }
   }
   if (!good) {  // a wait ran out
@@ -892,7 +955,8 @@ cudaError_t launch_chain(int kid, const LinP& P, const LinOp& op, int fwd, cudaS
   if (e != cudaSuccess) return e;
   LinMaps m = {};
   if ((!ONLY && !encode_head_rows(&m.x, op.x, P.Ntok, P.H, DK)) || !encode_head_rows(&m.y, op.y, P.Ntok, P.H, DK) ||
-      !encode_head_rows(&m.z, op.z, P.Ntok, P.H, op.DVt))
+      !encode_head_rows(&m.z, op.z, P.Ntok, P.H, op.DVt) ||
+      (!ONLY && !encode_head_rows(&m.o, op.out, P.Ntok, P.H, op.DVt)))
     return cudaErrorInvalidValue;
   prof_begin(kid, st);
   lin_chain_kernel<DK, DVS, ONLY>
