@@ -122,60 +122,65 @@ __global__ void __launch_bounds__(1024) lin_table_kernel(LinP P) {
 
 // Turns the segments' own states into their start states, in the chain's
 // direction: start_0 = init, start_{s+1} = e^{-a len_s} start_s + own_s.  A
-// thread per four elements of a (split document, head)'s state; four segments'
-// loads in flight.
-__global__ void __launch_bounds__(256) lin_fold_kernel(LinP P, float* segc, const float* init, int rev, int N, int fwd) {
+// thread per four elements of a (split document, head)'s state, eight segments'
+// loads in flight; the CTAs loop over the pieces, whose number the device alone
+// may know (a grid of its bound, mostly empty, took 36 to 62 us).
+constexpr int FTH = 128, FCTAS = 8 * LIN_SMS;
+__global__ void __launch_bounds__(FTH) lin_fold_kernel(LinP P, float* segc, const float* init, int rev, int N, int fwd) {
   pdl_wait();
   pdl_release();
   if (!ready(P, fwd)) return;
-  const int d = blockIdx.x / P.H, h = blockIdx.x % P.H, at = (blockIdx.y * 256 + threadIdx.x) * 4;
-  if (at >= N) return;
-  int u0, ns, doc, len, last;
-  if (P.rows) {
-    ns = (P.T + P.L - 1) / P.L;
-    u0 = d * ns;
-    doc = d;
-    len = P.L;
-    last = P.T - (ns - 1) * P.L;
-  } else {
-    if (d >= P.counts[2]) return;
-    u0 = P.longs[d].x;
-    ns = P.longs[d].y;
-    doc = P.units[u0].x;
-    len = P.units[u0].z;
-    last = P.units[u0 + ns - 1].z;
-  }
-  const float a = decay_of(P.A_log, h), full = decay_pow(a, len), first = rev ? decay_pow(a, last) : full;
-  float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (init) {
-    st = *reinterpret_cast<const float4*>(init + ((int64_t)doc * P.H + h) * N + at);
-    const float m = rev ? 1.0f / P.scale : 1.0f;
-    st.x *= m; st.y *= m; st.z *= m; st.w *= m;
-  }
-  auto own = [&](int k) -> float4* {  // k-th segment in the chain's direction
-    return reinterpret_cast<float4*>(segc + ((int64_t)(u0 + (rev ? ns - 1 - k : k)) * P.H + h) * N + at);
-  };
-  float4 v[4], nx[4];
+  constexpr int F = 8;
+  const int pieces = N / (4 * FTH);
+  const int64_t total = (int64_t)(P.rows ? P.n_long : P.counts[2]) * P.H * pieces;
+  for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+    const int at = ((int)(item % pieces) * FTH + threadIdx.x) * 4, dh = (int)(item / pieces), d = dh / P.H, h = dh % P.H;
+    int u0, ns, doc, len, last;
+    if (P.rows) {
+      ns = (P.T + P.L - 1) / P.L;
+      u0 = d * ns;
+      doc = d;
+      len = P.L;
+      last = P.T - (ns - 1) * P.L;
+    } else {
+      u0 = P.longs[d].x;
+      ns = P.longs[d].y;
+      doc = P.units[u0].x;
+      len = P.units[u0].z;
+      last = P.units[u0 + ns - 1].z;
+    }
+    const float a = decay_of(P.A_log, h), full = decay_pow(a, len), first = rev ? decay_pow(a, last) : full;
+    float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (init) {
+      st = *reinterpret_cast<const float4*>(init + ((int64_t)doc * P.H + h) * N + at);
+      const float m = rev ? 1.0f / P.scale : 1.0f;
+      st.x *= m; st.y *= m; st.z *= m; st.w *= m;
+    }
+    auto own = [&](int k) -> float4* {  // k-th segment in the chain's direction
+      return reinterpret_cast<float4*>(segc + ((int64_t)(u0 + (rev ? ns - 1 - k : k)) * P.H + h) * N + at);
+    };
+    float4 v[F], nx[F];
 #pragma unroll
-  for (int e = 0; e < 4; e++)
-    if (e < ns - 1) v[e] = *own(e);
-  for (int k = 0; k < ns - 1; k += 4) {
-    // (start k + 4 goes where own state k + 4 was: the next four are read first)
+    for (int e = 0; e < F; e++)
+      if (e < ns - 1) v[e] = *own(e);
+    for (int k = 0; k < ns - 1; k += F) {
+      // (start k + F goes where own state k + F was: the next F are read first)
 #pragma unroll
-    for (int e = 0; e < 4; e++)
-      if (k + 4 + e < ns - 1) nx[e] = *own(k + 4 + e);
+      for (int e = 0; e < F; e++)
+        if (k + F + e < ns - 1) nx[e] = *own(k + F + e);
 #pragma unroll
-    for (int e = 0; e < 4; e++)
-      if (k + e < ns - 1) {
-        const float g = k + e == 0 ? first : full;
-        st.x = fmaf(g, st.x, v[e].x);
-        st.y = fmaf(g, st.y, v[e].y);
-        st.z = fmaf(g, st.z, v[e].z);
-        st.w = fmaf(g, st.w, v[e].w);
-        *own(k + e + 1) = st;
-      }
+      for (int e = 0; e < F; e++)
+        if (k + e < ns - 1) {
+          const float g = k + e == 0 ? first : full;
+          st.x = fmaf(g, st.x, v[e].x);
+          st.y = fmaf(g, st.y, v[e].y);
+          st.z = fmaf(g, st.z, v[e].z);
+          st.w = fmaf(g, st.w, v[e].w);
+          *own(k + e + 1) = st;
+        }
 #pragma unroll
-    for (int e = 0; e < 4; e++) v[e] = nx[e];
+      for (int e = 0; e < F; e++) v[e] = nx[e];
+    }
   }
 }
 
@@ -277,22 +282,32 @@ __device__ __forceinline__ void zero_rows(unsigned char* stg, int n) {
   }
 }
 
-// A warp's 16 columns x 64 tokens of an output (accumulator fragments of its
-// transpose, token block t at 16 blk(t)) to rows of `ld` elements, transposed
-// through 2 KB of shared memory, 16 bytes a lane; tokens < n.
-__device__ __forceinline__ void store_rows(bf16* buf, const float (&o)[8][4], bf16* out, int64_t ld, int n, bool rev) {
+// A warp's 16 columns (from c0) of an output, accumulator fragments of its
+// transpose with token block t at 16 (rev ? 3 - t : t), into a 64 x W tile in the
+// maps' swizzle.
+template <int W>
+__device__ __forceinline__ unsigned char* tile_at(unsigned char* tile, int row, int cg) {
+  return W == 32 ? tile + row * 64 + ((cg ^ ((row >> 1) & 3)) << 4) : tile + row * 128 + ((cg ^ (row & 7)) << 4);
+}
+template <int W>
+__device__ __forceinline__ void stage_tile(unsigned char* tile, int c0, const float (&o)[8][4], bool rev) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int p = 0; p < 4; p++)  // four 8 x 8 tiles
-    stsm4t(buf + (4 * p + (lane >> 3)) * 64 + (lane & 7) * 8, pack2(o[2 * p][0], o[2 * p][1]),
-           pack2(o[2 * p][2], o[2 * p][3]), pack2(o[2 * p + 1][0], o[2 * p + 1][1]),
-           pack2(o[2 * p + 1][2], o[2 * p + 1][3]));
+  for (int p = 0; p < 4; p++) {  // four 8 x 8 tiles: 16 tokens by 16 columns
+    const int row = 16 * (rev ? 3 - p : p) + 8 * (lane >> 4) + (lane & 7), cg = c0 / 8 + ((lane >> 3) & 1);
+    stsm4t(tile_at<W>(tile, row, cg), pack2(o[2 * p][0], o[2 * p][1]), pack2(o[2 * p][2], o[2 * p][3]),
+           pack2(o[2 * p + 1][0], o[2 * p + 1][1]), pack2(o[2 * p + 1][2], o[2 * p + 1][3]));
+  }
+}
+// The warp's NC columns (from c0) of the tile's first n rows to rows ld apart:
+// for a chunk that is not full.
+template <int W, int NC>
+__device__ __forceinline__ void copy_rows(const unsigned char* tile, int c0, bf16* out, int64_t ld, int n) {
   __syncwarp();
-#pragma unroll
-  for (int p = 0; p < 4; p++) {
-    const int m = lane >> 3, row = 16 * (rev ? 3 - p : p) + 8 * (m >> 1) + (lane & 7);
-    const uint4 v = *reinterpret_cast<const uint4*>(buf + (4 * p + m) * 64 + (lane & 7) * 8);
-    if (row < n) *reinterpret_cast<uint4*>(out + row * ld + 8 * (m & 1)) = v;
+  for (int g = threadIdx.x & 31; g < n * (NC / 8); g += 32) {
+    const int row = g / (NC / 8), cg = c0 / 8 + g % (NC / 8);
+    *reinterpret_cast<uint4*>(out + row * ld + 8 * cg) =
+        *reinterpret_cast<const uint4*>(tile_at<W>(const_cast<unsigned char*>(tile), row, cg));
   }
 }
 
@@ -533,23 +548,9 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
       }
       // ---- out: transposed into tO, and from there as a tile (a chunk that is not full: row by row)
 #pragma unroll
-      for (int m = 0; m < MT; m++)
-#pragma unroll
-        for (int p = 0; p < 4; p++) {  // four 8 x 8 tiles: 16 tokens by 16 columns
-          const int row = 16 * blk(p) + 8 * (lane >> 4) + (lane & 7), cg = (r0 + 16 * m) / 8 + ((lane >> 3) & 1);
-          stsm4t(tO + row * 128 + ((cg ^ (row & 7)) << 4), pack2(o[m][2 * p][0], o[m][2 * p][1]),
-                 pack2(o[m][2 * p][2], o[m][2 * p][3]), pack2(o[m][2 * p + 1][0], o[m][2 * p + 1][1]),
-                 pack2(o[m][2 * p + 1][2], o[m][2 * p + 1][3]));
-        }
+      for (int m = 0; m < MT; m++) stage_tile<DVS>(tO, r0 + 16 * m, o[m], rev);
       out_t0 = n == C ? t0 : -1;
-      if (n < C) {
-        __syncwarp();
-        for (int g = lane; g < n * 2 * MT; g += 32) {
-          const int row = g / (2 * MT), cg = r0 / 8 + g % (2 * MT);
-          *reinterpret_cast<uint4*>((bf16*)op.out + ((int64_t)(t0 + row) * H + h) * DVt + c0 + 8 * cg) =
-              *reinterpret_cast<const uint4*>(tO + row * 128 + ((cg ^ (row & 7)) << 4));
-        }
-      }
+      if (n < C) copy_rows<DVS, 16 * MT>(tO, r0, (bf16*)op.out + ((int64_t)t0 * H + h) * DVt + c0, (int64_t)H * DVt, n);
     }
     // ---- the state: S^T = e^{-an} S^T + (weighted z)^T y.  The product is summed apart from the
     // state (the tensor core truncates what an addition shifts out: into a long chain's state that
@@ -659,7 +660,7 @@ struct DShape {
 };
 
 struct DqkMaps {
-  CUtensorMap q, k, v, dO;
+  CUtensorMap q, k, v, dO, dq, dk;
 };
 struct DqkOp {
   void *dq, *dk;
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
   if (tid == 0) {
     for (int s = 0; s < SH::STG; s++) mma::mbar_init(bar + s, 1);
     mma::mbar_init_fence();
-    load(0);
+    for (int s = 0; s < SH::STG && s < nch; s++) load(s);
   }
   for (int i = tid; i < 65; i += NTH) tab[i] = decay_pow(a, i);
   __syncthreads();
@@ -743,12 +744,10 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
       n_w = n;
     }
     zero_rows<SH::STAGE, 2 * SH::OB, 128, DVS == 32 ? 64 : 128, NTH>(stg, n);
-    mma::fence_async_smem();  // this thread's accesses to the other stage precede the copies into it
     if (__syncthreads_or(!good)) {
       good = false;
       break;
     }
-    if (SH::STG == 2 && tid == 0 && c + 1 < nch) load(c + 1);
 
     float part = 0.f;
     // ---- pairs, three blocks at a time
@@ -897,17 +896,30 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
           mma::mma_bf16(dk[2 * p + 1], fq[kk], fp[p][2], fp[p][3]);
         }
       }
-    // ---- out, through the warp's 4 KB of the dO and v tiles
-    store_rows(reinterpret_cast<bf16*>(stg) + warp * 2048, dq, (bf16*)op.dq + ((int64_t)t0 * H + h) * DKt + c0 + 16 * warp,
-               (int64_t)H * DKt, n, false);
-    store_rows(reinterpret_cast<bf16*>(stg) + warp * 2048 + 1024, dk,
-               (bf16*)op.dk + ((int64_t)t0 * H + h) * DKt + c0 + 16 * warp, (int64_t)H * DKt, n, false);
-    if (SH::STG == 1 && c + 1 < nch) {
-      mma::fence_async_smem();
-      __syncthreads();
-      if (tid == 0) load(c + 1);
+    // ---- out, in the place of the q and k tiles (their last reads were before the barrier)
+    unsigned char *uQ = stg + 2 * SH::OB, *uK = uQ + SH::QB;
+    stage_tile<DVS>(uQ, 16 * warp, dq, false);
+    stage_tile<DVS>(uK, 16 * warp, dk, false);
+    if (n < C) {
+      const int64_t at = ((int64_t)t0 * H + h) * DKt + c0;
+      copy_rows<DVS, 16>(uQ, 16 * warp, (bf16*)op.dq + at, (int64_t)H * DKt, n);
+      copy_rows<DVS, 16>(uK, 16 * warp, (bf16*)op.dk + at, (int64_t)H * DKt, n);
+    }
+    mma::fence_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      if (n == C) {
+        tma_store_2d(&maps.dq, h * DKt + c0, t0, uQ);
+        tma_store_2d(&maps.dk, h * DKt + c0, t0, uK);
+        mma::bulk_commit();
+      }
+      if (c + SH::STG < nch) {  // the next chunk of this stage
+        mma::bulk_wait_read();
+        load(c + SH::STG);
+      }
     }
   }
+  if (tid == 0) mma::bulk_wait_all();
   if (!good) {  // a wait ran out
     if (tid == 0) *P.err = KDA_ERR_DEVICE;
     return;
@@ -988,7 +1000,8 @@ cudaError_t launch_dqk(const LinP& P, const LinGrads& g, const DqkOp& op, int dk
   if (e != cudaSuccess) return e;
   DqkMaps m = {};
   if (!encode_head_rows(&m.q, g.q, P.Ntok, P.H, dk) || !encode_head_rows(&m.k, g.k, P.Ntok, P.H, dk) ||
-      !encode_head_rows(&m.v, g.v, P.Ntok, P.H, DV) || !encode_head_rows(&m.dO, g.dO, P.Ntok, P.H, DV))
+      !encode_head_rows(&m.v, g.v, P.Ntok, P.H, DV) || !encode_head_rows(&m.dO, g.dO, P.Ntok, P.H, DV) ||
+      !encode_head_rows(&m.dq, g.dq, P.Ntok, P.H, dk) || !encode_head_rows(&m.dk, g.dk, P.Ntok, P.H, dk))
     return cudaErrorInvalidValue;
   prof_begin(K_LIN_DQK, st);
   lin_dqk_kernel<DV, DVS, DA>
@@ -1119,7 +1132,7 @@ cudaError_t run_seg(const LinP& P, const Dims& d, const void* y, const void* z, 
   if (e != cudaSuccess) return e;
   const int N = d.dk * d.dv;
   prof_begin(K_LIN_FOLD, st);
-  e = launch_pdl(lin_fold_kernel, dim3((unsigned)P.n_long * d.H, (N + 1023) / 1024), dim3(256), 0, st, P, segc, init, rev, N,
+  e = launch_pdl(lin_fold_kernel, dim3(FCTAS), dim3(FTH), 0, st, P, segc, init, rev, N,
                  fwd == 1 ? 2 : fwd);
   prof_end(K_LIN_FOLD, st);
   return e;
