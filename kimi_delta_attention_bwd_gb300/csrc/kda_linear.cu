@@ -29,9 +29,11 @@
 //   D  entry state to exit state, n e^{-an} <S, R>
 //
 // The state stays in fp32 registers for a whole chain.  Operands that are not
-// inputs are split into bf16 parts: two (about 16 bits) where the result is
-// rounded to bf16, three (24 bits) where it enters the fp32 state or the decay
-// gradient's sums.  fp32 io: kda_linear_f32.cu.
+// inputs are rounded to bf16 where the product ends in a bf16 output (the pairs
+// and the state's rows: as much again as the output's own rounding, 2-norm
+// error 1.7e-3 -> 2.3e-3; a second part each, 16 bits, cost the chains a fifth of
+// their time), and split into three bf16 parts (24 bits) where it enters the fp32
+// state or the decay gradient's sums.  fp32 io: kda_linear_f32.cu.
 #include "kda_linear.cuh"
 
 namespace kda {
@@ -196,7 +198,7 @@ struct Shape {
   static constexpr int XB = ONLY ? 0 : 128 * DK, YB = 128 * DK, ZB = 128 * DVS;
   static constexpr int STAGE = XB + YB + ZB;
   static constexpr int STG = DK == 128 || ONLY ? 2 : 1;
-  static constexpr int PB = ONLY ? 0 : 2 * 64 * 64 * 2, OB = ONLY ? 0 : 128 * DVS;
+  static constexpr int PB = ONLY ? 0 : 64 * 64 * 2, OB = ONLY ? 0 : 128 * DVS;
   static constexpr int SMEM = 1024 /* alignment */ + STG * STAGE + PB + OB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
   static constexpr int NTK = DK / 8;  // 8-key tiles of a warp's state rows
   // resident CTAs: what registers and shared memory allow
@@ -250,12 +252,79 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 __device__ __forceinline__ float even(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float odd(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// The 16 x 16 blocks (row r, column c <= r) of a chunk's pairs that a warp
-// forms, a byte 4 r + c + 1 each, 0 ends: ten over four warps or two.
-template <int NW>
-__device__ __forceinline__ uint64_t pair_blocks(int warp) {
-  if (NW == 2) return warp == 0 ? 0x01100f0e0dull : 0x06050b0a09ull;
-  return warp == 0 ? 0x0f0e0dull : warp == 1 ? 0x0a0910ull : warp == 2 ? 0x050bull : 0x0106ull;
+// The 16 x 16 blocks (row r, column c <= r) of a chunk's pairs, ten over four
+// warps or two: a warp's list, 4 r + c each.  Blocks of a list that share a row
+// or a column share that operand's fragments.
+template <int... RC>
+struct Blocks {
+  static constexpr int N = sizeof...(RC);
+  static __host__ __device__ constexpr int row(int t) {
+    const int rc[N] = {RC...};
+    return rc[t] >> 2;
+  }
+  static __host__ __device__ constexpr int col(int t) {
+    const int rc[N] = {RC...};
+    return rc[t] & 3;
+  }
+  static __host__ __device__ constexpr bool has_row(int r) { return ((RC >> 2 == r) || ...); }
+  static __host__ __device__ constexpr bool has_col(int c) { return (((RC & 3) == c) || ...); }
+};
+template <int NW, class F>
+__device__ __forceinline__ void for_my_blocks(int warp, F f) {
+  if constexpr (NW == 2) {
+    if (warp == 0) f(Blocks<12, 13, 14, 15, 0>());
+    else f(Blocks<8, 9, 10, 4, 5>());
+  } else {
+    if (warp == 0) f(Blocks<12, 13, 14>());
+    else if (warp == 1) f(Blocks<8, 9, 10>());
+    else if (warp == 2) f(Blocks<4, 5, 15>());
+    else f(Blocks<0>());
+  }
+}
+// p[t] = block t of x y^T over DK columns; row(r) and col(c) load fragments of a
+// 16-row block at column 16 kk.
+template <int DK, class B, class FR, class FC>
+__device__ __forceinline__ void pair_products(float (&p)[B::N][2][4], FR row, FC col) {
+#pragma unroll
+  for (int t = 0; t < B::N; t++) mma::zero<2>(p[t]);
+#pragma unroll
+  for (int kk = 0; kk < DK / 16; kk++) {
+    uint32_t fa[4][4], fb[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if (B::has_row(i)) row(fa[i], i, kk);
+      if (B::has_col(i)) col(fb[i], i, kk);
+    }
+#pragma unroll
+    for (int t = 0; t < B::N; t++) {
+      mma::mma_bf16(p[t][0], fa[B::row(t)], fb[B::col(t)][0], fb[B::col(t)][1]);
+      mma::mma_bf16(p[t][1], fa[B::row(t)], fb[B::col(t)][2], fb[B::col(t)][3]);
+    }
+  }
+}
+// Weights the pairs (lut: weights of a pair of neighbouring columns by distance,
+// index 64 at distance 0; sign: +1 where rows come after columns) and stores
+// them as bf16 in tP [64][64], blocks in the chain's order.
+template <class B>
+__device__ __forceinline__ void pair_store(float (&p)[B::N][2][4], const float2* lut, unsigned char* tP, int sign) {
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  const float2* lp = lut + 64 + sign * (gq - 2 * tq);
+  unsigned char* pp = tP + gq * 128 + 4 * tq;
+#pragma unroll
+  for (int t = 0; t < B::N; t++) {
+    const int r = B::row(t), c = B::col(t);
+#pragma unroll
+    for (int j = 0; j < 2; j++)
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        // (in reverse a later block lies before: its distance is positive too)
+        const float2 w = lp[16 * (r - c) + sign * (8 * k - 8 * j)];
+        p[t][j][2 * k] *= w.x;
+        p[t][j][2 * k + 1] *= w.y;
+        *reinterpret_cast<uint32_t*>(pp + (16 * r + 8 * k) * 128 + (((2 * c + j) ^ gq) << 4)) =
+            pack2(p[t][j][2 * k], p[t][j][2 * k + 1]);
+      }
+  }
 }
 
 // The tensors of a chain as [Ntok][H d] maps with boxes of 64 tokens.
@@ -315,7 +384,7 @@ __device__ __forceinline__ void copy_rows(const unsigned char* tile, int c0, bf1
 // value rows of S^T as fp32 accumulator fragments for the whole
 // chain; per chunk
 //   pairs  P = w (x y^T), the ten 16 x 16 blocks on and below the diagonal
-//          shared out over the warps, to shared memory as two parts
+//          shared out over the warps, to shared memory
 //   o^T    = row weight * (S^T x^T) (S as register fragments) + z^T P^T
 //   S^T    = e^{-an} S^T + (weighted z)^T y
 // so that the state never leaves its registers and a chunk needs two barriers;
@@ -325,13 +394,13 @@ __device__ __forceinline__ void copy_rows(const unsigned char* tile, int c0, bf1
 // mma.sync rather than tcgen05: the chain is bound by the instructions around
 // its products, and accumulators that are the next product's operands save
 // the round trips through TMEM and shared memory.
-template <int DK, int DVS, bool ONLY>
+template <int DK, int DVS, bool ONLY, bool rev>
 __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u, int h, int slice) {
   using SH = Shape<DK, DVS, ONLY>;
   constexpr int NTH = SH::NTH, NW = SH::NW, NTK = SH::NTK, MT = SH::MT;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (mma::smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned char* tP = smem + SH::STG * SH::STAGE;  // [2 parts][64][64]
+  unsigned char* tP = smem + SH::STG * SH::STAGE;  // [64][64], blocks in the chain's order
   unsigned char* tO = tP + SH::PB;                 // [64][DVS], the output's rows
   float2* lut = reinterpret_cast<float2*>(tO + SH::OB);
   float* tab = reinterpret_cast<float*>(lut + 128);  // [65] e^{-a m}
@@ -342,12 +411,11 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
 
   Unit un;
   if (!unit_of(P, u, un)) return;
-  if (ONLY && un.seg == (op.rev ? 0 : un.nseg - 1)) return;  // the last segment of its direction feeds nobody
+  if (ONLY && un.seg == (rev ? 0 : un.nseg - 1)) return;  // the last segment of its direction feeds nobody
   const int H = P.H, DVt = op.DVt, c0 = slice * DVS;
   const int64_t stN = (int64_t)DK * DVt;
   const float a = decay_of(P.A_log, h);
   const int nch = (un.ntok + C - 1) / C;
-  const bool rev = op.rev != 0;
   auto blk = [&](int t) { return rev ? 3 - t : t; };  // 16-token block t in the chain's direction
 
   auto load = [&](int c) {  // one thread
@@ -437,53 +505,15 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
         tma_store_2d(&maps.o, h * DVt + c0, out_t0, tO);
         mma::bulk_commit();
       }
-      // ---- pairs: three blocks at a time, so that consecutive products are independent
-      for (uint64_t todo = pair_blocks<NW>(warp); todo; todo >>= 24) {
-        int rr[3], cc[3];
-        float p[3][2][4];
-#pragma unroll
-        for (int t = 0; t < 3; t++) {
-          int code = (int)(todo >> (8 * t)) & 255;
-          if (!code) code = (int)todo & 255;  // (the first once more, not stored)
-          rr[t] = blk((code - 1) >> 2);
-          cc[t] = blk((code - 1) & 3);
-          mma::zero<2>(p[t]);
-        }
-#pragma unroll
-        for (int kk = 0; kk < DK / 16; kk++) {
-          uint32_t fa[3][4], fb[3][4];
-#pragma unroll
-          for (int t = 0; t < 3; t++) {
-            ldsm(fa[t], k1.at(tX, 16 * rr[t], 16 * kk));
-            ldsm(fb[t], k2.at(tY, 16 * cc[t], 16 * kk));
-          }
-#pragma unroll
-          for (int t = 0; t < 3; t++) {
-            mma::mma_bf16(p[t][0], fa[t], fb[t][0], fb[t][1]);
-            mma::mma_bf16(p[t][1], fa[t], fb[t][2], fb[t][3]);
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < 3; t++) {
-          if (t > 0 && !((todo >> (8 * t)) & 255)) continue;
-          const int d = 16 * (rr[t] - cc[t]) + gq - 2 * tq;  // row - column of the thread's first pair
-          const float2* lp = lut + 64 + (rev ? -d : d);
-#pragma unroll
-          for (int j = 0; j < 2; j++)
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-              const int dd = 8 * k - 8 * j;
-              const float2 w = lp[rev ? -dd : dd];
-              p[t][j][2 * k] *= w.x;
-              p[t][j][2 * k + 1] *= w.y;
-              uint32_t s[2];
-              split2<2>(p[t][j][2 * k], p[t][j][2 * k + 1], s);
-              unsigned char* at = tP + (16 * rr[t] + 8 * k + gq) * 128 + (((2 * cc[t] + j) ^ gq) << 4) + 4 * tq;
-              *reinterpret_cast<uint32_t*>(at) = s[0];
-              *reinterpret_cast<uint32_t*>(at + 8192) = s[1];
-            }
-        }
-      }
+      // ---- pairs
+      for_my_blocks<NW>(warp, [&](auto blocks) {
+        using B = decltype(blocks);
+        float p[B::N][2][4];
+        pair_products<DK, B>(
+            p, [&](uint32_t (&f)[4], int r, int kk) { ldsm(f, k1.at(tX, 16 * blk(r), 16 * kk)); },
+            [&](uint32_t (&f)[4], int c, int kk) { ldsm(f, k2.at(tY, 16 * blk(c), 16 * kk)); });
+        pair_store<B>(p, lut, tP, rev ? -1 : 1);
+      });
       if (tid == 0) mma::bulk_wait_read();  // tO is free again
       __syncthreads();                      // the pairs of every warp
       // ---- the entry state's rows: o^T = S^T x^T
@@ -492,7 +522,7 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
       for (int m = 0; m < MT; m++) mma::zero<8>(o[m]);
 #pragma unroll
       for (int kk = 0; kk < DK / 16; kk++) {
-        uint32_t f[MT][2][4], fb[4][4];
+        uint32_t f[MT][4], fb[4][4];
 #pragma unroll
         for (int p = 0; p < 4; p++) ldsm(fb[p], k2.at(tX, 16 * blk(p), 16 * kk));
 #pragma unroll
@@ -500,20 +530,15 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
 #pragma unroll
           for (int q = 0; q < 4; q++) {  // accumulator tiles 2 kk, 2 kk + 1 are the 16 x 16 operand
             const float* st2 = &S[m][2 * kk + (q >> 1)][2 * (q & 1)];
-            uint32_t s[2];
-            split2<2>(st2[0], st2[1], s);
-            f[m][0][q] = s[0];
-            f[m][1][q] = s[1];
+            f[m][q] = pack2(st2[0], st2[1]);
           }
 #pragma unroll
-        for (int b = 1; b >= 0; b--)
+        for (int m = 0; m < MT; m++)
 #pragma unroll
-          for (int m = 0; m < MT; m++)
-#pragma unroll
-            for (int p = 0; p < 4; p++) {
-              mma::mma_bf16(o[m][2 * p], f[m][b], fb[p][0], fb[p][1]);
-              mma::mma_bf16(o[m][2 * p + 1], f[m][b], fb[p][2], fb[p][3]);
-            }
+          for (int p = 0; p < 4; p++) {
+            mma::mma_bf16(o[m][2 * p], f[m], fb[p][0], fb[p][1]);
+            mma::mma_bf16(o[m][2 * p + 1], f[m], fb[p][2], fb[p][3]);
+          }
       }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
@@ -532,19 +557,16 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
         uint32_t zr[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; m++) ldsm_t(zr[m], v2.at(tZ, 16 * blk(kk), r0 + 16 * m));
+        uint32_t fb[4][4];
 #pragma unroll
-        for (int b = 1; b >= 0; b--) {
-          uint32_t fb[4][4];
+        for (int p = kk; p < 4; p++) ldsm(fb[p], p2.at(mma::smem_u32(tP), 16 * p, 16 * kk));
 #pragma unroll
-          for (int p = kk; p < 4; p++) ldsm(fb[p], p2.at(mma::smem_u32(tP) + 8192 * b, 16 * blk(p), 16 * blk(kk)));
+        for (int m = 0; m < MT; m++)
 #pragma unroll
-          for (int m = 0; m < MT; m++)
-#pragma unroll
-            for (int p = kk; p < 4; p++) {
-              mma::mma_bf16(o[m][2 * p], zr[m], fb[p][0], fb[p][1]);
-              mma::mma_bf16(o[m][2 * p + 1], zr[m], fb[p][2], fb[p][3]);
-            }
-        }
+          for (int p = kk; p < 4; p++) {
+            mma::mma_bf16(o[m][2 * p], zr[m], fb[p][0], fb[p][1]);
+            mma::mma_bf16(o[m][2 * p + 1], zr[m], fb[p][2], fb[p][3]);
+          }
       }
       // ---- out: transposed into tO, and from there as a tile (a chunk that is not full: row by row)
 #pragma unroll
@@ -628,12 +650,12 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
   }
 }
 
-template <int DK, int DVS, bool ONLY>
+template <int DK, int DVS, bool ONLY, bool rev>
 __global__ void __launch_bounds__(Shape<DK, DVS, ONLY>::NTH, Shape<DK, DVS, ONLY>::CTAS)
     lin_chain_kernel(const __grid_constant__ LinMaps maps, LinP P, LinOp op, int fwd) {
   if (!ready(P, fwd)) return;
   const int ns = op.DVt / DVS;
-  chain<DK, DVS, ONLY>(P, op, maps, blockIdx.x / (ns * P.H), (blockIdx.x / ns) % P.H, blockIdx.x % ns);
+  chain<DK, DVS, ONLY, rev>(P, op, maps, blockIdx.x / (ns * P.H), (blockIdx.x / ns) % P.H, blockIdx.x % ns);
 }
 
 // ------------------------------------------------------------ dq and dk, bf16
@@ -646,15 +668,23 @@ __global__ void __launch_bounds__(Shape<DK, DVS, ONLY>::NTH, Shape<DK, DVS, ONLY
 // and reads its rows of S and R from memory as operand fragments, once.
 constexpr int CPB = 4;
 
+// A warp's blocks (row r, column c <= r) of the pairs, a byte 4 r + c + 1 each,
+// 0 ends.
+template <int NW>
+__device__ __forceinline__ uint64_t pair_list(int warp) {
+  if (NW == 2) return warp == 0 ? 0x01100f0e0dull : 0x06050b0a09ull;
+  return warp == 0 ? 0x0f0e0dull : warp == 1 ? 0x0a0910ull : warp == 2 ? 0x050bull : 0x0106ull;
+}
+
 template <int DV, int DVS, bool DA>
 struct DShape {
   static constexpr int NW = DVS / 16, NTH = 32 * NW;
   static constexpr int OB = 128 * DV, QB = 128 * DVS;  // bytes of the dO and v, the q and k tiles
   static constexpr int STAGE = 2 * OB + 2 * QB;
   static constexpr int STG = DV == 128 ? 1 : 2;        // (one stage there: three CTAs per SM)
-  static constexpr int PB = 2 * 64 * 64 * 2;
+  static constexpr int PB = 64 * 64 * 2;
   static constexpr int SMEM = 1024 + STG * STAGE + PB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
-  static constexpr int SP = DA ? 3 : 2;  // parts of the states as operands: fp32 sums need the third
+  static constexpr int SP = DA ? 3 : 1;  // parts of the states as operands: their rows enter fp32 sums
   static constexpr int BY_REG = 65536 / (NTH * 168), BY_SMEM = 227 * 1024 / (SMEM + 1024);
   static constexpr int CTAS = BY_REG < BY_SMEM ? BY_REG : BY_SMEM;
 };
@@ -675,7 +705,7 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
   constexpr int NTH = SH::NTH, NW = SH::NW, SP = SH::SP;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (mma::smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned char* tP = smem + SH::STG * SH::STAGE;  // [2 parts][64][64]
+  unsigned char* tP = smem + SH::STG * SH::STAGE;  // [64][64]
   float2* lut = reinterpret_cast<float2*>(tP + SH::PB);
   float* tab = reinterpret_cast<float*>(lut + 128);
   float* rq = tab + 96;  // [64] scale e^{-a(i+1)}
@@ -750,8 +780,9 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
     }
 
     float part = 0.f;
-    // ---- pairs, three blocks at a time
-    for (uint64_t todo = pair_blocks<NW>(warp); todo; todo >>= 24) {
+    // ---- pairs, three blocks at a time (the same code for every warp: a copy for each, as the chain
+    // has, overflows the instruction caches here, 551 -> 898 us at 128/128)
+    for (uint64_t todo = pair_list<NW>(warp); todo; todo >>= 24) {
       int rr[3], cc[3];
       float p[3][2][4];
 #pragma unroll
@@ -787,11 +818,8 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
             const float2 w = lut[64 + d + 8 * k - 8 * j];
             p[t][j][2 * k] *= w.x;
             p[t][j][2 * k + 1] *= w.y;
-            uint32_t s[2];
-            split2<2>(p[t][j][2 * k], p[t][j][2 * k + 1], s);
-            unsigned char* at = tP + (16 * rr[t] + 8 * k + gq) * 128 + (((2 * cc[t] + j) ^ gq) << 4) + 4 * tq;
-            *reinterpret_cast<uint32_t*>(at) = s[0];
-            *reinterpret_cast<uint32_t*>(at + 8192) = s[1];
+            *reinterpret_cast<uint32_t*>(tP + (16 * rr[t] + 8 * k + gq) * 128 + (((2 * cc[t] + j) ^ gq) << 4) + 4 * tq) =
+                pack2(p[t][j][2 * k], p[t][j][2 * k + 1]);
           }
         if constexpr (DA) {  // A: the same pairs of q and k (this slice's columns)
           float m2[2][4];
@@ -819,7 +847,7 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
     const int64_t sat = ((int64_t)(g0 + c) * H + h) * DV * DKt + c0 + 16 * warp + gq;
     const float *pS = op.S + sat, *pR = op.R + sat;
     float dot = 0.f;
-#pragma unroll
+#pragma unroll (DA ? 2 : DV / 16)  // (the instruction caches again)
     for (int kk = 0; kk < DV / 16; kk++) {
       uint32_t fs[SP][4], fr[SP][4];
 #pragma unroll
@@ -876,26 +904,24 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
     __syncthreads();  // the pairs of every warp; dO and v have been read
     // ---- dq^T += k^T P^T, dk^T += q^T P
 #pragma unroll
-    for (int kk = 0; kk < 4; kk++)
+    for (int kk = 0; kk < 4; kk++) {
+      const uint32_t tp = mma::smem_u32(tP);
+      uint32_t fp[4][4];
 #pragma unroll
-      for (int b = 1; b >= 0; b--) {
-        const uint32_t tp = mma::smem_u32(tP) + 8192 * b;
-        uint32_t fp[4][4];
+      for (int p = kk; p < 4; p++) ldsm(fp[p], p2.at(tp, 16 * p, 16 * kk));  // tokens i of block p, j of kk
 #pragma unroll
-        for (int p = kk; p < 4; p++) ldsm(fp[p], p2.at(tp, 16 * p, 16 * kk));  // tokens i of block p, j of kk
-#pragma unroll
-        for (int p = kk; p < 4; p++) {
-          mma::mma_bf16(dq[2 * p], fk[kk], fp[p][0], fp[p][1]);
-          mma::mma_bf16(dq[2 * p + 1], fk[kk], fp[p][2], fp[p][3]);
-        }
-#pragma unroll
-        for (int p = 0; p <= kk; p++) ldsm_t(fp[p], p1.at(tp, 16 * kk, 16 * p));  // tokens i of block kk, j of p
-#pragma unroll
-        for (int p = 0; p <= kk; p++) {
-          mma::mma_bf16(dk[2 * p], fq[kk], fp[p][0], fp[p][1]);
-          mma::mma_bf16(dk[2 * p + 1], fq[kk], fp[p][2], fp[p][3]);
-        }
+      for (int p = kk; p < 4; p++) {
+        mma::mma_bf16(dq[2 * p], fk[kk], fp[p][0], fp[p][1]);
+        mma::mma_bf16(dq[2 * p + 1], fk[kk], fp[p][2], fp[p][3]);
       }
+#pragma unroll
+      for (int p = 0; p <= kk; p++) ldsm_t(fp[p], p1.at(tp, 16 * kk, 16 * p));  // tokens i of block kk, j of p
+#pragma unroll
+      for (int p = 0; p <= kk; p++) {
+        mma::mma_bf16(dk[2 * p], fq[kk], fp[p][0], fp[p][1]);
+        mma::mma_bf16(dk[2 * p + 1], fq[kk], fp[p][2], fp[p][3]);
+      }
+    }
     // ---- out, in the place of the q and k tiles (their last reads were before the barrier)
     unsigned char *uQ = stg + 2 * SH::OB, *uK = uQ + SH::QB;
     stage_tile<DVS>(uQ, 16 * warp, dq, false);
@@ -960,10 +986,10 @@ __global__ void __launch_bounds__(256) lin_decay_kernel(LinP P, const double* p1
 }
 
 // ------------------------------------------------------------ launches
-template <int DK, int DVS, bool ONLY>
+template <int DK, int DVS, bool ONLY, bool rev>
 cudaError_t launch_chain(int kid, const LinP& P, const LinOp& op, int fwd, cudaStream_t st) {
   using SH = Shape<DK, DVS, ONLY>;
-  cudaError_t e = raise_smem<lin_chain_kernel<DK, DVS, ONLY>>(SH::SMEM);
+  cudaError_t e = raise_smem<lin_chain_kernel<DK, DVS, ONLY, rev>>(SH::SMEM);
   if (e != cudaSuccess) return e;
   LinMaps m = {};
   if ((!ONLY && !encode_head_rows(&m.x, op.x, P.Ntok, P.H, DK)) || !encode_head_rows(&m.y, op.y, P.Ntok, P.H, DK) ||
@@ -971,17 +997,21 @@ cudaError_t launch_chain(int kid, const LinP& P, const LinOp& op, int fwd, cudaS
       (!ONLY && !encode_head_rows(&m.o, op.out, P.Ntok, P.H, op.DVt)))
     return cudaErrorInvalidValue;
   prof_begin(kid, st);
-  lin_chain_kernel<DK, DVS, ONLY>
+  lin_chain_kernel<DK, DVS, ONLY, rev>
       <<<(unsigned)((int64_t)P.nu * P.H * (op.DVt / DVS)), SH::NTH, SH::SMEM, st>>>(m, P, op, fwd);
   prof_end(kid, st);
   return cudaGetLastError();
 }
 
+template <bool ONLY, bool rev>
+cudaError_t launch_key(int kid, int key, const LinP& P, const LinOp& op, int fwd, cudaStream_t st) {
+  if (key == 32) return launch_chain<32, 64, ONLY, rev>(kid, P, op, fwd, st);
+  if (key == 64) return launch_chain<64, 64, ONLY, rev>(kid, P, op, fwd, st);
+  return launch_chain<128, 64, ONLY, rev>(kid, P, op, fwd, st);
+}
 template <bool ONLY>
 cudaError_t launch_bf16(int kid, int key, const LinP& P, const LinOp& op, int fwd, cudaStream_t st) {
-  if (key == 32) return launch_chain<32, 64, ONLY>(kid, P, op, fwd, st);
-  if (key == 64) return launch_chain<64, 64, ONLY>(kid, P, op, fwd, st);
-  return launch_chain<128, 64, ONLY>(kid, P, op, fwd, st);
+  return op.rev ? launch_key<ONLY, true>(kid, key, P, op, fwd, st) : launch_key<ONLY, false>(kid, key, P, op, fwd, st);
 }
 
 struct LinGrads {
