@@ -1047,7 +1047,8 @@ cudaError_t dqk(const LinP& P, const Dims& d, const LinGrads& g, const DqkOp& op
   return launch_dqk<128, 64, DA>(P, g, op, d.dk, st);
 }
 
-int value_slice(int dtype, int DVt) { return dtype == KDA_F32 || DVt == 32 ? 32 : 64; }
+// Value columns of a chain's CTA whose state has `key` key columns.
+int value_slice(int dtype, int key, int DVt) { return DVt == 32 || (dtype == KDA_F32 && key == 128) ? 32 : 64; }
 
 // ------------------------------------------------------------ plan, workspace
 struct LinLayout {
@@ -1060,7 +1061,7 @@ struct LinLayout {
 // out.  Whole rows of 2048 tokens (300M) take 77 us, two CTAs per SM 51, eight
 // 45; more pieces cost more in the fold than they give.
 void lin_plan(const kda_problem* p, const Dims& d, LinP& P) {
-  const int64_t per = (int64_t)d.H * (d.dv / value_slice(p->dtype, d.dv));
+  const int64_t per = (int64_t)d.H * (d.dv / value_slice(p->dtype, d.dk, d.dv));
   int64_t L = ((int64_t)d.Ntok * per + 8 * LIN_SMS - 1) / (8 * LIN_SMS);
   if (L < SEG_TOK) L = SEG_TOK;
   L = (L + C - 1) / C * C;
@@ -1113,7 +1114,7 @@ LinLayout lin_layout(const kda_problem* p, const Dims& d, const LinP& P, int for
       L.off_p2 = take(8 * (size_t)P.nu * d.H * (d.dk / 32));
     } else {
       L.off_R = take(P.nc * st);
-      L.off_p1 = take(8 * (size_t)dqk_groups(P) * d.H * (d.dk / value_slice(p->dtype, d.dk)));
+      L.off_p1 = take(8 * (size_t)dqk_groups(P) * d.H * (d.dk / value_slice(p->dtype, d.dv, d.dk)));
     }
   }
   L.total = o;
@@ -1212,7 +1213,7 @@ cudaError_t lin_backward(const LinP& P, const Dims& d, const LinGrads& g, const 
   if (!F) op.states = w.R;
   e = F ? launch_f32(0, K_LIN_CHAIN, d.dk, P, op, 0, st) : launch_bf16<false>(K_LIN_CHAIN, d.dk, P, op, 0, st);
   if (e != cudaSuccess) return e;
-  const int ns = d.dk / value_slice(F ? KDA_F32 : KDA_BF16, d.dk);
+  const int ns = d.dk / value_slice(F ? KDA_F32 : KDA_BF16, d.dv, d.dk);
   if constexpr (!F) {
     const DqkOp dop{g.dq, g.dk, w.S, w.R, w.p1};
     e = g.dA ? dqk<true>(P, d, g, dop, st) : dqk<false>(P, d, g, dop, st);

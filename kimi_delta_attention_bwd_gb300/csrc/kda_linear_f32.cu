@@ -2,8 +2,8 @@
 // Every operand is three bf16 parts (24 bits) and every product the six part
 // products of order 2^-16 and above, on tcgen05 (M = 64, operands in shared
 // memory, accumulators in TMEM): three parts of everything would not fit the
-// registers of the bf16 chain, and fp32 FMAs have an eighth of the rate.  A
-// CTA carries one chain of a 32-column value slice: its state in fp32
+// registers of the bf16 chain.  A CTA carries one chain of a value slice of 64
+// columns (32 where shared memory or the head has no more): its state in fp32
 // registers, warp w with rows (value columns) 16 (w % 4) .. and the key columns
 // of half w / 4.  Small part products are accumulated first: the tensor core
 // truncates what an addition shifts out.
@@ -16,7 +16,6 @@ namespace {
 
 constexpr int LTH = 256;  // threads of a chain CTA
 constexpr int NP = 3;     // bf16 parts of an operand
-constexpr int DVS = 32;   // value columns of a CTA
 
 // Eight values as three parts, stored `stride` elements apart.
 __device__ __forceinline__ void split8(const float (&v)[8], bf16* dst, int stride) {
@@ -123,7 +122,7 @@ __device__ __forceinline__ void ld_tiles(uint32_t tbase, int c0, float (&v)[NT][
   }
 }
 
-template <int DK, int DEC>
+template <int DK, int DVS, int DEC>
 struct Shape {
   static constexpr bool ONLY = DEC >= 3;  // a segment's own state: no output rows
   static constexpr int XE = ONLY ? 0 : NP * 64 * DK, YE = NP * 64 * DK, ZE = NP * 64 * DVS;
@@ -137,9 +136,9 @@ struct Shape {
   static constexpr int NTK = DK / 16;   // and of the key side
 };
 
-template <int DK, int DEC>
+template <int DK, int DVS, int DEC>
 __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
-  using SH = Shape<DK, DEC>;
+  using SH = Shape<DK, DVS, DEC>;
   constexpr int NTV = SH::NTV, NTK = SH::NTK;
   constexpr bool ONLY = SH::ONLY;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -394,21 +393,22 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
   if (warp == 0) tc::tmem_dealloc(tm, SH::TMEM);
 }
 
-template <int DK, int DEC>
-__global__ void __launch_bounds__(LTH, Shape<DK, DEC>::SMEM <= 113 * 1024 ? 2 : 1)
+template <int DK, int DVS, int DEC>
+__global__ void __launch_bounds__(LTH, Shape<DK, DVS, DEC>::SMEM <= 113 * 1024 ? 2 : 1)
     lin_f32_kernel(LinP P, LinOp op, int fwd) {
   if (!ready(P, fwd)) return;
   const int ns = op.DVt / DVS;
-  chain<DK, DEC>(P, op, blockIdx.x / (ns * P.H), (blockIdx.x / ns) % P.H, blockIdx.x % ns);
+  chain<DK, DVS, DEC>(P, op, blockIdx.x / (ns * P.H), (blockIdx.x / ns) % P.H, blockIdx.x % ns);
 }
 
-template <int DK, int DEC>
+template <int DK, int DVS, int DEC>
 cudaError_t launch(int kid, const LinP& P, const LinOp& op, int fwd, cudaStream_t st) {
-  constexpr int smem = Shape<DK, DEC>::SMEM;
-  cudaError_t e = raise_smem<lin_f32_kernel<DK, DEC>>(smem);
+  constexpr int smem = Shape<DK, DVS, DEC>::SMEM;
+  cudaError_t e = raise_smem<lin_f32_kernel<DK, DVS, DEC>>(smem);
   if (e != cudaSuccess) return e;
   prof_begin(kid, st);
-  lin_f32_kernel<DK, DEC><<<(unsigned)((int64_t)P.nu * P.H * (op.DVt / DVS)), LTH, smem, st>>>(P, op, fwd);
+  lin_f32_kernel<DK, DVS, DEC>
+      <<<(unsigned)((int64_t)P.nu * P.H * (op.DVt / DVS)), LTH, smem, st>>>(P, op, fwd);
   prof_end(kid, st);
   return cudaGetLastError();
 }
@@ -417,10 +417,13 @@ template <int DEC>
 cudaError_t by_key(int kid, int key, const LinP& P, const LinOp& op, int fwd, cudaStream_t st) {
   // (the gradients' chains have dv as their key side, the others dk)
   if constexpr (DEC != 1 && DEC != 2) {
-    if (key == 32) return launch<32, DEC>(kid, P, op, fwd, st);
+    if (key == 32) return launch<32, 64, DEC>(kid, P, op, fwd, st);
   }
-  if (key == 64) return launch<64, DEC>(kid, P, op, fwd, st);
-  return launch<128, DEC>(kid, P, op, fwd, st);
+  if constexpr (DEC != 3) {
+    if (key == 64 && op.DVt == 32) return launch<64, 32, DEC>(kid, P, op, fwd, st);
+  }
+  if (key == 64) return launch<64, 64, DEC>(kid, P, op, fwd, st);
+  return launch<128, 32, DEC>(kid, P, op, fwd, st);
 }
 
 }  // namespace
