@@ -653,6 +653,8 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
 template <int DK, int DVS, bool ONLY, bool rev>
 __global__ void __launch_bounds__(Shape<DK, DVS, ONLY>::NTH, Shape<DK, DVS, ONLY>::CTAS)
     lin_chain_kernel(const __grid_constant__ LinMaps maps, LinP P, LinOp op, int fwd) {
+  pdl_wait();
+  pdl_release();
   if (!ready(P, fwd)) return;
   const int ns = op.DVt / DVS;
   chain<DK, DVS, ONLY, rev>(P, op, maps, blockIdx.x / (ns * P.H), (blockIdx.x / ns) % P.H, blockIdx.x % ns);
@@ -713,6 +715,8 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
   uint64_t* bar = reinterpret_cast<uint64_t*>(rk + 64);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
   const int ns = DKt / DVS, slice = blockIdx.x % ns, h = (blockIdx.x / ns) % P.H, g0 = blockIdx.x / (ns * P.H) * CPB;
+  pdl_wait();
+  pdl_release();
   if (!ready(P, 0)) return;
   const int nchunks = P.rows ? P.nc : P.counts[1], nch = min(CPB, nchunks - g0);
   if (nch <= 0) {
@@ -997,10 +1001,10 @@ cudaError_t launch_chain(int kid, const LinP& P, const LinOp& op, int fwd, cudaS
       (!ONLY && !encode_head_rows(&m.o, op.out, P.Ntok, P.H, op.DVt)))
     return cudaErrorInvalidValue;
   prof_begin(kid, st);
-  lin_chain_kernel<DK, DVS, ONLY, rev>
-      <<<(unsigned)((int64_t)P.nu * P.H * (op.DVt / DVS)), SH::NTH, SH::SMEM, st>>>(m, P, op, fwd);
+  e = launch_after(op.after, lin_chain_kernel<DK, DVS, ONLY, rev>,
+                   dim3((unsigned)((int64_t)P.nu * P.H * (op.DVt / DVS))), SH::NTH, SH::SMEM, st, m, P, op, fwd);
   prof_end(kid, st);
-  return cudaGetLastError();
+  return e;
 }
 
 template <bool ONLY, bool rev>
@@ -1034,10 +1038,10 @@ cudaError_t launch_dqk(const LinP& P, const LinGrads& g, const DqkOp& op, int dk
       !encode_head_rows(&m.dq, g.dq, P.Ntok, P.H, dk) || !encode_head_rows(&m.dk, g.dk, P.Ntok, P.H, dk))
     return cudaErrorInvalidValue;
   prof_begin(K_LIN_DQK, st);
-  lin_dqk_kernel<DV, DVS, DA>
-      <<<(unsigned)(dqk_groups(P) * P.H * (dk / DVS)), SH::NTH, SH::SMEM, st>>>(m, P, op, dk);
+  e = launch_after(true, lin_dqk_kernel<DV, DVS, DA>, dim3((unsigned)(dqk_groups(P) * P.H * (dk / DVS))), SH::NTH,
+                   SH::SMEM, st, m, P, op, dk);
   prof_end(K_LIN_DQK, st);
-  return cudaGetLastError();
+  return e;
 }
 
 template <bool DA>
@@ -1158,6 +1162,7 @@ cudaError_t run_seg(const LinP& P, const Dims& d, const void* y, const void* z, 
   op.rev = rev;
   op.DVt = d.dv;
   op.segc = segc;
+  op.after = !rev && !P.rows;  // behind the table
   cudaError_t e = sizeof(T) == 4 ? launch_f32(3, K_LIN_SEG, d.dk, P, op, fwd, st)
                                  : launch_bf16<true>(K_LIN_SEG, d.dk, P, op, fwd, st);
   if (e != cudaSuccess) return e;
@@ -1191,6 +1196,7 @@ cudaError_t lin_forward(const LinP& P, const Dims& d, const void* q, const void*
   op.DVt = d.dv;
   op.segc = P.seg ? segf : nullptr;
   op.states = P.save ? S : nullptr;
+  op.after = !P.rows || P.seg;
   const int fwd = P.rows && !P.seg ? 1 : 2;
   return sizeof(T) == 4 ? launch_f32(0, K_LIN_CHAIN, d.dk, P, op, fwd, st)
                         : launch_bf16<false>(K_LIN_CHAIN, d.dk, P, op, fwd, st);
@@ -1211,6 +1217,7 @@ cudaError_t lin_backward(const LinP& P, const Dims& d, const LinGrads& g, const 
   op.x = g.k; op.y = g.q; op.z = g.dO; op.out = g.dv; op.init = g.dhf; op.fin = g.dh0; op.rev = 1; op.DVt = d.dv;
   op.segc = P.seg ? w.segr : nullptr;
   if (!F) op.states = w.R;
+  op.after = P.seg;
   e = F ? launch_f32(0, K_LIN_CHAIN, d.dk, P, op, 0, st) : launch_bf16<false>(K_LIN_CHAIN, d.dk, P, op, 0, st);
   if (e != cudaSuccess) return e;
   const int ns = d.dk / value_slice(F ? KDA_F32 : KDA_BF16, d.dv, d.dk);
@@ -1220,12 +1227,12 @@ cudaError_t lin_backward(const LinP& P, const Dims& d, const LinGrads& g, const 
   } else {
     op = LinOp{};
     op.x = g.dO; op.y = g.v; op.z = g.k; op.out = g.dq; op.init = g.h0; op.tr = 1; op.DVt = d.dk;
-    op.segc = P.seg ? w.segf : nullptr; op.wx = g.q; op.pda = w.p1;
+    op.segc = P.seg ? w.segf : nullptr; op.wx = g.q; op.pda = w.p1; op.after = 1;
     e = launch_f32(g.dA ? 1 : 0, K_LIN_CHAIN, d.dv, P, op, 0, st);
     if (e != cudaSuccess) return e;
     op = LinOp{};
     op.x = g.v; op.y = g.dO; op.z = g.q; op.out = g.dk; op.init = g.dhf; op.tr = 1; op.rev = 1; op.DVt = d.dk;
-    op.segc = P.seg ? w.segr : nullptr; op.wx = g.k; op.ent = w.S; op.pda = w.p2;
+    op.segc = P.seg ? w.segr : nullptr; op.wx = g.k; op.ent = w.S; op.pda = w.p2; op.after = 1;
     e = launch_f32(g.dA ? 2 : 0, K_LIN_CHAIN, d.dv, P, op, 0, st);
   }
   if (e != cudaSuccess || !g.dA) return e;

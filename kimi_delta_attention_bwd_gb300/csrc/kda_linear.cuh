@@ -36,6 +36,7 @@ struct LinOp {
   const float* init;  // state at the chain's start (nullptr: 0)
   float* fin;         // state at its end (nullptr: not wanted)
   int tr, rev, DVt;
+  int after;          // launched behind another kernel of the same call (programmatic dependent launch)
   float* segc;        // per unit [nu][H][key * DVt]: a segment's own state, then (lin_fold) its start state
   float* states;      // per chunk [nc][H][dv][dk]: the state where the chain enters it (nullptr: not kept)
   const void* wx;     // fp32 decay gradient: q (dq chain) or k (dk chain), laid out like z
@@ -86,6 +87,16 @@ __device__ __forceinline__ void rows_reset(const LinP& P) {
 
 __device__ __forceinline__ float decay_of(const float* A_log, int h) { return fminf(expf(A_log[h]), 1e30f); }
 __device__ __forceinline__ float decay_pow(float a, int m) { return m > 0 ? expf(-a * (float)m) : 1.0f; }
+
+// Launches k, behind another kernel of the same call as its programmatic
+// dependent (every kernel here waits for the grid before it, first thing).
+template <typename... KA, typename... A>
+inline cudaError_t launch_after(bool after, void (*k)(KA...), dim3 grid, int block, size_t smem, cudaStream_t st,
+                                A... args) {
+  if (after) return launch_pdl(k, grid, dim3(block), smem, st, args...);
+  k<<<grid, block, smem, st>>>(args...);
+  return cudaGetLastError();
+}
 
 // Whether a chain CTA has work: fwd 1 is a forward's first kernel (it resets
 // the words of equal rows), 2 a later one, 0 a backward, which needs the

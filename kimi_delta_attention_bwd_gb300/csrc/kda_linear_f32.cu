@@ -396,6 +396,8 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
 template <int DK, int DVS, int DEC>
 __global__ void __launch_bounds__(LTH, Shape<DK, DVS, DEC>::SMEM <= 113 * 1024 ? 2 : 1)
     lin_f32_kernel(LinP P, LinOp op, int fwd) {
+  pdl_wait();
+  pdl_release();
   if (!ready(P, fwd)) return;
   const int ns = op.DVt / DVS;
   chain<DK, DVS, DEC>(P, op, blockIdx.x / (ns * P.H), (blockIdx.x / ns) % P.H, blockIdx.x % ns);
@@ -407,10 +409,10 @@ cudaError_t launch(int kid, const LinP& P, const LinOp& op, int fwd, cudaStream_
   cudaError_t e = raise_smem<lin_f32_kernel<DK, DVS, DEC>>(smem);
   if (e != cudaSuccess) return e;
   prof_begin(kid, st);
-  lin_f32_kernel<DK, DVS, DEC>
-      <<<(unsigned)((int64_t)P.nu * P.H * (op.DVt / DVS)), LTH, smem, st>>>(P, op, fwd);
+  e = launch_after(op.after, lin_f32_kernel<DK, DVS, DEC>, dim3((unsigned)((int64_t)P.nu * P.H * (op.DVt / DVS))), LTH,
+                   smem, st, P, op, fwd);
   prof_end(kid, st);
-  return cudaGetLastError();
+  return e;
 }
 
 template <int DEC>
