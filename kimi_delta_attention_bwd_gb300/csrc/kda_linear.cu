@@ -202,7 +202,7 @@ struct Shape {
   static constexpr int SMEM = 1024 /* alignment */ + STG * STAGE + PB + OB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
   static constexpr int NTK = DK / 8;  // 8-key tiles of a warp's state rows
   // resident CTAs: what registers and shared memory allow
-  static constexpr int REGS = DK == 32 ? 200 : 255;
+  static constexpr int REGS = DK == 32 ? 168 : 255;
   static constexpr int BY_REG = 65536 / (NTH * REGS), BY_SMEM = 227 * 1024 / (SMEM + 1024);
   static constexpr int CTAS = BY_REG < BY_SMEM ? (BY_REG < 1 ? 1 : BY_REG) : BY_SMEM;
 };
@@ -1059,33 +1059,63 @@ struct LinLayout {
   size_t off_counts, off_units, off_ch0, off_longs, off_chunks, off_segf, off_segr, off_S, off_R, off_p1, off_p2, total;
 };
 
-// Segment length: long documents are cut into equal pieces of at most L tokens
-// (whole chunks, at least SEG_TOK tokens), L chosen so that about eight chain
-// CTAs per SM exist: two or three run at once, and uneven documents then even
-// out.  Whole rows of 2048 tokens (300M) take 77 us, two CTAs per SM 51, eight
-// 45; more pieces cost more in the fold than they give.
+// Chain CTAs that an SM holds.
+int chain_ctas(int dtype, int dk) {
+  if (dtype == KDA_F32) return dk == 32 ? 2 : 1;
+  return dk == 32 ? Shape<32, 64, false>::CTAS : dk == 64 ? Shape<64, 64, false>::CTAS : Shape<128, 64, false>::CTAS;
+}
+
+// Segment length in tokens (whole chunks, at least SEG_TOK): long documents are
+// cut into equal pieces of at most that.  `per`: CTAs of a unit, `slots`: CTAs that
+// run at once.
+// Equal rows: the number of pieces that costs least, in chunk times: waves of
+// CTAs x (chunks of a piece + a start of one and a half), the segments' own
+// states (0.45 of that over all pieces but the last) and the fold (a fortieth per
+// piece).  300M (2048 tokens, 128 chains): whole rows 77 us, 8 pieces (1024 CTAs
+// on 912 slots) 37, 7 pieces 31.
+// Packed documents, whose lengths only the device may know: N / L + n_docs / 2
+// units fill the least number of waves that holds 2.5 units per document, so
+// that the documents' last, shorter pieces do not decide (300M packed 42 us with
+// pieces of 256 tokens, 39 with 384).
+int seg_len(const Dims& d, int64_t per, int64_t slots) {
+  if (d.rows) {
+    int best = 1;
+    double least = 1e300;
+    const int most = (d.T + SEG_TOK - 1) / SEG_TOK;
+    for (int ns = 1; ns <= most && ns <= 4096; ns++) {
+      const double len = ((d.T + ns - 1) / ns + C - 1) / C;
+      auto waves = [&](int64_t units) { return (double)((units * per + slots - 1) / slots); };
+      double cost = waves((int64_t)d.B * ns) * (len + 1.5);
+      if (ns > 1) cost += 0.45 * waves((int64_t)d.B * (ns - 1)) * (len + 1.5) + ns / 40.0 + 1.0;
+      if (cost < least) { least = cost; best = ns; }
+    }
+    return ((d.T + best - 1) / best + C - 1) / C * C;
+  }
+  const int64_t want = 5 * (int64_t)d.n_docs / 2 + 1;
+  const int64_t k = (want * per + slots - 1) / slots, units = k * slots / per - d.n_docs / 2;
+  int64_t L = (d.Ntok + units - 1) / units;
+  if (L < SEG_TOK) L = SEG_TOK;
+  return (int)((L + C - 1) / C * C);
+}
 void lin_plan(const kda_problem* p, const Dims& d, LinP& P) {
   const int64_t per = (int64_t)d.H * (d.dv / value_slice(p->dtype, d.dk, d.dv));
-  int64_t L = ((int64_t)d.Ntok * per + 8 * LIN_SMS - 1) / (8 * LIN_SMS);
-  if (L < SEG_TOK) L = SEG_TOK;
-  L = (L + C - 1) / C * C;
-  if (d.rows) L = seg_tokens((int)L, d.T);
+  const int L = seg_len(d, per, (int64_t)LIN_SMS * chain_ctas(p->dtype, d.dk));
   P.Ntok = d.Ntok;
   P.H = d.H;
   P.n_docs = d.n_docs;
   P.T = d.T;
   P.rows = d.rows;
-  P.L = (int)L;
+  P.L = L;
   P.nc = d.nc_max;
   P.scale = d.scale;
   P.cu = p->cu_seqlens;
   if (P.rows) {
     P.seg = d.T > L;
-    P.nu = d.B * (int)((d.T + L - 1) / L);
+    P.nu = d.B * ((d.T + L - 1) / L);
     P.n_long = d.B;
   } else {
-    P.nu = d.n_docs + (int)(d.Ntok / L);
-    P.n_long = (int)(d.Ntok / L);
+    P.nu = d.n_docs + d.Ntok / L;
+    P.n_long = d.Ntok / L;
     P.seg = d.Ntok > L;
     if (p->cu_seqlens_host && P.seg) {
       P.seg = 0;
