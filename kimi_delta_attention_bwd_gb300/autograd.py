@@ -98,13 +98,21 @@ def gated_norm(x, g, w, eps: Optional[float] = None):
     return _GatedNorm.apply(x, g, w, eps)
 
 
+def _given(g):
+    """An incoming gradient as the library takes it: contiguous, and 16-byte
+    aligned, which a slice of a larger tensor's gradient need not be."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class _LinearAttention(torch.autograd.Function):
     @staticmethod
-    def forward(fctx, q, k, v, A_log, h0, scale, cu_seqlens, cu_seqlens_host, want_final):
+    def forward(fctx, q, k, v, A_log, h0, scale, cu_seqlens, cu_seqlens_host, want_final, recorded):
         fctx.set_materialize_grads(False)
         o, hf, lctx = kda_linear_forward(q, k, v, A_log, scale=scale, h0=h0, cu_seqlens=cu_seqlens,
                                          cu_seqlens_host=cu_seqlens_host,
-                                         save_for_backward=any(fctx.needs_input_grad), want_final_state=want_final)
+                                         save_for_backward=recorded and any(fctx.needs_input_grad),
+                                         want_final_state=want_final)
         fctx.save_for_backward(q, k, v, A_log, h0, cu_seqlens)
         fctx.rest = (lctx.problem, lctx.cu_seqlens_host, lctx.workspace, lctx.n_docs, lctx.saved)
         return (o, hf) if want_final else o
@@ -115,11 +123,11 @@ class _LinearAttention(torch.autograd.Function):
         q, k, v, A_log, h0, cu_seqlens = fctx.saved_tensors
         problem, cu_host, workspace, n_docs, saved = fctx.rest
         lctx = LinearContext(problem, q, k, v, A_log, h0, cu_seqlens, cu_host, workspace, n_docs, saved)
-        dO = torch.zeros_like(v) if dO is None else dO.contiguous()
-        g = kda_linear_backward(lctx, dO, None if dhf is None else dhf.contiguous(),
+        dO = torch.zeros_like(v) if dO is None else _given(dO)
+        g = kda_linear_backward(lctx, dO, None if dhf is None else _given(dhf),
                                 want_dA_log=fctx.needs_input_grad[3],
                                 want_dh0=h0 is not None and fctx.needs_input_grad[4])
-        return g["dq"], g["dk"], g["dv"], g["dA_log"], g["dh0"], None, None, None, None
+        return g["dq"], g["dk"], g["dv"], g["dA_log"], g["dh0"], None, None, None, None, None
 
 
 def linear_attention(q, k, v, A_log, scale: Optional[float] = None, h0=None, cu_seqlens=None, cu_seqlens_host=None,
@@ -127,13 +135,14 @@ def linear_attention(q, k, v, A_log, scale: Optional[float] = None, h0=None, cu_
     """Differentiable linear attention: o (and h_final when
     output_final_state) from the layouts of kda_linear_forward; gradients to q,
     k, v, A_log and h0 through kda_linear_backward."""
-    return _LinearAttention.apply(q, k, v, A_log, h0, scale, cu_seqlens, cu_seqlens_host, output_final_state)
+    return _LinearAttention.apply(q, k, v, A_log, h0, scale, cu_seqlens, cu_seqlens_host, output_final_state,
+                                  torch.is_grad_enabled())
 
 
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
-    def forward(fctx, x, w, bias, eps):
-        if not any(fctx.needs_input_grad):
+    def forward(fctx, x, w, bias, eps, recorded):
+        if not (recorded and any(fctx.needs_input_grad)):
             return kda_layer_norm(x, w, bias, eps)
         y, mean, rstd = kda_layer_norm(x, w, bias, eps, return_stats=True)
         fctx.save_for_backward(x, w, mean, rstd)
@@ -144,10 +153,10 @@ class _LayerNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(fctx, dy):
         x, w, mean, rstd = fctx.saved_tensors
-        dx, dw, db = kda_layer_norm_backward(x, w, dy.contiguous(), mean, rstd, want_dbias=fctx.has_bias)
-        return dx, dw, db, None
+        dx, dw, db = kda_layer_norm_backward(x, w, _given(dy), mean, rstd, want_dbias=fctx.has_bias)
+        return dx, dw, db, None, None
 
 
 def layer_norm(x, w, bias=None, eps: Optional[float] = None):
     """Differentiable layer norm over the last axis (kda_layer_norm)."""
-    return _LayerNorm.apply(x, w, bias, eps)
+    return _LayerNorm.apply(x, w, bias, eps, torch.is_grad_enabled())

@@ -43,7 +43,7 @@ kda_status check_problem(const kda_problem* p, Dims* d);
 namespace lin {
 namespace {
 
-constexpr int LIN_SMS = 152;  // SMs of a GB300: the segment rule's denominator
+constexpr int LIN_SMS = 152;  // SMs of a GB300, for the segment rule
 constexpr int SEG_TOK = 256;  // shortest segment (tokens)
 
 // Inclusive scan of x over the 1024-thread block; the block's sum in *total.
@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(1024) lin_table_kernel(LinP P) {
   for (int base = 0; base < n; base += 1024) {
     const int i = base + tid;
     const int t0 = i < n ? P.cu[i] : 0, len = i < n ? P.cu[i + 1] - t0 : 0;
-    const int L = seg_tokens(P.L, len);
+    // (no document is cut without the kernels that form the pieces' states, whatever the host's offsets said)
+    const int L = P.seg ? seg_tokens(P.L, len) : max(len, 1);
     const int ns = i < n ? max(1, (len + L - 1) / L) : 0, nc = (len + C - 1) / C;
     int all;
     const int u0 = units + block_scan(ns, s_w, &all) - ns;
@@ -122,8 +123,8 @@ __global__ void __launch_bounds__(1024) lin_table_kernel(LinP P) {
   }
 }
 
-// Turns the segments' own states into their start states, in the chain's
-// direction: start_0 = init, start_{s+1} = e^{-a len_s} start_s + own_s.  A
+// Turns the segments' own states into their start states, in place and in the
+// chain's direction: start_0 = init, start_{s+1} = e^{-a len_s} start_s + own_s.  A
 // thread per four elements of a (split document, head)'s state, eight segments'
 // loads in flight; the CTAs loop over the pieces, whose number the device alone
 // may know (a grid of its bound, mostly empty, took 36 to 62 us).
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(FTH) lin_fold_kernel(LinP P, float* segc, cons
 #pragma unroll
     for (int e = 0; e < F; e++)
       if (e < ns - 1) v[e] = *own(e);
+    *own(0) = st;
     for (int k = 0; k < ns - 1; k += F) {
       // (start k + F goes where own state k + F was: the next F are read first)
 #pragma unroll
@@ -780,6 +782,8 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
     zero_rows<SH::STAGE, 2 * SH::OB, 128, DVS == 32 ? 64 : 128, NTH>(stg, n);
     if (__syncthreads_or(!good)) {
       good = false;
+      // the other stage's copy may be under way
+      if (SH::STG == 2 && tid == 0 && c + 1 < nch) mma::mbar_wait(bar + ((c + 1) & 1), ((c + 1) >> 1) & 1);
       break;
     }
 
@@ -1083,7 +1087,7 @@ int seg_len(const Dims& d, int64_t per, int64_t slots) {
     double least = 1e300;
     const int most = (d.T + SEG_TOK - 1) / SEG_TOK;
     for (int ns = 1; ns <= most && ns <= 4096; ns++) {
-      const double len = ((d.T + ns - 1) / ns + C - 1) / C;
+      const double len = (double)((((int64_t)d.T + ns - 1) / ns + C - 1) / C);
       auto waves = [&](int64_t units) { return (double)((units * per + slots - 1) / slots); };
       double cost = waves((int64_t)d.B * ns) * (len + 1.5);
       if (ns > 1) cost += 0.45 * waves((int64_t)d.B * (ns - 1)) * (len + 1.5) + ns / 40.0 + 1.0;

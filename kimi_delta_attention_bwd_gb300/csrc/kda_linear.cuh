@@ -107,7 +107,8 @@ __device__ __forceinline__ bool ready(const LinP& P, int fwd) {
     return true;
   }
   if (fwd == 2) return *P.err == KDA_OK;
-  if (*P.wtag != P.tag) {
+  // (a forward that cut documents, and a backward whose host offsets hold none to cut)
+  if (*P.wtag != P.tag || (!P.rows && !P.seg && P.counts[2] > 0)) {
     if (threadIdx.x == 0) *P.err = KDA_ERR_WORKSPACE;
     return false;
   }
@@ -134,14 +135,15 @@ __device__ __forceinline__ Rows rows_of(const Unit& un, int rev, int c) {
   return r;
 }
 
-// The state at a unit's start.  each(fn) calls fn(s, at) for every state
+// The state at a unit's start (of a document in pieces always from segc: its
+// last piece may already have written an h_final that is h0).  each(fn) calls fn(s, at) for every state
 // element a thread holds.
 template <class EACH>
 __device__ __forceinline__ void start_state(const LinP& P, const LinOp& op, const Unit& un, int u, int h, int64_t stN,
                                             EACH each) {
   const float *p = nullptr;
   float w = 1.0f;
-  if (op.segc && un.seg != (op.rev ? un.nseg - 1 : 0)) {
+  if (op.segc && un.nseg > 1) {
     p = op.segc + ((int64_t)u * P.H + h) * stN;
   } else if (op.init) {
     p = op.init + ((int64_t)un.doc * P.H + h) * stN;

@@ -60,7 +60,9 @@ def kda_linear_forward(q, k, v, A_log, scale: Optional[float] = None, h0=None, c
                        final_state: Optional[torch.Tensor] = None):
     """Forward pass.  Returns (o, h_final or None, ctx); ctx feeds
     kda_linear_backward when save_for_backward is set.  scale: 1/sqrt(dk)
-    unless given (> 0).  out / final_state: optional preallocated outputs."""
+    unless given (> 0).  out / final_state: optional preallocated outputs;
+    final_state may be h0 (states updated in place) unless the call saves for
+    the backward, which reads h0."""
     _dims(q, "q", 4)
     _dims(v, "v", 4)
     B, T, H, dk = q.shape
@@ -80,6 +82,8 @@ def kda_linear_forward(q, k, v, A_log, scale: Optional[float] = None, h0=None, c
         _require(q=(q, q.shape, io), k=(k, q.shape, io), v=(v, (B, T, H, dv), io), A_log=(A_log, (H,), f32),
                  h0=(h0, states, f32), out=(out, (B, T, H, dv), io), final_state=(final_state, states, f32),
                  cu_seqlens=(cu_seqlens, (n_docs + 1,), torch.int32))
+    if save_for_backward and h0 is not None and final_state is not None and h0.data_ptr() == final_state.data_ptr():
+        raise ValueError("final_state cannot be h0 when the call saves for the backward")
     prob = _lib.make_problem(B, T, H, dk, dv, io, scale, cu_seqlens, cu_seqlens_host)
     if workspace is None:
         # (size 0 for a problem that the call below refuses with its own status)

@@ -332,6 +332,113 @@ def test_layer_norm_linear_attention_layer_norm():
         assert e <= 12 * 2.0 ** -8, float(e)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_states_updated_in_place(dt):
+    # h_final in h0's place, the long document in pieces that may end in any order
+    x = make(30, [1500, 20, 0], 2, 64, 64, dt)
+    ref = run(x, backward=False)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    for _ in range(5):
+        st = d["h0"].clone()
+        o, hf, _ = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=st, final_state=st,
+                                          cu_seqlens=d["cu"], save_for_backward=False)
+        assert hf is st and torch.equal(o, ref["o"]) and torch.equal(st, ref["h_final"])
+    with pytest.raises(ValueError, match="final_state"):
+        kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=st, final_state=st, cu_seqlens=d["cu"])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_graph_replayed_on_other_offsets(dt):
+    # captured with documents that need no cut, replayed with one that elsewhere would be cut
+    x, y = make(31, [200] * 5, 2, 32, 64, dt), make(31, [0, 960, 10, 30, 0], 2, 32, 64, dt)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    run(x)
+
+    def step():
+        o, hf, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=d["h0"], cu_seqlens=d["cu"],
+                                            cu_seqlens_host=x["cu"])
+        return dict(o=o, h_final=hf, **kda.kda_linear_backward(ctx, d["dO"], d["dh"]))
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for z in (y, x):
+        for n in ("q", "k", "v", "A_log", "h0", "cu", "dO", "dh"):
+            d[n].copy_(z[n])
+        g.replay()
+        torch.cuda.synchronize()
+        check(got, oracle(z), dt)
+
+
+def test_two_calls_at_once():
+    # one problem, two streams, a workspace each
+    x = make(32, [700, 1, 64, 0, 35], 2, 128, 128, "bf16")
+    ref = run(x)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            o, hf, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=d["h0"], cu_seqlens=d["cu"])
+            got.append(dict(o=o, h_final=hf, **kda.kda_linear_backward(ctx, d["dO"], d["dh"])))
+    torch.cuda.synchronize()
+    for a in got:
+        for n in ref:
+            assert torch.equal(a[n], ref[n]), n
+
+
+def test_a_training_step_captured_into_a_graph():
+    x = make(33, [90, 300], 2, 64, 64, "bf16")
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    w = torch.linspace(0.5, 1.5, 64, device="cuda")
+
+    def step():
+        leaves = [d[n].detach().requires_grad_() for n in ("q", "k", "v", "A_log", "h0")] + [w.detach().requires_grad_()]
+        o, hf = kda.linear_attention(*leaves[:4], h0=leaves[4], cu_seqlens=d["cu"], cu_seqlens_host=x["cu"],
+                                     output_final_state=True)
+        y = kda.layer_norm(o, leaves[5])
+        return torch.autograd.grad([y, hf], leaves, [d["dO"], d["dh"]])
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        ref = [t.clone() for t in step()]
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)
+
+
+def test_gradients_that_arrive_unaligned():
+    # slices of a larger gradient, and nothing saved where nothing is recorded
+    x = make(34, [70], 1, 32, 64, "bf16", rows=True)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"])[2]
+    ref = kda.kda_linear_backward(ctx, d["dO"], d["dh"], want_dA_log=False)
+    q = d["q"].clone().requires_grad_()
+    o, hf = kda.linear_attention(q, d["k"], d["v"], d["A_log"], output_final_state=True)
+    buf, hbuf = torch.empty(1 + o.numel(), dtype=o.dtype, device="cuda"), torch.empty(1 + hf.numel(), device="cuda")
+    dO, dh = buf[1:].view_as(o).copy_(d["dO"]), hbuf[1:].view_as(hf).copy_(d["dh"])
+    gq, = torch.autograd.grad([o, hf], [q], [dO, dh])
+    assert torch.equal(gq, ref["dq"])
+    y = kda.layer_norm(q, torch.ones(32, device="cuda"))
+    gy = torch.empty(1 + y.numel(), dtype=y.dtype, device="cuda")[1:].view_as(y).copy_(d["k"])
+    assert bool(torch.isfinite(torch.autograd.grad(y, [q], gy)[0]).all())
+    with torch.no_grad():
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        kda.linear_attention(q, d["k"], d["v"], d["A_log"])
+        ws = torch.cuda.max_memory_allocated() - before - 2 * d["v"].numel()
+    prob = _lib.make_problem(1, 70, 1, 32, 64, torch.bfloat16, None, None, None)
+    assert ws < _lib.kda_linear_workspace_size(prob, True)
+
+
 def test_python_refusals_on_the_device():
     x = make(24, [40], 2, 32, 64, "bf16", rows=True)
     d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
