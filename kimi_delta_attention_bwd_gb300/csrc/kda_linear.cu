@@ -471,17 +471,18 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
     const int st = SH::STG == 2 ? c & 1 : 0;
     unsigned char* stg = smem + st * SH::STAGE;
     const uint32_t tX = mma::smem_u32(stg), tY = tX + SH::XB, tZ = tY + SH::YB;
-    if (!ONLY && op.states) {  // the state where the chain enters the chunk, [dv][dk]
-      float* p = op.states + ((int64_t)(un.ch0 + idx) * H + h) * stN + (int64_t)(c0 + r0 + gq) * DK + 2 * tq;
+    if (!ONLY && op.states) {
+      // the state where the chain enters the chunk, tiles of 16 values x 8 keys in the accumulators' order
+      // (512 bytes a store; as rows, 32-byte pieces, the two chains took 614 us for 569 and lin_dqk's loads
+      // 521 for 483 at 128/128)
+      float* p = op.states + ((int64_t)(un.ch0 + idx) * H + h) * stN + (int64_t)(c0 + r0) * DK + 4 * lane;
       const float w = rev ? P.scale : 1.0f;
 #pragma unroll
       for (int m = 0; m < MT; m++)
 #pragma unroll
         for (int j = 0; j < NTK; j++)
-#pragma unroll
-          for (int k = 0; k < 2; k++)
-            *reinterpret_cast<float2*>(p + (16 * m + 8 * k) * DK + 8 * j) =
-                make_float2(w * S[m][j][2 * k], w * S[m][j][2 * k + 1]);
+          *reinterpret_cast<float4*>(p + 16 * m * DK + 128 * j) =
+              make_float4(w * S[m][j][0], w * S[m][j][1], w * S[m][j][2], w * S[m][j][3]);
       if (!rev && h == 0 && slice == 0 && tid == 0) P.chunks[un.ch0 + idx] = make_int2(t0, n);
     }
     good = mma::mbar_wait(bar + st, (SH::STG == 2 ? c >> 1 : c) & 1);
@@ -664,7 +665,7 @@ __global__ void __launch_bounds__(Shape<DK, DVS, ONLY>::NTH, Shape<DK, DVS, ONLY
 
 // ------------------------------------------------------------ dq and dk, bf16
 // Every chunk by itself, from its entry state S and its exit state's gradient
-// R (fp32, [dv][dk]): with P = scale e^{-a(i-j)} (dO_i . v_j), i >= j,
+// R (fp32): with P = scale e^{-a(i-j)} (dO_i . v_j), i >= j,
 //   dq_i = sum_j P_ij k_j + scale e^{-a(i+1)} S dO_i
 //   dk_j = sum_i P_ij q_i + e^{-a(n-1-j)} R v_j
 // and, with DA, the decay gradient's A, B, C, D.  A CTA takes CPB chunks of a
@@ -852,24 +853,31 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
     float dq[8][4], dk[8][4];
     mma::zero<8>(dq);
     mma::zero<8>(dk);
-    const int64_t sat = ((int64_t)(g0 + c) * H + h) * DV * DKt + c0 + 16 * warp + gq;
+    const int64_t sat = ((int64_t)(g0 + c) * H + h) * DV * DKt + 16 * (c0 + 16 * warp) + 32 * tq + 4 * (gq >> 1) + (gq & 1);
     const float *pS = op.S + sat, *pR = op.R + sat;
     float dot = 0.f;
 #pragma unroll (DA ? 2 : DV / 16)  // (the instruction caches again)
     for (int kk = 0; kk < DV / 16; kk++) {
       uint32_t fs[SP][4], fr[SP][4];
 #pragma unroll
-      for (int q = 0; q < 4; q++) {  // rows (dk) gq + 8 (q & 1), columns (dv) 16 kk + 8 (q >> 1) + 2 tq, + 1
-        const int64_t at = (int64_t)(16 * kk + 8 * (q >> 1) + 2 * tq) * DKt + 8 * (q & 1);
-        const float s0 = __ldg(pS + at), s1 = __ldg(pS + at + DKt), r0 = __ldg(pR + at), r1 = __ldg(pR + at + DKt);
-        if constexpr (DA) dot = fmaf(s0, r0, fmaf(s1, r1, dot));
-        uint32_t w[SP];
-        split2<SP>(s0, s1, w);
+      for (int k = 0; k < 2; k++) {  // rows (dk) gq + 8 k: columns (dv) 16 kk + 2 tq, + 1 and those 8 further
+        // (four single words: as float4 with a select 574 us, as pairs side by side 488, so 483)
+        const float* at = pS + 16 * kk * DKt + 128 * k;
+        const float* ar = pR + 16 * kk * DKt + 128 * k;
+        const float sx[4] = {__ldg(at), __ldg(at + 16), __ldg(at + 2), __ldg(at + 18)};
+        const float rx[4] = {__ldg(ar), __ldg(ar + 16), __ldg(ar + 2), __ldg(ar + 18)};
 #pragma unroll
-        for (int b = 0; b < SP; b++) fs[b][q] = w[b];
-        split2<SP>(r0, r1, w);
+        for (int g = 0; g < 2; g++) {
+          const int q = k + 2 * g;
+          if constexpr (DA) dot = fmaf(sx[2 * g], rx[2 * g], fmaf(sx[2 * g + 1], rx[2 * g + 1], dot));
+          uint32_t w[SP];
+          split2<SP>(sx[2 * g], sx[2 * g + 1], w);
 #pragma unroll
-        for (int b = 0; b < SP; b++) fr[b][q] = w[b];
+          for (int b = 0; b < SP; b++) fs[b][q] = w[b];
+          split2<SP>(rx[2 * g], rx[2 * g + 1], w);
+#pragma unroll
+          for (int b = 0; b < SP; b++) fr[b][q] = w[b];
+        }
       }
       uint32_t fo[4][4], fv[4][4];
 #pragma unroll
