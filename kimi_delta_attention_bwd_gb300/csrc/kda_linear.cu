@@ -472,17 +472,20 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
     unsigned char* stg = smem + st * SH::STAGE;
     const uint32_t tX = mma::smem_u32(stg), tY = tX + SH::XB, tZ = tY + SH::YB;
     if (!ONLY && op.states) {
-      // the state where the chain enters the chunk, tiles of 16 values x 8 keys in the accumulators' order
-      // (512 bytes a store; as rows, 32-byte pieces, the two chains took 614 us for 569 and lin_dqk's loads
-      // 521 for 483 at 128/128)
-      float* p = op.states + ((int64_t)(un.ch0 + idx) * H + h) * stN + (int64_t)(c0 + r0) * DK + 4 * lane;
+      // the state where the chain enters the chunk, in tiles of 16 values x 8 keys [value / 8][value % 2]
+      // [value % 8 / 2][key]: a word of lin_dqk's operand fragments is 128 bytes of a tile, a pair stored here
+      // fills whole sectors (128/128, the two chains and lin_dqk: [dv][dk] 614 + 521 us, the accumulators'
+      // own order 569 + 483, this 560 + 484)
+      float* p = op.states + ((int64_t)(un.ch0 + idx) * H + h) * stN + (int64_t)(c0 + r0) * DK + 32 * (gq & 1) + 8 * (gq >> 1) + 2 * tq;
       const float w = rev ? P.scale : 1.0f;
 #pragma unroll
       for (int m = 0; m < MT; m++)
 #pragma unroll
         for (int j = 0; j < NTK; j++)
-          *reinterpret_cast<float4*>(p + 16 * m * DK + 128 * j) =
-              make_float4(w * S[m][j][0], w * S[m][j][1], w * S[m][j][2], w * S[m][j][3]);
+#pragma unroll
+          for (int k = 0; k < 2; k++)
+            *reinterpret_cast<float2*>(p + 16 * m * DK + 128 * j + 64 * k) =
+                make_float2(w * S[m][j][2 * k], w * S[m][j][2 * k + 1]);
       if (!rev && h == 0 && slice == 0 && tid == 0) P.chunks[un.ch0 + idx] = make_int2(t0, n);
     }
     good = mma::mbar_wait(bar + st, (SH::STG == 2 ? c >> 1 : c) & 1);
@@ -853,7 +856,7 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
     float dq[8][4], dk[8][4];
     mma::zero<8>(dq);
     mma::zero<8>(dk);
-    const int64_t sat = ((int64_t)(g0 + c) * H + h) * DV * DKt + 16 * (c0 + 16 * warp) + 32 * tq + 4 * (gq >> 1) + (gq & 1);
+    const int64_t sat = ((int64_t)(g0 + c) * H + h) * DV * DKt + 16 * (c0 + 16 * warp) + 8 * tq + gq;
     const float *pS = op.S + sat, *pR = op.R + sat;
     float dot = 0.f;
 #pragma unroll (DA ? 2 : DV / 16)  // (the instruction caches again)
@@ -861,11 +864,10 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
       uint32_t fs[SP][4], fr[SP][4];
 #pragma unroll
       for (int k = 0; k < 2; k++) {  // rows (dk) gq + 8 k: columns (dv) 16 kk + 2 tq, + 1 and those 8 further
-        // (four single words: as float4 with a select 574 us, as pairs side by side 488, so 483)
         const float* at = pS + 16 * kk * DKt + 128 * k;
         const float* ar = pR + 16 * kk * DKt + 128 * k;
-        const float sx[4] = {__ldg(at), __ldg(at + 16), __ldg(at + 2), __ldg(at + 18)};
-        const float rx[4] = {__ldg(ar), __ldg(ar + 16), __ldg(ar + 2), __ldg(ar + 18)};
+        const float sx[4] = {__ldg(at), __ldg(at + 32), __ldg(at + 64), __ldg(at + 96)};
+        const float rx[4] = {__ldg(ar), __ldg(ar + 32), __ldg(ar + 64), __ldg(ar + 96)};
 #pragma unroll
         for (int g = 0; g < 2; g++) {
           const int q = k + 2 * g;

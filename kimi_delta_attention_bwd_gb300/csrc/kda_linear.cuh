@@ -39,7 +39,7 @@ struct LinOp {
   int after;          // launched behind another kernel of the same call (programmatic dependent launch)
   float* segc;        // per unit [nu][H][key * DVt]: a segment's own state, then (lin_fold) its start state
   float* states;      // per chunk [nc][H][dv dk]: the state where the chain enters it (fp32 io: [dv][dk];
-                      // bf16: fragments, see chain); nullptr: not kept
+                      // bf16: tiles, see chain); nullptr: not kept
   const void* wx;     // fp32 decay gradient: q (dq chain) or k (dk chain), laid out like z
   const float* ent;   // fp32 decay gradient, dk chain: the forward's states
   double* pda;        // fp32 decay gradient: per CTA partial
