@@ -737,23 +737,41 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
     const int cpr = (P.T + C - 1) / C, r = g / cpr, i = g % cpr;
     return make_int2(r * P.T + i * C, min(C, P.T - i * C));
   };
-  auto load = [&](int c) {  // one thread
+  // A chunk's tiles, by one thread.  One stage: dO and v on barrier 0, q and k on 1, as each pair's place
+  // is free; two stages: both pairs on the stage's barrier.
+  auto load_ov = [&](int c) {
     const int t0 = chunk(c).x, s = SH::STG == 2 ? c & 1 : 0;
     unsigned char* p = smem + s * SH::STAGE;
-    mma::mbar_expect_tx(bar + s, SH::STAGE);
+    mma::mbar_expect_tx(bar + s, SH::STG == 2 ? SH::STAGE : 2 * SH::OB);
 #pragma unroll
     for (int b = 0; b < (DV + 63) / 64; b++) {
       mma::tma_load_2d(p + 8192 * b, &maps.dO, h * DV + 64 * b, t0, bar + s);
       mma::tma_load_2d(p + SH::OB + 8192 * b, &maps.v, h * DV + 64 * b, t0, bar + s);
     }
-    mma::tma_load_2d(p + 2 * SH::OB, &maps.q, h * DKt + c0, t0, bar + s);
-    mma::tma_load_2d(p + 2 * SH::OB + SH::QB, &maps.k, h * DKt + c0, t0, bar + s);
+  };
+  auto load_qk = [&](int c) {
+    const int t0 = chunk(c).x, s = SH::STG == 2 ? c & 1 : 1;
+    unsigned char* p = smem + (SH::STG == 2 ? s * SH::STAGE : 0) + 2 * SH::OB;
+    if (SH::STG == 1) mma::mbar_expect_tx(bar + 1, 2 * SH::QB);
+    mma::tma_load_2d(p, &maps.q, h * DKt + c0, t0, bar + s);
+    mma::tma_load_2d(p + SH::QB, &maps.k, h * DKt + c0, t0, bar + s);
   };
   if (tid == 0) {
-    for (int s = 0; s < SH::STG; s++) mma::mbar_init(bar + s, 1);
+    for (int s = 0; s < 2; s++) mma::mbar_init(bar + s, 1);
     mma::mbar_init_fence();
-    for (int s = 0; s < SH::STG && s < nch; s++) load(s);
+    for (int s = 0; s < SH::STG && s < nch; s++) {
+      load_ov(s);
+      load_qk(s);
+    }
   }
+  // the states of a chunk on their way to L2 a chunk ahead: 78 -> 74 us at 32/64 (300M); with one stage,
+  // where the SM's three CTAs cover the latency, 484 -> 494 at 128/128
+  auto warm = [&](int c) {
+    if (SH::STG == 2 && c < nch && tid < 2 * DV / 16)
+      mma::bulk_prefetch_l2((tid & 1 ? op.R : op.S) + (((int64_t)(g0 + c) * H + h) * DV + 16 * (tid >> 1)) * DKt + 16 * c0,
+                            64 * DVS);
+  };
+  warm(0);
   for (int i = tid; i < 65; i += NTH) tab[i] = decay_pow(a, i);
   __syncthreads();
   for (int i = tid; i < 128; i += NTH) {
@@ -777,7 +795,9 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
     const int t0 = ck.x, n = ck.y, st = SH::STG == 2 ? c & 1 : 0;
     unsigned char* stg = smem + st * SH::STAGE;
     const uint32_t tO = mma::smem_u32(stg), tV = tO + SH::OB, tQ = tV + SH::OB, tK = tQ + SH::QB;
+    warm(c + 1);
     good = mma::mbar_wait(bar + st, (SH::STG == 2 ? c >> 1 : c) & 1);
+    if (SH::STG == 1) good &= mma::mbar_wait(bar + 1, c & 1);
     if (n != n_w) {
       if (n_w >= 0) __syncthreads();
       for (int i = tid; i < C; i += NTH) rk[i] = i < n ? tab[n - 1 - i] : 0.f;
@@ -919,7 +939,9 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
       }
     }
     if constexpr (DA) dacc += (double)part + (double)(dot * (float)n * tab[n]);
+    if (SH::STG == 1) mma::fence_async_smem();
     __syncthreads();  // the pairs of every warp; dO and v have been read
+    if (SH::STG == 1 && tid == 0 && c + 1 < nch) load_ov(c + 1);
     // ---- dq^T += k^T P^T, dk^T += q^T P
 #pragma unroll
     for (int kk = 0; kk < 4; kk++) {
@@ -959,7 +981,8 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
       }
       if (c + SH::STG < nch) {  // the next chunk of this stage
         mma::bulk_wait_read();
-        load(c + SH::STG);
+        if (SH::STG == 2) load_ov(c + 2);
+        load_qk(c + SH::STG);
       }
     }
   }
