@@ -390,13 +390,16 @@ KDA_API kda_status kda_short_conv_bwd(int64_t n_tok, int C, int dtype, int activ
  * document's other tokens, up to 63 before it (never another document's).
  * The workspace (kda_linear_workspace_size(p, for_backward) bytes, 256-byte
  * aligned) holds the error word (kda_device_status), the table of the packed
- * documents' units and the states of a long document's segments; with
- * save_for_backward = 1 it must be passed to kda_linear_bwd unmodified, with
- * the same inputs.  Documents longer than about the tokens that one of two
- * chains per SM would get are cut into segments whose states are formed in
- * parallel and folded onto h0 (the segment length depends on B * T, H, dv and
- * the dtype: a document's last bits can differ between batches of other
- * sizes). */
+ * documents' units, the states of a long document's segments and, with
+ * save_for_backward = 1, every 64-token chunk's states (4 dk dv bytes per chunk
+ * and head, twice that for bf16); it must then be passed to kda_linear_bwd
+ * unmodified, with the same inputs.  Long documents are cut into equal segments
+ * of at least 256 tokens whose states are formed in parallel and folded onto h0
+ * (their length depends on B, T, H, dk, dv, n_docs and the dtype: a document's
+ * last bits can differ between batches of other sizes).  With cu_seqlens_host
+ * and no document to cut, none is cut in a replay on other offsets either.
+ * Outputs must not overlap inputs, but for h_final, which may be h0 where
+ * nothing is saved. */
 KDA_API size_t kda_linear_workspace_size(const kda_problem* p, int for_backward);
 KDA_API kda_status kda_linear_fwd(const kda_problem* p, const void* q, const void* k, const void* v,
                    const float* A_log, const float* h0, void* o, float* h_final,

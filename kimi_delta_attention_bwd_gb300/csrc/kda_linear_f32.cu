@@ -7,6 +7,12 @@
 // registers, warp w with rows (value columns) 16 (w % 4) .. and the key columns
 // of half w / 4.  Small part products are accumulated first: the tensor core
 // truncates what an addition shifts out.
+// Bound by the chunk's chain of dependent steps (loads and splits, pairs, their
+// product), at one CTA per SM in most shapes: so the entry state's rows and the
+// state's product run while the pairs are weighted, and the next chunk's tiles
+// are under way to registers meanwhile (4 x 1001 tokens, H 8, 64/64, forward and
+// backward: 196 us with every product waited for and tiles loaded between, 153
+// so).
 #include "kda_linear.cuh"
 #include "kda_tc.cuh"
 
@@ -32,55 +38,46 @@ __device__ __forceinline__ void put2(float x0, float x1, bf16* dst, int stride) 
 #pragma unroll
   for (int p = 0; p < NP; p++) *reinterpret_cast<uint32_t*>(dst + p * stride) = w[p];
 }
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int e = 0; e < 4; e++) {
-    v[2 * e] = __uint_as_float(w[e] << 16);
-    v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-  }
-}
-
-// Loads a 64 x W tile (columns c0 .. of a head's D) as three parts in
-// core-matrix order: the group of eight columns idx lands at element 8 idx, so
-// eight lanes fill one 128-byte core matrix.
+// A 64 x W tile (columns c0 .. of a head's D) on its way: loaded into registers
+// at once, later put as three parts in core-matrix order: the group of eight
+// columns idx lands at element 8 idx, so eight lanes fill one 128-byte core
+// matrix.
 template <int W>
-__device__ __forceinline__ void load_tile(bf16* dst, const float* g, const Rows& r, int H, int h, int D, int c0) {
-  for (int idx = threadIdx.x; idx < 8 * W; idx += LTH) {
-    const int row = (idx & 7) + 8 * (idx / W), cg = (idx >> 3) % (W / 8);
-    float v[8];
-    if (row < r.n) {
-      const float4* p = reinterpret_cast<const float4*>(g + ((r.t0 + (int64_t)r.dir * row) * H + h) * D + c0 + 8 * cg);
+struct Tile {
+  static constexpr int IT = 8 * W / LTH;
+  float v[IT][8];
+  static __device__ __forceinline__ int row(int t) {
+    const int idx = threadIdx.x + t * LTH;
+    return (idx & 7) + 8 * (idx / W);
+  }
+  __device__ __forceinline__ void load(const float* g, const Rows& r, int H, int h, int D, int c0) {
+#pragma unroll
+    for (int t = 0; t < IT; t++) {
+      const int cg = ((threadIdx.x + t * LTH) >> 3) % (W / 8);
+      const bool in = row(t) < r.n;
+      const float4* p =
+          reinterpret_cast<const float4*>(g + ((r.t0 + (int64_t)r.dir * (in ? row(t) : 0)) * H + h) * D + c0 + 8 * cg);
       const float4 f0 = __ldg(p), f1 = __ldg(p + 1);
-      v[0] = f0.x; v[1] = f0.y; v[2] = f0.z; v[3] = f0.w;
-      v[4] = f1.x; v[5] = f1.y; v[6] = f1.z; v[7] = f1.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; e++) v[e] = 0.f;
+      v[t][0] = in ? f0.x : 0.f; v[t][1] = in ? f0.y : 0.f; v[t][2] = in ? f0.z : 0.f; v[t][3] = in ? f0.w : 0.f;
+      v[t][4] = in ? f1.x : 0.f; v[t][5] = in ? f1.y : 0.f; v[t][6] = in ? f1.z : 0.f; v[t][7] = in ? f1.w : 0.f;
     }
-    split8(v, dst + 8 * idx, 64 * W);
   }
-}
-
-// sc = the 64 x W tile `raw` with row i times sw[i]; each thread scales the groups
-// that it loaded itself (load_tile's mapping), so it needs no barrier between.
-template <int W>
-__device__ __forceinline__ void scale_tile(bf16* sc, const bf16* raw, const float* sw) {
-  for (int idx = threadIdx.x; idx < 8 * W; idx += LTH) {
-    const float w = sw[(idx & 7) + 8 * (idx / W)];
-    float v[8], u[8];
-    unpack8(*reinterpret_cast<const uint4*>(raw + 8 * idx), v);
+  __device__ __forceinline__ void put(bf16* dst) const {
 #pragma unroll
-    for (int p = 1; p < NP; p++) {
-      unpack8(*reinterpret_cast<const uint4*>(raw + p * 64 * W + 8 * idx), u);
+    for (int t = 0; t < IT; t++) split8(v[t], dst + 8 * (threadIdx.x + t * LTH), 64 * W);
+  }
+  template <class F>
+  __device__ __forceinline__ void put_weighted(bf16* dst, int n, F w) const {  // row i times w(i)
 #pragma unroll
-      for (int e = 0; e < 8; e++) v[e] += u[e];
+    for (int t = 0; t < IT; t++) {
+      const float m = row(t) < n ? w(row(t)) : 0.f;
+      float u[8];
+#pragma unroll
+      for (int e = 0; e < 8; e++) u[e] = m * v[t][e];
+      split8(u, dst + 8 * (threadIdx.x + t * LTH), 64 * W);
     }
-#pragma unroll
-    for (int e = 0; e < 8; e++) v[e] *= w;
-    split8(v, sc + 8 * idx, 64 * W);
   }
-}
+};
 
 // D = A B over ksteps x 16, A's and B's parts sa and sb elements apart: the
 // products of parts i, j with i + j <= 2, the smallest first.  One thread issues.
@@ -125,13 +122,15 @@ __device__ __forceinline__ void ld_tiles(uint32_t tbase, int c0, float (&v)[NT][
 template <int DK, int DVS, int DEC>
 struct Shape {
   static constexpr bool ONLY = DEC >= 3;  // a segment's own state: no output rows
-  static constexpr int XE = ONLY ? 0 : NP * 64 * DK, YE = NP * 64 * DK, ZE = NP * 64 * DVS;
-  static constexpr int SE = ONLY ? 0 : NP * DVS * DK, SCE = ZE, PE = ONLY ? 0 : NP * 64 * 64;
+  static constexpr int XE = ONLY ? 0 : NP * 64 * DK, YE = NP * 64 * DK, ZE = ONLY ? 0 : NP * 64 * DVS;
+  static constexpr int SE = ONLY ? 0 : NP * DVS * DK, SCE = NP * 64 * DVS, PE = ONLY ? 0 : NP * 64 * 64;
   static constexpr int QE = DEC == 1 ? ZE : 0;
   // 512 bytes after the tiles: an M = 64 view of a 32-column tile reads up to four cores past it
   static constexpr int ELEMS = XE + YE + ZE + SE + SCE + PE + QE + 256;
-  static constexpr int TMEM = DEC == 1 || 64 + DK > 128 ? 256 : 128;  // (DEC 1: 64 more for the pairs of q and k)
-  static constexpr int SMEM = ELEMS * 2 + 1024 /* lut */ + 384 /* tab */ + 256 /* sw */ + 64;
+  // accumulator columns: pairs and o 64, the entry state's rows DVS, the state's product DK, pairs of q and k 64
+  static constexpr int C_X = ONLY ? 0 : 64, C_S = C_X + (ONLY ? 0 : DVS), C_A = C_S + DK, COLS = C_A + (DEC == 1 ? 64 : 0);
+  static constexpr int TMEM = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static constexpr int SMEM = ELEMS * 2 + 1024 /* lut */ + 384 /* tab */ + 64;
   static constexpr int NTV = DVS / 16;  // 8-column tiles of a warp's half of the value side
   static constexpr int NTK = DK / 16;   // and of the key side
 };
@@ -151,9 +150,8 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
   bf16* tQ = tP + SH::PE;
   float2* lut = reinterpret_cast<float2*>(smem + SH::ELEMS * 2);  // [128] (w(m), w(m - 1)), m = index - 64
   float* tab = reinterpret_cast<float*>(lut + 128);               // [65] e^{-a m}
-  float* sw = tab + 96;                                           // [64] state weights of the chunk's rows
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sw + 64);
-  uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 1);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(tab + 96);          // pairs; entry state's rows and state; o
+  uint32_t* slot = reinterpret_cast<uint32_t*>(bar + 3);
   int* s_fail = reinterpret_cast<int*>(slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
   const int q4 = warp & 3, half = warp >> 2, r0 = 16 * q4 + gq;
@@ -170,7 +168,7 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
 
   if (warp == 0) tc::tmem_alloc(slot, SH::TMEM);
   if (tid == 0) {
-    mma::mbar_init(bar, 1);
+    for (int i = 0; i < 3; i++) mma::mbar_init(bar + i, 1);
     mma::mbar_init_fence();
     *s_fail = 0;
   }
@@ -213,9 +211,60 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
   uint32_t ph = 0;
   bool good = true;
   const int nch = (un.ntok + C - 1) / C;
+  auto rows = [&](int c) { return rows_of(un, op.rev, c); };
+  Tile<DK> x, y;
+  Tile<DVS> z, wq;
+  auto load_xy = [&](const Rows& r) {
+    if constexpr (!ONLY) x.load((const float*)op.x, r, H, h, DK, 0);
+    y.load((const float*)op.y, r, H, h, DK, 0);
+  };
+  auto put_xy = [&]() {
+    if constexpr (!ONLY) x.put(tX);
+    y.put(tY);
+  };
+  auto load_z = [&](const Rows& r) {
+    z.load((const float*)op.z, r, H, h, DVt, c0);
+    if constexpr (DEC == 1) wq.load((const float*)op.wx, r, H, h, DVt, c0);
+  };
+  auto put_z = [&](int n) {  // the state's operand with the weights of row to exit state
+    if constexpr (!ONLY) z.put(tZ);
+    z.put_weighted(tSC, n, [&](int row) { return tab[n - 1 - row + (op.rev ? 1 : 0)]; });
+    if constexpr (DEC == 1) wq.put(tQ);
+  };
+  auto wait = [&](int b) {
+    __syncwarp();
+    if (!mma::mbar_wait(bar + b, ph)) *s_fail = 1;
+    tc::fence_after();
+  };
+  if (nch > 0) {
+    load_xy(rows(0));
+    load_z(rows(0));
+    put_xy();
+    put_z(rows(0).n);
+  }
   for (int c = 0; c < nch; c++) {
-    const Rows rw = rows_of(un, op.rev, c);
+    const Rows rw = rows(c);
     const int n = rw.n, idx = op.rev ? nch - 1 - c : c;
+    mma::fence_async_smem();
+    tc::fence_before();
+    // the chunk's tiles and state of every warp; the last chunk's accumulators have been read
+    if (__syncthreads_or(!good)) {
+      good = false;
+      break;
+    }
+    if (tid == 0) {
+      tc::fence_after();
+      if constexpr (!ONLY) {
+        gemm_parts(tm, kview(tX, DK), 64 * DK, kview(tY, DK), 64 * DK, 64, DK / 16);
+        if constexpr (DEC == 1)
+          gemm_parts(tm + SH::C_A, kview(tQ, DVS), 64 * DVS, kview(tZ, DVS), 64 * DVS, 64, DVS / 16);
+        tc::commit(bar);
+        gemm_parts(tm + SH::C_X, kview(tX, DK), 64 * DK, kview(tS, DK), DVS * DK, DVS, DK / 16);
+      }
+      // S'^T += (weighted z)^T y: rows are the value columns
+      gemm_parts(tm + SH::C_S, mview(tSC, DVS), 64 * DVS, mview(tY, DK), 64 * DK, DK, 4);
+      tc::commit(bar + 1);
+    }
     if (!ONLY && st_rows) {
       const int64_t at0 = ((int64_t)(un.ch0 + idx) * H + h) * stN;
       if (op.states) {  // the saving forward: [dv][dk]
@@ -228,13 +277,8 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
         dacc += (double)(part * P.scale * (float)n * tab[n]);
       }
     }
-    if (tid < C) sw[tid] = tid < n ? tab[n - 1 - tid + (op.rev ? 1 : 0)] : 0.f;
-    if constexpr (!ONLY) load_tile<DK>(tX, (const float*)op.x, rw, H, h, DK, 0);
-    load_tile<DK>(tY, (const float*)op.y, rw, H, h, DK, 0);
-    load_tile<DVS>(tZ, (const float*)op.z, rw, H, h, DVt, c0);
-    if constexpr (DEC == 1) load_tile<DVS>(tQ, (const float*)op.wx, rw, H, h, DVt, c0);
     [[maybe_unused]] float kx[NTV][4];
-    if constexpr (DEC == 2) {  // k's rows in fragment order, used after the first products
+    if constexpr (DEC == 2) {  // k's rows in fragment order
 #pragma unroll
       for (int j = 0; j < NTV; j++)
 #pragma unroll
@@ -249,28 +293,12 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
           kx[j][2 * k + 1] = f.y;
         }
     }
-    __syncthreads();  // sw
-    scale_tile<DVS>(tSC, tZ, sw);
-    mma::fence_async_smem();
-    tc::fence_before();
-    __syncthreads();
     float o[NTV][4];
+    float part = 0.f;
     if constexpr (!ONLY) {
-      if (tid == 0) {
-        tc::fence_after();
-        gemm_parts(tm, kview(tX, DK), 64 * DK, kview(tY, DK), 64 * DK, 64, DK / 16);
-        gemm_parts(tm + 64, kview(tX, DK), 64 * DK, kview(tS, DK), DVS * DK, DVS, DK / 16);
-        if constexpr (DEC == 1)
-          gemm_parts(tm + 128, kview(tQ, DVS), 64 * DVS, kview(tZ, DVS), 64 * DVS, 64, DVS / 16);
-        tc::commit(bar);
-      }
-      __syncwarp();
-      if (!mma::mbar_wait(bar, ph)) *s_fail = 1;
-      ph ^= 1;
-      tc::fence_after();
+      wait(0);
       float p[4][4];
       ld_tiles<4>(tm, half * 32, p);
-      float part = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; j++)
 #pragma unroll
@@ -281,67 +309,66 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
           p[j][2 * k + 1] *= w.y;
           put2(p[j][2 * k], p[j][2 * k + 1], tP + mma::opix(row, col, 64), 64 * 64);
         }
+      if constexpr (DEC == 1) {  // A: pairs inside the chunk
+        float m2[4][4];
+        ld_tiles<4>(tm + SH::C_A, half * 32, m2);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const int d = r0 + 8 * (e >> 1) - (half * 32 + 8 * j + 2 * tq + (e & 1));
+            part = fmaf((float)d * p[j][e], m2[j][e], part);
+          }
+      }
+      mma::fence_async_smem();
+      tc::fence_before();
+      __syncthreads();  // the pairs of every warp
+      if (tid == 0) {
+        tc::fence_after();
+        gemm_parts(tm, kview(tP, 64), 64 * 64, mview(tZ, DVS), 64 * DVS, DVS, 4);
+        tc::commit(bar + 2);
+      }
+    }
+    // ---- the entry state's rows and the state, while the tensor core forms o
+    if (c + 1 < nch) load_xy(rows(c + 1));
+    wait(1);
+    if constexpr (!ONLY) {
       const float rs[2] = {P.scale * tab[r0 + (op.rev ? 0 : 1)], P.scale * tab[r0 + 8 + (op.rev ? 0 : 1)]};
-      ld_tiles<NTV>(tm + 64, half * (DVS / 2), o);
-      if constexpr (DEC == 1) {
-        {  // A: pairs inside the chunk
-          float m2[4][4];
-          ld_tiles<4>(tm + 128, half * 32, m2);
+      ld_tiles<NTV>(tm + SH::C_X, half * (DVS / 2), o);
 #pragma unroll
-          for (int j = 0; j < 4; j++)
+      for (int j = 0; j < NTV; j++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-              const int d = r0 + 8 * (e >> 1) - (half * 32 + 8 * j + 2 * tq + (e & 1));
-              part = fmaf((float)d * p[j][e], m2[j][e], part);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < NTV; j++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) {  // B
-            const int row = r0 + 8 * (e >> 1), at = mma::opix(row, half * (DVS / 2) + 8 * j + 2 * tq + (e & 1), DVS);
+        for (int e = 0; e < 4; e++) {
+          const int row = r0 + 8 * (e >> 1);
+          if constexpr (DEC == 1) {  // B
+            const int at = mma::opix(row, half * (DVS / 2) + 8 * j + 2 * tq + (e & 1), DVS);
             float qv = 0.f;
 #pragma unroll
             for (int b = 0; b < NP; b++) qv += __bfloat162float(tQ[b * 64 * DVS + at]);
             part = fmaf(rs[e >> 1] * qv * (float)(row + 1), o[j][e], part);
           }
-      }
-#pragma unroll
-      for (int j = 0; j < NTV; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
           o[j][e] *= rs[e >> 1];
-          if constexpr (DEC == 2) part = fmaf((float)(r0 + 8 * (e >> 1)) * kx[j][e], o[j][e], part);
+          if constexpr (DEC == 2) part = fmaf((float)row * kx[j][e], o[j][e], part);  // C
         }
       if constexpr (DEC == 1 || DEC == 2) dacc += (double)part;
-      mma::fence_async_smem();
-      tc::fence_before();
-      __syncthreads();
     }
-    if (tid == 0) {
-      tc::fence_after();
-      // S'^T += (weighted z)^T y: rows are the value columns
-      gemm_parts(tm + 64, mview(tSC, DVS), 64 * DVS, mview(tY, DK), 64 * DK, DK, 4);
-      if constexpr (!ONLY) gemm_parts(tm, kview(tP, 64), 64 * 64, mview(tZ, DVS), 64 * DVS, DVS, 4);
-      tc::commit(bar);
-    }
-    __syncwarp();
-    if (!mma::mbar_wait(bar, ph)) *s_fail = 1;
-    ph ^= 1;
-    tc::fence_after();
     {
       const Decay dec(a, n);
       float d[NTK][4];
-      ld_tiles<NTK>(tm + 64, half * (DK / 2), d);
+      ld_tiles<NTK>(tm + SH::C_S, half * (DK / 2), d);
 #pragma unroll
       for (int j = 0; j < NTK; j++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          S[j][e] = dec(S[j][e]) + d[j][e];
-        }
+        for (int e = 0; e < 4; e++) S[j][e] = dec(S[j][e]) + d[j][e];
+    }
+    // the next chunk's x, y and state: every product that reads these tiles has completed
+    if (c + 1 < nch) {
+      if constexpr (!ONLY) put_state();
+      put_xy();
+      load_z(rows(c + 1));
     }
     if constexpr (!ONLY) {
-      if (c + 1 < nch) put_state();
+      wait(2);
       float v[NTV][4];
       ld_tiles<NTV>(tm, half * (DVS / 2), v);
 #pragma unroll
@@ -356,13 +383,14 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
         }
       }
     }
-    tc::fence_before();
-    if (*s_fail) good = false;  // a wait ran out: no thread starts another chunk
-    if (__syncthreads_or(!good)) {
-      good = false;
-      break;
-    }
+    ph ^= 1;
+    if (DEC == 1) __syncthreads();  // q's rows (B) have been read
+    if (c + 1 < nch) put_z(rows(c + 1).n);
+    if (*(volatile int*)s_fail) good = false;  // a wait ran out: no thread starts another chunk
   }
+  tc::fence_before();
+  __syncthreads();
+  if (*s_fail) good = false;
   if (!good && tid == 0) *P.err = KDA_ERR_DEVICE;
 
   if (good && st_rows) {  // the unit's state
