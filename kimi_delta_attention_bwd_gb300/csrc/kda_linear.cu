@@ -688,10 +688,11 @@ template <int DV, int DVS, bool DA>
 struct DShape {
   static constexpr int NW = DVS / 16, NTH = 32 * NW;
   static constexpr int OB = 128 * DV, QB = 128 * DVS;  // bytes of the dO and v, the q and k tiles
+  // one chunk's tiles: a second set would hide their loads, but takes more CTAs off the SM than that is worth
+  // (32/64 74 us for 69, 64/64 at 8 x 4096 tokens 105 for 94)
   static constexpr int STAGE = 2 * OB + 2 * QB;
-  static constexpr int STG = DV == 128 ? 1 : 2;        // (one stage there: three CTAs per SM)
   static constexpr int PB = 64 * 64 * 2;
-  static constexpr int SMEM = 1024 + STG * STAGE + PB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
+  static constexpr int SMEM = 1024 + STAGE + PB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
   static constexpr int SP = DA ? 3 : 1;  // parts of the states as operands: their rows enter fp32 sums
   static constexpr int BY_REG = 65536 / (NTH * 168), BY_SMEM = 227 * 1024 / (SMEM + 1024);
   static constexpr int CTAS = BY_REG < BY_SMEM ? BY_REG : BY_SMEM;
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
   constexpr int NTH = SH::NTH, NW = SH::NW, SP = SH::SP;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (mma::smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned char* tP = smem + SH::STG * SH::STAGE;  // [64][64]
+  unsigned char* tP = smem + SH::STAGE;  // [64][64]
   float2* lut = reinterpret_cast<float2*>(tP + SH::PB);
   float* tab = reinterpret_cast<float*>(lut + 128);
   float* rq = tab + 96;  // [64] scale e^{-a(i+1)}
@@ -737,37 +738,32 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
     const int cpr = (P.T + C - 1) / C, r = g / cpr, i = g % cpr;
     return make_int2(r * P.T + i * C, min(C, P.T - i * C));
   };
-  // A chunk's tiles, by one thread.  One stage: dO and v on barrier 0, q and k on 1, as each pair's place
-  // is free; two stages: both pairs on the stage's barrier.
+  // A chunk's tiles, by one thread: dO and v on barrier 0, q and k on 1, each pair as soon as its place is free.
   auto load_ov = [&](int c) {
-    const int t0 = chunk(c).x, s = SH::STG == 2 ? c & 1 : 0;
-    unsigned char* p = smem + s * SH::STAGE;
-    mma::mbar_expect_tx(bar + s, SH::STG == 2 ? SH::STAGE : 2 * SH::OB);
+    const int t0 = chunk(c).x;
+    mma::mbar_expect_tx(bar, 2 * SH::OB);
 #pragma unroll
     for (int b = 0; b < (DV + 63) / 64; b++) {
-      mma::tma_load_2d(p + 8192 * b, &maps.dO, h * DV + 64 * b, t0, bar + s);
-      mma::tma_load_2d(p + SH::OB + 8192 * b, &maps.v, h * DV + 64 * b, t0, bar + s);
+      mma::tma_load_2d(smem + 8192 * b, &maps.dO, h * DV + 64 * b, t0, bar);
+      mma::tma_load_2d(smem + SH::OB + 8192 * b, &maps.v, h * DV + 64 * b, t0, bar);
     }
   };
   auto load_qk = [&](int c) {
-    const int t0 = chunk(c).x, s = SH::STG == 2 ? c & 1 : 1;
-    unsigned char* p = smem + (SH::STG == 2 ? s * SH::STAGE : 0) + 2 * SH::OB;
-    if (SH::STG == 1) mma::mbar_expect_tx(bar + 1, 2 * SH::QB);
-    mma::tma_load_2d(p, &maps.q, h * DKt + c0, t0, bar + s);
-    mma::tma_load_2d(p + SH::QB, &maps.k, h * DKt + c0, t0, bar + s);
+    const int t0 = chunk(c).x;
+    mma::mbar_expect_tx(bar + 1, 2 * SH::QB);
+    mma::tma_load_2d(smem + 2 * SH::OB, &maps.q, h * DKt + c0, t0, bar + 1);
+    mma::tma_load_2d(smem + 2 * SH::OB + SH::QB, &maps.k, h * DKt + c0, t0, bar + 1);
   };
   if (tid == 0) {
     for (int s = 0; s < 2; s++) mma::mbar_init(bar + s, 1);
     mma::mbar_init_fence();
-    for (int s = 0; s < SH::STG && s < nch; s++) {
-      load_ov(s);
-      load_qk(s);
-    }
+    load_ov(0);
+    load_qk(0);
   }
-  // the states of a chunk on their way to L2 a chunk ahead: 78 -> 74 us at 32/64 (300M); with one stage,
-  // where the SM's three CTAs cover the latency, 484 -> 494 at 128/128
+  // the states of a chunk on their way to L2 a chunk ahead: 78 -> 74 us at 32/64 (300M), but 484 -> 494 at
+  // 128/128, whose CTAs have 64 KB of them under way anyhow
   auto warm = [&](int c) {
-    if (SH::STG == 2 && c < nch && tid < 2 * DV / 16)
+    if (DV == 64 && c < nch && tid < 2 * DV / 16)
       mma::bulk_prefetch_l2((tid & 1 ? op.R : op.S) + (((int64_t)(g0 + c) * H + h) * DV + 16 * (tid >> 1)) * DKt + 16 * c0,
                             64 * DVS);
   };
@@ -792,22 +788,19 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
   bool good = true;
   for (int c = 0; c < nch; c++) {
     const int2 ck = chunk(c);
-    const int t0 = ck.x, n = ck.y, st = SH::STG == 2 ? c & 1 : 0;
-    unsigned char* stg = smem + st * SH::STAGE;
-    const uint32_t tO = mma::smem_u32(stg), tV = tO + SH::OB, tQ = tV + SH::OB, tK = tQ + SH::QB;
+    const int t0 = ck.x, n = ck.y;
+    const uint32_t tO = mma::smem_u32(smem), tV = tO + SH::OB, tQ = tV + SH::OB, tK = tQ + SH::QB;
     warm(c + 1);
-    good = mma::mbar_wait(bar + st, (SH::STG == 2 ? c >> 1 : c) & 1);
-    if (SH::STG == 1) good &= mma::mbar_wait(bar + 1, c & 1);
+    good = mma::mbar_wait(bar, c & 1);
+    good &= mma::mbar_wait(bar + 1, c & 1);
     if (n != n_w) {
       if (n_w >= 0) __syncthreads();
       for (int i = tid; i < C; i += NTH) rk[i] = i < n ? tab[n - 1 - i] : 0.f;
       n_w = n;
     }
-    zero_rows<SH::STAGE, 2 * SH::OB, 128, DVS == 32 ? 64 : 128, NTH>(stg, n);
+    zero_rows<SH::STAGE, 2 * SH::OB, 128, DVS == 32 ? 64 : 128, NTH>(smem, n);
     if (__syncthreads_or(!good)) {
       good = false;
-      // the other stage's copy may be under way
-      if (SH::STG == 2 && tid == 0 && c + 1 < nch) mma::mbar_wait(bar + ((c + 1) & 1), ((c + 1) >> 1) & 1);
       break;
     }
 
@@ -939,9 +932,9 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
       }
     }
     if constexpr (DA) dacc += (double)part + (double)(dot * (float)n * tab[n]);
-    if (SH::STG == 1) mma::fence_async_smem();
+    mma::fence_async_smem();
     __syncthreads();  // the pairs of every warp; dO and v have been read
-    if (SH::STG == 1 && tid == 0 && c + 1 < nch) load_ov(c + 1);
+    if (tid == 0 && c + 1 < nch) load_ov(c + 1);
     // ---- dq^T += k^T P^T, dk^T += q^T P
 #pragma unroll
     for (int kk = 0; kk < 4; kk++) {
@@ -963,7 +956,7 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
       }
     }
     // ---- out, in the place of the q and k tiles (their last reads were before the barrier)
-    unsigned char *uQ = stg + 2 * SH::OB, *uK = uQ + SH::QB;
+    unsigned char *uQ = smem + 2 * SH::OB, *uK = uQ + SH::QB;
     stage_tile<DVS>(uQ, 16 * warp, dq, false);
     stage_tile<DVS>(uK, 16 * warp, dk, false);
     if (n < C) {
@@ -979,10 +972,9 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
         tma_store_2d(&maps.dk, h * DKt + c0, t0, uK);
         mma::bulk_commit();
       }
-      if (c + SH::STG < nch) {  // the next chunk of this stage
+      if (c + 1 < nch) {
         mma::bulk_wait_read();
-        if (SH::STG == 2) load_ov(c + 2);
-        load_qk(c + SH::STG);
+        load_qk(c + 1);
       }
     }
   }
