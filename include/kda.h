@@ -430,8 +430,8 @@ KDA_API kda_status kda_linear_decode(int n_seq, int H, int dk, int dv, int dtype
  * x, y, dy, dx : [n_rows, D] contiguous in dtype (KDA_BF16 or KDA_F32); w, bias,
  * dw, dbias : [D] fp32 (bias and dbias may be NULL); mean, rstd : [n_rows] fp32,
  * written by the forward for the backward (both NULL: not wanted).  eps <= 0
- * selects 1e-6.  Device pointers, 16-byte aligned.  The backward overwrites dx,
- * dw and dbias; its scratch (per-CTA partials of dw and dbias, summed in a
+ * selects 1e-6.  Device pointers, 16-byte aligned; y may be x.  The backward
+ * overwrites dx, dw and dbias; its scratch (per-CTA partials of dw and dbias, summed in a
  * fixed order) is kda_layer_norm_workspace_size(n_rows, D, dtype) bytes (0 for
  * invalid sizes). */
 KDA_API size_t kda_layer_norm_workspace_size(int64_t n_rows, int D, int dtype);

@@ -29,8 +29,8 @@ def _rows(x, w, bias=None):
 
 def kda_layer_norm(x, w, bias=None, eps: Optional[float] = None, out: Optional[torch.Tensor] = None,
                    return_stats: bool = False):
-    """Layer norm of x [..., D]; eps 1e-6 unless given (> 0).  With
-    return_stats returns (y, mean, rstd), the rows' statistics [...] in fp32
+    """Layer norm of x [..., D]; eps 1e-6 unless given (> 0); out may be x
+    (in place).  With return_stats returns (y, mean, rstd), the rows' statistics [...] in fp32
     that the backward takes."""
     n, D = _rows(x, w, bias)
     if out is None:

@@ -122,6 +122,16 @@ def test_without_bias_shapes_and_outputs():
     assert (np.abs(big - r) <= 2.0 ** -8 * np.abs(r) + 2.0 ** -16).all()
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,D", [(700, 64), (37, 1001), (5, 40003)])
+def test_in_place(n, D, dt):
+    g = torch.Generator().manual_seed(D)
+    x = torch.randn(n, D, generator=g).to(dt).cuda()
+    w, b = (torch.randn(D, generator=g).cuda() for _ in range(2))
+    y = kda.kda_layer_norm(x, w, b)
+    assert kda.kda_layer_norm(x, w, b, out=x) is x and torch.equal(x, y)
+
+
 def test_deterministic_on_another_stream_and_as_a_graph():
     t = make(6, 3001, 640, "bf16")
     ref = run(t)

@@ -370,6 +370,14 @@ def test_a_graph_replayed_on_other_offsets(dt):
         check(got, oracle(z), dt)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_more_documents_than_the_table_has_threads(dt):
+    docs = [int(n) for n in np.random.default_rng(35).integers(0, 4, 2500)]
+    docs[1200] = 600
+    x = make(35, docs, 1, 32, 64, dt)
+    check(run(x, host=False), oracle(x), dt)
+
+
 def test_two_calls_at_once():
     # one problem, two streams, a workspace each
     x = make(32, [700, 1, 64, 0, 35], 2, 128, 128, "bf16")
