@@ -18,9 +18,10 @@
 // vectors that a row shares with its neighbours are read and written value by
 // value.  Sixteen columns a thread: with eight, the shuffles of the row sums and
 // the bookkeeping took the larger part of the issue slots (bf16 32768 x 2048
-// forward: 68 us at 76% of them, 44 now, 68% of them; backward 68).  The next rows are under way to the thread's
-// own slots of shared memory (cp.async, no barrier) while a row is summed.  The
-// backward's per-CTA partials are added in a fixed order (deterministic).
+// forward: 68 us at 76% of them, 44 now, 68% of them; backward 68).  The next
+// rows are under way to the thread's own slots of shared memory (cp.async, no
+// barrier) while a row is summed.  The backward's per-CTA partials are added in
+// a fixed order (deterministic).
 #include "kda_internal.cuh"
 #include "../../include/kda.h"
 
@@ -556,10 +557,10 @@ struct LnArgs {
   cudaStream_t st;
 };
 
-// Launches K with smem dynamic bytes, its limit raised where they pass 48 KB.
+// Launches K with smem dynamic bytes, its limit raised where they and the static kilobyte pass 48 KB.
 template <typename... KA, typename... A>
 cudaError_t ln_run(void (*k)(KA...), int nblk, int thr, size_t smem, cudaStream_t st, A... args) {
-  if (smem > 48 * 1024) {
+  if (smem > 47 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
@@ -572,10 +573,11 @@ cudaError_t ln_fwd_launch(const LnShape& s, const LnArgs& a, int nblk) {
   constexpr int NR = 2;
   const int thr = s.blk ? s.G : LN_NTHR;
   auto run = [&](auto* kernel) {
-    return ln_run(kernel, nblk, thr, s.keep ? 2 * NR * LN_PER * sizeof(T) * thr : 0, a.st, a.n, a.D, s.G, a.eps, (const T*)a.x, a.w,
-                  a.b, (T*)a.y, a.mean, a.rstd);
+    return ln_run(kernel, nblk, thr, s.keep ? 2 * NR * LN_PER * sizeof(T) * thr : 0, a.st, a.n, a.D, s.G, a.eps,
+                  (const T*)a.x, a.w, a.b, (T*)a.y, a.mean, a.rstd);
   };
-  if (!s.keep) return s.edge ? run(ln_fwd_kernel<T, true, true, false, 1>) : run(ln_fwd_kernel<T, true, false, false, 1>);
+  if (!s.keep)
+    return s.edge ? run(ln_fwd_kernel<T, true, true, false, 1>) : run(ln_fwd_kernel<T, true, false, false, 1>);
   if (s.blk) return s.edge ? run(ln_fwd_kernel<T, true, true, true, NR>) : run(ln_fwd_kernel<T, true, false, true, NR>);
   return s.edge ? run(ln_fwd_kernel<T, false, true, true, NR>) : run(ln_fwd_kernel<T, false, false, true, NR>);
 }
@@ -667,7 +669,8 @@ extern "C" KDA_API kda_status kda_layer_norm_bwd(int64_t n_rows, int D, int dtyp
   prof_begin(K_LN_BWD, st);
   if (s.wide) {
     if (dtype == KDA_BF16)
-      ln_bwd_wide_kernel<B><<<nblk, LN_CTHR, 0, st>>>(n_rows, D, (const B*)x, w, (const B*)dy, mean, rstd, (B*)dx, a.part);
+      ln_bwd_wide_kernel<B><<<nblk, LN_CTHR, 0, st>>>(n_rows, D, (const B*)x, w, (const B*)dy, mean, rstd, (B*)dx,
+                                                      a.part);
     else
       ln_bwd_wide_kernel<float><<<nblk, LN_CTHR, 0, st>>>(n_rows, D, (const float*)x, w, (const float*)dy, mean, rstd,
                                                        (float*)dx, a.part);

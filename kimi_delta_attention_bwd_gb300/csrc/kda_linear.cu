@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(1024) lin_table_kernel(LinP P) {
 // loads in flight; the CTAs loop over the pieces, whose number the device alone
 // may know (a grid of its bound, mostly empty, took 36 to 62 us).
 constexpr int FTH = 128, FCTAS = 8 * LIN_SMS;
-__global__ void __launch_bounds__(FTH) lin_fold_kernel(LinP P, float* segc, const float* init, int rev, int N, int fwd) {
+__global__ void __launch_bounds__(FTH) lin_fold_kernel(LinP P, float* segc, const float* init, int rev, int N,
+                                                       int fwd) {
   pdl_wait();
   pdl_release();
   if (!ready(P, fwd)) return;
@@ -137,7 +138,8 @@ __global__ void __launch_bounds__(FTH) lin_fold_kernel(LinP P, float* segc, cons
   const int pieces = N / (4 * FTH);
   const int64_t total = (int64_t)(P.rows ? P.n_long : P.counts[2]) * P.H * pieces;
   for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
-    const int at = ((int)(item % pieces) * FTH + threadIdx.x) * 4, dh = (int)(item / pieces), d = dh / P.H, h = dh % P.H;
+    const int at = ((int)(item % pieces) * FTH + threadIdx.x) * 4, dh = (int)(item / pieces);
+    const int d = dh / P.H, h = dh % P.H;
     int u0, ns, doc, len, last;
     if (P.rows) {
       ns = (P.T + P.L - 1) / P.L;
@@ -478,7 +480,8 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
       // [value % 8 / 2][key]: a word of lin_dqk's operand fragments is 128 bytes of a tile, a pair stored here
       // fills whole sectors (128/128, the two chains and lin_dqk: [dv][dk] 614 + 521 us, the accumulators'
       // own order 569 + 483, this 560 + 484)
-      float* p = op.states + ((int64_t)(un.ch0 + idx) * H + h) * stN + (int64_t)(c0 + r0) * DK + 32 * (gq & 1) + 8 * (gq >> 1) + 2 * tq;
+      float* p = op.states + ((int64_t)(un.ch0 + idx) * H + h) * stN + (int64_t)(c0 + r0) * DK + 32 * (gq & 1) +
+                 8 * (gq >> 1) + 2 * tq;
       const float w = rev ? P.scale : 1.0f;
 #pragma unroll
       for (int m = 0; m < MT; m++)
@@ -768,8 +771,8 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
   // 128/128, whose CTAs have 64 KB of them under way anyhow
   auto warm = [&](int c) {
     if (DV == 64 && c < nch && tid < 2 * DV / 16)
-      mma::bulk_prefetch_l2((tid & 1 ? op.R : op.S) + (((int64_t)(g0 + c) * H + h) * DV + 16 * (tid >> 1)) * DKt + 16 * c0,
-                            64 * DVS);
+      mma::bulk_prefetch_l2(
+          (tid & 1 ? op.R : op.S) + (((int64_t)(g0 + c) * H + h) * DV + 16 * (tid >> 1)) * DKt + 16 * c0, 64 * DVS);
   };
   warm(0);
   for (int i = tid; i < 65; i += NTH) tab[i] = decay_pow(a, i);
@@ -847,8 +850,8 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
             const float2 w = lut[64 + d + 8 * k - 8 * j];
             p[t][j][2 * k] *= w.x;
             p[t][j][2 * k + 1] *= w.y;
-            *reinterpret_cast<uint32_t*>(tP + (16 * rr[t] + 8 * k + gq) * 128 + (((2 * cc[t] + j) ^ gq) << 4) + 4 * tq) =
-                pack2(p[t][j][2 * k], p[t][j][2 * k + 1]);
+            unsigned char* at = tP + (16 * rr[t] + 8 * k + gq) * 128 + (((2 * cc[t] + j) ^ gq) << 4) + 4 * tq;
+            *reinterpret_cast<uint32_t*>(at) = pack2(p[t][j][2 * k], p[t][j][2 * k + 1]);
           }
         if constexpr (DA) {  // A: the same pairs of q and k (this slice's columns)
           float m2[2][4];

@@ -128,7 +128,8 @@ struct Shape {
   // 512 bytes after the tiles: an M = 64 view of a 32-column tile reads up to four cores past it
   static constexpr int ELEMS = XE + YE + ZE + SE + SCE + PE + QE + 256;
   // accumulator columns: pairs and o 64, the entry state's rows DVS, the state's product DK, pairs of q and k 64
-  static constexpr int C_X = ONLY ? 0 : 64, C_S = C_X + (ONLY ? 0 : DVS), C_A = C_S + DK, COLS = C_A + (DEC == 1 ? 64 : 0);
+  static constexpr int C_X = ONLY ? 0 : 64, C_S = C_X + (ONLY ? 0 : DVS), C_A = C_S + DK;
+  static constexpr int COLS = C_A + (DEC == 1 ? 64 : 0);
   static constexpr int TMEM = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static constexpr int SMEM = ELEMS * 2 + 1024 /* lut */ + 384 /* tab */ + 64;
   static constexpr int NTV = DVS / 16;  // 8-column tiles of a warp's half of the value side

@@ -69,6 +69,12 @@ def test_matches_oracle(n, D, dt):
     check(run(t), limits(**t, dt=dt))
 
 
+@pytest.mark.parametrize("n,D,dt", [(9, 6001, "bf16"), (9, 6016, "bf16"), (9, 2999, "f32"), (9, 3008, "f32")])
+def test_rows_whose_slots_fill_48_kilobytes(n, D, dt):
+    t = make(D, n, D, dt)
+    check(run(t), limits(t["x"], t["w"], t["b"], t["dy"], dt))
+
+
 def test_many_short_rows():
     t = make(1, 40003, 64, "f32")
     check(run(t), limits(**t, dt="f32"))
