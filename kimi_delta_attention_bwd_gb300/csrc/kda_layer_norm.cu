@@ -34,6 +34,7 @@ constexpr int LN_PER = 16;       // values of a row per thread, twice that in ro
 constexpr int LN_SMS = 152;      // the grids: what the SMs hold at once
 constexpr int LN_FWD_THR = 512, LN_BWD_THR = 512;  // resident threads per SM (their registers)
 constexpr int LN_MAX_D = 1 << 24;
+constexpr size_t LN_SMEM = 225 * 1024;  // dynamic shared memory of a CTA at most
 
 // 16 bytes as loaded (half the registers for bf16) until they are used.
 template <typename T>
@@ -168,12 +169,16 @@ struct Ahead {
     return base + (((g & 1) * SLOTS + (t * NR + k) * NCH + i) * blockDim.x) + threadIdx.x;
   }
   __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-  // all but the newest group are here
-  __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group 1;\n" ::: "memory"); }
+  // all but the newest N groups are here
+  template <int N>
+  __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 };
 
 // KEEP: w and b in registers and the next rows under way; else (32 columns a
-// thread) both are read as they are needed.
+// thread) w and b in the thread's own words of shared memory, and the next row
+// under way from when this one is in registers (bf16, 128 MB: 8200 columns
+// 124 us with w, b and the rows read as they were needed, 79 so; 10001 columns
+// 257 and 81).
 template <typename T, bool BLK, bool EDGE, bool KEEP, int NR>
 __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_FWD_THR / LN_NTHR)
     ln_fwd_kernel(int64_t n, int D, int G, float eps, const T* __restrict__ x, const float* __restrict__ w,
@@ -203,12 +208,20 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_FWD_THR 
   const T* px = x + row0 * D;
   T* py = y + row0 * D;
   float wv[KEEP ? E : V], bv[KEEP ? E : V];
-  if constexpr (KEEP) {
-    fetch(0, row0, px);
+  // !KEEP: word e of vector i of w, E * blockDim.x further on of b
+  float* own = reinterpret_cast<float*>(smem) + (KEEP ? 0 : NCH * 4 * blockDim.x) + threadIdx.x;
+  fetch(0, row0, px);
 #pragma unroll
-    for (int i = 0; i < NCH; i++) {
-      cols(i).param(w, wv + i * V);
-      cols(i).param(b, bv + i * V);
+  for (int i = 0; i < NCH; i++) {
+    const int at = KEEP ? i * V : 0;
+    cols(i).param(w, wv + at);
+    cols(i).param(b, bv + at);
+    if constexpr (!KEEP) {
+#pragma unroll
+      for (int e = 0; e < V; e++) {
+        own[(i * V + e) * blockDim.x] = wv[e];
+        own[(E + i * V + e) * blockDim.x] = bv[e];
+      }
     }
   }
   int flip = 0;
@@ -216,10 +229,12 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_FWD_THR 
   int64_t row = row0;
   for (int g = 0; row - gid < n; g++) {
     float v[NR][E], m[NR], var[NR];
+    px += NR * stepD;
     if constexpr (KEEP) {
-      px += NR * stepD;
       fetch(g + 1, row + NR * step, px);
-      q.wait();
+      q.template wait<1>();
+    } else {
+      q.template wait<0>();
     }
 #pragma unroll
     for (int k = 0; k < NR; k++) {
@@ -228,17 +243,16 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_FWD_THR 
       for (int i = 0; i < NCH; i++) {
         Pack<T> p;
         p.u = make_uint4(0, 0, 0, 0);
-        if (cols(i).any()) {  // (a row past the last: whatever the slot held, not stored)
-          if constexpr (KEEP) p.u = *q.slot(g, 0, k, i);
-          else p = cols(i).load(px);
-        }
+        // (a row past the last: whatever the slot held, not stored)
+        if (cols(i).any()) p.u = *q.slot(KEEP ? g : 0, 0, k, i);
         p.get(v[k] + i * V);
-        if constexpr (EDGE && KEEP) cols(i).clear(v[k] + i * V);
+        if constexpr (EDGE) cols(i).clear(v[k] + i * V);
 #pragma unroll
         for (int e = 0; e < V; e++) m[k] += v[k][i * V + e];
       }
     }
     row_sums<BLK, NR>(m, G, red[flip]);
+    if constexpr (!KEEP) fetch(0, row + NR * step, px);
 #pragma unroll
     for (int k = 0; k < NR; k++) {
       m[k] *= inv;
@@ -266,8 +280,11 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_FWD_THR 
         if (!cols(i).any()) continue;
         const int at = KEEP ? i * V : 0;
         if constexpr (!KEEP) {
-          cols(i).param(w, wv);
-          cols(i).param(b, bv);
+#pragma unroll
+          for (int e = 0; e < V; e++) {
+            wv[e] = own[(i * V + e) * blockDim.x];
+            bv[e] = own[(E + i * V + e) * blockDim.x];
+          }
         }
         float o[V];
 #pragma unroll
@@ -277,13 +294,14 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_FWD_THR 
     }
     row += NR * step;
     py += NR * stepD;
-    if constexpr (!KEEP) px += NR * stepD;
   }
 }
 
 // KEEP as in the forward; without it the dw / db sums are in shared memory, in
-// slots of the thread's own.
-template <typename T, bool BLK, bool EDGE, bool KEEP>
+// words of the thread's own and, where shared memory has room, the next row under
+// way as in the forward (MORE >= 1) and w too (MORE = 2) (bf16, 128 MB: 8200
+// columns 242 us without, 166 with; 10001 columns 269 and 213).
+template <typename T, bool BLK, bool EDGE, bool KEEP, int MORE>
 __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_BWD_THR / LN_NTHR)
     ln_bwd_kernel(int64_t n, int D, int G, const T* __restrict__ x, const float* __restrict__ w,
                   const T* __restrict__ dy, const float* __restrict__ mean, const float* __restrict__ rstd,
@@ -291,13 +309,14 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_BWD_THR 
   constexpr int V = Pack<T>::V, E = KEEP ? LN_PER : 2 * LN_PER, NCH = E / V;
   __shared__ float red[2][2][32];
   extern __shared__ __align__(16) unsigned char smem[];
-  const Ahead<T, 2, 1, NCH> q = {reinterpret_cast<uint4*>(smem)};
   float* acc = reinterpret_cast<float*>(smem);  // !KEEP: [2][E][blockDim.x]; !BLK, at the end: [256 / G][D]
+  const Ahead<T, 2, 1, NCH> q = {reinterpret_cast<uint4*>(acc + (KEEP ? 0 : 2 * E * blockDim.x))};
+  float* own = reinterpret_cast<float*>(q.base + 2 * NCH * blockDim.x) + threadIdx.x;  // MORE = 2: w
   pdl_release();
   const int gid = BLK ? 0 : threadIdx.x / G, lane = BLK ? threadIdx.x : threadIdx.x % G;
   const int rpc = BLK ? 1 : LN_NTHR / G;
   const int64_t row0 = (int64_t)blockIdx.x * rpc + gid, step = (int64_t)gridDim.x * rpc, stepD = step * D;
-  const int s = EDGE ? (int)((row0 % V) * (D % V) % V) : 0;
+  int s = EDGE ? (int)((row0 % V) * (D % V) % V) : 0;
   const float inv = 1.0f / (float)D;
   const T *xend = x + n * D, *dend = dy + n * D;
   auto cols = [&](int i) { return Cols<T, EDGE>{(i * G + lane) * V - s, D}; };
@@ -317,8 +336,8 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_BWD_THR 
   };
   int64_t at = row0 * D, row = row0;
   float aw[KEEP ? E : 1], ab[KEEP ? E : 1], wv[KEEP ? E : V];
+  if constexpr (MORE > 0) fetch(0, row, at);
   if constexpr (KEEP) {
-    fetch(0, row, at);
 #pragma unroll
     for (int i = 0; i < NCH; i++) cols(i).param(w, wv + i * V);
 #pragma unroll
@@ -326,18 +345,30 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_BWD_THR 
   } else {
 #pragma unroll
     for (int e = 0; e < 2 * E; e++) acc[e * blockDim.x + threadIdx.x] = 0.f;
+    if constexpr (MORE == 2) {
+#pragma unroll
+      for (int i = 0; i < NCH; i++) {
+        cols(i).param(w, wv);
+#pragma unroll
+        for (int e = 0; e < V; e++) own[(i * V + e) * blockDim.x] = wv[e];
+      }
+    }
   }
   int flip = 0;
   for (int g = 0; row - gid < n; g++) {
     const bool ok = row < n;
-    if (!KEEP && ok) {
+    if (MORE == 0 && ok) {
       nmu = mean[row];
       nr = rstd[row];
     }
+    // (a row's columns are found anew: kept over the rows, as the compiler would, they spill)
+    if constexpr (EDGE && !KEEP) asm volatile("" : "+r"(s));
     const float mu = nmu, r = nr;
     if constexpr (KEEP) {
       fetch(g + 1, row + step, at + stepD);
-      q.wait();
+      q.template wait<1>();
+    } else {
+      q.template wait<0>();
     }
     float xh[E], dd[E], m[2] = {0.f, 0.f};
 #pragma unroll
@@ -345,9 +376,9 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_BWD_THR 
       Pack<T> px, pd;
       px.u = pd.u = make_uint4(0, 0, 0, 0);
       if (ok && cols(i).any()) {
-        if constexpr (KEEP) {
-          px.u = *q.slot(g, 0, 0, i);
-          pd.u = *q.slot(g, 1, 0, i);
+        if constexpr (MORE > 0) {
+          px.u = *q.slot(KEEP ? g : 0, 0, 0, i);
+          pd.u = *q.slot(KEEP ? g : 0, 1, 0, i);
         } else {
           px = cols(i).load(x + at);
           pd = cols(i).load(dy + at);
@@ -355,8 +386,15 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_BWD_THR 
       }
       px.get(xh + i * V);
       pd.get(dd + i * V);
-      if constexpr (!KEEP) cols(i).param(w, wv);
-      if constexpr (EDGE && KEEP) {
+      if constexpr (!KEEP) {
+        if constexpr (MORE == 2) {
+#pragma unroll
+          for (int e = 0; e < V; e++) wv[e] = own[(i * V + e) * blockDim.x];
+        } else {
+          cols(i).param(w, wv);
+        }
+      }
+      if constexpr (EDGE) {
         cols(i).clear(xh + i * V);
         cols(i).clear(dd + i * V);
       }
@@ -376,9 +414,11 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_BWD_THR 
         m[0] += dd[j];
         m[1] += dd[j] * h;
       }
+      if constexpr (!KEEP) asm volatile("" ::: "memory");  // (the next vector's loads not before: registers)
     }
     row_sums<BLK, 2>(m, G, red[flip]);
     flip ^= 1;
+    if constexpr (!KEEP && MORE > 0) fetch(0, row + step, at + stepD);
     if (ok) {
       m[0] *= inv;
       m[1] *= inv;
@@ -537,10 +577,10 @@ LnShape ln_shape(int D, int dtype) {
 
 // Persistent CTAs: no more than the rows need or than the SMs hold at once, in
 // a number that makes the row step a multiple of a vector's values.
-int ln_blocks(int64_t n, int D, int dtype, int thr) {
+int ln_blocks(int64_t n, int D, int dtype, bool bwd) {
   const LnShape s = ln_shape(D, dtype);
   if (s.wide) return (int)(n < LN_SMS ? n : LN_SMS);
-  const int rpc = s.blk ? 1 : LN_NTHR / s.G, per = thr / (s.blk ? s.G : LN_NTHR);
+  const int rpc = s.blk ? 1 : LN_NTHR / s.G, per = (bwd ? LN_BWD_THR : LN_FWD_THR) / (s.blk ? s.G : LN_NTHR);
   const int64_t need = (n + rpc - 1) / rpc;
   const int64_t most = (int64_t)LN_SMS * (per < 1 ? 1 : per);  // a multiple of 8
   return (int)(need < most ? (need + 7) / 8 * 8 : most);
@@ -573,8 +613,8 @@ cudaError_t ln_fwd_launch(const LnShape& s, const LnArgs& a, int nblk) {
   constexpr int NR = 2;
   const int thr = s.blk ? s.G : LN_NTHR;
   auto run = [&](auto* kernel) {
-    return ln_run(kernel, nblk, thr, s.keep ? 2 * NR * LN_PER * sizeof(T) * thr : 0, a.st, a.n, a.D, s.G, a.eps,
-                  (const T*)a.x, a.w, a.b, (T*)a.y, a.mean, a.rstd);
+    return ln_run(kernel, nblk, thr, (s.keep ? 2 * NR * LN_PER * sizeof(T) : 2 * LN_PER * (sizeof(T) + 8)) * thr, a.st,
+                  a.n, a.D, s.G, a.eps, (const T*)a.x, a.w, a.b, (T*)a.y, a.mean, a.rstd);
   };
   if (!s.keep)
     return s.edge ? run(ln_fwd_kernel<T, true, true, false, 1>) : run(ln_fwd_kernel<T, true, false, false, 1>);
@@ -585,15 +625,27 @@ cudaError_t ln_fwd_launch(const LnShape& s, const LnArgs& a, int nblk) {
 template <typename T>
 cudaError_t ln_bwd_launch(const LnShape& s, const LnArgs& a, int nblk) {
   const int thr = s.blk ? s.G : LN_NTHR;
-  const size_t slots = s.keep ? 2 * 2 * LN_PER * sizeof(T) * thr : 0;
+  const size_t slots = 2 * 2 * LN_PER * sizeof(T) * thr;
   const size_t acc = !s.keep ? 4 * LN_PER * sizeof(float) * thr : s.blk ? 0 : (size_t)(LN_NTHR / s.G) * a.D * 4;
+  // (without keep: the sums, then what has room of the next row and of w)
+  const size_t wb = 2 * LN_PER * 4 * thr;
+  const int more = acc + slots + wb <= LN_SMEM ? 2 : acc + slots <= LN_SMEM ? 1 : 0;
+  const size_t smem = s.keep ? (acc > slots ? acc : slots) : acc + (more > 0 ? slots : 0) + (more > 1 ? wb : 0);
   auto run = [&](auto* kernel) {
-    return ln_run(kernel, nblk, thr, acc > slots ? acc : slots, a.st, a.n, a.D, s.G, (const T*)a.x, a.w,
+    return ln_run(kernel, nblk, thr, smem, a.st, a.n, a.D, s.G, (const T*)a.x, a.w,
                   (const T*)a.dy, (const float*)a.mean, (const float*)a.rstd, (T*)a.dx, a.part);
   };
-  if (!s.keep) return s.edge ? run(ln_bwd_kernel<T, true, true, false>) : run(ln_bwd_kernel<T, true, false, false>);
-  if (s.blk) return s.edge ? run(ln_bwd_kernel<T, true, true, true>) : run(ln_bwd_kernel<T, true, false, true>);
-  return s.edge ? run(ln_bwd_kernel<T, false, true, true>) : run(ln_bwd_kernel<T, false, false, true>);
+  if (!s.keep && more == 2)
+    return s.edge ? run(ln_bwd_kernel<T, true, true, false, 2>) : run(ln_bwd_kernel<T, true, false, false, 2>);
+  if (!s.keep && (more == 1 || sizeof(T) == 2))  // (bf16 rows always fit)
+    return s.edge ? run(ln_bwd_kernel<T, true, true, false, 1>) : run(ln_bwd_kernel<T, true, false, false, 1>);
+  if constexpr (sizeof(T) == 4) {
+    if (!s.keep)
+      return s.edge ? run(ln_bwd_kernel<T, true, true, false, 0>) : run(ln_bwd_kernel<T, true, false, false, 0>);
+  }
+  if (s.blk)
+    return s.edge ? run(ln_bwd_kernel<T, true, true, true, 1>) : run(ln_bwd_kernel<T, true, false, true, 1>);
+  return s.edge ? run(ln_bwd_kernel<T, false, true, true, 1>) : run(ln_bwd_kernel<T, false, false, true, 1>);
 }
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
@@ -612,7 +664,7 @@ using namespace kda;
 
 extern "C" KDA_API size_t kda_layer_norm_workspace_size(int64_t n_rows, int D, int dtype) {
   if (ln_check(n_rows, D, dtype) != KDA_OK) return 0;
-  return (size_t)ln_blocks(n_rows, D, dtype, LN_BWD_THR) * 2 * (size_t)D * sizeof(float);
+  return (size_t)ln_blocks(n_rows, D, dtype, true) * 2 * (size_t)D * sizeof(float);
 }
 
 extern "C" KDA_API kda_status kda_layer_norm_fwd(int64_t n_rows, int D, int dtype, float eps, const void* x,
@@ -625,7 +677,7 @@ extern "C" KDA_API kda_status kda_layer_norm_fwd(int64_t n_rows, int D, int dtyp
   for (const void* p : ptrs)
     if (!aligned16(p)) return KDA_ERR_ALIGNMENT;
   const LnShape s = ln_shape(D, dtype);
-  const int nblk = ln_blocks(n_rows, D, dtype, LN_FWD_THR);
+  const int nblk = ln_blocks(n_rows, D, dtype, false);
   LnArgs a = {};
   a.n = n_rows; a.D = D; a.eps = eps > 0.f ? eps : 1e-6f;
   a.x = x; a.w = w; a.b = bias; a.y = y; a.mean = mean; a.rstd = rstd; a.st = st;
@@ -659,7 +711,7 @@ extern "C" KDA_API kda_status kda_layer_norm_bwd(int64_t n_rows, int D, int dtyp
   if (!workspace || workspace_bytes < kda_layer_norm_workspace_size(n_rows, D, dtype)) return KDA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return KDA_ERR_ALIGNMENT;
   const LnShape s = ln_shape(D, dtype);
-  const int nblk = ln_blocks(n_rows, D, dtype, LN_BWD_THR);
+  const int nblk = ln_blocks(n_rows, D, dtype, true);
   LnArgs a = {};
   a.n = n_rows; a.D = D;
   a.x = x; a.w = w; a.dy = dy; a.dx = dx; a.mean = (float*)mean; a.rstd = (float*)rstd; a.part = (float*)workspace;

@@ -129,7 +129,7 @@ def test_without_bias_shapes_and_outputs():
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("n,D", [(700, 64), (37, 1001), (5, 40003)])
+@pytest.mark.parametrize("n,D", [(700, 64), (37, 1001), (400, 10001), (5, 40003)])
 def test_in_place(n, D, dt):
     g = torch.Generator().manual_seed(D)
     x = torch.randn(n, D, generator=g).to(dt).cuda()
