@@ -33,6 +33,10 @@ constexpr int LN_CTHR = 512;     // most threads of a one-row CTA (128 registers
 constexpr int LN_PER = 16;       // values of a row per thread, twice that in rows that LN_CTHR threads do not hold
 constexpr int LN_SMS = 152;      // the grids: what the SMs hold at once
 constexpr int LN_FWD_THR = 512, LN_BWD_THR = 512;  // resident threads per SM (their registers)
+// A forward's CTAs of 257 to LN_PAIR threads leave an SM of LN_FWD_THR half empty: in bf16 two of them there, at
+// 102 registers a thread (128 MB: 5003 columns 84 us with one, 68 with two, 5120 columns 59 and 49).  fp32 has
+// twice the bytes under way and gains nothing (5003 columns 65 and 69).
+constexpr int LN_PAIR = 320;
 constexpr int LN_MAX_D = 1 << 24;
 constexpr size_t LN_SMEM = 225 * 1024;  // dynamic shared memory of a CTA at most
 
@@ -179,8 +183,9 @@ struct Ahead {
 // under way from when this one is in registers (bf16, 128 MB: 8200 columns
 // 124 us with w, b and the rows read as they were needed, 79 so; 10001 columns
 // 257 and 81).
-template <typename T, bool BLK, bool EDGE, bool KEEP, int NR>
-__global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_FWD_THR / LN_NTHR)
+template <typename T, bool BLK, bool EDGE, bool KEEP, int NR, bool PAIR = false>
+__global__ void __launch_bounds__(BLK ? (PAIR ? LN_PAIR : LN_CTHR) : LN_NTHR,
+                                  BLK ? (PAIR ? 2 : 1) : LN_FWD_THR / LN_NTHR)
     ln_fwd_kernel(int64_t n, int D, int G, float eps, const T* __restrict__ x, const float* __restrict__ w,
                   const float* __restrict__ b, T* __restrict__ y, float* __restrict__ mean,
                   float* __restrict__ rstd) {
@@ -575,12 +580,17 @@ LnShape ln_shape(int D, int dtype) {
   return s;
 }
 
+bool ln_pair(const LnShape& s, int dtype) {
+  return dtype == KDA_BF16 && s.blk && s.keep && s.G > LN_FWD_THR / 2 && s.G <= LN_PAIR;
+}
+
 // Persistent CTAs: no more than the rows need or than the SMs hold at once, in
 // a number that makes the row step a multiple of a vector's values.
 int ln_blocks(int64_t n, int D, int dtype, bool bwd) {
   const LnShape s = ln_shape(D, dtype);
   if (s.wide) return (int)(n < LN_SMS ? n : LN_SMS);
-  const int rpc = s.blk ? 1 : LN_NTHR / s.G, per = (bwd ? LN_BWD_THR : LN_FWD_THR) / (s.blk ? s.G : LN_NTHR);
+  const int rpc = s.blk ? 1 : LN_NTHR / s.G;
+  const int per = !bwd && ln_pair(s, dtype) ? 2 : (bwd ? LN_BWD_THR : LN_FWD_THR) / (s.blk ? s.G : LN_NTHR);
   const int64_t need = (n + rpc - 1) / rpc;
   const int64_t most = (int64_t)LN_SMS * (per < 1 ? 1 : per);  // a multiple of 8
   return (int)(need < most ? (need + 7) / 8 * 8 : most);
@@ -618,6 +628,11 @@ cudaError_t ln_fwd_launch(const LnShape& s, const LnArgs& a, int nblk) {
   };
   if (!s.keep)
     return s.edge ? run(ln_fwd_kernel<T, true, true, false, 1>) : run(ln_fwd_kernel<T, true, false, false, 1>);
+  if constexpr (sizeof(T) == 2) {
+    if (ln_pair(s, KDA_BF16))
+      return s.edge ? run(ln_fwd_kernel<T, true, true, true, NR, true>)
+                    : run(ln_fwd_kernel<T, true, false, true, NR, true>);
+  }
   if (s.blk) return s.edge ? run(ln_fwd_kernel<T, true, true, true, NR>) : run(ln_fwd_kernel<T, true, false, true, NR>);
   return s.edge ? run(ln_fwd_kernel<T, false, true, true, NR>) : run(ln_fwd_kernel<T, false, false, true, NR>);
 }
