@@ -29,10 +29,9 @@
 //   D  entry state to exit state, n e^{-an} <S, R>
 //
 // The state stays in fp32 registers for a whole chain.  Operands that are not
-// inputs are rounded to bf16 where the product ends in a bf16 output (the pairs
-// and the state's rows: as much again as the output's own rounding, 2-norm
-// error 1.7e-3 -> 2.3e-3; a second part each, 16 bits, cost the chains a fifth of
-// their time), and split into three bf16 parts (24 bits) where it enters the fp32
+// inputs are split into bf16 parts: two (off by 2^-16 at most) where the
+// product ends in a bf16 output (the pairs and the state's rows), so that its only
+// rounding that counts is its own, and three (2^-24) where it enters the fp32
 // state or the decay gradient's sums.  fp32 io: kda_linear_f32.cu.
 #include "kda_linear.cuh"
 
@@ -191,6 +190,7 @@ __global__ void __launch_bounds__(FTH) lin_fold_kernel(LinP P, float* segc, cons
 }
 
 // ------------------------------------------------------------ bf16 chain
+constexpr int PART = 10 * 512;  // bytes of a part of a chunk's pairs (pair_at)
 // ONLY: state only (a segment's own state), no output rows.
 template <int DK, int DVS, bool ONLY>
 struct Shape {
@@ -202,8 +202,8 @@ struct Shape {
   static constexpr int XB = ONLY ? 0 : 128 * DK, YB = 128 * DK, ZB = 128 * DVS;
   static constexpr int STAGE = XB + YB + ZB;
   static constexpr int STG = DK == 128 || ONLY ? 2 : 1;
-  static constexpr int PB = ONLY ? 0 : 64 * 64 * 2, OB = ONLY ? 0 : 128 * DVS;
-  static constexpr int SMEM = 1024 /* alignment */ + STG * STAGE + PB + OB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
+  static constexpr int PB = ONLY ? 0 : 2 * PART, OB = ONLY ? 0 : 128 * DVS;
+  static constexpr int SMEM = 1024 /* alignment */ + STG * STAGE + PB + OB + 1024 /* lut */ + 272 /* tab */ + 512 + 32;
   static constexpr int NTK = DK / 8;  // 8-key tiles of a warp's state rows
   // resident CTAs: what registers and shared memory allow
   static constexpr int REGS = DK == 32 ? 168 : 255;
@@ -306,14 +306,26 @@ __device__ __forceinline__ void pair_products(float (&p)[B::N][2][4], FR row, FC
     }
   }
 }
+// A chunk's pairs in shared memory, two parts of the ten 16 x 16 blocks: rows of
+// 32 bytes whose two halves change places in every other group of four, so that
+// eight rows of a half lie in different banks.  (Whole 64 x 64 parts take the
+// 32/64 kernels' sixth CTA off an SM: 300M prompt 70 us, 57 so.)
+__host__ __device__ constexpr int pair_at(int r, int c) { return (r * (r + 1) / 2 + c) * 512; }
+// A lane's offset in a block; PAT as Frag's.
+template <int PAT>
+__device__ __forceinline__ uint32_t pair_lane() {
+  const int lane = threadIdx.x & 31, l7 = lane & 7, mi = lane >> 3;
+  const int r = PAT == 1 ? mi & 1 : mi >> 1, b = PAT == 1 ? mi >> 1 : mi & 1;
+  return (l7 + 8 * r) * 32 + ((b ^ (l7 >> 2)) << 4);
+}
 // Weights the pairs (lut: weights of a pair of neighbouring columns by distance,
 // index 64 at distance 0; sign: +1 where rows come after columns) and stores
-// them as bf16 in tP [64][64], blocks in the chain's order.
+// them as two parts in tP, blocks in the chain's order.
 template <class B>
 __device__ __forceinline__ void pair_store(float (&p)[B::N][2][4], const float2* lut, unsigned char* tP, int sign) {
   const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
   const float2* lp = lut + 64 + sign * (gq - 2 * tq);
-  unsigned char* pp = tP + gq * 128 + 4 * tq;
+  unsigned char* pp = tP + gq * 32 + 4 * tq;
 #pragma unroll
   for (int t = 0; t < B::N; t++) {
     const int r = B::row(t), c = B::col(t);
@@ -325,8 +337,11 @@ __device__ __forceinline__ void pair_store(float (&p)[B::N][2][4], const float2*
         const float2 w = lp[16 * (r - c) + sign * (8 * k - 8 * j)];
         p[t][j][2 * k] *= w.x;
         p[t][j][2 * k + 1] *= w.y;
-        *reinterpret_cast<uint32_t*>(pp + (16 * r + 8 * k) * 128 + (((2 * c + j) ^ gq) << 4)) =
-            pack2(p[t][j][2 * k], p[t][j][2 * k + 1]);
+        uint32_t s[2];
+        split2<2>(p[t][j][2 * k], p[t][j][2 * k + 1], s);
+        unsigned char* at = pp + pair_at(r, c) + 256 * k + ((j ^ (gq >> 2)) << 4);
+        *reinterpret_cast<uint32_t*>(at) = s[0];
+        *reinterpret_cast<uint32_t*>(at + PART) = s[1];
       }
   }
 }
@@ -406,11 +421,11 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
   constexpr int NTH = SH::NTH, NW = SH::NW, NTK = SH::NTK, MT = SH::MT;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (mma::smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned char* tP = smem + SH::STG * SH::STAGE;  // [64][64], blocks in the chain's order
+  unsigned char* tP = smem + SH::STG * SH::STAGE;  // the pairs, blocks in the chain's order
   unsigned char* tO = tP + SH::PB;                 // [64][DVS], the output's rows
   float2* lut = reinterpret_cast<float2*>(tO + SH::OB);
   float* tab = reinterpret_cast<float*>(lut + 128);  // [65] e^{-a m}
-  float* sw = tab + 96;                              // [64] weights of the chunk's rows in its state
+  float* sw = tab + 68;                              // [64] weights of the chunk's rows in its state
   float* rwt = sw + 64;                              // [64] weights of the entry state in its rows
   uint64_t* bar = reinterpret_cast<uint64_t*>(rwt + 64);  // [STG]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
@@ -466,7 +481,7 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
   const Frag<DK, 1> k1;   // x and y tiles
   const Frag<DK, 2> k2;
   const Frag<DVS, 2> v2;  // z tile
-  const Frag<64, 2> p2;   // pairs
+  const uint32_t p2 = mma::smem_u32(tP) + pair_lane<2>();
 
   bool good = true;
   int out_t0 = -1;  // first token of the output tile that waits in tO
@@ -533,7 +548,7 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
       for (int m = 0; m < MT; m++) mma::zero<8>(o[m]);
 #pragma unroll
       for (int kk = 0; kk < DK / 16; kk++) {
-        uint32_t f[MT][4], fb[4][4];
+        uint32_t f[MT][2][4], fb[4][4];
 #pragma unroll
         for (int p = 0; p < 4; p++) ldsm(fb[p], k2.at(tX, 16 * blk(p), 16 * kk));
 #pragma unroll
@@ -541,15 +556,20 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
 #pragma unroll
           for (int q = 0; q < 4; q++) {  // accumulator tiles 2 kk, 2 kk + 1 are the 16 x 16 operand
             const float* st2 = &S[m][2 * kk + (q >> 1)][2 * (q & 1)];
-            f[m][q] = pack2(st2[0], st2[1]);
+            uint32_t s[2];
+            split2<2>(st2[0], st2[1], s);
+            f[m][0][q] = s[0];
+            f[m][1][q] = s[1];
           }
 #pragma unroll
-        for (int m = 0; m < MT; m++)
+        for (int b = 1; b >= 0; b--)
 #pragma unroll
-          for (int p = 0; p < 4; p++) {
-            mma::mma_bf16(o[m][2 * p], f[m], fb[p][0], fb[p][1]);
-            mma::mma_bf16(o[m][2 * p + 1], f[m], fb[p][2], fb[p][3]);
-          }
+          for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+              mma::mma_bf16(o[m][2 * p], f[m][b], fb[p][0], fb[p][1]);
+              mma::mma_bf16(o[m][2 * p + 1], f[m][b], fb[p][2], fb[p][3]);
+            }
       }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
@@ -568,16 +588,19 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
         uint32_t zr[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; m++) ldsm_t(zr[m], v2.at(tZ, 16 * blk(kk), r0 + 16 * m));
-        uint32_t fb[4][4];
 #pragma unroll
-        for (int p = kk; p < 4; p++) ldsm(fb[p], p2.at(mma::smem_u32(tP), 16 * p, 16 * kk));
+        for (int b = 1; b >= 0; b--) {
+          uint32_t fb[4][4];
 #pragma unroll
-        for (int m = 0; m < MT; m++)
+          for (int p = kk; p < 4; p++) ldsm(fb[p], p2 + b * PART + pair_at(p, kk));
 #pragma unroll
-          for (int p = kk; p < 4; p++) {
-            mma::mma_bf16(o[m][2 * p], zr[m], fb[p][0], fb[p][1]);
-            mma::mma_bf16(o[m][2 * p + 1], zr[m], fb[p][2], fb[p][3]);
-          }
+          for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int p = kk; p < 4; p++) {
+              mma::mma_bf16(o[m][2 * p], zr[m], fb[p][0], fb[p][1]);
+              mma::mma_bf16(o[m][2 * p + 1], zr[m], fb[p][2], fb[p][3]);
+            }
+        }
       }
       // ---- out: transposed into tO, and from there as a tile (a chunk that is not full: row by row)
 #pragma unroll
@@ -698,9 +721,9 @@ struct DShape {
   // one chunk's tiles: a second set would hide their loads, but takes more CTAs off the SM than that is worth
   // (32/64 74 us for 69, 64/64 at 8 x 4096 tokens 105 for 94)
   static constexpr int STAGE = 2 * OB + 2 * QB;
-  static constexpr int PB = 64 * 64 * 2;
-  static constexpr int SMEM = 1024 + STAGE + PB + 1024 /* lut */ + 384 /* tab */ + 512 + 32;
-  static constexpr int SP = DA ? 3 : 1;  // parts of the states as operands: their rows enter fp32 sums
+  static constexpr int PB = 2 * PART;
+  static constexpr int SMEM = 1024 + STAGE + PB + 1024 /* lut */ + 272 /* tab */ + 512 + 32;
+  static constexpr int SP = DA ? 3 : 2;  // parts of the states as operands: fp32 sums need the third
   static constexpr int BY_REG = 65536 / (NTH * 168), BY_SMEM = 227 * 1024 / (SMEM + 1024);
   static constexpr int CTAS = BY_REG < BY_SMEM ? BY_REG : BY_SMEM;
 };
@@ -721,10 +744,10 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
   constexpr int NTH = SH::NTH, NW = SH::NW, SP = SH::SP;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (mma::smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned char* tP = smem + SH::STAGE;  // [64][64]
+  unsigned char* tP = smem + SH::STAGE;  // the pairs
   float2* lut = reinterpret_cast<float2*>(tP + SH::PB);
   float* tab = reinterpret_cast<float*>(lut + 128);
-  float* rq = tab + 96;  // [64] scale e^{-a(i+1)}
+  float* rq = tab + 68;  // [64] scale e^{-a(i+1)}
   float* rk = rq + 64;   // [64] e^{-a(n-1-j)}
   uint64_t* bar = reinterpret_cast<uint64_t*>(rk + 64);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
@@ -788,8 +811,7 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
   const Frag<DV, 2> o2;
   const Frag<DVS, 1> v1;  // q and k tiles
   const Frag<DVS, 2> v2;
-  const Frag<64, 1> p1;   // pairs
-  const Frag<64, 2> p2;
+  const uint32_t p1 = mma::smem_u32(tP) + pair_lane<1>(), p2 = mma::smem_u32(tP) + pair_lane<2>();
 
   double dacc = 0.0;
   bool good = true;
@@ -850,8 +872,11 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
             const float2 w = lut[64 + d + 8 * k - 8 * j];
             p[t][j][2 * k] *= w.x;
             p[t][j][2 * k + 1] *= w.y;
-            unsigned char* at = tP + (16 * rr[t] + 8 * k + gq) * 128 + (((2 * cc[t] + j) ^ gq) << 4) + 4 * tq;
-            *reinterpret_cast<uint32_t*>(at) = pack2(p[t][j][2 * k], p[t][j][2 * k + 1]);
+            uint32_t s[2];
+            split2<2>(p[t][j][2 * k], p[t][j][2 * k + 1], s);
+            unsigned char* at = tP + pair_at(rr[t], cc[t]) + (8 * k + gq) * 32 + ((j ^ (gq >> 2)) << 4) + 4 * tq;
+            *reinterpret_cast<uint32_t*>(at) = s[0];
+            *reinterpret_cast<uint32_t*>(at + PART) = s[1];
           }
         if constexpr (DA) {  // A: the same pairs of q and k (this slice's columns)
           float m2[2][4];
@@ -944,24 +969,26 @@ __global__ void __launch_bounds__(DShape<DV, DVS, DA>::NTH, DShape<DV, DVS, DA>:
     if (tid == 0 && c + 1 < nch) load_ov(c + 1);
     // ---- dq^T += k^T P^T, dk^T += q^T P
 #pragma unroll
-    for (int kk = 0; kk < 4; kk++) {
-      const uint32_t tp = mma::smem_u32(tP);
-      uint32_t fp[4][4];
+    for (int kk = 0; kk < 4; kk++)
 #pragma unroll
-      for (int p = kk; p < 4; p++) ldsm(fp[p], p2.at(tp, 16 * p, 16 * kk));  // tokens i of block p, j of kk
+      for (int b = 1; b >= 0; b--) {
+        uint32_t fp[4][4];
 #pragma unroll
-      for (int p = kk; p < 4; p++) {
-        mma::mma_bf16(dq[2 * p], fk[kk], fp[p][0], fp[p][1]);
-        mma::mma_bf16(dq[2 * p + 1], fk[kk], fp[p][2], fp[p][3]);
+        for (int p = kk; p < 4; p++) ldsm(fp[p], p2 + b * PART + pair_at(p, kk));  // tokens i of block p, j of kk
+#pragma unroll
+        for (int p = kk; p < 4; p++) {
+          mma::mma_bf16(dq[2 * p], fk[kk], fp[p][0], fp[p][1]);
+          mma::mma_bf16(dq[2 * p + 1], fk[kk], fp[p][2], fp[p][3]);
+        }
+#pragma unroll
+        for (int p = 0; p <= kk; p++)
+          ldsm_t(fp[p], p1 + b * PART + pair_at(kk, p));  // tokens i of block kk, j of p
+#pragma unroll
+        for (int p = 0; p <= kk; p++) {
+          mma::mma_bf16(dk[2 * p], fq[kk], fp[p][0], fp[p][1]);
+          mma::mma_bf16(dk[2 * p + 1], fq[kk], fp[p][2], fp[p][3]);
+        }
       }
-#pragma unroll
-      for (int p = 0; p <= kk; p++) ldsm_t(fp[p], p1.at(tp, 16 * kk, 16 * p));  // tokens i of block kk, j of p
-#pragma unroll
-      for (int p = 0; p <= kk; p++) {
-        mma::mma_bf16(dk[2 * p], fq[kk], fp[p][0], fp[p][1]);
-        mma::mma_bf16(dk[2 * p + 1], fq[kk], fp[p][2], fp[p][3]);
-      }
-    }
     // ---- out, in the place of the q and k tiles (their last reads were before the barrier)
     unsigned char *uQ = smem + 2 * SH::OB, *uK = uQ + SH::QB;
     stage_tile<DVS>(uQ, 16 * warp, dq, false);

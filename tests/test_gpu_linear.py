@@ -11,6 +11,9 @@ inputs (the sum of the magnitudes of the terms of each output):
  - fp32 io.  Three parts (2^-24) per operand, six products: below 100 sums per
    chunk and product, 100 * 2^-23 < 2^-16, M; plus 2^-24 of the value.
 The decays add a few 2^-23 of a term times a m e^-am <= 1/e, well inside both.
+The bound on bf16 outputs above is wider than the kernels need: they keep every
+computed operand in two bf16 parts, off by 2^-16 of itself, and
+test_outputs_are_rounded_once holds them to that.
 """
 import numpy as np
 import pytest
@@ -469,3 +472,29 @@ def test_python_refusals_on_the_device():
         kda.kda_linear_decode_step(z, z, torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda"), d["A_log"],
                                    torch.zeros(0, 2, 32, 64, device="cuda"))
     assert _lib.load() is not None
+
+
+def check_rounded_once(got, res):
+    """bf16 outputs y of a value r are its rounding, but where the computed value
+    c lies across a border: |y - r| <= |y - c| + d <= |bf16(r) - c| + d <=
+    |bf16(r) - r| + 2 d with d = |c - r|.  A term passes at most two computed
+    operands, each off by 2^-16, and the fp32 sums of at most 64 + 16 products a
+    chunk add as much again (80 * 2^-23): d <= 2^-14 M per element.  In the 2-norm
+    the terms' errors are as independent as the terms themselves, whose sum r is:
+    d <= (2 * 2^-16 + 2^-16) |r|, below 2^-14 |r|."""
+    for n in ("o", "dq", "dk", "dv"):
+        r = res["ref"][n]
+        g = got[n].double().cpu().numpy().reshape(r.shape)
+        once = np.abs(torch.from_numpy(r).to(torch.bfloat16).double().numpy() - r)
+        bad = ~(np.abs(g - r) <= once + 2 * 2.0 ** -14 * np.abs(res["mag"][n]) + 1e-30)
+        assert not bad.any(), (n, int(bad.sum()))
+        e, lim = np.linalg.norm(g - r), np.linalg.norm(once) + 2 * 2.0 ** -14 * np.linalg.norm(r)
+        assert e <= lim, (n, e / np.linalg.norm(r), lim / np.linalg.norm(r))
+
+
+@pytest.mark.parametrize("rows", [False, True])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_outputs_are_rounded_once(dk, dv, rows):
+    docs = [301, 301] if rows else [5, 0, 300, 1, 64, 700]
+    x = make(40 + dk + dv, docs, 2, dk, dv, "bf16", rows=rows)
+    check_rounded_once(run(x), oracle(x))
