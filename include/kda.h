@@ -409,7 +409,8 @@ KDA_API kda_status kda_linear_fwd(const kda_problem* p, const void* q, const voi
  * save_for_backward = 1 (another workspace is refused by the device:
  * KDA_ERR_WORKSPACE from kda_device_status).  Writes dq, dk, dv (dtype),
  * dA_log [H] and dh0 (fp32; either may be NULL: not returned; without dA_log
- * its extra products are skipped).  Sums run in a fixed order: deterministic.
+ * its extra products are skipped, and the others keep their bits).  Sums run in a
+ * fixed order: deterministic.
  * The workspace may be used by several backwards of one forward, one at a
  * time. */
 KDA_API kda_status kda_linear_bwd(const kda_problem* p, const void* q, const void* k, const void* v,

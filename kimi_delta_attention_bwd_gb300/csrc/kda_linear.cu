@@ -723,7 +723,9 @@ struct DShape {
   static constexpr int STAGE = 2 * OB + 2 * QB;
   static constexpr int PB = 2 * PART;
   static constexpr int SMEM = 1024 + STAGE + PB + 1024 /* lut */ + 272 /* tab */ + 512 + 32;
-  static constexpr int SP = DA ? 3 : 2;  // parts of the states as operands: fp32 sums need the third
+  // parts of the states as operands: the decay gradient's fp32 sums need the third, and dq and dk keep their bits
+  // whether it is wanted or not
+  static constexpr int SP = 3;
   static constexpr int BY_REG = 65536 / (NTH * 168), BY_SMEM = 227 * 1024 / (SMEM + 1024);
   static constexpr int CTAS = BY_REG < BY_SMEM ? BY_REG : BY_SMEM;
 };

@@ -103,7 +103,8 @@ def kda_linear_forward(q, k, v, A_log, scale: Optional[float] = None, h0=None, c
 def kda_linear_backward(ctx: LinearContext, dO, dh_final=None, want_dA_log: bool = True, want_dh0: bool = True):
     """Backward of sum(o * dO) + sum(h_final * dh_final).  Returns a dict with
     dq, dk, dv (io dtype), dA_log and dh0 (fp32; None where not wanted:
-    without dA_log, e.g. for fixed decays, its products are skipped)."""
+    without dA_log, e.g. for fixed decays, its products are skipped, and the
+    others keep their bits)."""
     if not ctx.saved:
         raise ValueError("the forward saved nothing: call kda_linear_forward with save_for_backward=True")
     q, v = ctx.q, ctx.v

@@ -498,3 +498,16 @@ def test_outputs_are_rounded_once(dk, dv, rows):
     docs = [301, 301] if rows else [5, 0, 300, 1, 64, 700]
     x = make(40 + dk + dv, docs, 2, dk, dv, "bf16", rows=rows)
     check_rounded_once(run(x), oracle(x))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_unwanted_gradients_leave_the_others_bits(dk, dv, dt):
+    # a frozen A_log or an h0 that needs no gradient: dq, dk and dv are what they are with them
+    x = make(50 + dk + dv, [70, 400, 3], 2, dk, dv, dt)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    _, _, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=d["h0"], cu_seqlens=d["cu"])
+    a = kda.kda_linear_backward(ctx, d["dO"], d["dh"])
+    b = kda.kda_linear_backward(ctx, d["dO"], d["dh"], want_dA_log=False, want_dh0=False)
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(a[n], b[n]), n
