@@ -1187,7 +1187,10 @@ void lin_plan(const kda_problem* p, const Dims& d, LinP& P) {
       for (int i = 0; i < d.n_docs; i++) P.seg |= p->cu_seqlens_host[i + 1] - p->cu_seqlens_host[i] > L;
     }
   }
-  P.tag = d.tag ^ 0x4c696e;
+  // the sizes' hash, and what else the layout of a saved workspace follows
+  uint32_t tag = (uint32_t)d.tag ^ 0x4c696eu;
+  for (const int32_t v : {P.rows, P.L}) tag = (tag ^ (uint32_t)v) * 16777619u;
+  P.tag = (int32_t)(tag | 1u);
 }
 
 LinLayout lin_layout(const kda_problem* p, const Dims& d, const LinP& P, int for_bwd) {

@@ -511,3 +511,20 @@ def test_unwanted_gradients_leave_the_others_bits(dk, dv, dt):
     b = kda.kda_linear_backward(ctx, d["dO"], d["dh"], want_dA_log=False, want_dh0=False)
     for n in ("dq", "dk", "dv"):
         assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("saved", ["rows", "offsets"])
+def test_a_workspace_saved_for_rows_does_not_serve_offsets(saved, dt):
+    # the same sizes and as many documents, but another layout of the workspace
+    x = make(60, [320, 320], 2, 32, 64, dt, rows=True)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    cu = torch.tensor([0, 320, 640], dtype=torch.int32, device="cuda")
+    size = max(_lib.kda_linear_workspace_size(_lib.make_problem(2, 320, 2, 32, 64, d["q"].dtype, None, c), True)
+               for c in (None, cu))
+    _, _, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], cu_seqlens=None if saved == "rows" else cu,
+                                       workspace=torch.empty(size, dtype=torch.uint8, device="cuda"))
+    assert kda.kda_device_status(ctx.workspace) == 0
+    ctx.problem = _lib.make_problem(2, 320, 2, 32, 64, d["q"].dtype, None, cu if saved == "rows" else None)
+    kda.kda_linear_backward(ctx, d["dO"])
+    assert kda.kda_device_status(ctx.workspace) == -5
