@@ -385,7 +385,7 @@ KDA_API kda_status kda_short_conv_bwd(int64_t n_tok, int C, int dtype, int activ
  * q and k enter as they are (no L2 norm).  Sizes, layouts, dtypes, documents
  * (rows or cu_seqlens), h0 / h_final and statuses are those of kda_fwd; the
  * problem's gate must be KDA_GATE_CHANNEL (it is not used).  A_log : [H] fp32;
- * A_log = -inf is no decay.  Inputs are finite: a chunk's pairs are formed as
+ * A_log = -inf is no decay, a NaN reaches its head's outputs.  Inputs are finite: a chunk's pairs are formed as
  * matrix products, so an infinity or NaN at one token also reaches its
  * document's other tokens, up to 63 before it (never another document's).
  * The workspace (kda_linear_workspace_size(p, for_backward) bytes, 256-byte

@@ -86,7 +86,11 @@ __device__ __forceinline__ void rows_reset(const LinP& P) {
   }
 }
 
-__device__ __forceinline__ float decay_of(const float* A_log, int h) { return fminf(expf(A_log[h]), 1e30f); }
+// a = exp(A_log), finite (0 tokens of an infinite decay would be NaN); a NaN stays one.
+__device__ __forceinline__ float decay_of(const float* A_log, int h) {
+  const float a = expf(A_log[h]);
+  return a > 1e30f ? 1e30f : a;
+}
 __device__ __forceinline__ float decay_pow(float a, int m) { return m > 0 ? expf(-a * (float)m) : 1.0f; }
 
 // Launches k, behind another kernel of the same call as its programmatic

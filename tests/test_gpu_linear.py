@@ -528,3 +528,25 @@ def test_a_workspace_saved_for_rows_does_not_serve_offsets(saved, dt):
     ctx.problem = _lib.make_problem(2, 320, 2, 32, 64, d["q"].dtype, None, cu if saved == "rows" else None)
     kda.kda_linear_backward(ctx, d["dO"])
     assert kda.kda_device_status(ctx.workspace) == -5
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_decay_that_is_not_a_number_shows(dt):
+    # a diverged A_log of one head reaches that head's outputs, and no other head's
+    x = make(61, [90, 400, 1], 3, 32, 64, dt, A=[-2.0, -1.0, 0.0])
+    y = dict(x, A_log=torch.tensor([-2.0, float("nan"), 0.0]))
+    a, b = run(x), run(y)
+    for n in ("o", "dq", "dv", "h_final", "dh0", "dA_log"):
+        g = b[n][:, 1] if n in ("h_final", "dh0") else b[n][1] if n == "dA_log" else b[n][:, :, 1]
+        assert bool(torch.isnan(g).all() if n != "dv" else torch.isnan(g[:, :89]).all()), n
+    for h in (0, 2):
+        for n in ("o", "dq", "dk", "dv"):
+            assert torch.equal(a[n][:, :, h], b[n][:, :, h]), n
+        for n in ("h_final", "dh0"):
+            assert torch.equal(a[n][:, h], b[n][:, h]), n
+        assert torch.equal(a["dA_log"][h], b["dA_log"][h])
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in y.items()}
+    state = d["h0"].clone()
+    o = kda.kda_linear_decode_step(*(d[n][0, :3].contiguous() for n in ("q", "k", "v")), d["A_log"], state)
+    assert bool(torch.isnan(o[:, 1]).all()) and bool(torch.isnan(state[:, 1]).all())
+    assert bool(torch.isfinite(o[:, ::2]).all()) and bool(torch.isfinite(state[:, ::2]).all())
