@@ -469,31 +469,43 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_BWD_THR 
 }
 
 // Rows wider than 32 columns for each of LN_CTHR threads: a CTA per row, the row read once per pass (its
-// later passes hit L2), the backward's column sums in its partial row.
-__device__ __forceinline__ float one_sum(float x, float (*red)[32]) {
-  float v[1] = {x};
-  row_sums<true>(v, 0, red);
-  return v[0];
-}
+// later passes hit L2), the backward's column sums in its partial row.  A thread's sums, of up to 2^15 values
+// here, are compensated (Kahan 1965).
+struct LongSum {
+  float s = 0.f, c = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float y = x - c, t = s + y;
+    c = (t - s) - y;
+    s = t;
+  }
+};
 
 template <typename T>
 __global__ void __launch_bounds__(LN_CTHR) ln_fwd_wide_kernel(int64_t n, int D, float eps, const T* __restrict__ x,
                                                            const float* __restrict__ w, const float* __restrict__ b,
                                                            T* __restrict__ y, float* __restrict__ mean,
                                                            float* __restrict__ rstd) {
-  __shared__ float red[2][1][32];
+  __shared__ float red[2][2][32];
   const float inv = 1.0f / (float)D;
   for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
     const T* xr = x + row * D;
-    float s = 0.f;
-    for (int c = threadIdx.x; c < D; c += blockDim.x) s += ldf(xr + c);
-    const float mu = one_sum(s, red[0]) * inv;
-    float q = 0.f;
+    LongSum s;
+    for (int c = threadIdx.x; c < D; c += blockDim.x) s.add(ldf(xr + c));
+    float m[1] = {s.s};
+    row_sums<true>(m, 0, red[0]);
+    float mu = m[0] * inv;
+    // the centred values' own mean is what rounding left in mu: against a spread near sqrt(eps) it would show
+    LongSum q, t;
     for (int c = threadIdx.x; c < D; c += blockDim.x) {
       const float d = ldf(xr + c) - mu;
-      q += d * d;
+      q.add(d * d);
+      t.add(d);
     }
-    const float r = 1.0f / sqrtf(one_sum(q, red[1]) * inv + eps);
+    float v[2] = {q.s, t.s};
+    row_sums<true>(v, 0, red[1]);
+    const float off = v[1] * inv, var = v[0] * inv - off * off;
+    mu += off;
+    const float r = 1.0f / sqrtf((var < 0.f ? 0.f : var) + eps);
     if (mean && threadIdx.x == 0) {
       mean[row] = mu;
       rstd[row] = r;
@@ -510,22 +522,24 @@ __global__ void __launch_bounds__(LN_CTHR) ln_bwd_wide_kernel(int64_t n, int D, 
                                                            const float* __restrict__ mean,
                                                            const float* __restrict__ rstd, T* __restrict__ dx,
                                                            float* __restrict__ part) {
-  __shared__ float red[2][1][32];
+  __shared__ float red[2][32];
   const float inv = 1.0f / (float)D;
   float* pw = part + (int64_t)blockIdx.x * 2 * D;
   pdl_release();
   for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
     const float mu = mean[row], r = rstd[row];
     const bool first = row == blockIdx.x;
-    float s1 = 0.f, s2 = 0.f;
+    LongSum s1, s2;
     for (int c = threadIdx.x; c < D; c += blockDim.x) {
       const float h = (ldf(x + row * D + c) - mu) * r, d = ldf(dy + row * D + c), g = d * w[c];
       pw[c] = (first ? 0.f : pw[c]) + d * h;
       pw[D + c] = (first ? 0.f : pw[D + c]) + d;
-      s1 += g;
-      s2 += g * h;
+      s1.add(g);
+      s2.add(g * h);
     }
-    const float m1 = one_sum(s1, red[0]) * inv, m2 = one_sum(s2, red[1]) * inv;
+    float m[2] = {s1.s, s2.s};
+    row_sums<true>(m, 0, red);
+    const float m1 = m[0] * inv, m2 = m[1] * inv;
     for (int c = threadIdx.x; c < D; c += blockDim.x) {
       const float h = (ldf(x + row * D + c) - mu) * r;
       stf(dx + row * D + c, r * (ldf(dy + row * D + c) * w[c] - m1 - h * m2));

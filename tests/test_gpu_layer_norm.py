@@ -213,3 +213,31 @@ def test_refusals_on_the_device():
     with pytest.raises(kda.KdaError, match="WORKSPACE"):
         s = torch.zeros(4, device="cuda")
         kda.kda_layer_norm_backward(x, w, x, s, s, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def flat(seed, n, D, dt, spread):
+    """Rows around 0.3, which no sum of copies represents exactly."""
+    t = make(seed, n, D, dt)
+    return dict(t, x=(0.3 + spread * torch.randn(n, D, generator=torch.Generator().manual_seed(D))).to(DT[dt]))
+
+
+# the bound by path.  Rows in registers: 16 (32 above 8192 columns) serial values and log2 levels per sum, the
+# 2^-18 (1 + mean |x| r) of above.  Rows above 16384 columns: compensated sums, and a mean that is corrected by its
+# own residual: 2^-24 |mu| r of its last rounding, 2^-24 each of x - mu, r's three operations (half of the
+# variance's 2^-22), xh and the product with w, below 2^-21 (1 + mean |x| r) in all.
+@pytest.mark.parametrize("spread", [0.0, 1e-4])
+@pytest.mark.parametrize("n,D", [(5, 300), (3, 5003), (3, 12001), (3, 40000), (2, 1 << 20)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_of_little_spread(n, D, dt, spread):
+    t = flat(n, n, D, dt, spread)
+    lim = limits(**t, dt=dt)
+    if D > 16384:
+        for k, rnd in (("y", ROUND[dt]), ("dx", ROUND[dt])):
+            ref, tol = lim[k]
+            lim[k] = (ref, (tol - rnd * np.abs(ref)) / 8 + rnd * np.abs(ref))
+    check(run(t), lim)
+
+
+def test_the_widest_rows():
+    t = flat(9, 2, 1 << 24, "f32", 1e-4)
+    check(run(t), limits(**t, dt="f32"))
