@@ -241,3 +241,22 @@ def test_rows_of_little_spread(n, D, dt, spread):
 def test_the_widest_rows():
     t = flat(9, 2, 1 << 24, "f32", 1e-4)
     check(run(t), limits(**t, dt="f32"))
+
+
+# At least three rows to a group of threads, of a number that leaves the last ones ragged: the groups' rows keep
+# their columns, the next rows come while one is summed, dw and db are carried over the rows.  Widths with and
+# without edges of: lane groups, one-row CTAs, two CTAs per SM (5003, 5120 in bf16), sums in shared memory (8200 to
+# 16384, in fp32 with and without room for the next row), rows read in passes.
+MANY = [(120001, 17), (40003, 100), (20011, 256), (6007, 513), (4001, 1001), (2503, 2050), (1013, 5003), (1013, 5120),
+        (509, 6144), (501, 8200), (501, 10001), (480, 13001), (470, 14400), (470, 16384), (470, 16386), (461, 20001)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n,D", MANY)
+def test_many_rows_to_a_group(n, D, dt):
+    t = make(n + D, n, D, dt)
+    lim = limits(**t, dt=dt)
+    check(run(t), lim)
+    x = t["x"].cuda()
+    kda.kda_layer_norm(x, t["w"].cuda(), t["b"].cuda(), out=x)
+    check(dict(y=x), {"y": lim["y"]})
