@@ -550,3 +550,18 @@ def test_a_decay_that_is_not_a_number_shows(dt):
     o = kda.kda_linear_decode_step(*(d[n][0, :3].contiguous() for n in ("q", "k", "v")), d["A_log"], state)
     assert bool(torch.isnan(o[:, 1]).all()) and bool(torch.isnan(state[:, 1]).all())
     assert bool(torch.isfinite(o[:, ::2]).all()) and bool(torch.isfinite(state[:, ::2]).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [False, True])
+def test_a_document_of_many_pieces(rows, dt):
+    # about twenty pieces of 256 tokens and a shorter last one: the fold takes them eight at a time, in place
+    docs = [5001] if rows else [40, 5001, 1, 70]
+    x = make(70, docs, 1, 32, 64, dt, rows=rows)
+    prob = _lib.make_problem(1, sum(docs), 1, 32, 64, x["q"].dtype, None, None if rows else x["cu"])
+    prob.cu_seqlens_host = None if rows else x["cu"].data_ptr()
+    states = 4 * 32 * 64
+    assert _lib.kda_linear_workspace_size(prob, False) > 18 * states  # (a state a piece)
+    check(run(x), oracle(x), dt)
+    if dt == "bf16":
+        check_rounded_once(run(x), oracle(x))
