@@ -506,7 +506,7 @@ __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u
           for (int k = 0; k < 2; k++)
             *reinterpret_cast<float2*>(p + 16 * m * DK + 128 * j + 64 * k) =
                 make_float2(w * S[m][j][2 * k], w * S[m][j][2 * k + 1]);
-      if (!rev && h == 0 && slice == 0 && tid == 0) P.chunks[un.ch0 + idx] = make_int2(t0, n);
+      if (!rev && !P.rows && h == 0 && slice == 0 && tid == 0) P.chunks[un.ch0 + idx] = make_int2(t0, n);
     }
     good = mma::mbar_wait(bar + st, (SH::STG == 2 ? c >> 1 : c) & 1);
     if (n != n_w) {  // the first chunk, and the one that is not full
@@ -1208,7 +1208,7 @@ LinLayout lin_layout(const kda_problem* p, const Dims& d, const LinP& P, int for
   const bool seg = P.rows ? P.seg : d.Ntok > P.L;
   L.off_segf = take(seg ? P.nu * st : 0);
   if (for_bwd) {
-    L.off_chunks = take(8 * (size_t)P.nc);
+    L.off_chunks = take(!P.rows && p->dtype == KDA_BF16 ? 8 * (size_t)P.nc : 0);
     L.off_segr = take(seg ? P.nu * st : 0);
     L.off_S = take(P.nc * st);
     if (p->dtype == KDA_F32) {

@@ -24,7 +24,7 @@ struct LinP {
   int4* units;                   // {document, first token, tokens, segment}
   int2* unit_at;                 // {first chunk, segments of the document}
   int2* longs;                   // split documents: {first unit, segments}
-  int2* chunks;                  // {first token, tokens}, written by the saving forward's chains
+  int2* chunks;                  // {first token, tokens} by packed documents' chunk, from the saving bf16 forward
 };
 
 // One application of the operator (see above).  z, out and the state's value

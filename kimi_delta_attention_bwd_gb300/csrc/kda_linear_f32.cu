@@ -268,10 +268,7 @@ __device__ void chain(const LinP& P, const LinOp& op, int u, int h, int slice) {
     }
     if (!ONLY && st_rows) {
       const int64_t at0 = ((int64_t)(un.ch0 + idx) * H + h) * stN;
-      if (op.states) {  // the saving forward: [dv][dk]
-        each_at(1, [&](float& s, int64_t at) { op.states[at0 + at] = s; });
-        if (h == 0 && slice == 0 && tid == 0) P.chunks[un.ch0 + idx] = make_int2((int)rw.t0, n);
-      }
+      if (op.states) each_at(1, [&](float& s, int64_t at) { op.states[at0 + at] = s; });  // saving forward: [dv][dk]
       if constexpr (DEC == 2) {  // D: n e^{-an} <the chunk's exit gradient, its entry state>
         float part = 0.f;
         each_at(0, [&](float& s, int64_t at) { part = fmaf(s, op.ent[at0 + at], part); });
