@@ -113,15 +113,16 @@ class _LinearAttention(torch.autograd.Function):
                                          cu_seqlens_host=cu_seqlens_host,
                                          save_for_backward=recorded and any(fctx.needs_input_grad),
                                          want_final_state=want_final)
-        fctx.save_for_backward(q, k, v, A_log, h0, cu_seqlens)
-        fctx.rest = (lctx.problem, lctx.cu_seqlens_host, lctx.workspace, lctx.n_docs, lctx.saved)
+        # (the workspace, which holds every chunk's states, among them: freed by the backward, seen by hooks)
+        fctx.save_for_backward(q, k, v, A_log, h0, cu_seqlens, lctx.workspace)
+        fctx.rest = (lctx.problem, lctx.cu_seqlens_host, lctx.n_docs, lctx.saved)
         return (o, hf) if want_final else o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(fctx, dO, dhf=None):
-        q, k, v, A_log, h0, cu_seqlens = fctx.saved_tensors
-        problem, cu_host, workspace, n_docs, saved = fctx.rest
+        q, k, v, A_log, h0, cu_seqlens, workspace = fctx.saved_tensors
+        problem, cu_host, n_docs, saved = fctx.rest
         lctx = LinearContext(problem, q, k, v, A_log, h0, cu_seqlens, cu_host, workspace, n_docs, saved)
         dO = torch.zeros_like(v) if dO is None else _given(dO)
         g = kda_linear_backward(lctx, dO, None if dhf is None else _given(dhf),

@@ -565,3 +565,30 @@ def test_a_document_of_many_pieces(rows, dt):
     check(run(x), oracle(x), dt)
     if dt == "bf16":
         check_rounded_once(run(x), oracle(x))
+
+
+def test_the_workspace_is_a_saved_tensor():
+    # freed by the backward while an output lives, and moved by the hooks that move saved tensors
+    x = make(71, [700, 1, 300], 2, 64, 64, "bf16")
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    ref = run(x)
+    size = _lib.kda_linear_workspace_size(_lib.make_problem(1, 1001, 2, 64, 64, torch.bfloat16, None, d["cu"]), True)
+
+    def step():
+        leaves = [d[n].clone().requires_grad_() for n in ("q", "k", "v", "A_log", "h0")]
+        out = kda.linear_attention(*leaves[:4], h0=leaves[4], cu_seqlens=d["cu"], cu_seqlens_host=x["cu"],
+                                   output_final_state=True)
+        return leaves, out
+
+    leaves, out = step()
+    grads = [torch.empty_like(t) for t in leaves]
+    before = torch.cuda.memory_allocated()
+    for g, t in zip(grads, torch.autograd.grad(out, leaves, [d["dO"], d["dh"]])):
+        g.copy_(t)
+    del t
+    assert before - torch.cuda.memory_allocated() >= size
+    with torch.autograd.graph.save_on_cpu():
+        leaves, out = step()
+    moved = torch.autograd.grad(out, leaves, [d["dO"], d["dh"]])
+    for a, b, n in zip(grads, moved, ("dq", "dk", "dv", "dA_log", "dh0")):
+        assert torch.equal(a, ref[n]) and torch.equal(b, ref[n]), n
