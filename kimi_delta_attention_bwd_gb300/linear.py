@@ -84,6 +84,10 @@ def kda_linear_forward(q, k, v, A_log, scale: Optional[float] = None, h0=None, c
                  cu_seqlens=(cu_seqlens, (n_docs + 1,), torch.int32))
     if save_for_backward and h0 is not None and final_state is not None and h0.data_ptr() == final_state.data_ptr():
         raise ValueError("final_state cannot be h0 when the call saves for the backward")
+    if save_for_backward and cu_seqlens_host is not None:
+        # the backward plans by them again: a buffer that the next batch's offsets overwrite must not change them
+        cu_seqlens_host = (cu_seqlens_host.clone() if isinstance(cu_seqlens_host, torch.Tensor)
+                           else cu_seqlens_host.copy())
     prob = _lib.make_problem(B, T, H, dk, dv, io, scale, cu_seqlens, cu_seqlens_host)
     if workspace is None:
         # (size 0 for a problem that the call below refuses with its own status)

@@ -592,3 +592,21 @@ def test_the_workspace_is_a_saved_tensor():
     moved = torch.autograd.grad(out, leaves, [d["dO"], d["dh"]])
     for a, b, n in zip(grads, moved, ("dq", "dk", "dv", "dA_log", "dh0")):
         assert torch.equal(a, ref[n]) and torch.equal(b, ref[n]), n
+
+
+@pytest.mark.parametrize("kind", ["tensor", "array"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_host_offsets_overwritten_between_the_passes(dt, kind):
+    # one host buffer for every batch's offsets, the next batch's (nothing to cut) in it before this one's backward
+    x = make(72, [600, 0, 100], 2, 32, 64, dt)
+    ref = run(x)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    host = x["cu"].clone() if kind == "tensor" else x["cu"].numpy().copy()
+    _, _, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=d["h0"], cu_seqlens=d["cu"],
+                                       cu_seqlens_host=host)
+    for i, n in enumerate((0, 240, 480, 700)):
+        host[i] = n
+    got = kda.kda_linear_backward(ctx, d["dO"], d["dh"])
+    assert kda.kda_device_status(ctx.workspace) == 0
+    for n in got:
+        assert torch.equal(got[n], ref[n]), n
