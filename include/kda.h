@@ -399,7 +399,7 @@ KDA_API kda_status kda_short_conv_bwd(int64_t n_tok, int C, int dtype, int activ
  * last bits can differ between batches of other sizes).  With cu_seqlens_host
  * and no document to cut, none is cut in a replay on other offsets either.
  * Outputs must not overlap inputs, but for h_final, which may be h0 where
- * nothing is saved. */
+ * nothing is saved (KDA_ERR_INVALID_ARG where something is). */
 KDA_API size_t kda_linear_workspace_size(const kda_problem* p, int for_backward);
 KDA_API kda_status kda_linear_fwd(const kda_problem* p, const void* q, const void* k, const void* v,
                    const float* A_log, const float* h0, void* o, float* h_final,

@@ -1434,6 +1434,7 @@ extern "C" KDA_API kda_status kda_linear_fwd(const kda_problem* p, const void* q
   const kda_status c = check_problem(p, &d);
   if (c != KDA_OK) return c;
   if (!q || !k || !v || !A_log || !o) return KDA_ERR_INVALID_ARG;
+  if (save_for_backward && h0 && h_final == h0) return KDA_ERR_INVALID_ARG;  // (the backward reads h0)
   const void* ptrs[] = {q, k, v, A_log, h0, o, h_final};
   for (const void* x : ptrs)
     if (!al(x, 16)) return KDA_ERR_ALIGNMENT;

@@ -199,3 +199,12 @@ def test_python_entry_points_refuse_host_tensors_and_bad_shapes():
         kda.kda_layer_norm(torch.zeros(2, 8), torch.ones(8))
     with pytest.raises(ValueError, match="last axis"):
         kda.kda_layer_norm(torch.zeros(2, 0), torch.ones(0))
+
+
+def test_linear_refuses_a_final_state_over_a_saved_h0():
+    # every other argument is valid but the workspace, which is checked last: nothing is launched
+    P = ctypes.c_void_p
+    call = lambda save, h_final: _lib.load().kda_linear_fwd(  # noqa: E731
+        ctypes.byref(_prob()), P(FAKE), P(FAKE), P(FAKE), P(FAKE), P(FAKE), P(FAKE), P(h_final), save, None, 0, None)
+    assert call(1, FAKE) == -1
+    assert call(0, FAKE) == -5 and call(1, 2 * FAKE) == -5
