@@ -110,6 +110,17 @@ def _require(**specs):
             raise ValueError(f"{name} is on {t.device}, the current device is {torch.cuda.current_device()}")
 
 
+def _apart(name, out, may_be=(), /, **inputs):
+    """A given output shares no memory with the inputs (other CTAs still read
+    them), but may be one of those named in may_be as a whole."""
+    a, n = out.data_ptr(), out.numel() * out.element_size()
+    for other, t in inputs.items():
+        if t is None or t.data_ptr() >= a + n or a >= t.data_ptr() + t.numel() * t.element_size():
+            continue
+        if other not in may_be or t.data_ptr() != a or t.shape != out.shape:
+            raise ValueError(f"{name} overlaps {other}")
+
+
 def _gate_of(f, dt_bias, qshape):
     """Gate mode from the shapes: f with q's shape (dt_bias [H, dk]) is KDA's
     per-channel gate; f without the dk axis (dt_bias [H]) is the scalar gate."""

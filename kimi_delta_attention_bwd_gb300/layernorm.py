@@ -11,7 +11,7 @@ from typing import Optional
 
 import torch
 
-from . import _all_well, _lib, _require
+from . import _all_well, _apart, _lib, _require
 
 
 def _rows(x, w, bias=None):
@@ -30,13 +30,14 @@ def _rows(x, w, bias=None):
 def kda_layer_norm(x, w, bias=None, eps: Optional[float] = None, out: Optional[torch.Tensor] = None,
                    return_stats: bool = False):
     """Layer norm of x [..., D]; eps 1e-6 unless given (> 0); out may be x
-    (in place).  With return_stats returns (y, mean, rstd), the rows' statistics [...] in fp32
+    (in place), else it shares no memory with the inputs.  With return_stats returns (y, mean, rstd), the rows' statistics [...] in fp32
     that the backward takes."""
     n, D = _rows(x, w, bias)
     if out is None:
         y = torch.empty_like(x)
     else:
         _require(out=(out, x.shape, x.dtype))
+        _apart("out", out, ("x",), x=x, w=w, bias=bias)
         y = out
     mean = rstd = None
     if return_stats:

@@ -14,7 +14,7 @@ from typing import Optional
 
 import torch
 
-from . import _all_well, _dims, _lib, _require
+from . import _all_well, _apart, _dims, _lib, _require
 
 
 @dataclass
@@ -60,9 +60,9 @@ def kda_linear_forward(q, k, v, A_log, scale: Optional[float] = None, h0=None, c
                        final_state: Optional[torch.Tensor] = None):
     """Forward pass.  Returns (o, h_final or None, ctx); ctx feeds
     kda_linear_backward when save_for_backward is set.  scale: 1/sqrt(dk)
-    unless given (> 0).  out / final_state: optional preallocated outputs;
-    final_state may be h0 (states updated in place) unless the call saves for
-    the backward, which reads h0."""
+    unless given (> 0).  out / final_state: optional preallocated outputs that
+    share no memory with the inputs; final_state may be h0 (states updated in
+    place) unless the call saves for the backward, which reads h0."""
     _dims(q, "q", 4)
     _dims(v, "v", 4)
     B, T, H, dk = q.shape
@@ -84,6 +84,10 @@ def kda_linear_forward(q, k, v, A_log, scale: Optional[float] = None, h0=None, c
                  cu_seqlens=(cu_seqlens, (n_docs + 1,), torch.int32))
     if save_for_backward and h0 is not None and final_state is not None and h0.data_ptr() == final_state.data_ptr():
         raise ValueError("final_state cannot be h0 when the call saves for the backward")
+    if out is not None:
+        _apart("out", out, q=q, k=k, v=v, h0=h0)
+    if final_state is not None:
+        _apart("final_state", final_state, ("h0",), q=q, k=k, v=v, h0=h0, out=out)
     if save_for_backward and cu_seqlens_host is not None:
         # the backward plans by them again: a buffer that the next batch's offsets overwrite must not change them
         cu_seqlens_host = (cu_seqlens_host.clone() if isinstance(cu_seqlens_host, torch.Tensor)
@@ -127,7 +131,8 @@ def kda_linear_backward(ctx: LinearContext, dO, dh_final=None, want_dA_log: bool
 def kda_linear_decode_step(q, k, v, A_log, state, scale: Optional[float] = None,
                            out: Optional[torch.Tensor] = None):
     """One token for each of n sequences: q, k [n, H, dk], v [n, H, dv] (bf16 or
-    fp32), A_log [H] and state [n, H, dk, dv] fp32, the state updated in place.
+    fp32), A_log [H] and state [n, H, dk, dv] fp32, the state updated in place;
+    out may be q, k or v, else it shares no memory with the inputs.
     Returns o [n, H, dv] in the io dtype."""
     _dims(q, "q", 3)
     _dims(v, "v", 3)
@@ -139,6 +144,8 @@ def kda_linear_decode_step(q, k, v, A_log, state, scale: Optional[float] = None,
         specs += ((out, v.shape, io),)
     if not _all_well(*specs):
         _require(**dict(zip(("q", "k", "v", "A_log", "state", "out"), specs)))
+    if out is not None:
+        _apart("out", out, ("q", "k", "v"), q=q, k=k, v=v, state=state)
     o = out if out is not None else torch.empty_like(v)
     _lib.kda_linear_decode(n, H, dk, dv, io, scale, q, k, v, A_log, state, o)
     return o

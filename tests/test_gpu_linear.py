@@ -610,3 +610,38 @@ def test_host_offsets_overwritten_between_the_passes(dt, kind):
     assert kda.kda_device_status(ctx.workspace) == 0
     for n in got:
         assert torch.equal(got[n], ref[n]), n
+
+
+def test_outputs_that_overlap_inputs_are_refused():
+    x = make(73, [70, 20], 2, 64, 64, "bf16")
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    f, size = kda.kda_linear_forward, d["v"].numel()
+    for n in ("q", "k", "v"):
+        with pytest.raises(ValueError, match=f"out overlaps {n}"):
+            f(d["q"], d["k"], d["v"], d["A_log"], cu_seqlens=d["cu"], out=d[n])
+    buf = torch.cat([d["v"].flatten(), d["v"].flatten()])
+    v = buf[:size].view_as(d["v"]).copy_(d["v"])
+    with pytest.raises(ValueError, match="out overlaps v"):
+        f(d["q"], d["k"], v, d["A_log"], cu_seqlens=d["cu"], out=buf[size - 64:2 * size - 64].view_as(v))
+    ref = f(d["q"], d["k"], d["v"], d["A_log"], cu_seqlens=d["cu"])[0]
+    assert torch.equal(ref, f(d["q"], d["k"], v, d["A_log"], cu_seqlens=d["cu"], out=buf[size:].view_as(v))[0])
+    states = torch.cat([d["h0"], d["h0"]])
+    with pytest.raises(ValueError, match="final_state overlaps h0"):
+        f(d["q"], d["k"], d["v"], d["A_log"], h0=states[:2], cu_seqlens=d["cu"], final_state=states[1:3],
+          save_for_backward=False)
+    # a token's step reads its q, k and v before it writes
+    q, k, v = (d[n][0, :3].contiguous() for n in ("q", "k", "v"))
+    a, b = d["h0"][:1].repeat(3, 1, 1, 1), d["h0"][:1].repeat(3, 1, 1, 1)
+    ref = kda.kda_linear_decode_step(q, k, v, d["A_log"], a)
+    for t in (q, k, v):
+        b.copy_(d["h0"][:1])
+        args = [t if t is u else u.clone() for u in (q, k, v)]
+        keep = t.clone()
+        assert torch.equal(kda.kda_linear_decode_step(*args, d["A_log"], b, out=t), ref) and torch.equal(a, b)
+        t.copy_(keep)
+    two = torch.cat([v, v])
+    with pytest.raises(ValueError, match="out overlaps v"):
+        kda.kda_linear_decode_step(q, k, two[:3], d["A_log"], a, out=two[1:4])
+    rows = torch.zeros(9, 64, device="cuda")
+    with pytest.raises(ValueError, match="out overlaps x"):
+        kda.kda_layer_norm(rows[:8], torch.ones(64, device="cuda"), out=rows[1:])
