@@ -119,7 +119,12 @@ def kda_linear_backward(ctx: LinearContext, dO, dh_final=None, want_dA_log: bool
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     states = (ctx.n_docs, H, dk, dv)
-    _require(dO=(dO, (B, T, H, dv), q.dtype), dh_final=(dh_final, states, torch.float32))
+    # (q stands for the forward's tensors: the current device may have changed since)
+    specs = dict(q=(q, q.shape, q.dtype), dO=(dO, (B, T, H, dv), q.dtype), dh_final=(dh_final, states, torch.float32))
+    if dh_final is None:
+        del specs["dh_final"]
+    if not _all_well(*specs.values()):
+        _require(**specs)
     gr = {"dq": torch.empty_like(q), "dk": torch.empty_like(q), "dv": torch.empty_like(v),
           "dA_log": torch.empty_like(ctx.A_log) if want_dA_log else None,
           "dh0": torch.empty(states, dtype=torch.float32, device=q.device) if want_dh0 else None}

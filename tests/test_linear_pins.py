@@ -208,3 +208,11 @@ def test_linear_refuses_a_final_state_over_a_saved_h0():
         ctypes.byref(_prob()), P(FAKE), P(FAKE), P(FAKE), P(FAKE), P(FAKE), P(FAKE), P(h_final), save, None, 0, None)
     assert call(1, FAKE) == -1
     assert call(0, FAKE) == -5 and call(1, 2 * FAKE) == -5
+
+
+def test_linear_backward_looks_at_the_forward_s_device():
+    # tensors of the forward that are not on the current device are refused like any other argument
+    q, v = torch.zeros(1, 4, 2, 32), torch.zeros(1, 4, 2, 64)
+    ctx = kda.LinearContext(None, q, q, v, torch.zeros(2), None, None, None, None, 1, True)
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        kda.kda_linear_backward(ctx, v)
