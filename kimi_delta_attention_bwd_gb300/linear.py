@@ -31,6 +31,7 @@ class LinearContext:
     workspace: torch.Tensor
     n_docs: int
     saved: bool
+    stream: Optional[int] = None  # the workspace's, where the forward allocated it
 
 
 def _host_offsets(cu_seqlens_host, cu_seqlens):
@@ -93,7 +94,9 @@ def kda_linear_forward(q, k, v, A_log, scale: Optional[float] = None, h0=None, c
         cu_seqlens_host = (cu_seqlens_host.clone() if isinstance(cu_seqlens_host, torch.Tensor)
                            else cu_seqlens_host.copy())
     prob = _lib.make_problem(B, T, H, dk, dv, io, scale, cu_seqlens, cu_seqlens_host)
+    stream = None
     if workspace is None:
+        stream = _lib._stream()
         # (size 0 for a problem that the call below refuses with its own status)
         workspace = torch.empty(_lib.kda_linear_workspace_size(prob, save_for_backward) or 1, dtype=torch.uint8,
                                 device=q.device)
@@ -105,7 +108,7 @@ def kda_linear_forward(q, k, v, A_log, scale: Optional[float] = None, h0=None, c
         hf = final_state if final_state is not None else torch.empty(states, dtype=f32, device=q.device)
     _lib.kda_linear_fwd(prob, q, k, v, A_log, h0, o, hf, save_for_backward, workspace)
     return o, hf, LinearContext(prob, q, k, v, A_log, h0, cu_seqlens, cu_seqlens_host, workspace, n_docs,
-                                bool(save_for_backward))
+                                bool(save_for_backward), stream)
 
 
 def kda_linear_backward(ctx: LinearContext, dO, dh_final=None, want_dA_log: bool = True, want_dh0: bool = True):
@@ -128,6 +131,9 @@ def kda_linear_backward(ctx: LinearContext, dO, dh_final=None, want_dA_log: bool
     gr = {"dq": torch.empty_like(q), "dk": torch.empty_like(q), "dv": torch.empty_like(v),
           "dA_log": torch.empty_like(ctx.A_log) if want_dA_log else None,
           "dh0": torch.empty(states, dtype=torch.float32, device=q.device) if want_dh0 else None}
+    if ctx.stream is not None and ctx.stream != _lib._stream():
+        # a context dropped after this call must not give its memory to the forward's stream before the kernels end
+        ctx.workspace.record_stream(torch.cuda.current_stream())
     _lib.kda_linear_bwd(ctx.problem, q, ctx.k, v, ctx.A_log, ctx.h0, dO, dh_final, gr["dq"], gr["dk"], gr["dv"],
                         gr["dA_log"], gr["dh0"], ctx.workspace)
     return gr

@@ -645,3 +645,24 @@ def test_outputs_that_overlap_inputs_are_refused():
     rows = torch.zeros(9, 64, device="cuda")
     with pytest.raises(ValueError, match="out overlaps x"):
         kda.kda_layer_norm(rows[:8], torch.ones(64, device="cuda"), out=rows[1:])
+
+
+def test_a_context_dropped_while_another_stream_s_backward_runs():
+    # its workspace is not handed out on the forward's stream before that backward has ended (only addresses are
+    # compared: nothing is written over it)
+    x = make(74, [300, 200], 2, 64, 64, "bf16")
+    ref = run(x)
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    other = torch.cuda.Stream()
+    _, _, ctx = kda.kda_linear_forward(d["q"], d["k"], d["v"], d["A_log"], h0=d["h0"], cu_seqlens=d["cu"])
+    size, at = ctx.workspace.numel(), ctx.workspace.data_ptr()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(100_000_000)  # about 50 ms: the backward waits behind it
+        got = kda.kda_linear_backward(ctx, d["dO"], d["dh"])
+    del ctx
+    blocks = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(not at - size < b.data_ptr() < at + size for b in blocks)
+    other.synchronize()
+    for n in got:
+        assert torch.equal(got[n], ref[n]), n
