@@ -388,6 +388,9 @@ KDA_API kda_status kda_short_conv_bwd(int64_t n_tok, int C, int dtype, int activ
  * A_log = -inf is no decay, a NaN reaches its head's outputs.  Inputs are finite: a chunk's pairs are formed as
  * matrix products, so an infinity or NaN at one token also reaches its
  * document's other tokens, up to 63 before it (never another document's).
+ * Precision: states, their sums and the decay gradient hold 24 bits of every
+ * operand, as do all products of fp32 io; with bf16 io the computed operands of o,
+ * dq, dk and dv are off by 2^-16 at most, so that those are rounded once.
  * The workspace (kda_linear_workspace_size(p, for_backward) bytes, 256-byte
  * aligned) holds the error word (kda_device_status), the table of the packed
  * documents' units, the states of a long document's segments and, with

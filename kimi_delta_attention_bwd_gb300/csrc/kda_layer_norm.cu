@@ -470,7 +470,8 @@ __global__ void __launch_bounds__(BLK ? LN_CTHR : LN_NTHR, BLK ? 1 : LN_BWD_THR 
 
 // Rows wider than 32 columns for each of LN_CTHR threads: a CTA per row, the row read once per pass (its
 // later passes hit L2), the backward's column sums in its partial row.  A thread's sums, of up to 2^15 values
-// here, are compensated (Kahan 1965).
+// here, are compensated (Kahan 1965; 128 MB of bf16, 16386 columns: forward 538 us, 521 without, backward 856 and
+// 852).  Bound by the latency of single values: 0.5 TB/s in bf16, 0.8 in fp32.
 struct LongSum {
   float s = 0.f, c = 0.f;
   __device__ __forceinline__ void add(float x) {

@@ -32,7 +32,11 @@
 // inputs are split into bf16 parts: two (off by 2^-16 at most) where the
 // product ends in a bf16 output (the pairs and the state's rows), so that its only
 // rounding that counts is its own, and three (2^-24) where it enters the fp32
-// state or the decay gradient's sums.  fp32 io: kda_linear_f32.cu.
+// state or the decay gradient's sums.  The second part of pairs and state rows costs
+// the chains 20 to 27% and lin_dqk 2 to 5% (300M prompt's chain 31 -> 37 us); one
+// part gave the outputs a 2-norm error of 2.35e-3 instead of 1.66e-3.  Where a
+// comment below compares two forms without saying so, pairs had one part in both.
+// fp32 io: kda_linear_f32.cu.
 #include "kda_linear.cuh"
 
 namespace kda {
@@ -412,9 +416,9 @@ __device__ __forceinline__ void copy_rows(const unsigned char* tile, int c0, bf1
 // walked from the other end (blk) and the weights run the other way.
 // mma.sync rather than tcgen05: the chain is bound by the instructions around
 // its products, and accumulators that are the next product's operands save
-// the round trips through TMEM and shared memory (300M layer, 16 x 2048: 31 us,
+// the round trips through TMEM and shared memory (300M layer, 16 x 2048: 37 us,
 // the tcgen05 form 87 before the steps that both could take; 128/128, 4 x 8192:
-// 271 us at 4.0 TB/s with the chunk states, tensor pipe 55%).
+// 315 us at 3.5 TB/s with the chunk states, tensor pipe 60%).
 template <int DK, int DVS, bool ONLY, bool rev>
 __device__ void chain(const LinP& P, const LinOp& op, const LinMaps& maps, int u, int h, int slice) {
   using SH = Shape<DK, DVS, ONLY>;
@@ -702,8 +706,8 @@ __global__ void __launch_bounds__(Shape<DK, DVS, ONLY>::NTH, Shape<DK, DVS, ONLY
 // and, with DA, the decay gradient's A, B, C, D.  A CTA takes CPB chunks of a
 // head and a DVS-column slice of dk; warp w forms rows 16 w .. of dq^T and dk^T
 // and reads its rows of S and R from memory as operand fragments, once (128/128,
-// 4 x 8192: 471 us, 4.0 TB/s, tensor pipe 49%; three chains instead of it took
-// 1.9 ms for the backward, 1.2 so).
+// 4 x 8192: 484 us, 3.9 TB/s, tensor pipe 52%, without DA 424 us; three chains
+// instead of it took 1.9 ms for the backward where this took 1.2).
 constexpr int CPB = 4;
 
 // A warp's blocks (row r, column c <= r) of the pairs, a byte 4 r + c + 1 each,
@@ -1136,12 +1140,12 @@ int chain_ctas(int dtype, int dk) {
 // Equal rows: the number of pieces that costs least, in chunk times: waves of
 // CTAs x (chunks of a piece + a start of one and a half), the segments' own
 // states (0.45 of that over all pieces but the last) and the fold (a fortieth per
-// piece).  300M (2048 tokens, 128 chains): whole rows 77 us, 8 pieces (1024 CTAs
-// on 912 slots) 37, 7 pieces 31.
+// piece).  300M (2048 tokens, 128 chains): whole rows 114 us, 8 pieces (1024 CTAs
+// on 912 slots) 43, 7 pieces 37.
 // Packed documents, whose lengths only the device may know: N / L + n_docs / 2
 // units fill the least number of waves that holds 2.5 units per document, so
-// that the documents' last, shorter pieces do not decide (300M packed 42 us with
-// pieces of 256 tokens, 39 with 384).
+// that the documents' last, shorter pieces do not decide (300M packed 48 us with
+// pieces of 256 tokens, 51 with 320, 45 with 384, 49 with 448).
 int seg_len(const Dims& d, int64_t per, int64_t slots) {
   if (d.rows) {
     int best = 1;

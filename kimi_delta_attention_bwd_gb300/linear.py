@@ -5,7 +5,9 @@
 per document and head; q and k enter as they are.  Shapes, dtypes and
 documents as kda_forward: q, k [B, T, H, dk]; v, o [B, T, H, dv] (bf16 or fp32;
 (dk, dv) = (32, 64), (64, 64), (64, 128), (128, 128)); A_log [H] fp32; states
-[n_docs, H, dk, dv] fp32; optional cu_seqlens int32 [n_docs + 1].
+[n_docs, H, dk, dv] fp32; optional cu_seqlens int32 [n_docs + 1].  States and
+the decay gradient are formed with 24 bits of every operand; bf16 outputs are
+rounded once (their computed operands are off by 2^-16 at most).
 """
 from __future__ import annotations
 
