@@ -385,9 +385,10 @@ KDA_API kda_status kda_short_conv_bwd(int64_t n_tok, int C, int dtype, int activ
  * q and k enter as they are (no L2 norm).  Sizes, layouts, dtypes, documents
  * (rows or cu_seqlens), h0 / h_final and statuses are those of kda_fwd; the
  * problem's gate must be KDA_GATE_CHANNEL (it is not used).  A_log : [H] fp32;
- * A_log = -inf is no decay, a NaN reaches its head's outputs.  Inputs are finite: a chunk's pairs are formed as
- * matrix products, so an infinity or NaN at one token also reaches its
- * document's other tokens, up to 63 before it (never another document's).
+ * A_log = -inf is no decay, a NaN reaches its head's outputs.  Inputs are
+ * finite: a chunk's pairs are formed as matrix products, so an infinity or NaN
+ * at one token also reaches its document's other tokens, up to 63 before it
+ * (never another document's).
  * Precision: states, their sums and the decay gradient hold 24 bits of every
  * operand, as do all products of fp32 io; with bf16 io the computed operands of o,
  * dq, dk and dv are off by 2^-16 at most, so that those are rounded once.

@@ -34,9 +34,9 @@
 // rounding that counts is its own, and three (2^-24) where it enters the fp32
 // state or the decay gradient's sums.  The second part of pairs and state rows costs
 // the chains 20 to 27% and lin_dqk 2 to 5% (300M prompt's chain 31 -> 37 us); one
-// part gave the outputs a 2-norm error of 2.35e-3 instead of 1.66e-3.  Where a
-// comment below compares two forms without saying so, pairs had one part in both.
-// fp32 io: kda_linear_f32.cu.
+// part gave the outputs a 2-norm error of 2.35e-3 instead of 1.66e-3.  (The forms
+// compared at the states' layout and at lin_dqk's chains, tiles, prefetch and list
+// of pairs were timed with pairs of one part.)  fp32 io: kda_linear_f32.cu.
 #include "kda_linear.cuh"
 
 namespace kda {
