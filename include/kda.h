@@ -446,6 +446,92 @@ KDA_API kda_status kda_layer_norm_bwd(int64_t n_rows, int D, int dtype, const vo
                    const void* dy, const float* mean, const float* rstd, void* dx, float* dw, float* dbias,
                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* Softmax attention with grouped heads: Hq query heads share Hkv key heads
+ * (Hq a multiple of Hkv; query head h reads key head h / (Hq / Hkv)).  Per
+ * document with Lq queries and Lk keys and per query head,
+ *   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i k_j - lse_i),  lse_i = log sum_j exp(scale q_i k_j)
+ * over the keys j <= i + Lk - Lq (causal = 1: the last query sees every key) or
+ * over all keys (causal = 0).  A query that sees no key gives o = 0, lse = -inf
+ * and takes no part in the gradients.
+ *  B, T, Tk  : rows, queries per row, keys per row.
+ *  D         : head dim of q, k, v and o: 64 or 128.
+ *  dtype     : kda_dtype of q, k, v, o and their gradients.
+ *  scale     : <= 0 selects 1/sqrt(D).
+ *  cu_seqlens, n_docs: DEVICE int32 [n_docs + 1] offsets of the documents'
+ *              queries in the flattened B*T axis, or NULL: the rows.
+ *  cu_seqlens_k: the same for their keys in the flattened B*Tk axis; NULL (only
+ *              where T = Tk): cu_seqlens.  Documents may have no queries or no keys.
+ *  cu_seqlens_host, cu_seqlens_k_host: optional HOST copies, validated before
+ *              any launch; offsets only on the device are validated there
+ *              (kda_device_status of the workspace). */
+typedef struct kda_softmax_problem {
+    int32_t B, T, Tk, Hq, Hkv, D;
+    int32_t dtype;
+    float scale;
+    int32_t causal;
+    int32_t n_docs;
+    const int32_t* cu_seqlens;
+    const int32_t* cu_seqlens_k;
+    const int32_t* cu_seqlens_host;
+    const int32_t* cu_seqlens_k_host;
+} kda_softmax_problem;
+
+/* Forward: q, o [B, T, Hq, D], k, v [B, Tk, Hkv, D] in dtype, lse [B, T, Hq]
+ * fp32 (natural logarithm).  The workspace (kda_softmax_workspace_size bytes,
+ * 256-byte aligned) holds the error word and the documents' tile tables and,
+ * with save_for_backward = 1, the rows' sums and (bf16) what rounding o left; it
+ * must then be passed to kda_softmax_bwd unmodified, with the same inputs and o.
+ * Outputs must not overlap inputs.  Inputs are finite: weights of unseen keys
+ * are exact zeros of a matrix product, so an infinity or NaN in a value also
+ * reaches its document's queries up to 255 before it, never another document's.
+ * Precision: logits, maxima, sums and o are accumulated in fp32; with bf16 io the
+ * weights (and, in the backward, their gradients) enter their products as bf16. */
+KDA_API size_t kda_softmax_workspace_size(const kda_softmax_problem* p, int for_backward);
+KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, const void* q, const void* k, const void* v,
+                   void* o, float* lse, int save_for_backward, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream);
+
+/* Backward of sum(o * dO): dq [B, T, Hq, D], dk, dv [B, Tk, Hkv, D] (dtype),
+ * from the forward's inputs, its o and its workspace (another one is refused by
+ * the device: KDA_ERR_WORKSPACE from kda_device_status).  dk and dv are summed over
+ * the heads of a group and over the queries by one CTA: a fixed order, no
+ * atomics.  The workspace may be used by several backwards, one at a time. */
+KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, const void* q, const void* k, const void* v,
+                   const void* o, const void* dO, void* dq, void* dk, void* dv, void* workspace,
+                   size_t workspace_bytes, cudaStream_t stream);
+
+/* Single-token step over a cache: q, o [n_seq, Hq, D], k, v [n_seq, Hkv, D],
+ * k_cache, v_cache [n_seq, cap, Hkv, D] in dtype, lengths [n_seq] DEVICE int32: the
+ * tokens in each cache before the step.  k and v are written to place
+ * lengths[i] of sequence i's cache and the query sees places 0 .. lengths[i]; places
+ * behind it are neither read nor written.  lengths[i] < 0: the sequence
+ * takes no step (a padded batch): its cache is left alone and its o is 0.
+ * lengths[i] >= cap: the same, and kda_device_status of the workspace reports
+ * KDA_ERR_BAD_SEQLENS.  The lengths are not advanced (the layers of a model share them).
+ * The workspace is kda_softmax_decode_workspace_size bytes (0 for invalid
+ * sizes), 256-byte aligned, and keeps nothing between calls; calls that overlap
+ * need one each. */
+KDA_API size_t kda_softmax_decode_workspace_size(int n_seq, int cap, int Hq, int Hkv, int D);
+KDA_API kda_status kda_softmax_decode(int n_seq, int cap, int Hq, int Hkv, int D, int dtype, float scale,
+                   const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
+                   const int32_t* lengths, void* o, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Rotary positions of q [n_tok, Hq, D] and k [n_tok, Hkv, D] (Hkv = 0: q alone):
+ * the first rot values of every head (even, <= D <= 1024) in pairs, value i with value
+ * i + rot/2 (interleaved = 0) or 2 i with 2 i + 1 (interleaved = 1), each
+ * turned by w = position * inv_freq[i] and multiplied by scale (<= 0: 1):
+ *   (a, b) -> scale (a cos w - b sin w, b cos w + a sin w);
+ * inverse = 1 turns by -w (the gradients' way back, with the same scale).  The
+ * other values pass.  inv_freq : [rot/2] fp32, taken as exact: the angle is
+ * right to about 1e-7 of a turn at any int32 position.  Positions: positions
+ * [n_tok] int32, or places in documents (cu_seqlens [n_docs + 1] int32 over the
+ * tokens), or (both NULL) places in rows of T tokens.  q_out and k_out are q and
+ * k (in place, both) or share no memory with them. */
+KDA_API kda_status kda_rotary(int64_t n_tok, int64_t T, int Hq, int Hkv, int D, int rot, int dtype,
+                   int interleaved, int inverse, float scale, const float* inv_freq, const int32_t* positions,
+                   const int32_t* cu_seqlens, int n_docs, const void* q, const void* k, void* q_out, void* k_out,
+                   cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

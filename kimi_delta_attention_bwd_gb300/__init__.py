@@ -21,6 +21,11 @@ libkda_gb300.so through its C ABI, include/kda.h):
   y = kda_layer_norm(x, weight, bias)                          # layer norm over the last axis
   dx, dw, db = kda_layer_norm_backward(x, weight, dy, mean, rstd)
   o = linear_attention(q, k, v, A_log); y = layer_norm(x, weight, bias)  # as torch.autograd ops
+  q, k = kda_rotary(q, k, inv_freq, ...)                       # rotary positions (kda_rotary_backward: the way back)
+  o, lse, ctx = kda_softmax_forward(q, k, v, ...)              # softmax attention, causal or full, grouped heads
+  grads = kda_softmax_backward(ctx, dO)                        # dq, dk, dv
+  o = kda_softmax_decode_step(q, k, v, k_cache, v_cache, lengths)  # one token over a cache, appended in place
+  q, k = rotary(q, k, inv_freq); o = softmax_attention(q, k, v)    # as torch.autograd ops
 
 Layouts: q, k, f [B, T, H, dk]; v [B, T, H, dv]; b [B, T, H] (bf16 or fp32);
 A_log [H], dt_bias [H, dk] fp32 (scalar-gated variant: f [B, T, H], dt_bias [H]); optional cu_seqlens int32 [n_docs + 1] over
@@ -41,7 +46,9 @@ __all__ = ["kda_forward", "kda_backward", "kda_forward_norm_gate", "kda_backward
            "kda_short_conv", "kda_short_conv_backward", "KdaContext", "KdaError", "kda_device_status",
            "kda_attention", "short_conv", "gated_norm", "kda_linear_forward", "kda_linear_backward",
            "kda_linear_decode_step", "LinearContext", "kda_layer_norm", "kda_layer_norm_backward",
-           "linear_attention", "layer_norm"]
+           "linear_attention", "layer_norm", "rotary_frequencies", "kda_rotary", "kda_rotary_backward",
+           "SoftmaxContext", "kda_softmax_forward", "kda_softmax_backward", "kda_softmax_decode_step",
+           "softmax_attention", "rotary"]
 
 
 @dataclass
@@ -514,4 +521,7 @@ def kda_short_conv_backward(x, w, dy, cu_seqlens=None, activation: str = "silu",
 
 from .linear import LinearContext, kda_linear_backward, kda_linear_decode_step, kda_linear_forward  # noqa: E402
 from .layernorm import kda_layer_norm, kda_layer_norm_backward  # noqa: E402
-from .autograd import gated_norm, kda_attention, layer_norm, linear_attention, short_conv  # noqa: E402  (differentiable forms)
+from .positions import kda_rotary, kda_rotary_backward, rotary_frequencies  # noqa: E402
+from .softmax import SoftmaxContext, kda_softmax_backward, kda_softmax_decode_step, kda_softmax_forward  # noqa: E402
+from .autograd import (gated_norm, kda_attention, layer_norm, linear_attention, rotary, short_conv,  # noqa: E402
+                       softmax_attention)  # (differentiable forms)

@@ -33,6 +33,14 @@ class kda_problem(ctypes.Structure):
                 ("scale", ctypes.c_float), ("n_docs", ctypes.c_int32),
                 ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p), ("gate", ctypes.c_int32)]
 
+class kda_softmax_problem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("Tk", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("causal", ctypes.c_int32), ("n_docs", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p),
+                ("cu_seqlens_k", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
+                ("cu_seqlens_k_host", ctypes.c_void_p)]
+
+
 KDA_GATE_CHANNEL, KDA_GATE_SCALAR = 0, 1
 
 
@@ -120,6 +128,19 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.kda_layer_norm_fwd.restype = I
         lib.kda_layer_norm_bwd.argtypes = [I64, I, I] + [P] * 9 + [SZ, P]
         lib.kda_layer_norm_bwd.restype = I
+        PS = ctypes.POINTER(kda_softmax_problem)
+        lib.kda_softmax_workspace_size.argtypes = [PS, I]
+        lib.kda_softmax_workspace_size.restype = SZ
+        lib.kda_softmax_fwd.argtypes = [PS] + [P] * 5 + [I, P, SZ, P]
+        lib.kda_softmax_fwd.restype = I
+        lib.kda_softmax_bwd.argtypes = [PS] + [P] * 9 + [SZ, P]
+        lib.kda_softmax_bwd.restype = I
+        lib.kda_softmax_decode_workspace_size.argtypes = [I] * 5
+        lib.kda_softmax_decode_workspace_size.restype = SZ
+        lib.kda_softmax_decode.argtypes = [I] * 6 + [F] + [P] * 8 + [SZ, P]
+        lib.kda_softmax_decode.restype = I
+        lib.kda_rotary.argtypes = [I64, I64] + [I] * 7 + [F] + [P] * 3 + [I] + [P] * 5
+        lib.kda_rotary.restype = I
         _lib = lib
         return lib
 
@@ -333,6 +354,60 @@ def kda_layer_norm_bwd(n_rows, D, dtype, x, w, dy, mean, rstd, dx, dw, dbias, wo
                                    _p(dw), _p(dbias), _p(workspace), workspace.numel(), _stream())
     if st != 0:
         raise KdaError(st, "kda_layer_norm_bwd")
+
+
+def _host_ptr(c):
+    return None if c is None else c.ctypes.data if hasattr(c, "ctypes") else c.data_ptr()
+
+
+def make_softmax_problem(B, T, Tk, Hq, Hkv, D, dtype, scale, causal, cu_seqlens=None, cu_seqlens_k=None,
+                         cu_seqlens_host=None, cu_seqlens_k_host=None):
+    """The kda_softmax_problem struct (device and host arrays kept alive by the caller)."""
+    n_docs = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    return kda_softmax_problem(B, T, Tk, Hq, Hkv, D, _dt(dtype), scale or 0.0, 1 if causal else 0, n_docs,
+                               _p(cu_seqlens), _p(cu_seqlens_k), _host_ptr(cu_seqlens_host),
+                               _host_ptr(cu_seqlens_k_host))
+
+
+def kda_softmax_workspace_size(problem, for_backward) -> int:
+    return int(load().kda_softmax_workspace_size(ctypes.byref(problem), 1 if for_backward else 0))
+
+
+def kda_softmax_fwd(problem, q, k, v, o, lse, save_for_backward, workspace):
+    st = load().kda_softmax_fwd(ctypes.byref(problem), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                lse.data_ptr(), 1 if save_for_backward else 0, workspace.data_ptr(),
+                                workspace.numel(), _stream())
+    if st != 0:
+        raise KdaError(st, "kda_softmax_fwd")
+
+
+def kda_softmax_bwd(problem, q, k, v, o, dO, dq, dk, dv, workspace):
+    st = load().kda_softmax_bwd(ctypes.byref(problem), _p(q), _p(k), _p(v), _p(o), _p(dO), _p(dq), _p(dk), _p(dv),
+                                _p(workspace), workspace.numel(), _stream())
+    if st != 0:
+        raise KdaError(st, "kda_softmax_bwd")
+
+
+def kda_softmax_decode_workspace_size(n_seq, cap, Hq, Hkv, D) -> int:
+    return int(load().kda_softmax_decode_workspace_size(n_seq, cap, Hq, Hkv, D))
+
+
+def kda_softmax_decode(n_seq, cap, Hq, Hkv, D, dtype, scale, q, k, v, k_cache, v_cache, lengths, o, workspace):
+    st = load().kda_softmax_decode(n_seq, cap, Hq, Hkv, D, _dt(dtype), scale or 0.0, q.data_ptr(), k.data_ptr(),
+                                   v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lengths.data_ptr(),
+                                   o.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream())
+    if st != 0:
+        raise KdaError(st, "kda_softmax_decode")
+
+
+def kda_rotary(n_tok, T, Hq, Hkv, D, rot, dtype, interleaved, inverse, scale, inv_freq, positions, cu_seqlens, q, k,
+               q_out, k_out):
+    nd = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    st = load().kda_rotary(n_tok, T, Hq, Hkv, D, rot, _dt(dtype), 1 if interleaved else 0, 1 if inverse else 0,
+                           scale or 0.0, inv_freq.data_ptr(), _p(positions), _p(cu_seqlens), nd, q.data_ptr(), _p(k),
+                           q_out.data_ptr(), _p(k_out), _stream())
+    if st != 0:
+        raise KdaError(st, "kda_rotary")
 
 
 def kda_device_status(workspace) -> int:

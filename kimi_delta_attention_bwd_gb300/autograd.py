@@ -8,6 +8,8 @@ points), wrapped so that a model can use them like any differentiable op.
   y = gated_norm(o, gate, weight)                                     # gated RMSNorm epilogue
   o = linear_attention(q, k, v, A_log)                                # linear attention, one decay per head
   y = layer_norm(x, weight, bias)                                     # layer norm over the last axis
+  q, k = rotary(q, k, inv_freq)                                       # rotary positions
+  o = softmax_attention(q, k, v)                                      # causal softmax attention, grouped heads
 
 Gradients flow to q, k, v, f, b, A_log, dt_bias and h0 (and to the
 convolution's input and taps, the norms' input, gate, weight and bias).  Each
@@ -20,10 +22,12 @@ from typing import Optional
 
 import torch
 
-from . import (LinearContext, kda_backward, kda_forward, kda_layer_norm, kda_layer_norm_backward, kda_linear_backward,
-               kda_linear_forward, kda_norm_gate, kda_norm_gate_backward, kda_short_conv, kda_short_conv_backward)
+from . import (LinearContext, SoftmaxContext, kda_backward, kda_forward, kda_layer_norm, kda_layer_norm_backward,
+               kda_linear_backward, kda_linear_forward, kda_norm_gate, kda_norm_gate_backward, kda_rotary,
+               kda_rotary_backward, kda_short_conv, kda_short_conv_backward, kda_softmax_backward,
+               kda_softmax_forward)
 
-__all__ = ["kda_attention", "short_conv", "gated_norm", "linear_attention", "layer_norm"]
+__all__ = ["kda_attention", "short_conv", "gated_norm", "linear_attention", "layer_norm", "softmax_attention", "rotary"]
 
 
 class _KdaAttention(torch.autograd.Function):
@@ -161,3 +165,61 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x, w, bias=None, eps: Optional[float] = None):
     """Differentiable layer norm over the last axis (kda_layer_norm)."""
     return _LayerNorm.apply(x, w, bias, eps, torch.is_grad_enabled())
+
+
+class _SoftmaxAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(fctx, q, k, v, scale, causal, cu_seqlens, cu_seqlens_k, cu_seqlens_host, cu_seqlens_k_host, recorded):
+        o, _, sctx = kda_softmax_forward(q, k, v, scale=scale, causal=causal, cu_seqlens=cu_seqlens,
+                                         cu_seqlens_k=cu_seqlens_k, cu_seqlens_host=cu_seqlens_host,
+                                         cu_seqlens_k_host=cu_seqlens_k_host,
+                                         save_for_backward=recorded and any(fctx.needs_input_grad))
+        # (the workspace among them: freed by the backward, seen by hooks)
+        fctx.save_for_backward(q, k, v, o, cu_seqlens, cu_seqlens_k, sctx.workspace)
+        fctx.rest = (sctx.problem, sctx.host, sctx.saved)
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(fctx, dO):
+        q, k, v, o, cu_seqlens, cu_seqlens_k, workspace = fctx.saved_tensors
+        problem, host, saved = fctx.rest
+        g = kda_softmax_backward(SoftmaxContext(problem, q, k, v, o, cu_seqlens, cu_seqlens_k, host, workspace, saved),
+                                 _given(dO))
+        return g["dq"], g["dk"], g["dv"], None, None, None, None, None, None, None
+
+
+def softmax_attention(q, k, v, scale: Optional[float] = None, causal: bool = True, cu_seqlens=None, cu_seqlens_k=None,
+                      cu_seqlens_host=None, cu_seqlens_k_host=None):
+    """Differentiable softmax attention: o from the layouts of
+    kda_softmax_forward; gradients to q, k and v through kda_softmax_backward."""
+    return _SoftmaxAttention.apply(q, k, v, scale, causal, cu_seqlens, cu_seqlens_k, cu_seqlens_host,
+                                   cu_seqlens_k_host, torch.is_grad_enabled())
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(fctx, q, k, inv_freq, positions, cu_seqlens, interleaved, scale):
+        fctx.set_materialize_grads(False)
+        fctx.save_for_backward(inv_freq, positions, cu_seqlens)
+        fctx.how = (interleaved, scale)
+        return kda_rotary(q, k, inv_freq, positions, cu_seqlens, interleaved, scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(fctx, dq, dk):
+        inv_freq, positions, cu_seqlens = fctx.saved_tensors
+        back = [None if g is None else _given(g) for g in (dq, dk)]
+        if back[0] is None and back[1] is None:
+            return (None,) * 7
+        if back[0] is None:  # (the keys' gradients alone)
+            back[1] = kda_rotary_backward(back[1], None, inv_freq, positions, cu_seqlens, *fctx.how)[0]
+        else:
+            back = kda_rotary_backward(*back, inv_freq, positions, cu_seqlens, *fctx.how)
+        return back[0], back[1], None, None, None, None, None
+
+
+def rotary(q, k, inv_freq, positions=None, cu_seqlens=None, interleaved: bool = False, scale: float = 1.0):
+    """Differentiable rotary positions: (q', k') from the layouts of kda_rotary
+    (k may be None); gradients to q and k through kda_rotary_backward."""
+    return _Rotary.apply(q, k, inv_freq, positions, cu_seqlens, interleaved, scale)

@@ -750,7 +750,9 @@ static const char* const k_names[K_COUNT] = {"chunk_table", "fwd_intra", "fwd_sc
                                              "conv_fwd",  "conv_bwd",  "conv_reduce",
                                              "fwd_state_norm", "bwd_scan_norm", "fwd_seg", "bwd_seg",
                                              "linear_chain", "linear_seg", "linear_fold", "linear_dqk", "linear_decay", "linear_decode",
-                                             "layer_norm_fwd", "layer_norm_bwd", "layer_norm_reduce"};
+                                             "layer_norm_fwd", "layer_norm_bwd", "layer_norm_reduce",
+                                             "softmax_table", "softmax_fwd", "softmax_delta", "softmax_dkv", "softmax_dq",
+                                             "softmax_decode", "softmax_join", "rotary"};
 
 const char* kda_prof_kernel_name(int i) { return (i >= 0 && i < K_COUNT) ? k_names[i] : nullptr; }
 

@@ -45,6 +45,14 @@ enum KernelId {
   K_LN_FWD,
   K_LN_BWD,
   K_LN_RED,
+  K_SMX_TABLE,
+  K_SMX_FWD,
+  K_SMX_DELTA,
+  K_SMX_DKV,
+  K_SMX_DQ,
+  K_SMX_DECODE,
+  K_SMX_JOIN,
+  K_ROTARY,
   K_COUNT
 };
 

@@ -1,0 +1,307 @@
+// Softmax attention with grouped heads: tile tables of packed documents, the
+// backward's row sums, argument checks, workspace and the C entries.
+#include "kda_softmax.cuh"
+
+#include <string.h>
+
+namespace kda {
+namespace smx {
+namespace {
+
+// ------------------------------------------------------------ tile tables
+// Block b builds list l0 + b: every document's tiles of queries (keys for list
+// 2), by decreasing pairs, so that the longest tiles start first and the grid's
+// end is short ones (a counting sort; tiles of equal weight in any order, which no
+// result depends on).  The offsets are checked before any of them is used.
+constexpr int TT = 1024, NB = 1024;
+
+__device__ int incl_scan(int x, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int y = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    s_warp[lane] = y;
+  }
+  __syncthreads();
+  const int r = x + (warp ? s_warp[warp - 1] : 0);
+  *total = s_warp[31];
+  __syncthreads();
+  return r;
+}
+
+__global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P, int l0) {
+  __shared__ int s_bad, s_warp[32], s_cnt[NB];
+  const int l = l0 + blockIdx.x, tid = threadIdx.x, n = P.n_docs, tile = P.tile[l];
+  const bool by_key = l == 2;
+  pdl_wait();
+  pdl_release();
+  const bool ok = l0 == 0 || (*P.wtag == P.tag && *P.err == KDA_OK);  // (block 0 may not write these before block 1 reads)
+  const int32_t *cu = P.cu, *cuk = P.cuk, *own = by_key ? cuk : cu;
+  if (tid == 0) s_bad = cu[0] != 0 || cu[n] != P.Nq || cuk[0] != 0 || cuk[n] != P.Nk;
+  __syncthreads();
+  for (int i = tid; i < n; i += TT)
+    if (cu[i + 1] < cu[i] || cuk[i + 1] < cuk[i]) s_bad = 1;
+  __syncthreads();
+  if (tid == 0 && l0 == 0) {
+    *P.err = s_bad ? KDA_ERR_BAD_SEQLENS : KDA_OK;
+    *P.wtag = P.save && !s_bad ? P.tag : 0;
+  } else if (tid == 0 && s_bad && ok) {  // offsets that changed since the forward (else its words stay)
+    *P.err = KDA_ERR_BAD_SEQLENS;
+  }
+  if (s_bad || !ok) {
+    if (tid == 0) P.counts[l] = 0;
+    return;
+  }
+  int carry = 0;
+  for (int base = 0; base < n; base += TT) {
+    const int i = base + tid, nt = i < n ? (own[i + 1] - own[i] + tile - 1) / tile : 0;
+    int total;
+    const int r = carry + incl_scan(nt, s_warp, &total) - nt;
+    if (i < n) P.pre[l][i] = r;
+    carry += total;
+  }
+  if (tid == 0) {
+    P.pre[l][n] = carry;
+    P.counts[l] = carry;
+  }
+  for (int b = tid; b < NB; b += TT) s_cnt[b] = 0;
+  __syncthreads();
+  auto find = [&](int x, int4& a, int& t) -> int {  // tile x in the documents' order; its bucket, heavy ones first
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (P.pre[l][mid] <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    t = x - P.pre[l][lo];
+    a = make_int4(cu[lo], cu[lo + 1] - cu[lo], cuk[lo], cuk[lo + 1] - cuk[lo]);
+    const int w = by_key ? a.y - first_query(P.causal, t * tile, a.y, a.w)
+                         : keys_of(P.causal, min(a.y, (t + 1) * tile) - 1, a.y, a.w);
+    return NB - 1 - min(NB - 1, (w + 63) >> 6);
+  };
+  int4 a;
+  int t;
+  for (int x = tid; x < carry; x += TT) atomicAdd(&s_cnt[find(x, a, t)], 1);
+  __syncthreads();
+  {
+    static_assert(NB == TT, "a bucket a thread");
+    int total;
+    const int c = s_cnt[tid], r = incl_scan(c, s_warp, &total) - c;
+    s_cnt[tid] = r;
+  }
+  __syncthreads();
+  for (int x = tid; x < carry; x += TT) {
+    const int at = atomicAdd(&s_cnt[find(x, a, t)], 1);
+    P.list[l][2 * (size_t)at] = a;
+    P.list[l][2 * (size_t)at + 1] = make_int4(t, 0, 0, 0);
+  }
+}
+
+// ------------------------------------------------------------ delta
+// delta_i = sum_d o_i dO_i per row (token, head), D / 8 threads a row.  With bf16
+// io o is the stored output plus what its rounding left: delta is subtracted from
+// dO v, and a rounded o would put a further rounding's error into every gradient.
+template <int D, typename T>
+__global__ void __launch_bounds__(256) smx_delta_kernel(SmxP P, const T* __restrict__ o, const T* __restrict__ dO) {
+  constexpr int TR = D / 8;
+  pdl_wait();
+  pdl_release();
+  if (!saved(P)) return;
+  const int64_t row = (int64_t)blockIdx.x * (256 / TR) + threadIdx.x / TR;
+  const bool in = row < (int64_t)P.Nq * P.Hq;
+  float s = 0.f;
+  if (in) {
+    const size_t at = (size_t)row * D + threadIdx.x % TR * 8;
+    if constexpr (sizeof(T) == 2) {
+      const uint4 a = *reinterpret_cast<const uint4*>(o + at), b = *reinterpret_cast<const uint4*>(dO + at),
+                  r = *reinterpret_cast<const uint4*>(P.res + at);
+      const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162*>(&a),
+                           *pb = reinterpret_cast<const __nv_bfloat162*>(&b),
+                           *pr = reinterpret_cast<const __nv_bfloat162*>(&r);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const float2 x = __bfloat1622float2(pa[e]), y = __bfloat1622float2(pb[e]), z = __bfloat1622float2(pr[e]);
+        s = fmaf(x.x + z.x, y.x, s);
+        s = fmaf(x.y + z.y, y.y, s);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        const float4 a = *reinterpret_cast<const float4*>(o + at + 4 * c),
+                     b = *reinterpret_cast<const float4*>(dO + at + 4 * c);
+        s = fmaf(a.x, b.x, s);
+        s = fmaf(a.y, b.y, s);
+        s = fmaf(a.z, b.z, s);
+        s = fmaf(a.w, b.w, s);
+      }
+    }
+  }
+#pragma unroll
+  for (int x = TR / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+  if (in && threadIdx.x % TR == 0) P.delta[(size_t)(row % P.Hq) * P.Nq + row / P.Hq] = s;
+}
+
+// ------------------------------------------------------------ host
+bool a16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+bool offsets_ok(const int32_t* c, int n, int64_t end) {
+  if (c[0] != 0 || c[n] != end) return false;
+  for (int i = 0; i < n; i++)
+    if (c[i + 1] < c[i]) return false;
+  return true;
+}
+
+kda_status check(const kda_softmax_problem* p, SmxP* out) {
+  if (!p) return KDA_ERR_INVALID_ARG;
+  if (p->B <= 0 || p->T <= 0 || p->Tk <= 0 || p->Hq <= 0 || p->Hkv <= 0) return KDA_ERR_INVALID_ARG;
+  if (p->dtype != KDA_BF16 && p->dtype != KDA_F32) return KDA_ERR_INVALID_ARG;
+  if (p->causal != 0 && p->causal != 1) return KDA_ERR_INVALID_ARG;
+  if (p->Hq > 4096 || p->Hq % p->Hkv != 0) return KDA_ERR_INVALID_ARG;
+  const int64_t nq = (int64_t)p->B * p->T, nk = (int64_t)p->B * p->Tk;
+  // (tile counts times heads fit a grid, and a tile's last row an int)
+  if (nq > ((int64_t)1 << 30) || nk > ((int64_t)1 << 30) || nq * p->Hq > ((int64_t)1 << 36) ||
+      nk * p->Hkv > ((int64_t)1 << 36))
+    return KDA_ERR_INVALID_ARG;
+  if (p->D != 64 && p->D != 128) return KDA_ERR_UNSUPPORTED;
+  SmxP P = {};
+  P.rows = p->cu_seqlens == nullptr;
+  if (P.rows) {
+    if (p->cu_seqlens_k || p->cu_seqlens_host || p->cu_seqlens_k_host) return KDA_ERR_INVALID_ARG;
+    P.n_docs = p->B;
+  } else {
+    if (p->n_docs <= 0 || p->n_docs > (1 << 24)) return KDA_ERR_INVALID_ARG;
+    if (!p->cu_seqlens_k && (p->T != p->Tk || p->cu_seqlens_k_host)) return KDA_ERR_INVALID_ARG;
+    if ((uintptr_t)p->cu_seqlens % 4 != 0 || (uintptr_t)p->cu_seqlens_k % 4 != 0) return KDA_ERR_ALIGNMENT;
+    if (p->cu_seqlens_host && !offsets_ok(p->cu_seqlens_host, p->n_docs, nq)) return KDA_ERR_BAD_SEQLENS;
+    if (p->cu_seqlens_k_host && !offsets_ok(p->cu_seqlens_k_host, p->n_docs, nk)) return KDA_ERR_BAD_SEQLENS;
+    P.n_docs = p->n_docs;
+    P.cu = p->cu_seqlens;
+    P.cuk = p->cu_seqlens_k ? p->cu_seqlens_k : p->cu_seqlens;
+  }
+  P.Nq = (int)nq;
+  P.Nk = (int)nk;
+  P.B = p->B;
+  P.T = p->T;
+  P.Tk = p->Tk;
+  P.Hq = p->Hq;
+  P.Hkv = p->Hkv;
+  P.G = p->Hq / p->Hkv;
+  P.causal = p->causal;
+  P.scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D);
+  P.scale2 = P.scale * LOG2E;
+  P.tile[0] = P.tile[1] = P.tile[2] = 64;
+  uint32_t tag = 0x536d61u;
+  for (const int32_t v : {P.B, P.T, P.Tk, P.Hq, P.Hkv, p->D, p->dtype, P.causal, P.n_docs, P.rows,
+                          (int32_t)(p->cu_seqlens_k != nullptr)})
+    tag = (tag ^ (uint32_t)v) * 16777619u;
+  uint32_t sb;
+  static_assert(sizeof(sb) == sizeof(P.scale), "");
+  memcpy(&sb, &P.scale, sizeof(sb));
+  tag = (tag ^ sb) * 16777619u;
+  P.tag = (int32_t)(tag | 1u);
+  *out = P;
+  return KDA_OK;
+}
+
+// Workspace: error word, saved-problem tag and tile counts; the tables; what a saving forward keeps.
+size_t layout(SmxP& P, int D, int dtype, bool bwd, void* base) {
+  unsigned char* w = (unsigned char*)base;
+  size_t o = 256;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = (o + bytes + 255) / 256 * 256;
+    return at;
+  };
+  P.err = (int32_t*)w;
+  P.wtag = (int32_t*)(w + 4);
+  P.counts = (int32_t*)(w + 8);
+  if (!P.rows)
+    for (int l = 0; l < (bwd ? 3 : 1); l++) {
+      P.pre[l] = (int32_t*)(w + take(((size_t)P.n_docs + 1) * sizeof(int32_t)));
+      P.list[l] = (int4*)(w + take((size_t)max_tiles(P, l) * 2 * sizeof(int4)));
+    }
+  if (bwd) {
+    P.lse2 = (float*)(w + take((size_t)P.Hq * P.Nq * sizeof(float)));
+    P.delta = (float*)(w + take((size_t)P.Hq * P.Nq * sizeof(float)));
+    if (dtype == KDA_BF16) P.res = (bf16*)(w + take((size_t)P.Nq * P.Hq * D * sizeof(bf16)));
+  }
+  return o;
+}
+
+template <int D, typename T>
+cudaError_t launch_delta(const SmxP& P, const void* o, const void* dO, cudaStream_t st) {
+  const int64_t rows = (int64_t)P.Nq * P.Hq, per = 256 / (D / 8), grid = (rows + per - 1) / per;
+  if (grid > 2147483647) return cudaErrorInvalidValue;
+  prof_begin(K_SMX_DELTA, st);
+  const cudaError_t e = launch_pdl(smx_delta_kernel<D, T>, dim3((unsigned)grid), dim3(256), 0, st, P, (const T*)o,
+                                   (const T*)dO);
+  prof_end(K_SMX_DELTA, st);
+  return e;
+}
+
+cudaError_t launch_table(const SmxP& P, int l0, int n, cudaStream_t st) {
+  prof_begin(K_SMX_TABLE, st);
+  const cudaError_t e = launch_pdl(smx_table_kernel, dim3(n), dim3(TT), 0, st, P, l0);
+  prof_end(K_SMX_TABLE, st);
+  return e;
+}
+
+}  // namespace
+}  // namespace smx
+}  // namespace kda
+
+using namespace kda;
+using namespace kda::smx;
+
+extern "C" KDA_API size_t kda_softmax_workspace_size(const kda_softmax_problem* p, int for_backward) {
+  SmxP P;
+  if (check(p, &P) != KDA_OK) return 0;
+  return layout(P, p->D, p->dtype, for_backward != 0, nullptr);
+}
+
+extern "C" KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, const void* q, const void* k,
+                                              const void* v, void* o, float* lse, int save_for_backward,
+                                              void* workspace, size_t workspace_bytes, cudaStream_t st) {
+  SmxP P;
+  const kda_status s = check(p, &P);
+  if (s != KDA_OK) return s;
+  if (!q || !k || !v || !o || !lse) return KDA_ERR_INVALID_ARG;
+  if (!a16(q) || !a16(k) || !a16(v) || !a16(o) || !a16(lse)) return KDA_ERR_ALIGNMENT;
+  P.save = save_for_backward != 0;
+  if (!workspace || workspace_bytes < layout(P, p->D, p->dtype, P.save, workspace)) return KDA_ERR_WORKSPACE;
+  if ((uintptr_t)workspace % 256 != 0) return KDA_ERR_ALIGNMENT;
+  if (!P.rows && launch_table(P, 0, 1, st) != cudaSuccess) return KDA_ERR_CUDA;
+  return launch_f32_fwd(P, p->D, p->dtype, q, k, v, o, lse, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, const void* q, const void* k,
+                                              const void* v, const void* o, const void* dO, void* dq, void* dk,
+                                              void* dv, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+  SmxP P;
+  const kda_status s = check(p, &P);
+  if (s != KDA_OK) return s;
+  if (!q || !k || !v || !o || !dO || !dq || !dk || !dv) return KDA_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, o, dO, (const void*)dq, (const void*)dk, (const void*)dv})
+    if (!a16(x)) return KDA_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < layout(P, p->D, p->dtype, true, workspace)) return KDA_ERR_WORKSPACE;
+  if ((uintptr_t)workspace % 256 != 0) return KDA_ERR_ALIGNMENT;
+  if (!P.rows && launch_table(P, 1, 2, st) != cudaSuccess) return KDA_ERR_CUDA;
+  cudaError_t e;
+  if (p->dtype == KDA_F32)
+    e = p->D == 64 ? launch_delta<64, float>(P, o, dO, st) : launch_delta<128, float>(P, o, dO, st);
+  else
+    e = p->D == 64 ? launch_delta<64, bf16>(P, o, dO, st) : launch_delta<128, bf16>(P, o, dO, st);
+  if (e != cudaSuccess) return KDA_ERR_CUDA;
+  return launch_f32_bwd(P, p->D, p->dtype, q, k, v, dO, dq, dk, dv, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}

@@ -1,0 +1,87 @@
+// Softmax attention with grouped heads: declarations shared by its kernels
+// (tables and entries: kda_softmax.cu, fp32: kda_softmax_f32.cu).
+#pragma once
+#include "kda_internal.cuh"
+#include "../../include/kda.h"
+
+namespace kda {
+namespace smx {
+
+using bf16 = __nv_bfloat16;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+struct SmxP {
+  int Nq, Nk, B, T, Tk, Hq, Hkv, G, n_docs, causal, rows;  // rows: documents are the rows of T queries, Tk keys
+  int save, tag;
+  float scale, scale2;  // scale2 = scale log2(e): exponentials are powers of two
+  const int32_t *cu, *cuk;
+  int32_t *err, *wtag, *counts;  // counts[l]: tiles of list l (cu_seqlens)
+  int32_t* pre[3];               // [n_docs + 1] first tile of each document
+  int4* list[3];                 // two int4 a tile, see Tile; 0: forward's queries, 1: dq's queries, 2: dk and dv's keys
+  int tile[3];                   // rows a tile
+  float *lse2, *delta;           // [Hq][Nq]: log2 of the rows' sums, saved by the forward; sum_d o dO
+  bf16* res;                     // [Nq, Hq, D] what rounding o to bf16 left, saved by the forward
+};
+
+// Rows t * tile .. of a document's queries (or keys): its first query, queries, first key, keys.
+struct Tile {
+  int q0, Lq, k0, Lk, t;
+};
+
+// Keys that query i of a document sees, as a bound on their index; queries that key j does not reach.
+__host__ __device__ inline int keys_of(int causal, int i, int Lq, int Lk) {
+  if (!causal) return Lk;
+  const int n = i + 1 + Lk - Lq;
+  return n < 0 ? 0 : n > Lk ? Lk : n;
+}
+__host__ __device__ inline int first_query(int causal, int j, int Lq, int Lk) {
+  if (!causal) return 0;
+  const int i = j - (Lk - Lq);
+  return i < 0 ? 0 : i > Lq ? Lq : i;
+}
+
+// Tile x of list l, the heavy ones first; false past the last.  by_key: the tiles are of keys.
+__device__ __forceinline__ bool tile_of(const SmxP& P, int l, int x, bool by_key, Tile& t) {
+  if (P.rows) {
+    const int nt = ((by_key ? P.Tk : P.T) + P.tile[l] - 1) / P.tile[l], i = x / P.B, b = x - i * P.B;
+    if (i >= nt) return false;
+    t.t = by_key ? i : nt - 1 - i;
+    t.q0 = b * P.T;
+    t.k0 = b * P.Tk;
+    t.Lq = P.T;
+    t.Lk = P.Tk;
+    return true;
+  }
+  if (x >= P.counts[l]) return false;
+  const int4 a = P.list[l][2 * (size_t)x], b = P.list[l][2 * (size_t)x + 1];
+  t.q0 = a.x;
+  t.Lq = a.y;
+  t.k0 = a.z;
+  t.Lk = a.w;
+  t.t = b.x;
+  return true;
+}
+
+// The backward's kernels read only what a forward of the same problem saved.
+__device__ __forceinline__ bool saved(const SmxP& P) {
+  if (*P.wtag == P.tag && *P.err == KDA_OK) return true;
+  if (*P.wtag != P.tag && blockIdx.x == 0 && threadIdx.x == 0) *P.err = KDA_ERR_WORKSPACE;
+  return false;
+}
+
+// Launches (fp32 io, and bf16): see the kernels.
+cudaError_t launch_f32_fwd(const SmxP& P, int D, int dtype, const void* q, const void* k, const void* v, void* o,
+                           float* lse, cudaStream_t st);
+cudaError_t launch_f32_bwd(const SmxP& P, int D, int dtype, const void* q, const void* k, const void* v,
+                           const void* dO, void* dq, void* dk, void* dv, cudaStream_t st);
+
+// Upper bound on the tiles of list l.
+inline int max_tiles(const SmxP& P, int l) {
+  const int n = l == 2 ? P.Nk : P.Nq, t = P.tile[l];
+  if (P.rows) return P.B * (((l == 2 ? P.Tk : P.T) + t - 1) / t);
+  const int64_t m = (int64_t)n / t + P.n_docs;
+  return (int)(m < n ? m : n);  // (every tile has a row)
+}
+
+}  // namespace smx
+}  // namespace kda

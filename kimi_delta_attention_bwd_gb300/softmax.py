@@ -1,0 +1,167 @@
+"""Softmax attention with grouped heads (kda_softmax_*): the full-attention
+layer that stands between the linear ones.
+
+  o_i = sum_j p_ij v_j,   p_ij = exp(scale q_i k_j - lse_i)
+
+per document and query head, over the keys j <= i + Lk - Lq (causal: the last
+query sees every key) or over all keys.  q, o [B, T, Hq, D]; k, v [B, Tk, Hkv, D]
+(bf16 or fp32; D = 64 or 128; Hq a multiple of Hkv); documents are the rows, or
+cu_seqlens int32 [n_docs + 1] over the flattened B*T queries, with cu_seqlens_k
+over the B*Tk keys where those differ (the next pieces of prompts whose keys are
+already there).  A query that sees no key gives o = 0 and lse = -inf.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import _all_well, _apart, _dims, _lib, _require
+from .linear import _host_offsets
+
+
+@dataclass
+class SoftmaxContext:
+    """What kda_softmax_backward needs from kda_softmax_forward."""
+    problem: object
+    q: torch.Tensor
+    k: torch.Tensor
+    v: torch.Tensor
+    o: torch.Tensor
+    cu_seqlens: Optional[torch.Tensor]
+    cu_seqlens_k: Optional[torch.Tensor]
+    host: tuple
+    workspace: torch.Tensor
+    saved: bool
+    stream: Optional[int] = None  # the workspace's, where the forward allocated it
+
+
+def _scale(scale):
+    if scale is not None and not scale > 0:
+        raise ValueError(f"scale must be positive, got {scale}")
+    return scale
+
+
+def _offsets(cu, name):
+    if cu is not None:
+        _dims(cu, name, 1)
+        if cu.numel() < 2:
+            raise ValueError(f"{name} must hold at least two offsets")
+
+
+def _groups(Hq, Hkv):
+    if Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hkv} key heads")
+
+
+def kda_softmax_forward(q, k, v, scale: Optional[float] = None, causal: bool = True, cu_seqlens=None,
+                        cu_seqlens_k=None, cu_seqlens_host=None, cu_seqlens_k_host=None,
+                        save_for_backward: bool = True, workspace: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None):
+    """Forward pass.  Returns (o, lse, ctx): lse [B, T, Hq] fp32, the rows'
+    log-sums; ctx feeds kda_softmax_backward when save_for_backward is set, which
+    reads o too: leave it as it is until then.  scale: 1/sqrt(D) unless given
+    (> 0).  out: optional preallocated o that shares no memory with the inputs."""
+    _dims(q, "q", 4)
+    _dims(k, "k", 4)
+    B, T, Hq, D = q.shape
+    Tk, Hkv = k.shape[1], k.shape[2]
+    io, i32 = q.dtype, torch.int32
+    _groups(Hq, Hkv)
+    _offsets(cu_seqlens, "cu_seqlens")
+    if cu_seqlens_k is not None:
+        _offsets(cu_seqlens_k, "cu_seqlens_k")
+        if cu_seqlens is None:
+            raise ValueError("cu_seqlens_k comes with cu_seqlens")
+    elif cu_seqlens is not None and T != Tk:
+        raise ValueError(f"{B * Tk} keys for {B * T} queries need cu_seqlens_k")
+    cu_seqlens_host = _host_offsets(cu_seqlens_host, cu_seqlens)
+    if cu_seqlens_k_host is not None and cu_seqlens_k is None:
+        raise ValueError("cu_seqlens_k_host comes with cu_seqlens_k")
+    cu_seqlens_k_host = _host_offsets(cu_seqlens_k_host, cu_seqlens_k)
+    n = 0 if cu_seqlens is None else cu_seqlens.numel()
+    keys = (B, Tk, Hkv, D)
+    specs = dict(q=(q, q.shape, io), k=(k, keys, io), v=(v, keys, io), out=(out, q.shape, io),
+                 cu_seqlens=(cu_seqlens, (n,), i32), cu_seqlens_k=(cu_seqlens_k, (n,), i32))
+    if not _all_well(*[s for s in specs.values() if s[0] is not None]):
+        _require(**specs)
+    if out is not None:
+        _apart("out", out, q=q, k=k, v=v)
+    if save_for_backward:  # (a buffer that the next batch's offsets overwrite must not change what the backward checks)
+        cu_seqlens_host, cu_seqlens_k_host = (
+            c if c is None else c.clone() if isinstance(c, torch.Tensor) else c.copy()
+            for c in (cu_seqlens_host, cu_seqlens_k_host))
+    prob = _lib.make_softmax_problem(B, T, Tk, Hq, Hkv, D, io, _scale(scale), causal, cu_seqlens, cu_seqlens_k,
+                                     cu_seqlens_host, cu_seqlens_k_host)
+    stream = None
+    if workspace is None:
+        stream = _lib._stream()
+        # (size 0 for a problem that the call below refuses with its own status)
+        workspace = torch.empty(_lib.kda_softmax_workspace_size(prob, save_for_backward) or 1, dtype=torch.uint8,
+                                device=q.device)
+    else:
+        _require(workspace=(workspace, workspace.shape, torch.uint8))
+    o = out if out is not None else torch.empty_like(q)
+    lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+    _lib.kda_softmax_fwd(prob, q, k, v, o, lse, save_for_backward, workspace)
+    return o, lse, SoftmaxContext(prob, q, k, v, o, cu_seqlens, cu_seqlens_k, (cu_seqlens_host, cu_seqlens_k_host),
+                                  workspace, bool(save_for_backward), stream)
+
+
+def kda_softmax_backward(ctx: SoftmaxContext, dO):
+    """Backward of sum(o * dO): a dict with dq, dk, dv in the io dtype.  Sums run
+    in a fixed order."""
+    if not ctx.saved:
+        raise ValueError("the forward saved nothing: call kda_softmax_forward with save_for_backward=True")
+    q, k = ctx.q, ctx.k
+    # (q stands for the forward's tensors: the current device may have changed since)
+    specs = dict(q=(q, q.shape, q.dtype), dO=(dO, q.shape, q.dtype))
+    if not _all_well(*specs.values()):
+        _require(**specs)
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(ctx.v)}
+    if ctx.stream is not None and ctx.stream != _lib._stream():
+        # a context dropped after this call must not give its memory to the forward's stream before the kernels end
+        ctx.workspace.record_stream(torch.cuda.current_stream())
+    _lib.kda_softmax_bwd(ctx.problem, q, k, ctx.v, ctx.o, dO, g["dq"], g["dk"], g["dv"], ctx.workspace)
+    return g
+
+
+def kda_softmax_decode_step(q, k, v, k_cache, v_cache, lengths, scale: Optional[float] = None,
+                            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """One token for each of n sequences: q [n, Hq, D], k, v [n, Hkv, D], caches
+    [n, cap, Hkv, D] (one dtype), lengths [n] int32 on the device: the tokens in
+    each cache.  k and v are written behind them, in place, and the query sees
+    them all and its own; lengths stays as it is (the layers of a model share it).
+    A negative length takes no step (o = 0, a padded batch), and neither does one
+    of cap or more (kda_device_status of a given workspace reports it).  out shares
+    no memory with the inputs, nor do the caches with each other or with k and v.
+    Returns o [n, Hq, D]."""
+    _dims(q, "q", 3)
+    _dims(k_cache, "k_cache", 4)
+    n, Hq, D = q.shape
+    cap, Hkv = k_cache.shape[1], k_cache.shape[2]
+    io = q.dtype
+    _groups(Hq, Hkv)
+    new, cache = (n, Hkv, D), (n, cap, Hkv, D)
+    specs = ((q, q.shape, io), (k, new, io), (v, new, io), (k_cache, cache, io), (v_cache, cache, io),
+             (lengths, (n,), torch.int32))
+    if out is not None:
+        specs += ((out, q.shape, io),)
+    if not _all_well(*specs):
+        _require(**dict(zip(("q", "k", "v", "k_cache", "v_cache", "lengths", "out"), specs)))
+    _apart("k_cache", k_cache, q=q, k=k, v=v, v_cache=v_cache)
+    _apart("v_cache", v_cache, q=q, k=k, v=v)
+    if out is not None:
+        _apart("out", out, q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache)
+    if workspace is None:
+        workspace = torch.empty(_lib.kda_softmax_decode_workspace_size(n, cap, Hq, Hkv, D) or 1, dtype=torch.uint8,
+                                device=q.device)
+    else:
+        _require(workspace=(workspace, workspace.shape, torch.uint8))
+    o = out if out is not None else torch.empty_like(q)
+    _lib.kda_softmax_decode(n, cap, Hq, Hkv, D, io, _scale(scale), q, k, v, k_cache, v_cache, lengths, o, workspace)
+    return o
+
+
+__all__ = ["SoftmaxContext", "kda_softmax_forward", "kda_softmax_backward", "kda_softmax_decode_step"]

@@ -1,0 +1,436 @@
+"""Softmax attention (kda_softmax_*) against its oracle.
+
+Tolerances, per element, from M, the sum of the magnitudes of an output's terms
+(the oracle's second answer), A the largest sum of magnitudes of a logit's
+terms, L the longest sum, D the head's width:
+ - a logit is a sum of D products in fp32, off by (D + 8) 2^-23 A (2^-23: the
+   tensor pipe's sums may truncate); weights are exponentials of differences of
+   two of them, by a function good to 2^-22: each is off by
+   E = 2 ((D + 8) 2^-23 A) + 2^-20 of itself, and quotients of them by 2 E;
+ - the sums over rows or keys add (L + D) 2^-23 M;
+ - bf16 io: weights (dv, o) and their gradients (dq, dk) are rounded to bf16
+   once, half a step is 2^-8 of each; delta is a sum over o, whose weights were
+   rounded too: 2 * 2^-8 M in dq and dk, whose M counts both;
+ - the output's own rounding, 2^-8 or 2^-24 of the value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import kimi_delta_attention_bwd_gb300 as kda
+from oracle import softmax_attention as osm
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+ROUND = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+def make(seed, lq, lk, Hq, Hkv, D, dt, rows=False, std=1.5):
+    g = torch.Generator().manual_seed(seed)
+    B = len(lq) if rows else 1
+    nq, nk = sum(lq) // B, sum(lk) // B
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x = dict(q=(std * r(B, nq, Hq, D)).to(DT[dt]), k=r(B, nk, Hkv, D).to(DT[dt]), v=r(B, nk, Hkv, D).to(DT[dt]),
+             dO=r(B, nq, Hq, D).to(DT[dt]))
+    off = lambda n: torch.tensor([0] + list(np.cumsum(n)), dtype=torch.int32)  # noqa: E731
+    x["cu"], x["cu_k"] = off(lq), off(lk)
+    x["rows"], x["same"] = rows, list(lq) == list(lk)
+    return x
+
+
+def flat(t):
+    return t.double().numpy().reshape(-1, *t.shape[2:])
+
+
+def oracle(x, causal=True, backward=True, scale=None):
+    D = x["q"].shape[-1]
+    return osm.attend(flat(x["q"]), flat(x["k"]), flat(x["v"]), x["cu"].tolist(), x["cu_k"].tolist(),
+                      scale or D ** -0.5, causal, flat(x["dO"]) if backward else None)
+
+
+def run(x, causal=True, backward=True, host=False, scale=None):
+    d = {n: t.cuda() if isinstance(t, torch.Tensor) else t for n, t in x.items()}
+    kw = {}
+    if not x["rows"]:
+        kw = dict(cu_seqlens=d["cu"], cu_seqlens_k=None if x["same"] else d["cu_k"])
+        if host:
+            kw.update(cu_seqlens_host=x["cu"], cu_seqlens_k_host=None if x["same"] else x["cu_k"])
+    o, lse, ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"], scale=scale, causal=causal,
+                                          save_for_backward=backward, **kw)
+    got = dict(o=o, lse=lse)
+    if backward:
+        got.update(kda.kda_softmax_backward(ctx, d["dO"]))
+    assert kda.kda_device_status(ctx.workspace) == 0
+    return got
+
+
+def limits(ans, dt, D, x):
+    ref, mag, A = ans
+    L = max(x["q"].shape[0] * x["q"].shape[1], x["k"].shape[0] * x["k"].shape[1]) + D
+    if "dk" in ref:
+        L *= x["q"].shape[2] // x["k"].shape[2]
+    E = 2 * (D + 8) * 2.0 ** -23 * A + 2.0 ** -20
+    R = ROUND[dt]
+    op = {"bf16": 2.0 ** -8, "f32": 0.0}[dt]
+    lim = {}
+    for n, r in ref.items():
+        if n == "lse":
+            lim[n] = 2 * E + L * 2.0 ** -23 + 2.0 ** -22 * mag[n]
+        else:
+            lim[n] = (2 * E + L * 2.0 ** -23 + op * (1 if n in ("o", "dv") else 2)) * mag[n] * (1 + R) + R * np.abs(r)
+    return lim
+
+
+def check(got, ans, dt, D, x):
+    for n, lim in limits(ans, dt, D, x).items():
+        r = ans[0][n]
+        g = got[n].detach().double().cpu().numpy().reshape(r.shape)
+        same = (g == r) & np.isinf(r)
+        bad = ~((np.abs(np.where(same, 0.0, g) - np.where(same, 0.0, r)) <= lim + 1e-30) | same)
+        assert not bad.any(), (n, int(bad.sum()), np.argwhere(bad)[:4].tolist(), g[bad][:4], r[bad][:4])
+
+
+# (query lengths, key lengths): one token to several tiles, tile borders, pieces over prefixes, rows without keys
+ROWS = [([1], [1]), ([2], [2]), ([63, 63], [63, 63]), ([64], [64]), ([65], [65]), ([127], [127]), ([128], [128]),
+        ([129], [129]), ([255], [255]), ([256], [256]), ([257] * 2, [257] * 2), ([300], [300]), ([515], [515]),
+        ([1], [700]), ([130], [389]), ([200], [70]), ([384], [129]), ([5], [1])]
+PACKED = [([5], [5]), ([1] * 9, [1] * 9), ([100, 0, 1, 27, 300, 128, 1], None), ([0, 0, 40], None), ([256, 1, 255], None),
+          ([7, 130, 0, 64], [200, 130, 33, 5]), ([60, 70], [0, 400]), ([300, 3], [1, 300])]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", range(len(ROWS)))
+def test_rows(dt, D, causal, case):
+    lq, lk = ROWS[case]
+    Hq, Hkv = [(2, 2), (4, 2), (3, 1)][case % 3]
+    x = make(case, lq, lk, Hq, Hkv, D, dt, rows=True)
+    check(run(x, causal), oracle(x, causal), dt, D, x)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", range(len(PACKED)))
+def test_packed(dt, D, causal, case):
+    lq, lk = PACKED[case]
+    Hq, Hkv = [(2, 1), (3, 3), (6, 2)][case % 3]
+    x = make(50 + case, lq, lk or lq, Hq, Hkv, D, dt)
+    check(run(x, causal, host=case % 2 == 0), oracle(x, causal), dt, D, x)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_many_documents(dt):
+    r = np.random.RandomState(5)
+    lq = r.randint(0, 7, 3000).tolist()
+    lk = [a + int(b) for a, b in zip(lq, r.randint(0, 4, 3000))]
+    x = make(6, lq, lk, 2, 1, 64, dt)
+    check(run(x), oracle(x), dt, 64, x)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_rows(D):
+    x = make(7, [2100], [2100], 2, 1, D, "bf16", rows=True)
+    check(run(x), oracle(x), "bf16", D, x)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_sharp_and_shifted_logits(dt, D):
+    """Logits far from zero: a running maximum that grows along the keys, and rows where one key takes all."""
+    x = make(8, [400], [400], 2, 2, D, dt, rows=True, std=1.0)
+    ramp = torch.linspace(0.0, 40.0, 400)[None, :, None]
+    x["q"][..., 0] = (D ** 0.5 * torch.ones(1, 400, 2)).to(DT[dt])
+    x["k"][..., 0] = ramp.expand(1, 400, 2).to(DT[dt])
+    check(run(x), oracle(x), dt, D, x)
+    x["k"][..., 0] = -x["k"][..., 0] * 4  # the largest logits come first, the rest vanish
+    check(run(x, causal=False), oracle(x, causal=False), dt, D, x)
+
+
+def test_scale_is_used():
+    x = make(9, [70], [70], 2, 2, 64, "bf16", rows=True)
+    check(run(x, scale=0.4), oracle(x, scale=0.4), "bf16", 64, x)
+
+
+@pytest.mark.parametrize("T", [2, 8, 40, 200, 700])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bf16_outputs_are_near_their_rounding(T, D):
+    """In the 2-norm the outputs are off by at most 1.5 times what rounding the exact ones to bf16 gives: the
+    roundings of the weights (or their gradients) and of the output are independent, sqrt(2), and delta adds little."""
+    x = make(10, [T] * max(1, 400 // T), [T] * max(1, 400 // T), 8, 4, D, "bf16")
+    got, (ref, _, _) = run(x), oracle(x)
+    for n in ("o", "dq", "dk", "dv"):
+        r = ref[n]
+        rounded = torch.from_numpy(r).to(torch.bfloat16).double().numpy()
+        off = np.linalg.norm(got[n].double().cpu().numpy().reshape(r.shape) - r)
+        assert off <= 1.5 * np.linalg.norm(rounded - r), (n, off / np.linalg.norm(rounded - r))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_neighbours_do_not_reach(dt):
+    """Infinities and NaN in one document leave the others' results as they were, bit for bit."""
+    lq, lk = [70, 130, 40], [90, 130, 300]
+    x = make(11, lq, lk, 4, 2, 64, dt)
+    want = run(x)
+    for n, cu in (("q", x["cu"]), ("k", x["cu_k"]), ("v", x["cu_k"]), ("dO", x["cu"])):
+        x[n][0, int(cu[1]):int(cu[2])] = float("nan") if n in ("q", "v") else float("inf")
+    got = run(x)
+    for n in want:
+        cu = x["cu_k"] if n in ("dk", "dv") else x["cu"]
+        for part in (slice(0, int(cu[1])), slice(int(cu[2]), None)):
+            assert torch.equal(got[n][0, part], want[n][0, part]), n
+        assert not torch.isfinite(got[n][0, int(cu[1]):int(cu[2])]).all() or n == "lse"
+
+
+def test_nan_reaches_its_own_row():
+    x = make(12, [40], [40], 1, 1, 64, "bf16", rows=True)
+    x["q"][0, 17, 0, 3] = float("nan")
+    got = run(x, backward=False)
+    assert torch.isnan(got["o"][0, 17]).all() and torch.isnan(got["lse"][0, 17]).all()
+    rest = [i for i in range(40) if i != 17]
+    assert torch.isfinite(got["o"][0, rest]).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_two_runs_give_the_same_bits(dt):
+    x = make(13, [300, 1, 200], [300, 1, 200], 8, 2, 128, dt)
+    a, b = run(x), run(x)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("rows", [True, False])
+def test_graph_replay_on_other_values_and_offsets(rows):
+    x = make(14, [150, 150], [150, 150], 4, 2, 64, "bf16", rows=rows)
+    y = make(15, [150, 150] if rows else [20, 280], [150, 150] if rows else [20, 280], 4, 2, 64, "bf16", rows=rows)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO", "cu")}
+    cu = None if rows else d["cu"]
+
+    def step():
+        o, lse, ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"], cu_seqlens=cu)
+        return dict(o=o, lse=lse, **kda.kda_softmax_backward(ctx, d["dO"]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for z in (x, y):
+        for n in d:
+            d[n].copy_(z[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run(z)
+        for n in got:
+            assert torch.equal(got[n], want[n]), n
+
+
+def test_backward_on_another_stream_and_twice():
+    x = make(16, [200], [200], 4, 4, 64, "bf16", rows=True)
+    want = run(x)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO")}
+    o, _, ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"])
+    first = kda.kda_softmax_backward(ctx, d["dO"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = kda.kda_softmax_backward(ctx, d["dO"])
+    del ctx
+    torch.cuda.synchronize()
+    for g in (first, second):
+        for n in g:
+            assert torch.equal(g[n], want[n]), n
+
+
+def test_bad_offsets_and_foreign_workspaces_are_reported():
+    x = make(17, [30, 40], [30, 40], 2, 2, 64, "bf16")
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO")}
+    for off in ([0, 80, 70], [1, 30, 70], [0, 30, 71], [0, -5, 70]):
+        out = torch.full_like(d["q"], 7.0)
+        bad = torch.tensor(off, dtype=torch.int32, device="cuda")
+        _, _, ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"], cu_seqlens=bad, out=out)
+        assert kda.kda_device_status(ctx.workspace) == -4
+        assert (out == 7.0).all()
+        kda.kda_softmax_backward(ctx, d["dO"])
+        assert kda.kda_device_status(ctx.workspace) != 0
+    # a workspace that another problem's forward saved
+    _, _, one = kda.kda_softmax_forward(d["q"], d["k"], d["v"], causal=False)
+    _, _, two = kda.kda_softmax_forward(d["q"], d["k"], d["v"], causal=True)
+    two.workspace = one.workspace
+    kda.kda_softmax_backward(two, d["dO"])
+    assert kda.kda_device_status(two.workspace) == -5
+
+
+def test_autograd_matches_the_calls_and_differences():
+    x = make(18, [33, 50], [33, 50], 4, 2, 64, "f32")
+    want = run(x)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO", "cu")}
+    leaves = [d[n].requires_grad_() for n in ("q", "k", "v")]
+    o = kda.softmax_attention(*leaves, cu_seqlens=d["cu"])
+    g = torch.autograd.grad(o, leaves, d["dO"])
+    assert torch.equal(o, want["o"])
+    for n, t in zip(("dq", "dk", "dv"), g):
+        assert torch.equal(t, want[n]), n
+    # without recording nothing is saved, and the bits are the same
+    with torch.no_grad():
+        assert torch.equal(kda.softmax_attention(*leaves, cu_seqlens=d["cu"]), o)
+    # an incoming gradient that is a strided view
+    wide = torch.zeros(*o.shape[:-1], 65, device="cuda")
+    wide[..., 1:] = d["dO"]
+    for t, u in zip(torch.autograd.grad(kda.softmax_attention(*leaves, cu_seqlens=d["cu"]), leaves, wide[..., 1:]), g):
+        assert torch.equal(t, u)
+
+
+# ---------------------------------------------------------------- single tokens
+def decode_case(seed, lens, cap, Hq, Hkv, D, dt):
+    g = torch.Generator().manual_seed(seed)
+    n = len(lens)
+    r = lambda *s: torch.randn(*s, generator=g).to(DT[dt])  # noqa: E731
+    return dict(q=(1.5 * torch.randn(n, Hq, D, generator=g)).to(DT[dt]), k=r(n, Hkv, D), v=r(n, Hkv, D),
+                k_cache=r(n, cap, Hkv, D), v_cache=r(n, cap, Hkv, D), lengths=torch.tensor(lens, dtype=torch.int32))
+
+
+def check_decode(x, dt, **kw):
+    d = {n: t.cuda() for n, t in x.items()}
+    cap, D = x["k_cache"].shape[1], x["q"].shape[-1]
+    # places behind the new token hold anything
+    for i, n in enumerate(x["lengths"].tolist()):
+        if 0 <= n < cap:
+            d["k_cache"][i, n + 1:] = float("nan")
+            d["v_cache"][i, n + 1:] = float("inf")
+    before = {n: d[n].clone() for n in ("k_cache", "v_cache")}
+    o = kda.kda_softmax_decode_step(d["q"], d["k"], d["v"], d["k_cache"], d["v_cache"], d["lengths"], **kw)
+    for i, n in enumerate(x["lengths"].tolist()):
+        if not 0 <= n < cap:
+            assert (o[i] == 0).all()
+            continue
+        for a in ("k", "v"):
+            before[a + "_cache"][i, n] = d[a][i]
+        K = torch.cat([x["k_cache"][i, :n], x["k"][i:i + 1]])[None]
+        V = torch.cat([x["v_cache"][i, :n], x["v"][i:i + 1]])[None]
+        one = dict(q=x["q"][i][None, None], k=K, v=V)
+        ans = osm.attend(flat(one["q"]), flat(K), flat(V), [0, 1], [0, n + 1], kw.get("scale") or D ** -0.5, True)
+        check(dict(o=o[i], lse=torch.from_numpy(ans[0]["lse"])), ans, dt, D, one)
+    for n, t in before.items():
+        assert torch.equal(d[n].nan_to_num(3.0, 4.0), t.nan_to_num(3.0, 4.0)), n
+    return o
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", [(1, 1), (8, 8), (6, 2), (16, 1), (17, 1), (40, 2)])
+def test_decode(dt, D, heads):
+    check_decode(decode_case(20, [0, 1, 15, 16, 63, 64, 100, 128, 199], 200, *heads, D, dt), dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,cap", [([5000], 5001), ([0], 1), ([130], 4096), ([1000, 1, 4095], 4096), ([255] * 70, 256)])
+def test_decode_lengths(dt, lens, cap):
+    check_decode(decode_case(21, lens, cap, 8, 2, 64, dt), dt)
+
+
+def test_decode_idle_and_full_sequences():
+    x = decode_case(22, [3, -1, 50, 7, 49], 50, 4, 2, 64, "bf16")
+    d = {n: t.cuda() for n, t in x.items()}
+    from kimi_delta_attention_bwd_gb300 import _lib
+    ws = torch.empty(_lib.kda_softmax_decode_workspace_size(5, 50, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    check_decode(x, "bf16", workspace=ws)
+    assert kda.kda_device_status(ws) == -4  # (a sequence has no room)
+    d["lengths"][2] = 9
+    kda.kda_softmax_decode_step(*(d[n] for n in ("q", "k", "v", "k_cache", "v_cache", "lengths")), workspace=ws)
+    assert kda.kda_device_status(ws) == 0
+
+
+def test_decode_pieces_agree_with_one_piece():
+    """A long cache read in pieces by one sequence, and whole where the sequences fill the GPU."""
+    x = decode_case(23, [3000], 3001, 4, 4, 128, "f32")
+    a = check_decode(x, "f32")
+    many = {n: t.expand(200, *t.shape[1:]).contiguous() for n, t in x.items()}
+    d = {n: t.cuda() for n, t in many.items()}
+    b = kda.kda_softmax_decode_step(*(d[n] for n in ("q", "k", "v", "k_cache", "v_cache", "lengths")))
+    assert torch.allclose(a.expand_as(b), b, rtol=0, atol=2e-6)
+
+
+def test_prompt_then_tokens_is_the_longer_prompt():
+    """A prompt through norm, rotary positions and attention into a cache, then tokens one by one, as a captured
+    graph that is replayed: the rows of the whole prompt."""
+    torch.manual_seed(24)
+    B, T, n, Hq, Hkv, D = 2, 37, 5, 4, 2, 64
+    f, s = kda.rotary_frequencies(32, base=500000.0, factor=2.0, scaling="yarn", original_length=64)
+    x = torch.randn(B, T + n, (Hq + 2 * Hkv) * D, device="cuda")
+    w = 1 + 0.1 * torch.randn(D, device="cuda")
+
+    def project(x):
+        q, k, v = x.to(torch.bfloat16).split([Hq * D, Hkv * D, Hkv * D], -1)
+        q, k, v = (t.unflatten(-1, (-1, D)).contiguous() for t in (q, k, v))
+        return kda.kda_layer_norm(q, w), kda.kda_layer_norm(k, w), v
+    q, k, v = project(x)
+    q, k = kda.kda_rotary(q, k, f, scale=s)
+    want, _, _ = kda.kda_softmax_forward(q, k, v, save_for_backward=False)
+    kc, vc = (torch.full((B, T + n, Hkv, D), float("nan"), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    kc[:, :T], vc[:, :T] = k[:, :T], v[:, :T]
+    lengths = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    token = x[:, T].clone()
+
+    def step():
+        q, k, v = project(token)
+        q, k = kda.kda_rotary(q, k, f, positions=lengths, scale=s)
+        o = kda.kda_softmax_decode_step(q, k, v, kc, vc, lengths)
+        lengths.add_(1)
+        return o
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    lengths.fill_(T)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = step()
+    lengths.fill_(T)
+    for i in range(n):
+        token.copy_(x[:, T + i])
+        graph.replay()
+        # two roundings of each side's weights and two of its outputs, of values below the largest |v|
+        assert float((o.float() - want[:, T + i].float()).abs().max()) <= 4 * 2.0 ** -8 * float(v.abs().max())
+    assert torch.equal(kc, k) and torch.equal(vc, v) and int(lengths[0]) == T + n
+
+
+def test_a_hybrid_block_trains():
+    """Norm, a linear-attention layer and a softmax-attention layer with rotary positions on packed documents: the
+    gradients of all leaves against differences along a random direction."""
+    torch.manual_seed(25)
+    B, T, Hq, Hkv, D = 1, 150, 4, 2, 64
+    cu = torch.tensor([0, 60, 61, 150], dtype=torch.int32, device="cuda")
+    f, _ = kda.rotary_frequencies(D)
+    x = torch.randn(B, T, Hq * D, device="cuda")
+    shapes = dict(w=(Hq * D,), wq=(Hq * D, Hq * D), wk=(Hq * D, Hkv * D), wv=(Hq * D, Hkv * D))
+    leaves = {n: (torch.randn(*s, device="cuda") / (Hq * D) ** 0.5).requires_grad_() for n, s in shapes.items()}
+    A = torch.linspace(-4.0, -1.0, Hq, device="cuda").requires_grad_()
+    leaves["A"] = A
+    up = torch.randn(B, T, Hq, D, device="cuda")
+
+    def block(p):
+        y = kda.layer_norm(x, 1 + p["w"])
+        h = y.view(B, T, Hq, D)
+        y = y + kda.linear_attention(h, h, h, p["A"], cu_seqlens=cu).reshape(B, T, Hq * D) * 0.1
+        q, k, v = ((y @ p[n]).view(B, T, -1, D) for n in ("wq", "wk", "wv"))
+        q, k = kda.rotary(q, k, f, cu_seqlens=cu)
+        return (kda.softmax_attention(q, k, v, cu_seqlens=cu) * up).sum()
+    names = list(leaves)
+    grads = torch.autograd.grad(block(leaves), [leaves[n] for n in names])
+    for n, g in zip(names, grads):
+        with torch.no_grad():
+            step = torch.randn_like(leaves[n])
+            h = 2e-3 * float(leaves[n].norm() / step.norm())
+            p, m = dict(leaves), dict(leaves)
+            p[n], m[n] = leaves[n] + h * step, leaves[n] - h * step
+            num = float(block(p).double() - block(m).double()) / (2 * h)
+        want = float((g.double() * step.double()).sum())
+        # the differences' own error: fp32 noise of a sum of B T Hq D terms over 2 h, and a third derivative's h^2
+        scale = float(g.norm() * step.norm())
+        assert abs(num - want) <= 2e-2 * scale, (n, num, want, scale)
