@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libkda_gb300.so")
 SOURCES = ["kda_api.cu", "kda_fwd.cu", "kda_bwd.cu", "kda_fast.cu", "kda_decode.cu", "kda_norm.cu", "kda_conv.cu",
-           "kda_linear.cu", "kda_linear_f32.cu", "kda_layer_norm.cu", "kda_softmax.cu", "kda_softmax_f32.cu",
+           "kda_linear.cu", "kda_linear_f32.cu", "kda_layer_norm.cu", "kda_softmax.cu", "kda_softmax_f32.cu", "kda_softmax_tc.cu",
            "kda_softmax_decode.cu", "kda_rotary.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -200,7 +200,8 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   P.causal = p->causal;
   P.scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D);
   P.scale2 = P.scale * LOG2E;
-  P.tile[0] = P.tile[1] = P.tile[2] = 64;
+  P.tile[0] = p->dtype == KDA_BF16 ? TC_FWD : 64;
+  P.tile[1] = P.tile[2] = 64;
   uint32_t tag = 0x536d61u;
   for (const int32_t v : {P.B, P.T, P.Tk, P.Hq, P.Hkv, p->D, p->dtype, P.causal, P.n_docs, P.rows,
                           (int32_t)(p->cu_seqlens_k != nullptr)})
@@ -282,7 +283,9 @@ extern "C" KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, cons
   if (!workspace || workspace_bytes < layout(P, p->D, p->dtype, P.save, workspace)) return KDA_ERR_WORKSPACE;
   if ((uintptr_t)workspace % 256 != 0) return KDA_ERR_ALIGNMENT;
   if (!P.rows && launch_table(P, 0, 1, st) != cudaSuccess) return KDA_ERR_CUDA;
-  return launch_f32_fwd(P, p->D, p->dtype, q, k, v, o, lse, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  const cudaError_t e = p->dtype == KDA_BF16 ? launch_tc_fwd(P, p->D, q, k, v, o, lse, st)
+                                             : launch_f32_fwd(P, p->D, p->dtype, q, k, v, o, lse, st);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 extern "C" KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, const void* q, const void* k,

@@ -1,5 +1,6 @@
 // Softmax attention with grouped heads: declarations shared by its kernels
-// (tables and entries: kda_softmax.cu, fp32: kda_softmax_f32.cu).
+// (tables and entries: kda_softmax.cu, bf16: kda_softmax_tc.cu, fp32:
+// kda_softmax_f32.cu).
 #pragma once
 #include "kda_internal.cuh"
 #include "../../include/kda.h"
@@ -74,6 +75,11 @@ cudaError_t launch_f32_fwd(const SmxP& P, int D, int dtype, const void* q, const
                            float* lse, cudaStream_t st);
 cudaError_t launch_f32_bwd(const SmxP& P, int D, int dtype, const void* q, const void* k, const void* v,
                            const void* dO, void* dq, void* dk, void* dv, cudaStream_t st);
+
+// bf16 io: tiles of 256 queries (forward), 128 queries and 128 keys (backward).
+constexpr int TC_FWD = 256;
+cudaError_t launch_tc_fwd(const SmxP& P, int D, const void* q, const void* k, const void* v, void* o, float* lse,
+                          cudaStream_t st);
 
 // Upper bound on the tiles of list l.
 inline int max_tiles(const SmxP& P, int l) {

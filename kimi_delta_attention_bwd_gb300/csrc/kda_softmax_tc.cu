@@ -1,0 +1,452 @@
+// Softmax attention for bf16 io on the 5th-generation tensor cores (tcgen05, accumulators in tensor memory).
+//
+// Forward, per CTA: 256 queries of one head as two tiles of 128 over the keys in blocks of 128.  One warp loads
+// (TMA, a ring of key and value blocks), one thread issues the products, and per tile four warps, a thread a row,
+// turn the block of logits S = q k^T into weights P = 2^(scale2 S - m): row maximum, exponentials, row sum.  P goes
+// back to tensor memory over S, as bf16, and is the product P v's operand there.  While one tile's weights are formed
+// the other's products run.  The maximum m that the exponents are taken against is raised (and o and the sum scaled
+// down) only where a row's maximum has grown by 2^8: weights stay below 2^8, which bf16 and fp32 hold with the same
+// relative precision as those below 1.
+// Weights are rounded to bf16 (2^-8, the operand's type; o's error with that is that of one rounding of o times
+// sqrt(2)), but in blocks that a mask cuts they enter as two parts (2^-16): rows with few keys have theirs there, and
+// the backward's delta = o dO cancels against dO v in just those rows.
+#include "kda_softmax.cuh"
+#include "kda_mma.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace smx {
+namespace {
+
+constexpr int BLK = 128;       // rows of a block of keys (or queries)
+constexpr int HALF = 16384;    // bytes of 128 rows by 64 columns, one swizzled half of a block
+constexpr float GROW = 8.0f;   // log2 of what a weight may exceed 1 by
+
+// ------------------------------------------------------------ helpers
+// Descriptors of a block of 128 rows in 128-byte swizzled halves of 64 columns (TMA's layout): 8-row groups 1024 bytes apart.
+// K-major (rows are M or N): 16 columns of the contraction are 32 bytes of the swizzled row.  MN-major (rows are the
+// contraction): 16 rows are 2048 bytes, and the next 64 columns are a half away.
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t desc_k(uint32_t block, int step) {  // columns 16 step ..
+  return sdesc(block + (step >> 2) * HALF + (step & 3) * 32, 16);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t block, int step) {  // rows 16 step ..
+  return sdesc(block + step * 2048, HALF);
+}
+constexpr uint32_t idesc(int M, int N, bool b_mn) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)b_mn << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+  tc::mma_issue(d, a, b, id, acc);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {  // A in tensor memory
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      : "memory");
+}
+
+// 32 columns of this warp's lanes, a lane a row.
+__device__ __forceinline__ void tm_ld32(uint32_t a, float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a));
+}
+__device__ __forceinline__ void tm_ld16(uint32_t a, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::"r"(
+          r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+      : "memory");
+}
+// Waits for the loads in flight; the values they bring depend on it, so that no use moves before it.
+__device__ __forceinline__ void tm_wait_ld(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                 "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]),
+                 "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
+                 "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                 "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+                 "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float low(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float high(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// Whole-warp wait on a barrier's phase; gives up (and lets every other wait of the CTA give up) after mma::WAIT_POLLS.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead) {
+  bool ok = mma::mbar_try(bar, parity);
+  for (int it = 0; !ok && it < mma::WAIT_POLLS; it++) {
+    ok = mma::mbar_try(bar, parity);
+    if (!ok && *(volatile int*)dead) break;
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) *(volatile int*)dead = 1;
+  return ok;
+}
+
+// 32 logits of a row: those from `left` on are not seen.
+__device__ __forceinline__ void mask(float (&v)[32], int left) {
+#pragma unroll
+  for (int e = 0; e < 32; e++) v[e] = e < left ? v[e] : -INFINITY;
+}
+__device__ __forceinline__ void row_max(float (&v)[32], bool cut, int left, float (&mx)[4]) {
+  if (cut) mask(v, left);
+#pragma unroll
+  for (int e = 0; e < 32; e++) mx[e & 3] = fmaxf(mx[e & 3], v[e]);
+}
+// 32 logits into weights, their sum, and as bf16 to tensor memory (second parts 16 columns further, where a mask cuts).
+__device__ __forceinline__ void weights(float (&v)[32], uint32_t to, float scale2, float neg, bool cut,
+                                        float (&sum)[4]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int e = 0; e < 32; e++) {
+    v[e] = ex2(fmaf(v[e], scale2, neg));
+    sum[e & 3] += v[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 16; e++) w[e] = pack(v[2 * e], v[2 * e + 1]);
+  tm_st16(to, w);
+  if (cut) {
+#pragma unroll
+    for (int e = 0; e < 16; e++) w[e] = pack(v[2 * e] - low(w[e]), v[2 * e + 1] - high(w[e]));
+    tm_st16(to + 16, w);
+  }
+}
+
+// Rows n .. of a block (other documents' tokens) become zeros, by one warp, before products read them.
+template <int D>
+__device__ __forceinline__ void zero_rows(unsigned char* block, int n) {
+  for (int i = threadIdx.x & 31; i < (BLK - n) * 8 * (D / 64); i += 32) {
+    const int half = i / ((BLK - n) * 8), r = i % ((BLK - n) * 8);
+    *reinterpret_cast<uint4*>(block + half * HALF + n * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+  }
+  mma::fence_async_smem();
+  __syncwarp();
+}
+template <int D>
+__device__ __forceinline__ void load_block(unsigned char* dst, const CUtensorMap* map, int head, int row,
+                                           uint64_t* bar) {
+#pragma unroll
+  for (int c = 0; c < D / 64; c++) mma::tma_load_2d(dst + c * HALF, map, head * D + 64 * c, row, bar);
+}
+
+// ------------------------------------------------------------ forward
+template <int D>
+struct Fwd {
+  static constexpr int BYTES = HALF * (D / 64);      // a block
+  static constexpr int STAGES = D == 64 ? 8 : 5;     // blocks in the ring of keys and values
+  static constexpr int SMEM = (2 + STAGES) * BYTES + 1024 + 256;
+  static constexpr uint32_t S0 = 0, O0 = 2 * BLK;    // tensor memory columns: S of both tiles, o of both tiles
+};
+
+struct FwdBars {
+  uint64_t q[2], full[8], empty[8], s[2], p[2], o[2], drain;
+  uint32_t tmem;
+  int dead;
+};
+
+constexpr int FWD_THREADS = 384;
+
+template <int D>
+__global__ void __launch_bounds__(FWD_THREADS, 1)
+smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, bf16* __restrict__ o, float* __restrict__ lse) {
+  using F = Fwd<D>;
+  extern __shared__ unsigned char raw[];
+  __shared__ FwdBars B;
+  unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
+  unsigned char* ring = sm + 2 * F::BYTES;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (warp == 8) tc::tmem_alloc(&B.tmem, 512);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; i++) {
+      mma::mbar_init(&B.q[i], 1);
+      mma::mbar_init(&B.s[i], 1);
+      mma::mbar_init(&B.p[i], 4);
+      mma::mbar_init(&B.o[i], 1);
+    }
+    for (int i = 0; i < F::STAGES; i++) {
+      mma::mbar_init(&B.full[i], 1);
+      mma::mbar_init(&B.empty[i], 1);
+    }
+    mma::mbar_init(&B.drain, 1);
+    B.dead = 0;
+    mma::mbar_init_fence();
+  }
+  pdl_wait();
+  if (P.rows && blockIdx.x == 0 && threadIdx.x == 0) {
+    *P.err = KDA_OK;
+    *P.wtag = P.save ? P.tag : 0;
+  }
+  Tile t;
+  const int h = blockIdx.x % P.Hq, hk = h / P.G;
+  const bool live = tile_of(P, 0, blockIdx.x / P.Hq, false, t);
+  int i0 = 0, nq = 0, nb[2] = {0, 0}, clean[2] = {0, 0};  // blocks of each tile; those that no mask cuts
+  if (live) {
+    i0 = t.t * TC_FWD;
+    nq = min(TC_FWD, t.Lq - i0);
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+      if (i * BLK < nq) {
+        nb[i] = (keys_of(P.causal, i0 + min(nq, (i + 1) * BLK) - 1, t.Lq, t.Lk) + BLK - 1) / BLK;
+        clean[i] = keys_of(P.causal, i0 + i * BLK, t.Lq, t.Lk) / BLK;
+      }
+  }
+  const int n = max(nb[0], nb[1]);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = B.tmem;
+
+  if (warp == 9) {  // loads
+    if (lane == 0 && n > 0) {
+      for (int i = 0; i < 2; i++)
+        if (nb[i]) {
+          mma::mbar_expect_tx(&B.q[i], F::BYTES);
+          load_block<D>(sm + i * F::BYTES, &mq, h, t.q0 + i0 + i * BLK, &B.q[i]);
+        }
+    }
+    __syncwarp();
+    int x = 0;
+    for (; x < 2 * n; x++) {
+      const int s = x % F::STAGES, r = x / F::STAGES;
+      if (r > 0 && !wait(&B.empty[s], (r - 1) & 1, &B.dead)) break;
+      if (lane == 0) {
+        mma::mbar_expect_tx(&B.full[s], F::BYTES);
+        load_block<D>(ring + s * F::BYTES, x & 1 ? &mv : &mk, hk, t.k0 + x / 2 * BLK, &B.full[s]);
+      }
+      __syncwarp();
+    }
+    if (*(volatile int*)&B.dead) {  // every copy lands before the shared memory is released
+      for (int y = max(0, x - F::STAGES); y < x; y++)
+        for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.full[y % F::STAGES], (y / F::STAGES) & 1); it++) {}
+      for (int i = 0; i < 2; i++)
+        if (nb[i])
+          for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.q[i], 0); it++) {}
+    }
+  } else if (warp == 8) {  // products
+    const uint32_t q0 = mma::smem_u32(sm), r0 = mma::smem_u32(ring);
+    constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
+    auto logits = [&](int i, int x) {
+      const uint32_t kb = r0 + x % F::STAGES * F::BYTES, qb = q0 + i * F::BYTES, d = tm + F::S0 + i * BLK;
+#pragma unroll
+      for (int s = 0; s < D / 16; s++) mma_ss(d, desc_k(qb, s), desc_k(kb, s), id_s, s > 0);
+      tc::commit(&B.s[i]);
+    };
+    auto run = [&]() -> bool {
+      if (!wait(&B.full[0], 0, &B.dead)) return false;
+      for (int i = 0; i < 2; i++)
+        if (nb[i]) {
+          if (!wait(&B.q[i], 0, &B.dead)) return false;
+          if (lane == 0) logits(i, 0);
+        }
+      if (lane == 0) tc::commit(&B.empty[0]);
+      __syncwarp();
+      for (int j = 0; j < n; j++) {
+        const int xv = 2 * j + 1, xk = 2 * j + 2, sv = xv % F::STAGES, sk = xk % F::STAGES;
+        if (!wait(&B.full[sv], (xv / F::STAGES) & 1, &B.dead)) return false;
+        if (t.Lk - j * BLK < BLK) zero_rows<D>(ring + sv * F::BYTES, t.Lk - j * BLK);
+        if (j + 1 < n && !wait(&B.full[sk], (xk / F::STAGES) & 1, &B.dead)) return false;
+        for (int i = 0; i < 2; i++) {
+          if (j >= nb[i]) continue;
+          if (!wait(&B.p[i], j & 1, &B.dead)) return false;
+          tc::fence_after();
+          if (lane == 0) {
+            const uint32_t a = tm + F::S0 + i * BLK, d = tm + F::O0 + i * D, vb = r0 + sv * F::BYTES;
+#pragma unroll
+            for (int s = 0; s < BLK / 16; s++) mma_ts(d, a + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, j > 0 || s > 0);
+            if (j >= clean[i])
+#pragma unroll
+              for (int s = 0; s < BLK / 16; s++) mma_ts(d, a + 16 + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, true);
+            tc::commit(&B.o[i]);
+            if (i == 1 || j >= nb[1]) tc::commit(&B.empty[sv]);
+            if (j + 1 < nb[i]) logits(i, xk);
+            if (j + 1 < n && (i == 1 || j + 1 >= nb[1])) tc::commit(&B.empty[sk]);
+          }
+          __syncwarp();
+        }
+      }
+      return true;
+    };
+    if (n > 0 && !run()) {  // (its products end before the tensor memory is released)
+      if (lane == 0) tc::commit(&B.drain);
+      __syncwarp();
+      for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
+    }
+  } else if (warp < 8 && live) {  // weights: a thread a row
+    const int i = warp / 4, r = i * BLK + (threadIdx.x & 127), nbi = i ? nb[1] : nb[0], cleani = i ? clean[1] : clean[0];
+    const bool in = r < nq;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tm + F::S0 + i * BLK + lanes, to = tm + F::O0 + i * D + lanes;
+    const int lim = in ? keys_of(P.causal, i0 + r, t.Lq, t.Lk) : 0;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < nbi; j++) {
+      ok = wait(&B.s[i], j & 1, &B.dead);
+      if (!ok) break;
+      tc::fence_after();
+      // The row in four pieces of 32 columns: all of them for the maximum, then again for the weights (two are still
+      // in registers).  A piece's weights replace it: 16 columns, and 16 for their second parts.
+      const bool cut = j >= cleani;
+      const int left = lim - j * BLK;
+      float a[32], b[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      tm_ld32(ts, a);
+      tm_wait_ld(a);
+      tm_ld32(ts + 32, b);
+      row_max(a, cut, left, mx);
+      tm_wait_ld(b);
+      tm_ld32(ts + 64, a);
+      row_max(b, cut, left - 32, mx);
+      tm_wait_ld(a);
+      tm_ld32(ts + 96, b);
+      row_max(a, cut, left - 64, mx);
+      tm_wait_ld(b);
+      row_max(b, cut, left - 96, mx);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const bool raise = top > m && !((top - m) * P.scale2 <= GROW);
+      if (__any_sync(0xffffffffu, raise)) {
+        const float up = raise ? ex2((m - top) * P.scale2) : 1.0f;
+        if (raise) m = top;
+        l *= up;
+        if (j > 0) {
+          ok = wait(&B.o[i], (j - 1) & 1, &B.dead);
+          if (!ok) break;
+          tc::fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float v[16];
+            tm_ld16(to + c, v);
+            tm_wait_ld(v);
+#pragma unroll
+            for (int e = 0; e < 16; e++) v[e] *= up;
+            tm_st16(to + c, reinterpret_cast<const uint32_t*>(v));
+          }
+        }
+      }
+      const float neg = m == -INFINITY ? 0.f : -m * P.scale2;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      weights(a, ts + 64, P.scale2, neg, cut, sum);
+      tm_ld32(ts, a);
+      weights(b, ts + 96, P.scale2, neg, cut, sum);
+      tm_wait_ld(a);
+      tm_ld32(ts + 32, b);
+      if (cut) mask(a, left);
+      weights(a, ts, P.scale2, neg, cut, sum);
+      tm_wait_ld(b);
+      if (cut) mask(b, left - 32);
+      weights(b, ts + 32, P.scale2, neg, cut, sum);
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tm_wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mma::mbar_arrive(&B.p[i]);
+    }
+    if (ok && nbi > 0) {
+      ok = wait(&B.o[i], (nbi - 1) & 1, &B.dead);
+      tc::fence_after();
+    }
+    if (ok) {
+      const float inv = l == 0.f ? 0.f : 1.0f / l, l2 = m * P.scale2 + log2f(l);
+      const size_t row = (size_t)(t.q0 + i0 + r) * P.Hq + h;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        float v[32];
+        if (nbi > 0) {
+          tm_ld32(to + c, v);
+          tm_wait_ld(v);
+        }
+        if (in) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t u[4];
+#pragma unroll
+          for (int y = 0; y < 4; y++) {
+            float &a = v[e + 2 * y], &b = v[e + 2 * y + 1];
+            a = l == 0.f ? 0.f : a * inv;
+            b = l == 0.f ? 0.f : b * inv;
+            u[y] = pack(a, b);
+            a -= low(u[y]);
+            b -= high(u[y]);
+          }
+          *reinterpret_cast<uint4*>(o + row * D + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
+          if (P.save)
+            *reinterpret_cast<uint4*>(P.res + row * D + c + e) =
+                make_uint4(pack(v[e], v[e + 1]), pack(v[e + 2], v[e + 3]), pack(v[e + 4], v[e + 5]), pack(v[e + 6], v[e + 7]));
+        }
+        }
+        __syncwarp();
+      }
+      if (in) {
+        lse[row] = l2 * LN2;
+        if (P.save) P.lse2[(size_t)h * P.Nq + t.q0 + i0 + r] = l2;
+      }
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && B.dead) *P.err = KDA_ERR_DEVICE;
+  if (warp == 8) {
+    tc::fence_after();
+    tc::tmem_dealloc(tm, 512);
+  }
+}
+
+template <int D>
+cudaError_t fwd(const SmxP& P, const void* q, const void* k, const void* v, void* o, float* lse, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  if (!encode_head_rows(&mq, q, P.Nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, P.Nk, P.Hkv, D, BLK) ||
+      !encode_head_rows(&mv, v, P.Nk, P.Hkv, D, BLK))
+    return cudaErrorInvalidValue;
+  const int64_t grid = (int64_t)max_tiles(P, 0) * P.Hq;
+  if (grid > 2147483647) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(smx_tc_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Fwd<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  prof_begin(K_SMX_FWD, st);
+  e = launch_pdl(smx_tc_fwd_kernel<D>, dim3((unsigned)grid), dim3(FWD_THREADS), Fwd<D>::SMEM, st, P, mq, mk, mv,
+                 (bf16*)o, lse);
+  prof_end(K_SMX_FWD, st);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_tc_fwd(const SmxP& P, int D, const void* q, const void* k, const void* v, void* o, float* lse,
+                          cudaStream_t st) {
+  return D == 64 ? fwd<64>(P, q, k, v, o, lse, st) : fwd<128>(P, q, k, v, o, lse, st);
+}
+
+}  // namespace smx
+}  // namespace kda
