@@ -201,7 +201,7 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   P.scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D);
   P.scale2 = P.scale * LOG2E;
   P.tile[0] = p->dtype == KDA_BF16 ? TC_FWD : 64;
-  P.tile[1] = P.tile[2] = 64;
+  P.tile[1] = P.tile[2] = p->dtype == KDA_BF16 ? TC_BWD : 64;
   uint32_t tag = 0x536d61u;
   for (const int32_t v : {P.B, P.T, P.Tk, P.Hq, P.Hkv, p->D, p->dtype, P.causal, P.n_docs, P.rows,
                           (int32_t)(p->cu_seqlens_k != nullptr)})
@@ -306,5 +306,7 @@ extern "C" KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, cons
   else
     e = p->D == 64 ? launch_delta<64, bf16>(P, o, dO, st) : launch_delta<128, bf16>(P, o, dO, st);
   if (e != cudaSuccess) return KDA_ERR_CUDA;
-  return launch_f32_bwd(P, p->D, p->dtype, q, k, v, dO, dq, dk, dv, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  e = p->dtype == KDA_BF16 ? launch_tc_bwd(P, p->D, q, k, v, dO, dq, dk, dv, st)
+                           : launch_f32_bwd(P, p->D, p->dtype, q, k, v, dO, dq, dk, dv, st);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

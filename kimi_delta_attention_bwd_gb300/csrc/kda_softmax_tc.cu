@@ -69,6 +69,16 @@ __device__ __forceinline__ void tm_ld16(uint32_t a, float (&v)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(a));
 }
+__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
+      : "memory");
+}
 __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::"r"(
@@ -441,11 +451,506 @@ cudaError_t fwd(const SmxP& P, const void* q, const void* k, const void* v, void
   return e;
 }
 
+// ------------------------------------------------------------ backward
+// The backward's weights of 32 logits of a key: queries lo .. hi - 1 of them see it; l2: the queries' log2 sums.
+__device__ __forceinline__ void bwd_weights(float (&v)[32], const float* l2, float scale2, bool cut, int lo, int hi) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(l2 + e);
+    v[e] = ex2(fmaf(v[e], scale2, -l.x));
+    v[e + 1] = ex2(fmaf(v[e + 1], scale2, -l.y));
+    v[e + 2] = ex2(fmaf(v[e + 2], scale2, -l.z));
+    v[e + 3] = ex2(fmaf(v[e + 3], scale2, -l.w));
+  }
+  if (cut)
+#pragma unroll
+    for (int e = 0; e < 32; e++) v[e] = e >= lo && e < hi ? v[e] : 0.f;
+}
+// 32 gradients p (dp - delta) as bf16 pairs (an unseen pair's is zero whatever dp holds).
+__device__ __forceinline__ void bwd_grads(const float (&p)[32], float (&dp)[32], const float* dl, bool cut, int lo,
+                                          int hi, uint32_t* w) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(dl + e);
+    dp[e] = p[e] * (dp[e] - l.x);
+    dp[e + 1] = p[e + 1] * (dp[e + 1] - l.y);
+    dp[e + 2] = p[e + 2] * (dp[e + 2] - l.z);
+    dp[e + 3] = p[e + 3] * (dp[e + 3] - l.w);
+  }
+  if (cut)
+#pragma unroll
+    for (int e = 0; e < 32; e++) dp[e] = e >= lo && e < hi ? dp[e] : 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; e++) w[e] = pack(dp[2 * e], dp[2 * e + 1]);
+}
+// The same of a query's row: its sums are scalars, its keys end at `left`.
+__device__ __forceinline__ void dq_grads(float (&v)[32], const float (&dp)[32], float l2, float dl, float scale2,
+                                         bool cut, int left, uint32_t* w) {
+#pragma unroll
+  for (int e = 0; e < 32; e++) v[e] = ex2(fmaf(v[e], scale2, -l2)) * (dp[e] - dl);
+  if (cut)
+#pragma unroll
+    for (int e = 0; e < 32; e++) v[e] = e < left ? v[e] : 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; e++) w[e] = pack(v[2 * e], v[2 * e + 1]);
+}
+// Half of a row of an accumulator, times f, as bf16 (zeros where nothing was accumulated).
+template <int D>
+__device__ __forceinline__ void store_row(bf16* dst, uint32_t tm, int half, bool in, bool any, float f) {
+#pragma unroll
+  for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+    float v[32];
+    if (any) {
+      tm_ld32(tm + c, v);
+      tm_wait_ld(v);
+    }
+    if (in) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        uint32_t u[4];
+#pragma unroll
+        for (int y = 0; y < 4; y++) u[y] = any ? pack(v[e + 2 * y] * f, v[e + 2 * y + 1] * f) : 0u;
+        *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// dk and dv, per CTA: 128 keys of one key head, over the blocks of 128 queries of its group's heads.  The pairs lie
+// transposed, a key a lane: S' = k q^T, P' = 2^(scale2 S' - lse2), dP' = v dO^T, dS' = P' (dP' - delta), and P' and
+// dS' (bf16, over S' and dP' in tensor memory) are the operands of dv += P' dO and dk += dS' q.  Eight warps form
+// them, each half of the queries' columns; the row sums of the queries come through shared memory.  The products are
+// issued as dv, next S', dk, next dP': while two run, the other two's operand is formed.
+template <int D>
+struct Bwd {
+  static constexpr int BYTES = HALF * (D / 64);
+  static constexpr int STAGES = D == 64 ? 4 : 2;     // of two blocks each
+  static constexpr int SMEM = (2 + 2 * STAGES) * BYTES + 1024;
+};
+constexpr int BWD_THREADS = 384;
+
+struct BwdBars {
+  uint64_t own, full[4], empty[4], s, dp, p, ds, done, drain;
+  uint32_t tmem;
+  int dead;
+};
+
+template <int D>
+__global__ void __launch_bounds__(BWD_THREADS, 1)
+smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
+                  bf16* __restrict__ dk, bf16* __restrict__ dv) {
+  using F = Bwd<D>;
+  constexpr uint32_t cS = 0, cDP = BLK, cDV = 2 * BLK, cDK = 2 * BLK + D;
+  extern __shared__ unsigned char raw[];
+  __shared__ BwdBars B;
+  __shared__ __align__(16) float stat[F::STAGES][2][BLK];  // lse2 and delta of a stage's queries
+  unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
+  unsigned char* ring = sm + 2 * F::BYTES;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (warp == 8) tc::tmem_alloc(&B.tmem, 512);
+  if (threadIdx.x == 0) {
+    mma::mbar_init(&B.own, 1);
+    for (int i = 0; i < F::STAGES; i++) {
+      mma::mbar_init(&B.full[i], 2);  // the copies and the row sums
+      mma::mbar_init(&B.empty[i], 1);
+    }
+    mma::mbar_init(&B.s, 1);
+    mma::mbar_init(&B.dp, 1);
+    mma::mbar_init(&B.p, 8);
+    mma::mbar_init(&B.ds, 8);
+    mma::mbar_init(&B.done, 1);
+    mma::mbar_init(&B.drain, 1);
+    B.dead = 0;
+    mma::mbar_init_fence();
+  }
+  pdl_wait();
+  Tile t;
+  const int hk = blockIdx.x % P.Hkv;
+  const bool live = saved(P) && tile_of(P, 2, blockIdx.x / P.Hkv, true, t);
+  int j0 = 0, nk = 0, first = 0, per = 0;  // first query block, blocks a head
+  if (live) {
+    j0 = t.t * BLK;
+    nk = min(BLK, t.Lk - j0);
+    first = first_query(P.causal, j0, t.Lq, t.Lk) / BLK;
+    per = max(0, (t.Lq + BLK - 1) / BLK - first);
+  }
+  const int n = per * P.G;
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = B.tmem;
+
+  if (warp == 9) {  // copies
+    if (lane == 0 && n > 0) {
+      mma::mbar_expect_tx(&B.own, 2 * F::BYTES);
+      load_block<D>(sm, &mk, hk, t.k0 + j0, &B.own);
+      load_block<D>(sm + F::BYTES, &mv, hk, t.k0 + j0, &B.own);
+    }
+    __syncwarp();
+    int x = 0;
+    for (; x < n; x++) {
+      const int s = x % F::STAGES, r = x / F::STAGES;
+      if (r > 0 && !wait(&B.empty[s], (r - 1) & 1, &B.dead)) break;
+      if (lane == 0) {
+        const int h = hk * P.G + x / per, row = t.q0 + (first + x % per) * BLK;
+        mma::mbar_expect_tx(&B.full[s], 2 * F::BYTES);
+        load_block<D>(ring + 2 * s * F::BYTES, &mq, h, row, &B.full[s]);
+        load_block<D>(ring + (2 * s + 1) * F::BYTES, &mg, h, row, &B.full[s]);
+      }
+      __syncwarp();
+    }
+    // (a wait gives up after a second: by then every copy under way has landed)
+  } else if (warp == 10) {  // row sums
+    for (int x = 0; x < n; x++) {
+      const int s = x % F::STAGES, r = x / F::STAGES;
+      if (r > 0 && !wait(&B.empty[s], (r - 1) & 1, &B.dead)) break;
+      const int h = hk * P.G + x / per, i0 = (first + x % per) * BLK;
+      const size_t at = (size_t)h * P.Nq + t.q0 + i0;
+#pragma unroll
+      for (int c = lane; c < BLK; c += 32) {
+        const bool in = i0 + c < t.Lq;
+        stat[s][0][c] = in ? P.lse2[at + c] : 0.f;
+        stat[s][1][c] = in ? P.delta[at + c] : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mma::mbar_arrive(&B.full[s]);
+    }
+  } else if (warp == 8) {  // products
+    const uint32_t k0 = mma::smem_u32(sm), v0 = k0 + F::BYTES, r0 = mma::smem_u32(ring);
+    constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
+    auto pairs = [&](uint32_t d, uint32_t a, uint32_t b, uint64_t* bar) {
+#pragma unroll
+      for (int s = 0; s < D / 16; s++) mma_ss(tm + d, desc_k(a, s), desc_k(b, s), id_s, s > 0);
+      tc::commit(bar);
+    };
+    auto apply = [&](uint32_t d, uint32_t a, uint32_t b, bool acc) {  // (each half's 64 columns are 32 of bf16 pairs)
+#pragma unroll
+      for (int s = 0; s < BLK / 16; s++)
+        mma_ts(tm + d, tm + a + 64 * (s >> 2) + 8 * (s & 3), desc_mn(b, s), id_o, acc || s > 0);
+    };
+    auto ready = [&](int x) -> bool {  // block x of queries has landed; rows behind its document's last are zeros
+      const int s = x % F::STAGES, left = t.Lq - (first + x % per) * BLK;
+      if (!wait(&B.full[s], (x / F::STAGES) & 1, &B.dead)) return false;
+      if (left < BLK) {
+        zero_rows<D>(ring + 2 * s * F::BYTES, left);
+        zero_rows<D>(ring + (2 * s + 1) * F::BYTES, left);
+      }
+      return true;
+    };
+    auto run = [&]() -> bool {
+      if (!wait(&B.own, 0, &B.dead) || !ready(0)) return false;
+      if (lane == 0) {
+        pairs(cS, k0, r0, &B.s);
+        pairs(cDP, v0, r0 + F::BYTES, &B.dp);
+      }
+      __syncwarp();
+      for (int x = 0; x < n; x++) {
+        const uint32_t qb = r0 + x % F::STAGES * 2 * F::BYTES, qn = r0 + (x + 1) % F::STAGES * 2 * F::BYTES;
+        const bool more = x + 1 < n;
+        if (!wait(&B.p, x & 1, &B.dead)) return false;
+        tc::fence_after();
+        if (lane == 0) apply(cDV, cS, qb + F::BYTES, x > 0);
+        __syncwarp();
+        if (more) {
+          if (!ready(x + 1)) return false;
+          if (lane == 0) pairs(cS, k0, qn, &B.s);
+          __syncwarp();
+        }
+        if (!wait(&B.ds, x & 1, &B.dead)) return false;
+        tc::fence_after();
+        if (lane == 0) {
+          apply(cDK, cDP, qb, x > 0);
+          tc::commit(&B.empty[x % F::STAGES]);
+          if (more) pairs(cDP, v0, qn + F::BYTES, &B.dp);
+          else tc::commit(&B.done);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+    if (n > 0 && !run()) {
+      if (lane == 0) tc::commit(&B.drain);
+      __syncwarp();
+      for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
+    }
+  } else if (warp < 8 && live) {  // weights and their gradients: a thread a key, 64 of a block's queries
+    const int half = warp / 4, r = threadIdx.x & 127;
+    const bool in = r < nk;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tm + cS + 64 * half + lanes, td = tm + cDP + 64 * half + lanes;
+    const int fq = first_query(P.causal, j0 + r, t.Lq, t.Lk), fq_last = first_query(P.causal, j0 + nk - 1, t.Lq, t.Lk);
+    bool ok = true;
+    for (int x = 0; x < n; x++) {
+      const int s = x % F::STAGES, i0 = (first + x % per) * BLK;
+      const float *l2 = stat[s][0] + 64 * half, *dl = stat[s][1] + 64 * half;
+      const bool cut = i0 < fq_last || i0 + BLK > t.Lq;
+      const int lo = fq - i0 - 64 * half, hi = t.Lq - i0 - 64 * half;
+      float a[32], b[32];
+      uint32_t w[32];
+      ok = wait(&B.full[s], (x / F::STAGES) & 1, &B.dead) && wait(&B.s, x & 1, &B.dead);
+      if (!ok) break;
+      tc::fence_after();
+      tm_ld32(ts, a);
+      tm_ld32(ts + 32, b);
+      tm_wait_ld(a);
+      tm_wait_ld(b);
+      bwd_weights(a, l2, P.scale2, cut, lo, hi);
+      bwd_weights(b, l2 + 32, P.scale2, cut, lo - 32, hi - 32);
+#pragma unroll
+      for (int e = 0; e < 16; e++) {
+        w[e] = pack(a[2 * e], a[2 * e + 1]);
+        w[16 + e] = pack(b[2 * e], b[2 * e + 1]);
+      }
+      tm_st32(ts, w);  // (over logits of its own: the other half's warp may still read its)
+      tm_wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mma::mbar_arrive(&B.p);
+      ok = wait(&B.dp, x & 1, &B.dead);
+      if (!ok) break;
+      tc::fence_after();
+      float c[32];
+      tm_ld32(td, c);
+      tm_wait_ld(c);
+      bwd_grads(a, c, dl, cut, lo, hi, w);
+      tm_ld32(td + 32, c);
+      tm_wait_ld(c);
+      bwd_grads(b, c, dl + 32, cut, lo - 32, hi - 32, w + 16);
+      tm_st32(td, w);
+      tm_wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mma::mbar_arrive(&B.ds);
+    }
+    if (ok && n > 0) {
+      ok = wait(&B.done, 0, &B.dead);
+      tc::fence_after();
+    }
+    if (ok) {
+      const size_t row = ((size_t)(t.k0 + j0 + r) * P.Hkv + hk) * D;
+      store_row<D>(dv + row, tm + cDV + lanes, half, in, n > 0, 1.0f);
+      store_row<D>(dk + row, tm + cDK + lanes, half, in, n > 0, P.scale);
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && B.dead) *P.err = KDA_ERR_DEVICE;
+  if (warp == 8) {
+    tc::fence_after();
+    tc::tmem_dealloc(tm, 512);
+  }
+}
+
+// dq, per CTA: 128 queries of one head over the blocks of keys: S = q k^T, dP = dO v^T, dS = P (dP - delta), dq += dS k.
+// S and dP are taken to registers at once, so that the next block's products run while dS is formed; dS has two places
+// of its own.
+struct DqBars {
+  uint64_t own, full[4], empty[4], s, taken, ds, used[2], drain;
+  uint32_t tmem;
+  int dead;
+};
+
+template <int D>
+__global__ void __launch_bounds__(BWD_THREADS, 1)
+smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
+                 bf16* __restrict__ dq) {
+  using F = Bwd<D>;
+  constexpr uint32_t cS = 0, cDP = BLK, cDQ = 2 * BLK, cDS = 2 * BLK + D;
+  extern __shared__ unsigned char raw[];
+  __shared__ DqBars B;
+  unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
+  unsigned char* ring = sm + 2 * F::BYTES;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (warp == 8) tc::tmem_alloc(&B.tmem, 512);
+  if (threadIdx.x == 0) {
+    mma::mbar_init(&B.own, 1);
+    for (int i = 0; i < F::STAGES; i++) {
+      mma::mbar_init(&B.full[i], 1);
+      mma::mbar_init(&B.empty[i], 1);
+    }
+    mma::mbar_init(&B.s, 1);
+    mma::mbar_init(&B.taken, 8);
+    mma::mbar_init(&B.ds, 8);
+    mma::mbar_init(&B.used[0], 1);
+    mma::mbar_init(&B.used[1], 1);
+    mma::mbar_init(&B.drain, 1);
+    B.dead = 0;
+    mma::mbar_init_fence();
+  }
+  pdl_wait();
+  Tile t;
+  const int h = blockIdx.x % P.Hq, hk = h / P.G;
+  const bool live = saved(P) && tile_of(P, 1, blockIdx.x / P.Hq, false, t);
+  int i0 = 0, nq = 0, n = 0, clean = 0;
+  if (live) {
+    i0 = t.t * BLK;
+    nq = min(BLK, t.Lq - i0);
+    n = (keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk) + BLK - 1) / BLK;
+    clean = keys_of(P.causal, i0, t.Lq, t.Lk) / BLK;
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = B.tmem;
+
+  if (warp == 9) {  // copies
+    if (lane == 0 && n > 0) {
+      mma::mbar_expect_tx(&B.own, 2 * F::BYTES);
+      load_block<D>(sm, &mq, h, t.q0 + i0, &B.own);
+      load_block<D>(sm + F::BYTES, &mg, h, t.q0 + i0, &B.own);
+    }
+    __syncwarp();
+    for (int x = 0; x < n; x++) {
+      const int s = x % F::STAGES, r = x / F::STAGES;
+      if (r > 0 && !wait(&B.empty[s], (r - 1) & 1, &B.dead)) break;
+      if (lane == 0) {
+        mma::mbar_expect_tx(&B.full[s], 2 * F::BYTES);
+        load_block<D>(ring + 2 * s * F::BYTES, &mk, hk, t.k0 + x * BLK, &B.full[s]);
+        load_block<D>(ring + (2 * s + 1) * F::BYTES, &mv, hk, t.k0 + x * BLK, &B.full[s]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 8) {  // products
+    const uint32_t q0 = mma::smem_u32(sm), g0 = q0 + F::BYTES, r0 = mma::smem_u32(ring);
+    constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
+    auto pairs = [&](int x) {
+      const uint32_t kb = r0 + x % F::STAGES * 2 * F::BYTES;
+#pragma unroll
+      for (int s = 0; s < D / 16; s++) mma_ss(tm + cS, desc_k(q0, s), desc_k(kb, s), id_s, s > 0);
+#pragma unroll
+      for (int s = 0; s < D / 16; s++) mma_ss(tm + cDP, desc_k(g0, s), desc_k(kb + F::BYTES, s), id_s, s > 0);
+      tc::commit(&B.s);
+    };
+    auto ready = [&](int x) -> bool {
+      const int s = x % F::STAGES, left = t.Lk - x * BLK;
+      if (!wait(&B.full[s], (x / F::STAGES) & 1, &B.dead)) return false;
+      if (left < BLK) zero_rows<D>(ring + 2 * s * F::BYTES, left);
+      return true;
+    };
+    auto run = [&]() -> bool {
+      if (!wait(&B.own, 0, &B.dead) || !ready(0)) return false;
+      if (lane == 0) pairs(0);
+      __syncwarp();
+      for (int x = 0; x < n; x++) {
+        if (x + 1 < n) {
+          if (!ready(x + 1) || !wait(&B.taken, x & 1, &B.dead)) return false;
+          tc::fence_after();
+          if (lane == 0) pairs(x + 1);
+          __syncwarp();
+        }
+        if (!wait(&B.ds, x & 1, &B.dead)) return false;
+        tc::fence_after();
+        if (lane == 0) {
+          const uint32_t kb = r0 + x % F::STAGES * 2 * F::BYTES;
+#pragma unroll
+          for (int s = 0; s < BLK / 16; s++)
+            mma_ts(tm + cDQ, tm + cDS + 64 * (x & 1) + 8 * s, desc_mn(kb, s), id_o, x > 0 || s > 0);
+          tc::commit(&B.used[x & 1]);
+          tc::commit(&B.empty[x % F::STAGES]);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+    if (n > 0 && !run()) {
+      if (lane == 0) tc::commit(&B.drain);
+      __syncwarp();
+      for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
+    }
+  } else if (warp < 8 && live) {  // a thread a query, 64 of a block's keys
+    const int half = warp / 4, r = threadIdx.x & 127;
+    const bool in = r < nq;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tm + cS + 64 * half + lanes, td = tm + cDP + 64 * half + lanes;
+    const int lim = in ? keys_of(P.causal, i0 + r, t.Lq, t.Lk) : 0;
+    const size_t at = (size_t)h * P.Nq + t.q0 + i0 + r;
+    const float l2 = in ? P.lse2[at] : 0.f, dl = in ? P.delta[at] : 0.f;
+    bool ok = true;
+    for (int x = 0; x < n; x++) {
+      ok = wait(&B.s, x & 1, &B.dead);
+      if (!ok) break;
+      tc::fence_after();
+      float a[32], b[32], c[32], d[32];
+      tm_ld32(ts, a);
+      tm_ld32(td, c);
+      tm_ld32(ts + 32, b);
+      tm_ld32(td + 32, d);
+      tm_wait_ld(a);
+      tm_wait_ld(b);
+      tm_wait_ld(c);
+      tm_wait_ld(d);
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mma::mbar_arrive(&B.taken);
+      const int left = lim - x * BLK - 64 * half;
+      const bool cut = x >= clean;
+      uint32_t w[32];
+      dq_grads(a, c, l2, dl, P.scale2, cut, left, w);
+      dq_grads(b, d, l2, dl, P.scale2, cut, left - 32, w + 16);
+      if (x >= 2) {
+        ok = wait(&B.used[x & 1], (x / 2 - 1) & 1, &B.dead);
+        if (!ok) break;
+        tc::fence_after();
+      }
+      tm_st32(tm + cDS + 64 * (x & 1) + 32 * half + lanes, w);
+      tm_wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mma::mbar_arrive(&B.ds);
+    }
+    if (ok && n > 0) {
+      ok = wait(&B.used[(n - 1) & 1], ((n - 1) / 2) & 1, &B.dead);
+      tc::fence_after();
+    }
+    if (ok)
+      store_row<D>(dq + ((size_t)(t.q0 + i0 + r) * P.Hq + h) * D, tm + cDQ + lanes, half, in, n > 0, P.scale);
+    tc::fence_before();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && B.dead) *P.err = KDA_ERR_DEVICE;
+  if (warp == 8) {
+    tc::fence_after();
+    tc::tmem_dealloc(tm, 512);
+  }
+}
+
+template <int D>
+cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, const void* dO, void* dq, void* dk,
+                void* dv, cudaStream_t st) {
+  CUtensorMap mq, mk, mv, mg;
+  if (!encode_head_rows(&mq, q, P.Nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, P.Nk, P.Hkv, D, BLK) ||
+      !encode_head_rows(&mv, v, P.Nk, P.Hkv, D, BLK) || !encode_head_rows(&mg, dO, P.Nq, P.Hq, D, BLK))
+    return cudaErrorInvalidValue;
+  const int64_t gk = (int64_t)max_tiles(P, 2) * P.Hkv, gq = (int64_t)max_tiles(P, 1) * P.Hq;
+  if (gk > 2147483647 || gq > 2147483647) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(smx_tc_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Bwd<D>::SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(smx_tc_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Bwd<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  prof_begin(K_SMX_DKV, st);
+  e = launch_pdl(smx_tc_dkv_kernel<D>, dim3((unsigned)gk), dim3(BWD_THREADS), Bwd<D>::SMEM, st, P, mq, mk, mv, mg,
+                 (bf16*)dk, (bf16*)dv);
+  prof_end(K_SMX_DKV, st);
+  if (e != cudaSuccess) return e;
+  prof_begin(K_SMX_DQ, st);
+  e = launch_pdl(smx_tc_dq_kernel<D>, dim3((unsigned)gq), dim3(BWD_THREADS), Bwd<D>::SMEM, st, P, mq, mk, mv, mg,
+                 (bf16*)dq);
+  prof_end(K_SMX_DQ, st);
+  return e;
+}
+
 }  // namespace
 
 cudaError_t launch_tc_fwd(const SmxP& P, int D, const void* q, const void* k, const void* v, void* o, float* lse,
                           cudaStream_t st) {
   return D == 64 ? fwd<64>(P, q, k, v, o, lse, st) : fwd<128>(P, q, k, v, o, lse, st);
+}
+cudaError_t launch_tc_bwd(const SmxP& P, int D, const void* q, const void* k, const void* v, const void* dO, void* dq,
+                          void* dk, void* dv, cudaStream_t st) {
+  return D == 64 ? bwd<64>(P, q, k, v, dO, dq, dk, dv, st) : bwd<128>(P, q, k, v, dO, dq, dk, dv, st);
 }
 
 }  // namespace smx
