@@ -26,9 +26,12 @@ constexpr float GROW = 8.0f;   // log2 of what a weight may exceed 1 by
 // Descriptors of a block of 128 rows in 128-byte swizzled halves of 64 columns (TMA's layout): 8-row groups 1024 bytes apart.
 // K-major (rows are M or N): 16 columns of the contraction are 32 bytes of the swizzled row.  MN-major (rows are the
 // contraction): 16 rows are 2048 bytes, and the next 64 columns are a half away.
+//
+// A warp issues products as a whole, one elected lane's predicate on the instruction: descriptors and addresses then
+// stay in uniform registers.  Issued inside a branch of one lane, from registers of that lane, a product took 70 to 180
+// cycles to issue, and 64 (128 x 128 x 16) to run.
 __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+  return (uint64_t)((addr >> 4) | (lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61);
 }
 __device__ __forceinline__ uint64_t desc_k(uint32_t block, int step) {  // columns 16 step ..
   return sdesc(block + (step >> 2) * HALF + (step & 3) * 32, 16);
@@ -39,13 +42,31 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t block, int step) {  // rows
 constexpr uint32_t idesc(int M, int N, bool b_mn) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)b_mn << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
-  tc::mma_issue(d, a, b, id, acc);
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {  // A in tensor memory
+// (whole warp; me: the elected lane)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc, uint32_t me) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc), "r"(me)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc, uint32_t me) {  // A in tensor memory
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc), "r"(me)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t me) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(mma::smem_u32(bar)),
+      "r"(me)
       : "memory");
 }
 
@@ -239,7 +260,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tm = B.tmem;
+  constexpr uint32_t tm = 0;  // (all 512 columns of the tensor memory: its first address)
 
   if (warp == 9) {  // loads
     if (lane == 0 && n > 0) {
@@ -270,50 +291,51 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   } else if (warp == 8) {  // products
     const uint32_t q0 = mma::smem_u32(sm), r0 = mma::smem_u32(ring);
     constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
+    const uint32_t me = elect();
     auto logits = [&](int i, int x) {
-      const uint32_t kb = r0 + x % F::STAGES * F::BYTES, qb = q0 + i * F::BYTES, d = tm + F::S0 + i * BLK;
+      const uint32_t kb = r0 + x % F::STAGES * F::BYTES, qb = q0 + i * F::BYTES, d = F::S0 + i * BLK;
 #pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(d, desc_k(qb, s), desc_k(kb, s), id_s, s > 0);
-      tc::commit(&B.s[i]);
+      for (int s = 0; s < D / 16; s++) mma_ss(d, desc_k(qb, s), desc_k(kb, s), id_s, s > 0, me);
+      commit(&B.s[i], me);
     };
     auto run = [&]() -> bool {
       if (!wait(&B.full[0], 0, &B.dead)) return false;
+#pragma unroll
       for (int i = 0; i < 2; i++)
         if (nb[i]) {
           if (!wait(&B.q[i], 0, &B.dead)) return false;
-          if (lane == 0) logits(i, 0);
+          logits(i, 0);
         }
-      if (lane == 0) tc::commit(&B.empty[0]);
-      __syncwarp();
+      commit(&B.empty[0], me);
       for (int j = 0; j < n; j++) {
         const int xv = 2 * j + 1, xk = 2 * j + 2, sv = xv % F::STAGES, sk = xk % F::STAGES;
         if (!wait(&B.full[sv], (xv / F::STAGES) & 1, &B.dead)) return false;
         if (t.Lk - j * BLK < BLK) zero_rows<D>(ring + sv * F::BYTES, t.Lk - j * BLK);
         if (j + 1 < n && !wait(&B.full[sk], (xk / F::STAGES) & 1, &B.dead)) return false;
+        const uint32_t vb = r0 + sv * F::BYTES;
+#pragma unroll
         for (int i = 0; i < 2; i++) {
           if (j >= nb[i]) continue;
           if (!wait(&B.p[i], j & 1, &B.dead)) return false;
           tc::fence_after();
-          if (lane == 0) {
-            const uint32_t a = tm + F::S0 + i * BLK, d = tm + F::O0 + i * D, vb = r0 + sv * F::BYTES;
+          const uint32_t a = F::S0 + i * BLK, d = F::O0 + i * D;
 #pragma unroll
-            for (int s = 0; s < BLK / 16; s++) mma_ts(d, a + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, j > 0 || s > 0);
-            if (j >= clean[i])
+          for (int s = 0; s < BLK / 16; s++)
+            mma_ts(d, a + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, j > 0 || s > 0, me);
+          if (j >= clean[i])
 #pragma unroll
-              for (int s = 0; s < BLK / 16; s++) mma_ts(d, a + 16 + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, true);
-            tc::commit(&B.o[i]);
-            if (i == 1 || j >= nb[1]) tc::commit(&B.empty[sv]);
-            if (j + 1 < nb[i]) logits(i, xk);
-            if (j + 1 < n && (i == 1 || j + 1 >= nb[1])) tc::commit(&B.empty[sk]);
-          }
-          __syncwarp();
+            for (int s = 0; s < BLK / 16; s++)
+              mma_ts(d, a + 16 + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, true, me);
+          commit(&B.o[i], me);
+          if (i == 1 || j >= nb[1]) commit(&B.empty[sv], me);
+          if (j + 1 < nb[i]) logits(i, xk);
+          if (j + 1 < n && (i == 1 || j + 1 >= nb[1])) commit(&B.empty[sk], me);
         }
       }
       return true;
     };
     if (n > 0 && !run()) {  // (its products end before the tensor memory is released)
-      if (lane == 0) tc::commit(&B.drain);
-      __syncwarp();
+      commit(&B.drain, me);
       for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
     }
   } else if (warp < 8 && live) {  // weights: a thread a row
@@ -580,7 +602,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tm = B.tmem;
+  constexpr uint32_t tm = 0;  // (all 512 columns of the tensor memory: its first address)
 
   if (warp == 9) {  // copies
     if (lane == 0 && n > 0) {
@@ -620,15 +642,16 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   } else if (warp == 8) {  // products
     const uint32_t k0 = mma::smem_u32(sm), v0 = k0 + F::BYTES, r0 = mma::smem_u32(ring);
     constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
+    const uint32_t me = elect();
     auto pairs = [&](uint32_t d, uint32_t a, uint32_t b, uint64_t* bar) {
 #pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(tm + d, desc_k(a, s), desc_k(b, s), id_s, s > 0);
-      tc::commit(bar);
+      for (int s = 0; s < D / 16; s++) mma_ss(d, desc_k(a, s), desc_k(b, s), id_s, s > 0, me);
+      commit(bar, me);
     };
     auto apply = [&](uint32_t d, uint32_t a, uint32_t b, bool acc) {  // (each half's 64 columns are 32 of bf16 pairs)
 #pragma unroll
       for (int s = 0; s < BLK / 16; s++)
-        mma_ts(tm + d, tm + a + 64 * (s >> 2) + 8 * (s & 3), desc_mn(b, s), id_o, acc || s > 0);
+        mma_ts(d, a + 64 * (s >> 2) + 8 * (s & 3), desc_mn(b, s), id_o, acc || s > 0, me);
     };
     auto ready = [&](int x) -> bool {  // block x of queries has landed; rows behind its document's last are zeros
       const int s = x % F::STAGES, left = t.Lq - (first + x % per) * BLK;
@@ -641,38 +664,29 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     };
     auto run = [&]() -> bool {
       if (!wait(&B.own, 0, &B.dead) || !ready(0)) return false;
-      if (lane == 0) {
-        pairs(cS, k0, r0, &B.s);
-        pairs(cDP, v0, r0 + F::BYTES, &B.dp);
-      }
-      __syncwarp();
+      pairs(cS, k0, r0, &B.s);
+      pairs(cDP, v0, r0 + F::BYTES, &B.dp);
       for (int x = 0; x < n; x++) {
         const uint32_t qb = r0 + x % F::STAGES * 2 * F::BYTES, qn = r0 + (x + 1) % F::STAGES * 2 * F::BYTES;
         const bool more = x + 1 < n;
         if (!wait(&B.p, x & 1, &B.dead)) return false;
         tc::fence_after();
-        if (lane == 0) apply(cDV, cS, qb + F::BYTES, x > 0);
-        __syncwarp();
+        apply(cDV, cS, qb + F::BYTES, x > 0);
         if (more) {
           if (!ready(x + 1)) return false;
-          if (lane == 0) pairs(cS, k0, qn, &B.s);
-          __syncwarp();
+          pairs(cS, k0, qn, &B.s);
         }
         if (!wait(&B.ds, x & 1, &B.dead)) return false;
         tc::fence_after();
-        if (lane == 0) {
-          apply(cDK, cDP, qb, x > 0);
-          tc::commit(&B.empty[x % F::STAGES]);
-          if (more) pairs(cDP, v0, qn + F::BYTES, &B.dp);
-          else tc::commit(&B.done);
-        }
-        __syncwarp();
+        apply(cDK, cDP, qb, x > 0);
+        commit(&B.empty[x % F::STAGES], me);
+        if (more) pairs(cDP, v0, qn + F::BYTES, &B.dp);
+        else commit(&B.done, me);
       }
       return true;
     };
     if (n > 0 && !run()) {
-      if (lane == 0) tc::commit(&B.drain);
-      __syncwarp();
+      commit(&B.drain, me);
       for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
     }
   } else if (warp < 8 && live) {  // weights and their gradients: a thread a key, 64 of a block's queries
@@ -794,7 +808,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tm = B.tmem;
+  constexpr uint32_t tm = 0;  // (all 512 columns of the tensor memory: its first address)
 
   if (warp == 9) {  // copies
     if (lane == 0 && n > 0) {
@@ -816,13 +830,14 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   } else if (warp == 8) {  // products
     const uint32_t q0 = mma::smem_u32(sm), g0 = q0 + F::BYTES, r0 = mma::smem_u32(ring);
     constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
+    const uint32_t me = elect();
     auto pairs = [&](int x) {
       const uint32_t kb = r0 + x % F::STAGES * 2 * F::BYTES;
 #pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(tm + cS, desc_k(q0, s), desc_k(kb, s), id_s, s > 0);
+      for (int s = 0; s < D / 16; s++) mma_ss(cS, desc_k(q0, s), desc_k(kb, s), id_s, s > 0, me);
 #pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(tm + cDP, desc_k(g0, s), desc_k(kb + F::BYTES, s), id_s, s > 0);
-      tc::commit(&B.s);
+      for (int s = 0; s < D / 16; s++) mma_ss(cDP, desc_k(g0, s), desc_k(kb + F::BYTES, s), id_s, s > 0, me);
+      commit(&B.s, me);
     };
     auto ready = [&](int x) -> bool {
       const int s = x % F::STAGES, left = t.Lk - x * BLK;
@@ -832,32 +847,26 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
     };
     auto run = [&]() -> bool {
       if (!wait(&B.own, 0, &B.dead) || !ready(0)) return false;
-      if (lane == 0) pairs(0);
-      __syncwarp();
+      pairs(0);
       for (int x = 0; x < n; x++) {
         if (x + 1 < n) {
           if (!ready(x + 1) || !wait(&B.taken, x & 1, &B.dead)) return false;
           tc::fence_after();
-          if (lane == 0) pairs(x + 1);
-          __syncwarp();
+          pairs(x + 1);
         }
         if (!wait(&B.ds, x & 1, &B.dead)) return false;
         tc::fence_after();
-        if (lane == 0) {
-          const uint32_t kb = r0 + x % F::STAGES * 2 * F::BYTES;
+        const uint32_t kb = r0 + x % F::STAGES * 2 * F::BYTES;
 #pragma unroll
-          for (int s = 0; s < BLK / 16; s++)
-            mma_ts(tm + cDQ, tm + cDS + 64 * (x & 1) + 8 * s, desc_mn(kb, s), id_o, x > 0 || s > 0);
-          tc::commit(&B.used[x & 1]);
-          tc::commit(&B.empty[x % F::STAGES]);
-        }
-        __syncwarp();
+        for (int s = 0; s < BLK / 16; s++)
+          mma_ts(cDQ, cDS + 64 * (x & 1) + 8 * s, desc_mn(kb, s), id_o, x > 0 || s > 0, me);
+        commit(&B.used[x & 1], me);
+        commit(&B.empty[x % F::STAGES], me);
       }
       return true;
     };
     if (n > 0 && !run()) {
-      if (lane == 0) tc::commit(&B.drain);
-      __syncwarp();
+      commit(&B.drain, me);
       for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
     }
   } else if (warp < 8 && live) {  // a thread a query, 64 of a block's keys
