@@ -153,22 +153,48 @@ __device__ __forceinline__ void mask(float (&v)[32], int left) {
 #pragma unroll
   for (int e = 0; e < 32; e++) v[e] = e < left ? v[e] : -INFINITY;
 }
-__device__ __forceinline__ void row_max(float (&v)[32], bool cut, int left, float (&mx)[4]) {
-  if (cut) mask(v, left);
+__device__ __forceinline__ void row_max(const float (&v)[32], float (&mx)[4]) {
 #pragma unroll
-  for (int e = 0; e < 32; e++) mx[e & 3] = fmaxf(mx[e & 3], v[e]);
+  for (int e = 0; e < 32; e += 8)
+#pragma unroll
+    for (int y = 0; y < 4; y++)
+      asm("max.f32 %0, %1, %2, %3;" : "=f"(mx[y]) : "f"(mx[y]), "f"(v[e + 2 * y]), "f"(v[e + 2 * y + 1]));
 }
-// 32 logits into weights, their sum, and as bf16 to tensor memory (second parts 16 columns further, where a mask cuts).
-__device__ __forceinline__ void weights(float (&v)[32], uint32_t to, float scale2, float neg, bool cut,
-                                        float (&sum)[4]) {
+// Pairs of floats in one register pair, for the two-wide fp32 instructions.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void one(uint64_t r, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 32 logits into weights 2^(sc v + ng), their sum, and as bf16 to tensor memory (second parts 16 columns further, where
+// a mask cuts).
+__device__ __forceinline__ void weights(float (&v)[32], uint32_t to, uint64_t sc, uint64_t ng, bool cut,
+                                        uint64_t (&sum)[2]) {
   uint32_t w[16];
 #pragma unroll
-  for (int e = 0; e < 32; e++) {
-    v[e] = ex2(fmaf(v[e], scale2, neg));
-    sum[e & 3] += v[e];
+  for (int e = 0; e < 32; e += 2) {
+    one(fma2(two(v[e], v[e + 1]), sc, ng), v[e], v[e + 1]);
+    v[e] = ex2(v[e]);
+    v[e + 1] = ex2(v[e + 1]);
+    sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], two(v[e], v[e + 1]));
+    w[e / 2] = pack(v[e], v[e + 1]);
   }
-#pragma unroll
-  for (int e = 0; e < 16; e++) w[e] = pack(v[2 * e], v[2 * e + 1]);
   tm_st16(to, w);
   if (cut) {
 #pragma unroll
@@ -350,23 +376,18 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       ok = wait(&B.s[i], j & 1, &B.dead);
       if (!ok) break;
       tc::fence_after();
-      // The row in four pieces of 32 columns: all of them for the maximum, then again for the weights (two are still
-      // in registers).  A piece's weights replace it: 16 columns, and 16 for their second parts.
       const bool cut = j >= cleani;
       const int left = lim - j * BLK;
-      float a[32], b[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      tm_ld32(ts, a);
-      tm_wait_ld(a);
-      tm_ld32(ts + 32, b);
-      row_max(a, cut, left, mx);
-      tm_wait_ld(b);
-      tm_ld32(ts + 64, a);
-      row_max(b, cut, left - 32, mx);
-      tm_wait_ld(a);
-      tm_ld32(ts + 96, b);
-      row_max(a, cut, left - 64, mx);
-      tm_wait_ld(b);
-      row_max(b, cut, left - 96, mx);
+      float s[4][32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 4; c++) tm_ld32(ts + 32 * c, s[c]);
+#pragma unroll
+      for (int c = 0; c < 4; c++) tm_wait_ld(s[c]);
+      if (cut)
+#pragma unroll
+        for (int c = 0; c < 4; c++) mask(s[c], left - 32 * c);
+#pragma unroll
+      for (int c = 0; c < 4; c++) row_max(s[c], mx);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       const bool raise = top > m && !((top - m) * P.scale2 <= GROW);
       if (__any_sync(0xffffffffu, raise)) {
@@ -389,18 +410,13 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
         }
       }
       const float neg = m == -INFINITY ? 0.f : -m * P.scale2;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      weights(a, ts + 64, P.scale2, neg, cut, sum);
-      tm_ld32(ts, a);
-      weights(b, ts + 96, P.scale2, neg, cut, sum);
-      tm_wait_ld(a);
-      tm_ld32(ts + 32, b);
-      if (cut) mask(a, left);
-      weights(a, ts, P.scale2, neg, cut, sum);
-      tm_wait_ld(b);
-      if (cut) mask(b, left - 32);
-      weights(b, ts + 32, P.scale2, neg, cut, sum);
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const uint64_t sc = two(P.scale2, P.scale2), ng = two(neg, neg);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int c = 0; c < 4; c++) weights(s[c], ts + 32 * c, sc, ng, cut, sum);
+      float s0, s1;
+      one(add2(sum[0], sum[1]), s0, s1);
+      l += s0 + s1;
       tm_wait_st();
       tc::fence_before();
       __syncwarp();
