@@ -490,30 +490,29 @@ cudaError_t fwd(const SmxP& P, const void* q, const void* k, const void* v, void
 }
 
 // ------------------------------------------------------------ backward
-// The backward's weights of 32 logits of a key: queries lo .. hi - 1 of them see it; l2: the queries' log2 sums.
-__device__ __forceinline__ void bwd_weights(float (&v)[32], const float* l2, float scale2, bool cut, int lo, int hi) {
+// The backward's weights of 32 logits of a key: queries lo .. hi - 1 of them see it; l2: the queries' log2 sums,
+// negated.
+__device__ __forceinline__ void bwd_weights(float (&v)[32], const float* l2, uint64_t sc, bool cut, int lo, int hi) {
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
-    const float4 l = *reinterpret_cast<const float4*>(l2 + e);
-    v[e] = ex2(fmaf(v[e], scale2, -l.x));
-    v[e + 1] = ex2(fmaf(v[e + 1], scale2, -l.y));
-    v[e + 2] = ex2(fmaf(v[e + 2], scale2, -l.z));
-    v[e + 3] = ex2(fmaf(v[e + 3], scale2, -l.w));
+    const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(l2 + e);
+    one(fma2(two(v[e], v[e + 1]), sc, l.x), v[e], v[e + 1]);
+    one(fma2(two(v[e + 2], v[e + 3]), sc, l.y), v[e + 2], v[e + 3]);
+#pragma unroll
+    for (int y = 0; y < 4; y++) v[e + y] = ex2(v[e + y]);
   }
   if (cut)
 #pragma unroll
     for (int e = 0; e < 32; e++) v[e] = e >= lo && e < hi ? v[e] : 0.f;
 }
-// 32 gradients p (dp - delta) as bf16 pairs (an unseen pair's is zero whatever dp holds).
+// 32 gradients p (dp - delta) as bf16 pairs (an unseen pair's is zero whatever dp holds); dl: -delta.
 __device__ __forceinline__ void bwd_grads(const float (&p)[32], float (&dp)[32], const float* dl, bool cut, int lo,
                                           int hi, uint32_t* w) {
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
-    const float4 l = *reinterpret_cast<const float4*>(dl + e);
-    dp[e] = p[e] * (dp[e] - l.x);
-    dp[e + 1] = p[e + 1] * (dp[e + 1] - l.y);
-    dp[e + 2] = p[e + 2] * (dp[e + 2] - l.z);
-    dp[e + 3] = p[e + 3] * (dp[e + 3] - l.w);
+    const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(dl + e);
+    one(mul2(two(p[e], p[e + 1]), add2(two(dp[e], dp[e + 1]), l.x)), dp[e], dp[e + 1]);
+    one(mul2(two(p[e + 2], p[e + 3]), add2(two(dp[e + 2], dp[e + 3]), l.y)), dp[e + 2], dp[e + 3]);
   }
   if (cut)
 #pragma unroll
@@ -521,11 +520,15 @@ __device__ __forceinline__ void bwd_grads(const float (&p)[32], float (&dp)[32],
 #pragma unroll
   for (int e = 0; e < 16; e++) w[e] = pack(dp[2 * e], dp[2 * e + 1]);
 }
-// The same of a query's row: its sums are scalars, its keys end at `left`.
-__device__ __forceinline__ void dq_grads(float (&v)[32], const float (&dp)[32], float l2, float dl, float scale2,
+// The same of a query's row: its (negated) sums are scalars, its keys end at `left`.
+__device__ __forceinline__ void dq_grads(float (&v)[32], const float (&dp)[32], uint64_t sc, uint64_t l2, uint64_t dl,
                                          bool cut, int left, uint32_t* w) {
 #pragma unroll
-  for (int e = 0; e < 32; e++) v[e] = ex2(fmaf(v[e], scale2, -l2)) * (dp[e] - dl);
+  for (int e = 0; e < 32; e += 2) {
+    float a, b;
+    one(fma2(two(v[e], v[e + 1]), sc, l2), a, b);
+    one(mul2(two(ex2(a), ex2(b)), add2(two(dp[e], dp[e + 1]), dl)), v[e], v[e + 1]);
+  }
   if (cut)
 #pragma unroll
     for (int e = 0; e < 32; e++) v[e] = e < left ? v[e] : 0.f;
@@ -560,19 +563,26 @@ __device__ __forceinline__ void store_row(bf16* dst, uint32_t tm, int half, bool
 // dS' (bf16, over S' and dP' in tensor memory) are the operands of dv += P' dO and dk += dS' q.  Eight warps form
 // them, each half of the queries' columns; the row sums of the queries come through shared memory.  The products are
 // issued as dv, next S', dk, next dP': while two run, the other two's operand is formed.
+//
+// Both kernels keep two blocks of their own and two rings: A, of the blocks that a first product and then the last one
+// reads (q for dk and dv, k for dq), and B, of those that are free earlier (dO, v).
 template <int D>
 struct Bwd {
   static constexpr int BYTES = HALF * (D / 64);
-  static constexpr int STAGES = D == 64 ? 4 : 2;     // of two blocks each
-  static constexpr int SMEM = (2 + 2 * STAGES) * BYTES + 1024;
+  static constexpr int NA = D == 64 ? 5 : 3, NB = D == 64 ? 5 : 2;
+  static constexpr int BLOCKS = (2 + NA + NB) * BYTES;
 };
 constexpr int BWD_THREADS = 384;
 
-struct BwdBars {
-  uint64_t own, full[4], empty[4], s, dp, p, ds, done, drain;
+struct BwdRest {  // (shared memory is full at D = 128: behind the blocks, whose swizzle wants 1024-byte alignment)
+  float stat[2][2][BLK];  // minus lse2 and minus delta of two blocks' queries
+  uint64_t own, fullA[5], emptyA[5], fullB[5], emptyB[5], fullS[2], s, dp, p, ds, done, drain;
   uint32_t tmem;
   int dead;
 };
+template <int D>
+constexpr int DKV_SMEM = Bwd<D>::BLOCKS + (int)sizeof(BwdRest);
+static_assert(DKV_SMEM<64> <= 232448 && DKV_SMEM<128> <= 232448, "227 KB of shared memory");
 
 template <int D>
 __global__ void __launch_bounds__(BWD_THREADS, 1)
@@ -581,19 +591,27 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
                   bf16* __restrict__ dk, bf16* __restrict__ dv) {
   using F = Bwd<D>;
   constexpr uint32_t cS = 0, cDP = BLK, cDV = 2 * BLK, cDK = 2 * BLK + D;
-  extern __shared__ unsigned char raw[];
-  __shared__ BwdBars B;
-  __shared__ __align__(16) float stat[F::STAGES][2][BLK];  // lse2 and delta of a stage's queries
-  unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
-  unsigned char* ring = sm + 2 * F::BYTES;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  BwdRest& B = *reinterpret_cast<BwdRest*>(sm + F::BLOCKS);
+  if (mma::smem_u32(sm) & 1023) {  // (dynamic shared memory alone starts on such a boundary)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *P.err = KDA_ERR_DEVICE;
+    return;
+  }
+  unsigned char *ringA = sm + 2 * F::BYTES, *ringB = ringA + F::NA * F::BYTES;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == 8) tc::tmem_alloc(&B.tmem, 512);
   if (threadIdx.x == 0) {
     mma::mbar_init(&B.own, 1);
-    for (int i = 0; i < F::STAGES; i++) {
-      mma::mbar_init(&B.full[i], 2);  // the copies and the row sums
-      mma::mbar_init(&B.empty[i], 1);
+    for (int i = 0; i < F::NA; i++) {
+      mma::mbar_init(&B.fullA[i], 1);
+      mma::mbar_init(&B.emptyA[i], 1);
     }
+    for (int i = 0; i < F::NB; i++) {
+      mma::mbar_init(&B.fullB[i], 1);
+      mma::mbar_init(&B.emptyB[i], 1);
+    }
+    mma::mbar_init(&B.fullS[0], 1);
+    mma::mbar_init(&B.fullS[1], 1);
     mma::mbar_init(&B.s, 1);
     mma::mbar_init(&B.dp, 1);
     mma::mbar_init(&B.p, 8);
@@ -627,36 +645,39 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       load_block<D>(sm + F::BYTES, &mv, hk, t.k0 + j0, &B.own);
     }
     __syncwarp();
-    int x = 0;
-    for (; x < n; x++) {
-      const int s = x % F::STAGES, r = x / F::STAGES;
-      if (r > 0 && !wait(&B.empty[s], (r - 1) & 1, &B.dead)) break;
+    for (int x = 0; x < n; x++) {
+      const int sa = x % F::NA, sb = x % F::NB, h = hk * P.G + x / per, row = t.q0 + (first + x % per) * BLK;
+      if (x >= F::NA && !wait(&B.emptyA[sa], (x / F::NA - 1) & 1, &B.dead)) break;
       if (lane == 0) {
-        const int h = hk * P.G + x / per, row = t.q0 + (first + x % per) * BLK;
-        mma::mbar_expect_tx(&B.full[s], 2 * F::BYTES);
-        load_block<D>(ring + 2 * s * F::BYTES, &mq, h, row, &B.full[s]);
-        load_block<D>(ring + (2 * s + 1) * F::BYTES, &mg, h, row, &B.full[s]);
+        mma::mbar_expect_tx(&B.fullA[sa], F::BYTES);
+        load_block<D>(ringA + sa * F::BYTES, &mq, h, row, &B.fullA[sa]);
+      }
+      __syncwarp();
+      if (x >= F::NB && !wait(&B.emptyB[sb], (x / F::NB - 1) & 1, &B.dead)) break;
+      if (lane == 0) {
+        mma::mbar_expect_tx(&B.fullB[sb], F::BYTES);
+        load_block<D>(ringB + sb * F::BYTES, &mg, h, row, &B.fullB[sb]);
       }
       __syncwarp();
     }
     // (a wait gives up after a second: by then every copy under way has landed)
   } else if (warp == 10) {  // row sums
     for (int x = 0; x < n; x++) {
-      const int s = x % F::STAGES, r = x / F::STAGES;
-      if (r > 0 && !wait(&B.empty[s], (r - 1) & 1, &B.dead)) break;
+      const int s = x & 1;  // (free once block x - 2 has left ring A)
+      if (x >= 2 && !wait(&B.emptyA[(x - 2) % F::NA], ((x - 2) / F::NA) & 1, &B.dead)) break;
       const int h = hk * P.G + x / per, i0 = (first + x % per) * BLK;
       const size_t at = (size_t)h * P.Nq + t.q0 + i0;
 #pragma unroll
       for (int c = lane; c < BLK; c += 32) {
         const bool in = i0 + c < t.Lq;
-        stat[s][0][c] = in ? P.lse2[at + c] : 0.f;
-        stat[s][1][c] = in ? P.delta[at + c] : 0.f;
+        B.stat[s][0][c] = in ? -P.lse2[at + c] : 0.f;
+        B.stat[s][1][c] = in ? -P.delta[at + c] : 0.f;
       }
       __syncwarp();
-      if (lane == 0) mma::mbar_arrive(&B.full[s]);
+      if (lane == 0) mma::mbar_arrive(&B.fullS[s]);
     }
   } else if (warp == 8) {  // products
-    const uint32_t k0 = mma::smem_u32(sm), v0 = k0 + F::BYTES, r0 = mma::smem_u32(ring);
+    const uint32_t k0 = mma::smem_u32(sm), v0 = k0 + F::BYTES, a0 = mma::smem_u32(ringA), b0 = mma::smem_u32(ringB);
     constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
     const uint32_t me = elect();
     auto pairs = [&](uint32_t d, uint32_t a, uint32_t b, uint64_t* bar) {
@@ -669,35 +690,42 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       for (int s = 0; s < BLK / 16; s++)
         mma_ts(d, a + 64 * (s >> 2) + 8 * (s & 3), desc_mn(b, s), id_o, acc || s > 0, me);
     };
-    auto ready = [&](int x) -> bool {  // block x of queries has landed; rows behind its document's last are zeros
-      const int s = x % F::STAGES, left = t.Lq - (first + x % per) * BLK;
-      if (!wait(&B.full[s], (x / F::STAGES) & 1, &B.dead)) return false;
-      if (left < BLK) {
-        zero_rows<D>(ring + 2 * s * F::BYTES, left);
-        zero_rows<D>(ring + (2 * s + 1) * F::BYTES, left);
-      }
+    // block x of queries (of their dO) has landed; rows behind its document's last are zeros
+    auto ready = [&](int x, unsigned char* block, uint64_t* full, int phase) -> bool {
+      const int left = t.Lq - (first + x % per) * BLK;
+      if (!wait(full, phase & 1, &B.dead)) return false;
+      if (left < BLK) zero_rows<D>(block, left);
       return true;
     };
+    auto readyA = [&](int x) { return ready(x, ringA + x % F::NA * F::BYTES, &B.fullA[x % F::NA], x / F::NA); };
+    auto readyB = [&](int x) { return ready(x, ringB + x % F::NB * F::BYTES, &B.fullB[x % F::NB], x / F::NB); };
     auto run = [&]() -> bool {
-      if (!wait(&B.own, 0, &B.dead) || !ready(0)) return false;
-      pairs(cS, k0, r0, &B.s);
-      pairs(cDP, v0, r0 + F::BYTES, &B.dp);
+      if (!wait(&B.own, 0, &B.dead) || !readyA(0)) return false;
+      pairs(cS, k0, a0, &B.s);
+      if (!readyB(0)) return false;
+      pairs(cDP, v0, b0, &B.dp);
       for (int x = 0; x < n; x++) {
-        const uint32_t qb = r0 + x % F::STAGES * 2 * F::BYTES, qn = r0 + (x + 1) % F::STAGES * 2 * F::BYTES;
+        const uint32_t qb = a0 + x % F::NA * F::BYTES, qn = a0 + (x + 1) % F::NA * F::BYTES;
+        const uint32_t gb = b0 + x % F::NB * F::BYTES, gn = b0 + (x + 1) % F::NB * F::BYTES;
         const bool more = x + 1 < n;
         if (!wait(&B.p, x & 1, &B.dead)) return false;
         tc::fence_after();
-        apply(cDV, cS, qb + F::BYTES, x > 0);
+        apply(cDV, cS, gb, x > 0);
+        commit(&B.emptyB[x % F::NB], me);
         if (more) {
-          if (!ready(x + 1)) return false;
+          if (!readyA(x + 1)) return false;
           pairs(cS, k0, qn, &B.s);
         }
         if (!wait(&B.ds, x & 1, &B.dead)) return false;
         tc::fence_after();
         apply(cDK, cDP, qb, x > 0);
-        commit(&B.empty[x % F::STAGES], me);
-        if (more) pairs(cDP, v0, qn + F::BYTES, &B.dp);
-        else commit(&B.done, me);
+        commit(&B.emptyA[x % F::NA], me);
+        if (more) {
+          if (!readyB(x + 1)) return false;
+          pairs(cDP, v0, gn, &B.dp);
+        } else {
+          commit(&B.done, me);
+        }
       }
       return true;
     };
@@ -711,23 +739,24 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tm + cS + 64 * half + lanes, td = tm + cDP + 64 * half + lanes;
     const int fq = first_query(P.causal, j0 + r, t.Lq, t.Lk), fq_last = first_query(P.causal, j0 + nk - 1, t.Lq, t.Lk);
+    const uint64_t sc = two(P.scale2, P.scale2);
     bool ok = true;
     for (int x = 0; x < n; x++) {
-      const int s = x % F::STAGES, i0 = (first + x % per) * BLK;
-      const float *l2 = stat[s][0] + 64 * half, *dl = stat[s][1] + 64 * half;
+      const int s = x & 1, i0 = (first + x % per) * BLK;
+      const float *l2 = B.stat[s][0] + 64 * half, *dl = B.stat[s][1] + 64 * half;
       const bool cut = i0 < fq_last || i0 + BLK > t.Lq;
       const int lo = fq - i0 - 64 * half, hi = t.Lq - i0 - 64 * half;
       float a[32], b[32];
       uint32_t w[32];
-      ok = wait(&B.full[s], (x / F::STAGES) & 1, &B.dead) && wait(&B.s, x & 1, &B.dead);
+      ok = wait(&B.fullS[s], (x >> 1) & 1, &B.dead) && wait(&B.s, x & 1, &B.dead);
       if (!ok) break;
       tc::fence_after();
       tm_ld32(ts, a);
       tm_ld32(ts + 32, b);
       tm_wait_ld(a);
       tm_wait_ld(b);
-      bwd_weights(a, l2, P.scale2, cut, lo, hi);
-      bwd_weights(b, l2 + 32, P.scale2, cut, lo - 32, hi - 32);
+      bwd_weights(a, l2, sc, cut, lo, hi);
+      bwd_weights(b, l2 + 32, sc, cut, lo - 32, hi - 32);
 #pragma unroll
       for (int e = 0; e < 16; e++) {
         w[e] = pack(a[2 * e], a[2 * e + 1]);
@@ -776,8 +805,10 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
 // dq, per CTA: 128 queries of one head over the blocks of keys: S = q k^T, dP = dO v^T, dS = P (dP - delta), dq += dS k.
 // S and dP are taken to registers at once, so that the next block's products run while dS is formed; dS has two places
 // of its own.
+template <int D>
+constexpr int DQ_SMEM = Bwd<D>::BLOCKS + 1024;  // (blocks on 1024-byte boundaries)
 struct DqBars {
-  uint64_t own, full[4], empty[4], s, taken, ds, used[2], drain;
+  uint64_t own, fullA[5], emptyA[5], fullB[5], emptyB[5], s, taken, ds, used[2], drain;
   uint32_t tmem;
   int dead;
 };
@@ -792,14 +823,18 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   extern __shared__ unsigned char raw[];
   __shared__ DqBars B;
   unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
-  unsigned char* ring = sm + 2 * F::BYTES;
+  unsigned char *ringA = sm + 2 * F::BYTES, *ringB = ringA + F::NA * F::BYTES;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == 8) tc::tmem_alloc(&B.tmem, 512);
   if (threadIdx.x == 0) {
     mma::mbar_init(&B.own, 1);
-    for (int i = 0; i < F::STAGES; i++) {
-      mma::mbar_init(&B.full[i], 1);
-      mma::mbar_init(&B.empty[i], 1);
+    for (int i = 0; i < F::NA; i++) {
+      mma::mbar_init(&B.fullA[i], 1);
+      mma::mbar_init(&B.emptyA[i], 1);
+    }
+    for (int i = 0; i < F::NB; i++) {
+      mma::mbar_init(&B.fullB[i], 1);
+      mma::mbar_init(&B.emptyB[i], 1);
     }
     mma::mbar_init(&B.s, 1);
     mma::mbar_init(&B.taken, 8);
@@ -834,32 +869,38 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
     }
     __syncwarp();
     for (int x = 0; x < n; x++) {
-      const int s = x % F::STAGES, r = x / F::STAGES;
-      if (r > 0 && !wait(&B.empty[s], (r - 1) & 1, &B.dead)) break;
+      const int sa = x % F::NA, sb = x % F::NB;
+      if (x >= F::NA && !wait(&B.emptyA[sa], (x / F::NA - 1) & 1, &B.dead)) break;
       if (lane == 0) {
-        mma::mbar_expect_tx(&B.full[s], 2 * F::BYTES);
-        load_block<D>(ring + 2 * s * F::BYTES, &mk, hk, t.k0 + x * BLK, &B.full[s]);
-        load_block<D>(ring + (2 * s + 1) * F::BYTES, &mv, hk, t.k0 + x * BLK, &B.full[s]);
+        mma::mbar_expect_tx(&B.fullA[sa], F::BYTES);
+        load_block<D>(ringA + sa * F::BYTES, &mk, hk, t.k0 + x * BLK, &B.fullA[sa]);
+      }
+      __syncwarp();
+      if (x >= F::NB && !wait(&B.emptyB[sb], (x / F::NB - 1) & 1, &B.dead)) break;
+      if (lane == 0) {
+        mma::mbar_expect_tx(&B.fullB[sb], F::BYTES);
+        load_block<D>(ringB + sb * F::BYTES, &mv, hk, t.k0 + x * BLK, &B.fullB[sb]);
       }
       __syncwarp();
     }
   } else if (warp == 8) {  // products
-    const uint32_t q0 = mma::smem_u32(sm), g0 = q0 + F::BYTES, r0 = mma::smem_u32(ring);
+    const uint32_t q0 = mma::smem_u32(sm), g0 = q0 + F::BYTES, a0 = mma::smem_u32(ringA), b0 = mma::smem_u32(ringB);
     constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
     const uint32_t me = elect();
     auto pairs = [&](int x) {
-      const uint32_t kb = r0 + x % F::STAGES * 2 * F::BYTES;
+      const uint32_t kb = a0 + x % F::NA * F::BYTES, vb = b0 + x % F::NB * F::BYTES;
 #pragma unroll
       for (int s = 0; s < D / 16; s++) mma_ss(cS, desc_k(q0, s), desc_k(kb, s), id_s, s > 0, me);
 #pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(cDP, desc_k(g0, s), desc_k(kb + F::BYTES, s), id_s, s > 0, me);
+      for (int s = 0; s < D / 16; s++) mma_ss(cDP, desc_k(g0, s), desc_k(vb, s), id_s, s > 0, me);
       commit(&B.s, me);
+      commit(&B.emptyB[x % F::NB], me);
     };
     auto ready = [&](int x) -> bool {
-      const int s = x % F::STAGES, left = t.Lk - x * BLK;
-      if (!wait(&B.full[s], (x / F::STAGES) & 1, &B.dead)) return false;
-      if (left < BLK) zero_rows<D>(ring + 2 * s * F::BYTES, left);
-      return true;
+      const int left = t.Lk - x * BLK;
+      if (!wait(&B.fullA[x % F::NA], (x / F::NA) & 1, &B.dead)) return false;
+      if (left < BLK) zero_rows<D>(ringA + x % F::NA * F::BYTES, left);
+      return wait(&B.fullB[x % F::NB], (x / F::NB) & 1, &B.dead);
     };
     auto run = [&]() -> bool {
       if (!wait(&B.own, 0, &B.dead) || !ready(0)) return false;
@@ -872,12 +913,12 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
         }
         if (!wait(&B.ds, x & 1, &B.dead)) return false;
         tc::fence_after();
-        const uint32_t kb = r0 + x % F::STAGES * 2 * F::BYTES;
+        const uint32_t kb = a0 + x % F::NA * F::BYTES;
 #pragma unroll
         for (int s = 0; s < BLK / 16; s++)
           mma_ts(cDQ, cDS + 64 * (x & 1) + 8 * s, desc_mn(kb, s), id_o, x > 0 || s > 0, me);
         commit(&B.used[x & 1], me);
-        commit(&B.empty[x % F::STAGES], me);
+        commit(&B.emptyA[x % F::NA], me);
       }
       return true;
     };
@@ -892,7 +933,8 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
     const uint32_t ts = tm + cS + 64 * half + lanes, td = tm + cDP + 64 * half + lanes;
     const int lim = in ? keys_of(P.causal, i0 + r, t.Lq, t.Lk) : 0;
     const size_t at = (size_t)h * P.Nq + t.q0 + i0 + r;
-    const float l2 = in ? P.lse2[at] : 0.f, dl = in ? P.delta[at] : 0.f;
+    const float nl = in ? -P.lse2[at] : 0.f, nd = in ? -P.delta[at] : 0.f;
+    const uint64_t sc = two(P.scale2, P.scale2), l2 = two(nl, nl), dl = two(nd, nd);
     bool ok = true;
     for (int x = 0; x < n; x++) {
       ok = wait(&B.s, x & 1, &B.dead);
@@ -913,8 +955,8 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       const int left = lim - x * BLK - 64 * half;
       const bool cut = x >= clean;
       uint32_t w[32];
-      dq_grads(a, c, l2, dl, P.scale2, cut, left, w);
-      dq_grads(b, d, l2, dl, P.scale2, cut, left - 32, w + 16);
+      dq_grads(a, c, sc, l2, dl, cut, left, w);
+      dq_grads(b, d, sc, l2, dl, cut, left - 32, w + 16);
       if (x >= 2) {
         ok = wait(&B.used[x & 1], (x / 2 - 1) & 1, &B.dead);
         if (!ok) break;
@@ -951,17 +993,17 @@ cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, cons
     return cudaErrorInvalidValue;
   const int64_t gk = (int64_t)max_tiles(P, 2) * P.Hkv, gq = (int64_t)max_tiles(P, 1) * P.Hq;
   if (gk > 2147483647 || gq > 2147483647) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(smx_tc_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Bwd<D>::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(smx_tc_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DKV_SMEM<D>);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(smx_tc_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Bwd<D>::SMEM);
+    e = cudaFuncSetAttribute(smx_tc_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DQ_SMEM<D>);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DKV, st);
-  e = launch_pdl(smx_tc_dkv_kernel<D>, dim3((unsigned)gk), dim3(BWD_THREADS), Bwd<D>::SMEM, st, P, mq, mk, mv, mg,
+  e = launch_pdl(smx_tc_dkv_kernel<D>, dim3((unsigned)gk), dim3(BWD_THREADS), DKV_SMEM<D>, st, P, mq, mk, mv, mg,
                  (bf16*)dk, (bf16*)dv);
   prof_end(K_SMX_DKV, st);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DQ, st);
-  e = launch_pdl(smx_tc_dq_kernel<D>, dim3((unsigned)gq), dim3(BWD_THREADS), Bwd<D>::SMEM, st, P, mq, mk, mv, mg,
+  e = launch_pdl(smx_tc_dq_kernel<D>, dim3((unsigned)gq), dim3(BWD_THREADS), DQ_SMEM<D>, st, P, mq, mk, mv, mg,
                  (bf16*)dq);
   prof_end(K_SMX_DQ, st);
   return e;
