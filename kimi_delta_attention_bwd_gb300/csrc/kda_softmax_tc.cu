@@ -22,6 +22,12 @@ constexpr int BLK = 128;       // rows of a block of keys (or queries)
 constexpr int HALF = 16384;    // bytes of 128 rows by 64 columns, one swizzled half of a block
 constexpr float GROW = 8.0f;   // log2 of what a weight may exceed 1 by
 
+// The tensor memory's address, the same for the whole warp: with all 512 columns its first one.
+template <int COLS>
+__device__ __forceinline__ uint32_t tm_base(uint32_t slot) {
+  return COLS == 512 ? 0u : __shfl_sync(0xffffffffu, slot, 0);
+}
+
 // ------------------------------------------------------------ helpers
 // Descriptors of a block of 128 rows in 128-byte swizzled halves of 64 columns (TMA's layout): 8-row groups 1024 bytes apart.
 // K-major (rows are M or N): 16 columns of the contraction are 32 bytes of the swizzled row.  MN-major (rows are the
@@ -204,10 +210,11 @@ __device__ __forceinline__ void weights(float (&v)[32], uint32_t to, uint64_t sc
 }
 
 // Rows n .. of a block (other documents' tokens) become zeros, by one warp, before products read them.
-template <int D>
+template <int D, int ROWS>
 __device__ __forceinline__ void zero_rows(unsigned char* block, int n) {
-  for (int i = threadIdx.x & 31; i < (BLK - n) * 8 * (D / 64); i += 32) {
-    const int half = i / ((BLK - n) * 8), r = i % ((BLK - n) * 8);
+  static_assert(D == 64 || ROWS == BLK, "the second half of the columns lies HALF bytes further");
+  for (int i = threadIdx.x & 31; i < (ROWS - n) * 8 * (D / 64); i += 32) {
+    const int half = i / ((ROWS - n) * 8), r = i % ((ROWS - n) * 8);
     *reinterpret_cast<uint4*>(block + half * HALF + n * 128 + r * 16) = make_uint4(0, 0, 0, 0);
   }
   mma::fence_async_smem();
@@ -221,12 +228,18 @@ __device__ __forceinline__ void load_block(unsigned char* dst, const CUtensorMap
 }
 
 // ------------------------------------------------------------ forward
+// NT tiles a CTA.  At D = 128 two, sharing every block of keys and values.  At D = 64 one, and two CTAs per SM (tensor
+// memory and registers hold both): as much in flight, and one's start and end lie under the other's products, which
+// with the shorter rows of such models are a third of the time (300M batch: 116 us with two tiles).
 template <int D>
 struct Fwd {
+  static constexpr int NT = D == 64 ? 1 : 2;
   static constexpr int BYTES = HALF * (D / 64);      // a block
-  static constexpr int STAGES = D == 64 ? 8 : 5;     // blocks in the ring of keys and values
-  static constexpr int SMEM = (2 + STAGES) * BYTES + 1024 + 256;
-  static constexpr uint32_t S0 = 0, O0 = 2 * BLK;    // tensor memory columns: S of both tiles, o of both tiles
+  static constexpr int STAGES = 5;                   // blocks in the ring of keys and values
+  static constexpr int SMEM = (NT + STAGES) * BYTES + 1024;
+  static constexpr int COLS = NT == 1 ? 256 : 512;
+  static constexpr uint32_t S0 = 0, O0 = NT * BLK;   // tensor memory columns: S of the tiles, o of the tiles
+  static constexpr int THREADS = NT * BLK + 64;
 };
 
 struct FwdBars {
@@ -235,21 +248,20 @@ struct FwdBars {
   int dead;
 };
 
-constexpr int FWD_THREADS = 384;
-
 template <int D>
-__global__ void __launch_bounds__(FWD_THREADS, 1)
+__global__ void __launch_bounds__(Fwd<D>::THREADS, D == 64 ? 2 : 1)
 smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, bf16* __restrict__ o, float* __restrict__ lse) {
   using F = Fwd<D>;
+  constexpr int NT = F::NT, W_MMA = 4 * NT, W_LOAD = W_MMA + 1;
   extern __shared__ unsigned char raw[];
   __shared__ FwdBars B;
   unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
-  unsigned char* ring = sm + 2 * F::BYTES;
+  unsigned char* ring = sm + NT * F::BYTES;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (warp == 8) tc::tmem_alloc(&B.tmem, 512);
+  if (warp == W_MMA) tc::tmem_alloc(&B.tmem, F::COLS);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < NT; i++) {
       mma::mbar_init(&B.q[i], 1);
       mma::mbar_init(&B.s[i], 1);
       mma::mbar_init(&B.p[i], 4);
@@ -273,10 +285,10 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   const bool live = tile_of(P, 0, blockIdx.x / P.Hq, false, t);
   int i0 = 0, nq = 0, nb[2] = {0, 0}, clean[2] = {0, 0};  // blocks of each tile; those that no mask cuts
   if (live) {
-    i0 = t.t * TC_FWD;
-    nq = min(TC_FWD, t.Lq - i0);
+    i0 = t.t * (NT * BLK);
+    nq = min(NT * BLK, t.Lq - i0);
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < NT; i++)
       if (i * BLK < nq) {
         nb[i] = (keys_of(P.causal, i0 + min(nq, (i + 1) * BLK) - 1, t.Lq, t.Lk) + BLK - 1) / BLK;
         clean[i] = keys_of(P.causal, i0 + i * BLK, t.Lq, t.Lk) / BLK;
@@ -286,11 +298,11 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  constexpr uint32_t tm = 0;  // (all 512 columns of the tensor memory: its first address)
+  const uint32_t tm = tm_base<F::COLS>(B.tmem);
 
-  if (warp == 9) {  // loads
+  if (warp == W_LOAD) {  // loads
     if (lane == 0 && n > 0) {
-      for (int i = 0; i < 2; i++)
+      for (int i = 0; i < NT; i++)
         if (nb[i]) {
           mma::mbar_expect_tx(&B.q[i], F::BYTES);
           load_block<D>(sm + i * F::BYTES, &mq, h, t.q0 + i0 + i * BLK, &B.q[i]);
@@ -310,16 +322,16 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     if (*(volatile int*)&B.dead) {  // every copy lands before the shared memory is released
       for (int y = max(0, x - F::STAGES); y < x; y++)
         for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.full[y % F::STAGES], (y / F::STAGES) & 1); it++) {}
-      for (int i = 0; i < 2; i++)
+      for (int i = 0; i < NT; i++)
         if (nb[i])
           for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.q[i], 0); it++) {}
     }
-  } else if (warp == 8) {  // products
+  } else if (warp == W_MMA) {  // products
     const uint32_t q0 = mma::smem_u32(sm), r0 = mma::smem_u32(ring);
     constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
     const uint32_t me = elect();
     auto logits = [&](int i, int x) {
-      const uint32_t kb = r0 + x % F::STAGES * F::BYTES, qb = q0 + i * F::BYTES, d = F::S0 + i * BLK;
+      const uint32_t kb = r0 + x % F::STAGES * F::BYTES, qb = q0 + i * F::BYTES, d = tm + F::S0 + i * BLK;
 #pragma unroll
       for (int s = 0; s < D / 16; s++) mma_ss(d, desc_k(qb, s), desc_k(kb, s), id_s, s > 0, me);
       commit(&B.s[i], me);
@@ -327,7 +339,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     auto run = [&]() -> bool {
       if (!wait(&B.full[0], 0, &B.dead)) return false;
 #pragma unroll
-      for (int i = 0; i < 2; i++)
+      for (int i = 0; i < NT; i++)
         if (nb[i]) {
           if (!wait(&B.q[i], 0, &B.dead)) return false;
           logits(i, 0);
@@ -336,15 +348,15 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       for (int j = 0; j < n; j++) {
         const int xv = 2 * j + 1, xk = 2 * j + 2, sv = xv % F::STAGES, sk = xk % F::STAGES;
         if (!wait(&B.full[sv], (xv / F::STAGES) & 1, &B.dead)) return false;
-        if (t.Lk - j * BLK < BLK) zero_rows<D>(ring + sv * F::BYTES, t.Lk - j * BLK);
+        if (t.Lk - j * BLK < BLK) zero_rows<D, BLK>(ring + sv * F::BYTES, t.Lk - j * BLK);
         if (j + 1 < n && !wait(&B.full[sk], (xk / F::STAGES) & 1, &B.dead)) return false;
         const uint32_t vb = r0 + sv * F::BYTES;
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < NT; i++) {
           if (j >= nb[i]) continue;
           if (!wait(&B.p[i], j & 1, &B.dead)) return false;
           tc::fence_after();
-          const uint32_t a = F::S0 + i * BLK, d = F::O0 + i * D;
+          const uint32_t a = tm + F::S0 + i * BLK, d = tm + F::O0 + i * D;
 #pragma unroll
           for (int s = 0; s < BLK / 16; s++)
             mma_ts(d, a + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, j > 0 || s > 0, me);
@@ -353,9 +365,9 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
             for (int s = 0; s < BLK / 16; s++)
               mma_ts(d, a + 16 + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, true, me);
           commit(&B.o[i], me);
-          if (i == 1 || j >= nb[1]) commit(&B.empty[sv], me);
+          if (i == NT - 1 || j >= nb[1]) commit(&B.empty[sv], me);
           if (j + 1 < nb[i]) logits(i, xk);
-          if (j + 1 < n && (i == 1 || j + 1 >= nb[1])) commit(&B.empty[sk], me);
+          if (j + 1 < n && (i == NT - 1 || j + 1 >= nb[1])) commit(&B.empty[sk], me);
         }
       }
       return true;
@@ -364,7 +376,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       commit(&B.drain, me);
       for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
     }
-  } else if (warp < 8 && live) {  // weights: a thread a row
+  } else if (warp < W_MMA && live) {  // weights: a thread a row
     const int i = warp / 4, r = i * BLK + (threadIdx.x & 127), nbi = i ? nb[1] : nb[0], cleani = i ? clean[1] : clean[0];
     const bool in = r < nq;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -466,9 +478,9 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   }
   __syncthreads();
   if (threadIdx.x == 0 && B.dead) *P.err = KDA_ERR_DEVICE;
-  if (warp == 8) {
+  if (warp == W_MMA) {
     tc::fence_after();
-    tc::tmem_dealloc(tm, 512);
+    tc::tmem_dealloc(tm, F::COLS);
   }
 }
 
@@ -483,7 +495,7 @@ cudaError_t fwd(const SmxP& P, const void* q, const void* k, const void* v, void
   cudaError_t e = cudaFuncSetAttribute(smx_tc_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Fwd<D>::SMEM);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_FWD, st);
-  e = launch_pdl(smx_tc_fwd_kernel<D>, dim3((unsigned)grid), dim3(FWD_THREADS), Fwd<D>::SMEM, st, P, mq, mk, mv,
+  e = launch_pdl(smx_tc_fwd_kernel<D>, dim3((unsigned)grid), dim3(Fwd<D>::THREADS), Fwd<D>::SMEM, st, P, mq, mk, mv,
                  (bf16*)o, lse);
   prof_end(K_SMX_FWD, st);
   return e;
@@ -535,11 +547,11 @@ __device__ __forceinline__ void dq_grads(float (&v)[32], const float (&dp)[32], 
 #pragma unroll
   for (int e = 0; e < 16; e++) w[e] = pack(v[2 * e], v[2 * e + 1]);
 }
-// Half of a row of an accumulator, times f, as bf16 (zeros where nothing was accumulated).
-template <int D>
-__device__ __forceinline__ void store_row(bf16* dst, uint32_t tm, int half, bool in, bool any, float f) {
+// Columns C0 .. C0 + N - 1 of a row of an accumulator, times f, as bf16 (zeros where nothing was accumulated).
+template <int C0, int N>
+__device__ __forceinline__ void store_row(bf16* dst, uint32_t tm, bool in, bool any, float f) {
 #pragma unroll
-  for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+  for (int c = C0; c < C0 + N; c += 32) {
     float v[32];
     if (any) {
       tm_ld32(tm + c, v);
@@ -566,40 +578,47 @@ __device__ __forceinline__ void store_row(bf16* dst, uint32_t tm, int half, bool
 //
 // Both kernels keep two blocks of their own and two rings: A, of the blocks that a first product and then the last one
 // reads (q for dk and dv, k for dq), and B, of those that are free earlier (dO, v).
+// The other side's blocks have XB rows: 128, and eight warps for the pairs, at D = 128; at D = 64 half of both, and two
+// CTAs per SM.
 template <int D>
 struct Bwd {
-  static constexpr int BYTES = HALF * (D / 64);
-  static constexpr int NA = D == 64 ? 5 : 3, NB = D == 64 ? 5 : 2;
-  static constexpr int BLOCKS = (2 + NA + NB) * BYTES;
+  static constexpr int XB = D == 64 ? 64 : 128;
+  static constexpr int OWN = HALF * (D / 64), BYTES = OWN / BLK * XB;  // a block of either side
+  static constexpr int NA = D == 64 ? 5 : 3, NB = D == 64 ? 4 : 2;
+  static constexpr int BLOCKS = 2 * OWN + (NA + NB) * BYTES;
+  static constexpr int EW = XB / 16;  // warps of the pairs: 64 of a row's pairs a thread
+  static constexpr int COLS = D == 64 ? 256 : 512;
+  static constexpr int PER_SM = D == 64 ? 2 : 1;
 };
-constexpr int BWD_THREADS = 384;
 
+template <int XB>
 struct BwdRest {  // (shared memory is full at D = 128: behind the blocks, whose swizzle wants 1024-byte alignment)
-  float stat[2][2][BLK];  // minus lse2 and minus delta of two blocks' queries
+  float stat[2][2][XB];  // minus lse2 and minus delta of two blocks' queries
   uint64_t own, fullA[5], emptyA[5], fullB[5], emptyB[5], fullS[2], s, dp, p, ds, done, drain;
   uint32_t tmem;
   int dead;
 };
 template <int D>
-constexpr int DKV_SMEM = Bwd<D>::BLOCKS + (int)sizeof(BwdRest);
-static_assert(DKV_SMEM<64> <= 232448 && DKV_SMEM<128> <= 232448, "227 KB of shared memory");
+constexpr int DKV_SMEM = Bwd<D>::BLOCKS + (int)sizeof(BwdRest<Bwd<D>::XB>);
+static_assert(2 * (DKV_SMEM<64> + 1024) <= 233472 && DKV_SMEM<128> <= 232448, "shared memory of an SM, of a CTA");
 
 template <int D>
-__global__ void __launch_bounds__(BWD_THREADS, 1)
+__global__ void __launch_bounds__(Bwd<D>::EW * 32 + 96, Bwd<D>::PER_SM)
 smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
                   bf16* __restrict__ dk, bf16* __restrict__ dv) {
   using F = Bwd<D>;
-  constexpr uint32_t cS = 0, cDP = BLK, cDV = 2 * BLK, cDK = 2 * BLK + D;
+  constexpr int XB = F::XB, EW = F::EW;
+  constexpr uint32_t cS = 0, cDP = XB, cDV = 2 * XB, cDK = 2 * XB + D;
   extern __shared__ __align__(1024) unsigned char sm[];
-  BwdRest& B = *reinterpret_cast<BwdRest*>(sm + F::BLOCKS);
+  BwdRest<XB>& B = *reinterpret_cast<BwdRest<XB>*>(sm + F::BLOCKS);
   if (mma::smem_u32(sm) & 1023) {  // (dynamic shared memory alone starts on such a boundary)
     if (blockIdx.x == 0 && threadIdx.x == 0) *P.err = KDA_ERR_DEVICE;
     return;
   }
-  unsigned char *ringA = sm + 2 * F::BYTES, *ringB = ringA + F::NA * F::BYTES;
+  unsigned char *ringA = sm + 2 * F::OWN, *ringB = ringA + F::NA * F::BYTES;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (warp == 8) tc::tmem_alloc(&B.tmem, 512);
+  if (warp == EW) tc::tmem_alloc(&B.tmem, F::COLS);
   if (threadIdx.x == 0) {
     mma::mbar_init(&B.own, 1);
     for (int i = 0; i < F::NA; i++) {
@@ -614,8 +633,8 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     mma::mbar_init(&B.fullS[1], 1);
     mma::mbar_init(&B.s, 1);
     mma::mbar_init(&B.dp, 1);
-    mma::mbar_init(&B.p, 8);
-    mma::mbar_init(&B.ds, 8);
+    mma::mbar_init(&B.p, EW);
+    mma::mbar_init(&B.ds, EW);
     mma::mbar_init(&B.done, 1);
     mma::mbar_init(&B.drain, 1);
     B.dead = 0;
@@ -629,24 +648,24 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   if (live) {
     j0 = t.t * BLK;
     nk = min(BLK, t.Lk - j0);
-    first = first_query(P.causal, j0, t.Lq, t.Lk) / BLK;
-    per = max(0, (t.Lq + BLK - 1) / BLK - first);
+    first = first_query(P.causal, j0, t.Lq, t.Lk) / XB;
+    per = max(0, (t.Lq + XB - 1) / XB - first);
   }
   const int n = per * P.G;
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  constexpr uint32_t tm = 0;  // (all 512 columns of the tensor memory: its first address)
+  const uint32_t tm = tm_base<F::COLS>(B.tmem);
 
-  if (warp == 9) {  // copies
+  if (warp == EW + 1) {  // copies
     if (lane == 0 && n > 0) {
-      mma::mbar_expect_tx(&B.own, 2 * F::BYTES);
+      mma::mbar_expect_tx(&B.own, 2 * F::OWN);
       load_block<D>(sm, &mk, hk, t.k0 + j0, &B.own);
-      load_block<D>(sm + F::BYTES, &mv, hk, t.k0 + j0, &B.own);
+      load_block<D>(sm + F::OWN, &mv, hk, t.k0 + j0, &B.own);
     }
     __syncwarp();
     for (int x = 0; x < n; x++) {
-      const int sa = x % F::NA, sb = x % F::NB, h = hk * P.G + x / per, row = t.q0 + (first + x % per) * BLK;
+      const int sa = x % F::NA, sb = x % F::NB, h = hk * P.G + x / per, row = t.q0 + (first + x % per) * XB;
       if (x >= F::NA && !wait(&B.emptyA[sa], (x / F::NA - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullA[sa], F::BYTES);
@@ -661,14 +680,14 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       __syncwarp();
     }
     // (a wait gives up after a second: by then every copy under way has landed)
-  } else if (warp == 10) {  // row sums
+  } else if (warp == EW + 2) {  // row sums
     for (int x = 0; x < n; x++) {
       const int s = x & 1;  // (free once block x - 2 has left ring A)
       if (x >= 2 && !wait(&B.emptyA[(x - 2) % F::NA], ((x - 2) / F::NA) & 1, &B.dead)) break;
-      const int h = hk * P.G + x / per, i0 = (first + x % per) * BLK;
+      const int h = hk * P.G + x / per, i0 = (first + x % per) * XB;
       const size_t at = (size_t)h * P.Nq + t.q0 + i0;
 #pragma unroll
-      for (int c = lane; c < BLK; c += 32) {
+      for (int c = lane; c < XB; c += 32) {
         const bool in = i0 + c < t.Lq;
         B.stat[s][0][c] = in ? -P.lse2[at + c] : 0.f;
         B.stat[s][1][c] = in ? -P.delta[at + c] : 0.f;
@@ -676,25 +695,25 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       __syncwarp();
       if (lane == 0) mma::mbar_arrive(&B.fullS[s]);
     }
-  } else if (warp == 8) {  // products
-    const uint32_t k0 = mma::smem_u32(sm), v0 = k0 + F::BYTES, a0 = mma::smem_u32(ringA), b0 = mma::smem_u32(ringB);
-    constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
+  } else if (warp == EW) {  // products
+    const uint32_t k0 = mma::smem_u32(sm), v0 = k0 + F::OWN, a0 = mma::smem_u32(ringA), b0 = mma::smem_u32(ringB);
+    constexpr uint32_t id_s = idesc(BLK, XB, false), id_o = idesc(BLK, D, true);
     const uint32_t me = elect();
     auto pairs = [&](uint32_t d, uint32_t a, uint32_t b, uint64_t* bar) {
 #pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(d, desc_k(a, s), desc_k(b, s), id_s, s > 0, me);
+      for (int s = 0; s < D / 16; s++) mma_ss(tm + d, desc_k(a, s), desc_k(b, s), id_s, s > 0, me);
       commit(bar, me);
     };
     auto apply = [&](uint32_t d, uint32_t a, uint32_t b, bool acc) {  // (each half's 64 columns are 32 of bf16 pairs)
 #pragma unroll
-      for (int s = 0; s < BLK / 16; s++)
-        mma_ts(d, a + 64 * (s >> 2) + 8 * (s & 3), desc_mn(b, s), id_o, acc || s > 0, me);
+      for (int s = 0; s < XB / 16; s++)
+        mma_ts(tm + d, tm + a + 64 * (s >> 2) + 8 * (s & 3), desc_mn(b, s), id_o, acc || s > 0, me);
     };
     // block x of queries (of their dO) has landed; rows behind its document's last are zeros
     auto ready = [&](int x, unsigned char* block, uint64_t* full, int phase) -> bool {
-      const int left = t.Lq - (first + x % per) * BLK;
+      const int left = t.Lq - (first + x % per) * XB;
       if (!wait(full, phase & 1, &B.dead)) return false;
-      if (left < BLK) zero_rows<D>(block, left);
+      if (left < XB) zero_rows<D, XB>(block, left);
       return true;
     };
     auto readyA = [&](int x) { return ready(x, ringA + x % F::NA * F::BYTES, &B.fullA[x % F::NA], x / F::NA); };
@@ -733,7 +752,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       commit(&B.drain, me);
       for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
     }
-  } else if (warp < 8 && live) {  // weights and their gradients: a thread a key, 64 of a block's queries
+  } else if (warp < EW && live) {  // weights and their gradients: a thread a key, 64 of a block's queries
     const int half = warp / 4, r = threadIdx.x & 127;
     const bool in = r < nk;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -742,9 +761,9 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     const uint64_t sc = two(P.scale2, P.scale2);
     bool ok = true;
     for (int x = 0; x < n; x++) {
-      const int s = x & 1, i0 = (first + x % per) * BLK;
+      const int s = x & 1, i0 = (first + x % per) * XB;
       const float *l2 = B.stat[s][0] + 64 * half, *dl = B.stat[s][1] + 64 * half;
-      const bool cut = i0 < fq_last || i0 + BLK > t.Lq;
+      const bool cut = i0 < fq_last || i0 + XB > t.Lq;
       const int lo = fq - i0 - 64 * half, hi = t.Lq - i0 - 64 * half;
       float a[32], b[32];
       uint32_t w[32];
@@ -789,16 +808,24 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     }
     if (ok) {
       const size_t row = ((size_t)(t.k0 + j0 + r) * P.Hkv + hk) * D;
-      store_row<D>(dv + row, tm + cDV + lanes, half, in, n > 0, 1.0f);
-      store_row<D>(dk + row, tm + cDK + lanes, half, in, n > 0, P.scale);
+      if (EW == 4) {
+        store_row<0, D>(dv + row, tm + cDV + lanes, in, n > 0, 1.0f);
+        store_row<0, D>(dk + row, tm + cDK + lanes, in, n > 0, P.scale);
+      } else if (half == 0) {
+        store_row<0, D / 2>(dv + row, tm + cDV + lanes, in, n > 0, 1.0f);
+        store_row<0, D / 2>(dk + row, tm + cDK + lanes, in, n > 0, P.scale);
+      } else {
+        store_row<D / 2, D / 2>(dv + row, tm + cDV + lanes, in, n > 0, 1.0f);
+        store_row<D / 2, D / 2>(dk + row, tm + cDK + lanes, in, n > 0, P.scale);
+      }
     }
     tc::fence_before();
   }
   __syncthreads();
   if (threadIdx.x == 0 && B.dead) *P.err = KDA_ERR_DEVICE;
-  if (warp == 8) {
+  if (warp == EW) {
     tc::fence_after();
-    tc::tmem_dealloc(tm, 512);
+    tc::tmem_dealloc(tm, F::COLS);
   }
 }
 
@@ -814,18 +841,19 @@ struct DqBars {
 };
 
 template <int D>
-__global__ void __launch_bounds__(BWD_THREADS, 1)
+__global__ void __launch_bounds__(Bwd<D>::EW * 32 + 64, Bwd<D>::PER_SM)
 smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
                  bf16* __restrict__ dq) {
   using F = Bwd<D>;
-  constexpr uint32_t cS = 0, cDP = BLK, cDQ = 2 * BLK, cDS = 2 * BLK + D;
+  constexpr int XB = F::XB, EW = F::EW;
+  constexpr uint32_t cS = 0, cDP = XB, cDQ = 2 * XB, cDS = 2 * XB + D;
   extern __shared__ unsigned char raw[];
   __shared__ DqBars B;
   unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
-  unsigned char *ringA = sm + 2 * F::BYTES, *ringB = ringA + F::NA * F::BYTES;
+  unsigned char *ringA = sm + 2 * F::OWN, *ringB = ringA + F::NA * F::BYTES;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (warp == 8) tc::tmem_alloc(&B.tmem, 512);
+  if (warp == EW) tc::tmem_alloc(&B.tmem, F::COLS);
   if (threadIdx.x == 0) {
     mma::mbar_init(&B.own, 1);
     for (int i = 0; i < F::NA; i++) {
@@ -837,8 +865,8 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       mma::mbar_init(&B.emptyB[i], 1);
     }
     mma::mbar_init(&B.s, 1);
-    mma::mbar_init(&B.taken, 8);
-    mma::mbar_init(&B.ds, 8);
+    mma::mbar_init(&B.taken, EW);
+    mma::mbar_init(&B.ds, EW);
     mma::mbar_init(&B.used[0], 1);
     mma::mbar_init(&B.used[1], 1);
     mma::mbar_init(&B.drain, 1);
@@ -853,19 +881,19 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   if (live) {
     i0 = t.t * BLK;
     nq = min(BLK, t.Lq - i0);
-    n = (keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk) + BLK - 1) / BLK;
-    clean = keys_of(P.causal, i0, t.Lq, t.Lk) / BLK;
+    n = (keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk) + XB - 1) / XB;
+    clean = keys_of(P.causal, i0, t.Lq, t.Lk) / XB;
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  constexpr uint32_t tm = 0;  // (all 512 columns of the tensor memory: its first address)
+  const uint32_t tm = tm_base<F::COLS>(B.tmem);
 
-  if (warp == 9) {  // copies
+  if (warp == EW + 1) {  // copies
     if (lane == 0 && n > 0) {
-      mma::mbar_expect_tx(&B.own, 2 * F::BYTES);
+      mma::mbar_expect_tx(&B.own, 2 * F::OWN);
       load_block<D>(sm, &mq, h, t.q0 + i0, &B.own);
-      load_block<D>(sm + F::BYTES, &mg, h, t.q0 + i0, &B.own);
+      load_block<D>(sm + F::OWN, &mg, h, t.q0 + i0, &B.own);
     }
     __syncwarp();
     for (int x = 0; x < n; x++) {
@@ -873,33 +901,33 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (x >= F::NA && !wait(&B.emptyA[sa], (x / F::NA - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullA[sa], F::BYTES);
-        load_block<D>(ringA + sa * F::BYTES, &mk, hk, t.k0 + x * BLK, &B.fullA[sa]);
+        load_block<D>(ringA + sa * F::BYTES, &mk, hk, t.k0 + x * XB, &B.fullA[sa]);
       }
       __syncwarp();
       if (x >= F::NB && !wait(&B.emptyB[sb], (x / F::NB - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullB[sb], F::BYTES);
-        load_block<D>(ringB + sb * F::BYTES, &mv, hk, t.k0 + x * BLK, &B.fullB[sb]);
+        load_block<D>(ringB + sb * F::BYTES, &mv, hk, t.k0 + x * XB, &B.fullB[sb]);
       }
       __syncwarp();
     }
-  } else if (warp == 8) {  // products
-    const uint32_t q0 = mma::smem_u32(sm), g0 = q0 + F::BYTES, a0 = mma::smem_u32(ringA), b0 = mma::smem_u32(ringB);
-    constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
+  } else if (warp == EW) {  // products
+    const uint32_t q0 = mma::smem_u32(sm), g0 = q0 + F::OWN, a0 = mma::smem_u32(ringA), b0 = mma::smem_u32(ringB);
+    constexpr uint32_t id_s = idesc(BLK, XB, false), id_o = idesc(BLK, D, true);
     const uint32_t me = elect();
     auto pairs = [&](int x) {
       const uint32_t kb = a0 + x % F::NA * F::BYTES, vb = b0 + x % F::NB * F::BYTES;
 #pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(cS, desc_k(q0, s), desc_k(kb, s), id_s, s > 0, me);
+      for (int s = 0; s < D / 16; s++) mma_ss(tm + cS, desc_k(q0, s), desc_k(kb, s), id_s, s > 0, me);
 #pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(cDP, desc_k(g0, s), desc_k(vb, s), id_s, s > 0, me);
+      for (int s = 0; s < D / 16; s++) mma_ss(tm + cDP, desc_k(g0, s), desc_k(vb, s), id_s, s > 0, me);
       commit(&B.s, me);
       commit(&B.emptyB[x % F::NB], me);
     };
     auto ready = [&](int x) -> bool {
-      const int left = t.Lk - x * BLK;
+      const int left = t.Lk - x * XB;
       if (!wait(&B.fullA[x % F::NA], (x / F::NA) & 1, &B.dead)) return false;
-      if (left < BLK) zero_rows<D>(ringA + x % F::NA * F::BYTES, left);
+      if (left < XB) zero_rows<D, XB>(ringA + x % F::NA * F::BYTES, left);
       return wait(&B.fullB[x % F::NB], (x / F::NB) & 1, &B.dead);
     };
     auto run = [&]() -> bool {
@@ -915,8 +943,8 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
         tc::fence_after();
         const uint32_t kb = a0 + x % F::NA * F::BYTES;
 #pragma unroll
-        for (int s = 0; s < BLK / 16; s++)
-          mma_ts(cDQ, cDS + 64 * (x & 1) + 8 * s, desc_mn(kb, s), id_o, x > 0 || s > 0, me);
+        for (int s = 0; s < XB / 16; s++)
+          mma_ts(tm + cDQ, tm + cDS + XB / 2 * (x & 1) + 8 * s, desc_mn(kb, s), id_o, x > 0 || s > 0, me);
         commit(&B.used[x & 1], me);
         commit(&B.emptyA[x % F::NA], me);
       }
@@ -926,7 +954,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       commit(&B.drain, me);
       for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
     }
-  } else if (warp < 8 && live) {  // a thread a query, 64 of a block's keys
+  } else if (warp < EW && live) {  // a thread a query, 64 of a block's keys
     const int half = warp / 4, r = threadIdx.x & 127;
     const bool in = r < nq;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -952,7 +980,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       tc::fence_before();
       __syncwarp();
       if (lane == 0) mma::mbar_arrive(&B.taken);
-      const int left = lim - x * BLK - 64 * half;
+      const int left = lim - x * XB - 64 * half;
       const bool cut = x >= clean;
       uint32_t w[32];
       dq_grads(a, c, sc, l2, dl, cut, left, w);
@@ -962,7 +990,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
         if (!ok) break;
         tc::fence_after();
       }
-      tm_st32(tm + cDS + 64 * (x & 1) + 32 * half + lanes, w);
+      tm_st32(tm + cDS + XB / 2 * (x & 1) + 32 * half + lanes, w);
       tm_wait_st();
       tc::fence_before();
       __syncwarp();
@@ -972,24 +1000,33 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       ok = wait(&B.used[(n - 1) & 1], ((n - 1) / 2) & 1, &B.dead);
       tc::fence_after();
     }
-    if (ok)
-      store_row<D>(dq + ((size_t)(t.q0 + i0 + r) * P.Hq + h) * D, tm + cDQ + lanes, half, in, n > 0, P.scale);
+    if (ok) {
+      bf16* dst = dq + ((size_t)(t.q0 + i0 + r) * P.Hq + h) * D;
+      if (EW == 4) store_row<0, D>(dst, tm + cDQ + lanes, in, n > 0, P.scale);
+      else if (half == 0) store_row<0, D / 2>(dst, tm + cDQ + lanes, in, n > 0, P.scale);
+      else store_row<D / 2, D / 2>(dst, tm + cDQ + lanes, in, n > 0, P.scale);
+    }
     tc::fence_before();
   }
   __syncthreads();
   if (threadIdx.x == 0 && B.dead) *P.err = KDA_ERR_DEVICE;
-  if (warp == 8) {
+  if (warp == EW) {
     tc::fence_after();
-    tc::tmem_dealloc(tm, 512);
+    tc::tmem_dealloc(tm, F::COLS);
   }
 }
 
 template <int D>
 cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, const void* dO, void* dq, void* dk,
                 void* dv, cudaStream_t st) {
-  CUtensorMap mq, mk, mv, mg;
+  constexpr int XB = Bwd<D>::XB;
+  CUtensorMap mq, mk, mv, mg, xq, xk, xv, xg;  // blocks of 128 rows, and of the other side's XB
   if (!encode_head_rows(&mq, q, P.Nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, P.Nk, P.Hkv, D, BLK) ||
       !encode_head_rows(&mv, v, P.Nk, P.Hkv, D, BLK) || !encode_head_rows(&mg, dO, P.Nq, P.Hq, D, BLK))
+    return cudaErrorInvalidValue;
+  xq = mq, xk = mk, xv = mv, xg = mg;
+  if (XB != BLK && (!encode_head_rows(&xq, q, P.Nq, P.Hq, D, XB) || !encode_head_rows(&xk, k, P.Nk, P.Hkv, D, XB) ||
+                    !encode_head_rows(&xv, v, P.Nk, P.Hkv, D, XB) || !encode_head_rows(&xg, dO, P.Nq, P.Hq, D, XB)))
     return cudaErrorInvalidValue;
   const int64_t gk = (int64_t)max_tiles(P, 2) * P.Hkv, gq = (int64_t)max_tiles(P, 1) * P.Hq;
   if (gk > 2147483647 || gq > 2147483647) return cudaErrorInvalidValue;
@@ -998,12 +1035,12 @@ cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, cons
     e = cudaFuncSetAttribute(smx_tc_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DQ_SMEM<D>);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DKV, st);
-  e = launch_pdl(smx_tc_dkv_kernel<D>, dim3((unsigned)gk), dim3(BWD_THREADS), DKV_SMEM<D>, st, P, mq, mk, mv, mg,
+  e = launch_pdl(smx_tc_dkv_kernel<D>, dim3((unsigned)gk), dim3(Bwd<D>::EW * 32 + 96), DKV_SMEM<D>, st, P, xq, mk, mv, xg,
                  (bf16*)dk, (bf16*)dv);
   prof_end(K_SMX_DKV, st);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DQ, st);
-  e = launch_pdl(smx_tc_dq_kernel<D>, dim3((unsigned)gq), dim3(BWD_THREADS), DQ_SMEM<D>, st, P, mq, mk, mv, mg,
+  e = launch_pdl(smx_tc_dq_kernel<D>, dim3((unsigned)gq), dim3(Bwd<D>::EW * 32 + 64), DQ_SMEM<D>, st, P, mq, xk, xv, mg,
                  (bf16*)dq);
   prof_end(K_SMX_DQ, st);
   return e;
