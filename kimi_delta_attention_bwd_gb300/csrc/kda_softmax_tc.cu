@@ -209,6 +209,44 @@ __device__ __forceinline__ void weights(float (&v)[32], uint32_t to, uint64_t sc
   }
 }
 
+// 64 columns (u: 32 bf16 pairs of this lane's row) of a warp's 32 rows to global memory, through 4 KB of shared memory
+// of its own (rows of 128 bytes, 16-byte pieces swizzled): a lane's row alone would make every store 32 half sectors.
+// The first n rows are stored; dst is the warp's first row, ld elements a row.
+__device__ __forceinline__ void store_rows(unsigned char* buf, const uint32_t (&u)[32], bf16* dst, size_t ld, int n) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 8; c++)
+    *reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const int r = 4 * i + lane / 8, c = lane & 7;
+    const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    if (r < n) *reinterpret_cast<uint4*>(dst + r * ld + 8 * c) = x;
+  }
+  __syncwarp();
+}
+// 64 columns of an accumulator, times f, as bf16 (zeros where nothing was accumulated).
+__device__ __forceinline__ void store_acc(unsigned char* buf, uint32_t tm, bool any, float f, bf16* dst, size_t ld,
+                                          int n) {
+  uint32_t u[32];
+#pragma unroll
+  for (int c = 0; c < 2; c++) {
+    float v[32];
+    if (any) {
+      tm_ld32(tm + 32 * c, v);
+      tm_wait_ld(v);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; e++) u[16 * c + e] = any ? pack(v[2 * e] * f, v[2 * e + 1] * f) : 0u;
+  }
+  store_rows(buf, u, dst, ld, n);
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
+}
+
 // Rows n .. of a block (other documents' tokens) become zeros, by one warp, before products read them.
 template <int D, int ROWS>
 __device__ __forceinline__ void zero_rows(unsigned char* block, int n) {
@@ -228,17 +266,19 @@ __device__ __forceinline__ void load_block(unsigned char* dst, const CUtensorMap
 }
 
 // ------------------------------------------------------------ forward
-// NT tiles a CTA.  At D = 128 two, sharing every block of keys and values.  At D = 64 one, and two CTAs per SM (tensor
-// memory and registers hold both): as much in flight, and one's start and end lie under the other's products, which
-// with the shorter rows of such models are a third of the time (300M batch: 116 us with two tiles).
+// At D = 128 a CTA has two tiles (NT), sharing every block of 128 keys and values.  At D = 64 it has one, blocks of 64
+// keys (XB) and two places for S (SB), so that a block's products run under the weights of the one before, and an
+// SM has two CTAs, whose starts and ends lie under each other's products.  The smaller products of D = 64 leave the
+// exponentials and these waits as the bound: with tiles and blocks as at D = 128 the 300M batch took 116 us, with two
+// CTAs of one tile and blocks of 128 107 us.
 template <int D>
 struct Fwd {
-  static constexpr int NT = D == 64 ? 1 : 2;
-  static constexpr int BYTES = HALF * (D / 64);      // a block
-  static constexpr int STAGES = 5;                   // blocks in the ring of keys and values
-  static constexpr int SMEM = (NT + STAGES) * BYTES + 1024;
-  static constexpr int COLS = NT == 1 ? 256 : 512;
-  static constexpr uint32_t S0 = 0, O0 = NT * BLK;   // tensor memory columns: S of the tiles, o of the tiles
+  static constexpr int NT = D == 64 ? 1 : 2, XB = D == 64 ? 64 : 128, SB = D == 64 ? 2 : 1;
+  static constexpr int OWN = HALF * (D / 64), BYTES = OWN / BLK * XB;  // a tile of queries, a block of keys or values
+  static constexpr int STAGES = D == 64 ? 8 : 5;                       // blocks in their ring
+  static constexpr int SMEM = NT * OWN + STAGES * BYTES + 1024;
+  static constexpr int COLS = D == 64 ? 256 : 512;
+  static constexpr uint32_t S0 = 0, O0 = 2 * XB;  // tensor memory columns: two S (of two tiles, or blocks), o of the tiles
   static constexpr int THREADS = NT * BLK + 64;
 };
 
@@ -253,15 +293,20 @@ __global__ void __launch_bounds__(Fwd<D>::THREADS, D == 64 ? 2 : 1)
 smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, bf16* __restrict__ o, float* __restrict__ lse) {
   using F = Fwd<D>;
-  constexpr int NT = F::NT, W_MMA = 4 * NT, W_LOAD = W_MMA + 1;
+  constexpr int NT = F::NT, XB = F::XB, SB = F::SB, W_MMA = 4 * NT, W_LOAD = W_MMA + 1;
   extern __shared__ unsigned char raw[];
   __shared__ FwdBars B;
   unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
-  unsigned char* ring = sm + NT * F::BYTES;
+  unsigned char* ring = sm + NT * F::OWN;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == W_MMA) tc::tmem_alloc(&B.tmem, F::COLS);
+  if (threadIdx.x == 32 * W_LOAD) {
+    prefetch_map(&mq);
+    prefetch_map(&mk);
+    prefetch_map(&mv);
+  }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NT; i++) {
+    for (int i = 0; i < 2; i++) {
       mma::mbar_init(&B.q[i], 1);
       mma::mbar_init(&B.s[i], 1);
       mma::mbar_init(&B.p[i], 4);
@@ -290,8 +335,8 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
 #pragma unroll
     for (int i = 0; i < NT; i++)
       if (i * BLK < nq) {
-        nb[i] = (keys_of(P.causal, i0 + min(nq, (i + 1) * BLK) - 1, t.Lq, t.Lk) + BLK - 1) / BLK;
-        clean[i] = keys_of(P.causal, i0 + i * BLK, t.Lq, t.Lk) / BLK;
+        nb[i] = (keys_of(P.causal, i0 + min(nq, (i + 1) * BLK) - 1, t.Lq, t.Lk) + XB - 1) / XB;
+        clean[i] = keys_of(P.causal, i0 + i * BLK, t.Lq, t.Lk) / XB;
       }
   }
   const int n = max(nb[0], nb[1]);
@@ -304,8 +349,8 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     if (lane == 0 && n > 0) {
       for (int i = 0; i < NT; i++)
         if (nb[i]) {
-          mma::mbar_expect_tx(&B.q[i], F::BYTES);
-          load_block<D>(sm + i * F::BYTES, &mq, h, t.q0 + i0 + i * BLK, &B.q[i]);
+          mma::mbar_expect_tx(&B.q[i], F::OWN);
+          load_block<D>(sm + i * F::OWN, &mq, h, t.q0 + i0 + i * BLK, &B.q[i]);
         }
     }
     __syncwarp();
@@ -315,7 +360,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       if (r > 0 && !wait(&B.empty[s], (r - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.full[s], F::BYTES);
-        load_block<D>(ring + s * F::BYTES, x & 1 ? &mv : &mk, hk, t.k0 + x / 2 * BLK, &B.full[s]);
+        load_block<D>(ring + s * F::BYTES, x & 1 ? &mv : &mk, hk, t.k0 + x / 2 * XB, &B.full[s]);
       }
       __syncwarp();
     }
@@ -328,46 +373,52 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     }
   } else if (warp == W_MMA) {  // products
     const uint32_t q0 = mma::smem_u32(sm), r0 = mma::smem_u32(ring);
-    constexpr uint32_t id_s = idesc(BLK, BLK, false), id_o = idesc(BLK, D, true);
+    constexpr uint32_t id_s = idesc(BLK, XB, false), id_o = idesc(BLK, D, true);
     const uint32_t me = elect();
-    auto logits = [&](int i, int x) {
-      const uint32_t kb = r0 + x % F::STAGES * F::BYTES, qb = q0 + i * F::BYTES, d = tm + F::S0 + i * BLK;
+    // S of tile i and key block j, into place u
+    auto logits = [&](int i, int j, int u) {
+      const uint32_t kb = r0 + 2 * j % F::STAGES * F::BYTES, qb = q0 + i * F::OWN, d = tm + F::S0 + u * XB;
 #pragma unroll
       for (int s = 0; s < D / 16; s++) mma_ss(d, desc_k(qb, s), desc_k(kb, s), id_s, s > 0, me);
-      commit(&B.s[i], me);
+      commit(&B.s[u], me);
     };
     auto run = [&]() -> bool {
-      if (!wait(&B.full[0], 0, &B.dead)) return false;
 #pragma unroll
-      for (int i = 0; i < NT; i++)
-        if (nb[i]) {
-          if (!wait(&B.q[i], 0, &B.dead)) return false;
-          logits(i, 0);
-        }
-      commit(&B.empty[0], me);
+      for (int j = 0; j < SB; j++) {
+        if (j >= n) break;
+        if (!wait(&B.full[2 * j], 0, &B.dead)) return false;
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+          if (nb[i]) {
+            if (!wait(&B.q[i], 0, &B.dead)) return false;
+            logits(i, j, SB == 1 ? i : j);
+          }
+        commit(&B.empty[2 * j], me);
+      }
       for (int j = 0; j < n; j++) {
-        const int xv = 2 * j + 1, xk = 2 * j + 2, sv = xv % F::STAGES, sk = xk % F::STAGES;
+        const int xv = 2 * j + 1, jn = j + SB, sv = xv % F::STAGES, sk = 2 * jn % F::STAGES;
         if (!wait(&B.full[sv], (xv / F::STAGES) & 1, &B.dead)) return false;
-        if (t.Lk - j * BLK < BLK) zero_rows<D, BLK>(ring + sv * F::BYTES, t.Lk - j * BLK);
-        if (j + 1 < n && !wait(&B.full[sk], (xk / F::STAGES) & 1, &B.dead)) return false;
+        if (t.Lk - j * XB < XB) zero_rows<D, XB>(ring + sv * F::BYTES, t.Lk - j * XB);
+        if (jn < n && !wait(&B.full[sk], (2 * jn / F::STAGES) & 1, &B.dead)) return false;
         const uint32_t vb = r0 + sv * F::BYTES;
 #pragma unroll
         for (int i = 0; i < NT; i++) {
           if (j >= nb[i]) continue;
-          if (!wait(&B.p[i], j & 1, &B.dead)) return false;
+          const int u = SB == 1 ? i : j & 1;
+          if (!wait(&B.p[u], (SB == 1 ? j : j >> 1) & 1, &B.dead)) return false;
           tc::fence_after();
-          const uint32_t a = tm + F::S0 + i * BLK, d = tm + F::O0 + i * D;
+          const uint32_t a = tm + F::S0 + u * XB, d = tm + F::O0 + i * D;
 #pragma unroll
-          for (int s = 0; s < BLK / 16; s++)
+          for (int s = 0; s < XB / 16; s++)
             mma_ts(d, a + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, j > 0 || s > 0, me);
           if (j >= clean[i])
 #pragma unroll
-            for (int s = 0; s < BLK / 16; s++)
+            for (int s = 0; s < XB / 16; s++)
               mma_ts(d, a + 16 + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, true, me);
           commit(&B.o[i], me);
           if (i == NT - 1 || j >= nb[1]) commit(&B.empty[sv], me);
-          if (j + 1 < nb[i]) logits(i, xk);
-          if (j + 1 < n && (i == NT - 1 || j + 1 >= nb[1])) commit(&B.empty[sk], me);
+          if (jn < nb[i]) logits(i, jn, u);
+          if (jn < n && (i == NT - 1 || jn >= nb[1])) commit(&B.empty[sk], me);
         }
       }
       return true;
@@ -380,26 +431,28 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     const int i = warp / 4, r = i * BLK + (threadIdx.x & 127), nbi = i ? nb[1] : nb[0], cleani = i ? clean[1] : clean[0];
     const bool in = r < nq;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tm + F::S0 + i * BLK + lanes, to = tm + F::O0 + i * D + lanes;
+    const uint32_t to = tm + F::O0 + i * D + lanes;
     const int lim = in ? keys_of(P.causal, i0 + r, t.Lq, t.Lk) : 0;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < nbi; j++) {
-      ok = wait(&B.s[i], j & 1, &B.dead);
+      const int u = SB == 1 ? i : j & 1;
+      const uint32_t ts = tm + F::S0 + u * XB + lanes;
+      ok = wait(&B.s[u], (SB == 1 ? j : j >> 1) & 1, &B.dead);
       if (!ok) break;
       tc::fence_after();
       const bool cut = j >= cleani;
-      const int left = lim - j * BLK;
-      float s[4][32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      const int left = lim - j * XB;
+      float s[XB / 32][32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 4; c++) tm_ld32(ts + 32 * c, s[c]);
+      for (int c = 0; c < XB / 32; c++) tm_ld32(ts + 32 * c, s[c]);
 #pragma unroll
-      for (int c = 0; c < 4; c++) tm_wait_ld(s[c]);
+      for (int c = 0; c < XB / 32; c++) tm_wait_ld(s[c]);
       if (cut)
 #pragma unroll
-        for (int c = 0; c < 4; c++) mask(s[c], left - 32 * c);
+        for (int c = 0; c < XB / 32; c++) mask(s[c], left - 32 * c);
 #pragma unroll
-      for (int c = 0; c < 4; c++) row_max(s[c], mx);
+      for (int c = 0; c < XB / 32; c++) row_max(s[c], mx);
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       const bool raise = top > m && !((top - m) * P.scale2 <= GROW);
       if (__any_sync(0xffffffffu, raise)) {
@@ -425,14 +478,14 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       const uint64_t sc = two(P.scale2, P.scale2), ng = two(neg, neg);
       uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int c = 0; c < 4; c++) weights(s[c], ts + 32 * c, sc, ng, cut, sum);
+      for (int c = 0; c < XB / 32; c++) weights(s[c], ts + 32 * c, sc, ng, cut, sum);
       float s0, s1;
       one(add2(sum[0], sum[1]), s0, s1);
       l += s0 + s1;
       tm_wait_st();
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) mma::mbar_arrive(&B.p[i]);
+      if (lane == 0) mma::mbar_arrive(&B.p[u]);
     }
     if (ok && nbi > 0) {
       ok = wait(&B.o[i], (nbi - 1) & 1, &B.dead);
@@ -440,34 +493,28 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     }
     if (ok) {
       const float inv = l == 0.f ? 0.f : 1.0f / l, l2 = m * P.scale2 + log2f(l);
-      const size_t row = (size_t)(t.q0 + i0 + r) * P.Hq + h;
+      const int w0 = r & ~31, rows = nq - w0;  // the warp's first row, rows from there on
+      const size_t row = (size_t)(t.q0 + i0 + r) * P.Hq + h, row0 = (size_t)(t.q0 + i0 + w0) * P.Hq + h;
+      unsigned char* buf = sm + i * F::OWN + (w0 & 127) * 128;  // (the tile's queries are no longer read)
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        float v[32];
-        if (nbi > 0) {
-          tm_ld32(to + c, v);
-          tm_wait_ld(v);
-        }
-        if (in) {
+      for (int c = 0; c < D; c += 64) {
+        uint32_t u[32], w[32];  // o, and what its rounding leaves
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint32_t u[4];
-#pragma unroll
-          for (int y = 0; y < 4; y++) {
-            float &a = v[e + 2 * y], &b = v[e + 2 * y + 1];
-            a = l == 0.f ? 0.f : a * inv;
-            b = l == 0.f ? 0.f : b * inv;
-            u[y] = pack(a, b);
-            a -= low(u[y]);
-            b -= high(u[y]);
+        for (int y = 0; y < 2; y++) {
+          float v[32];
+          if (nbi > 0) {
+            tm_ld32(to + c + 32 * y, v);
+            tm_wait_ld(v);
           }
-          *reinterpret_cast<uint4*>(o + row * D + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
-          if (P.save)
-            *reinterpret_cast<uint4*>(P.res + row * D + c + e) =
-                make_uint4(pack(v[e], v[e + 1]), pack(v[e + 2], v[e + 3]), pack(v[e + 4], v[e + 5]), pack(v[e + 6], v[e + 7]));
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            const float a = l == 0.f ? 0.f : v[2 * e] * inv, b = l == 0.f ? 0.f : v[2 * e + 1] * inv;
+            u[16 * y + e] = pack(a, b);
+            w[16 * y + e] = pack(a - low(u[16 * y + e]), b - high(u[16 * y + e]));
+          }
         }
-        }
-        __syncwarp();
+        store_rows(buf, u, o + row0 * D + c, (size_t)P.Hq * D, rows);
+        if (P.save) store_rows(buf, w, P.res + row0 * D + c, (size_t)P.Hq * D, rows);
       }
       if (in) {
         lse[row] = l2 * LN2;
@@ -486,9 +533,10 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
 
 template <int D>
 cudaError_t fwd(const SmxP& P, const void* q, const void* k, const void* v, void* o, float* lse, cudaStream_t st) {
+  constexpr int XB = Fwd<D>::XB;
   CUtensorMap mq, mk, mv;
-  if (!encode_head_rows(&mq, q, P.Nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, P.Nk, P.Hkv, D, BLK) ||
-      !encode_head_rows(&mv, v, P.Nk, P.Hkv, D, BLK))
+  if (!encode_head_rows(&mq, q, P.Nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, P.Nk, P.Hkv, D, XB) ||
+      !encode_head_rows(&mv, v, P.Nk, P.Hkv, D, XB))
     return cudaErrorInvalidValue;
   const int64_t grid = (int64_t)max_tiles(P, 0) * P.Hq;
   if (grid > 2147483647) return cudaErrorInvalidValue;
@@ -547,29 +595,6 @@ __device__ __forceinline__ void dq_grads(float (&v)[32], const float (&dp)[32], 
 #pragma unroll
   for (int e = 0; e < 16; e++) w[e] = pack(v[2 * e], v[2 * e + 1]);
 }
-// Columns C0 .. C0 + N - 1 of a row of an accumulator, times f, as bf16 (zeros where nothing was accumulated).
-template <int C0, int N>
-__device__ __forceinline__ void store_row(bf16* dst, uint32_t tm, bool in, bool any, float f) {
-#pragma unroll
-  for (int c = C0; c < C0 + N; c += 32) {
-    float v[32];
-    if (any) {
-      tm_ld32(tm + c, v);
-      tm_wait_ld(v);
-    }
-    if (in) {
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint32_t u[4];
-#pragma unroll
-        for (int y = 0; y < 4; y++) u[y] = any ? pack(v[e + 2 * y] * f, v[e + 2 * y + 1] * f) : 0u;
-        *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
-      }
-    }
-    __syncwarp();
-  }
-}
-
 // dk and dv, per CTA: 128 keys of one key head, over the blocks of 128 queries of its group's heads.  The pairs lie
 // transposed, a key a lane: S' = k q^T, P' = 2^(scale2 S' - lse2), dP' = v dO^T, dS' = P' (dP' - delta), and P' and
 // dS' (bf16, over S' and dP' in tensor memory) are the operands of dv += P' dO and dk += dS' q.  Eight warps form
@@ -619,6 +644,12 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   unsigned char *ringA = sm + 2 * F::OWN, *ringB = ringA + F::NA * F::BYTES;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == EW) tc::tmem_alloc(&B.tmem, F::COLS);
+  if (threadIdx.x == 32 * (EW + 1)) {
+    prefetch_map(&mq);
+    prefetch_map(&mk);
+    prefetch_map(&mv);
+    prefetch_map(&mg);
+  }
   if (threadIdx.x == 0) {
     mma::mbar_init(&B.own, 1);
     for (int i = 0; i < F::NA; i++) {
@@ -754,7 +785,6 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     }
   } else if (warp < EW && live) {  // weights and their gradients: a thread a key, 64 of a block's queries
     const int half = warp / 4, r = threadIdx.x & 127;
-    const bool in = r < nk;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tm + cS + 64 * half + lanes, td = tm + cDP + 64 * half + lanes;
     const int fq = first_query(P.causal, j0 + r, t.Lq, t.Lk), fq_last = first_query(P.causal, j0 + nk - 1, t.Lq, t.Lk);
@@ -807,17 +837,11 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       tc::fence_after();
     }
     if (ok) {
-      const size_t row = ((size_t)(t.k0 + j0 + r) * P.Hkv + hk) * D;
-      if (EW == 4) {
-        store_row<0, D>(dv + row, tm + cDV + lanes, in, n > 0, 1.0f);
-        store_row<0, D>(dk + row, tm + cDK + lanes, in, n > 0, P.scale);
-      } else if (half == 0) {
-        store_row<0, D / 2>(dv + row, tm + cDV + lanes, in, n > 0, 1.0f);
-        store_row<0, D / 2>(dk + row, tm + cDK + lanes, in, n > 0, P.scale);
-      } else {
-        store_row<D / 2, D / 2>(dv + row, tm + cDV + lanes, in, n > 0, 1.0f);
-        store_row<D / 2, D / 2>(dk + row, tm + cDK + lanes, in, n > 0, P.scale);
-      }
+      const int w0 = r & ~31, c = 64 * half;  // (the CTA's own blocks are no longer read)
+      const size_t at = ((size_t)(t.k0 + j0 + w0) * P.Hkv + hk) * D + c, ld = (size_t)P.Hkv * D;
+      unsigned char* buf = sm + half * HALF + w0 * 128;
+      store_acc(buf, tm + cDV + c + lanes, n > 0, 1.0f, dv + at, ld, nk - w0);
+      store_acc(buf, tm + cDK + c + lanes, n > 0, P.scale, dk + at, ld, nk - w0);
     }
     tc::fence_before();
   }
@@ -854,6 +878,12 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   unsigned char *ringA = sm + 2 * F::OWN, *ringB = ringA + F::NA * F::BYTES;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == EW) tc::tmem_alloc(&B.tmem, F::COLS);
+  if (threadIdx.x == 32 * (EW + 1)) {
+    prefetch_map(&mq);
+    prefetch_map(&mk);
+    prefetch_map(&mv);
+    prefetch_map(&mg);
+  }
   if (threadIdx.x == 0) {
     mma::mbar_init(&B.own, 1);
     for (int i = 0; i < F::NA; i++) {
@@ -1001,10 +1031,9 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       tc::fence_after();
     }
     if (ok) {
-      bf16* dst = dq + ((size_t)(t.q0 + i0 + r) * P.Hq + h) * D;
-      if (EW == 4) store_row<0, D>(dst, tm + cDQ + lanes, in, n > 0, P.scale);
-      else if (half == 0) store_row<0, D / 2>(dst, tm + cDQ + lanes, in, n > 0, P.scale);
-      else store_row<D / 2, D / 2>(dst, tm + cDQ + lanes, in, n > 0, P.scale);
+      const int w0 = r & ~31, c = 64 * half;
+      store_acc(sm + half * HALF + w0 * 128, tm + cDQ + c + lanes, n > 0, P.scale,
+                dq + ((size_t)(t.q0 + i0 + w0) * P.Hq + h) * D + c, (size_t)P.Hq * D, nq - w0);
     }
     tc::fence_before();
   }
