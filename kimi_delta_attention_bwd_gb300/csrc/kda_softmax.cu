@@ -200,7 +200,7 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   P.causal = p->causal;
   P.scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D);
   P.scale2 = P.scale * LOG2E;
-  P.tile[0] = p->dtype == KDA_BF16 ? tc_fwd_tile(p->D) : 64;
+  P.tile[0] = p->dtype == KDA_BF16 ? TC_FWD : 64;
   P.tile[1] = P.tile[2] = p->dtype == KDA_BF16 ? TC_BWD : 64;
   uint32_t tag = 0x536d61u;
   for (const int32_t v : {P.B, P.T, P.Tk, P.Hq, P.Hkv, p->D, p->dtype, P.causal, P.n_docs, P.rows,

@@ -76,9 +76,8 @@ cudaError_t launch_f32_fwd(const SmxP& P, int D, int dtype, const void* q, const
 cudaError_t launch_f32_bwd(const SmxP& P, int D, int dtype, const void* q, const void* k, const void* v,
                            const void* dO, void* dq, void* dk, void* dv, cudaStream_t st);
 
-// bf16 io: tiles of 128 (D = 64) or 256 queries (forward), 128 queries and 128 keys (backward).
-constexpr int tc_fwd_tile(int D) { return D == 64 ? 128 : 256; }
-constexpr int TC_BWD = 128;
+// bf16 io: tiles of 256 queries (forward), 128 queries and 128 keys (backward).
+constexpr int TC_FWD = 256, TC_BWD = 128;
 cudaError_t launch_tc_fwd(const SmxP& P, int D, const void* q, const void* k, const void* v, void* o, float* lse,
                           cudaStream_t st);
 cudaError_t launch_tc_bwd(const SmxP& P, int D, const void* q, const void* k, const void* v, const void* dO, void* dq,

@@ -8,8 +8,8 @@
 // down) only where a row's maximum has grown by 2^8: weights stay below 2^8, which bf16 and fp32 hold with the same
 // relative precision as those below 1.
 // Weights are rounded to bf16 (2^-8, the operand's type; o's error with that is that of one rounding of o times
-// sqrt(2)), but in blocks that a mask cuts they enter as two parts (2^-16): rows with few keys have theirs there, and
-// the backward's delta = o dO cancels against dO v in just those rows.
+// sqrt(2)), but in a first block that a mask cuts they enter as two parts (2^-16): rows with few keys have theirs there,
+// and the backward's delta = o dO cancels against dO v in just those rows.
 #include "kda_softmax.cuh"
 #include "kda_mma.cuh"
 #include "kda_tc.cuh"
@@ -78,22 +78,21 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t me) {
 
 // 32 columns of this warp's lanes, a lane a row.
 __device__ __forceinline__ void tm_ld32(uint32_t a, float (&v)[32]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(a));
 }
 __device__ __forceinline__ void tm_ld16(uint32_t a, float (&v)[16]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(a));
 }
 __device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t* r) {
@@ -105,6 +104,11 @@ __device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t* r) {
       "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
       : "memory");
+}
+__device__ __forceinline__ void tm_st8(uint32_t a, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};\n" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(a)
+               : "memory");
 }
 __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t* r) {
   asm volatile(
@@ -154,14 +158,16 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead) 
   return ok;
 }
 
-// 32 logits of a row: those from `left` on are not seen.
-__device__ __forceinline__ void mask(float (&v)[32], int left) {
+// Logits of a row: those from `left` on are not seen.
+template <int N>
+__device__ __forceinline__ void mask(float (&v)[N], int left) {
 #pragma unroll
-  for (int e = 0; e < 32; e++) v[e] = e < left ? v[e] : -INFINITY;
+  for (int e = 0; e < N; e++) v[e] = e < left ? v[e] : -INFINITY;
 }
-__device__ __forceinline__ void row_max(const float (&v)[32], float (&mx)[4]) {
+template <int N>
+__device__ __forceinline__ void row_max(const float (&v)[N], float (&mx)[4]) {
 #pragma unroll
-  for (int e = 0; e < 32; e += 8)
+  for (int e = 0; e < N; e += 8)
 #pragma unroll
     for (int y = 0; y < 4; y++)
       asm("max.f32 %0, %1, %2, %3;" : "=f"(mx[y]) : "f"(mx[y]), "f"(v[e + 2 * y]), "f"(v[e + 2 * y + 1]));
@@ -188,24 +194,24 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 32 logits into weights 2^(sc v + ng), their sum, and as bf16 to tensor memory (second parts 16 columns further, where
-// a mask cuts).
-__device__ __forceinline__ void weights(float (&v)[32], uint32_t to, uint64_t sc, uint64_t ng, bool cut,
-                                        uint64_t (&sum)[2]) {
-  uint32_t w[16];
+// Logits into weights 2^(sc v + ng), their sum, and as bf16 pairs; what that rounding leaves.
+template <int N>
+__device__ __forceinline__ void weights(float (&v)[N], uint64_t sc, uint64_t ng, uint64_t (&sum)[2], uint32_t* w) {
 #pragma unroll
-  for (int e = 0; e < 32; e += 2) {
+  for (int e = 0; e < N; e += 2) {
     one(fma2(two(v[e], v[e + 1]), sc, ng), v[e], v[e + 1]);
     v[e] = ex2(v[e]);
     v[e + 1] = ex2(v[e + 1]);
     sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], two(v[e], v[e + 1]));
     w[e / 2] = pack(v[e], v[e + 1]);
   }
-  tm_st16(to, w);
-  if (cut) {
+}
+template <int N>
+__device__ __forceinline__ void second_parts(const float (&v)[N], uint32_t* w) {
 #pragma unroll
-    for (int e = 0; e < 16; e++) w[e] = pack(v[2 * e] - low(w[e]), v[2 * e + 1] - high(w[e]));
-    tm_st16(to + 16, w);
+  for (int e = 0; e < N / 2; e++) {
+    const uint32_t h = pack(v[2 * e], v[2 * e + 1]);
+    w[e] = pack(v[2 * e] - low(h), v[2 * e + 1] - high(h));
   }
 }
 
@@ -266,19 +272,21 @@ __device__ __forceinline__ void load_block(unsigned char* dst, const CUtensorMap
 }
 
 // ------------------------------------------------------------ forward
-// At D = 128 a CTA has two tiles (NT), sharing every block of 128 keys and values.  At D = 64 it has one, blocks of 64
-// keys (XB) and two places for S (SB), so that a block's products run under the weights of the one before, and an
-// SM has two CTAs, whose starts and ends lie under each other's products.  The smaller products of D = 64 leave the
-// exponentials and these waits as the bound: with tiles and blocks as at D = 128 the 300M batch took 116 us, with two
-// CTAs of one tile and blocks of 128 107 us.
+// A CTA has two tiles that share every block of keys and values.  At D = 128 the products bound it, with one CTA per SM
+// and blocks of 128 keys.  At D = 64 they are half of that, and the exponentials and the waits between the steps count:
+// blocks of 64 keys let two CTAs share an SM (256 columns of tensor memory, 80 registers a thread), so that four tiles'
+// steps hide each other (300M batch: 88 us; with tiles and blocks as at D = 128 116 us, two CTAs of one tile 104).
 template <int D>
 struct Fwd {
-  static constexpr int NT = D == 64 ? 1 : 2, XB = D == 64 ? 64 : 128, SB = D == 64 ? 2 : 1;
+  static constexpr int NT = 2, XB = D == 64 ? 64 : 128;
   static constexpr int OWN = HALF * (D / 64), BYTES = OWN / BLK * XB;  // a tile of queries, a block of keys or values
   static constexpr int STAGES = D == 64 ? 8 : 5;                       // blocks in their ring
   static constexpr int SMEM = NT * OWN + STAGES * BYTES + 1024;
   static constexpr int COLS = D == 64 ? 256 : 512;
-  static constexpr uint32_t S0 = 0, O0 = 2 * XB;  // tensor memory columns: two S (of two tiles, or blocks), o of the tiles
+  static constexpr uint32_t S0 = 0, O0 = NT * XB;  // tensor memory columns: S of the tiles, o of the tiles
+  // Weights lie over the logits they come from: those of 16 keys at part(s), their second parts SECOND further.
+  static constexpr int SECOND = D == 64 ? 8 : 16;
+  static __device__ constexpr int part(int s) { return D == 64 ? 16 * s : 32 * (s >> 1) + 8 * (s & 1); }
   static constexpr int THREADS = NT * BLK + 64;
 };
 
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(Fwd<D>::THREADS, D == 64 ? 2 : 1)
 smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, bf16* __restrict__ o, float* __restrict__ lse) {
   using F = Fwd<D>;
-  constexpr int NT = F::NT, XB = F::XB, SB = F::SB, W_MMA = 4 * NT, W_LOAD = W_MMA + 1;
+  constexpr int NT = F::NT, XB = F::XB, W_MMA = 4 * NT, W_LOAD = W_MMA + 1;
   extern __shared__ unsigned char raw[];
   __shared__ FwdBars B;
   unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
@@ -375,50 +383,42 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     const uint32_t q0 = mma::smem_u32(sm), r0 = mma::smem_u32(ring);
     constexpr uint32_t id_s = idesc(BLK, XB, false), id_o = idesc(BLK, D, true);
     const uint32_t me = elect();
-    // S of tile i and key block j, into place u
-    auto logits = [&](int i, int j, int u) {
-      const uint32_t kb = r0 + 2 * j % F::STAGES * F::BYTES, qb = q0 + i * F::OWN, d = tm + F::S0 + u * XB;
+    auto logits = [&](int i, int j) {  // S of tile i and key block j
+      const uint32_t kb = r0 + 2 * j % F::STAGES * F::BYTES, qb = q0 + i * F::OWN, d = tm + F::S0 + i * XB;
 #pragma unroll
       for (int s = 0; s < D / 16; s++) mma_ss(d, desc_k(qb, s), desc_k(kb, s), id_s, s > 0, me);
-      commit(&B.s[u], me);
+      commit(&B.s[i], me);
     };
     auto run = [&]() -> bool {
+      if (!wait(&B.full[0], 0, &B.dead)) return false;
 #pragma unroll
-      for (int j = 0; j < SB; j++) {
-        if (j >= n) break;
-        if (!wait(&B.full[2 * j], 0, &B.dead)) return false;
-#pragma unroll
-        for (int i = 0; i < NT; i++)
-          if (nb[i]) {
-            if (!wait(&B.q[i], 0, &B.dead)) return false;
-            logits(i, j, SB == 1 ? i : j);
-          }
-        commit(&B.empty[2 * j], me);
-      }
+      for (int i = 0; i < NT; i++)
+        if (nb[i]) {
+          if (!wait(&B.q[i], 0, &B.dead)) return false;
+          logits(i, 0);
+        }
+      commit(&B.empty[0], me);
       for (int j = 0; j < n; j++) {
-        const int xv = 2 * j + 1, jn = j + SB, sv = xv % F::STAGES, sk = 2 * jn % F::STAGES;
+        const int xv = 2 * j + 1, xk = 2 * j + 2, sv = xv % F::STAGES, sk = xk % F::STAGES;
         if (!wait(&B.full[sv], (xv / F::STAGES) & 1, &B.dead)) return false;
         if (t.Lk - j * XB < XB) zero_rows<D, XB>(ring + sv * F::BYTES, t.Lk - j * XB);
-        if (jn < n && !wait(&B.full[sk], (2 * jn / F::STAGES) & 1, &B.dead)) return false;
+        if (j + 1 < n && !wait(&B.full[sk], (xk / F::STAGES) & 1, &B.dead)) return false;
         const uint32_t vb = r0 + sv * F::BYTES;
 #pragma unroll
         for (int i = 0; i < NT; i++) {
           if (j >= nb[i]) continue;
-          const int u = SB == 1 ? i : j & 1;
-          if (!wait(&B.p[u], (SB == 1 ? j : j >> 1) & 1, &B.dead)) return false;
+          if (!wait(&B.p[i], j & 1, &B.dead)) return false;
           tc::fence_after();
-          const uint32_t a = tm + F::S0 + u * XB, d = tm + F::O0 + i * D;
+          const uint32_t a = tm + F::S0 + i * XB, d = tm + F::O0 + i * D;
 #pragma unroll
-          for (int s = 0; s < XB / 16; s++)
-            mma_ts(d, a + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, j > 0 || s > 0, me);
-          if (j >= clean[i])
+          for (int s = 0; s < XB / 16; s++) mma_ts(d, a + F::part(s), desc_mn(vb, s), id_o, j > 0 || s > 0, me);
+          if (j == 0 && clean[i] == 0)
 #pragma unroll
-            for (int s = 0; s < XB / 16; s++)
-              mma_ts(d, a + 16 + 32 * (s >> 1) + 8 * (s & 1), desc_mn(vb, s), id_o, true, me);
+            for (int s = 0; s < XB / 16; s++) mma_ts(d, a + F::part(s) + F::SECOND, desc_mn(vb, s), id_o, true, me);
           commit(&B.o[i], me);
           if (i == NT - 1 || j >= nb[1]) commit(&B.empty[sv], me);
-          if (jn < nb[i]) logits(i, jn, u);
-          if (jn < n && (i == NT - 1 || jn >= nb[1])) commit(&B.empty[sk], me);
+          if (j + 1 < nb[i]) logits(i, j + 1);
+          if (j + 1 < n && (i == NT - 1 || j + 1 >= nb[1])) commit(&B.empty[sk], me);
         }
       }
       return true;
@@ -431,61 +431,134 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     const int i = warp / 4, r = i * BLK + (threadIdx.x & 127), nbi = i ? nb[1] : nb[0], cleani = i ? clean[1] : clean[0];
     const bool in = r < nq;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t to = tm + F::O0 + i * D + lanes;
-    const int lim = in ? keys_of(P.causal, i0 + r, t.Lq, t.Lk) : 0;
+    const uint32_t ts = tm + F::S0 + i * XB + lanes, to = tm + F::O0 + i * D + lanes;
+    const int lim = keys_of(P.causal, i0 + r, t.Lq, t.Lk);  // (grows with the row)
+    const uint64_t sc = two(P.scale2, P.scale2);
     float m = -INFINITY, l = 0.f;
+    // A new reference, the block's maximum `top`, in rows where it has grown by 2^GROW (or that ask for it): o and l are
+    // scaled down to it.  False: a wait gave up.
+    auto raise = [&](int j, float top, bool ask) -> bool {
+      const bool grew = top > m && (ask || !((top - m) * P.scale2 <= GROW));
+      if (!__any_sync(0xffffffffu, grew)) return true;
+      const float up = grew ? ex2((m - top) * P.scale2) : 1.0f;
+      if (grew) m = top;
+      l *= up;
+      if (j == 0) return true;
+      if (!wait(&B.o[i], (j - 1) & 1, &B.dead)) return false;
+      tc::fence_after();
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        float v[16];
+        tm_ld16(to + c, v);
+        tm_wait_ld(v);
+#pragma unroll
+        for (int e = 0; e < 16; e++) v[e] *= up;
+        tm_st16(to + c, reinterpret_cast<const uint32_t*>(v));
+      }
+      return true;
+    };
+    auto reference = [&]() { return m == -INFINITY ? 0.f : -m * P.scale2; };
     bool ok = true;
     for (int j = 0; j < nbi; j++) {
-      const int u = SB == 1 ? i : j & 1;
-      const uint32_t ts = tm + F::S0 + u * XB + lanes;
-      ok = wait(&B.s[u], (SB == 1 ? j : j >> 1) & 1, &B.dead);
+      ok = wait(&B.s[i], j & 1, &B.dead);
       if (!ok) break;
       tc::fence_after();
-      const bool cut = j >= cleani;
-      const int left = lim - j * XB;
-      float s[XB / 32][32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      const bool cut = j >= cleani, few = cut && j == 0;  // a mask cuts the block; some rows may have few keys in all
+      const int left = lim - j * XB, least = cut ? __shfl_sync(0xffffffffu, left, 0) : XB;  // (the warp's first row's)
+      uint64_t sum[2] = {0, 0};
+      float s0, s1;
+      if constexpr (D == 128) {
+        float s[4][32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < XB / 32; c++) tm_ld32(ts + 32 * c, s[c]);
+        for (int c = 0; c < 4; c++) tm_ld32(ts + 32 * c, s[c]);
 #pragma unroll
-      for (int c = 0; c < XB / 32; c++) tm_wait_ld(s[c]);
-      if (cut)
+        for (int c = 0; c < 4; c++) tm_wait_ld(s[c]);
+        if (cut)
 #pragma unroll
-        for (int c = 0; c < XB / 32; c++) mask(s[c], left - 32 * c);
+          for (int c = 0; c < 4; c++) mask(s[c], left - 32 * c);
 #pragma unroll
-      for (int c = 0; c < XB / 32; c++) row_max(s[c], mx);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const bool raise = top > m && !((top - m) * P.scale2 <= GROW);
-      if (__any_sync(0xffffffffu, raise)) {
-        const float up = raise ? ex2((m - top) * P.scale2) : 1.0f;
-        if (raise) m = top;
-        l *= up;
-        if (j > 0) {
-          ok = wait(&B.o[i], (j - 1) & 1, &B.dead);
-          if (!ok) break;
-          tc::fence_after();
+        for (int c = 0; c < 4; c++) row_max(s[c], mx);
+        ok = raise(j, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), false);
+        if (!ok) break;
+        const float neg = reference();
+        const uint64_t ng = two(neg, neg);
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          uint32_t w[16];
+          weights(s[c], sc, ng, sum, w);
+          tm_st16(ts + 32 * c, w);
+          if (few) {
+            second_parts(s[c], w);
+            tm_st16(ts + 32 * c + 16, w);
+          }
+        }
+      } else {
+        // The weights against the reference as it is: a row's sum of at most 2^GROW says that none is above it, and the
+        // maximum need not be known.  Else, and in the first block, the maximum first (a NaN row: every time).
+        float a[16], b[16];
+        bool ask = false, again = j == 0;
+        if (!again) {
+          const float neg = reference();
+          const uint64_t ng = two(neg, neg);
+          uint32_t w[32];
+          tm_ld16(ts, a);
+          tm_wait_ld(a);
+          tm_ld16(ts + 16, b);
+          if (least < 16) mask(a, left);
+          weights(a, sc, ng, sum, w);
+          tm_wait_ld(b);
+          tm_ld16(ts + 32, a);
+          if (least < 32) mask(b, left - 16);
+          weights(b, sc, ng, sum, w + 8);
+          tm_wait_ld(a);
+          tm_ld16(ts + 48, b);
+          if (least < 48) mask(a, left - 32);
+          weights(a, sc, ng, sum, w + 16);
+          tm_wait_ld(b);
+          if (least < 64) mask(b, left - 48);
+          weights(b, sc, ng, sum, w + 24);
+          one(add2(sum[0], sum[1]), s0, s1);
+          ask = !(s0 + s1 <= 256.0f) || m == -INFINITY;
+          again = __any_sync(0xffffffffu, ask);
+          if (!again)
+#pragma unroll
+            for (int c = 0; c < 4; c++) tm_st8(ts + 16 * c, w + 8 * c);
+        }
+        if (again) {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            float v[16];
-            tm_ld16(to + c, v);
-            tm_wait_ld(v);
-#pragma unroll
-            for (int e = 0; e < 16; e++) v[e] *= up;
-            tm_st16(to + c, reinterpret_cast<const uint32_t*>(v));
+          for (int c = 0; c < 4; c++) {
+            tm_ld16(ts + 16 * c, a);
+            tm_wait_ld(a);
+            if (least < 16 * (c + 1)) mask(a, left - 16 * c);
+            row_max(a, mx);
+          }
+          ok = raise(j, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), ask);
+          if (!ok) break;
+          const float neg = reference();
+          const uint64_t ng = two(neg, neg);
+          sum[0] = sum[1] = 0;
+#pragma unroll 1
+          for (int c = 0; c < 4; c++) {
+            uint32_t w[8];
+            tm_ld16(ts + 16 * c, a);
+            tm_wait_ld(a);
+            if (least < 16 * (c + 1)) mask(a, left - 16 * c);
+            weights(a, sc, ng, sum, w);
+            tm_st8(ts + 16 * c, w);
+            if (few) {
+              second_parts(a, w);
+              tm_st8(ts + 16 * c + 8, w);
+            }
           }
         }
       }
-      const float neg = m == -INFINITY ? 0.f : -m * P.scale2;
-      const uint64_t sc = two(P.scale2, P.scale2), ng = two(neg, neg);
-      uint64_t sum[2] = {0, 0};
-#pragma unroll
-      for (int c = 0; c < XB / 32; c++) weights(s[c], ts + 32 * c, sc, ng, cut, sum);
-      float s0, s1;
       one(add2(sum[0], sum[1]), s0, s1);
       l += s0 + s1;
       tm_wait_st();
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) mma::mbar_arrive(&B.p[u]);
+      if (lane == 0) mma::mbar_arrive(&B.p[i]);
     }
     if (ok && nbi > 0) {
       ok = wait(&B.o[i], (nbi - 1) & 1, &B.dead);
