@@ -200,8 +200,8 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   P.causal = p->causal;
   P.scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D);
   P.scale2 = P.scale * LOG2E;
-  P.tile[0] = p->dtype == KDA_BF16 ? TC_FWD : 64;
-  P.tile[1] = P.tile[2] = p->dtype == KDA_BF16 ? TC_BWD : 64;
+  for (int l = 0; l < 3; l++)
+    P.tile[l] = p->dtype == KDA_F32 ? f32_rows(p->D, l) : l == 0 ? TC_FWD : TC_BWD;
   uint32_t tag = 0x536d61u;
   for (const int32_t v : {P.B, P.T, P.Tk, P.Hq, P.Hkv, p->D, p->dtype, P.causal, P.n_docs, P.rows,
                           (int32_t)(p->cu_seqlens_k != nullptr)})
@@ -284,7 +284,8 @@ extern "C" KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, cons
   if ((uintptr_t)workspace % 256 != 0) return KDA_ERR_ALIGNMENT;
   if (!P.rows && launch_table(P, 0, 1, st) != cudaSuccess) return KDA_ERR_CUDA;
   const cudaError_t e = p->dtype == KDA_BF16 ? launch_tc_fwd(P, p->D, q, k, v, o, lse, st)
-                                             : launch_f32_fwd(P, p->D, p->dtype, q, k, v, o, lse, st);
+                                             : launch_f32_fwd(P, p->D, (const float*)q, (const float*)k, (const float*)v,
+                                                              (float*)o, lse, st);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -307,6 +308,7 @@ extern "C" KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, cons
     e = p->D == 64 ? launch_delta<64, bf16>(P, o, dO, st) : launch_delta<128, bf16>(P, o, dO, st);
   if (e != cudaSuccess) return KDA_ERR_CUDA;
   e = p->dtype == KDA_BF16 ? launch_tc_bwd(P, p->D, q, k, v, dO, dq, dk, dv, st)
-                           : launch_f32_bwd(P, p->D, p->dtype, q, k, v, dO, dq, dk, dv, st);
+                           : launch_f32_bwd(P, p->D, (const float*)q, (const float*)k, (const float*)v, (const float*)dO,
+                                            (float*)dq, (float*)dk, (float*)dv, st);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -70,11 +70,12 @@ __device__ __forceinline__ bool saved(const SmxP& P) {
   return false;
 }
 
-// Launches (fp32 io, and bf16): see the kernels.
-cudaError_t launch_f32_fwd(const SmxP& P, int D, int dtype, const void* q, const void* k, const void* v, void* o,
-                           float* lse, cudaStream_t st);
-cudaError_t launch_f32_bwd(const SmxP& P, int D, int dtype, const void* q, const void* k, const void* v,
-                           const void* dO, void* dq, void* dk, void* dv, cudaStream_t st);
+// fp32 io: rows of list l's tiles (128 where shared memory holds them).
+constexpr int f32_rows(int D, int l) { return D == 64 || l == 0 ? 128 : 64; }
+cudaError_t launch_f32_fwd(const SmxP& P, int D, const float* q, const float* k, const float* v, float* o, float* lse,
+                           cudaStream_t st);
+cudaError_t launch_f32_bwd(const SmxP& P, int D, const float* q, const float* k, const float* v, const float* dO,
+                           float* dq, float* dk, float* dv, cudaStream_t st);
 
 // bf16 io: tiles of 256 queries (forward), 128 queries and 128 keys (backward).
 constexpr int TC_FWD = 256, TC_BWD = 128;

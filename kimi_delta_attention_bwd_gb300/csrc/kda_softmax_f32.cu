@@ -1,11 +1,13 @@
-// Softmax attention on the fp32 pipe: the fp32 io path (and any io type).
+// Softmax attention for fp32 io, on the fp32 pipe.
 // Per document, query head h and its key head h / G:
 //   s_ij = scale q_i k_j,  p_ij = exp(s_ij - lse_i),  o_i = sum_j p_ij v_j
 //   dv_j = sum_i p_ij dO_i,  ds_ij = p_ij (dO_i v_j - delta_i),  delta_i = o_i dO_i
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
-// 64 x 64 tiles of pairs, 256 threads with 4 x 4 pairs each; operands of the pair
-// products lie transposed in shared memory ([d][row]) so that a thread's four rows
-// are one 16-byte load.  The forward keeps a running maximum and sum per row.  dk
+// Tiles of 16 R own rows by 64 of the other side, 256 threads with R x 4 pairs each;
+// operands of the pair products lie transposed in shared memory ([d][row]) so that a
+// thread's rows are one or two 16-byte loads.  R = 8 where shared memory holds it (32
+// products for three loads; R = 4, 16 for two, took XX times as long), the next block's values are
+// on their way to registers meanwhile.  The forward keeps a running maximum and sum per row.  dk
 // and dv of a key tile are summed by one CTA over the queries of its whole head
 // group, dq by one CTA over the keys: no atomics, a fixed order.
 #include "kda_softmax.cuh"
@@ -14,86 +16,98 @@ namespace kda {
 namespace smx {
 namespace {
 
-constexpr int TM = 64, NT = 256, PP = TM + 4;
+constexpr int TM = 64, NT = 256;  // rows of the other side's blocks; threads
 
-__device__ __forceinline__ void ld4(const float* p, float (&v)[4]) {
+__device__ __forceinline__ void ld4(const float* p, float* v) {
   const float4 f = *reinterpret_cast<const float4*>(p);
   v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
 }
-__device__ __forceinline__ void ld4(const bf16* p, float (&v)[4]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-}
-__device__ __forceinline__ void st4(float* p, const float (&v)[4]) {
+__device__ __forceinline__ void st4(float* p, const float* v) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ void st4(bf16* p, const float (&v)[4]) {
-  uint2 u;
-  *reinterpret_cast<__nv_bfloat162*>(&u.x) = __floats2bfloat162_rn(v[0], v[1]);
-  *reinterpret_cast<__nv_bfloat162*>(&u.y) = __floats2bfloat162_rn(v[2], v[3]);
-  *reinterpret_cast<uint2*>(p) = u;
-}
 
-// Rows 0 .. n - 1 (of TM; the rest zero, so that a neighbour's values never enter a
-// product) of x, whose rows are ld elements apart: tr[d][row], and pl[row][d] where wanted.
-template <int D, typename T>
-__device__ __forceinline__ void load_tile(const T* x, size_t ld, int n, float* tr, float* pl) {
-  for (int i = threadIdx.x; i < TM * D / 4; i += NT) {
-    const int r = i % TM, d = i / TM * 4;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r < n) ld4(x + r * ld + d, v);
-    if (tr)
+// A block of ROWS rows of x (ld elements apart) on its way to shared memory: rows from n on are zeros, so that a
+// neighbour's values never enter a product.
+template <int D, int ROWS>
+struct Block {
+  static constexpr int N = ROWS * D / 4 / NT;
+  float4 v[N];
+  __device__ __forceinline__ void load(const float* x, size_t ld, int n) {
 #pragma unroll
-      for (int e = 0; e < 4; e++) tr[(d + e) * TM + r] = v[e];
-    if (pl) st4(pl + r * D + d, v);
+    for (int k = 0; k < N; k++) {
+      const int i = threadIdx.x + k * NT, r = i % ROWS, d = i / ROWS * 4;
+      v[k] = r < n ? *reinterpret_cast<const float4*>(x + r * ld + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   }
-}
-
-// c[i][j] = sum_d a[d][r0 + i] b[d][c0 + j]
-template <int D>
-__device__ __forceinline__ void pairs(const float* a, const float* b, int r0, int c0, float (&c)[4][4]) {
+  // to tr[d][row], and to pl[row][d], where not null
+  __device__ __forceinline__ void store(float* tr, float* pl) const {
 #pragma unroll
-  for (int i = 0; i < 4; i++)
+    for (int k = 0; k < N; k++) {
+      const int i = threadIdx.x + k * NT, r = i % ROWS, d = i / ROWS * 4;
+      if (tr) {
+        tr[d * ROWS + r] = v[k].x;
+        tr[(d + 1) * ROWS + r] = v[k].y;
+        tr[(d + 2) * ROWS + r] = v[k].z;
+        tr[(d + 3) * ROWS + r] = v[k].w;
+      }
+      if (pl) *reinterpret_cast<float4*>(pl + r * D + d) = v[k];
+    }
+  }
+};
+
+// c[i][j] = sum_d a[d][r0 + i] b[d][c0 + j]: a has 16 R rows, b TM
+template <int D, int R>
+__device__ __forceinline__ void pairs(const float* a, const float* b, int r0, int c0, float (&c)[R][4]) {
+#pragma unroll
+  for (int i = 0; i < R; i++)
 #pragma unroll
     for (int j = 0; j < 4; j++) c[i][j] = 0.f;
 #pragma unroll 8
   for (int d = 0; d < D; d++) {
-    float x[4], y[4];
-    ld4(a + d * TM + r0, x);
+    float x[R], y[4];
+#pragma unroll
+    for (int i = 0; i < R; i += 4) ld4(a + d * 16 * R + r0 + i, x + i);
     ld4(b + d * TM + c0, y);
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < R; i++)
 #pragma unroll
       for (int j = 0; j < 4; j++) c[i][j] = fmaf(x[i], y[j], c[i][j]);
   }
 }
-// c[i][64 m + 4 tx + e] += sum_n w[n][r0 + i] x[n][64 m + 4 tx + e]
-template <int D>
-__device__ __forceinline__ void apply(const float* w, const float* x, int r0, int tx, float (&c)[4][D / 16]) {
+// c[i][64 m + 4 tx + e] += sum_n w[n][r0 + i] x[n][64 m + 4 tx + e]: w's rows are PP apart
+template <int R>
+constexpr int PP = 16 * R + 4;
+template <int D, int R>
+__device__ __forceinline__ void apply(const float* w, const float* x, int r0, int tx, float (&c)[R][D / 16]) {
 #pragma unroll 4
   for (int n = 0; n < TM; n++) {
-    float a[4];
-    ld4(w + n * PP + r0, a);
+    float a[R];
+#pragma unroll
+    for (int i = 0; i < R; i += 4) ld4(w + n * PP<R> + r0 + i, a + i);
 #pragma unroll
     for (int m = 0; m < D / 64; m++) {
       float y[4];
       ld4(x + n * D + 64 * m + 4 * tx, y);
 #pragma unroll
-      for (int i = 0; i < 4; i++)
+      for (int i = 0; i < R; i++)
 #pragma unroll
         for (int e = 0; e < 4; e++) c[i][4 * m + e] = fmaf(a[i], y[e], c[i][4 * m + e]);
     }
   }
 }
+template <int R>
+__device__ __forceinline__ void put_column(float* dst, const float (&v)[R]) {
+#pragma unroll
+  for (int i = 0; i < R; i += 4) st4(dst + i, v + i);
+}
 
-template <int D, typename T>
-__global__ void __launch_bounds__(NT) smx_fwd_kernel(SmxP P, const T* __restrict__ q, const T* __restrict__ k,
-                                                    const T* __restrict__ v, T* __restrict__ o,
+template <int D, int R>
+__global__ void __launch_bounds__(NT) smx_fwd_kernel(SmxP P, const float* __restrict__ q, const float* __restrict__ k,
+                                                    const float* __restrict__ v, float* __restrict__ o,
                                                     float* __restrict__ lse) {
+  constexpr int OWN = 16 * R;
   extern __shared__ __align__(16) float sm[];
-  float *sQ = sm, *sK = sQ + D * TM, *sV = sK + D * TM, *sP = sV + D * TM;
+  float *sQ = sm, *sK = sQ + D * OWN, *sV = sK + D * TM, *sP = sV + D * TM;
   pdl_wait();
   if (P.rows && blockIdx.x == 0 && threadIdx.x == 0) {
     *P.err = KDA_OK;
@@ -102,27 +116,38 @@ __global__ void __launch_bounds__(NT) smx_fwd_kernel(SmxP P, const T* __restrict
   const int h = blockIdx.x % P.Hq, hk = h / P.G, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   Tile t;
   if (!tile_of(P, 0, blockIdx.x / P.Hq, false, t)) return;
-  const int i0 = t.t * TM, nq = min(TM, t.Lq - i0);
-  load_tile<D>(q + ((size_t)(t.q0 + i0) * P.Hq + h) * D, (size_t)P.Hq * D, nq, sQ, (float*)nullptr);
-  float acc[4][D / 16] = {}, m[4], l[4];
-  int lim[4];
+  const int i0 = t.t * OWN, nq = min(OWN, t.Lq - i0);
+  {
+    Block<D, OWN> b;
+    b.load(q + ((size_t)(t.q0 + i0) * P.Hq + h) * D, (size_t)P.Hq * D, nq);
+    b.store(sQ, nullptr);
+  }
+  float acc[R][D / 16] = {}, m[R], l[R];
+  int lim[R];
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
+  for (int i = 0; i < R; i++) {
     m[i] = -INFINITY;
     l[i] = 0.f;
-    lim[i] = keys_of(P.causal, i0 + 4 * ty + i, t.Lq, t.Lk);
+    lim[i] = keys_of(P.causal, i0 + R * ty + i, t.Lq, t.Lk);
   }
   const int nk = keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk);
+  const size_t ld = (size_t)P.Hkv * D, at = ((size_t)t.k0 * P.Hkv + hk) * D;
+  Block<D, TM> bk, bv;
+  bk.load(k + at, ld, t.Lk);
+  bv.load(v + at, ld, t.Lk);
   for (int j0 = 0; j0 < nk; j0 += TM) {
     __syncthreads();
-    const size_t at = ((size_t)(t.k0 + j0) * P.Hkv + hk) * D;
-    load_tile<D>(k + at, (size_t)P.Hkv * D, t.Lk - j0, sK, (float*)nullptr);
-    load_tile<D>(v + at, (size_t)P.Hkv * D, t.Lk - j0, (float*)nullptr, sV);
+    bk.store(sK, nullptr);
+    bv.store(nullptr, sV);
     __syncthreads();
-    float s[4][4];
-    pairs<D>(sQ, sK, 4 * ty, 4 * tx, s);
+    if (j0 + TM < nk) {
+      bk.load(k + at + (j0 + TM) * ld, ld, t.Lk - j0 - TM);
+      bv.load(v + at + (j0 + TM) * ld, ld, t.Lk - j0 - TM);
+    }
+    float s[R][4];
+    pairs<D, R>(sQ, sK, R * ty, 4 * tx, s);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < R; i++) {
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; j++) {
@@ -145,17 +170,19 @@ __global__ void __launch_bounds__(NT) smx_fwd_kernel(SmxP P, const T* __restrict
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      const float col[4] = {s[0][j], s[1][j], s[2][j], s[3][j]};
-      st4(sP + (4 * tx + j) * PP + 4 * ty, col);
+      float col[R];
+#pragma unroll
+      for (int i = 0; i < R; i++) col[i] = s[i][j];
+      put_column<R>(sP + (4 * tx + j) * PP<R> + R * ty, col);
     }
     __syncwarp();  // a row's pairs are formed and used by one half warp
-    apply<D>(sP, sV, 4 * ty, tx, acc);
+    apply<D, R>(sP, sV, R * ty, tx, acc);
   }
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
+  for (int i = 0; i < R; i++) {
 #pragma unroll
     for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-    const int r = 4 * ty + i;
+    const int r = R * ty + i;
     if (r >= nq) continue;
     const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i], l2 = m[i] + log2f(l[i]);
     const size_t row = (size_t)(t.q0 + i0 + r) * P.Hq + h;
@@ -164,13 +191,6 @@ __global__ void __launch_bounds__(NT) smx_fwd_kernel(SmxP P, const T* __restrict
       const float y[4] = {acc[i][4 * c] * inv, acc[i][4 * c + 1] * inv, acc[i][4 * c + 2] * inv,
                           acc[i][4 * c + 3] * inv};
       st4(o + row * D + 64 * c + 4 * tx, y);
-      if (P.save && sizeof(T) == 2) {
-        float z[4];
-        ld4(o + row * D + 64 * c + 4 * tx, z);
-#pragma unroll
-        for (int e = 0; e < 4; e++) z[e] = y[e] - z[e];
-        st4(P.res + row * D + 64 * c + 4 * tx, z);
-      }
     }
     if (tx == 0) {
       lse[row] = l2 * LN2;
@@ -179,63 +199,90 @@ __global__ void __launch_bounds__(NT) smx_fwd_kernel(SmxP P, const T* __restrict
   }
 }
 
-// dk and dv of 64 keys of one key head.  Threads: keys 4 ty .., queries 4 tx ..
-template <int D, typename T>
-__global__ void __launch_bounds__(NT) smx_dkv_kernel(SmxP P, const T* __restrict__ q, const T* __restrict__ k,
-                                                    const T* __restrict__ v, const T* __restrict__ dO,
-                                                    T* __restrict__ dk, T* __restrict__ dv) {
+// dk and dv of 16 R keys of one key head.  Threads: keys R ty .., queries 4 tx ..
+template <int D, int R>
+__global__ void __launch_bounds__(NT) smx_dkv_kernel(SmxP P, const float* __restrict__ q, const float* __restrict__ k,
+                                                    const float* __restrict__ v, const float* __restrict__ dO,
+                                                    float* __restrict__ dk, float* __restrict__ dv) {
+  constexpr int OWN = 16 * R;
   extern __shared__ __align__(16) float sm[];
-  float *tK = sm, *tV = tK + D * TM, *tQ = tV + D * TM, *tG = tQ + D * TM, *sQ = tG + D * TM, *sG = sQ + D * TM;
-  float *sP = sG + D * TM, *sD = sP + TM * PP, *sl = sD + TM * PP, *sd = sl + TM;
+  float *tK = sm, *tV = tK + D * OWN, *tQ = tV + D * OWN, *tG = tQ + D * TM, *sQ = tG + D * TM, *sG = sQ + D * TM;
+  float *sP = sG + D * TM, *sl = sP + TM * PP<R>, *sd = sl + TM;  // (the weights, then their gradients)
   pdl_wait();
   if (!saved(P)) return;
   const int hk = blockIdx.x % P.Hkv, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   Tile t;
   if (!tile_of(P, 2, blockIdx.x / P.Hkv, true, t)) return;
-  const int j0 = t.t * TM, nk = min(TM, t.Lk - j0);
-  const size_t at = ((size_t)(t.k0 + j0) * P.Hkv + hk) * D;
-  load_tile<D>(k + at, (size_t)P.Hkv * D, nk, tK, (float*)nullptr);
-  load_tile<D>(v + at, (size_t)P.Hkv * D, nk, tV, (float*)nullptr);
-  float ak[4][D / 16] = {}, av[4][D / 16] = {};
-  const int first = first_query(P.causal, j0, t.Lq, t.Lk) / TM * TM;
-  for (int g = 0; g < P.G; g++) {
-    const int h = hk * P.G + g;
-    for (int i0 = first; i0 < t.Lq; i0 += TM) {
-      __syncthreads();
-      const size_t qa = ((size_t)(t.q0 + i0) * P.Hq + h) * D;
-      load_tile<D>(q + qa, (size_t)P.Hq * D, t.Lq - i0, tQ, sQ);
-      load_tile<D>(dO + qa, (size_t)P.Hq * D, t.Lq - i0, tG, sG);
-      if (threadIdx.x < TM) {
-        const bool in = i0 + (int)threadIdx.x < t.Lq;
-        const size_t r = (size_t)h * P.Nq + t.q0 + i0 + threadIdx.x;
-        sl[threadIdx.x] = in ? P.lse2[r] : 0.f;
-        sd[threadIdx.x] = in ? P.delta[r] : 0.f;
-      }
-      __syncthreads();
-      float s[4][4], dp[4][4];
-      pairs<D>(tK, tQ, 4 * ty, 4 * tx, s);
-      pairs<D>(tV, tG, 4 * ty, 4 * tx, dp);
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int i = i0 + 4 * tx + j, lim = i < t.Lq ? keys_of(P.causal, i, t.Lq, t.Lk) : 0;
-        float p[4], d[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const bool seen = j0 + 4 * ty + e < lim;
-          p[e] = seen ? ex2(fmaf(s[e][j], P.scale2, -sl[4 * tx + j])) : 0.f;
-          d[e] = seen ? p[e] * (dp[e][j] - sd[4 * tx + j]) : 0.f;
-        }
-        st4(sP + (4 * tx + j) * PP + 4 * ty, p);
-        st4(sD + (4 * tx + j) * PP + 4 * ty, d);
-      }
-      __syncwarp();
-      apply<D>(sP, sG, 4 * ty, tx, av);
-      apply<D>(sD, sQ, 4 * ty, tx, ak);
+  const int j0 = t.t * OWN, nk = min(OWN, t.Lk - j0);
+  {
+    const size_t at = ((size_t)(t.k0 + j0) * P.Hkv + hk) * D;
+    Block<D, OWN> b;
+    b.load(k + at, (size_t)P.Hkv * D, nk);
+    b.store(tK, nullptr);
+    b.load(v + at, (size_t)P.Hkv * D, nk);
+    b.store(tV, nullptr);
+  }
+  float ak[R][D / 16] = {}, av[R][D / 16] = {};
+  const int first = first_query(P.causal, j0, t.Lq, t.Lk) / TM, per = max(0, (t.Lq + TM - 1) / TM - first);
+  const size_t ld = (size_t)P.Hq * D;
+  Block<D, TM> bq, bg;
+  float nl = 0.f, nd = 0.f;
+  auto load = [&](int x) {  // block x of the group's heads' queries
+    const int h = hk * P.G + x / per, i0 = (first + x % per) * TM;
+    const size_t at = ((size_t)(t.q0 + i0) * P.Hq + h) * D;
+    bq.load(q + at, ld, t.Lq - i0);
+    bg.load(dO + at, ld, t.Lq - i0);
+    if (threadIdx.x < TM) {
+      const bool in = i0 + (int)threadIdx.x < t.Lq;
+      const size_t r = (size_t)h * P.Nq + t.q0 + i0 + threadIdx.x;
+      nl = in ? P.lse2[r] : 0.f;
+      nd = in ? P.delta[r] : 0.f;
     }
+  };
+  const int n = per * P.G;
+  if (n > 0) load(0);
+  for (int x = 0; x < n; x++) {
+    const int i0 = (first + x % per) * TM;
+    __syncthreads();
+    bq.store(tQ, sQ);
+    bg.store(tG, sG);
+    if (threadIdx.x < TM) {
+      sl[threadIdx.x] = nl;
+      sd[threadIdx.x] = nd;
+    }
+    __syncthreads();
+    if (x + 1 < n) load(x + 1);
+    float s[R][4], dp[R][4];
+    pairs<D, R>(tK, tQ, R * ty, 4 * tx, s);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int i = i0 + 4 * tx + j, lim = i < t.Lq ? keys_of(P.causal, i, t.Lq, t.Lk) : 0;
+      float p[R];
+#pragma unroll
+      for (int e = 0; e < R; e++) {
+        p[e] = j0 + R * ty + e < lim ? ex2(fmaf(s[e][j], P.scale2, -sl[4 * tx + j])) : 0.f;
+        s[e][j] = p[e];
+      }
+      put_column<R>(sP + (4 * tx + j) * PP<R> + R * ty, p);
+    }
+    __syncwarp();
+    apply<D, R>(sP, sG, R * ty, tx, av);
+    pairs<D, R>(tV, tG, R * ty, 4 * tx, dp);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      float d[R];
+#pragma unroll
+      for (int e = 0; e < R; e++) d[e] = s[e][j] == 0.f ? 0.f : s[e][j] * (dp[e][j] - sd[4 * tx + j]);
+      put_column<R>(sP + (4 * tx + j) * PP<R> + R * ty, d);
+    }
+    __syncwarp();
+    apply<D, R>(sP, sQ, R * ty, tx, ak);
+    __syncwarp();
   }
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int r = 4 * ty + i;
+  for (int i = 0; i < R; i++) {
+    const int r = R * ty + i;
     if (r >= nk) continue;
     const size_t row = ((size_t)(t.k0 + j0 + r) * P.Hkv + hk) * D;
 #pragma unroll
@@ -249,56 +296,69 @@ __global__ void __launch_bounds__(NT) smx_dkv_kernel(SmxP P, const T* __restrict
   }
 }
 
-// dq of 64 queries of one head.  Threads: queries 4 ty .., keys 4 tx ..
-template <int D, typename T>
-__global__ void __launch_bounds__(NT) smx_dq_kernel(SmxP P, const T* __restrict__ q, const T* __restrict__ k,
-                                                   const T* __restrict__ v, const T* __restrict__ dO,
-                                                   T* __restrict__ dq) {
+// dq of 16 R queries of one head.  Threads: queries R ty .., keys 4 tx ..
+template <int D, int R>
+__global__ void __launch_bounds__(NT) smx_dq_kernel(SmxP P, const float* __restrict__ q, const float* __restrict__ k,
+                                                   const float* __restrict__ v, const float* __restrict__ dO,
+                                                   float* __restrict__ dq) {
+  constexpr int OWN = 16 * R;
   extern __shared__ __align__(16) float sm[];
-  float *tQ = sm, *tG = tQ + D * TM, *tK = tG + D * TM, *tV = tK + D * TM, *sK = tV + D * TM, *sD = sK + D * TM;
+  float *tQ = sm, *tG = tQ + D * OWN, *tK = tG + D * OWN, *tV = tK + D * TM, *sK = tV + D * TM, *sD = sK + D * TM;
   pdl_wait();
   if (!saved(P)) return;
   const int h = blockIdx.x % P.Hq, hk = h / P.G, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   Tile t;
   if (!tile_of(P, 1, blockIdx.x / P.Hq, false, t)) return;
-  const int i0 = t.t * TM, nq = min(TM, t.Lq - i0);
+  const int i0 = t.t * OWN, nq = min(OWN, t.Lq - i0);
   const size_t qa = ((size_t)(t.q0 + i0) * P.Hq + h) * D;
-  load_tile<D>(q + qa, (size_t)P.Hq * D, nq, tQ, (float*)nullptr);
-  load_tile<D>(dO + qa, (size_t)P.Hq * D, nq, tG, (float*)nullptr);
-  float acc[4][D / 16] = {}, l2[4], del[4];
-  int lim[4];
+  {
+    Block<D, OWN> b;
+    b.load(q + qa, (size_t)P.Hq * D, nq);
+    b.store(tQ, nullptr);
+    b.load(dO + qa, (size_t)P.Hq * D, nq);
+    b.store(tG, nullptr);
+  }
+  float acc[R][D / 16] = {}, l2[R], del[R];
+  int lim[R];
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int r = 4 * ty + i;
+  for (int i = 0; i < R; i++) {
+    const int r = R * ty + i;
     const size_t at = (size_t)h * P.Nq + t.q0 + i0 + r;
     l2[i] = r < nq ? P.lse2[at] : 0.f;
     del[i] = r < nq ? P.delta[at] : 0.f;
     lim[i] = r < nq ? keys_of(P.causal, i0 + r, t.Lq, t.Lk) : 0;
   }
   const int nk = keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk);
+  const size_t ld = (size_t)P.Hkv * D, at = ((size_t)t.k0 * P.Hkv + hk) * D;
+  Block<D, TM> bk, bv;
+  bk.load(k + at, ld, t.Lk);
+  bv.load(v + at, ld, t.Lk);
   for (int j0 = 0; j0 < nk; j0 += TM) {
     __syncthreads();
-    const size_t at = ((size_t)(t.k0 + j0) * P.Hkv + hk) * D;
-    load_tile<D>(k + at, (size_t)P.Hkv * D, t.Lk - j0, tK, sK);
-    load_tile<D>(v + at, (size_t)P.Hkv * D, t.Lk - j0, tV, (float*)nullptr);
+    bk.store(tK, sK);
+    bv.store(tV, nullptr);
     __syncthreads();
-    float s[4][4], dp[4][4];
-    pairs<D>(tQ, tK, 4 * ty, 4 * tx, s);
-    pairs<D>(tG, tV, 4 * ty, 4 * tx, dp);
+    if (j0 + TM < nk) {
+      bk.load(k + at + (j0 + TM) * ld, ld, t.Lk - j0 - TM);
+      bv.load(v + at + (j0 + TM) * ld, ld, t.Lk - j0 - TM);
+    }
+    float s[R][4], dp[R][4];
+    pairs<D, R>(tQ, tK, R * ty, 4 * tx, s);
+    pairs<D, R>(tG, tV, R * ty, 4 * tx, dp);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      float d[4];
+      float d[R];
 #pragma unroll
-      for (int i = 0; i < 4; i++)
+      for (int i = 0; i < R; i++)
         d[i] = j0 + 4 * tx + j < lim[i] ? ex2(fmaf(s[i][j], P.scale2, -l2[i])) * (dp[i][j] - del[i]) : 0.f;
-      st4(sD + (4 * tx + j) * PP + 4 * ty, d);
+      put_column<R>(sD + (4 * tx + j) * PP<R> + R * ty, d);
     }
     __syncwarp();
-    apply<D>(sD, sK, 4 * ty, tx, acc);
+    apply<D, R>(sD, sK, R * ty, tx, acc);
   }
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int r = 4 * ty + i;
+  for (int i = 0; i < R; i++) {
+    const int r = R * ty + i;
     if (r >= nq) continue;
 #pragma unroll
     for (int c = 0; c < D / 64; c++) {
@@ -320,36 +380,33 @@ cudaError_t launch(int kid, void (*kern)(KArgs...), int64_t grid, size_t smem, c
   return e;
 }
 
-template <int D, typename T>
-cudaError_t fwd(const SmxP& P, const void* q, const void* k, const void* v, void* o, float* lse, cudaStream_t st) {
-  const size_t smem = (3 * D * TM + TM * PP) * sizeof(float);
-  return launch(K_SMX_FWD, smx_fwd_kernel<D, T>, (int64_t)max_tiles(P, 0) * P.Hq, smem, st, P, (const T*)q,
-                (const T*)k, (const T*)v, (T*)o, lse);
+template <int D>
+cudaError_t fwd(const SmxP& P, const float* q, const float* k, const float* v, float* o, float* lse, cudaStream_t st) {
+  constexpr int R = f32_rows(D, 0) / 16;
+  const size_t smem = (D * 16 * R + 2 * D * TM + TM * PP<R>) * sizeof(float);
+  return launch(K_SMX_FWD, smx_fwd_kernel<D, R>, (int64_t)max_tiles(P, 0) * P.Hq, smem, st, P, q, k, v, o, lse);
 }
-template <int D, typename T>
-cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, const void* dO, void* dq, void* dk,
-                void* dv, cudaStream_t st) {
-  const size_t s1 = (6 * D * TM + 2 * TM * PP + 2 * TM) * sizeof(float), s2 = (5 * D * TM + TM * PP) * sizeof(float);
-  cudaError_t e = launch(K_SMX_DKV, smx_dkv_kernel<D, T>, (int64_t)max_tiles(P, 2) * P.Hkv, s1, st, P, (const T*)q,
-                         (const T*)k, (const T*)v, (const T*)dO, (T*)dk, (T*)dv);
+template <int D>
+cudaError_t bwd(const SmxP& P, const float* q, const float* k, const float* v, const float* dO, float* dq, float* dk,
+                float* dv, cudaStream_t st) {
+  constexpr int RK = f32_rows(D, 2) / 16, RQ = f32_rows(D, 1) / 16;
+  const size_t s1 = (2 * D * 16 * RK + 4 * D * TM + TM * PP<RK> + 2 * TM) * sizeof(float);
+  const size_t s2 = (2 * D * 16 * RQ + 3 * D * TM + TM * PP<RQ>) * sizeof(float);
+  cudaError_t e = launch(K_SMX_DKV, smx_dkv_kernel<D, RK>, (int64_t)max_tiles(P, 2) * P.Hkv, s1, st, P, q, k, v, dO, dk,
+                         dv);
   if (e != cudaSuccess) return e;
-  return launch(K_SMX_DQ, smx_dq_kernel<D, T>, (int64_t)max_tiles(P, 1) * P.Hq, s2, st, P, (const T*)q, (const T*)k,
-                (const T*)v, (const T*)dO, (T*)dq);
+  return launch(K_SMX_DQ, smx_dq_kernel<D, RQ>, (int64_t)max_tiles(P, 1) * P.Hq, s2, st, P, q, k, v, dO, dq);
 }
 
 }  // namespace
 
-cudaError_t launch_f32_fwd(const SmxP& P, int D, int dtype, const void* q, const void* k, const void* v, void* o,
-                           float* lse, cudaStream_t st) {
-  if (dtype == KDA_F32)
-    return D == 64 ? fwd<64, float>(P, q, k, v, o, lse, st) : fwd<128, float>(P, q, k, v, o, lse, st);
-  return D == 64 ? fwd<64, bf16>(P, q, k, v, o, lse, st) : fwd<128, bf16>(P, q, k, v, o, lse, st);
+cudaError_t launch_f32_fwd(const SmxP& P, int D, const float* q, const float* k, const float* v, float* o, float* lse,
+                           cudaStream_t st) {
+  return D == 64 ? fwd<64>(P, q, k, v, o, lse, st) : fwd<128>(P, q, k, v, o, lse, st);
 }
-cudaError_t launch_f32_bwd(const SmxP& P, int D, int dtype, const void* q, const void* k, const void* v,
-                           const void* dO, void* dq, void* dk, void* dv, cudaStream_t st) {
-  if (dtype == KDA_F32)
-    return D == 64 ? bwd<64, float>(P, q, k, v, dO, dq, dk, dv, st) : bwd<128, float>(P, q, k, v, dO, dq, dk, dv, st);
-  return D == 64 ? bwd<64, bf16>(P, q, k, v, dO, dq, dk, dv, st) : bwd<128, bf16>(P, q, k, v, dO, dq, dk, dv, st);
+cudaError_t launch_f32_bwd(const SmxP& P, int D, const float* q, const float* k, const float* v, const float* dO,
+                           float* dq, float* dk, float* dv, cudaStream_t st) {
+  return D == 64 ? bwd<64>(P, q, k, v, dO, dq, dk, dv, st) : bwd<128>(P, q, k, v, dO, dq, dk, dv, st);
 }
 
 }  // namespace smx
