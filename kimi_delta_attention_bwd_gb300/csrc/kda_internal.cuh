@@ -52,6 +52,7 @@ enum KernelId {
   K_SMX_DQ,
   K_SMX_DECODE,
   K_SMX_JOIN,
+  K_SMX_SPLIT,
   K_ROTARY,
   K_COUNT
 };

@@ -170,7 +170,8 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   if (p->Hq > 4096 || p->Hq % p->Hkv != 0) return KDA_ERR_INVALID_ARG;
   const int64_t nq = (int64_t)p->B * p->T, nk = (int64_t)p->B * p->Tk;
   // (tile counts times heads fit a grid, and a tile's last row an int)
-  if (nq > ((int64_t)1 << 30) || nk > ((int64_t)1 << 30) || nq * p->Hq > ((int64_t)1 << 36) ||
+  const int64_t most = p->dtype == KDA_F32 ? (int64_t)1 << 29 : (int64_t)1 << 30;  // (three parts' rows in one map)
+  if (nq > most || nk > most || nq * p->Hq > ((int64_t)1 << 36) ||
       nk * p->Hkv > ((int64_t)1 << 36))
     return KDA_ERR_INVALID_ARG;
   if (p->D != 64 && p->D != 128) return KDA_ERR_UNSUPPORTED;
@@ -200,8 +201,8 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   P.causal = p->causal;
   P.scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D);
   P.scale2 = P.scale * LOG2E;
-  for (int l = 0; l < 3; l++)
-    P.tile[l] = p->dtype == KDA_F32 ? f32_rows(p->D, l) : l == 0 ? TC_FWD : TC_BWD;
+  const int parts = p->dtype == KDA_F32 ? 3 : 1;
+  for (int l = 0; l < 3; l++) P.tile[l] = parts == 3 && p->D == 128 && l > 0 ? F32_TILE : tc_tile(p->D, parts, l);
   uint32_t tag = 0x536d61u;
   for (const int32_t v : {P.B, P.T, P.Tk, P.Hq, P.Hkv, p->D, p->dtype, P.causal, P.n_docs, P.rows,
                           (int32_t)(p->cu_seqlens_k != nullptr)})
@@ -236,6 +237,13 @@ size_t layout(SmxP& P, int D, int dtype, bool bwd, void* base) {
     P.lse2 = (float*)(w + take((size_t)P.Hq * P.Nq * sizeof(float)));
     P.delta = (float*)(w + take((size_t)P.Hq * P.Nq * sizeof(float)));
     if (dtype == KDA_BF16) P.res = (bf16*)(w + take((size_t)P.Nq * P.Hq * D * sizeof(bf16)));
+  }
+  if (dtype == KDA_F32) {
+    const size_t nq = 3 * (size_t)P.Nq * P.Hq * D * sizeof(bf16), nk = 3 * (size_t)P.Nk * P.Hkv * D * sizeof(bf16);
+    P.pq = (bf16*)(w + take(nq));
+    P.pk = (bf16*)(w + take(nk));
+    P.pv = (bf16*)(w + take(nk));
+    if (bwd && D == 64) P.pg = (bf16*)(w + take(nq));
   }
   return o;
 }
@@ -283,9 +291,16 @@ extern "C" KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, cons
   if (!workspace || workspace_bytes < layout(P, p->D, p->dtype, P.save, workspace)) return KDA_ERR_WORKSPACE;
   if ((uintptr_t)workspace % 256 != 0) return KDA_ERR_ALIGNMENT;
   if (!P.rows && launch_table(P, 0, 1, st) != cudaSuccess) return KDA_ERR_CUDA;
-  const cudaError_t e = p->dtype == KDA_BF16 ? launch_tc_fwd(P, p->D, q, k, v, o, lse, st)
-                                             : launch_f32_fwd(P, p->D, (const float*)q, (const float*)k, (const float*)v,
-                                                              (float*)o, lse, st);
+  cudaError_t e;
+  if (p->dtype == KDA_F32) {
+    const float* x[3] = {(const float*)q, (const float*)k, (const float*)v};
+    bf16* const parts[3] = {P.pq, P.pk, P.pv};
+    const int64_t nk = (int64_t)P.Nk * P.Hkv * p->D, n[3] = {(int64_t)P.Nq * P.Hq * p->D, nk, nk};
+    e = launch_split(3, x, parts, n, st);
+    if (e == cudaSuccess) e = launch_tc_fwd(P, p->D, 3, P.pq, P.pk, P.pv, o, lse, st);
+  } else {
+    e = launch_tc_fwd(P, p->D, 1, q, k, v, o, lse, st);
+  }
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -307,8 +322,17 @@ extern "C" KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, cons
   else
     e = p->D == 64 ? launch_delta<64, bf16>(P, o, dO, st) : launch_delta<128, bf16>(P, o, dO, st);
   if (e != cudaSuccess) return KDA_ERR_CUDA;
-  e = p->dtype == KDA_BF16 ? launch_tc_bwd(P, p->D, q, k, v, dO, dq, dk, dv, st)
-                           : launch_f32_bwd(P, p->D, (const float*)q, (const float*)k, (const float*)v, (const float*)dO,
-                                            (float*)dq, (float*)dk, (float*)dv, st);
+  if (p->dtype == KDA_BF16) {
+    e = launch_tc_bwd(P, p->D, 1, q, k, v, dO, dq, dk, dv, st);
+  } else if (p->D == 64) {
+    const float* x[1] = {(const float*)dO};
+    bf16* const parts[1] = {P.pg};
+    const int64_t n[1] = {(int64_t)P.Nq * P.Hq * p->D};
+    e = launch_split(1, x, parts, n, st);
+    if (e == cudaSuccess) e = launch_tc_bwd(P, 64, 3, P.pq, P.pk, P.pv, P.pg, dq, dk, dv, st);
+  } else {
+    e = launch_f32_bwd(P, (const float*)q, (const float*)k, (const float*)v, (const float*)dO, (float*)dq, (float*)dk,
+                       (float*)dv, st);
+  }
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -1,6 +1,6 @@
 // Softmax attention with grouped heads: declarations shared by its kernels
-// (tables and entries: kda_softmax.cu, bf16: kda_softmax_tc.cu, fp32:
-// kda_softmax_f32.cu).
+// (tables and entries: kda_softmax.cu, tensor cores: kda_softmax_tc.cu, fp32
+// pipe: kda_softmax_f32.cu).
 #pragma once
 #include "kda_internal.cuh"
 #include "../../include/kda.h"
@@ -22,6 +22,7 @@ struct SmxP {
   int tile[3];                   // rows a tile
   float *lse2, *delta;           // [Hq][Nq]: log2 of the rows' sums, saved by the forward; sum_d o dO
   bf16* res;                     // [Nq, Hq, D] what rounding o to bf16 left, saved by the forward
+  bf16 *pq, *pk, *pv, *pg;       // fp32 io: parts of q, k, v (the forward's) and dO
 };
 
 // Rows t * tile .. of a document's queries (or keys): its first query, queries, first key, keys.
@@ -70,19 +71,20 @@ __device__ __forceinline__ bool saved(const SmxP& P) {
   return false;
 }
 
-// fp32 io: rows of list l's tiles (128 where shared memory holds them).
-constexpr int f32_rows(int D, int l) { return D == 64 || l == 0 ? 128 : 64; }
-cudaError_t launch_f32_fwd(const SmxP& P, int D, const float* q, const float* k, const float* v, float* o, float* lse,
-                           cudaStream_t st);
-cudaError_t launch_f32_bwd(const SmxP& P, int D, const float* q, const float* k, const float* v, const float* dO,
-                           float* dq, float* dk, float* dv, cudaStream_t st);
+// Tensor-core kernels.  parts = 1: bf16 io; 3: fp32 io, its inputs as three bf16 arrays one behind the other
+// (launch_split), the backward at D = 64 only.  Rows of list l's tiles: tc_tile.
+constexpr int tc_tile(int D, int parts, int l) { return l > 0 || (parts == 3 && D == 128) ? 128 : 256; }
+cudaError_t launch_tc_fwd(const SmxP& P, int D, int parts, const void* q, const void* k, const void* v, void* o,
+                          float* lse, cudaStream_t st);
+cudaError_t launch_tc_bwd(const SmxP& P, int D, int parts, const void* q, const void* k, const void* v, const void* dO,
+                          void* dq, void* dk, void* dv, cudaStream_t st);
+// Up to three fp32 arrays (their sizes multiples of 8) into their parts.
+cudaError_t launch_split(int n, const float* const* x, bf16* const* parts, const int64_t* values, cudaStream_t st);
 
-// bf16 io: tiles of 256 queries (forward), 128 queries and 128 keys (backward).
-constexpr int TC_FWD = 256, TC_BWD = 128;
-cudaError_t launch_tc_fwd(const SmxP& P, int D, const void* q, const void* k, const void* v, void* o, float* lse,
-                          cudaStream_t st);
-cudaError_t launch_tc_bwd(const SmxP& P, int D, const void* q, const void* k, const void* v, const void* dO, void* dq,
-                          void* dk, void* dv, cudaStream_t st);
+// The backward of fp32 io at D = 128, on the fp32 pipe: tiles of 64 rows.
+constexpr int F32_TILE = 64;
+cudaError_t launch_f32_bwd(const SmxP& P, const float* q, const float* k, const float* v, const float* dO, float* dq,
+                           float* dk, float* dv, cudaStream_t st);
 
 // Upper bound on the tiles of list l.
 inline int max_tiles(const SmxP& P, int l) {

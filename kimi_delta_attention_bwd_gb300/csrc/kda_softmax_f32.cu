@@ -1,15 +1,14 @@
-// Softmax attention for fp32 io, on the fp32 pipe.
-// Per document, query head h and its key head h / G:
-//   s_ij = scale q_i k_j,  p_ij = exp(s_ij - lse_i),  o_i = sum_j p_ij v_j
-//   dv_j = sum_i p_ij dO_i,  ds_ij = p_ij (dO_i v_j - delta_i),  delta_i = o_i dO_i
+// Softmax attention, the backward of fp32 io at D = 128, on the fp32 pipe (the other
+// fp32 passes run on the tensor cores in three bf16 parts; here both own blocks in three
+// parts would fill shared memory).  Per document, query head h and its key head h / G:
+//   p_ij = exp(scale q_i k_j - lse_i),  dv_j = sum_i p_ij dO_i
+//   ds_ij = p_ij (dO_i v_j - delta_i),  delta_i = o_i dO_i
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
 // Tiles of 16 R own rows by 64 of the other side, 256 threads with R x 4 pairs each;
 // operands of the pair products lie transposed in shared memory ([d][row]) so that a
-// thread's rows are one or two 16-byte loads.  R = 8 where shared memory holds it (32
-// products for three loads; R = 4, 16 for two, took XX times as long), the next block's values are
-// on their way to registers meanwhile.  The forward keeps a running maximum and sum per row.  dk
-// and dv of a key tile are summed by one CTA over the queries of its whole head
-// group, dq by one CTA over the keys: no atomics, a fixed order.
+// thread's rows are one 16-byte load; the next block's values are on their way to
+// registers meanwhile.  dk and dv of a key tile are summed by one CTA over the queries
+// of its whole head group, dq by one CTA over the keys: no atomics, a fixed order.
 #include "kda_softmax.cuh"
 
 namespace kda {
@@ -99,104 +98,6 @@ template <int R>
 __device__ __forceinline__ void put_column(float* dst, const float (&v)[R]) {
 #pragma unroll
   for (int i = 0; i < R; i += 4) st4(dst + i, v + i);
-}
-
-template <int D, int R>
-__global__ void __launch_bounds__(NT) smx_fwd_kernel(SmxP P, const float* __restrict__ q, const float* __restrict__ k,
-                                                    const float* __restrict__ v, float* __restrict__ o,
-                                                    float* __restrict__ lse) {
-  constexpr int OWN = 16 * R;
-  extern __shared__ __align__(16) float sm[];
-  float *sQ = sm, *sK = sQ + D * OWN, *sV = sK + D * TM, *sP = sV + D * TM;
-  pdl_wait();
-  if (P.rows && blockIdx.x == 0 && threadIdx.x == 0) {
-    *P.err = KDA_OK;
-    *P.wtag = P.save ? P.tag : 0;
-  }
-  const int h = blockIdx.x % P.Hq, hk = h / P.G, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  Tile t;
-  if (!tile_of(P, 0, blockIdx.x / P.Hq, false, t)) return;
-  const int i0 = t.t * OWN, nq = min(OWN, t.Lq - i0);
-  {
-    Block<D, OWN> b;
-    b.load(q + ((size_t)(t.q0 + i0) * P.Hq + h) * D, (size_t)P.Hq * D, nq);
-    b.store(sQ, nullptr);
-  }
-  float acc[R][D / 16] = {}, m[R], l[R];
-  int lim[R];
-#pragma unroll
-  for (int i = 0; i < R; i++) {
-    m[i] = -INFINITY;
-    l[i] = 0.f;
-    lim[i] = keys_of(P.causal, i0 + R * ty + i, t.Lq, t.Lk);
-  }
-  const int nk = keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk);
-  const size_t ld = (size_t)P.Hkv * D, at = ((size_t)t.k0 * P.Hkv + hk) * D;
-  Block<D, TM> bk, bv;
-  bk.load(k + at, ld, t.Lk);
-  bv.load(v + at, ld, t.Lk);
-  for (int j0 = 0; j0 < nk; j0 += TM) {
-    __syncthreads();
-    bk.store(sK, nullptr);
-    bv.store(nullptr, sV);
-    __syncthreads();
-    if (j0 + TM < nk) {
-      bk.load(k + at + (j0 + TM) * ld, ld, t.Lk - j0 - TM);
-      bv.load(v + at + (j0 + TM) * ld, ld, t.Lk - j0 - TM);
-    }
-    float s[R][4];
-    pairs<D, R>(sQ, sK, R * ty, 4 * tx, s);
-#pragma unroll
-    for (int i = 0; i < R; i++) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        s[i][j] = j0 + 4 * tx + j < lim[i] ? s[i][j] * P.scale2 : -INFINITY;
-        mx = fmaxf(mx, s[i][j]);
-      }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-      const float mn = fmaxf(m[i], mx), mu = mn == -INFINITY ? 0.f : mn, c = ex2(m[i] - mu);
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        s[i][j] = ex2(s[i][j] - mu);
-        sum += s[i][j];
-      }
-      l[i] = l[i] * c + sum;
-      m[i] = mn;
-#pragma unroll
-      for (int e = 0; e < D / 16; e++) acc[i][e] *= c;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      float col[R];
-#pragma unroll
-      for (int i = 0; i < R; i++) col[i] = s[i][j];
-      put_column<R>(sP + (4 * tx + j) * PP<R> + R * ty, col);
-    }
-    __syncwarp();  // a row's pairs are formed and used by one half warp
-    apply<D, R>(sP, sV, R * ty, tx, acc);
-  }
-#pragma unroll
-  for (int i = 0; i < R; i++) {
-#pragma unroll
-    for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-    const int r = R * ty + i;
-    if (r >= nq) continue;
-    const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i], l2 = m[i] + log2f(l[i]);
-    const size_t row = (size_t)(t.q0 + i0 + r) * P.Hq + h;
-#pragma unroll
-    for (int c = 0; c < D / 64; c++) {
-      const float y[4] = {acc[i][4 * c] * inv, acc[i][4 * c + 1] * inv, acc[i][4 * c + 2] * inv,
-                          acc[i][4 * c + 3] * inv};
-      st4(o + row * D + 64 * c + 4 * tx, y);
-    }
-    if (tx == 0) {
-      lse[row] = l2 * LN2;
-      if (P.save) P.lse2[(size_t)h * P.Nq + t.q0 + i0 + r] = l2;
-    }
-  }
 }
 
 // dk and dv of 16 R keys of one key head.  Threads: keys R ty .., queries 4 tx ..
@@ -380,33 +281,16 @@ cudaError_t launch(int kid, void (*kern)(KArgs...), int64_t grid, size_t smem, c
   return e;
 }
 
-template <int D>
-cudaError_t fwd(const SmxP& P, const float* q, const float* k, const float* v, float* o, float* lse, cudaStream_t st) {
-  constexpr int R = f32_rows(D, 0) / 16;
-  const size_t smem = (D * 16 * R + 2 * D * TM + TM * PP<R>) * sizeof(float);
-  return launch(K_SMX_FWD, smx_fwd_kernel<D, R>, (int64_t)max_tiles(P, 0) * P.Hq, smem, st, P, q, k, v, o, lse);
-}
-template <int D>
-cudaError_t bwd(const SmxP& P, const float* q, const float* k, const float* v, const float* dO, float* dq, float* dk,
-                float* dv, cudaStream_t st) {
-  constexpr int RK = f32_rows(D, 2) / 16, RQ = f32_rows(D, 1) / 16;
-  const size_t s1 = (2 * D * 16 * RK + 4 * D * TM + TM * PP<RK> + 2 * TM) * sizeof(float);
-  const size_t s2 = (2 * D * 16 * RQ + 3 * D * TM + TM * PP<RQ>) * sizeof(float);
-  cudaError_t e = launch(K_SMX_DKV, smx_dkv_kernel<D, RK>, (int64_t)max_tiles(P, 2) * P.Hkv, s1, st, P, q, k, v, dO, dk,
-                         dv);
-  if (e != cudaSuccess) return e;
-  return launch(K_SMX_DQ, smx_dq_kernel<D, RQ>, (int64_t)max_tiles(P, 1) * P.Hq, s2, st, P, q, k, v, dO, dq);
-}
-
 }  // namespace
 
-cudaError_t launch_f32_fwd(const SmxP& P, int D, const float* q, const float* k, const float* v, float* o, float* lse,
-                           cudaStream_t st) {
-  return D == 64 ? fwd<64>(P, q, k, v, o, lse, st) : fwd<128>(P, q, k, v, o, lse, st);
-}
-cudaError_t launch_f32_bwd(const SmxP& P, int D, const float* q, const float* k, const float* v, const float* dO,
-                           float* dq, float* dk, float* dv, cudaStream_t st) {
-  return D == 64 ? bwd<64>(P, q, k, v, dO, dq, dk, dv, st) : bwd<128>(P, q, k, v, dO, dq, dk, dv, st);
+cudaError_t launch_f32_bwd(const SmxP& P, const float* q, const float* k, const float* v, const float* dO, float* dq,
+                           float* dk, float* dv, cudaStream_t st) {
+  constexpr int D = 128, R = F32_TILE / 16;
+  const size_t s1 = (2 * D * 16 * R + 4 * D * TM + TM * PP<R> + 2 * TM) * sizeof(float);
+  const size_t s2 = (2 * D * 16 * R + 3 * D * TM + TM * PP<R>) * sizeof(float);
+  cudaError_t e = launch(K_SMX_DKV, smx_dkv_kernel<D, R>, (int64_t)max_tiles(P, 2) * P.Hkv, s1, st, P, q, k, v, dO, dk, dv);
+  if (e != cudaSuccess) return e;
+  return launch(K_SMX_DQ, smx_dq_kernel<D, R>, (int64_t)max_tiles(P, 1) * P.Hq, s2, st, P, q, k, v, dO, dq);
 }
 
 }  // namespace smx

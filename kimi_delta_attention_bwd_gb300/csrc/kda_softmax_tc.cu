@@ -29,7 +29,7 @@ __device__ __forceinline__ uint32_t tm_base(uint32_t slot) {
 }
 
 // ------------------------------------------------------------ helpers
-// Descriptors of a block of 128 rows in 128-byte swizzled halves of 64 columns (TMA's layout): 8-row groups 1024 bytes apart.
+// Descriptors of a block of rows in 128-byte swizzled halves of 64 columns (TMA's layout): 8-row groups 1024 bytes apart.
 // K-major (rows are M or N): 16 columns of the contraction are 32 bytes of the swizzled row.  MN-major (rows are the
 // contraction): 16 rows are 2048 bytes, and the next 64 columns are a half away.
 //
@@ -39,11 +39,13 @@ __device__ __forceinline__ uint32_t tm_base(uint32_t slot) {
 __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo) {
   return (uint64_t)((addr >> 4) | (lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61);
 }
+template <int ROWS>
 __device__ __forceinline__ uint64_t desc_k(uint32_t block, int step) {  // columns 16 step ..
-  return sdesc(block + (step >> 2) * HALF + (step & 3) * 32, 16);
+  return sdesc(block + (step >> 2) * (ROWS * 128) + (step & 3) * 32, 16);
 }
+template <int ROWS>
 __device__ __forceinline__ uint64_t desc_mn(uint32_t block, int step) {  // rows 16 step ..
-  return sdesc(block + step * 2048, HALF);
+  return sdesc(block + step * 2048, ROWS * 128);
 }
 constexpr uint32_t idesc(int M, int N, bool b_mn) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)b_mn << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
@@ -145,6 +147,15 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 }
 __device__ __forceinline__ float low(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float high(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+// The second (y = 1) or third bf16 parts of two floats.
+__device__ __forceinline__ uint32_t rest(float a, float b, int y) {
+  for (int i = 0; i < y; i++) {
+    const uint32_t u = pack(a, b);
+    a -= low(u);
+    b -= high(u);
+  }
+  return pack(a, b);
+}
 
 // Whole-warp wait on a barrier's phase; gives up (and lets every other wait of the CTA give up) after mma::WAIT_POLLS.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead) {
@@ -215,10 +226,11 @@ __device__ __forceinline__ void second_parts(const float (&v)[N], uint32_t* w) {
   }
 }
 
-// 64 columns (u: 32 bf16 pairs of this lane's row) of a warp's 32 rows to global memory, through 4 KB of shared memory
-// of its own (rows of 128 bytes, 16-byte pieces swizzled): a lane's row alone would make every store 32 half sectors.
+// 128 bytes (u: 64 bf16 or 32 fp32 values of this lane's row) of each of a warp's 32 rows to global memory, through 4 KB
+// of shared memory of its own (16-byte pieces swizzled): a lane's row alone would make every store 32 half sectors.
 // The first n rows are stored; dst is the warp's first row, ld elements a row.
-__device__ __forceinline__ void store_rows(unsigned char* buf, const uint32_t (&u)[32], bf16* dst, size_t ld, int n) {
+template <typename T>
+__device__ __forceinline__ void store_rows(unsigned char* buf, const uint32_t (&u)[32], T* dst, size_t ld, int n) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c = 0; c < 8; c++)
@@ -229,13 +241,13 @@ __device__ __forceinline__ void store_rows(unsigned char* buf, const uint32_t (&
   for (int i = 0; i < 8; i++) {
     const int r = 4 * i + lane / 8, c = lane & 7;
     const uint4 x = *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
-    if (r < n) *reinterpret_cast<uint4*>(dst + r * ld + 8 * c) = x;
+    if (r < n) *reinterpret_cast<uint4*>(dst + r * ld + 16 / sizeof(T) * c) = x;
   }
   __syncwarp();
 }
-// 64 columns of an accumulator, times f, as bf16 (zeros where nothing was accumulated).
-__device__ __forceinline__ void store_acc(unsigned char* buf, uint32_t tm, bool any, float f, bf16* dst, size_t ld,
-                                          int n) {
+// 64 columns of an accumulator, times f (zeros where nothing was accumulated).
+template <typename T>
+__device__ __forceinline__ void store_acc(unsigned char* buf, uint32_t tm, bool any, float f, T* dst, size_t ld, int n) {
   uint32_t u[32];
 #pragma unroll
   for (int c = 0; c < 2; c++) {
@@ -244,49 +256,106 @@ __device__ __forceinline__ void store_acc(unsigned char* buf, uint32_t tm, bool 
       tm_ld32(tm + 32 * c, v);
       tm_wait_ld(v);
     }
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int e = 0; e < 16; e++) u[16 * c + e] = any ? pack(v[2 * e] * f, v[2 * e + 1] * f) : 0u;
+      for (int e = 0; e < 16; e++) u[16 * c + e] = any ? pack(v[2 * e] * f, v[2 * e + 1] * f) : 0u;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; e++) u[e] = any ? __float_as_uint(v[e] * f) : 0u;
+      store_rows(buf, u, dst + 32 * c, ld, n);
+    }
   }
-  store_rows(buf, u, dst, ld, n);
+  if constexpr (sizeof(T) == 2) store_rows(buf, u, dst, ld, n);
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
 }
 
-// Rows n .. of a block (other documents' tokens) become zeros, by one warp, before products read them.
-template <int D, int ROWS>
+// A block in shared memory: PARTS arrays (below) of ROWS rows by D columns, each in halves of 64 columns.
+// Its rows from n on (other documents' tokens) become zeros, by one warp, before products read them.
+template <int D, int ROWS, int PARTS>
 __device__ __forceinline__ void zero_rows(unsigned char* block, int n) {
-  static_assert(D == 64 || ROWS == BLK, "the second half of the columns lies HALF bytes further");
-  for (int i = threadIdx.x & 31; i < (ROWS - n) * 8 * (D / 64); i += 32) {
-    const int half = i / ((ROWS - n) * 8), r = i % ((ROWS - n) * 8);
-    *reinterpret_cast<uint4*>(block + half * HALF + n * 128 + r * 16) = make_uint4(0, 0, 0, 0);
-  }
+  for (int i = threadIdx.x & 31; i < (ROWS - n) * 8; i += 32)
+#pragma unroll
+    for (int c = 0; c < D / 64 * PARTS; c++)
+      *reinterpret_cast<uint4*>(block + (c * ROWS + n) * 128 + i * 16) = make_uint4(0, 0, 0, 0);
   mma::fence_async_smem();
   __syncwarp();
 }
-template <int D>
-__device__ __forceinline__ void load_block(unsigned char* dst, const CUtensorMap* map, int head, int row,
+// Its load; the parts lie `stride` rows apart in the map.
+template <int D, int ROWS, int PARTS>
+__device__ __forceinline__ void load_block(unsigned char* dst, const CUtensorMap* map, int head, int row, int stride,
                                            uint64_t* bar) {
 #pragma unroll
-  for (int c = 0; c < D / 64; c++) mma::tma_load_2d(dst + c * HALF, map, head * D + 64 * c, row, bar);
+  for (int p = 0; p < PARTS; p++)
+#pragma unroll
+    for (int c = 0; c < D / 64; c++)
+      mma::tma_load_2d(dst + (p * (D / 64) + c) * (ROWS * 128), map, head * D + 64 * c, row + p * stride, bar);
 }
+
+// fp32 io comes as three bf16 parts of every value (x = x0 + x1 + x2 to 2^-24), and a product is the six products of
+// parts above that: bytes and time of six, and the fp32 pipe's precision.  Smallest first.
+template <int PARTS>
+struct Prod {
+  static constexpr int N = 1;
+  static __device__ constexpr int a(int) { return 0; }
+  static __device__ constexpr int b(int) { return 0; }
+};
+template <>
+struct Prod<3> {
+  static constexpr int N = 6;
+  static __device__ constexpr int a(int i) { return i == 0 ? 0 : i == 1 ? 2 : i == 2 ? 1 : i == 3 ? 0 : i == 4 ? 1 : 0; }
+  static __device__ constexpr int b(int i) { return i == 0 ? 2 : i == 1 ? 0 : i == 2 ? 1 : i == 3 ? 1 : 0; }
+};
+// d = A B^T over D columns, both K-major blocks
+template <int D, int PARTS, int RA, int RB>
+__device__ __forceinline__ void prod_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t me) {
+  using Q = Prod<PARTS>;
+#pragma unroll
+  for (int i = 0; i < Q::N; i++)
+#pragma unroll
+    for (int s = 0; s < D / 16; s++)
+      mma_ss(d, desc_k<RA>(a + Q::a(i) * (RA * D * 2), s), desc_k<RB>(b + Q::b(i) * (RB * D * 2), s), id, i > 0 || s > 0,
+             me);
+}
+// Three parts of 2 n floats as bf16 pairs, taken off v one by one.
+template <int N>
+__device__ __forceinline__ void next_part(float (&v)[N], uint32_t* w) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    const uint32_t u = pack(v[e], v[e + 1]);
+    w[e / 2] = u;
+    v[e] -= low(u);
+    v[e + 1] -= high(u);
+  }
+}
+template <int PARTS>
+struct Io {
+  using T = bf16;
+};
+template <>
+struct Io<3> {
+  using T = float;
+};
 
 // ------------------------------------------------------------ forward
 // A CTA has two tiles that share every block of keys and values.  At D = 128 the products bound it, with one CTA per SM
 // and blocks of 128 keys.  At D = 64 they are half of that, and the exponentials and the waits between the steps count:
 // blocks of 64 keys let two CTAs share an SM (256 columns of tensor memory, 80 registers a thread), so that four tiles'
 // steps hide each other (300M batch: 88 us; with tiles and blocks as at D = 128 116 us, two CTAs of one tile 104).
-template <int D>
+// fp32 io (three parts a value): blocks of 64 keys, one CTA per SM, at D = 128 of one tile.
+template <int D, int PARTS>
 struct Fwd {
-  static constexpr int NT = 2, XB = D == 64 ? 64 : 128;
-  static constexpr int OWN = HALF * (D / 64), BYTES = OWN / BLK * XB;  // a tile of queries, a block of keys or values
-  static constexpr int STAGES = D == 64 ? 8 : 5;                       // blocks in their ring
+  static constexpr int NT = D == 128 && PARTS == 3 ? 1 : 2, XB = D == 64 || PARTS == 3 ? 64 : 128;
+  static constexpr int OWN = BLK * D * 2 * PARTS, BYTES = XB * D * 2 * PARTS;  // a tile of queries, a block of keys or values
+  static constexpr int STAGES = PARTS == 3 ? (D == 64 ? 5 : 2) : D == 64 ? 8 : 5;  // blocks in their ring
   static constexpr int SMEM = NT * OWN + STAGES * BYTES + 1024;
-  static constexpr int COLS = D == 64 ? 256 : 512;
-  static constexpr uint32_t S0 = 0, O0 = NT * XB;  // tensor memory columns: S of the tiles, o of the tiles
+  static constexpr int COLS = D == 64 && PARTS == 1 ? 256 : 512, PER_SM = COLS == 256 ? 2 : 1;
+  // tensor memory columns: S of the tiles, o of the tiles, third parts of the weights
+  static constexpr uint32_t S0 = 0, O0 = NT * XB, X0 = O0 + NT * D;
   // Weights lie over the logits they come from: those of 16 keys at part(s), their second parts SECOND further.
-  static constexpr int SECOND = D == 64 ? 8 : 16;
-  static __device__ constexpr int part(int s) { return D == 64 ? 16 * s : 32 * (s >> 1) + 8 * (s & 1); }
+  static constexpr int SECOND = XB == 64 ? 8 : 16;
+  static __device__ constexpr int part(int s) { return XB == 64 ? 16 * s : 32 * (s >> 1) + 8 * (s & 1); }
   static constexpr int THREADS = NT * BLK + 64;
 };
 
@@ -296,11 +365,12 @@ struct FwdBars {
   int dead;
 };
 
-template <int D>
-__global__ void __launch_bounds__(Fwd<D>::THREADS, D == 64 ? 2 : 1)
+template <int D, int PARTS>
+__global__ void __launch_bounds__(Fwd<D, PARTS>::THREADS, Fwd<D, PARTS>::PER_SM)
 smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                  const __grid_constant__ CUtensorMap mv, bf16* __restrict__ o, float* __restrict__ lse) {
-  using F = Fwd<D>;
+                  const __grid_constant__ CUtensorMap mv, typename Io<PARTS>::T* __restrict__ o,
+                  float* __restrict__ lse) {
+  using F = Fwd<D, PARTS>;
   constexpr int NT = F::NT, XB = F::XB, W_MMA = 4 * NT, W_LOAD = W_MMA + 1;
   extern __shared__ unsigned char raw[];
   __shared__ FwdBars B;
@@ -358,7 +428,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       for (int i = 0; i < NT; i++)
         if (nb[i]) {
           mma::mbar_expect_tx(&B.q[i], F::OWN);
-          load_block<D>(sm + i * F::OWN, &mq, h, t.q0 + i0 + i * BLK, &B.q[i]);
+          load_block<D, BLK, PARTS>(sm + i * F::OWN, &mq, h, t.q0 + i0 + i * BLK, P.Nq, &B.q[i]);
         }
     }
     __syncwarp();
@@ -368,7 +438,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       if (r > 0 && !wait(&B.empty[s], (r - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.full[s], F::BYTES);
-        load_block<D>(ring + s * F::BYTES, x & 1 ? &mv : &mk, hk, t.k0 + x / 2 * XB, &B.full[s]);
+        load_block<D, XB, PARTS>(ring + s * F::BYTES, x & 1 ? &mv : &mk, hk, t.k0 + x / 2 * XB, P.Nk, &B.full[s]);
       }
       __syncwarp();
     }
@@ -384,9 +454,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     constexpr uint32_t id_s = idesc(BLK, XB, false), id_o = idesc(BLK, D, true);
     const uint32_t me = elect();
     auto logits = [&](int i, int j) {  // S of tile i and key block j
-      const uint32_t kb = r0 + 2 * j % F::STAGES * F::BYTES, qb = q0 + i * F::OWN, d = tm + F::S0 + i * XB;
-#pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(d, desc_k(qb, s), desc_k(kb, s), id_s, s > 0, me);
+      prod_ss<D, PARTS, BLK, XB>(tm + F::S0 + i * XB, q0 + i * F::OWN, r0 + 2 * j % F::STAGES * F::BYTES, id_s, me);
       commit(&B.s[i], me);
     };
     auto run = [&]() -> bool {
@@ -401,7 +469,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       for (int j = 0; j < n; j++) {
         const int xv = 2 * j + 1, xk = 2 * j + 2, sv = xv % F::STAGES, sk = xk % F::STAGES;
         if (!wait(&B.full[sv], (xv / F::STAGES) & 1, &B.dead)) return false;
-        if (t.Lk - j * XB < XB) zero_rows<D, XB>(ring + sv * F::BYTES, t.Lk - j * XB);
+        if (t.Lk - j * XB < XB) zero_rows<D, XB, PARTS>(ring + sv * F::BYTES, t.Lk - j * XB);
         if (j + 1 < n && !wait(&B.full[sk], (xk / F::STAGES) & 1, &B.dead)) return false;
         const uint32_t vb = r0 + sv * F::BYTES;
 #pragma unroll
@@ -409,12 +477,18 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
           if (j >= nb[i]) continue;
           if (!wait(&B.p[i], j & 1, &B.dead)) return false;
           tc::fence_after();
-          const uint32_t a = tm + F::S0 + i * XB, d = tm + F::O0 + i * D;
+          const uint32_t a = tm + F::S0 + i * XB, d = tm + F::O0 + i * D, c = tm + F::X0 + i * (XB / 2);
+          using Q = Prod<PARTS>;
 #pragma unroll
-          for (int s = 0; s < XB / 16; s++) mma_ts(d, a + F::part(s), desc_mn(vb, s), id_o, j > 0 || s > 0, me);
-          if (j == 0 && clean[i] == 0)
+          for (int y = 0; y < Q::N; y++)
 #pragma unroll
-            for (int s = 0; s < XB / 16; s++) mma_ts(d, a + F::part(s) + F::SECOND, desc_mn(vb, s), id_o, true, me);
+            for (int s = 0; s < XB / 16; s++)
+              mma_ts(d, Q::a(y) == 2 ? c + 8 * s : a + F::part(s) + Q::a(y) * F::SECOND,
+                     desc_mn<XB>(vb + Q::b(y) * (XB * D * 2), s), id_o, j > 0 || y > 0 || s > 0, me);
+          if (PARTS == 1 && j == 0 && clean[i] == 0)
+#pragma unroll
+            for (int s = 0; s < XB / 16; s++)
+              mma_ts(d, a + F::part(s) + F::SECOND, desc_mn<XB>(vb, s), id_o, true, me);
           commit(&B.o[i], me);
           if (i == NT - 1 || j >= nb[1]) commit(&B.empty[sv], me);
           if (j + 1 < nb[i]) logits(i, j + 1);
@@ -467,7 +541,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       const int left = lim - j * XB, least = cut ? __shfl_sync(0xffffffffu, left, 0) : XB;  // (the warp's first row's)
       uint64_t sum[2] = {0, 0};
       float s0, s1;
-      if constexpr (D == 128) {
+      if constexpr (XB == 128) {
         float s[4][32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 4; c++) tm_ld32(ts + 32 * c, s[c]);
@@ -496,8 +570,8 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
         // The weights against the reference as it is: a row's sum of at most 2^GROW says that none is above it, and the
         // maximum need not be known.  Else, and in the first block, the maximum first (a NaN row: every time).
         float a[16], b[16];
-        bool ask = false, again = j == 0;
-        if (!again) {
+        bool ask = false, again = j == 0 || PARTS == 3;
+        if (PARTS == 1 && !again) {
           const float neg = reference();
           const uint64_t ng = two(neg, neg);
           uint32_t w[32];
@@ -545,10 +619,19 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
             tm_wait_ld(a);
             if (least < 16 * (c + 1)) mask(a, left - 16 * c);
             weights(a, sc, ng, sum, w);
-            tm_st8(ts + 16 * c, w);
-            if (few) {
-              second_parts(a, w);
+            if (PARTS == 3) {
+              next_part(a, w);
+              tm_st8(ts + 16 * c, w);
+              next_part(a, w);
               tm_st8(ts + 16 * c + 8, w);
+              next_part(a, w);
+              tm_st8(tm + F::X0 + i * (XB / 2) + lanes + 8 * c, w);
+            } else {
+              tm_st8(ts + 16 * c, w);
+              if (few) {
+                second_parts(a, w);
+                tm_st8(ts + 16 * c + 8, w);
+              }
             }
           }
         }
@@ -569,25 +652,38 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       const int w0 = r & ~31, rows = nq - w0;  // the warp's first row, rows from there on
       const size_t row = (size_t)(t.q0 + i0 + r) * P.Hq + h, row0 = (size_t)(t.q0 + i0 + w0) * P.Hq + h;
       unsigned char* buf = sm + i * F::OWN + (w0 & 127) * 128;  // (the tile's queries are no longer read)
-#pragma unroll
-      for (int c = 0; c < D; c += 64) {
-        uint32_t u[32], w[32];  // o, and what its rounding leaves
-#pragma unroll
-        for (int y = 0; y < 2; y++) {
-          float v[32];
-          if (nbi > 0) {
-            tm_ld32(to + c + 32 * y, v);
-            tm_wait_ld(v);
-          }
-#pragma unroll
-          for (int e = 0; e < 16; e++) {
-            const float a = l == 0.f ? 0.f : v[2 * e] * inv, b = l == 0.f ? 0.f : v[2 * e + 1] * inv;
-            u[16 * y + e] = pack(a, b);
-            w[16 * y + e] = pack(a - low(u[16 * y + e]), b - high(u[16 * y + e]));
-          }
+      auto take = [&](int c, float (&v)[32]) {  // columns c .. of o
+        if (nbi > 0) {
+          tm_ld32(to + c, v);
+          tm_wait_ld(v);
         }
-        store_rows(buf, u, o + row0 * D + c, (size_t)P.Hq * D, rows);
-        if (P.save) store_rows(buf, w, P.res + row0 * D + c, (size_t)P.Hq * D, rows);
+#pragma unroll
+        for (int e = 0; e < 32; e++) v[e] = l == 0.f ? 0.f : v[e] * inv;
+      };
+      if constexpr (PARTS == 3) {
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          uint32_t u[32];
+          take(c, v);
+#pragma unroll
+          for (int e = 0; e < 32; e++) u[e] = __float_as_uint(v[e]);
+          store_rows(buf, u, o + row0 * D + c, (size_t)P.Hq * D, rows);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < D; c += 64) {
+          uint32_t u[32], w[32];  // o, and what its rounding leaves
+#pragma unroll
+          for (int y = 0; y < 2; y++) {
+            float v[32];
+            take(c + 32 * y, v);
+            next_part(v, u + 16 * y);
+            next_part(v, w + 16 * y);
+          }
+          store_rows(buf, u, o + row0 * D + c, (size_t)P.Hq * D, rows);
+          if (P.save) store_rows(buf, w, P.res + row0 * D + c, (size_t)P.Hq * D, rows);
+        }
       }
       if (in) {
         lse[row] = l2 * LN2;
@@ -604,20 +700,21 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   }
 }
 
-template <int D>
+template <int D, int PARTS>
 cudaError_t fwd(const SmxP& P, const void* q, const void* k, const void* v, void* o, float* lse, cudaStream_t st) {
-  constexpr int XB = Fwd<D>::XB;
+  using F = Fwd<D, PARTS>;
   CUtensorMap mq, mk, mv;
-  if (!encode_head_rows(&mq, q, P.Nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, P.Nk, P.Hkv, D, XB) ||
-      !encode_head_rows(&mv, v, P.Nk, P.Hkv, D, XB))
+  if (!encode_head_rows(&mq, q, PARTS * P.Nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, PARTS * P.Nk, P.Hkv, D, F::XB) ||
+      !encode_head_rows(&mv, v, PARTS * P.Nk, P.Hkv, D, F::XB))
     return cudaErrorInvalidValue;
   const int64_t grid = (int64_t)max_tiles(P, 0) * P.Hq;
   if (grid > 2147483647) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(smx_tc_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Fwd<D>::SMEM);
+  auto kern = smx_tc_fwd_kernel<D, PARTS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_FWD, st);
-  e = launch_pdl(smx_tc_fwd_kernel<D>, dim3((unsigned)grid), dim3(Fwd<D>::THREADS), Fwd<D>::SMEM, st, P, mq, mk, mv,
-                 (bf16*)o, lse);
+  e = launch_pdl(kern, dim3((unsigned)grid), dim3(F::THREADS), F::SMEM, st, P, mq, mk, mv,
+                 (typename Io<PARTS>::T*)o, lse);
   prof_end(K_SMX_FWD, st);
   return e;
 }
@@ -638,24 +735,44 @@ __device__ __forceinline__ void bwd_weights(float (&v)[32], const float* l2, uin
 #pragma unroll
     for (int e = 0; e < 32; e++) v[e] = e >= lo && e < hi ? v[e] : 0.f;
 }
-// 32 gradients p (dp - delta) as bf16 pairs (an unseen pair's is zero whatever dp holds); dl: -delta.
-__device__ __forceinline__ void bwd_grads(const float (&p)[32], float (&dp)[32], const float* dl, bool cut, int lo,
-                                          int hi, uint32_t* w) {
+// 32 gradients p <- p (dp - delta) (an unseen pair's is zero whatever dp holds); dl: -delta.
+__device__ __forceinline__ void bwd_grads(float (&p)[32], const float (&dp)[32], const float* dl, bool cut, int lo,
+                                          int hi) {
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
     const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(dl + e);
-    one(mul2(two(p[e], p[e + 1]), add2(two(dp[e], dp[e + 1]), l.x)), dp[e], dp[e + 1]);
-    one(mul2(two(p[e + 2], p[e + 3]), add2(two(dp[e + 2], dp[e + 3]), l.y)), dp[e + 2], dp[e + 3]);
+    one(mul2(two(p[e], p[e + 1]), add2(two(dp[e], dp[e + 1]), l.x)), p[e], p[e + 1]);
+    one(mul2(two(p[e + 2], p[e + 3]), add2(two(dp[e + 2], dp[e + 3]), l.y)), p[e + 2], p[e + 3]);
   }
   if (cut)
 #pragma unroll
-    for (int e = 0; e < 32; e++) dp[e] = e >= lo && e < hi ? dp[e] : 0.f;
+    for (int e = 0; e < 32; e++) p[e] = e >= lo && e < hi ? p[e] : 0.f;
+}
+// 64 pairs of a row as operands: bf16 at `to`, second parts 32 columns further, third at `x3`.  With three parts a and b
+// come back as they were.
+template <int PARTS>
+__device__ __forceinline__ void put_parts(float (&a)[32], float (&b)[32], uint32_t (&w)[32], uint32_t to, uint32_t x3) {
 #pragma unroll
-  for (int e = 0; e < 16; e++) w[e] = pack(dp[2 * e], dp[2 * e + 1]);
+  for (int e = 0; e < 16; e++) {
+    w[e] = pack(a[2 * e], a[2 * e + 1]);
+    w[16 + e] = pack(b[2 * e], b[2 * e + 1]);
+  }
+  tm_st32(to, w);
+  if constexpr (PARTS == 3) {
+#pragma unroll
+    for (int y = 1; y < 3; y++) {
+#pragma unroll
+      for (int e = 0; e < 16; e++) {
+        w[e] = rest(a[2 * e], a[2 * e + 1], y);
+        w[16 + e] = rest(b[2 * e], b[2 * e + 1], y);
+      }
+      tm_st32(y == 1 ? to + 32 : x3, w);
+    }
+  }
 }
 // The same of a query's row: its (negated) sums are scalars, its keys end at `left`.
 __device__ __forceinline__ void dq_grads(float (&v)[32], const float (&dp)[32], uint64_t sc, uint64_t l2, uint64_t dl,
-                                         bool cut, int left, uint32_t* w) {
+                                         bool cut, int left) {
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
     float a, b;
@@ -665,8 +782,6 @@ __device__ __forceinline__ void dq_grads(float (&v)[32], const float (&dp)[32], 
   if (cut)
 #pragma unroll
     for (int e = 0; e < 32; e++) v[e] = e < left ? v[e] : 0.f;
-#pragma unroll
-  for (int e = 0; e < 16; e++) w[e] = pack(v[2 * e], v[2 * e + 1]);
 }
 // dk and dv, per CTA: 128 keys of one key head, over the blocks of 128 queries of its group's heads.  The pairs lie
 // transposed, a key a lane: S' = k q^T, P' = 2^(scale2 S' - lse2), dP' = v dO^T, dS' = P' (dP' - delta), and P' and
@@ -678,15 +793,15 @@ __device__ __forceinline__ void dq_grads(float (&v)[32], const float (&dp)[32], 
 // reads (q for dk and dv, k for dq), and B, of those that are free earlier (dO, v).
 // The other side's blocks have XB rows: 128, and eight warps for the pairs, at D = 128; at D = 64 half of both, and two
 // CTAs per SM.
-template <int D>
+template <int D, int PARTS>
 struct Bwd {
+  static_assert(PARTS == 1 || D == 64, "at D = 128 three parts of both own blocks leave no room for a ring");
   static constexpr int XB = D == 64 ? 64 : 128;
-  static constexpr int OWN = HALF * (D / 64), BYTES = OWN / BLK * XB;  // a block of either side
-  static constexpr int NA = D == 64 ? 5 : 3, NB = D == 64 ? 4 : 2;
+  static constexpr int OWN = BLK * D * 2 * PARTS, BYTES = XB * D * 2 * PARTS;  // a block of either side
+  static constexpr int NA = D == 64 && PARTS == 1 ? 5 : 3, NB = D == 64 && PARTS == 1 ? 4 : 2;
   static constexpr int BLOCKS = 2 * OWN + (NA + NB) * BYTES;
   static constexpr int EW = XB / 16;  // warps of the pairs: 64 of a row's pairs a thread
-  static constexpr int COLS = D == 64 ? 256 : 512;
-  static constexpr int PER_SM = D == 64 ? 2 : 1;
+  static constexpr int COLS = D == 64 && PARTS == 1 ? 256 : 512, PER_SM = COLS == 256 ? 2 : 1;
 };
 
 template <int XB>
@@ -696,18 +811,19 @@ struct BwdRest {  // (shared memory is full at D = 128: behind the blocks, whose
   uint32_t tmem;
   int dead;
 };
-template <int D>
-constexpr int DKV_SMEM = Bwd<D>::BLOCKS + (int)sizeof(BwdRest<Bwd<D>::XB>);
-static_assert(2 * (DKV_SMEM<64> + 1024) <= 233472 && DKV_SMEM<128> <= 232448, "shared memory of an SM, of a CTA");
+template <int D, int PARTS>
+constexpr int DKV_SMEM = Bwd<D, PARTS>::BLOCKS + (int)sizeof(BwdRest<Bwd<D, PARTS>::XB>);
+static_assert(2 * (DKV_SMEM<64, 1> + 1024) <= 233472 && DKV_SMEM<128, 1> <= 232448 && DKV_SMEM<64, 3> <= 232448,
+              "shared memory of an SM, of a CTA");
 
-template <int D>
-__global__ void __launch_bounds__(Bwd<D>::EW * 32 + 96, Bwd<D>::PER_SM)
+template <int D, int PARTS>
+__global__ void __launch_bounds__(Bwd<D, PARTS>::EW * 32 + 96, Bwd<D, PARTS>::PER_SM)
 smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
-                  bf16* __restrict__ dk, bf16* __restrict__ dv) {
-  using F = Bwd<D>;
+                  typename Io<PARTS>::T* __restrict__ dk, typename Io<PARTS>::T* __restrict__ dv) {
+  using F = Bwd<D, PARTS>;
   constexpr int XB = F::XB, EW = F::EW;
-  constexpr uint32_t cS = 0, cDP = XB, cDV = 2 * XB, cDK = 2 * XB + D;
+  constexpr uint32_t cS = 0, cDP = XB, cDV = 2 * XB, cDK = 2 * XB + D, cX = 2 * XB + 2 * D;  // (X: third parts)
   extern __shared__ __align__(1024) unsigned char sm[];
   BwdRest<XB>& B = *reinterpret_cast<BwdRest<XB>*>(sm + F::BLOCKS);
   if (mma::smem_u32(sm) & 1023) {  // (dynamic shared memory alone starts on such a boundary)
@@ -764,8 +880,8 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   if (warp == EW + 1) {  // copies
     if (lane == 0 && n > 0) {
       mma::mbar_expect_tx(&B.own, 2 * F::OWN);
-      load_block<D>(sm, &mk, hk, t.k0 + j0, &B.own);
-      load_block<D>(sm + F::OWN, &mv, hk, t.k0 + j0, &B.own);
+      load_block<D, BLK, PARTS>(sm, &mk, hk, t.k0 + j0, P.Nk, &B.own);
+      load_block<D, BLK, PARTS>(sm + F::OWN, &mv, hk, t.k0 + j0, P.Nk, &B.own);
     }
     __syncwarp();
     for (int x = 0; x < n; x++) {
@@ -773,13 +889,13 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       if (x >= F::NA && !wait(&B.emptyA[sa], (x / F::NA - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullA[sa], F::BYTES);
-        load_block<D>(ringA + sa * F::BYTES, &mq, h, row, &B.fullA[sa]);
+        load_block<D, XB, PARTS>(ringA + sa * F::BYTES, &mq, h, row, P.Nq, &B.fullA[sa]);
       }
       __syncwarp();
       if (x >= F::NB && !wait(&B.emptyB[sb], (x / F::NB - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullB[sb], F::BYTES);
-        load_block<D>(ringB + sb * F::BYTES, &mg, h, row, &B.fullB[sb]);
+        load_block<D, XB, PARTS>(ringB + sb * F::BYTES, &mg, h, row, P.Nq, &B.fullB[sb]);
       }
       __syncwarp();
     }
@@ -804,20 +920,24 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     constexpr uint32_t id_s = idesc(BLK, XB, false), id_o = idesc(BLK, D, true);
     const uint32_t me = elect();
     auto pairs = [&](uint32_t d, uint32_t a, uint32_t b, uint64_t* bar) {
-#pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(tm + d, desc_k(a, s), desc_k(b, s), id_s, s > 0, me);
+      prod_ss<D, PARTS, BLK, XB>(tm + d, a, b, id_s, me);
       commit(bar, me);
     };
-    auto apply = [&](uint32_t d, uint32_t a, uint32_t b, bool acc) {  // (each half's 64 columns are 32 of bf16 pairs)
+    // (64 columns of pairs are 32 of bf16; second parts 32 further, third at x3)
+    auto apply = [&](uint32_t d, uint32_t a, uint32_t x3, uint32_t b, bool acc) {
+      using Q = Prod<PARTS>;
 #pragma unroll
-      for (int s = 0; s < XB / 16; s++)
-        mma_ts(tm + d, tm + a + 64 * (s >> 2) + 8 * (s & 3), desc_mn(b, s), id_o, acc || s > 0, me);
+      for (int y = 0; y < Q::N; y++)
+#pragma unroll
+        for (int s = 0; s < XB / 16; s++)
+          mma_ts(tm + d, tm + (Q::a(y) == 2 ? x3 + 8 * s : a + 64 * (s >> 2) + 8 * (s & 3) + 32 * Q::a(y)),
+                 desc_mn<XB>(b + Q::b(y) * (XB * D * 2), s), id_o, acc || y > 0 || s > 0, me);
     };
     // block x of queries (of their dO) has landed; rows behind its document's last are zeros
     auto ready = [&](int x, unsigned char* block, uint64_t* full, int phase) -> bool {
       const int left = t.Lq - (first + x % per) * XB;
       if (!wait(full, phase & 1, &B.dead)) return false;
-      if (left < XB) zero_rows<D, XB>(block, left);
+      if (left < XB) zero_rows<D, XB, PARTS>(block, left);
       return true;
     };
     auto readyA = [&](int x) { return ready(x, ringA + x % F::NA * F::BYTES, &B.fullA[x % F::NA], x / F::NA); };
@@ -833,7 +953,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
         const bool more = x + 1 < n;
         if (!wait(&B.p, x & 1, &B.dead)) return false;
         tc::fence_after();
-        apply(cDV, cS, gb, x > 0);
+        apply(cDV, cS, cX, gb, x > 0);
         commit(&B.emptyB[x % F::NB], me);
         if (more) {
           if (!readyA(x + 1)) return false;
@@ -841,7 +961,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
         }
         if (!wait(&B.ds, x & 1, &B.dead)) return false;
         tc::fence_after();
-        apply(cDK, cDP, qb, x > 0);
+        apply(cDK, cDP, cX + XB / 2, qb, x > 0);
         commit(&B.emptyA[x % F::NA], me);
         if (more) {
           if (!readyB(x + 1)) return false;
@@ -879,12 +999,8 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       tm_wait_ld(b);
       bwd_weights(a, l2, sc, cut, lo, hi);
       bwd_weights(b, l2 + 32, sc, cut, lo - 32, hi - 32);
-#pragma unroll
-      for (int e = 0; e < 16; e++) {
-        w[e] = pack(a[2 * e], a[2 * e + 1]);
-        w[16 + e] = pack(b[2 * e], b[2 * e + 1]);
-      }
-      tm_st32(ts, w);  // (over logits of its own: the other half's warp may still read its)
+      // (over logits of its own: the other half's warp may still read its)
+      put_parts<PARTS>(a, b, w, ts, tm + cX + lanes);
       tm_wait_st();
       tc::fence_before();
       __syncwarp();
@@ -895,11 +1011,11 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       float c[32];
       tm_ld32(td, c);
       tm_wait_ld(c);
-      bwd_grads(a, c, dl, cut, lo, hi, w);
+      bwd_grads(a, c, dl, cut, lo, hi);
       tm_ld32(td + 32, c);
       tm_wait_ld(c);
-      bwd_grads(b, c, dl + 32, cut, lo - 32, hi - 32, w + 16);
-      tm_st32(td, w);
+      bwd_grads(b, c, dl + 32, cut, lo - 32, hi - 32);
+      put_parts<PARTS>(a, b, w, td, tm + cX + XB / 2 + lanes);
       tm_wait_st();
       tc::fence_before();
       __syncwarp();
@@ -929,22 +1045,20 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
 // dq, per CTA: 128 queries of one head over the blocks of keys: S = q k^T, dP = dO v^T, dS = P (dP - delta), dq += dS k.
 // S and dP are taken to registers at once, so that the next block's products run while dS is formed; dS has two places
 // of its own.
-template <int D>
-constexpr int DQ_SMEM = Bwd<D>::BLOCKS + 1024;  // (blocks on 1024-byte boundaries)
 struct DqBars {
   uint64_t own, fullA[5], emptyA[5], fullB[5], emptyB[5], s, taken, ds, used[2], drain;
   uint32_t tmem;
   int dead;
 };
 
-template <int D>
-__global__ void __launch_bounds__(Bwd<D>::EW * 32 + 64, Bwd<D>::PER_SM)
+template <int D, int PARTS>
+__global__ void __launch_bounds__(Bwd<D, PARTS>::EW * 32 + 64, Bwd<D, PARTS>::PER_SM)
 smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
-                 bf16* __restrict__ dq) {
-  using F = Bwd<D>;
+                 typename Io<PARTS>::T* __restrict__ dq) {
+  using F = Bwd<D, PARTS>;
   constexpr int XB = F::XB, EW = F::EW;
-  constexpr uint32_t cS = 0, cDP = XB, cDQ = 2 * XB, cDS = 2 * XB + D;
+  constexpr uint32_t cS = 0, cDP = XB, cDQ = 2 * XB, cDS = 2 * XB + D, nDS = XB / 2 * PARTS;  // (columns of one dS: its parts)
   extern __shared__ unsigned char raw[];
   __shared__ DqBars B;
   unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
@@ -995,8 +1109,8 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   if (warp == EW + 1) {  // copies
     if (lane == 0 && n > 0) {
       mma::mbar_expect_tx(&B.own, 2 * F::OWN);
-      load_block<D>(sm, &mq, h, t.q0 + i0, &B.own);
-      load_block<D>(sm + F::OWN, &mg, h, t.q0 + i0, &B.own);
+      load_block<D, BLK, PARTS>(sm, &mq, h, t.q0 + i0, P.Nq, &B.own);
+      load_block<D, BLK, PARTS>(sm + F::OWN, &mg, h, t.q0 + i0, P.Nq, &B.own);
     }
     __syncwarp();
     for (int x = 0; x < n; x++) {
@@ -1004,13 +1118,13 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (x >= F::NA && !wait(&B.emptyA[sa], (x / F::NA - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullA[sa], F::BYTES);
-        load_block<D>(ringA + sa * F::BYTES, &mk, hk, t.k0 + x * XB, &B.fullA[sa]);
+        load_block<D, XB, PARTS>(ringA + sa * F::BYTES, &mk, hk, t.k0 + x * XB, P.Nk, &B.fullA[sa]);
       }
       __syncwarp();
       if (x >= F::NB && !wait(&B.emptyB[sb], (x / F::NB - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullB[sb], F::BYTES);
-        load_block<D>(ringB + sb * F::BYTES, &mv, hk, t.k0 + x * XB, &B.fullB[sb]);
+        load_block<D, XB, PARTS>(ringB + sb * F::BYTES, &mv, hk, t.k0 + x * XB, P.Nk, &B.fullB[sb]);
       }
       __syncwarp();
     }
@@ -1020,17 +1134,15 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
     const uint32_t me = elect();
     auto pairs = [&](int x) {
       const uint32_t kb = a0 + x % F::NA * F::BYTES, vb = b0 + x % F::NB * F::BYTES;
-#pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(tm + cS, desc_k(q0, s), desc_k(kb, s), id_s, s > 0, me);
-#pragma unroll
-      for (int s = 0; s < D / 16; s++) mma_ss(tm + cDP, desc_k(g0, s), desc_k(vb, s), id_s, s > 0, me);
+      prod_ss<D, PARTS, BLK, XB>(tm + cS, q0, kb, id_s, me);
+      prod_ss<D, PARTS, BLK, XB>(tm + cDP, g0, vb, id_s, me);
       commit(&B.s, me);
       commit(&B.emptyB[x % F::NB], me);
     };
     auto ready = [&](int x) -> bool {
       const int left = t.Lk - x * XB;
       if (!wait(&B.fullA[x % F::NA], (x / F::NA) & 1, &B.dead)) return false;
-      if (left < XB) zero_rows<D, XB>(ringA + x % F::NA * F::BYTES, left);
+      if (left < XB) zero_rows<D, XB, PARTS>(ringA + x % F::NA * F::BYTES, left);
       return wait(&B.fullB[x % F::NB], (x / F::NB) & 1, &B.dead);
     };
     auto run = [&]() -> bool {
@@ -1045,9 +1157,13 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
         if (!wait(&B.ds, x & 1, &B.dead)) return false;
         tc::fence_after();
         const uint32_t kb = a0 + x % F::NA * F::BYTES;
+        using Q = Prod<PARTS>;
 #pragma unroll
-        for (int s = 0; s < XB / 16; s++)
-          mma_ts(tm + cDQ, tm + cDS + XB / 2 * (x & 1) + 8 * s, desc_mn(kb, s), id_o, x > 0 || s > 0, me);
+        for (int y = 0; y < Q::N; y++)
+#pragma unroll
+          for (int s = 0; s < XB / 16; s++)
+            mma_ts(tm + cDQ, tm + cDS + nDS * (x & 1) + XB / 2 * Q::a(y) + 8 * s,
+                   desc_mn<XB>(kb + Q::b(y) * (XB * D * 2), s), id_o, x > 0 || y > 0 || s > 0, me);
         commit(&B.used[x & 1], me);
         commit(&B.emptyA[x % F::NA], me);
       }
@@ -1085,15 +1201,16 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (lane == 0) mma::mbar_arrive(&B.taken);
       const int left = lim - x * XB - 64 * half;
       const bool cut = x >= clean;
-      uint32_t w[32];
-      dq_grads(a, c, sc, l2, dl, cut, left, w);
-      dq_grads(b, d, sc, l2, dl, cut, left - 32, w + 16);
+      dq_grads(a, c, sc, l2, dl, cut, left);
+      dq_grads(b, d, sc, l2, dl, cut, left - 32);
       if (x >= 2) {
         ok = wait(&B.used[x & 1], (x / 2 - 1) & 1, &B.dead);
         if (!ok) break;
         tc::fence_after();
       }
-      tm_st32(tm + cDS + XB / 2 * (x & 1) + 32 * half + lanes, w);
+      uint32_t w[32];
+      const uint32_t to = tm + cDS + nDS * (x & 1) + 32 * half + lanes;
+      put_parts<PARTS>(a, b, w, to, to + 64);
       tm_wait_st();
       tc::fence_before();
       __syncwarp();
@@ -1118,45 +1235,91 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   }
 }
 
-template <int D>
+template <int D, int PARTS>
 cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, const void* dO, void* dq, void* dk,
                 void* dv, cudaStream_t st) {
-  constexpr int XB = Bwd<D>::XB;
+  using F = Bwd<D, PARTS>;
+  using T = typename Io<PARTS>::T;
   CUtensorMap mq, mk, mv, mg, xq, xk, xv, xg;  // blocks of 128 rows, and of the other side's XB
-  if (!encode_head_rows(&mq, q, P.Nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, P.Nk, P.Hkv, D, BLK) ||
-      !encode_head_rows(&mv, v, P.Nk, P.Hkv, D, BLK) || !encode_head_rows(&mg, dO, P.Nq, P.Hq, D, BLK))
+  const int nq = PARTS * P.Nq, nk = PARTS * P.Nk;
+  if (!encode_head_rows(&mq, q, nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, nk, P.Hkv, D, BLK) ||
+      !encode_head_rows(&mv, v, nk, P.Hkv, D, BLK) || !encode_head_rows(&mg, dO, nq, P.Hq, D, BLK))
     return cudaErrorInvalidValue;
   xq = mq, xk = mk, xv = mv, xg = mg;
-  if (XB != BLK && (!encode_head_rows(&xq, q, P.Nq, P.Hq, D, XB) || !encode_head_rows(&xk, k, P.Nk, P.Hkv, D, XB) ||
-                    !encode_head_rows(&xv, v, P.Nk, P.Hkv, D, XB) || !encode_head_rows(&xg, dO, P.Nq, P.Hq, D, XB)))
+  if (F::XB != BLK && (!encode_head_rows(&xq, q, nq, P.Hq, D, F::XB) || !encode_head_rows(&xk, k, nk, P.Hkv, D, F::XB) ||
+                       !encode_head_rows(&xv, v, nk, P.Hkv, D, F::XB) || !encode_head_rows(&xg, dO, nq, P.Hq, D, F::XB)))
     return cudaErrorInvalidValue;
   const int64_t gk = (int64_t)max_tiles(P, 2) * P.Hkv, gq = (int64_t)max_tiles(P, 1) * P.Hq;
   if (gk > 2147483647 || gq > 2147483647) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(smx_tc_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DKV_SMEM<D>);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(smx_tc_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DQ_SMEM<D>);
+  auto dkv = smx_tc_dkv_kernel<D, PARTS>;
+  auto dqk = smx_tc_dq_kernel<D, PARTS>;
+  cudaError_t e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, DKV_SMEM<D, PARTS>);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(dqk, cudaFuncAttributeMaxDynamicSharedMemorySize, F::BLOCKS + 1024);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DKV, st);
-  e = launch_pdl(smx_tc_dkv_kernel<D>, dim3((unsigned)gk), dim3(Bwd<D>::EW * 32 + 96), DKV_SMEM<D>, st, P, xq, mk, mv, xg,
-                 (bf16*)dk, (bf16*)dv);
+  e = launch_pdl(dkv, dim3((unsigned)gk), dim3(F::EW * 32 + 96), DKV_SMEM<D, PARTS>, st, P, xq, mk, mv, xg, (T*)dk,
+                 (T*)dv);
   prof_end(K_SMX_DKV, st);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DQ, st);
-  e = launch_pdl(smx_tc_dq_kernel<D>, dim3((unsigned)gq), dim3(Bwd<D>::EW * 32 + 64), DQ_SMEM<D>, st, P, mq, xk, xv, mg,
-                 (bf16*)dq);
+  e = launch_pdl(dqk, dim3((unsigned)gq), dim3(F::EW * 32 + 64), F::BLOCKS + 1024, st, P, mq, xk, xv, mg, (T*)dq);
   prof_end(K_SMX_DQ, st);
   return e;
 }
 
+// ------------------------------------------------------------ fp32 io: the parts
+// Array y of up to three: its 8 n_y values as three bf16 arrays one behind the other.
+struct Split {
+  const float* x[3];
+  bf16* parts[3];
+  int64_t n[3];
+};
+__global__ void __launch_bounds__(256) smx_split_kernel(Split s) {
+  pdl_wait();
+  pdl_release();
+  const int y = blockIdx.y;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < s.n[y]; i += (int64_t)gridDim.x * 256) {
+    float v[8];
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+      const float4 f = *reinterpret_cast<const float4*>(s.x[y] + 8 * i + 4 * c);
+      v[4 * c] = f.x; v[4 * c + 1] = f.y; v[4 * c + 2] = f.z; v[4 * c + 3] = f.w;
+    }
+#pragma unroll
+    for (int p = 0; p < 3; p++) {
+      uint32_t w[4];
+      next_part(v, w);
+      *reinterpret_cast<uint4*>(s.parts[y] + 8 * (p * s.n[y] + i)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 }  // namespace
 
-cudaError_t launch_tc_fwd(const SmxP& P, int D, const void* q, const void* k, const void* v, void* o, float* lse,
-                          cudaStream_t st) {
-  return D == 64 ? fwd<64>(P, q, k, v, o, lse, st) : fwd<128>(P, q, k, v, o, lse, st);
+cudaError_t launch_tc_fwd(const SmxP& P, int D, int parts, const void* q, const void* k, const void* v, void* o,
+                          float* lse, cudaStream_t st) {
+  if (parts == 3) return D == 64 ? fwd<64, 3>(P, q, k, v, o, lse, st) : fwd<128, 3>(P, q, k, v, o, lse, st);
+  return D == 64 ? fwd<64, 1>(P, q, k, v, o, lse, st) : fwd<128, 1>(P, q, k, v, o, lse, st);
 }
-cudaError_t launch_tc_bwd(const SmxP& P, int D, const void* q, const void* k, const void* v, const void* dO, void* dq,
-                          void* dk, void* dv, cudaStream_t st) {
-  return D == 64 ? bwd<64>(P, q, k, v, dO, dq, dk, dv, st) : bwd<128>(P, q, k, v, dO, dq, dk, dv, st);
+cudaError_t launch_tc_bwd(const SmxP& P, int D, int parts, const void* q, const void* k, const void* v, const void* dO,
+                          void* dq, void* dk, void* dv, cudaStream_t st) {
+  if (parts == 3) return bwd<64, 3>(P, q, k, v, dO, dq, dk, dv, st);
+  return D == 64 ? bwd<64, 1>(P, q, k, v, dO, dq, dk, dv, st) : bwd<128, 1>(P, q, k, v, dO, dq, dk, dv, st);
+}
+cudaError_t launch_split(int n, const float* const* x, bf16* const* parts, const int64_t* values, cudaStream_t st) {
+  Split s = {};
+  int64_t most = 0;
+  for (int y = 0; y < n; y++) {
+    s.x[y] = x[y];
+    s.parts[y] = parts[y];
+    s.n[y] = values[y] / 8;
+    if (s.n[y] > most) most = s.n[y];
+  }
+  const int64_t grid = (most + 255) / 256;
+  prof_begin(K_SMX_SPLIT, st);
+  const cudaError_t e = launch_pdl(smx_split_kernel, dim3((unsigned)(grid < 16384 ? grid : 16384), n), dim3(256), 0, st, s);
+  prof_end(K_SMX_SPLIT, st);
+  return e;
 }
 
 }  // namespace smx
