@@ -61,16 +61,24 @@ __device__ __forceinline__ void pairs(const float* a, const float* b, int r0, in
   for (int i = 0; i < R; i++)
 #pragma unroll
     for (int j = 0; j < 4; j++) c[i][j] = 0.f;
+#pragma unroll 1
+  for (int d0 = 0; d0 < D; d0 += 32) {  // (sums of 32, then their sum: a third of one long sum's rounding)
+    float u[R][4] = {};
 #pragma unroll 8
-  for (int d = 0; d < D; d++) {
-    float x[R], y[4];
+    for (int d = d0; d < d0 + 32; d++) {
+      float x[R], y[4];
 #pragma unroll
-    for (int i = 0; i < R; i += 4) ld4(a + d * 16 * R + r0 + i, x + i);
-    ld4(b + d * TM + c0, y);
+      for (int i = 0; i < R; i += 4) ld4(a + d * 16 * R + r0 + i, x + i);
+      ld4(b + d * TM + c0, y);
+#pragma unroll
+      for (int i = 0; i < R; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) u[i][j] = fmaf(x[i], y[j], u[i][j]);
+    }
 #pragma unroll
     for (int i = 0; i < R; i++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) c[i][j] = fmaf(x[i], y[j], c[i][j]);
+      for (int j = 0; j < 4; j++) c[i][j] += u[i][j];
   }
 }
 // c[i][64 m + 4 tx + e] += sum_n w[n][r0 + i] x[n][64 m + 4 tx + e]: w's rows are PP apart

@@ -97,16 +97,6 @@ __device__ __forceinline__ void tm_ld16(uint32_t a, float (&v)[16]) {
         "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(a));
 }
-__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
-      : "memory");
-}
 __device__ __forceinline__ void tm_st8(uint32_t a, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};\n" ::"r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(a)
@@ -245,9 +235,9 @@ __device__ __forceinline__ void store_rows(unsigned char* buf, const uint32_t (&
   }
   __syncwarp();
 }
-// 64 columns of an accumulator, times f (zeros where nothing was accumulated).
-template <typename T>
-__device__ __forceinline__ void store_acc(unsigned char* buf, uint32_t tm, bool any, float f, T* dst, size_t ld, int n) {
+// 64 columns of an accumulator, times f, as bf16 (zeros where nothing was accumulated).
+__device__ __forceinline__ void store_acc(unsigned char* buf, uint32_t tm, bool any, float f, bf16* dst, size_t ld,
+                                          int n) {
   uint32_t u[32];
 #pragma unroll
   for (int c = 0; c < 2; c++) {
@@ -256,16 +246,10 @@ __device__ __forceinline__ void store_acc(unsigned char* buf, uint32_t tm, bool 
       tm_ld32(tm + 32 * c, v);
       tm_wait_ld(v);
     }
-    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int e = 0; e < 16; e++) u[16 * c + e] = any ? pack(v[2 * e] * f, v[2 * e + 1] * f) : 0u;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; e++) u[e] = any ? __float_as_uint(v[e] * f) : 0u;
-      store_rows(buf, u, dst + 32 * c, ld, n);
-    }
+    for (int e = 0; e < 16; e++) u[16 * c + e] = any ? pack(v[2 * e] * f, v[2 * e + 1] * f) : 0u;
   }
-  if constexpr (sizeof(T) == 2) store_rows(buf, u, dst, ld, n);
+  store_rows(buf, u, dst, ld, n);
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
@@ -294,7 +278,9 @@ __device__ __forceinline__ void load_block(unsigned char* dst, const CUtensorMap
 }
 
 // fp32 io comes as three bf16 parts of every value (x = x0 + x1 + x2 to 2^-24), and a product is the six products of
-// parts above that: bytes and time of six, and the fp32 pipe's precision.  Smallest first.
+// parts above that, smallest first: bytes and time of six, and the fp32 pipe's precision.  The tensor pipe truncates its
+// sums, so a sum over many blocks would be off by 2^-24 for every 16 of its terms (o after 1001 keys by 6e-6): each
+// block's product starts from zero and is added to the row's sum in registers (3e-7).
 template <int PARTS>
 struct Prod {
   static constexpr int N = 1;
@@ -484,7 +470,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
 #pragma unroll
             for (int s = 0; s < XB / 16; s++)
               mma_ts(d, Q::a(y) == 2 ? c + 8 * s : a + F::part(s) + Q::a(y) * F::SECOND,
-                     desc_mn<XB>(vb + Q::b(y) * (XB * D * 2), s), id_o, j > 0 || y > 0 || s > 0, me);
+                     desc_mn<XB>(vb + Q::b(y) * (XB * D * 2), s), id_o, (PARTS == 1 && j > 0) || y > 0 || s > 0, me);
           if (PARTS == 1 && j == 0 && clean[i] == 0)
 #pragma unroll
             for (int s = 0; s < XB / 16; s++)
@@ -509,6 +495,17 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     const int lim = keys_of(P.causal, i0 + r, t.Lq, t.Lk);  // (grows with the row)
     const uint64_t sc = two(P.scale2, P.scale2);
     float m = -INFINITY, l = 0.f;
+    float sums[PARTS == 3 ? D : 1] = {};  // (three parts) o
+    auto take_block = [&]() {  // the product of the block before is done: its S was issued earlier than this one's
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        float v[16];
+        tm_ld16(to + c, v);
+        tm_wait_ld(v);
+#pragma unroll
+        for (int e = 0; e < 16; e++) sums[c + e] += v[e];
+      }
+    };
     // A new reference, the block's maximum `top`, in rows where it has grown by 2^GROW (or that ask for it): o and l are
     // scaled down to it.  False: a wait gave up.
     auto raise = [&](int j, float top, bool ask) -> bool {
@@ -518,6 +515,11 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       if (grew) m = top;
       l *= up;
       if (j == 0) return true;
+      if constexpr (PARTS == 3) {
+#pragma unroll
+        for (int c = 0; c < D; c++) sums[c] *= up;
+        return true;
+      }
       if (!wait(&B.o[i], (j - 1) & 1, &B.dead)) return false;
       tc::fence_after();
 #pragma unroll 1
@@ -537,6 +539,8 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       ok = wait(&B.s[i], j & 1, &B.dead);
       if (!ok) break;
       tc::fence_after();
+      if constexpr (PARTS == 3)
+        if (j > 0) take_block();
       const bool cut = j >= cleani, few = cut && j == 0;  // a mask cuts the block; some rows may have few keys in all
       const int left = lim - j * XB, least = cut ? __shfl_sync(0xffffffffu, left, 0) : XB;  // (the warp's first row's)
       uint64_t sum[2] = {0, 0};
@@ -646,28 +650,20 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     if (ok && nbi > 0) {
       ok = wait(&B.o[i], (nbi - 1) & 1, &B.dead);
       tc::fence_after();
+      if constexpr (PARTS == 3)
+        if (ok) take_block();
     }
     if (ok) {
       const float inv = l == 0.f ? 0.f : 1.0f / l, l2 = m * P.scale2 + log2f(l);
       const int w0 = r & ~31, rows = nq - w0;  // the warp's first row, rows from there on
       const size_t row = (size_t)(t.q0 + i0 + r) * P.Hq + h, row0 = (size_t)(t.q0 + i0 + w0) * P.Hq + h;
       unsigned char* buf = sm + i * F::OWN + (w0 & 127) * 128;  // (the tile's queries are no longer read)
-      auto take = [&](int c, float (&v)[32]) {  // columns c .. of o
-        if (nbi > 0) {
-          tm_ld32(to + c, v);
-          tm_wait_ld(v);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e++) v[e] = l == 0.f ? 0.f : v[e] * inv;
-      };
       if constexpr (PARTS == 3) {
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
-          float v[32];
           uint32_t u[32];
-          take(c, v);
 #pragma unroll
-          for (int e = 0; e < 32; e++) u[e] = __float_as_uint(v[e]);
+          for (int e = 0; e < 32; e++) u[e] = __float_as_uint(sums[c + e] * inv);
           store_rows(buf, u, o + row0 * D + c, (size_t)P.Hq * D, rows);
         }
       } else {
@@ -677,7 +673,12 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
 #pragma unroll
           for (int y = 0; y < 2; y++) {
             float v[32];
-            take(c + 32 * y, v);
+            if (nbi > 0) {
+              tm_ld32(to + c + 32 * y, v);
+              tm_wait_ld(v);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e++) v[e] = l == 0.f ? 0.f : v[e] * inv;
             next_part(v, u + 16 * y);
             next_part(v, w + 16 * y);
           }
@@ -748,26 +749,43 @@ __device__ __forceinline__ void bwd_grads(float (&p)[32], const float (&dp)[32],
 #pragma unroll
     for (int e = 0; e < 32; e++) p[e] = e >= lo && e < hi ? p[e] : 0.f;
 }
-// 64 pairs of a row as operands: bf16 at `to`, second parts 32 columns further, third at `x3`.  With three parts a and b
-// come back as they were.
-template <int PARTS>
-__device__ __forceinline__ void put_parts(float (&a)[32], float (&b)[32], uint32_t (&w)[32], uint32_t to, uint32_t x3) {
+// 32 H pairs of a row as operands: bf16 at `to`, second parts 16 H columns further, third at `x3`.
+template <int PARTS, int H>
+__device__ __forceinline__ void put_parts(float (&v)[H][32], uint32_t to, uint32_t x3) {
 #pragma unroll
-  for (int e = 0; e < 16; e++) {
-    w[e] = pack(a[2 * e], a[2 * e + 1]);
-    w[16 + e] = pack(b[2 * e], b[2 * e + 1]);
-  }
-  tm_st32(to, w);
-  if constexpr (PARTS == 3) {
+  for (int y = 0; y < PARTS; y++)
 #pragma unroll
-    for (int y = 1; y < 3; y++) {
+    for (int c = 0; c < H; c++) {
+      uint32_t w[16];
+      if (PARTS == 1) {
 #pragma unroll
-      for (int e = 0; e < 16; e++) {
-        w[e] = rest(a[2 * e], a[2 * e + 1], y);
-        w[16 + e] = rest(b[2 * e], b[2 * e + 1], y);
+        for (int e = 0; e < 16; e++) w[e] = pack(v[c][2 * e], v[c][2 * e + 1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; e++) w[e] = rest(v[c][2 * e], v[c][2 * e + 1], y);
       }
-      tm_st32(y == 1 ? to + 32 : x3, w);
+      tm_st16((y == 2 ? x3 : to + 16 * H * y) + 16 * c, w);
     }
+}
+template <int N>
+__device__ __forceinline__ void add_columns(float (&sum)[N], uint32_t tm) {
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    float v[32];
+    tm_ld32(tm + c, v);
+    tm_wait_ld(v);
+#pragma unroll
+    for (int e = 0; e < 32; e++) sum[c + e] += v[e];
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_sums(unsigned char* buf, const float (&sum)[N], float f, float* dst, size_t ld, int n) {
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    uint32_t u[32];
+#pragma unroll
+    for (int e = 0; e < 32; e++) u[e] = __float_as_uint(sum[c + e] * f);
+    store_rows(buf, u, dst + c, ld, n);
   }
 }
 // The same of a query's row: its (negated) sums are scalars, its keys end at `left`.
@@ -800,7 +818,8 @@ struct Bwd {
   static constexpr int OWN = BLK * D * 2 * PARTS, BYTES = XB * D * 2 * PARTS;  // a block of either side
   static constexpr int NA = D == 64 && PARTS == 1 ? 5 : 3, NB = D == 64 && PARTS == 1 ? 4 : 2;
   static constexpr int BLOCKS = 2 * OWN + (NA + NB) * BYTES;
-  static constexpr int EW = XB / 16;  // warps of the pairs: 64 of a row's pairs a thread
+  // warps of the pairs: 64 of a row's pairs a thread; with three parts in dk and dv 32, and 32 columns of both sums
+  static constexpr int EW = XB / 16, EWK = PARTS == 3 ? 2 * EW : EW;
   static constexpr int COLS = D == 64 && PARTS == 1 ? 256 : 512, PER_SM = COLS == 256 ? 2 : 1;
 };
 
@@ -817,12 +836,12 @@ static_assert(2 * (DKV_SMEM<64, 1> + 1024) <= 233472 && DKV_SMEM<128, 1> <= 2324
               "shared memory of an SM, of a CTA");
 
 template <int D, int PARTS>
-__global__ void __launch_bounds__(Bwd<D, PARTS>::EW * 32 + 96, Bwd<D, PARTS>::PER_SM)
+__global__ void __launch_bounds__(Bwd<D, PARTS>::EWK * 32 + 96, Bwd<D, PARTS>::PER_SM)
 smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
                   typename Io<PARTS>::T* __restrict__ dk, typename Io<PARTS>::T* __restrict__ dv) {
   using F = Bwd<D, PARTS>;
-  constexpr int XB = F::XB, EW = F::EW;
+  constexpr int XB = F::XB, EW = F::EWK, H = PARTS == 3 ? 1 : 2;
   constexpr uint32_t cS = 0, cDP = XB, cDV = 2 * XB, cDK = 2 * XB + D, cX = 2 * XB + 2 * D;  // (X: third parts)
   extern __shared__ __align__(1024) unsigned char sm[];
   BwdRest<XB>& B = *reinterpret_cast<BwdRest<XB>*>(sm + F::BLOCKS);
@@ -923,15 +942,15 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       prod_ss<D, PARTS, BLK, XB>(tm + d, a, b, id_s, me);
       commit(bar, me);
     };
-    // (64 columns of pairs are 32 of bf16; second parts 32 further, third at x3)
+    // (a thread's pairs, 32 H columns, are 16 H of bf16, second parts 16 H further, third at x3)
     auto apply = [&](uint32_t d, uint32_t a, uint32_t x3, uint32_t b, bool acc) {
       using Q = Prod<PARTS>;
 #pragma unroll
       for (int y = 0; y < Q::N; y++)
 #pragma unroll
         for (int s = 0; s < XB / 16; s++)
-          mma_ts(tm + d, tm + (Q::a(y) == 2 ? x3 + 8 * s : a + 64 * (s >> 2) + 8 * (s & 3) + 32 * Q::a(y)),
-                 desc_mn<XB>(b + Q::b(y) * (XB * D * 2), s), id_o, acc || y > 0 || s > 0, me);
+          mma_ts(tm + d, tm + (Q::a(y) == 2 ? x3 + 8 * s : a + 32 * H * (s / (2 * H)) + 8 * (s % (2 * H)) + 16 * H * Q::a(y)),
+                 desc_mn<XB>(b + Q::b(y) * (XB * D * 2), s), id_o, (PARTS == 1 && acc) || y > 0 || s > 0, me);
     };
     // block x of queries (of their dO) has landed; rows behind its document's last are zeros
     auto ready = [&](int x, unsigned char* block, uint64_t* full, int phase) -> bool {
@@ -979,28 +998,32 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   } else if (warp < EW && live) {  // weights and their gradients: a thread a key, 64 of a block's queries
     const int half = warp / 4, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tm + cS + 64 * half + lanes, td = tm + cDP + 64 * half + lanes;
+    constexpr int W = 32 * H;  // a thread's columns of a block's pairs
+    const uint32_t ts = tm + cS + W * half + lanes, td = tm + cDP + W * half + lanes;
+    const uint32_t x3 = tm + cX + W / 2 * half + lanes;
     const int fq = first_query(P.causal, j0 + r, t.Lq, t.Lk), fq_last = first_query(P.causal, j0 + nk - 1, t.Lq, t.Lk);
     const uint64_t sc = two(P.scale2, P.scale2);
+    float sv[PARTS == 3 ? 32 : 1] = {}, sk[PARTS == 3 ? 32 : 1] = {};  // (three parts) dv and dk, columns 32 half ..
     bool ok = true;
     for (int x = 0; x < n; x++) {
       const int s = x & 1, i0 = (first + x % per) * XB;
-      const float *l2 = B.stat[s][0] + 64 * half, *dl = B.stat[s][1] + 64 * half;
+      const float *l2 = B.stat[s][0] + W * half, *dl = B.stat[s][1] + W * half;
       const bool cut = i0 < fq_last || i0 + XB > t.Lq;
-      const int lo = fq - i0 - 64 * half, hi = t.Lq - i0 - 64 * half;
-      float a[32], b[32];
-      uint32_t w[32];
+      const int lo = fq - i0 - W * half, hi = t.Lq - i0 - W * half;
+      float a[H][32];
       ok = wait(&B.fullS[s], (x >> 1) & 1, &B.dead) && wait(&B.s, x & 1, &B.dead);
       if (!ok) break;
       tc::fence_after();
-      tm_ld32(ts, a);
-      tm_ld32(ts + 32, b);
-      tm_wait_ld(a);
-      tm_wait_ld(b);
-      bwd_weights(a, l2, sc, cut, lo, hi);
-      bwd_weights(b, l2 + 32, sc, cut, lo - 32, hi - 32);
+#pragma unroll
+      for (int c = 0; c < H; c++) tm_ld32(ts + 32 * c, a[c]);
+#pragma unroll
+      for (int c = 0; c < H; c++) tm_wait_ld(a[c]);
+#pragma unroll
+      for (int c = 0; c < H; c++) bwd_weights(a[c], l2 + 32 * c, sc, cut, lo - 32 * c, hi - 32 * c);
       // (over logits of its own: the other half's warp may still read its)
-      put_parts<PARTS>(a, b, w, ts, tm + cX + lanes);
+      put_parts<PARTS, H>(a, ts, x3);
+      if constexpr (PARTS == 3)
+        if (x > 0) add_columns(sv, tm + cDV + 32 * half + lanes);  // (the block before's: issued before this S')
       tm_wait_st();
       tc::fence_before();
       __syncwarp();
@@ -1008,14 +1031,16 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       ok = wait(&B.dp, x & 1, &B.dead);
       if (!ok) break;
       tc::fence_after();
-      float c[32];
-      tm_ld32(td, c);
-      tm_wait_ld(c);
-      bwd_grads(a, c, dl, cut, lo, hi);
-      tm_ld32(td + 32, c);
-      tm_wait_ld(c);
-      bwd_grads(b, c, dl + 32, cut, lo - 32, hi - 32);
-      put_parts<PARTS>(a, b, w, td, tm + cX + XB / 2 + lanes);
+#pragma unroll
+      for (int c = 0; c < H; c++) {
+        float g[32];
+        tm_ld32(td + 32 * c, g);
+        tm_wait_ld(g);
+        bwd_grads(a[c], g, dl + 32 * c, cut, lo - 32 * c, hi - 32 * c);
+      }
+      put_parts<PARTS, H>(a, td, x3 + XB / 2);
+      if constexpr (PARTS == 3)
+        if (x > 0) add_columns(sk, tm + cDK + 32 * half + lanes);
       tm_wait_st();
       tc::fence_before();
       __syncwarp();
@@ -1026,11 +1051,20 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       tc::fence_after();
     }
     if (ok) {
-      const int w0 = r & ~31, c = 64 * half;  // (the CTA's own blocks are no longer read)
+      const int w0 = r & ~31, c = PARTS == 3 ? 32 * half : 64 * half;  // (the CTA's own blocks are no longer read)
       const size_t at = ((size_t)(t.k0 + j0 + w0) * P.Hkv + hk) * D + c, ld = (size_t)P.Hkv * D;
       unsigned char* buf = sm + half * HALF + w0 * 128;
-      store_acc(buf, tm + cDV + c + lanes, n > 0, 1.0f, dv + at, ld, nk - w0);
-      store_acc(buf, tm + cDK + c + lanes, n > 0, P.scale, dk + at, ld, nk - w0);
+      if constexpr (PARTS == 3) {
+        if (n > 0) {
+          add_columns(sv, tm + cDV + c + lanes);
+          add_columns(sk, tm + cDK + c + lanes);
+        }
+        store_sums(buf, sv, 1.0f, dv + at, ld, nk - w0);
+        store_sums(buf, sk, P.scale, dk + at, ld, nk - w0);
+      } else {
+        store_acc(buf, tm + cDV + c + lanes, n > 0, 1.0f, dv + at, ld, nk - w0);
+        store_acc(buf, tm + cDK + c + lanes, n > 0, P.scale, dk + at, ld, nk - w0);
+      }
     }
     tc::fence_before();
   }
@@ -1058,7 +1092,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
                  typename Io<PARTS>::T* __restrict__ dq) {
   using F = Bwd<D, PARTS>;
   constexpr int XB = F::XB, EW = F::EW;
-  constexpr uint32_t cS = 0, cDP = XB, cDQ = 2 * XB, cDS = 2 * XB + D, nDS = XB / 2 * PARTS;  // (columns of one dS: its parts)
+  constexpr uint32_t cS = 0, cDP = XB, cDQ = 2 * XB, nDQ = PARTS == 3 ? D : 0, cDS = 2 * XB + D + nDQ, nDS = XB / 2 * PARTS;  // (columns to the other dq; of one dS, its parts)
   extern __shared__ unsigned char raw[];
   __shared__ DqBars B;
   unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
@@ -1162,8 +1196,8 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
         for (int y = 0; y < Q::N; y++)
 #pragma unroll
           for (int s = 0; s < XB / 16; s++)
-            mma_ts(tm + cDQ, tm + cDS + nDS * (x & 1) + XB / 2 * Q::a(y) + 8 * s,
-                   desc_mn<XB>(kb + Q::b(y) * (XB * D * 2), s), id_o, x > 0 || y > 0 || s > 0, me);
+            mma_ts(tm + cDQ + nDQ * (x & 1), tm + cDS + nDS * (x & 1) + XB / 2 * Q::a(y) + 8 * s,
+                   desc_mn<XB>(kb + Q::b(y) * (XB * D * 2), s), id_o, (PARTS == 1 && x > 0) || y > 0 || s > 0, me);
         commit(&B.used[x & 1], me);
         commit(&B.emptyA[x % F::NA], me);
       }
@@ -1182,35 +1216,38 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
     const size_t at = (size_t)h * P.Nq + t.q0 + i0 + r;
     const float nl = in ? -P.lse2[at] : 0.f, nd = in ? -P.delta[at] : 0.f;
     const uint64_t sc = two(P.scale2, P.scale2), l2 = two(nl, nl), dl = two(nd, nd);
+    float sum[PARTS == 3 ? 64 : 1] = {};  // (three parts) dq
     bool ok = true;
     for (int x = 0; x < n; x++) {
       ok = wait(&B.s, x & 1, &B.dead);
       if (!ok) break;
       tc::fence_after();
-      float a[32], b[32], c[32], d[32];
-      tm_ld32(ts, a);
-      tm_ld32(td, c);
-      tm_ld32(ts + 32, b);
-      tm_ld32(td + 32, d);
-      tm_wait_ld(a);
-      tm_wait_ld(b);
-      tm_wait_ld(c);
-      tm_wait_ld(d);
+      float a[2][32], g[2][32];
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        tm_ld32(ts + 32 * c, a[c]);
+        tm_ld32(td + 32 * c, g[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        tm_wait_ld(a[c]);
+        tm_wait_ld(g[c]);
+      }
       tc::fence_before();
       __syncwarp();
       if (lane == 0) mma::mbar_arrive(&B.taken);
       const int left = lim - x * XB - 64 * half;
       const bool cut = x >= clean;
-      dq_grads(a, c, sc, l2, dl, cut, left);
-      dq_grads(b, d, sc, l2, dl, cut, left - 32);
+#pragma unroll
+      for (int c = 0; c < 2; c++) dq_grads(a[c], g[c], sc, l2, dl, cut, left - 32 * c);
       if (x >= 2) {
         ok = wait(&B.used[x & 1], (x / 2 - 1) & 1, &B.dead);
         if (!ok) break;
         tc::fence_after();
+        if constexpr (PARTS == 3) add_columns(sum, tm + cDQ + nDQ * (x & 1) + lanes);  // (block x - 2's)
       }
-      uint32_t w[32];
       const uint32_t to = tm + cDS + nDS * (x & 1) + 32 * half + lanes;
-      put_parts<PARTS>(a, b, w, to, to + 64);
+      put_parts<PARTS, 2>(a, to, to + 64);
       tm_wait_st();
       tc::fence_before();
       __syncwarp();
@@ -1220,7 +1257,14 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       ok = wait(&B.used[(n - 1) & 1], ((n - 1) / 2) & 1, &B.dead);
       tc::fence_after();
     }
-    if (ok) {
+    if constexpr (PARTS == 3) {
+      if (ok) {
+        const int w0 = r & ~31;
+        for (int x = max(0, n - 2); x < n; x++) add_columns(sum, tm + cDQ + nDQ * (x & 1) + lanes);
+        store_sums(sm + w0 * 128, sum, P.scale, dq + ((size_t)(t.q0 + i0 + w0) * P.Hq + h) * D, (size_t)P.Hq * D,
+                   nq - w0);
+      }
+    } else if (ok) {
       const int w0 = r & ~31, c = 64 * half;
       store_acc(sm + half * HALF + w0 * 128, tm + cDQ + c + lanes, n > 0, P.scale,
                 dq + ((size_t)(t.q0 + i0 + w0) * P.Hq + h) * D + c, (size_t)P.Hq * D, nq - w0);
@@ -1257,7 +1301,7 @@ cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, cons
   if (e == cudaSuccess) e = cudaFuncSetAttribute(dqk, cudaFuncAttributeMaxDynamicSharedMemorySize, F::BLOCKS + 1024);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DKV, st);
-  e = launch_pdl(dkv, dim3((unsigned)gk), dim3(F::EW * 32 + 96), DKV_SMEM<D, PARTS>, st, P, xq, mk, mv, xg, (T*)dk,
+  e = launch_pdl(dkv, dim3((unsigned)gk), dim3(F::EWK * 32 + 96), DKV_SMEM<D, PARTS>, st, P, xq, mk, mv, xg, (T*)dk,
                  (T*)dv);
   prof_end(K_SMX_DKV, st);
   if (e != cudaSuccess) return e;
