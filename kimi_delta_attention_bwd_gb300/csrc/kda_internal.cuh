@@ -7,6 +7,8 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include <atomic>
+
 namespace kda {
 
 constexpr int C = 64;          // chunk length (tokens)
@@ -275,6 +277,24 @@ inline cudaError_t launch_cluster(void (*k)(KArgs...), dim3 grid, dim3 block, si
   cfg.numAttrs = pdl ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
+// Before a launch of kernel K: its dynamic shared memory limit, raised once per device.
+template <auto K>
+cudaError_t raise_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  // the driver's tensor-map encoder wants this thread's context bound, which a thread that has made no
+  // runtime call yet (autograd's) lacks
+  e = cudaSetDevice(dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load() & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit);
+  return e;
+}
+
 cudaError_t launch_chunk_table(const int32_t* cu, const Dims& d, const Ws& w, cudaStream_t st);
 cudaError_t launch_fwd_intra(int dtype, const Dims& d, const FwdIO& io, const Ws& w, cudaStream_t st);
 cudaError_t launch_fwd_scan(int dtype, const Dims& d, const FwdIO& io, const Ws& w, cudaStream_t st);

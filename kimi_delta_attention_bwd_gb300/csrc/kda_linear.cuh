@@ -183,24 +183,6 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t (&w)[N]) {
   }
 }
 
-// Before a launch of kernel K: its dynamic shared memory limit, raised once per device.
-template <auto K>
-cudaError_t raise_smem(int bytes) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  // the driver's tensor-map encoder wants this thread's context bound, which a thread that has made no
-  // runtime call yet (autograd's) lacks
-  e = cudaSetDevice(dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (dev < 64 && (done.load() & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) done.fetch_or(bit);
-  return e;
-}
-
 // The fp32 chain (kda_linear_f32.cu): `dec` as in kda_linear.cu.
 cudaError_t launch_f32(int dec, int kid, int key, const LinP& P, const LinOp& op, int fwd, cudaStream_t st);
 

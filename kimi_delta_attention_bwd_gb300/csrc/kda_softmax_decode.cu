@@ -339,13 +339,16 @@ __global__ void __launch_bounds__(WARPS * 32) smx_decode_f32_kernel(DecP P, cons
   finish<D>(P, c, sm, o);
 }
 
-// Joins the pieces of one (sequence, query head): warp w takes pieces w, w + 8, ..
+// Joins the pieces of one (sequence, query head): their weights first, then warp w sums pieces w, w + JW, .. whose loads
+// do not wait for one another (with a running maximum along them 114 pieces took 12.7 us, so 5).
+constexpr int JW = 16;
 template <int D, typename T>
-__global__ void __launch_bounds__(256) smx_join_kernel(DecP P, T* __restrict__ o) {
+__global__ void __launch_bounds__(JW * 32) smx_join_kernel(DecP P, T* __restrict__ o) {
   constexpr int NV = D / 32;
-  __shared__ float sm[8], sl[8], so[8][D];
+  extern __shared__ float sw[];  // [ns]
+  __shared__ float red[JW], so[JW][D];
   const int seq = blockIdx.x / P.Hq, h = blockIdx.x % P.Hq, hk = h / P.G, r = h % P.G;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, rr = r % MH;
   pdl_wait();
   const int L = P.len[seq];
   T* out = o + ((size_t)seq * P.Hq + h) * D;
@@ -353,50 +356,57 @@ __global__ void __launch_bounds__(256) smx_join_kernel(DecP P, T* __restrict__ o
     if (threadIdx.x < D) dec_out(out + threadIdx.x, 0.f);
     return;
   }
-  const float* part = P.part + (((size_t)seq * P.Hkv + hk) * P.HG + r / MH) * P.ns * (MH * (D + 2));
-  const int rr = r % MH;
-  float m = -INFINITY, l = 0.f, acc[NV] = {};
-#pragma unroll 4
-  for (int s = warp; s < P.ns; s += 8) {
-    const float* p = part + (size_t)s * (MH * (D + 2));
-    const float ms = p[rr], ls = p[MH + rr];
-    float x[NV];
-#pragma unroll
-    for (int e = 0; e < NV; e++) x[e] = p[2 * MH + rr * D + lane * NV + e];
-    const float mx = fmaxf(m, ms), mu = mx == -INFINITY ? 0.f : mx, a = ex2(m - mu), b = ex2(ms - mu);
-    m = mx;
-    l = l * a + ls * b;
-#pragma unroll
-    for (int e = 0; e < NV; e++) acc[e] = acc[e] * a + x[e] * b;
+  constexpr size_t ST = MH * (D + 2);
+  const float* part = P.part + (((size_t)seq * P.Hkv + hk) * P.HG + r / MH) * P.ns * ST;
+  float m = -INFINITY;
+  for (int s = threadIdx.x; s < P.ns; s += JW * 32) {
+    sw[s] = part[s * ST + rr];
+    m = fmaxf(m, sw[s]);
   }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < JW; w++) m = fmaxf(m, red[w]);
+  const float mu = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  for (int s = threadIdx.x; s < P.ns; s += JW * 32) {
+    sw[s] = ex2(sw[s] - mu);
+    l += sw[s] * part[s * ST + MH + rr];
+  }
+  l = warp_sum(l);
+  __syncthreads();  // (red is read, the weights are there)
+  if (lane == 0) red[warp] = l;
+  float acc[NV] = {};
+  const float* p = part + 2 * MH + rr * D + lane * NV;
+#pragma unroll 8
+  for (int s = warp; s < P.ns; s += JW) {
+    const float w = sw[s];
+#pragma unroll
+    for (int e = 0; e < NV; e++) acc[e] = fmaf(w, p[s * ST + e], acc[e]);
   }
 #pragma unroll
   for (int e = 0; e < NV; e++) so[warp][lane * NV + e] = acc[e];
   __syncthreads();
   if (threadIdx.x < D) {
-    float mx = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 8; w++) mx = fmaxf(mx, sm[w]);
-    const float mu = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f, x = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; w++) {
-      const float e = ex2(sm[w] - mu);
-      sum += e * sl[w];
-      x += e * so[w][threadIdx.x];
+    for (int w = 0; w < JW; w++) {
+      sum += red[w];
+      x += so[w][threadIdx.x];
     }
     dec_out(out + threadIdx.x, x / sum);
   }
 }
 
-// Pieces of a sequence: enough CTAs for three on each of 152 SMs, none of fewer than 128 keys of a full cache.
-int pieces(int64_t units, int cap) {
-  const int64_t want = (3 * 152 + units - 1) / units, most = ((int64_t)cap + 127) / 128;
-  const int64_t n = want < most ? want : most;
-  return (int)(n < 1 ? 1 : n);
+// Pieces of a sequence, none of fewer than 128 keys of a full cache: for one sequence as many as the CTAs that 152
+// SMs hold (three each), so that its equal pieces are one wave; several sequences differ in length, and smaller pieces
+// even that out.
+int pieces(int n, int64_t units, int cap) {
+  const int64_t want = ((n == 1 ? 3 : 8) * 152 + units - 1) / units, most = ((int64_t)cap + 127) / 128;
+  const int64_t ns = want < most ? want : most;
+  return (int)(ns < 1 ? 1 : ns);
 }
 
 bool sizes_ok(int n, int cap, int Hq, int Hkv, int dtype) {
@@ -422,9 +432,9 @@ cudaError_t launch(const DecP& P, int dtype, const void* q, const void* k, const
   if (e != cudaSuccess || P.ns == 1) return e;
   prof_begin(K_SMX_JOIN, st);
   if (dtype == KDA_BF16)
-    e = launch_pdl(smx_join_kernel<D, bf16>, dim3(P.n * P.Hq), dim3(256), 0, st, P, (bf16*)o);
+    e = launch_pdl(smx_join_kernel<D, bf16>, dim3(P.n * P.Hq), dim3(JW * 32), P.ns * sizeof(float), st, P, (bf16*)o);
   else
-    e = launch_pdl(smx_join_kernel<D, float>, dim3(P.n * P.Hq), dim3(256), 0, st, P, (float*)o);
+    e = launch_pdl(smx_join_kernel<D, float>, dim3(P.n * P.Hq), dim3(JW * 32), P.ns * sizeof(float), st, P, (float*)o);
   prof_end(K_SMX_JOIN, st);
   return e;
 }
@@ -439,7 +449,7 @@ using namespace kda::smx;
 extern "C" KDA_API size_t kda_softmax_decode_workspace_size(int n_seq, int cap, int Hq, int Hkv, int D) {
   if (!sizes_ok(n_seq, cap, Hq, Hkv, KDA_BF16) || (D != 64 && D != 128)) return 0;
   const int64_t units = (int64_t)n_seq * Hkv * ((Hq / Hkv + MH - 1) / MH);
-  const int ns = pieces(units, cap);
+  const int ns = pieces(n_seq, units, cap);
   return 256 + (ns == 1 ? 0 : (size_t)units * ns * MH * (D + 2) * sizeof(float));
 }
 
@@ -462,7 +472,7 @@ extern "C" KDA_API kda_status kda_softmax_decode(int n_seq, int cap, int Hq, int
   P.Hkv = Hkv;
   P.G = Hq / Hkv;
   P.HG = (P.G + MH - 1) / MH;
-  P.ns = pieces((int64_t)n_seq * Hkv * P.HG, cap);
+  P.ns = pieces(n_seq, (int64_t)n_seq * Hkv * P.HG, cap);
   P.scale2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
   P.len = lengths;
   P.err = (int32_t*)workspace;

@@ -278,17 +278,6 @@ __global__ void __launch_bounds__(NT) smx_dq_kernel(SmxP P, const float* __restr
   }
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch(int kid, void (*kern)(KArgs...), int64_t grid, size_t smem, cudaStream_t st, Args... args) {
-  if (grid <= 0 || grid > 2147483647) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  prof_begin(kid, st);
-  e = launch_pdl(kern, dim3((unsigned)grid), dim3(NT), smem, st, args...);
-  prof_end(kid, st);
-  return e;
-}
-
 }  // namespace
 
 cudaError_t launch_f32_bwd(const SmxP& P, const float* q, const float* k, const float* v, const float* dO, float* dq,
@@ -296,9 +285,19 @@ cudaError_t launch_f32_bwd(const SmxP& P, const float* q, const float* k, const 
   constexpr int D = 128, R = F32_TILE / 16;
   const size_t s1 = (2 * D * 16 * R + 4 * D * TM + TM * PP<R> + 2 * TM) * sizeof(float);
   const size_t s2 = (2 * D * 16 * R + 3 * D * TM + TM * PP<R>) * sizeof(float);
-  cudaError_t e = launch(K_SMX_DKV, smx_dkv_kernel<D, R>, (int64_t)max_tiles(P, 2) * P.Hkv, s1, st, P, q, k, v, dO, dk, dv);
+  const int64_t gk = (int64_t)max_tiles(P, 2) * P.Hkv, gq = (int64_t)max_tiles(P, 1) * P.Hq;
+  if (gk > 2147483647 || gq > 2147483647) return cudaErrorInvalidValue;
+  cudaError_t e = raise_smem<smx_dkv_kernel<D, R>>((int)s1);
+  if (e == cudaSuccess) e = raise_smem<smx_dq_kernel<D, R>>((int)s2);
   if (e != cudaSuccess) return e;
-  return launch(K_SMX_DQ, smx_dq_kernel<D, R>, (int64_t)max_tiles(P, 1) * P.Hq, s2, st, P, q, k, v, dO, dq);
+  prof_begin(K_SMX_DKV, st);
+  e = launch_pdl(smx_dkv_kernel<D, R>, dim3((unsigned)gk), dim3(NT), s1, st, P, q, k, v, dO, dk, dv);
+  prof_end(K_SMX_DKV, st);
+  if (e != cudaSuccess) return e;
+  prof_begin(K_SMX_DQ, st);
+  e = launch_pdl(smx_dq_kernel<D, R>, dim3((unsigned)gq), dim3(NT), s2, st, P, q, k, v, dO, dq);
+  prof_end(K_SMX_DQ, st);
+  return e;
 }
 
 }  // namespace smx

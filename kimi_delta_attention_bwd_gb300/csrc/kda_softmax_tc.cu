@@ -704,17 +704,16 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
 template <int D, int PARTS>
 cudaError_t fwd(const SmxP& P, const void* q, const void* k, const void* v, void* o, float* lse, cudaStream_t st) {
   using F = Fwd<D, PARTS>;
+  cudaError_t e = raise_smem<smx_tc_fwd_kernel<D, PARTS>>(F::SMEM);
+  if (e != cudaSuccess) return e;
   CUtensorMap mq, mk, mv;
   if (!encode_head_rows(&mq, q, PARTS * P.Nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, PARTS * P.Nk, P.Hkv, D, F::XB) ||
       !encode_head_rows(&mv, v, PARTS * P.Nk, P.Hkv, D, F::XB))
     return cudaErrorInvalidValue;
   const int64_t grid = (int64_t)max_tiles(P, 0) * P.Hq;
   if (grid > 2147483647) return cudaErrorInvalidValue;
-  auto kern = smx_tc_fwd_kernel<D, PARTS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
-  if (e != cudaSuccess) return e;
   prof_begin(K_SMX_FWD, st);
-  e = launch_pdl(kern, dim3((unsigned)grid), dim3(F::THREADS), F::SMEM, st, P, mq, mk, mv,
+  e = launch_pdl(smx_tc_fwd_kernel<D, PARTS>, dim3((unsigned)grid), dim3(F::THREADS), F::SMEM, st, P, mq, mk, mv,
                  (typename Io<PARTS>::T*)o, lse);
   prof_end(K_SMX_FWD, st);
   return e;
@@ -1284,6 +1283,9 @@ cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, cons
                 void* dv, cudaStream_t st) {
   using F = Bwd<D, PARTS>;
   using T = typename Io<PARTS>::T;
+  cudaError_t e = raise_smem<smx_tc_dkv_kernel<D, PARTS>>(DKV_SMEM<D, PARTS>);
+  if (e == cudaSuccess) e = raise_smem<smx_tc_dq_kernel<D, PARTS>>(F::BLOCKS + 1024);
+  if (e != cudaSuccess) return e;
   CUtensorMap mq, mk, mv, mg, xq, xk, xv, xg;  // blocks of 128 rows, and of the other side's XB
   const int nq = PARTS * P.Nq, nk = PARTS * P.Nk;
   if (!encode_head_rows(&mq, q, nq, P.Hq, D, BLK) || !encode_head_rows(&mk, k, nk, P.Hkv, D, BLK) ||
@@ -1295,18 +1297,13 @@ cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, cons
     return cudaErrorInvalidValue;
   const int64_t gk = (int64_t)max_tiles(P, 2) * P.Hkv, gq = (int64_t)max_tiles(P, 1) * P.Hq;
   if (gk > 2147483647 || gq > 2147483647) return cudaErrorInvalidValue;
-  auto dkv = smx_tc_dkv_kernel<D, PARTS>;
-  auto dqk = smx_tc_dq_kernel<D, PARTS>;
-  cudaError_t e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, DKV_SMEM<D, PARTS>);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(dqk, cudaFuncAttributeMaxDynamicSharedMemorySize, F::BLOCKS + 1024);
-  if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DKV, st);
-  e = launch_pdl(dkv, dim3((unsigned)gk), dim3(F::EWK * 32 + 96), DKV_SMEM<D, PARTS>, st, P, xq, mk, mv, xg, (T*)dk,
+  e = launch_pdl(smx_tc_dkv_kernel<D, PARTS>, dim3((unsigned)gk), dim3(F::EWK * 32 + 96), DKV_SMEM<D, PARTS>, st, P, xq, mk, mv, xg, (T*)dk,
                  (T*)dv);
   prof_end(K_SMX_DKV, st);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DQ, st);
-  e = launch_pdl(dqk, dim3((unsigned)gq), dim3(F::EW * 32 + 64), F::BLOCKS + 1024, st, P, mq, xk, xv, mg, (T*)dq);
+  e = launch_pdl(smx_tc_dq_kernel<D, PARTS>, dim3((unsigned)gq), dim3(F::EW * 32 + 64), F::BLOCKS + 1024, st, P, mq, xk, xv, mg, (T*)dq);
   prof_end(K_SMX_DQ, st);
   return e;
 }

@@ -58,47 +58,58 @@ def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, sca
 
 
 def _rotate(inverse, q, k, inv_freq, positions, cu_seqlens, interleaved, scale, out_q, out_k):
-    if q.dim() not in (3, 4):
-        raise ValueError(f"q must be [B, T, H, D] or [n, H, D], got shape {tuple(q.shape)}")
-    lead, (Hq, D) = q.shape[:-2], q.shape[-2:]
+    qs = q.shape
+    if len(qs) not in (3, 4):
+        raise ValueError(f"q must be [B, T, H, D] or [n, H, D], got shape {tuple(qs)}")
+    lead, (Hq, D) = qs[:-2], qs[-2:]
     _dims(inv_freq, "inv_freq", 1)
     rot = 2 * inv_freq.numel()
     if not 0 < rot <= D:
         raise ValueError(f"inv_freq of {rot // 2} pairs for heads of {D} values")
     if not scale > 0:
         raise ValueError(f"scale must be positive, got {scale}")
-    io = q.dtype
+    io, i32 = q.dtype, torch.int32
+    specs, names = [(q, qs, io), (inv_freq, inv_freq.shape, torch.float32)], ["q", "inv_freq"]
     Hkv = 0
     if k is not None:
-        _dims(k, "k", q.dim())
+        _dims(k, "k", len(qs))
         Hkv = k.shape[-2]
-    if positions is not None and cu_seqlens is not None:
-        raise ValueError("positions or cu_seqlens, not both")
-    if cu_seqlens is not None:
+        specs.append((k, (*lead, Hkv, D), io))
+        names.append("k")
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    if positions is not None:
+        if cu_seqlens is not None:
+            raise ValueError("positions or cu_seqlens, not both")
+        specs.append((positions, lead, i32))
+        names.append("positions")
+    elif cu_seqlens is not None:
         _dims(cu_seqlens, "cu_seqlens", 1)
         if cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must hold at least two offsets")
-    elif positions is None and q.dim() == 3:
+        specs.append((cu_seqlens, cu_seqlens.shape, i32))
+        names.append("cu_seqlens")
+    elif len(qs) == 3:
         raise ValueError("single tokens [n, H, D] need positions")
-    kshape = (*lead, Hkv, D)
-    specs = dict(q=(q, q.shape, io), k=(k, kshape, io), inv_freq=(inv_freq, inv_freq.shape, torch.float32),
-                 positions=(positions, lead, torch.int32), out_q=(out_q, q.shape, io), out_k=(out_k, kshape, io),
-                 cu_seqlens=(cu_seqlens, cu_seqlens.shape if cu_seqlens is not None else None, torch.int32))
-    if k is None and out_k is not None:
-        raise ValueError("out_k without k")
-    if not _all_well(*[s for s in specs.values() if s[0] is not None]):
-        _require(**specs)
-    in_place = out_q is not None and out_q.data_ptr() == q.data_ptr()
-    if out_q is not None:
-        _apart("out_q", out_q, ("q",), q=q, k=k, inv_freq=inv_freq, positions=positions)
-    if out_k is not None:
-        _apart("out_k", out_k, ("k",), q=q, k=k, out_q=out_q, inv_freq=inv_freq, positions=positions)
-    if k is not None and in_place != (out_k is not None and out_k.data_ptr() == k.data_ptr()):
-        raise ValueError("q and k are turned in place together or not at all")
+    for name, t, shape in (("out_q", out_q, qs), ("out_k", out_k, (*lead, Hkv, D))):
+        if t is not None:
+            specs.append((t, shape, io))
+            names.append(name)
+    if not _all_well(*specs):
+        _require(**dict(zip(names, specs)))
+    if out_q is not None or out_k is not None:
+        in_place = out_q is not None and out_q.data_ptr() == q.data_ptr()
+        if out_q is not None:
+            _apart("out_q", out_q, ("q",), q=q, k=k, inv_freq=inv_freq, positions=positions, cu_seqlens=cu_seqlens)
+        if out_k is not None:
+            _apart("out_k", out_k, ("k",), q=q, k=k, out_q=out_q, inv_freq=inv_freq, positions=positions,
+                   cu_seqlens=cu_seqlens)
+        if k is not None and in_place != (out_k is not None and out_k.data_ptr() == k.data_ptr()):
+            raise ValueError("q and k are turned in place together or not at all")
     y = out_q if out_q is not None else torch.empty_like(q)
     z = None if k is None else out_k if out_k is not None else torch.empty_like(k)
-    n = q.numel() // (Hq * D) if Hq * D else 0
-    _lib.kda_rotary(n, q.shape[1] if q.dim() == 4 else 1, Hq, Hkv, D, rot, io, interleaved, inverse, scale, inv_freq,
+    n = q.numel() // (Hq * D) if Hq else 0
+    _lib.kda_rotary(n, qs[1] if len(qs) == 4 else 1, Hq, Hkv, D, rot, io, interleaved, inverse, scale, inv_freq,
                     positions, cu_seqlens, q, k, y, z)
     return y, z
 

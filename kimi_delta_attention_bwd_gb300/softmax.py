@@ -37,22 +37,11 @@ class SoftmaxContext:
     stream: Optional[int] = None  # the workspace's, where the forward allocated it
 
 
-def _scale(scale):
-    if scale is not None and not scale > 0:
-        raise ValueError(f"scale must be positive, got {scale}")
-    return scale
-
-
 def _offsets(cu, name):
     if cu is not None:
         _dims(cu, name, 1)
         if cu.numel() < 2:
             raise ValueError(f"{name} must hold at least two offsets")
-
-
-def _groups(Hq, Hkv):
-    if Hkv == 0 or Hq % Hkv:
-        raise ValueError(f"{Hq} query heads are not a multiple of {Hkv} key heads")
 
 
 def kda_softmax_forward(q, k, v, scale: Optional[float] = None, causal: bool = True, cu_seqlens=None,
@@ -65,34 +54,45 @@ def kda_softmax_forward(q, k, v, scale: Optional[float] = None, causal: bool = T
     (> 0).  out: optional preallocated o that shares no memory with the inputs."""
     _dims(q, "q", 4)
     _dims(k, "k", 4)
-    B, T, Hq, D = q.shape
-    Tk, Hkv = k.shape[1], k.shape[2]
-    io, i32 = q.dtype, torch.int32
-    _groups(Hq, Hkv)
-    _offsets(cu_seqlens, "cu_seqlens")
-    if cu_seqlens_k is not None:
+    qs = q.shape
+    B, T, Hq, D = qs
+    _, Tk, Hkv, _ = k.shape
+    io, keys = q.dtype, (B, Tk, Hkv, D)
+    if Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hkv} key heads")
+    specs = [(q, qs, io), (k, keys, io), (v, keys, io)]
+    names = ["q", "k", "v"]
+    if cu_seqlens is not None or cu_seqlens_k is not None or cu_seqlens_host is not None \
+            or cu_seqlens_k_host is not None:
+        _offsets(cu_seqlens, "cu_seqlens")
         _offsets(cu_seqlens_k, "cu_seqlens_k")
-        if cu_seqlens is None:
+        if cu_seqlens_k is not None and cu_seqlens is None:
             raise ValueError("cu_seqlens_k comes with cu_seqlens")
-    elif cu_seqlens is not None and T != Tk:
-        raise ValueError(f"{B * Tk} keys for {B * T} queries need cu_seqlens_k")
-    cu_seqlens_host = _host_offsets(cu_seqlens_host, cu_seqlens)
-    if cu_seqlens_k_host is not None and cu_seqlens_k is None:
-        raise ValueError("cu_seqlens_k_host comes with cu_seqlens_k")
-    cu_seqlens_k_host = _host_offsets(cu_seqlens_k_host, cu_seqlens_k)
-    n = 0 if cu_seqlens is None else cu_seqlens.numel()
-    keys = (B, Tk, Hkv, D)
-    specs = dict(q=(q, q.shape, io), k=(k, keys, io), v=(v, keys, io), out=(out, q.shape, io),
-                 cu_seqlens=(cu_seqlens, (n,), i32), cu_seqlens_k=(cu_seqlens_k, (n,), i32))
-    if not _all_well(*[s for s in specs.values() if s[0] is not None]):
-        _require(**specs)
+        if cu_seqlens_k is None and T != Tk and cu_seqlens is not None:
+            raise ValueError(f"{B * Tk} keys for {B * T} queries need cu_seqlens_k")
+        cu_seqlens_host = _host_offsets(cu_seqlens_host, cu_seqlens)
+        if cu_seqlens_k_host is not None and cu_seqlens_k is None:
+            raise ValueError("cu_seqlens_k_host comes with cu_seqlens_k")
+        cu_seqlens_k_host = _host_offsets(cu_seqlens_k_host, cu_seqlens_k)
+        n = cu_seqlens.numel()
+        for name, cu in (("cu_seqlens", cu_seqlens), ("cu_seqlens_k", cu_seqlens_k)):
+            if cu is not None:
+                specs.append((cu, (n,), torch.int32))
+                names.append(name)
+        if save_for_backward:  # (a buffer that the next batch's offsets overwrite must not change what is checked)
+            cu_seqlens_host, cu_seqlens_k_host = (
+                c if c is None else c.clone() if isinstance(c, torch.Tensor) else c.copy()
+                for c in (cu_seqlens_host, cu_seqlens_k_host))
+    if out is not None:
+        specs.append((out, qs, io))
+        names.append("out")
+    if not _all_well(*specs):
+        _require(**dict(zip(names, specs)))
     if out is not None:
         _apart("out", out, q=q, k=k, v=v)
-    if save_for_backward:  # (a buffer that the next batch's offsets overwrite must not change what the backward checks)
-        cu_seqlens_host, cu_seqlens_k_host = (
-            c if c is None else c.clone() if isinstance(c, torch.Tensor) else c.copy()
-            for c in (cu_seqlens_host, cu_seqlens_k_host))
-    prob = _lib.make_softmax_problem(B, T, Tk, Hq, Hkv, D, io, _scale(scale), causal, cu_seqlens, cu_seqlens_k,
+    if scale is not None and not scale > 0:
+        raise ValueError(f"scale must be positive, got {scale}")
+    prob = _lib.make_softmax_problem(B, T, Tk, Hq, Hkv, D, io, scale, causal, cu_seqlens, cu_seqlens_k,
                                      cu_seqlens_host, cu_seqlens_k_host)
     stream = None
     if workspace is None:
@@ -139,28 +139,41 @@ def kda_softmax_decode_step(q, k, v, k_cache, v_cache, lengths, scale: Optional[
     Returns o [n, Hq, D]."""
     _dims(q, "q", 3)
     _dims(k_cache, "k_cache", 4)
-    n, Hq, D = q.shape
-    cap, Hkv = k_cache.shape[1], k_cache.shape[2]
-    io = q.dtype
-    _groups(Hq, Hkv)
-    new, cache = (n, Hkv, D), (n, cap, Hkv, D)
-    specs = ((q, q.shape, io), (k, new, io), (v, new, io), (k_cache, cache, io), (v_cache, cache, io),
+    qs, cache = q.shape, k_cache.shape
+    n, Hq, D = qs
+    _, cap, Hkv, _ = cache
+    io, new = q.dtype, (n, Hkv, D)
+    if Hkv == 0 or Hq % Hkv:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hkv} key heads")
+    if cache[0] != n or cache[3] != D:
+        raise ValueError(f"k_cache must have shape {(n, cap, Hkv, D)}, got {tuple(cache)}")
+    specs = ((q, qs, io), (k, new, io), (v, new, io), (k_cache, cache, io), (v_cache, cache, io),
              (lengths, (n,), torch.int32))
     if out is not None:
-        specs += ((out, q.shape, io),)
+        specs += ((out, qs, io),)
     if not _all_well(*specs):
         _require(**dict(zip(("q", "k", "v", "k_cache", "v_cache", "lengths", "out"), specs)))
-    _apart("k_cache", k_cache, q=q, k=k, v=v, v_cache=v_cache)
-    _apart("v_cache", v_cache, q=q, k=k, v=v)
+    # the caches share no memory with the other tensors or with each other (the named checks say which)
+    kc, vc, size = k_cache.data_ptr(), v_cache.data_ptr(), k_cache.numel() * k_cache.element_size()
+    near = kc < vc + size and vc < kc + size
+    for t in (q, k, v):
+        a = t.data_ptr()
+        b = a + t.numel() * t.element_size()
+        near = near or (a < kc + size and kc < b) or (a < vc + size and vc < b)
+    if near:
+        _apart("k_cache", k_cache, q=q, k=k, v=v, v_cache=v_cache)
+        _apart("v_cache", v_cache, q=q, k=k, v=v)
     if out is not None:
         _apart("out", out, q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache)
+    if scale is not None and not scale > 0:
+        raise ValueError(f"scale must be positive, got {scale}")
     if workspace is None:
         workspace = torch.empty(_lib.kda_softmax_decode_workspace_size(n, cap, Hq, Hkv, D) or 1, dtype=torch.uint8,
                                 device=q.device)
     else:
         _require(workspace=(workspace, workspace.shape, torch.uint8))
     o = out if out is not None else torch.empty_like(q)
-    _lib.kda_softmax_decode(n, cap, Hq, Hkv, D, io, _scale(scale), q, k, v, k_cache, v_cache, lengths, o, workspace)
+    _lib.kda_softmax_decode(n, cap, Hq, Hkv, D, io, scale, q, k, v, k_cache, v_cache, lengths, o, workspace)
     return o
 
 
