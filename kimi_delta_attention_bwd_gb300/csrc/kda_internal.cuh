@@ -55,6 +55,7 @@ enum KernelId {
   K_SMX_DECODE,
   K_SMX_JOIN,
   K_SMX_SPLIT,
+  K_SMX_JOIN_ROWS,
   K_ROTARY,
   K_COUNT
 };

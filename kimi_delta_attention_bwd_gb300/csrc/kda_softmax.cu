@@ -13,6 +13,11 @@ namespace {
 // 2), by decreasing pairs, so that the longest tiles start first and the grid's
 // end is short ones (a counting sort; tiles of equal weight in any order, which no
 // result depends on).  The offsets are checked before any of them is used.
+// The forward's tiles with more than 1.5 times the load that `target` CTAs would have on
+// average are cut along their keys into pieces of about that load, which a further kernel
+// joins: a few queries against long prefixes would else leave most SMs idle behind the
+// longest (11 pieces of prompts, 4096 queries on 30011 keys: 127 us whole, 97 cut; 128 queries
+// of 16 heads on 16384 keys: 176 and 51).
 constexpr int TT = 1024, NB = 1024;
 
 __device__ int incl_scan(int x, int* s_warp, int* total) {
@@ -41,15 +46,28 @@ __device__ int incl_scan(int x, int* s_warp, int* total) {
 }
 
 __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P, int l0) {
-  __shared__ int s_bad, s_warp[32], s_cnt[NB];
+  constexpr int NS = 1024;  // documents whose offsets shared memory holds
+  __shared__ int s_bad, s_piece, s_join, s_warp[32], s_cnt[NB], s_off[3][NS + 1];
   const int l = l0 + blockIdx.x, tid = threadIdx.x, n = P.n_docs, tile = P.tile[l];
-  const bool by_key = l == 2;
+  const bool by_key = l == 2, near = n <= NS;
   pdl_wait();
   pdl_release();
   const bool ok = l0 == 0 || (*P.wtag == P.tag && *P.err == KDA_OK);  // (block 0 may not write these before block 1 reads)
-  const int32_t *cu = P.cu, *cuk = P.cuk, *own = by_key ? cuk : cu;
-  if (tid == 0) s_bad = cu[0] != 0 || cu[n] != P.Nq || cuk[0] != 0 || cuk[n] != P.Nk;
+  const int32_t *cu = P.cu, *cuk = P.cuk;
+  int32_t* pre = P.pre[l];
+  if (near) {
+    for (int i = tid; i <= n; i += TT) {
+      s_off[0][i] = P.rows ? i * P.T : cu[i];
+      s_off[1][i] = P.rows ? i * P.Tk : cuk[i];
+    }
+    cu = s_off[0];
+    cuk = s_off[1];
+    pre = s_off[2];
+  }
+  const int32_t* own = by_key ? cuk : cu;
+  if (tid == 0) s_bad = 0;
   __syncthreads();
+  if (tid == 0 && (cu[0] != 0 || cu[n] != P.Nq || cuk[0] != 0 || cuk[n] != P.Nk)) s_bad = 1;
   for (int i = tid; i < n; i += TT)
     if (cu[i + 1] < cu[i] || cuk[i + 1] < cuk[i]) s_bad = 1;
   __syncthreads();
@@ -68,43 +86,116 @@ __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P, int l0) {
     const int i = base + tid, nt = i < n ? (own[i + 1] - own[i] + tile - 1) / tile : 0;
     int total;
     const int r = carry + incl_scan(nt, s_warp, &total) - nt;
-    if (i < n) P.pre[l][i] = r;
+    if (i < n) pre[i] = r;
     carry += total;
   }
-  if (tid == 0) {
-    P.pre[l][n] = carry;
-    P.counts[l] = carry;
-  }
   for (int b = tid; b < NB; b += TT) s_cnt[b] = 0;
+  if (tid == 0) s_piece = s_join = 0;
   __syncthreads();
-  auto find = [&](int x, int4& a, int& t) -> int {  // tile x in the documents' order; its bucket, heavy ones first
+  struct Found {
+    int4 doc;
+    int t, w;  // tile of the document; its pairs a row: keys (queries)
+  };
+  auto find = [&](int x) -> Found {  // tile x in the documents' order
     int lo = 0, hi = n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (P.pre[l][mid] <= x) lo = mid;
+      if (pre[mid] <= x) lo = mid;
       else hi = mid - 1;
     }
-    t = x - P.pre[l][lo];
-    a = make_int4(cu[lo], cu[lo + 1] - cu[lo], cuk[lo], cuk[lo + 1] - cuk[lo]);
-    const int w = by_key ? a.y - first_query(P.causal, t * tile, a.y, a.w)
-                         : keys_of(P.causal, min(a.y, (t + 1) * tile) - 1, a.y, a.w);
-    return NB - 1 - min(NB - 1, (w + 63) >> 6);
+    Found f;
+    f.t = x - pre[lo];
+    f.doc = make_int4(cu[lo], cu[lo + 1] - cu[lo], cuk[lo], cuk[lo + 1] - cuk[lo]);
+    f.w = by_key ? f.doc.y - first_query(P.causal, f.t * tile, f.doc.y, f.doc.w)
+                 : keys_of(P.causal, min(f.doc.y, (f.t + 1) * tile) - 1, f.doc.y, f.doc.w);
+    return f;
   };
-  int4 a;
-  int t;
-  for (int x = tid; x < carry; x += TT) atomicAdd(&s_cnt[find(x, a, t)], 1);
+  const bool may_cut = l == 0 && P.target > 0;
+  int per = INT_MAX / 2;  // blocks a piece
+  if (may_cut) {
+    int blocks = 0, total;
+    for (int x = tid; x < carry; x += TT) blocks += (find(x).w + P.xb - 1) / P.xb;
+    incl_scan(blocks, s_warp, &total);
+    per = max(512 / P.xb, (int)(((int64_t)total * P.Hq + P.target - 1) / P.target));
+  }
+  auto pieces_of = [&](const Found& f) {
+    const int nb = (f.w + P.xb - 1) / P.xb;
+    return may_cut && nb > per + per / 2 ? (nb + per - 1) / per : 1;
+  };
+  auto bucket = [&](const Found& f, int np) { return NB - 1 - min(NB - 1, (f.w / np + 63) >> 6); };
+  for (int x = tid; x < carry; x += TT) {
+    const Found f = find(x);
+    const int np = pieces_of(f);
+    atomicAdd(&s_cnt[bucket(f, np)], np);
+  }
   __syncthreads();
+  int entries;
   {
     static_assert(NB == TT, "a bucket a thread");
-    int total;
-    const int c = s_cnt[tid], r = incl_scan(c, s_warp, &total) - c;
+    const int c = s_cnt[tid], r = incl_scan(c, s_warp, &entries) - c;
     s_cnt[tid] = r;
   }
   __syncthreads();
   for (int x = tid; x < carry; x += TT) {
-    const int at = atomicAdd(&s_cnt[find(x, a, t)], 1);
-    P.list[l][2 * (size_t)at] = a;
-    P.list[l][2 * (size_t)at + 1] = make_int4(t, 0, 0, 0);
+    const Found f = find(x);
+    const int np = pieces_of(f), at = atomicAdd(&s_cnt[bucket(f, np)], np), nb = (f.w + P.xb - 1) / P.xb;
+    int first = -1;
+    if (np > 1) {  // (the room is the bound that the host forms from the same rule)
+      first = atomicAdd(&s_piece, np);
+      const int j = atomicAdd(&s_join, 1), i0 = f.t * tile;
+      P.joins[j] = make_int4(f.doc.x + i0, min(tile, f.doc.y - i0), first, np);
+    }
+    const int len = (nb + np - 1) / np;
+    for (int y = 0; y < np; y++) {
+      P.list[l][2 * (size_t)(at + y)] = f.doc;
+      P.list[l][2 * (size_t)(at + y) + 1] =
+          np > 1 ? make_int4(f.t, y * len, (y + 1) * len, first + y) : make_int4(f.t, 0, INT_MAX, -1);
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    P.counts[l] = entries;
+    if (l == 0) P.counts[3] = s_join;
+  }
+}
+
+// Joins the pieces of the cut tiles, a warp a row: o = sum_p 2^(l_p - l) o_p, 2^l = sum_p 2^l_p.
+template <int D, typename T>
+__global__ void __launch_bounds__(256) smx_join_rows_kernel(SmxP P, T* __restrict__ o, float* __restrict__ lse) {
+  constexpr int NV = D / 32;
+  pdl_wait();
+  const int tile = P.tile[0], lane = threadIdx.x % 32;
+  const size_t step = (size_t)P.Hq * tile;
+  const int rows = P.counts[0] == 0 ? 0 : P.counts[3] * tile * P.Hq;  // (at most pieces / 2 tiles of them)
+  for (int x = blockIdx.x * 8 + threadIdx.x / 32; x < rows; x += gridDim.x * 8) {
+    const int h = x % P.Hq, r = x / P.Hq % tile;
+    const int4 e = P.joins[x / (P.Hq * tile)];
+    if (r >= e.y) continue;
+    const size_t at = ((size_t)e.z * P.Hq + h) * tile + r;
+    float m = -INFINITY;
+    for (int p = 0; p < e.w; p++) m = fmaxf(m, P.pl[at + p * step]);
+    const float mu = m == -INFINITY ? 0.f : m;
+    float sum = 0.f, acc[NV] = {};
+#pragma unroll 4
+    for (int p = 0; p < e.w; p++) {
+      const float l = P.pl[at + p * step], w = l == -INFINITY ? 0.f : ex2(l - mu);  // (NaN stays)
+      sum += w;
+#pragma unroll
+      for (int y = 0; y < NV; y++) acc[y] = fmaf(w, P.po[(at + p * step) * D + lane * NV + y], acc[y]);
+    }
+    const size_t row = (size_t)(e.x + r) * P.Hq + h;
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum, l2 = sum != sum ? sum : m + log2f(sum);
+#pragma unroll
+    for (int y = 0; y < NV; y++) {
+      const float z = acc[y] * inv;
+      stf(o + row * D + lane * NV + y, z);
+      if constexpr (sizeof(T) == 2)
+        if (P.save) stf(P.res + row * D + lane * NV + y, z - __bfloat162float(__float2bfloat16_rn(z)));
+    }
+    if (lane == 0) {
+      lse[row] = l2 * LN2;
+      if (P.save) P.lse2[(size_t)h * P.Nq + e.x + r] = l2;
+    }
   }
 }
 
@@ -155,6 +246,22 @@ __global__ void __launch_bounds__(256) smx_delta_kernel(SmxP P, const T* __restr
 // ------------------------------------------------------------ host
 bool a16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
+// Whether equal rows have tiles to cut (the table kernel's rule on their heaviest tile).
+bool worth_cutting(const SmxP& P) {
+  const int tile = P.tile[0], nt = (P.T + tile - 1) / tile;
+  int64_t total = 0;
+  int most = 0;
+  for (int t = 0; t < nt; t++) {
+    const int last = (t + 1) * tile < P.T ? (t + 1) * tile : P.T;
+    const int nb = (keys_of(P.causal, last - 1, P.T, P.Tk) + P.xb - 1) / P.xb;
+    total += nb;
+    most = nb > most ? nb : most;
+  }
+  int64_t per = (total * P.B * P.Hq + P.target - 1) / P.target;
+  if (per < 512 / P.xb) per = 512 / P.xb;
+  return most > per + per / 2;
+}
+
 bool offsets_ok(const int32_t* c, int n, int64_t end) {
   if (c[0] != 0 || c[n] != end) return false;
   for (int i = 0; i < n; i++)
@@ -203,6 +310,18 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   P.scale2 = P.scale * LOG2E;
   const int parts = p->dtype == KDA_F32 ? 3 : 1;
   for (int l = 0; l < 3; l++) P.tile[l] = parts == 3 && p->D == 128 && l > 0 ? F32_TILE : tc_tile(p->D, parts, l);
+  // The forward's cut tiles: where whole tiles would be fewer than four for each of 152 SMs, and some could have more
+  // than a few blocks of keys; a CTA's load is the average of one CTA per SM (half of that, at D = 64 with its two
+  // CTAs, cut tiles of the packed 300M step whose join took what it gave; twice as many pieces for either head dim
+  // lost 3 to 10%).
+  P.xb = tc_block(p->D, parts);
+  const int wave = 152;
+  if ((int64_t)max_tiles(P, 0) * P.Hq <= 4 * wave && (P.rows ? P.Tk : P.Nk) > 1024 && (!P.rows || P.B <= 1024)) {
+    P.target = wave;
+    // a tile of q > 1.5 average loads has ceil(q) pieces, at most 1.5 q, and all tiles' q sum to at most target / Hq
+    P.pieces = (P.target + P.Hq - 1) / P.Hq * 3 / 2 + 2;
+    if (P.rows && !worth_cutting(P)) P.target = P.pieces = 0;
+  }
   uint32_t tag = 0x536d61u;
   for (const int32_t v : {P.B, P.T, P.Tk, P.Hq, P.Hkv, p->D, p->dtype, P.causal, P.n_docs, P.rows,
                           (int32_t)(p->cu_seqlens_k != nullptr)})
@@ -228,11 +347,17 @@ size_t layout(SmxP& P, int D, int dtype, bool bwd, void* base) {
   P.err = (int32_t*)w;
   P.wtag = (int32_t*)(w + 4);
   P.counts = (int32_t*)(w + 8);
-  if (!P.rows)
-    for (int l = 0; l < (bwd ? 3 : 1); l++) {
-      P.pre[l] = (int32_t*)(w + take(((size_t)P.n_docs + 1) * sizeof(int32_t)));
-      P.list[l] = (int4*)(w + take((size_t)max_tiles(P, l) * 2 * sizeof(int4)));
-    }
+  for (int l = 0; l < (bwd ? 3 : 1); l++) {
+    if (P.rows && (l > 0 || !P.target)) continue;
+    P.pre[l] = (int32_t*)(w + take(((size_t)P.n_docs + 1) * sizeof(int32_t)));
+    P.list[l] = (int4*)(w + take((size_t)max_tiles(P, l) * 2 * sizeof(int4)));
+  }
+  if (P.target) {
+    const size_t rows = (size_t)P.pieces * P.Hq * P.tile[0];
+    P.joins = (int4*)(w + take((size_t)P.pieces * sizeof(int4)));
+    P.pl = (float*)(w + take(rows * sizeof(float)));
+    P.po = (float*)(w + take(rows * D * sizeof(float)));
+  }
   if (bwd) {
     P.lse2 = (float*)(w + take((size_t)P.Hq * P.Nq * sizeof(float)));
     P.delta = (float*)(w + take((size_t)P.Hq * P.Nq * sizeof(float)));
@@ -256,6 +381,16 @@ cudaError_t launch_delta(const SmxP& P, const void* o, const void* dO, cudaStrea
   const cudaError_t e = launch_pdl(smx_delta_kernel<D, T>, dim3((unsigned)grid), dim3(256), 0, st, P, (const T*)o,
                                    (const T*)dO);
   prof_end(K_SMX_DELTA, st);
+  return e;
+}
+
+template <int D, typename T>
+cudaError_t launch_join(const SmxP& P, void* o, float* lse, cudaStream_t st) {
+  const int64_t most = (int64_t)(P.pieces / 2) * P.Hq * (P.tile[0] / 8);  // (a cut tile has two pieces at least)
+  const int64_t grid = most < 8 * 152 ? most : 8 * 152;
+  prof_begin(K_SMX_JOIN_ROWS, st);
+  const cudaError_t e = launch_pdl(smx_join_rows_kernel<D, T>, dim3((unsigned)grid), dim3(256), 0, st, P, (T*)o, lse);
+  prof_end(K_SMX_JOIN_ROWS, st);
   return e;
 }
 
@@ -290,7 +425,7 @@ extern "C" KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, cons
   P.save = save_for_backward != 0;
   if (!workspace || workspace_bytes < layout(P, p->D, p->dtype, P.save, workspace)) return KDA_ERR_WORKSPACE;
   if ((uintptr_t)workspace % 256 != 0) return KDA_ERR_ALIGNMENT;
-  if (!P.rows && launch_table(P, 0, 1, st) != cudaSuccess) return KDA_ERR_CUDA;
+  if (P.list[0] && launch_table(P, 0, 1, st) != cudaSuccess) return KDA_ERR_CUDA;
   cudaError_t e;
   if (p->dtype == KDA_F32) {
     const float* x[3] = {(const float*)q, (const float*)k, (const float*)v};
@@ -300,6 +435,12 @@ extern "C" KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, cons
     if (e == cudaSuccess) e = launch_tc_fwd(P, p->D, 3, P.pq, P.pk, P.pv, o, lse, st);
   } else {
     e = launch_tc_fwd(P, p->D, 1, q, k, v, o, lse, st);
+  }
+  if (e == cudaSuccess && P.target) {
+    if (p->dtype == KDA_F32)
+      e = p->D == 64 ? launch_join<64, float>(P, o, lse, st) : launch_join<128, float>(P, o, lse, st);
+    else
+      e = p->D == 64 ? launch_join<64, bf16>(P, o, lse, st) : launch_join<128, bf16>(P, o, lse, st);
   }
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

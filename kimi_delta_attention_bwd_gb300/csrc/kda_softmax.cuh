@@ -5,6 +5,8 @@
 #include "kda_internal.cuh"
 #include "../../include/kda.h"
 
+#include <limits.h>
+
 namespace kda {
 namespace smx {
 
@@ -16,9 +18,16 @@ struct SmxP {
   int save, tag;
   float scale, scale2;  // scale2 = scale log2(e): exponentials are powers of two
   const int32_t *cu, *cuk;
-  int32_t *err, *wtag, *counts;  // counts[l]: tiles of list l (cu_seqlens)
+  int32_t *err, *wtag, *counts;  // counts[l]: entries of list l; counts[3]: split tiles
   int32_t* pre[3];               // [n_docs + 1] first tile of each document
   int4* list[3];                 // two int4 a tile, see Tile; 0: forward's queries, 1: dq's queries, 2: dk and dv's keys
+                                 // (nullptr: equal rows, whose tiles follow from their number)
+  // The forward's tiles whose keys are cut into pieces, see smx_table_kernel: pieces' blocks of xb keys, how many CTAs
+  // to aim at (0: no tile is cut), room for how many pieces, their o and log2 sums [piece][Hq][tile][D], the cut tiles
+  // (first query, rows, first piece, pieces).
+  int xb, target, pieces;
+  float *po, *pl;
+  int4* joins;
   int tile[3];                   // rows a tile
   float *lse2, *delta;           // [Hq][Nq]: log2 of the rows' sums, saved by the forward; sum_d o dO
   bf16* res;                     // [Nq, Hq, D] what rounding o to bf16 left, saved by the forward
@@ -26,8 +35,9 @@ struct SmxP {
 };
 
 // Rows t * tile .. of a document's queries (or keys): its first query, queries, first key, keys.
+// The forward takes blocks j0 .. j1 - 1 of its keys, as piece `piece` (-1: it takes them all).
 struct Tile {
-  int q0, Lq, k0, Lk, t;
+  int q0, Lq, k0, Lk, t, j0, j1, piece;
 };
 
 // Keys that query i of a document sees, as a bound on their index; queries that key j does not reach.
@@ -44,7 +54,10 @@ __host__ __device__ inline int first_query(int causal, int j, int Lq, int Lk) {
 
 // Tile x of list l, the heavy ones first; false past the last.  by_key: the tiles are of keys.
 __device__ __forceinline__ bool tile_of(const SmxP& P, int l, int x, bool by_key, Tile& t) {
-  if (P.rows) {
+  t.j0 = 0;
+  t.j1 = INT_MAX;
+  t.piece = -1;
+  if (!P.list[l]) {
     const int nt = ((by_key ? P.Tk : P.T) + P.tile[l] - 1) / P.tile[l], i = x / P.B, b = x - i * P.B;
     if (i >= nt) return false;
     t.t = by_key ? i : nt - 1 - i;
@@ -61,6 +74,11 @@ __device__ __forceinline__ bool tile_of(const SmxP& P, int l, int x, bool by_key
   t.k0 = a.z;
   t.Lk = a.w;
   t.t = b.x;
+  if (l == 0) {
+    t.j0 = b.y;
+    t.j1 = b.z;
+    t.piece = b.w;
+  }
   return true;
 }
 
@@ -73,6 +91,7 @@ __device__ __forceinline__ bool saved(const SmxP& P) {
 
 // Tensor-core kernels.  parts = 1: bf16 io; 3: fp32 io, its inputs as three bf16 arrays one behind the other
 // (launch_split), the backward at D = 64 only.  Rows of list l's tiles: tc_tile.
+constexpr int tc_block(int D, int parts) { return D == 64 || parts == 3 ? 64 : 128; }  // the forward's blocks of keys
 constexpr int tc_tile(int D, int parts, int l) { return l > 0 || (parts == 3 && D == 128) ? 128 : 256; }
 cudaError_t launch_tc_fwd(const SmxP& P, int D, int parts, const void* q, const void* k, const void* v, void* o,
                           float* lse, cudaStream_t st);
@@ -86,12 +105,12 @@ constexpr int F32_TILE = 64;
 cudaError_t launch_f32_bwd(const SmxP& P, const float* q, const float* k, const float* v, const float* dO, float* dq,
                            float* dk, float* dv, cudaStream_t st);
 
-// Upper bound on the tiles of list l.
+// Upper bound on the entries of list l: its tiles, and the pieces of those that are cut.
 inline int max_tiles(const SmxP& P, int l) {
-  const int n = l == 2 ? P.Nk : P.Nq, t = P.tile[l];
-  if (P.rows) return P.B * (((l == 2 ? P.Tk : P.T) + t - 1) / t);
+  const int n = l == 2 ? P.Nk : P.Nq, t = P.tile[l], more = l == 0 ? P.pieces : 0;
+  if (P.rows) return P.B * (((l == 2 ? P.Tk : P.T) + t - 1) / t) + more;
   const int64_t m = (int64_t)n / t + P.n_docs;
-  return (int)(m < n ? m : n);  // (every tile has a row)
+  return (int)(m < n ? m : n) + more;  // (every tile has a row)
 }
 
 }  // namespace smx

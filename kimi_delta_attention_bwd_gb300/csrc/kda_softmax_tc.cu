@@ -400,6 +400,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     for (int i = 0; i < NT; i++)
       if (i * BLK < nq) {
         nb[i] = (keys_of(P.causal, i0 + min(nq, (i + 1) * BLK) - 1, t.Lq, t.Lk) + XB - 1) / XB;
+        nb[i] = max(0, min(nb[i], t.j1) - t.j0);
         clean[i] = keys_of(P.causal, i0 + i * BLK, t.Lq, t.Lk) / XB;
       }
   }
@@ -424,7 +425,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       if (r > 0 && !wait(&B.empty[s], (r - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.full[s], F::BYTES);
-        load_block<D, XB, PARTS>(ring + s * F::BYTES, x & 1 ? &mv : &mk, hk, t.k0 + x / 2 * XB, P.Nk, &B.full[s]);
+        load_block<D, XB, PARTS>(ring + s * F::BYTES, x & 1 ? &mv : &mk, hk, t.k0 + (t.j0 + x / 2) * XB, P.Nk, &B.full[s]);
       }
       __syncwarp();
     }
@@ -455,7 +456,8 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       for (int j = 0; j < n; j++) {
         const int xv = 2 * j + 1, xk = 2 * j + 2, sv = xv % F::STAGES, sk = xk % F::STAGES;
         if (!wait(&B.full[sv], (xv / F::STAGES) & 1, &B.dead)) return false;
-        if (t.Lk - j * XB < XB) zero_rows<D, XB, PARTS>(ring + sv * F::BYTES, t.Lk - j * XB);
+        const int left = t.Lk - (t.j0 + j) * XB;
+        if (left < XB) zero_rows<D, XB, PARTS>(ring + sv * F::BYTES, left);
         if (j + 1 < n && !wait(&B.full[sk], (xk / F::STAGES) & 1, &B.dead)) return false;
         const uint32_t vb = r0 + sv * F::BYTES;
 #pragma unroll
@@ -471,7 +473,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
             for (int s = 0; s < XB / 16; s++)
               mma_ts(d, Q::a(y) == 2 ? c + 8 * s : a + F::part(s) + Q::a(y) * F::SECOND,
                      desc_mn<XB>(vb + Q::b(y) * (XB * D * 2), s), id_o, (PARTS == 1 && j > 0) || y > 0 || s > 0, me);
-          if (PARTS == 1 && j == 0 && clean[i] == 0)
+          if (PARTS == 1 && t.j0 + j == 0 && clean[i] == 0)
 #pragma unroll
             for (int s = 0; s < XB / 16; s++)
               mma_ts(d, a + F::part(s) + F::SECOND, desc_mn<XB>(vb, s), id_o, true, me);
@@ -541,8 +543,8 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       tc::fence_after();
       if constexpr (PARTS == 3)
         if (j > 0) take_block();
-      const bool cut = j >= cleani, few = cut && j == 0;  // a mask cuts the block; some rows may have few keys in all
-      const int left = lim - j * XB, least = cut ? __shfl_sync(0xffffffffu, left, 0) : XB;  // (the warp's first row's)
+      const bool cut = t.j0 + j >= cleani, few = cut && t.j0 + j == 0;  // a mask cuts the block; some rows may have few keys in all
+      const int left = lim - (t.j0 + j) * XB, least = cut ? __shfl_sync(0xffffffffu, left, 0) : XB;  // (the warp's first row's)
       uint64_t sum[2] = {0, 0};
       float s0, s1;
       if constexpr (XB == 128) {
@@ -658,15 +660,27 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       const int w0 = r & ~31, rows = nq - w0;  // the warp's first row, rows from there on
       const size_t row = (size_t)(t.q0 + i0 + r) * P.Hq + h, row0 = (size_t)(t.q0 + i0 + w0) * P.Hq + h;
       unsigned char* buf = sm + i * F::OWN + (w0 & 127) * 128;  // (the tile's queries are no longer read)
-      if constexpr (PARTS == 3) {
+      // a piece's o, or o of fp32 io
+      const size_t at = ((size_t)t.piece * P.Hq + h) * (NT * BLK);
+      if (PARTS == 3 || t.piece >= 0) {
+        float* dst = t.piece >= 0 ? P.po + (at + w0) * D : (float*)o + row0 * D;
+        const size_t ld = t.piece >= 0 ? D : (size_t)P.Hq * D;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
+          float v[32];
+          if constexpr (PARTS == 3) {
+#pragma unroll
+            for (int e = 0; e < 32; e++) v[e] = sums[c + e];
+          } else if (nbi > 0) {
+            tm_ld32(to + c, v);
+            tm_wait_ld(v);
+          }
           uint32_t u[32];
 #pragma unroll
-          for (int e = 0; e < 32; e++) u[e] = __float_as_uint(sums[c + e] * inv);
-          store_rows(buf, u, o + row0 * D + c, (size_t)P.Hq * D, rows);
+          for (int e = 0; e < 32; e++) u[e] = __float_as_uint(l == 0.f ? 0.f : v[e] * inv);
+          store_rows(buf, u, dst + c, ld, rows);
         }
-      } else {
+      } else if constexpr (PARTS == 1) {
 #pragma unroll
         for (int c = 0; c < D; c += 64) {
           uint32_t u[32], w[32];  // o, and what its rounding leaves
@@ -686,7 +700,9 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
           if (P.save) store_rows(buf, w, P.res + row0 * D + c, (size_t)P.Hq * D, rows);
         }
       }
-      if (in) {
+      if (in && t.piece >= 0) {
+        P.pl[at + r] = l2;
+      } else if (in) {
         lse[row] = l2 * LN2;
         if (P.save) P.lse2[(size_t)h * P.Nq + t.q0 + i0 + r] = l2;
       }

@@ -149,6 +149,28 @@ def test_sharp_and_shifted_logits(dt, D):
     check(run(x, causal=False), oracle(x, causal=False), dt, D, x)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lq,lk,rows,causal", [
+    ([1], [5000], True, True), ([300], [3001], True, True), ([300], [3001], True, False), ([40] * 3, [1500] * 3, True, True),
+    ([130, 0, 9, 1, 300, 60], [4000, 10, 9, 2500, 150, 0], False, True), ([3000, 1], [3000, 1], False, True),
+    ([2, 500], [3500, 520], False, False)])
+def test_few_queries_on_many_keys(dt, D, lq, lk, rows, causal):
+    """Tiles whose keys are cut into pieces and joined, whole ones beside them, and the backward after them."""
+    x = make(40, lq, lk, 2, 1, D, dt, rows=rows)
+    check(run(x, causal), oracle(x, causal), dt, D, x)
+
+
+def test_pieces_with_values_that_are_not_finite():
+    x = make(41, [3, 200], [4000, 200], 2, 1, 64, "bf16")
+    want = run(x, backward=False)
+    x["q"][0, 1, 0, 5] = float("nan")
+    got = run(x, backward=False)
+    assert torch.isnan(got["o"][0, 1, 0]).all() and torch.isnan(got["lse"][0, 1, 0])
+    got["o"][0, 1, 0], got["lse"][0, 1, 0] = want["o"][0, 1, 0], want["lse"][0, 1, 0]
+    assert torch.equal(got["o"], want["o"]) and torch.equal(got["lse"], want["lse"])
+
+
 def test_scale_is_used():
     x = make(9, [70], [70], 2, 2, 64, "bf16", rows=True)
     check(run(x, scale=0.4), oracle(x, scale=0.4), "bf16", 64, x)
