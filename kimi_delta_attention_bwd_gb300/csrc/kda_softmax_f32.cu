@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(NT) smx_dkv_kernel(SmxP P, const float* __rest
   float *tK = sm, *tV = tK + D * OWN, *tQ = tV + D * OWN, *tG = tQ + D * TM, *sQ = tG + D * TM, *sG = sQ + D * TM;
   float *sP = sG + D * TM, *sl = sP + TM * PP<R>, *sd = sl + TM;  // (the weights, then their gradients)
   pdl_wait();
+  pdl_release();  // dq's CTAs may follow this grid's last ones: they wait for it at their end only
   if (!saved(P)) return;
   const int hk = blockIdx.x % P.Hkv, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   Tile t;
@@ -213,7 +214,9 @@ __global__ void __launch_bounds__(NT) smx_dq_kernel(SmxP P, const float* __restr
   constexpr int OWN = 16 * R;
   extern __shared__ __align__(16) float sm[];
   float *tQ = sm, *tG = tQ + D * OWN, *tK = tG + D * OWN, *tV = tK + D * TM, *sK = tV + D * TM, *sD = sK + D * TM;
-  pdl_wait();
+  struct Last {  // what follows this grid follows dk and dv too
+    __device__ ~Last() { pdl_wait(); }
+  } last;
   if (!saved(P)) return;
   const int h = blockIdx.x % P.Hq, hk = h / P.G, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   Tile t;

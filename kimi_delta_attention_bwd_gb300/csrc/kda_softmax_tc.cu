@@ -895,6 +895,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     mma::mbar_init_fence();
   }
   pdl_wait();
+  pdl_release();  // dq's CTAs may follow this grid's last ones: they wait for it at their end only
   Tile t;
   const int hk = blockIdx.x % P.Hkv;
   const bool live = saved(P) && tile_of(P, 2, blockIdx.x / P.Hkv, true, t);
@@ -1091,7 +1092,8 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   }
 }
 
-// dq, per CTA: 128 queries of one head over the blocks of keys: S = q k^T, dP = dO v^T, dS = P (dP - delta), dq += dS k.
+// dq, per CTA (its grid starts behind dk and dv's last CTAs and needs nothing of theirs): 128 queries of one head over
+// the blocks of keys: S = q k^T, dP = dO v^T, dS = P (dP - delta), dq += dS k.
 // S and dP are taken to registers at once, so that the next block's products run while dS is formed; dS has two places
 // of its own.
 struct DqBars {
@@ -1139,7 +1141,6 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
     B.dead = 0;
     mma::mbar_init_fence();
   }
-  pdl_wait();
   Tile t;
   const int h = blockIdx.x % P.Hq, hk = h / P.G;
   const bool live = saved(P) && tile_of(P, 1, blockIdx.x / P.Hq, false, t);
@@ -1292,6 +1293,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
     tc::fence_after();
     tc::tmem_dealloc(tm, F::COLS);
   }
+  pdl_wait();  // (what follows this grid follows dk and dv too)
 }
 
 template <int D, int PARTS>
