@@ -2,6 +2,7 @@
 // library (not part of the C ABI).
 #pragma once
 #include <cuda.h>  // CUtensorMap (the maps are encoded through the runtime's driver entry point)
+#include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -218,6 +219,8 @@ struct BwdIO {
   int ld;
   const float *cwq, *cwk, *cwv;
 };
+
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder();  // nullptr: the driver has none
 
 // TMA tensor maps of the raw per-token inputs, each viewed as a 2-D [Ntok][H d]
 // bf16 tensor with a box of one head's d channels x C tokens (encoded on the

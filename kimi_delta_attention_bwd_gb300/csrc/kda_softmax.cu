@@ -322,6 +322,8 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
     P.pieces = (P.target + P.Hq - 1) / P.Hq * 3 / 2 + 2;
     if (P.rows && !worth_cutting(P)) P.target = P.pieces = 0;
   }
+  for (int l = 0; l < 3; l++)  // (documents, most of them empty, times heads: a grid each)
+    if ((int64_t)max_tiles(P, l) * (l == 2 ? P.Hkv : P.Hq) > 2147483647) return KDA_ERR_INVALID_ARG;
   uint32_t tag = 0x536d61u;
   for (const int32_t v : {P.B, P.T, P.Tk, P.Hq, P.Hkv, p->D, p->dtype, P.causal, P.n_docs, P.rows,
                           (int32_t)(p->cu_seqlens_k != nullptr)})

@@ -6,10 +6,9 @@
 // bandwidth.  Where sequences and heads do not fill the GPU the length is cut into equal
 // pieces, whose (maximum, sum, o) are joined by a second kernel in a fixed order.
 //
-// bf16: a warp takes 16 keys at a time straight from global memory into mma.sync
-// fragments; which d (of a key) or which column (of a value) a lane's 16-byte load
-// stands for is free as long as both operands agree, so no shared memory and no
-// transposing loads are needed.  The weights enter the value product as two bf16 parts
+// bf16: one warp loads blocks of 64 keys and values (TMA, a ring of 96 KB a CTA, two CTAs per SM: what keeps HBM busy is
+// bytes in flight; with 16 keys a warp loaded to registers 64 caches of up to 8192 places took 155 us, so 126),
+// four warps take 16 keys each of a block into mma.sync.  The weights enter the value product as two bf16 parts
 // (off by 2^-16): the tensor pipe has room, and the output is rounded once.
 #include "kda_internal.cuh"
 #include "kda_mma.cuh"
@@ -64,7 +63,7 @@ template <int D, typename T>
 __device__ __forceinline__ void finish(const DecP& P, const Place& c, const float* sm, T* o) {
   const float *m = sm, *l = sm + WARPS * MH, *a = l + WARPS * MH;
   float* part = P.part + (size_t)blockIdx.x * (MH * (D + 2));
-  for (int i = threadIdx.x; i < c.nh * D; i += WARPS * 32) {
+  for (int i = threadIdx.x; i < c.nh * D; i += blockDim.x) {
     const int r = i / D, d = i % D;
     float mx = -INFINITY;
 #pragma unroll
@@ -93,22 +92,18 @@ __device__ __forceinline__ void finish(const DecP& P, const Place& c, const floa
 template <int D, typename T>
 __device__ __forceinline__ void no_step(const DecP& P, const Place& c, T* o) {
   if (P.ns == 1)
-    for (int i = threadIdx.x; i < c.nh * D; i += WARPS * 32) dec_out(o + ((size_t)c.seq * P.Hq + c.h0) * D + i, 0.f);
+    for (int i = threadIdx.x; i < c.nh * D; i += blockDim.x) dec_out(o + ((size_t)c.seq * P.Hq + c.h0) * D + i, 0.f);
 }
 
 // The error word: a length without room in its cache (block 0 looks at all).
 __device__ __forceinline__ void check_lengths(const DecP& P) {
   if (blockIdx.x != 0) return;
   int bad = 0;
-  for (int i = threadIdx.x; i < P.n; i += WARPS * 32) bad |= P.len[i] >= P.cap;
+  for (int i = threadIdx.x; i < P.n; i += blockDim.x) bad |= P.len[i] >= P.cap;
   bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) *P.err = bad ? KDA_ERR_BAD_SEQLENS : KDA_OK;
 }
 
-__device__ __forceinline__ uint4 ldg16(const bf16* p, bool in) {
-  return in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-}
-__device__ __forceinline__ uint32_t word(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 // two probabilities as a bf16 pair and what that left
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -118,132 +113,205 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Lane (g, t) = (lane / 4, lane % 4).  q k: step 2 j + s of the contraction holds d = 32 j + 8 t + 4 s .. + 3 of
-// lane t's 16-byte load j.  p v: column g of tile (c, e) is d = 64 c + 8 g + e, so a lane's load c of a key
-// gives it one column of eight tiles, and it ends with d = 64 c + 16 t .. + 15 of rows g and g + 8.
+// ------------------------------------------------------------ bf16
+constexpr int KB = 64;  // keys of a block
 template <int D>
-__global__ void __launch_bounds__(WARPS * 32) smx_decode_kernel(DecP P, const bf16* __restrict__ q,
-                                                              const bf16* __restrict__ kn,
-                                                              const bf16* __restrict__ vn, bf16* kc, bf16* vc,
-                                                              bf16* __restrict__ o) {
-  constexpr int NJ = D / 32, NC = D / 64;
-  extern __shared__ __align__(16) float sm[];
+struct Ring {
+  static constexpr int HALF = KB * 128, BLOCK = KB * D * 2;  // 64 columns; a block of keys or of values
+  static constexpr int STAGES = D == 64 ? 6 : 3;
+  static constexpr int SMEM = STAGES * 2 * BLOCK + 1024;
+};
+// 16 bytes (columns 8 c ..) of row r of a block: halves of 64 columns, 128-byte swizzle
+template <int D>
+__device__ __forceinline__ unsigned char* at_chunk(unsigned char* block, int r, int c) {
+  return block + (c >> 3) * Ring<D>::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          mma::smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(mma::smem_u32(bar))
+      : "memory");
+}
+
+// Maps: the caches as [sequence][place][Hkv D].  Lane (g, t) = (lane / 4, lane % 4) holds rows (query heads) g and g + 8.
+template <int D>
+__global__ void __launch_bounds__(WARPS * 32 + 32) smx_decode_kernel(DecP P, const __grid_constant__ CUtensorMap mk,
+                                                                   const __grid_constant__ CUtensorMap mv,
+                                                                   const bf16* __restrict__ q,
+                                                                   const bf16* __restrict__ kn,
+                                                                   const bf16* __restrict__ vn, bf16* kc, bf16* vc,
+                                                                   bf16* __restrict__ o) {
+  using R = Ring<D>;
+  constexpr int NS = D / 16, NT = D / 8;  // steps of q k; tiles of p v
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t full[R::STAGES], empty[R::STAGES];
+  __shared__ int dead;
+  unsigned char* ring = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R::STAGES; i++) {
+      mma::mbar_init(&full[i], 1);
+      mma::mbar_init(&empty[i], WARPS);
+    }
+    dead = 0;
+    mma::mbar_init_fence();
+  }
   pdl_wait();
   pdl_release();
   check_lengths(P);
   Place c;
-  if (!place_of(P, c)) return no_step<D>(P, c, o);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const bool live = place_of(P, c);
+  __syncthreads();
+  if (!live) return no_step<D>(P, c, o);
+  const int n = (c.hi - c.lo + KB - 1) / KB;
   const size_t row = (size_t)P.Hkv * D, cache = ((size_t)c.seq * P.cap * P.Hkv + c.hk) * D;
-  const bf16 *kb = kc + cache, *vb = vc + cache, *k1 = kn + ((size_t)c.seq * P.Hkv + c.hk) * D,
-             *v1 = vn + ((size_t)c.seq * P.Hkv + c.hk) * D;
-  if (c.h0 == c.hk * P.G && blockIdx.x % P.ns == 0 && warp == 0 && lane < D / 8) {  // (no reader takes it from the cache)
-    *reinterpret_cast<uint4*>(kc + cache + (size_t)c.L * row + 8 * lane) = ldg16(k1 + 8 * lane, true);
-    *reinterpret_cast<uint4*>(vc + cache + (size_t)c.L * row + 8 * lane) = ldg16(v1 + 8 * lane, true);
-  }
-  uint4 qa[NJ], qb[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; j++) {
-    const bf16* p = q + ((size_t)c.seq * P.Hq + c.h0) * D + 32 * j + 8 * t;
-    qa[j] = ldg16(p + g * D, g < c.nh);
-    qb[j] = ldg16(p + (g + 8) * D, g + 8 < c.nh);
-  }
-  float acc[NC * 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll 1
-  for (int j0 = c.lo + 16 * warp; j0 < c.hi; j0 += 16 * WARPS) {
-    uint4 kr[2][NJ], vr[4][NC];
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-      const int j = j0 + 8 * x + g;
-      const bf16* p = (j == c.L ? k1 : kb + (size_t)j * row) + 8 * t;
-#pragma unroll
-      for (int y = 0; y < NJ; y++) kr[x][y] = j < c.hi ? *reinterpret_cast<const uint4*>(p + 32 * y) : make_uint4(0, 0, 0, 0);
+  const bf16 *k1 = kn + ((size_t)c.seq * P.Hkv + c.hk) * D, *v1 = vn + ((size_t)c.seq * P.Hkv + c.hk) * D;
+  auto wait = [&](uint64_t* bar, int phase) -> bool {
+    bool ok = mma::mbar_try(bar, phase & 1);
+    for (int it = 0; !ok && it < mma::WAIT_POLLS; it++) {
+      ok = mma::mbar_try(bar, phase & 1);
+      if (!ok && *(volatile int*)&dead) break;
     }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) *(volatile int*)&dead = 1;
+    return ok;
+  };
+  float acc[NT][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  if (warp == WARPS) {  // loads (a wait gives up after a second: by then every copy under way has landed)
+    for (int x = 0; x < n; x++) {
+      const int s = x % R::STAGES;
+      if (x >= R::STAGES && !wait(&empty[s], x / R::STAGES - 1)) break;
+      if (lane == 0) {
+        unsigned char* dst = ring + s * 2 * R::BLOCK;
+        mma::mbar_expect_tx(&full[s], 2 * R::BLOCK);
 #pragma unroll
-    for (int x = 0; x < 4; x++) {
-      const int j = j0 + 2 * t + (x & 1) + 8 * (x >> 1);
-      const bf16* p = (j == c.L ? v1 : vb + (size_t)j * row) + 8 * g;
-#pragma unroll
-      for (int y = 0; y < NC; y++) vr[x][y] = j < c.hi ? *reinterpret_cast<const uint4*>(p + 64 * y) : make_uint4(0, 0, 0, 0);
-    }
-    float s[2][4] = {};
-#pragma unroll
-    for (int y = 0; y < NJ; y++)
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const uint32_t a[4] = {word(qa[y], 2 * h), word(qb[y], 2 * h), word(qa[y], 2 * h + 1), word(qb[y], 2 * h + 1)};
-#pragma unroll
-        for (int x = 0; x < 2; x++) mma::mma_bf16(s[x], a, word(kr[x][y], 2 * h), word(kr[x][y], 2 * h + 1));
+        for (int y = 0; y < D / 64; y++) {
+          tma_load_3d(dst + y * R::HALF, &mk, c.hk * D + 64 * y, c.lo + x * KB, c.seq, &full[s]);
+          tma_load_3d(dst + R::BLOCK + y * R::HALF, &mv, c.hk * D + 64 * y, c.lo + x * KB, c.seq, &full[s]);
+        }
       }
-    uint32_t ph[4], pl[4];
-    bool grew = false;
-    float corr[2];
+      __syncwarp();
+    }
+  } else {
+    if (c.h0 == c.hk * P.G && blockIdx.x % P.ns == 0 && warp == 0 && lane < D / 8) {  // (no reader takes it from the cache)
+      *reinterpret_cast<uint4*>(kc + cache + (size_t)c.L * row + 8 * lane) = *reinterpret_cast<const uint4*>(k1 + 8 * lane);
+      *reinterpret_cast<uint4*>(vc + cache + (size_t)c.L * row + 8 * lane) = *reinterpret_cast<const uint4*>(v1 + 8 * lane);
+    }
+    uint32_t qa[NS][4];
+    const bf16* qb = q + ((size_t)c.seq * P.Hq + c.h0) * D + 2 * t;
+#pragma unroll
+    for (int s = 0; s < NS; s++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const int r = g + 8 * (e & 1);
+        qa[s][e] = r < c.nh ? *reinterpret_cast<const uint32_t*>(qb + (size_t)r * D + 16 * s + 8 * (e >> 1)) : 0u;
+      }
+#pragma unroll 1
+    for (int x = 0; x < n; x++) {
+      const int s = x % R::STAGES, r0 = 16 * warp, j0 = c.lo + x * KB + r0;  // the warp's rows of the block, its first key
+      if (!wait(&full[s], x / R::STAGES)) break;
+      unsigned char *bk = ring + s * 2 * R::BLOCK, *bv = bk + R::BLOCK;
+      if (j0 < c.hi) {
+        if (j0 + 16 >= c.hi) {  // the last keys: the new token's row, and zeros for places behind it, which hold anything
+          for (int i = lane; i < 16 * (D / 8); i += 32) {
+            const int r = i / (D / 8), y = i % (D / 8);
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            if (j0 + r == c.L) {
+              *reinterpret_cast<uint4*>(at_chunk<D>(bk, r0 + r, y)) = *reinterpret_cast<const uint4*>(k1 + 8 * y);
+              *reinterpret_cast<uint4*>(at_chunk<D>(bv, r0 + r, y)) = *reinterpret_cast<const uint4*>(v1 + 8 * y);
+            } else if (j0 + r >= c.hi) {
+              *reinterpret_cast<uint4*>(at_chunk<D>(bv, r0 + r, y)) = zero;
+            }
+          }
+          __syncwarp();
+        }
+        float sc[2][4] = {};
+#pragma unroll
+        for (int y = 0; y < NS / 2; y++)
+#pragma unroll
+          for (int z = 0; z < 2; z++) {
+            uint32_t b[4];
+            mma::ldsm4(b, at_chunk<D>(bk, r0 + 8 * z + (lane & 7), 4 * y + (lane >> 3)));
+            mma::mma_bf16(sc[z], qa[2 * y], b[0], b[1]);
+            mma::mma_bf16(sc[z], qa[2 * y + 1], b[2], b[3]);
+          }
+        uint32_t ph[4], pl[4];
+        bool grew = false;
+        float corr[2];
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+          float mx = m[r];
+#pragma unroll
+          for (int z = 0; z < 2; z++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              float& v = sc[z][2 * r + e];
+              v = j0 + 8 * z + 2 * t + e < c.hi ? v * P.scale2 : -INFINITY;
+              mx = fmaxf(mx, v);
+            }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mu = mx == -INFINITY ? 0.f : mx;
+          corr[r] = ex2(m[r] - mu);
+          grew |= mx != m[r];
+          m[r] = mx;
+          float sum = 0.f;
+#pragma unroll
+          for (int z = 0; z < 2; z++) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              sc[z][2 * r + e] = ex2(sc[z][2 * r + e] - mu);
+              sum += sc[z][2 * r + e];
+            }
+            split2(sc[z][2 * r], sc[z][2 * r + 1], ph[2 * z + r], pl[2 * z + r]);
+          }
+          l[r] = l[r] * corr[r] + sum;
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int i = 0; i < NT; i++) {
+            acc[i][0] *= corr[0];
+            acc[i][1] *= corr[0];
+            acc[i][2] *= corr[1];
+            acc[i][3] *= corr[1];
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < NT / 2; y++) {
+          uint32_t b[4];
+          mma::ldsm4t(b, at_chunk<D>(bv, r0 + 8 * ((lane >> 3) & 1) + (lane & 7), 2 * y + (lane >> 4)));
+          mma::mma_bf16(acc[2 * y], ph, b[0], b[1]);
+          mma::mma_bf16(acc[2 * y + 1], ph, b[2], b[3]);
+          mma::mma_bf16(acc[2 * y], pl, b[0], b[1]);
+          mma::mma_bf16(acc[2 * y + 1], pl, b[2], b[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mma::mbar_arrive(&empty[s]);  // (a block that was written to is the last: no copy follows)
+    }
+  }
+  __syncthreads();
+  if (dead) {  // (uniform: written before the barrier)
+    if (threadIdx.x == 0) *P.err = KDA_ERR_DEVICE;
+    return;
+  }
+  float* sm = reinterpret_cast<float*>(ring);  // (no copy is under way, no block is read)
+  float *sM = sm, *sL = sm + WARPS * MH, *sO = sL + WARPS * MH;
+  if (warp < WARPS)
 #pragma unroll
     for (int r = 0; r < 2; r++) {
-      float mx = m[r];
-#pragma unroll
-      for (int x = 0; x < 2; x++)
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-          float& z = s[x][2 * r + e];
-          z = j0 + 8 * x + 2 * t + e < c.hi ? z * P.scale2 : -INFINITY;
-          mx = fmaxf(mx, z);
-        }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mu = mx == -INFINITY ? 0.f : mx;
-      corr[r] = ex2(m[r] - mu);
-      grew |= mx != m[r];
-      m[r] = mx;
-      float sum = 0.f;
-#pragma unroll
-      for (int x = 0; x < 2; x++) {
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-          s[x][2 * r + e] = ex2(s[x][2 * r + e] - mu);
-          sum += s[x][2 * r + e];
-        }
-        split2(s[x][2 * r], s[x][2 * r + 1], ph[2 * x + r], pl[2 * x + r]);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int i = warp * MH + g + 8 * r;
+      if (t == 0) {
+        sM[i] = m[r];
+        sL[i] = l[r];
       }
-      l[r] = l[r] * corr[r] + sum;
+#pragma unroll
+      for (int y = 0; y < NT; y++)
+        *reinterpret_cast<float2*>(sO + (size_t)i * D + 8 * y + 2 * t) = make_float2(acc[y][2 * r], acc[y][2 * r + 1]);
     }
-    if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-      for (int i = 0; i < NC * 8; i++) {
-        acc[i][0] *= corr[0];
-        acc[i][1] *= corr[0];
-        acc[i][2] *= corr[1];
-        acc[i][3] *= corr[1];
-      }
-    }
-#pragma unroll
-    for (int y = 0; y < NC; y++)
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
-        const uint32_t b0 = __byte_perm(word(vr[0][y], e / 2), word(vr[1][y], e / 2), sel);
-        const uint32_t b1 = __byte_perm(word(vr[2][y], e / 2), word(vr[3][y], e / 2), sel);
-        mma::mma_bf16(acc[8 * y + e], ph, b0, b1);
-        mma::mma_bf16(acc[8 * y + e], pl, b0, b1);
-      }
-  }
-  float *sM = sm, *sL = sm + WARPS * MH, *sO = sL + WARPS * MH;
-#pragma unroll
-  for (int r = 0; r < 2; r++) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    const int i = warp * MH + g + 8 * r;
-    if (t == 0) {
-      sM[i] = m[r];
-      sL[i] = l[r];
-    }
-#pragma unroll
-    for (int y = 0; y < NC; y++)
-#pragma unroll
-      for (int e = 0; e < 2; e++)
-#pragma unroll
-        for (int z = 0; z < 8; z++) sO[(size_t)i * D + 64 * y + 16 * t + 8 * e + z] = acc[8 * y + z][2 * r + e];
-  }
   __syncthreads();
   finish<D>(P, c, sm, o);
 }
@@ -271,7 +339,7 @@ __global__ void __launch_bounds__(WARPS * 32) smx_decode_f32_kernel(DecP P, cons
       kc[cache + (size_t)c.L * row + d] = k1[d];
       vc[cache + (size_t)c.L * row + d] = v1[d];
     }
-  for (int i = threadIdx.x; i < c.nh * D; i += WARPS * 32) sq[i] = q[((size_t)c.seq * P.Hq + c.h0) * D + i];
+  for (int i = threadIdx.x; i < c.nh * D; i += blockDim.x) sq[i] = q[((size_t)c.seq * P.Hq + c.h0) * D + i];
   __syncthreads();
   float acc[MH][NV] = {}, m[MH], l[MH] = {};
 #pragma unroll
@@ -339,16 +407,16 @@ __global__ void __launch_bounds__(WARPS * 32) smx_decode_f32_kernel(DecP P, cons
   finish<D>(P, c, sm, o);
 }
 
-// Joins the pieces of one (sequence, query head): their weights first, then warp w sums pieces w, w + JW, .. whose loads
+// Joins the pieces of one (sequence, query head): their weights first, then warp w sums pieces w, w + nw, .. whose loads
 // do not wait for one another (with a running maximum along them 114 pieces took 12.7 us, so 5).
-constexpr int JW = 16;
+constexpr int JW = 32;  // warps at most
 template <int D, typename T>
 __global__ void __launch_bounds__(JW * 32) smx_join_kernel(DecP P, T* __restrict__ o) {
   constexpr int NV = D / 32;
   extern __shared__ float sw[];  // [ns]
   __shared__ float red[JW], so[JW][D];
   const int seq = blockIdx.x / P.Hq, h = blockIdx.x % P.Hq, hk = h / P.G, r = h % P.G;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, rr = r % MH;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, rr = r % MH, nw = blockDim.x / 32;
   pdl_wait();
   const int L = P.len[seq];
   T* out = o + ((size_t)seq * P.Hq + h) * D;
@@ -359,7 +427,7 @@ __global__ void __launch_bounds__(JW * 32) smx_join_kernel(DecP P, T* __restrict
   constexpr size_t ST = MH * (D + 2);
   const float* part = P.part + (((size_t)seq * P.Hkv + hk) * P.HG + r / MH) * P.ns * ST;
   float m = -INFINITY;
-  for (int s = threadIdx.x; s < P.ns; s += JW * 32) {
+  for (int s = threadIdx.x; s < P.ns; s += blockDim.x) {
     sw[s] = part[s * ST + rr];
     m = fmaxf(m, sw[s]);
   }
@@ -367,11 +435,10 @@ __global__ void __launch_bounds__(JW * 32) smx_join_kernel(DecP P, T* __restrict
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   if (lane == 0) red[warp] = m;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < JW; w++) m = fmaxf(m, red[w]);
+  for (int w = 0; w < nw; w++) m = fmaxf(m, red[w]);
   const float mu = m == -INFINITY ? 0.f : m;
   float l = 0.f;
-  for (int s = threadIdx.x; s < P.ns; s += JW * 32) {
+  for (int s = threadIdx.x; s < P.ns; s += blockDim.x) {
     sw[s] = ex2(sw[s] - mu);
     l += sw[s] * part[s * ST + MH + rr];
   }
@@ -381,7 +448,7 @@ __global__ void __launch_bounds__(JW * 32) smx_join_kernel(DecP P, T* __restrict
   float acc[NV] = {};
   const float* p = part + 2 * MH + rr * D + lane * NV;
 #pragma unroll 8
-  for (int s = warp; s < P.ns; s += JW) {
+  for (int s = warp; s < P.ns; s += nw) {
     const float w = sw[s];
 #pragma unroll
     for (int e = 0; e < NV; e++) acc[e] = fmaf(w, p[s * ST + e], acc[e]);
@@ -391,8 +458,7 @@ __global__ void __launch_bounds__(JW * 32) smx_join_kernel(DecP P, T* __restrict
   __syncthreads();
   if (threadIdx.x < D) {
     float sum = 0.f, x = 0.f;
-#pragma unroll
-    for (int w = 0; w < JW; w++) {
+    for (int w = 0; w < nw; w++) {
       sum += red[w];
       x += so[w][threadIdx.x];
     }
@@ -400,11 +466,11 @@ __global__ void __launch_bounds__(JW * 32) smx_join_kernel(DecP P, T* __restrict
   }
 }
 
-// Pieces of a sequence, none of fewer than 128 keys of a full cache: for one sequence as many as the CTAs that 152
-// SMs hold (three each), so that its equal pieces are one wave; several sequences differ in length, and smaller pieces
-// even that out.
+// Pieces of a sequence, none of fewer than 128 keys of a full cache: for one sequence a CTA for each of 152 SMs
+// (131072 places of 4 key heads: 49 us, with two 50, three 54); several sequences differ in length, and smaller
+// pieces even that out (16 of up to 16384 places: 68 us with four CTAs per SM, 71 with eight).
 int pieces(int n, int64_t units, int cap) {
-  const int64_t want = ((n == 1 ? 3 : 8) * 152 + units - 1) / units, most = ((int64_t)cap + 127) / 128;
+  const int64_t want = ((n == 1 ? 1 : 4) * 152 + units - 1) / units, most = ((int64_t)cap + 127) / 128;
   const int64_t ns = want < most ? want : most;
   return (int)(ns < 1 ? 1 : ns);
 }
@@ -414,27 +480,47 @@ bool sizes_ok(int n, int cap, int Hq, int Hkv, int dtype) {
          (int64_t)n * cap <= ((int64_t)1 << 40) && (dtype == KDA_BF16 || dtype == KDA_F32);
 }
 
+// A cache [n][cap][Hkv D] with boxes of 64 columns by KB places of one sequence, in the 128-byte swizzle.
+bool encode_cache(CUtensorMap* m, const void* base, int n, int cap, int width) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)cap, (cuuint64_t)n};
+  const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)width * 2 * (cuuint64_t)cap};
+  const cuuint32_t box[3] = {64, KB, 1}, es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 cudaError_t launch(const DecP& P, int dtype, const void* q, const void* k, const void* v, void* kc, void* vc, void* o,
                    cudaStream_t st) {
   const unsigned grid = (unsigned)((int64_t)P.n * P.Hkv * P.HG * P.ns);
-  const size_t smem = WARPS * MH * (D + 2) * sizeof(float), s32 = smem + MH * D * sizeof(float);
-  cudaError_t e;
+  const size_t s32 = (WARPS * MH * (D + 2) + MH * D) * sizeof(float);
+  cudaError_t e = cudaSuccess;
+  CUtensorMap mk, mv;
+  if (dtype == KDA_BF16) {
+    e = raise_smem<smx_decode_kernel<D>>(Ring<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    if (!encode_cache(&mk, kc, P.n, P.cap, P.Hkv * D) || !encode_cache(&mv, vc, P.n, P.cap, P.Hkv * D))
+      return cudaErrorInvalidValue;
+  }
   prof_begin(K_SMX_DECODE, st);
   if (dtype == KDA_BF16) {
-    e = launch_pdl(smx_decode_kernel<D>, dim3(grid), dim3(WARPS * 32), smem, st, P, (const bf16*)q, (const bf16*)k,
-                   (const bf16*)v, (bf16*)kc, (bf16*)vc, (bf16*)o);
+    e = launch_pdl(smx_decode_kernel<D>, dim3(grid), dim3(WARPS * 32 + 32), Ring<D>::SMEM, st, P, mk, mv, (const bf16*)q,
+                   (const bf16*)k, (const bf16*)v, (bf16*)kc, (bf16*)vc, (bf16*)o);
   } else {
     e = launch_pdl(smx_decode_f32_kernel<D>, dim3(grid), dim3(WARPS * 32), s32, st, P, (const float*)q,
                    (const float*)k, (const float*)v, (float*)kc, (float*)vc, (float*)o);
   }
   prof_end(K_SMX_DECODE, st);
   if (e != cudaSuccess || P.ns == 1) return e;
+  const int jw = P.ns >= 4 * JW ? JW : P.ns <= 16 ? 4 : (P.ns + 3) / 4;  // about four pieces a warp; D threads at least
   prof_begin(K_SMX_JOIN, st);
   if (dtype == KDA_BF16)
-    e = launch_pdl(smx_join_kernel<D, bf16>, dim3(P.n * P.Hq), dim3(JW * 32), P.ns * sizeof(float), st, P, (bf16*)o);
+    e = launch_pdl(smx_join_kernel<D, bf16>, dim3(P.n * P.Hq), dim3(jw * 32), P.ns * sizeof(float), st, P, (bf16*)o);
   else
-    e = launch_pdl(smx_join_kernel<D, float>, dim3(P.n * P.Hq), dim3(JW * 32), P.ns * sizeof(float), st, P, (float*)o);
+    e = launch_pdl(smx_join_kernel<D, float>, dim3(P.n * P.Hq), dim3(jw * 32), P.ns * sizeof(float), st, P, (float*)o);
   prof_end(K_SMX_JOIN, st);
   return e;
 }

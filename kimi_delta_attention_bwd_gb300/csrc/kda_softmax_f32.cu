@@ -289,7 +289,6 @@ cudaError_t launch_f32_bwd(const SmxP& P, const float* q, const float* k, const 
   const size_t s1 = (2 * D * 16 * R + 4 * D * TM + TM * PP<R> + 2 * TM) * sizeof(float);
   const size_t s2 = (2 * D * 16 * R + 3 * D * TM + TM * PP<R>) * sizeof(float);
   const int64_t gk = (int64_t)max_tiles(P, 2) * P.Hkv, gq = (int64_t)max_tiles(P, 1) * P.Hq;
-  if (gk > 2147483647 || gq > 2147483647) return cudaErrorInvalidValue;
   cudaError_t e = raise_smem<smx_dkv_kernel<D, R>>((int)s1);
   if (e == cudaSuccess) e = raise_smem<smx_dq_kernel<D, R>>((int)s2);
   if (e != cudaSuccess) return e;

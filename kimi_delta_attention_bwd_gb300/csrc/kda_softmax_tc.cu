@@ -727,7 +727,6 @@ cudaError_t fwd(const SmxP& P, const void* q, const void* k, const void* v, void
       !encode_head_rows(&mv, v, PARTS * P.Nk, P.Hkv, D, F::XB))
     return cudaErrorInvalidValue;
   const int64_t grid = (int64_t)max_tiles(P, 0) * P.Hq;
-  if (grid > 2147483647) return cudaErrorInvalidValue;
   prof_begin(K_SMX_FWD, st);
   e = launch_pdl(smx_tc_fwd_kernel<D, PARTS>, dim3((unsigned)grid), dim3(F::THREADS), F::SMEM, st, P, mq, mk, mv,
                  (typename Io<PARTS>::T*)o, lse);
@@ -1314,7 +1313,6 @@ cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, cons
                        !encode_head_rows(&xv, v, nk, P.Hkv, D, F::XB) || !encode_head_rows(&xg, dO, nq, P.Hq, D, F::XB)))
     return cudaErrorInvalidValue;
   const int64_t gk = (int64_t)max_tiles(P, 2) * P.Hkv, gq = (int64_t)max_tiles(P, 1) * P.Hq;
-  if (gk > 2147483647 || gq > 2147483647) return cudaErrorInvalidValue;
   prof_begin(K_SMX_DKV, st);
   e = launch_pdl(smx_tc_dkv_kernel<D, PARTS>, dim3((unsigned)gk), dim3(F::EWK * 32 + 96), DKV_SMEM<D, PARTS>, st, P, xq, mk, mv, xg, (T*)dk,
                  (T*)dv);

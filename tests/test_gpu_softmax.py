@@ -268,6 +268,53 @@ def test_backward_on_another_stream_and_twice():
             assert torch.equal(g[n], want[n]), n
 
 
+def test_a_thread_s_first_call():
+    """Threads that have made no CUDA call yet: a forward in one, a backward in another."""
+    import threading
+    x = make(42, [200], [200], 4, 4, 64, "bf16", rows=True)
+    want = run(x)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO")}
+    torch.cuda.synchronize()
+    out = {}
+
+    def forward():
+        out["o"], _, out["ctx"] = kda.kda_softmax_forward(d["q"], d["k"], d["v"])
+
+    def backward():
+        out.update(kda.kda_softmax_backward(out["ctx"], d["dO"]))
+    for f in (forward, backward):
+        t = threading.Thread(target=f)
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    for n in ("o", "dq", "dk", "dv"):
+        assert torch.equal(out[n], want[n]), n
+
+
+def test_more_than_2_31_values():
+    """Offsets past 31 bits: the last documents of a long axis give the bits that they give alone."""
+    docs, L, Hq, D = 3000, 90, 64, 128
+    g = torch.Generator(device="cuda").manual_seed(43)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, k, v, dO = r(1, docs * L, Hq, D), r(1, docs * L, 1, D), r(1, docs * L, 1, D), r(1, docs * L, Hq, D)
+    assert q.numel() > 2 ** 31
+
+    def step(part, n):
+        cu = torch.arange(n + 1, dtype=torch.int32, device="cuda") * L
+        o, lse, ctx = kda.kda_softmax_forward(*(t[:, part] for t in (q, k, v)), cu_seqlens=cu)
+        res = dict(o=o, lse=lse, **kda.kda_softmax_backward(ctx, dO[:, part]))
+        assert kda.kda_device_status(ctx.workspace) == 0
+        return res
+    whole, tail = step(slice(0, None), docs), step(slice((docs - 3) * L, None), 3)
+    for n in tail:
+        assert torch.equal(whole[n][:, -3 * L:], tail[n]), n
+    f, _ = kda.rotary_frequencies(D)
+    pos = torch.arange(docs * L, dtype=torch.int32, device="cuda")[None]
+    a, _ = kda.kda_rotary(q, None, f, positions=pos)
+    b, _ = kda.kda_rotary(q[:, -50:], None, f, positions=pos[:, -50:].contiguous())
+    assert torch.equal(a[:, -50:], b)
+
+
 def test_bad_offsets_and_foreign_workspaces_are_reported():
     x = make(17, [30, 40], [30, 40], 2, 2, 64, "bf16")
     d = {n: x[n].cuda() for n in ("q", "k", "v", "dO")}
@@ -375,6 +422,23 @@ def test_decode_pieces_agree_with_one_piece():
     d = {n: t.cuda() for n, t in many.items()}
     b = kda.kda_softmax_decode_step(*(d[n] for n in ("q", "k", "v", "k_cache", "v_cache", "lengths")))
     assert torch.allclose(a.expand_as(b), b, rtol=0, atol=2e-6)
+
+
+def test_decode_in_a_cache_of_more_than_2_31_values():
+    g = torch.Generator(device="cuda").manual_seed(44)
+    n, cap, H, D = 2, 180000, 48, 128
+    kc, vc = (torch.randn(n, cap, H, D, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    assert kc.numel() > 2 ** 31
+    q, k, v = (torch.randn(n, H, D, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    lengths = torch.tensor([5, cap - 1], dtype=torch.int32, device="cuda")
+    o = kda.kda_softmax_decode_step(q, k, v, kc, vc, lengths)
+    assert torch.equal(kc[1, cap - 1], k[1]) and torch.equal(vc[1, cap - 1], v[1])
+    for h in (0, 47):
+        p = torch.softmax((q[1, h].double() @ kc[1, :, h].double().T) * D ** -0.5, -1)
+        V = vc[1, :, h].double()
+        want, mag = p @ V, p @ V.abs()
+        # two-part weights (2^-16), fp32 sums over 180000 keys in pieces of below 2^13 (2^-10), the output's rounding
+        assert ((o[1, h].double() - want).abs() <= 2.0 ** -10 * mag + 2.0 ** -8 * want.abs()).all()
 
 
 def test_prompt_then_tokens_is_the_longer_prompt():

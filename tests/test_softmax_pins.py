@@ -140,7 +140,8 @@ def test_softmax_refusals():
     for call in (_fwd, _bwd):
         for bad in (dict(B=0), dict(T=0), dict(Tk=0), dict(Hq=0), dict(Hkv=0), dict(Hq=3), dict(Hq=8192), dict(causal=2),
                     dict(dtype=torch.float16), dict(B=1 << 16, T=1 << 16), dict(cu=FAKE, n_docs=0),
-                    dict(cuk=FAKE), dict(cu=FAKE, Tk=101)):
+                    dict(cuk=FAKE), dict(cu=FAKE, Tk=101),
+                    dict(B=1, T=1 << 23, Tk=1 << 23, Hq=4096, Hkv=1, cu=FAKE, n_docs=1 << 23)):
             assert call(_prob(**bad)) == -1, bad
         assert call(_prob(D=96)) == -2 and call(_prob(D=32)) == -2
         assert call(_prob(cu=FAKE + 2)) == -3
