@@ -752,7 +752,8 @@ static const char* const k_names[K_COUNT] = {"chunk_table", "fwd_intra", "fwd_sc
                                              "linear_chain", "linear_seg", "linear_fold", "linear_dqk", "linear_decay", "linear_decode",
                                              "layer_norm_fwd", "layer_norm_bwd", "layer_norm_reduce",
                                              "softmax_table", "softmax_fwd", "softmax_delta", "softmax_dkv", "softmax_dq",
-                                             "softmax_decode", "softmax_join", "softmax_split", "softmax_join_rows", "rotary"};
+                                             "softmax_decode", "softmax_join", "softmax_split", "softmax_join_rows",
+                                             "softmax_join_grads", "rotary"};
 
 const char* kda_prof_kernel_name(int i) { return (i >= 0 && i < K_COUNT) ? k_names[i] : nullptr; }
 

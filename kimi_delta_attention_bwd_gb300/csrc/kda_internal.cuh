@@ -57,6 +57,7 @@ enum KernelId {
   K_SMX_JOIN,
   K_SMX_SPLIT,
   K_SMX_JOIN_ROWS,
+  K_SMX_JOIN_GRADS,
   K_ROTARY,
   K_COUNT
 };

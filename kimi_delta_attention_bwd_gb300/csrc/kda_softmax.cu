@@ -13,11 +13,12 @@ namespace {
 // 2), by decreasing pairs, so that the longest tiles start first and the grid's
 // end is short ones (a counting sort; tiles of equal weight in any order, which no
 // result depends on).  The offsets are checked before any of them is used.
-// The forward's tiles with more than 1.5 times the load that `target` CTAs would have on
-// average are cut along their keys into pieces of about that load, which a further kernel
-// joins: a few queries against long prefixes would else leave most SMs idle behind the
-// longest (11 pieces of prompts, 4096 queries on 30011 keys: 127 us whole, 97 cut; 128 queries
-// of 16 heads on 16384 keys: 176 and 51).
+// Tiles with more than 1.5 times the load that `target` CTAs would have on average are
+// cut along the other side into pieces of about that load, which a further kernel joins:
+// a few queries against long prefixes, or few heads, would else leave most SMs idle
+// behind the longest (11 pieces of prompts, 4096 queries on 30011 keys: 127 us whole, 97
+// cut; 128 queries of 16 heads on 16384 keys: 176 and 51; a training step of 8192 tokens,
+// four heads on one key head at 64: 627 and 303).
 constexpr int TT = 1024, NB = 1024;
 
 __device__ int incl_scan(int x, int* s_warp, int* total) {
@@ -52,6 +53,7 @@ __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P, int l0) {
   const bool by_key = l == 2, near = n <= NS;
   pdl_wait();
   pdl_release();
+  if (!P.list[l]) return;
   const bool ok = l0 == 0 || (*P.wtag == P.tag && *P.err == KDA_OK);  // (block 0 may not write these before block 1 reads)
   const int32_t *cu = P.cu, *cuk = P.cuk;
   int32_t* pre = P.pre[l];
@@ -92,9 +94,10 @@ __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P, int l0) {
   for (int b = tid; b < NB; b += TT) s_cnt[b] = 0;
   if (tid == 0) s_piece = s_join = 0;
   __syncthreads();
+  const int xb = P.xb[l], H = by_key ? P.Hkv : P.Hq;
   struct Found {
     int4 doc;
-    int t, w;  // tile of the document; its pairs a row: keys (queries)
+    int t, nb;  // tile of the document; its blocks of the other side
   };
   auto find = [&](int x) -> Found {  // tile x in the documents' order
     int lo = 0, hi = n - 1;
@@ -106,23 +109,19 @@ __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P, int l0) {
     Found f;
     f.t = x - pre[lo];
     f.doc = make_int4(cu[lo], cu[lo + 1] - cu[lo], cuk[lo], cuk[lo + 1] - cuk[lo]);
-    f.w = by_key ? f.doc.y - first_query(P.causal, f.t * tile, f.doc.y, f.doc.w)
-                 : keys_of(P.causal, min(f.doc.y, (f.t + 1) * tile) - 1, f.doc.y, f.doc.w);
+    f.nb = blocks_of(by_key, P.causal, f.t, tile, xb, P.G, f.doc.y, f.doc.w);
     return f;
   };
-  const bool may_cut = l == 0 && P.target > 0;
+  const bool may_cut = P.target[l] > 0;
   int per = INT_MAX / 2;  // blocks a piece
   if (may_cut) {
     int blocks = 0, total;
-    for (int x = tid; x < carry; x += TT) blocks += (find(x).w + P.xb - 1) / P.xb;
+    for (int x = tid; x < carry; x += TT) blocks += find(x).nb;
     incl_scan(blocks, s_warp, &total);
-    per = max(512 / P.xb, (int)(((int64_t)total * P.Hq + P.target - 1) / P.target));
+    per = max(512 / xb, (int)(((int64_t)total * H + P.target[l] - 1) / P.target[l]));
   }
-  auto pieces_of = [&](const Found& f) {
-    const int nb = (f.w + P.xb - 1) / P.xb;
-    return may_cut && nb > per + per / 2 ? (nb + per - 1) / per : 1;
-  };
-  auto bucket = [&](const Found& f, int np) { return NB - 1 - min(NB - 1, (f.w / np + 63) >> 6); };
+  auto pieces_of = [&](const Found& f) { return may_cut && f.nb > per + per / 2 ? (f.nb + per - 1) / per : 1; };
+  auto bucket = [&](const Found& f, int np) { return NB - 1 - min(NB - 1, f.nb / np); };
   for (int x = tid; x < carry; x += TT) {
     const Found f = find(x);
     const int np = pieces_of(f);
@@ -138,14 +137,15 @@ __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P, int l0) {
   __syncthreads();
   for (int x = tid; x < carry; x += TT) {
     const Found f = find(x);
-    const int np = pieces_of(f), at = atomicAdd(&s_cnt[bucket(f, np)], np), nb = (f.w + P.xb - 1) / P.xb;
+    const int np = pieces_of(f), at = atomicAdd(&s_cnt[bucket(f, np)], np);
     int first = -1;
     if (np > 1) {  // (the room is the bound that the host forms from the same rule)
       first = atomicAdd(&s_piece, np);
       const int j = atomicAdd(&s_join, 1), i0 = f.t * tile;
-      P.joins[j] = make_int4(f.doc.x + i0, min(tile, f.doc.y - i0), first, np);
+      P.joins[l][j] = by_key ? make_int4(f.doc.z + i0, min(tile, f.doc.w - i0), first, np)
+                             : make_int4(f.doc.x + i0, min(tile, f.doc.y - i0), first, np);
     }
-    const int len = (nb + np - 1) / np;
+    const int len = (f.nb + np - 1) / np;
     for (int y = 0; y < np; y++) {
       P.list[l][2 * (size_t)(at + y)] = f.doc;
       P.list[l][2 * (size_t)(at + y) + 1] =
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P, int l0) {
   __syncthreads();
   if (tid == 0) {
     P.counts[l] = entries;
-    if (l == 0) P.counts[3] = s_join;
+    P.counts[3 + l] = s_join;
   }
 }
 
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(256) smx_join_rows_kernel(SmxP P, T* __restric
   const int rows = P.counts[0] == 0 ? 0 : P.counts[3] * tile * P.Hq;  // (at most pieces / 2 tiles of them)
   for (int x = blockIdx.x * 8 + threadIdx.x / 32; x < rows; x += gridDim.x * 8) {
     const int h = x % P.Hq, r = x / P.Hq % tile;
-    const int4 e = P.joins[x / (P.Hq * tile)];
+    const int4 e = P.joins[0][x / (P.Hq * tile)];
     if (r >= e.y) continue;
     const size_t at = ((size_t)e.z * P.Hq + h) * tile + r;
     float m = -INFINITY;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(256) smx_join_rows_kernel(SmxP P, T* __restric
       const float l = P.pl[at + p * step], w = l == -INFINITY ? 0.f : ex2(l - mu);  // (NaN stays)
       sum += w;
 #pragma unroll
-      for (int y = 0; y < NV; y++) acc[y] = fmaf(w, P.po[(at + p * step) * D + lane * NV + y], acc[y]);
+      for (int y = 0; y < NV; y++) acc[y] = fmaf(w, P.po[0][(at + p * step) * D + lane * NV + y], acc[y]);
     }
     const size_t row = (size_t)(e.x + r) * P.Hq + h;
     const float inv = sum == 0.f ? 0.f : 1.0f / sum, l2 = sum != sum ? sum : m + log2f(sum);
@@ -196,6 +196,34 @@ __global__ void __launch_bounds__(256) smx_join_rows_kernel(SmxP P, T* __restric
       lse[row] = l2 * LN2;
       if (P.save) P.lse2[(size_t)h * P.Nq + e.x + r] = l2;
     }
+  }
+}
+
+// The same of the backward, sums of pieces: blockIdx.y 0: dq, 1: dk, 2: dv.
+template <int D, typename T>
+__global__ void __launch_bounds__(256) smx_join_grads_kernel(SmxP P, T* __restrict__ dq, T* __restrict__ dk,
+                                                            T* __restrict__ dv) {
+  constexpr int NV = D / 32;
+  pdl_wait();
+  const int l = blockIdx.y == 0 ? 1 : 2, H = l == 1 ? P.Hq : P.Hkv, tile = P.tile[l], lane = threadIdx.x % 32;
+  if (!P.list[l] || !P.target[l] || *P.err != KDA_OK) return;
+  const size_t step = (size_t)H * tile;
+  const float* part = P.po[l] + (blockIdx.y == 2 ? (size_t)P.pieces[l] * step * D : 0);
+  const float f = blockIdx.y == 2 ? 1.0f : P.scale;
+  T* out = blockIdx.y == 0 ? dq : blockIdx.y == 1 ? dk : dv;
+  const int rows = P.counts[l] == 0 ? 0 : P.counts[3 + l] * tile * H;
+  for (int x = blockIdx.x * 8 + threadIdx.x / 32; x < rows; x += gridDim.x * 8) {
+    const int h = x % H, r = x / H % tile;
+    const int4 e = P.joins[l][x / (H * tile)];
+    if (r >= e.y) continue;
+    const size_t at = ((size_t)e.z * H + h) * tile + r;
+    float acc[NV] = {};
+#pragma unroll 4
+    for (int p = 0; p < e.w; p++)
+#pragma unroll
+      for (int y = 0; y < NV; y++) acc[y] += part[(at + p * step) * D + lane * NV + y];
+#pragma unroll
+    for (int y = 0; y < NV; y++) stf(out + ((size_t)(e.x + r) * H + h) * D + lane * NV + y, acc[y] * f);
   }
 }
 
@@ -247,18 +275,17 @@ __global__ void __launch_bounds__(256) smx_delta_kernel(SmxP P, const T* __restr
 bool a16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
 // Whether equal rows have tiles to cut (the table kernel's rule on their heaviest tile).
-bool worth_cutting(const SmxP& P) {
-  const int tile = P.tile[0], nt = (P.T + tile - 1) / tile;
+bool worth_cutting(const SmxP& P, int l) {
+  const int tile = P.tile[l], nt = ((l == 2 ? P.Tk : P.T) + tile - 1) / tile;
   int64_t total = 0;
   int most = 0;
   for (int t = 0; t < nt; t++) {
-    const int last = (t + 1) * tile < P.T ? (t + 1) * tile : P.T;
-    const int nb = (keys_of(P.causal, last - 1, P.T, P.Tk) + P.xb - 1) / P.xb;
+    const int nb = blocks_of(l == 2, P.causal, t, tile, P.xb[l], P.G, P.T, P.Tk);
     total += nb;
     most = nb > most ? nb : most;
   }
-  int64_t per = (total * P.B * P.Hq + P.target - 1) / P.target;
-  if (per < 512 / P.xb) per = 512 / P.xb;
+  int64_t per = (total * P.B * (l == 2 ? P.Hkv : P.Hq) + P.target[l] - 1) / P.target[l];
+  if (per < 512 / P.xb[l]) per = 512 / P.xb[l];
   return most > per + per / 2;
 }
 
@@ -310,17 +337,20 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   P.scale2 = P.scale * LOG2E;
   const int parts = p->dtype == KDA_F32 ? 3 : 1;
   for (int l = 0; l < 3; l++) P.tile[l] = parts == 3 && p->D == 128 && l > 0 ? F32_TILE : tc_tile(p->D, parts, l);
-  // The forward's cut tiles: where whole tiles would be fewer than four for each of 152 SMs, and some could have more
-  // than a few blocks of keys; a CTA's load is the average of one CTA per SM (half of that, at D = 64 with its two
-  // CTAs, cut tiles of the packed 300M step whose join took what it gave; twice as many pieces for either head dim
-  // lost 3 to 10%).
-  P.xb = tc_block(p->D, parts);
+  // Cut tiles: where whole tiles would be fewer than four for each of 152 SMs, and some could have more than a few
+  // blocks; a CTA's load is the average of one CTA per SM (half of that, at D = 64 with its two CTAs, cut tiles of the
+  // packed 300M step whose join took what it gave; twice as many pieces for either head dim lost 3 to 10%).
   const int wave = 152;
-  if ((int64_t)max_tiles(P, 0) * P.Hq <= 4 * wave && (P.rows ? P.Tk : P.Nk) > 1024 && (!P.rows || P.B <= 1024)) {
-    P.target = wave;
-    // a tile of q > 1.5 average loads has ceil(q) pieces, at most 1.5 q, and all tiles' q sum to at most target / Hq
-    P.pieces = (P.target + P.Hq - 1) / P.Hq * 3 / 2 + 2;
-    if (P.rows && !worth_cutting(P)) P.target = P.pieces = 0;
+  for (int l = 0; l < 3; l++) {
+    const int H = l == 2 ? P.Hkv : P.Hq, other = l == 2 ? (P.rows ? P.T : P.Nq) : P.rows ? P.Tk : P.Nk;
+    P.xb[l] = parts == 3 && p->D == 128 && l > 0 ? F32_BLOCK : tc_block(p->D, parts, l);
+    if ((int64_t)max_tiles(P, l) * H <= 4 * wave && (int64_t)other * (l == 2 ? P.G : 1) > 1024 &&
+        (!P.rows || P.B <= 1024)) {
+      P.target[l] = wave;
+      // a tile of q > 1.5 average loads has ceil(q) pieces, at most 1.5 q, and all tiles' q sum to at most target / H
+      P.pieces[l] = (wave + H - 1) / H * 3 / 2 + 2;
+      if (P.rows && !worth_cutting(P, l)) P.target[l] = P.pieces[l] = 0;
+    }
   }
   for (int l = 0; l < 3; l++)  // (documents, most of them empty, times heads: a grid each)
     if ((int64_t)max_tiles(P, l) * (l == 2 ? P.Hkv : P.Hq) > 2147483647) return KDA_ERR_INVALID_ARG;
@@ -350,15 +380,16 @@ size_t layout(SmxP& P, int D, int dtype, bool bwd, void* base) {
   P.wtag = (int32_t*)(w + 4);
   P.counts = (int32_t*)(w + 8);
   for (int l = 0; l < (bwd ? 3 : 1); l++) {
-    if (P.rows && (l > 0 || !P.target)) continue;
-    P.pre[l] = (int32_t*)(w + take(((size_t)P.n_docs + 1) * sizeof(int32_t)));
-    P.list[l] = (int4*)(w + take((size_t)max_tiles(P, l) * 2 * sizeof(int4)));
-  }
-  if (P.target) {
-    const size_t rows = (size_t)P.pieces * P.Hq * P.tile[0];
-    P.joins = (int4*)(w + take((size_t)P.pieces * sizeof(int4)));
-    P.pl = (float*)(w + take(rows * sizeof(float)));
-    P.po = (float*)(w + take(rows * D * sizeof(float)));
+    if (!P.rows || P.target[l]) {
+      P.pre[l] = (int32_t*)(w + take(((size_t)P.n_docs + 1) * sizeof(int32_t)));
+      P.list[l] = (int4*)(w + take((size_t)max_tiles(P, l) * 2 * sizeof(int4)));
+    }
+    if (P.target[l]) {
+      const size_t rows = (size_t)P.pieces[l] * (l == 2 ? P.Hkv : P.Hq) * P.tile[l];
+      P.joins[l] = (int4*)(w + take((size_t)P.pieces[l] * sizeof(int4)));
+      if (l == 0) P.pl = (float*)(w + take(rows * sizeof(float)));
+      P.po[l] = (float*)(w + take(rows * (l == 2 ? 2 : 1) * D * sizeof(float)));
+    }
   }
   if (bwd) {
     P.lse2 = (float*)(w + take((size_t)P.Hq * P.Nq * sizeof(float)));
@@ -387,8 +418,17 @@ cudaError_t launch_delta(const SmxP& P, const void* o, const void* dO, cudaStrea
 }
 
 template <int D, typename T>
+cudaError_t launch_join_grads(const SmxP& P, void* dq, void* dk, void* dv, cudaStream_t st) {
+  prof_begin(K_SMX_JOIN_GRADS, st);
+  const cudaError_t e = launch_pdl(smx_join_grads_kernel<D, T>, dim3(4 * 152, P.target[2] ? 3 : 1), dim3(256), 0, st, P,
+                                   (T*)dq, (T*)dk, (T*)dv);
+  prof_end(K_SMX_JOIN_GRADS, st);
+  return e;
+}
+
+template <int D, typename T>
 cudaError_t launch_join(const SmxP& P, void* o, float* lse, cudaStream_t st) {
-  const int64_t most = (int64_t)(P.pieces / 2) * P.Hq * (P.tile[0] / 8);  // (a cut tile has two pieces at least)
+  const int64_t most = (int64_t)(P.pieces[0] / 2) * P.Hq * (P.tile[0] / 8);  // (a cut tile has two pieces at least)
   const int64_t grid = most < 8 * 152 ? most : 8 * 152;
   prof_begin(K_SMX_JOIN_ROWS, st);
   const cudaError_t e = launch_pdl(smx_join_rows_kernel<D, T>, dim3((unsigned)grid), dim3(256), 0, st, P, (T*)o, lse);
@@ -438,7 +478,7 @@ extern "C" KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, cons
   } else {
     e = launch_tc_fwd(P, p->D, 1, q, k, v, o, lse, st);
   }
-  if (e == cudaSuccess && P.target) {
+  if (e == cudaSuccess && P.target[0]) {
     if (p->dtype == KDA_F32)
       e = p->D == 64 ? launch_join<64, float>(P, o, lse, st) : launch_join<128, float>(P, o, lse, st);
     else
@@ -458,7 +498,7 @@ extern "C" KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, cons
     if (!a16(x)) return KDA_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < layout(P, p->D, p->dtype, true, workspace)) return KDA_ERR_WORKSPACE;
   if ((uintptr_t)workspace % 256 != 0) return KDA_ERR_ALIGNMENT;
-  if (!P.rows && launch_table(P, 1, 2, st) != cudaSuccess) return KDA_ERR_CUDA;
+  if ((P.list[1] || P.list[2]) && launch_table(P, 1, 2, st) != cudaSuccess) return KDA_ERR_CUDA;
   cudaError_t e;
   if (p->dtype == KDA_F32)
     e = p->D == 64 ? launch_delta<64, float>(P, o, dO, st) : launch_delta<128, float>(P, o, dO, st);
@@ -476,6 +516,12 @@ extern "C" KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, cons
   } else {
     e = launch_f32_bwd(P, (const float*)q, (const float*)k, (const float*)v, (const float*)dO, (float*)dq, (float*)dk,
                        (float*)dv, st);
+  }
+  if (e == cudaSuccess && (P.target[1] || P.target[2])) {
+    if (p->dtype == KDA_F32)
+      e = p->D == 64 ? launch_join_grads<64, float>(P, dq, dk, dv, st) : launch_join_grads<128, float>(P, dq, dk, dv, st);
+    else
+      e = p->D == 64 ? launch_join_grads<64, bf16>(P, dq, dk, dv, st) : launch_join_grads<128, bf16>(P, dq, dk, dv, st);
   }
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

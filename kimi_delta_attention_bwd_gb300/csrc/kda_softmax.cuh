@@ -18,16 +18,16 @@ struct SmxP {
   int save, tag;
   float scale, scale2;  // scale2 = scale log2(e): exponentials are powers of two
   const int32_t *cu, *cuk;
-  int32_t *err, *wtag, *counts;  // counts[l]: entries of list l; counts[3]: split tiles
+  int32_t *err, *wtag, *counts;  // counts[l]: entries of list l; counts[3 + l]: its cut tiles
   int32_t* pre[3];               // [n_docs + 1] first tile of each document
   int4* list[3];                 // two int4 a tile, see Tile; 0: forward's queries, 1: dq's queries, 2: dk and dv's keys
                                  // (nullptr: equal rows, whose tiles follow from their number)
-  // The forward's tiles whose keys are cut into pieces, see smx_table_kernel: pieces' blocks of xb keys, how many CTAs
-  // to aim at (0: no tile is cut), room for how many pieces, their o and log2 sums [piece][Hq][tile][D], the cut tiles
-  // (first query, rows, first piece, pieces).
-  int xb, target, pieces;
-  float *po, *pl;
-  int4* joins;
+  // Tiles that are cut into pieces along the other side, see smx_table_kernel.  Per list: rows of a block of that
+  // side, how many CTAs to aim at (0: no tile is cut), room for how many pieces, the cut tiles (first row, rows, first
+  // piece, pieces), and the pieces' fp32 results [piece][head][tile][D]: o and its log2 sums (pl); dq; dk, then dv.
+  int xb[3], target[3], pieces[3];
+  int4* joins[3];
+  float *po[3], *pl;
   int tile[3];                   // rows a tile
   float *lse2, *delta;           // [Hq][Nq]: log2 of the rows' sums, saved by the forward; sum_d o dO
   bf16* res;                     // [Nq, Hq, D] what rounding o to bf16 left, saved by the forward
@@ -35,7 +35,7 @@ struct SmxP {
 };
 
 // Rows t * tile .. of a document's queries (or keys): its first query, queries, first key, keys.
-// The forward takes blocks j0 .. j1 - 1 of its keys, as piece `piece` (-1: it takes them all).
+// Blocks j0 .. j1 - 1 of the other side (keys; for dk and dv queries, head after head) are taken, as piece `piece` (-1: all).
 struct Tile {
   int q0, Lq, k0, Lk, t, j0, j1, piece;
 };
@@ -74,12 +74,17 @@ __device__ __forceinline__ bool tile_of(const SmxP& P, int l, int x, bool by_key
   t.k0 = a.z;
   t.Lk = a.w;
   t.t = b.x;
-  if (l == 0) {
-    t.j0 = b.y;
-    t.j1 = b.z;
-    t.piece = b.w;
-  }
+  t.j0 = b.y;
+  t.j1 = b.z;
+  t.piece = b.w;
   return true;
+}
+
+// Blocks of the other side that tile t of a document has.
+__host__ __device__ inline int blocks_of(bool by_key, int causal, int t, int tile, int xb, int G, int Lq, int Lk) {
+  if (by_key) return ((Lq + xb - 1) / xb - first_query(causal, t * tile, Lq, Lk) / xb) * G;
+  const int end = (t + 1) * tile < Lq ? (t + 1) * tile : Lq;
+  return (keys_of(causal, end - 1, Lq, Lk) + xb - 1) / xb;
 }
 
 // The backward's kernels read only what a forward of the same problem saved.
@@ -91,7 +96,7 @@ __device__ __forceinline__ bool saved(const SmxP& P) {
 
 // Tensor-core kernels.  parts = 1: bf16 io; 3: fp32 io, its inputs as three bf16 arrays one behind the other
 // (launch_split), the backward at D = 64 only.  Rows of list l's tiles: tc_tile.
-constexpr int tc_block(int D, int parts) { return D == 64 || parts == 3 ? 64 : 128; }  // the forward's blocks of keys
+constexpr int tc_block(int D, int parts, int l) { return D == 64 || (l == 0 && parts == 3) ? 64 : 128; }  // their blocks
 constexpr int tc_tile(int D, int parts, int l) { return l > 0 || (parts == 3 && D == 128) ? 128 : 256; }
 cudaError_t launch_tc_fwd(const SmxP& P, int D, int parts, const void* q, const void* k, const void* v, void* o,
                           float* lse, cudaStream_t st);
@@ -101,13 +106,13 @@ cudaError_t launch_tc_bwd(const SmxP& P, int D, int parts, const void* q, const 
 cudaError_t launch_split(int n, const float* const* x, bf16* const* parts, const int64_t* values, cudaStream_t st);
 
 // The backward of fp32 io at D = 128, on the fp32 pipe: tiles of 64 rows.
-constexpr int F32_TILE = 64;
+constexpr int F32_TILE = 64, F32_BLOCK = 64;
 cudaError_t launch_f32_bwd(const SmxP& P, const float* q, const float* k, const float* v, const float* dO, float* dq,
                            float* dk, float* dv, cudaStream_t st);
 
 // Upper bound on the entries of list l: its tiles, and the pieces of those that are cut.
 inline int max_tiles(const SmxP& P, int l) {
-  const int n = l == 2 ? P.Nk : P.Nq, t = P.tile[l], more = l == 0 ? P.pieces : 0;
+  const int n = l == 2 ? P.Nk : P.Nq, t = P.tile[l], more = P.pieces[l];
   if (P.rows) return P.B * (((l == 2 ? P.Tk : P.T) + t - 1) / t) + more;
   const int64_t m = (int64_t)n / t + P.n_docs;
   return (int)(m < n ? m : n) + more;  // (every tile has a row)

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(NT) smx_dkv_kernel(SmxP P, const float* __rest
   Block<D, TM> bq, bg;
   float nl = 0.f, nd = 0.f;
   auto load = [&](int x) {  // block x of the group's heads' queries
-    const int h = hk * P.G + x / per, i0 = (first + x % per) * TM;
+    const int y = t.j0 + x, h = hk * P.G + y / per, i0 = (first + y % per) * TM;
     const size_t at = ((size_t)(t.q0 + i0) * P.Hq + h) * D;
     bq.load(q + at, ld, t.Lq - i0);
     bg.load(dO + at, ld, t.Lq - i0);
@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(NT) smx_dkv_kernel(SmxP P, const float* __rest
       nd = in ? P.delta[r] : 0.f;
     }
   };
-  const int n = per * P.G;
+  const int n = min(per * P.G, t.j1) - t.j0;
   if (n > 0) load(0);
   for (int x = 0; x < n; x++) {
-    const int i0 = (first + x % per) * TM;
+    const int i0 = (first + (t.j0 + x) % per) * TM;
     __syncthreads();
     bq.store(tQ, sQ);
     bg.store(tG, sG);
@@ -194,14 +194,17 @@ __global__ void __launch_bounds__(NT) smx_dkv_kernel(SmxP P, const float* __rest
   for (int i = 0; i < R; i++) {
     const int r = R * ty + i;
     if (r >= nk) continue;
-    const size_t row = ((size_t)(t.k0 + j0 + r) * P.Hkv + hk) * D;
+    const bool whole = t.piece < 0;
+    const size_t row = ((size_t)(t.k0 + j0 + r) * P.Hkv + hk) * D, pa = (((size_t)t.piece * P.Hkv + hk) * OWN + r) * D;
+    float* ok = whole ? dk + row : P.po[2] + pa;
+    float* ov = whole ? dv + row : P.po[2] + (size_t)P.pieces[2] * P.Hkv * OWN * D + pa;
+    const float f = whole ? P.scale : 1.0f;
 #pragma unroll
     for (int c = 0; c < D / 64; c++) {
-      const float x[4] = {ak[i][4 * c] * P.scale, ak[i][4 * c + 1] * P.scale, ak[i][4 * c + 2] * P.scale,
-                          ak[i][4 * c + 3] * P.scale};
+      const float x[4] = {ak[i][4 * c] * f, ak[i][4 * c + 1] * f, ak[i][4 * c + 2] * f, ak[i][4 * c + 3] * f};
       const float y[4] = {av[i][4 * c], av[i][4 * c + 1], av[i][4 * c + 2], av[i][4 * c + 3]};
-      st4(dk + row + 64 * c + 4 * tx, x);
-      st4(dv + row + 64 * c + 4 * tx, y);
+      st4(ok + 64 * c + 4 * tx, x);
+      st4(ov + 64 * c + 4 * tx, y);
     }
   }
 }
@@ -240,12 +243,15 @@ __global__ void __launch_bounds__(NT) smx_dq_kernel(SmxP P, const float* __restr
     del[i] = r < nq ? P.delta[at] : 0.f;
     lim[i] = r < nq ? keys_of(P.causal, i0 + r, t.Lq, t.Lk) : 0;
   }
-  const int nk = keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk);
+  const int nk = (int)min((int64_t)keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk), (int64_t)t.j1 * TM);
   const size_t ld = (size_t)P.Hkv * D, at = ((size_t)t.k0 * P.Hkv + hk) * D;
   Block<D, TM> bk, bv;
-  bk.load(k + at, ld, t.Lk);
-  bv.load(v + at, ld, t.Lk);
-  for (int j0 = 0; j0 < nk; j0 += TM) {
+  const int first = t.j0 * TM;
+  if (first < nk) {
+    bk.load(k + at + first * ld, ld, t.Lk - first);
+    bv.load(v + at + first * ld, ld, t.Lk - first);
+  }
+  for (int j0 = first; j0 < nk; j0 += TM) {
     __syncthreads();
     bk.store(tK, sK);
     bv.store(tV, nullptr);
@@ -272,11 +278,13 @@ __global__ void __launch_bounds__(NT) smx_dq_kernel(SmxP P, const float* __restr
   for (int i = 0; i < R; i++) {
     const int r = R * ty + i;
     if (r >= nq) continue;
+    const bool whole = t.piece < 0;
+    float* out = whole ? dq + qa + (size_t)r * P.Hq * D : P.po[1] + (((size_t)t.piece * P.Hq + h) * OWN + r) * D;
+    const float f = whole ? P.scale : 1.0f;
 #pragma unroll
     for (int c = 0; c < D / 64; c++) {
-      const float x[4] = {acc[i][4 * c] * P.scale, acc[i][4 * c + 1] * P.scale, acc[i][4 * c + 2] * P.scale,
-                          acc[i][4 * c + 3] * P.scale};
-      st4(dq + qa + (size_t)r * P.Hq * D + 64 * c + 4 * tx, x);
+      const float x[4] = {acc[i][4 * c] * f, acc[i][4 * c + 1] * f, acc[i][4 * c + 2] * f, acc[i][4 * c + 3] * f};
+      st4(out + 64 * c + 4 * tx, x);
     }
   }
 }

@@ -251,6 +251,20 @@ __device__ __forceinline__ void store_acc(unsigned char* buf, uint32_t tm, bool 
   }
   store_rows(buf, u, dst, ld, n);
 }
+__device__ __forceinline__ void store_acc_f32(unsigned char* buf, uint32_t tm, bool any, float* dst, size_t ld, int n) {
+#pragma unroll
+  for (int c = 0; c < 64; c += 32) {
+    float v[32];
+    uint32_t u[32];
+    if (any) {
+      tm_ld32(tm + c, v);
+      tm_wait_ld(v);
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e++) u[e] = any ? __float_as_uint(v[e]) : 0u;
+    store_rows(buf, u, dst + c, ld, n);
+  }
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
 }
@@ -663,7 +677,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       // a piece's o, or o of fp32 io
       const size_t at = ((size_t)t.piece * P.Hq + h) * (NT * BLK);
       if (PARTS == 3 || t.piece >= 0) {
-        float* dst = t.piece >= 0 ? P.po + (at + w0) * D : (float*)o + row0 * D;
+        float* dst = t.piece >= 0 ? P.po[0] + (at + w0) * D : (float*)o + row0 * D;
         const size_t ld = t.piece >= 0 ? D : (size_t)P.Hq * D;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
@@ -905,7 +919,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     first = first_query(P.causal, j0, t.Lq, t.Lk) / XB;
     per = max(0, (t.Lq + XB - 1) / XB - first);
   }
-  const int n = per * P.G;
+  const int n = live ? min(per * P.G, t.j1) - t.j0 : 0;
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -919,7 +933,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     }
     __syncwarp();
     for (int x = 0; x < n; x++) {
-      const int sa = x % F::NA, sb = x % F::NB, h = hk * P.G + x / per, row = t.q0 + (first + x % per) * XB;
+      const int sa = x % F::NA, sb = x % F::NB, y = t.j0 + x, h = hk * P.G + y / per, row = t.q0 + (first + y % per) * XB;
       if (x >= F::NA && !wait(&B.emptyA[sa], (x / F::NA - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullA[sa], F::BYTES);
@@ -938,7 +952,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     for (int x = 0; x < n; x++) {
       const int s = x & 1;  // (free once block x - 2 has left ring A)
       if (x >= 2 && !wait(&B.emptyA[(x - 2) % F::NA], ((x - 2) / F::NA) & 1, &B.dead)) break;
-      const int h = hk * P.G + x / per, i0 = (first + x % per) * XB;
+      const int y = t.j0 + x, h = hk * P.G + y / per, i0 = (first + y % per) * XB;
       const size_t at = (size_t)h * P.Nq + t.q0 + i0;
 #pragma unroll
       for (int c = lane; c < XB; c += 32) {
@@ -969,7 +983,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     };
     // block x of queries (of their dO) has landed; rows behind its document's last are zeros
     auto ready = [&](int x, unsigned char* block, uint64_t* full, int phase) -> bool {
-      const int left = t.Lq - (first + x % per) * XB;
+      const int left = t.Lq - (first + (t.j0 + x) % per) * XB;
       if (!wait(full, phase & 1, &B.dead)) return false;
       if (left < XB) zero_rows<D, XB, PARTS>(block, left);
       return true;
@@ -1021,7 +1035,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     float sv[PARTS == 3 ? 32 : 1] = {}, sk[PARTS == 3 ? 32 : 1] = {};  // (three parts) dv and dk, columns 32 half ..
     bool ok = true;
     for (int x = 0; x < n; x++) {
-      const int s = x & 1, i0 = (first + x % per) * XB;
+      const int s = x & 1, i0 = (first + (t.j0 + x) % per) * XB;
       const float *l2 = B.stat[s][0] + W * half, *dl = B.stat[s][1] + W * half;
       const bool cut = i0 < fq_last || i0 + XB > t.Lq;
       const int lo = fq - i0 - W * half, hi = t.Lq - i0 - W * half;
@@ -1069,13 +1083,19 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       const int w0 = r & ~31, c = PARTS == 3 ? 32 * half : 64 * half;  // (the CTA's own blocks are no longer read)
       const size_t at = ((size_t)(t.k0 + j0 + w0) * P.Hkv + hk) * D + c, ld = (size_t)P.Hkv * D;
       unsigned char* buf = sm + half * HALF + w0 * 128;
+      const size_t pa = (((size_t)t.piece * P.Hkv + hk) * BLK + w0) * D + c;  // (a piece's place)
+      const size_t more = (size_t)P.pieces[2] * P.Hkv * BLK * D;
       if constexpr (PARTS == 3) {
         if (n > 0) {
           add_columns(sv, tm + cDV + c + lanes);
           add_columns(sk, tm + cDK + c + lanes);
         }
-        store_sums(buf, sv, 1.0f, dv + at, ld, nk - w0);
-        store_sums(buf, sk, P.scale, dk + at, ld, nk - w0);
+        const bool whole = t.piece < 0;
+        store_sums(buf, sv, 1.0f, whole ? dv + at : P.po[2] + more + pa, whole ? ld : D, nk - w0);
+        store_sums(buf, sk, whole ? P.scale : 1.0f, whole ? dk + at : P.po[2] + pa, whole ? ld : D, nk - w0);
+      } else if (t.piece >= 0) {
+        store_acc_f32(buf, tm + cDV + c + lanes, n > 0, P.po[2] + more + pa, D, nk - w0);
+        store_acc_f32(buf, tm + cDK + c + lanes, n > 0, P.po[2] + pa, D, nk - w0);
       } else {
         store_acc(buf, tm + cDV + c + lanes, n > 0, 1.0f, dv + at, ld, nk - w0);
         store_acc(buf, tm + cDK + c + lanes, n > 0, P.scale, dk + at, ld, nk - w0);
@@ -1147,7 +1167,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   if (live) {
     i0 = t.t * BLK;
     nq = min(BLK, t.Lq - i0);
-    n = (keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk) + XB - 1) / XB;
+    n = min((keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk) + XB - 1) / XB, t.j1) - t.j0;
     clean = keys_of(P.causal, i0, t.Lq, t.Lk) / XB;
   }
   tc::fence_before();
@@ -1167,13 +1187,13 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (x >= F::NA && !wait(&B.emptyA[sa], (x / F::NA - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullA[sa], F::BYTES);
-        load_block<D, XB, PARTS>(ringA + sa * F::BYTES, &mk, hk, t.k0 + x * XB, P.Nk, &B.fullA[sa]);
+        load_block<D, XB, PARTS>(ringA + sa * F::BYTES, &mk, hk, t.k0 + (t.j0 + x) * XB, P.Nk, &B.fullA[sa]);
       }
       __syncwarp();
       if (x >= F::NB && !wait(&B.emptyB[sb], (x / F::NB - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullB[sb], F::BYTES);
-        load_block<D, XB, PARTS>(ringB + sb * F::BYTES, &mv, hk, t.k0 + x * XB, P.Nk, &B.fullB[sb]);
+        load_block<D, XB, PARTS>(ringB + sb * F::BYTES, &mv, hk, t.k0 + (t.j0 + x) * XB, P.Nk, &B.fullB[sb]);
       }
       __syncwarp();
     }
@@ -1189,7 +1209,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       commit(&B.emptyB[x % F::NB], me);
     };
     auto ready = [&](int x) -> bool {
-      const int left = t.Lk - x * XB;
+      const int left = t.Lk - (t.j0 + x) * XB;
       if (!wait(&B.fullA[x % F::NA], (x / F::NA) & 1, &B.dead)) return false;
       if (left < XB) zero_rows<D, XB, PARTS>(ringA + x % F::NA * F::BYTES, left);
       return wait(&B.fullB[x % F::NB], (x / F::NB) & 1, &B.dead);
@@ -1251,8 +1271,8 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       tc::fence_before();
       __syncwarp();
       if (lane == 0) mma::mbar_arrive(&B.taken);
-      const int left = lim - x * XB - 64 * half;
-      const bool cut = x >= clean;
+      const int left = lim - (t.j0 + x) * XB - 64 * half;
+      const bool cut = t.j0 + x >= clean;
 #pragma unroll
       for (int c = 0; c < 2; c++) dq_grads(a[c], g[c], sc, l2, dl, cut, left - 32 * c);
       if (x >= 2) {
@@ -1272,17 +1292,20 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       ok = wait(&B.used[(n - 1) & 1], ((n - 1) / 2) & 1, &B.dead);
       tc::fence_after();
     }
-    if constexpr (PARTS == 3) {
-      if (ok) {
-        const int w0 = r & ~31;
-        for (int x = max(0, n - 2); x < n; x++) add_columns(sum, tm + cDQ + nDQ * (x & 1) + lanes);
-        store_sums(sm + w0 * 128, sum, P.scale, dq + ((size_t)(t.q0 + i0 + w0) * P.Hq + h) * D, (size_t)P.Hq * D,
-                   nq - w0);
-      }
-    } else if (ok) {
+    if (ok) {
       const int w0 = r & ~31, c = 64 * half;
-      store_acc(sm + half * HALF + w0 * 128, tm + cDQ + c + lanes, n > 0, P.scale,
-                dq + ((size_t)(t.q0 + i0 + w0) * P.Hq + h) * D + c, (size_t)P.Hq * D, nq - w0);
+      unsigned char* buf = sm + half * HALF + w0 * 128;
+      const size_t to = ((size_t)(t.q0 + i0 + w0) * P.Hq + h) * D + c, ld = (size_t)P.Hq * D;
+      const size_t pa = (((size_t)t.piece * P.Hq + h) * BLK + w0) * D + c;  // (a piece's place)
+      if constexpr (PARTS == 3) {
+        for (int x = max(0, n - 2); x < n; x++) add_columns(sum, tm + cDQ + nDQ * (x & 1) + lanes);
+        const bool whole = t.piece < 0;
+        store_sums(buf, sum, whole ? P.scale : 1.0f, whole ? dq + to : P.po[1] + pa, whole ? ld : D, nq - w0);
+      } else if (t.piece >= 0) {
+        store_acc_f32(buf, tm + cDQ + c + lanes, n > 0, P.po[1] + pa, D, nq - w0);
+      } else {
+        store_acc(buf, tm + cDQ + c + lanes, n > 0, P.scale, dq + to, ld, nq - w0);
+      }
     }
     tc::fence_before();
   }
