@@ -9,10 +9,15 @@
 // relative precision as those below 1.
 // Weights are rounded to bf16 (2^-8, the operand's type; o's error with that is that of one rounding of o times
 // sqrt(2)), but in a first block that a mask cuts they enter as two parts (2^-16): rows with few keys have theirs there,
-// and the backward's delta = o dO cancels against dO v in just those rows.
+// and the backward's delta = o dO cancels against dO v in just those rows.  Documents
+// of few rows, or against few of the other side (FEW_ROWS, FEW), take two parts throughout, in the backward too, where
+// the whole problem is small (SmxP::few): a handful of roundings does not average out (up to 1.8 times the error of
+// weights that are multiplied in fp32 and a result rounded once; with two parts 1.5).
 #include "kda_softmax.cuh"
 #include "kda_mma.cuh"
 #include "kda_tc.cuh"
+
+#include <type_traits>
 
 namespace kda {
 namespace smx {
@@ -20,6 +25,7 @@ namespace {
 
 constexpr int BLK = 128;       // rows of a block of keys (or queries)
 constexpr int HALF = 16384;    // bytes of 128 rows by 64 columns, one swizzled half of a block
+constexpr int FEW_ROWS = 64, FEW = 256;  // a document's rows on a kernel's own side, and on the other, for two parts
 constexpr float GROW = 8.0f;   // log2 of what a weight may exceed 1 by
 
 // The tensor memory's address, the same for the whole warp: with all 512 columns its first one.
@@ -265,6 +271,13 @@ __device__ __forceinline__ void store_acc_f32(unsigned char* buf, uint32_t tm, b
     store_rows(buf, u, dst + c, ld, n);
   }
 }
+// f with `twice` as a constant (a branch inside its loop cost dk and dv 8% and dq 5% at D = 128)
+template <int PARTS, class F>
+__device__ __forceinline__ bool with_parts(bool twice, F f) {
+  if constexpr (PARTS == 1)
+    if (twice) return f(std::true_type{});
+  return f(std::false_type{});
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
 }
@@ -407,9 +420,11 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   const int h = blockIdx.x % P.Hq, hk = h / P.G;
   const bool live = tile_of(P, 0, blockIdx.x / P.Hq, false, t);
   int i0 = 0, nq = 0, nb[2] = {0, 0}, clean[2] = {0, 0};  // blocks of each tile; those that no mask cuts
+  bool twice = false;                                     // every weight in two parts
   if (live) {
     i0 = t.t * (NT * BLK);
     nq = min(NT * BLK, t.Lq - i0);
+    twice = PARTS == 1 && P.few && (t.Lq <= FEW_ROWS || t.Lk <= FEW);
 #pragma unroll
     for (int i = 0; i < NT; i++)
       if (i * BLK < nq) {
@@ -487,7 +502,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
             for (int s = 0; s < XB / 16; s++)
               mma_ts(d, Q::a(y) == 2 ? c + 8 * s : a + F::part(s) + Q::a(y) * F::SECOND,
                      desc_mn<XB>(vb + Q::b(y) * (XB * D * 2), s), id_o, (PARTS == 1 && j > 0) || y > 0 || s > 0, me);
-          if (PARTS == 1 && t.j0 + j == 0 && clean[i] == 0)
+          if (PARTS == 1 && (twice || (t.j0 + j == 0 && clean[i] == 0)))
 #pragma unroll
             for (int s = 0; s < XB / 16; s++)
               mma_ts(d, a + F::part(s) + F::SECOND, desc_mn<XB>(vb, s), id_o, true, me);
@@ -557,7 +572,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       tc::fence_after();
       if constexpr (PARTS == 3)
         if (j > 0) take_block();
-      const bool cut = t.j0 + j >= cleani, few = cut && t.j0 + j == 0;  // a mask cuts the block; some rows may have few keys in all
+      const bool cut = t.j0 + j >= cleani, few = twice || (cut && t.j0 + j == 0);  // a mask cuts the block; two parts
       const int left = lim - (t.j0 + j) * XB, least = cut ? __shfl_sync(0xffffffffu, left, 0) : XB;  // (the warp's first row's)
       uint64_t sum[2] = {0, 0};
       float s0, s1;
@@ -590,7 +605,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
         // The weights against the reference as it is: a row's sum of at most 2^GROW says that none is above it, and the
         // maximum need not be known.  Else, and in the first block, the maximum first (a NaN row: every time).
         float a[16], b[16];
-        bool ask = false, again = j == 0 || PARTS == 3;
+        bool ask = false, again = j == 0 || few || PARTS == 3;
         if (PARTS == 1 && !again) {
           const float neg = reference();
           const uint64_t ng = two(neg, neg);
@@ -777,23 +792,34 @@ __device__ __forceinline__ void bwd_grads(float (&p)[32], const float (&dp)[32],
 #pragma unroll
     for (int e = 0; e < 32; e++) p[e] = e >= lo && e < hi ? p[e] : 0.f;
 }
-// 32 H pairs of a row as operands: bf16 at `to`, second parts 16 H columns further, third at `x3`.
-template <int PARTS, int H>
+// 32 H pairs of a row as operands: bf16 at `to`, second parts (three parts, or TWICE) 16 H columns further,
+// third at `x3`.
+template <int PARTS, bool TWICE, int H>
 __device__ __forceinline__ void put_parts(float (&v)[H][32], uint32_t to, uint32_t x3) {
 #pragma unroll
-  for (int y = 0; y < PARTS; y++)
+  for (int y = 0; y < (TWICE ? 2 : PARTS); y++) {
 #pragma unroll
     for (int c = 0; c < H; c++) {
       uint32_t w[16];
-      if (PARTS == 1) {
 #pragma unroll
-        for (int e = 0; e < 16; e++) w[e] = pack(v[c][2 * e], v[c][2 * e + 1]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; e++) w[e] = rest(v[c][2 * e], v[c][2 * e + 1], y);
-      }
+      for (int e = 0; e < 16; e++) w[e] = rest(v[c][2 * e], v[c][2 * e + 1], y);
       tm_st16((y == 2 ? x3 : to + 16 * H * y) + 16 * c, w);
     }
+  }
+}
+// The same in dq, whose parts lie XB / 2 columns apart.
+template <int PARTS, bool TWICE, int XB>
+__device__ __forceinline__ void put_dq(float (&v)[2][32], uint32_t to) {
+#pragma unroll
+  for (int y = 0; y < (TWICE ? 2 : PARTS); y++) {
+#pragma unroll
+    for (int c = 0; c < 2; c++) {
+      uint32_t w[16];
+#pragma unroll
+      for (int e = 0; e < 16; e++) w[e] = rest(v[c][2 * e], v[c][2 * e + 1], y);
+      tm_st16(to + XB / 2 * y + 16 * c, w);
+    }
+  }
 }
 template <int N>
 __device__ __forceinline__ void add_columns(float (&sum)[N], uint32_t tm) {
@@ -919,6 +945,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     first = first_query(P.causal, j0, t.Lq, t.Lk) / XB;
     per = max(0, (t.Lq + XB - 1) / XB - first);
   }
+  const bool twice = PARTS == 1 && P.few && live && (t.Lk <= FEW_ROWS || t.Lq <= FEW);
   const int n = live ? min(per * P.G, t.j1) - t.j0 : 0;
   tc::fence_before();
   __syncthreads();
@@ -972,7 +999,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       commit(bar, me);
     };
     // (a thread's pairs, 32 H columns, are 16 H of bf16, second parts 16 H further, third at x3)
-    auto apply = [&](uint32_t d, uint32_t a, uint32_t x3, uint32_t b, bool acc) {
+    auto apply = [&](auto tw, uint32_t d, uint32_t a, uint32_t x3, uint32_t b, bool acc) {
       using Q = Prod<PARTS>;
 #pragma unroll
       for (int y = 0; y < Q::N; y++)
@@ -980,6 +1007,10 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
         for (int s = 0; s < XB / 16; s++)
           mma_ts(tm + d, tm + (Q::a(y) == 2 ? x3 + 8 * s : a + 32 * H * (s / (2 * H)) + 8 * (s % (2 * H)) + 16 * H * Q::a(y)),
                  desc_mn<XB>(b + Q::b(y) * (XB * D * 2), s), id_o, (PARTS == 1 && acc) || y > 0 || s > 0, me);
+      if constexpr (decltype(tw)::value)
+#pragma unroll
+        for (int s = 0; s < XB / 16; s++)
+          mma_ts(tm + d, tm + a + 32 * H * (s / (2 * H)) + 8 * (s % (2 * H)) + 16 * H, desc_mn<XB>(b, s), id_o, true, me);
     };
     // block x of queries (of their dO) has landed; rows behind its document's last are zeros
     auto ready = [&](int x, unsigned char* block, uint64_t* full, int phase) -> bool {
@@ -990,7 +1021,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     };
     auto readyA = [&](int x) { return ready(x, ringA + x % F::NA * F::BYTES, &B.fullA[x % F::NA], x / F::NA); };
     auto readyB = [&](int x) { return ready(x, ringB + x % F::NB * F::BYTES, &B.fullB[x % F::NB], x / F::NB); };
-    auto run = [&]() -> bool {
+    auto run = [&](auto tw) -> bool {
       if (!wait(&B.own, 0, &B.dead) || !readyA(0)) return false;
       pairs(cS, k0, a0, &B.s);
       if (!readyB(0)) return false;
@@ -1001,7 +1032,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
         const bool more = x + 1 < n;
         if (!wait(&B.p, x & 1, &B.dead)) return false;
         tc::fence_after();
-        apply(cDV, cS, cX, gb, x > 0);
+        apply(tw, cDV, cS, cX, gb, x > 0);
         commit(&B.emptyB[x % F::NB], me);
         if (more) {
           if (!readyA(x + 1)) return false;
@@ -1009,7 +1040,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
         }
         if (!wait(&B.ds, x & 1, &B.dead)) return false;
         tc::fence_after();
-        apply(cDK, cDP, cX + XB / 2, qb, x > 0);
+        apply(tw, cDK, cDP, cX + XB / 2, qb, x > 0);
         commit(&B.emptyA[x % F::NA], me);
         if (more) {
           if (!readyB(x + 1)) return false;
@@ -1020,7 +1051,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       }
       return true;
     };
-    if (n > 0 && !run()) {
+    if (n > 0 && !with_parts<PARTS>(twice, run)) {
       commit(&B.drain, me);
       for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
     }
@@ -1033,48 +1064,49 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     const int fq = first_query(P.causal, j0 + r, t.Lq, t.Lk), fq_last = first_query(P.causal, j0 + nk - 1, t.Lq, t.Lk);
     const uint64_t sc = two(P.scale2, P.scale2);
     float sv[PARTS == 3 ? 32 : 1] = {}, sk[PARTS == 3 ? 32 : 1] = {};  // (three parts) dv and dk, columns 32 half ..
-    bool ok = true;
-    for (int x = 0; x < n; x++) {
-      const int s = x & 1, i0 = (first + (t.j0 + x) % per) * XB;
-      const float *l2 = B.stat[s][0] + W * half, *dl = B.stat[s][1] + W * half;
-      const bool cut = i0 < fq_last || i0 + XB > t.Lq;
-      const int lo = fq - i0 - W * half, hi = t.Lq - i0 - W * half;
-      float a[H][32];
-      ok = wait(&B.fullS[s], (x >> 1) & 1, &B.dead) && wait(&B.s, x & 1, &B.dead);
-      if (!ok) break;
-      tc::fence_after();
+    auto pairs = [&](auto tw) -> bool {
+      for (int x = 0; x < n; x++) {
+        const int s = x & 1, i0 = (first + (t.j0 + x) % per) * XB;
+        const float *l2 = B.stat[s][0] + W * half, *dl = B.stat[s][1] + W * half;
+        const bool cut = i0 < fq_last || i0 + XB > t.Lq;
+        const int lo = fq - i0 - W * half, hi = t.Lq - i0 - W * half;
+        float a[H][32];
+        if (!wait(&B.fullS[s], (x >> 1) & 1, &B.dead) || !wait(&B.s, x & 1, &B.dead)) return false;
+        tc::fence_after();
 #pragma unroll
-      for (int c = 0; c < H; c++) tm_ld32(ts + 32 * c, a[c]);
+        for (int c = 0; c < H; c++) tm_ld32(ts + 32 * c, a[c]);
 #pragma unroll
-      for (int c = 0; c < H; c++) tm_wait_ld(a[c]);
+        for (int c = 0; c < H; c++) tm_wait_ld(a[c]);
 #pragma unroll
-      for (int c = 0; c < H; c++) bwd_weights(a[c], l2 + 32 * c, sc, cut, lo - 32 * c, hi - 32 * c);
-      // (over logits of its own: the other half's warp may still read its)
-      put_parts<PARTS, H>(a, ts, x3);
-      if constexpr (PARTS == 3)
-        if (x > 0) add_columns(sv, tm + cDV + 32 * half + lanes);  // (the block before's: issued before this S')
-      tm_wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mma::mbar_arrive(&B.p);
-      ok = wait(&B.dp, x & 1, &B.dead);
-      if (!ok) break;
-      tc::fence_after();
+        for (int c = 0; c < H; c++) bwd_weights(a[c], l2 + 32 * c, sc, cut, lo - 32 * c, hi - 32 * c);
+        // (over logits of its own: the other half's warp may still read its)
+        put_parts<PARTS, decltype(tw)::value, H>(a, ts, x3);
+        if constexpr (PARTS == 3)
+          if (x > 0) add_columns(sv, tm + cDV + 32 * half + lanes);  // (the block before's: issued before this S')
+        tm_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mma::mbar_arrive(&B.p);
+        if (!wait(&B.dp, x & 1, &B.dead)) return false;
+        tc::fence_after();
 #pragma unroll
-      for (int c = 0; c < H; c++) {
-        float g[32];
-        tm_ld32(td + 32 * c, g);
-        tm_wait_ld(g);
-        bwd_grads(a[c], g, dl + 32 * c, cut, lo - 32 * c, hi - 32 * c);
+        for (int c = 0; c < H; c++) {
+          float g[32];
+          tm_ld32(td + 32 * c, g);
+          tm_wait_ld(g);
+          bwd_grads(a[c], g, dl + 32 * c, cut, lo - 32 * c, hi - 32 * c);
+        }
+        put_parts<PARTS, decltype(tw)::value, H>(a, td, x3 + XB / 2);
+        if constexpr (PARTS == 3)
+          if (x > 0) add_columns(sk, tm + cDK + 32 * half + lanes);
+        tm_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mma::mbar_arrive(&B.ds);
       }
-      put_parts<PARTS, H>(a, td, x3 + XB / 2);
-      if constexpr (PARTS == 3)
-        if (x > 0) add_columns(sk, tm + cDK + 32 * half + lanes);
-      tm_wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mma::mbar_arrive(&B.ds);
-    }
+      return true;
+    };
+    bool ok = with_parts<PARTS>(twice, pairs);
     if (ok && n > 0) {
       ok = wait(&B.done, 0, &B.dead);
       tc::fence_after();
@@ -1128,7 +1160,8 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
                  typename Io<PARTS>::T* __restrict__ dq) {
   using F = Bwd<D, PARTS>;
   constexpr int XB = F::XB, EW = F::EW;
-  constexpr uint32_t cS = 0, cDP = XB, cDQ = 2 * XB, nDQ = PARTS == 3 ? D : 0, cDS = 2 * XB + D + nDQ, nDS = XB / 2 * PARTS;  // (columns to the other dq; of one dS, its parts)
+  constexpr uint32_t cS = 0, cDP = XB, cDQ = 2 * XB, nDQ = PARTS == 3 ? D : 0;         // (nDQ: columns to the other dq)
+  constexpr uint32_t cDS = 2 * XB + D + nDQ, nDS = XB / 2 * PARTS;                     // (nDS: of one dS, its parts)
   extern __shared__ unsigned char raw[];
   __shared__ DqBars B;
   unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
@@ -1164,9 +1197,11 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   const int h = blockIdx.x % P.Hq, hk = h / P.G;
   const bool live = saved(P) && tile_of(P, 1, blockIdx.x / P.Hq, false, t);
   int i0 = 0, nq = 0, n = 0, clean = 0;
+  bool twice = false;  // dS in two parts, in its two places together
   if (live) {
     i0 = t.t * BLK;
     nq = min(BLK, t.Lq - i0);
+    twice = PARTS == 1 && P.few && (t.Lq <= FEW_ROWS || t.Lk <= FEW);
     n = min((keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk) + XB - 1) / XB, t.j1) - t.j0;
     clean = keys_of(P.causal, i0, t.Lq, t.Lk) / XB;
   }
@@ -1174,6 +1209,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   __syncthreads();
   tc::fence_after();
   const uint32_t tm = tm_base<F::COLS>(B.tmem);
+  auto place = [](auto tw, int x) { return decltype(tw)::value ? 0 : x & 1; };  // of block x's dS
 
   if (warp == EW + 1) {  // copies
     if (lane == 0 && n > 0) {
@@ -1214,7 +1250,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       if (left < XB) zero_rows<D, XB, PARTS>(ringA + x % F::NA * F::BYTES, left);
       return wait(&B.fullB[x % F::NB], (x / F::NB) & 1, &B.dead);
     };
-    auto run = [&]() -> bool {
+    auto run = [&](auto tw) -> bool {
       if (!wait(&B.own, 0, &B.dead) || !ready(0)) return false;
       pairs(0);
       for (int x = 0; x < n; x++) {
@@ -1231,14 +1267,17 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
         for (int y = 0; y < Q::N; y++)
 #pragma unroll
           for (int s = 0; s < XB / 16; s++)
-            mma_ts(tm + cDQ + nDQ * (x & 1), tm + cDS + nDS * (x & 1) + XB / 2 * Q::a(y) + 8 * s,
+            mma_ts(tm + cDQ + nDQ * (x & 1), tm + cDS + nDS * place(tw, x) + XB / 2 * Q::a(y) + 8 * s,
                    desc_mn<XB>(kb + Q::b(y) * (XB * D * 2), s), id_o, (PARTS == 1 && x > 0) || y > 0 || s > 0, me);
-        commit(&B.used[x & 1], me);
+        if constexpr (decltype(tw)::value)
+#pragma unroll
+          for (int s = 0; s < XB / 16; s++) mma_ts(tm + cDQ, tm + cDS + XB / 2 + 8 * s, desc_mn<XB>(kb, s), id_o, true, me);
+        commit(&B.used[place(tw, x)], me);
         commit(&B.emptyA[x % F::NA], me);
       }
       return true;
     };
-    if (n > 0 && !run()) {
+    if (n > 0 && !with_parts<PARTS>(twice, run)) {
       commit(&B.drain, me);
       for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
     }
@@ -1252,46 +1291,46 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
     const float nl = in ? -P.lse2[at] : 0.f, nd = in ? -P.delta[at] : 0.f;
     const uint64_t sc = two(P.scale2, P.scale2), l2 = two(nl, nl), dl = two(nd, nd);
     float sum[PARTS == 3 ? 64 : 1] = {};  // (three parts) dq
-    bool ok = true;
-    for (int x = 0; x < n; x++) {
-      ok = wait(&B.s, x & 1, &B.dead);
-      if (!ok) break;
-      tc::fence_after();
-      float a[2][32], g[2][32];
-#pragma unroll
-      for (int c = 0; c < 2; c++) {
-        tm_ld32(ts + 32 * c, a[c]);
-        tm_ld32(td + 32 * c, g[c]);
-      }
-#pragma unroll
-      for (int c = 0; c < 2; c++) {
-        tm_wait_ld(a[c]);
-        tm_wait_ld(g[c]);
-      }
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mma::mbar_arrive(&B.taken);
-      const int left = lim - (t.j0 + x) * XB - 64 * half;
-      const bool cut = t.j0 + x >= clean;
-#pragma unroll
-      for (int c = 0; c < 2; c++) dq_grads(a[c], g[c], sc, l2, dl, cut, left - 32 * c);
-      if (x >= 2) {
-        ok = wait(&B.used[x & 1], (x / 2 - 1) & 1, &B.dead);
-        if (!ok) break;
+    auto pairs = [&](auto tw) -> bool {
+      constexpr bool TW = decltype(tw)::value;
+      for (int x = 0; x < n; x++) {
+        if (!wait(&B.s, x & 1, &B.dead)) return false;
         tc::fence_after();
-        if constexpr (PARTS == 3) add_columns(sum, tm + cDQ + nDQ * (x & 1) + lanes);  // (block x - 2's)
+        float a[2][32], g[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          tm_ld32(ts + 32 * c, a[c]);
+          tm_ld32(td + 32 * c, g[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          tm_wait_ld(a[c]);
+          tm_wait_ld(g[c]);
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mma::mbar_arrive(&B.taken);
+        const int left = lim - (t.j0 + x) * XB - 64 * half;
+        const bool cut = t.j0 + x >= clean;
+#pragma unroll
+        for (int c = 0; c < 2; c++) dq_grads(a[c], g[c], sc, l2, dl, cut, left - 32 * c);
+        if (x >= (TW ? 1 : 2)) {
+          if (!wait(&B.used[place(tw, x)], ((TW ? x : x / 2) - 1) & 1, &B.dead)) return false;
+          tc::fence_after();
+          if constexpr (PARTS == 3) add_columns(sum, tm + cDQ + nDQ * (x & 1) + lanes);  // (block x - 2's)
+        }
+        const uint32_t to = tm + cDS + nDS * place(tw, x) + 32 * half + lanes;
+        put_dq<PARTS, TW, XB>(a, to);
+        tm_wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mma::mbar_arrive(&B.ds);
       }
-      const uint32_t to = tm + cDS + nDS * (x & 1) + 32 * half + lanes;
-      put_parts<PARTS, 2>(a, to, to + 64);
-      tm_wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mma::mbar_arrive(&B.ds);
-    }
-    if (ok && n > 0) {
-      ok = wait(&B.used[(n - 1) & 1], ((n - 1) / 2) & 1, &B.dead);
+      if (n > 0 && !wait(&B.used[place(tw, n - 1)], (TW ? n - 1 : (n - 1) / 2) & 1, &B.dead)) return false;
       tc::fence_after();
-    }
+      return true;
+    };
+    const bool ok = with_parts<PARTS>(twice, pairs);
     if (ok) {
       const int w0 = r & ~31, c = 64 * half;
       unsigned char* buf = sm + half * HALF + w0 * 128;
