@@ -478,14 +478,21 @@ typedef struct kda_softmax_problem {
 
 /* Forward: q, o [B, T, Hq, D], k, v [B, Tk, Hkv, D] in dtype, lse [B, T, Hq]
  * fp32 (natural logarithm).  The workspace (kda_softmax_workspace_size bytes,
- * 256-byte aligned) holds the error word and the documents' tile tables and,
- * with save_for_backward = 1, the rows' sums and (bf16) what rounding o left; it
- * must then be passed to kda_softmax_bwd unmodified, with the same inputs and o.
- * Outputs must not overlap inputs.  Inputs are finite: weights of unseen keys
+ * 256-byte aligned) holds the error word, the documents' tile tables, the fp32
+ * results of tiles that are cut into pieces, with fp32 io the inputs' bf16 parts
+ * and, with save_for_backward = 1, the rows' sums and (bf16 io) what rounding o
+ * left; it must then be passed to kda_softmax_bwd unmodified, with the same inputs
+ * and o.  Outputs must not overlap inputs.  Inputs are finite: weights of unseen keys
  * are exact zeros of a matrix product, so an infinity or NaN in a value also
  * reaches its document's queries up to 255 before it, never another document's.
- * Precision: logits, maxima, sums and o are accumulated in fp32; with bf16 io the
- * weights (and, in the backward, their gradients) enter their products as bf16. */
+ * Precision: logits, maxima, sums and o are accumulated in fp32.  With bf16 io the
+ * weights (and, in the backward, their gradients) enter their products as bf16, in
+ * two parts (2^-16) in short documents of small problems.  With fp32 io every operand
+ * enters as three bf16 parts (2^-24 together); values whose bf16 rounding is
+ * finite (below 3.39e38).
+ * The results of a call depend on its inputs alone and repeat to the bit.  A batch
+ * with few long rows cuts their tiles into pieces and adds the pieces in order, so a
+ * document's last bits may differ from those that it has in another batch. */
 KDA_API size_t kda_softmax_workspace_size(const kda_softmax_problem* p, int for_backward);
 KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, const void* q, const void* k, const void* v,
                    void* o, float* lse, int save_for_backward, void* workspace, size_t workspace_bytes,
@@ -494,8 +501,9 @@ KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, const void* q, 
 /* Backward of sum(o * dO): dq [B, T, Hq, D], dk, dv [B, Tk, Hkv, D] (dtype),
  * from the forward's inputs, its o and its workspace (another one is refused by
  * the device: KDA_ERR_WORKSPACE from kda_device_status).  dk and dv are summed over
- * the heads of a group and over the queries by one CTA: a fixed order, no
- * atomics.  The workspace may be used by several backwards, one at a time. */
+ * the heads of a group and over the queries by one CTA, or by a few whose sums are
+ * added in order: no atomics.  The workspace may be used by several backwards, one
+ * at a time (pieces' results and dO's parts lie in it). */
 KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, const void* q, const void* k, const void* v,
                    const void* o, const void* dO, void* dq, void* dk, void* dv, void* workspace,
                    size_t workspace_bytes, cudaStream_t stream);

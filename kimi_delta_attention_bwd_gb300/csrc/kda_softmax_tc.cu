@@ -1,7 +1,7 @@
 // Softmax attention for bf16 io on the 5th-generation tensor cores (tcgen05, accumulators in tensor memory).
 //
 // Forward, per CTA: 256 queries of one head as two tiles of 128 over the keys in blocks of 128.  One warp loads
-// (TMA, a ring of key and value blocks), one thread issues the products, and per tile four warps, a thread a row,
+// (TMA, a ring of key and value blocks), one issues the products, and per tile four warps, a thread a row,
 // turn the block of logits S = q k^T into weights P = 2^(scale2 S - m): row maximum, exponentials, row sum.  P goes
 // back to tensor memory over S, as bf16, and is the product P v's operand there.  While one tile's weights are formed
 // the other's products run.  The maximum m that the exponents are taken against is raised (and o and the sum scaled
