@@ -339,14 +339,14 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   // packed batch they do, and short documents' second products are seen (300M step, 16384 rows: 218 against 226 us).
   P.few = (P.Nq < P.Nk ? P.Nq : P.Nk) <= 1024;
   const int parts = p->dtype == KDA_F32 ? 3 : 1;
-  for (int l = 0; l < 3; l++) P.tile[l] = parts == 3 && p->D == 128 && l > 0 ? F32_TILE : tc_tile(p->D, parts, l);
+  for (int l = 0; l < 3; l++) P.tile[l] = tc_tile(p->D, parts, l);
   // Cut tiles: where whole tiles would be fewer than four for each of 152 SMs, and some could have more than a few
   // blocks; a CTA's load is the average of one CTA per SM (half of that, at D = 64 with its two CTAs, cut tiles of the
   // packed 300M step whose join took what it gave; twice as many pieces for either head dim lost 3 to 10%).
   const int wave = 152;
   for (int l = 0; l < 3; l++) {
     const int H = l == 2 ? P.Hkv : P.Hq, other = l == 2 ? (P.rows ? P.T : P.Nq) : P.rows ? P.Tk : P.Nk;
-    P.xb[l] = parts == 3 && p->D == 128 && l > 0 ? F32_BLOCK : tc_block(p->D, parts, l);
+    P.xb[l] = tc_block(p->D, parts, l);
     if ((int64_t)max_tiles(P, l) * H <= 4 * wave && (int64_t)other * (l == 2 ? P.G : 1) > 1024 &&
         (!P.rows || P.B <= 1024)) {
       P.target[l] = wave;
@@ -404,7 +404,7 @@ size_t layout(SmxP& P, int D, int dtype, bool bwd, void* base) {
     P.pq = (bf16*)(w + take(nq));
     P.pk = (bf16*)(w + take(nk));
     P.pv = (bf16*)(w + take(nk));
-    if (bwd && D == 64) P.pg = (bf16*)(w + take(nq));
+    if (bwd) P.pg = (bf16*)(w + take(nq));
   }
   return o;
 }
@@ -510,15 +510,14 @@ extern "C" KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, cons
   if (e != cudaSuccess) return KDA_ERR_CUDA;
   if (p->dtype == KDA_BF16) {
     e = launch_tc_bwd(P, p->D, 1, q, k, v, dO, dq, dk, dv, st);
-  } else if (p->D == 64) {
+  } else {
     const float* x[1] = {(const float*)dO};
     bf16* const parts[1] = {P.pg};
     const int64_t n[1] = {(int64_t)P.Nq * P.Hq * p->D};
     e = launch_split(1, x, parts, n, st);
-    if (e == cudaSuccess) e = launch_tc_bwd(P, 64, 3, P.pq, P.pk, P.pv, P.pg, dq, dk, dv, st);
-  } else {
-    e = launch_f32_bwd(P, (const float*)q, (const float*)k, (const float*)v, (const float*)dO, (float*)dq, (float*)dk,
-                       (float*)dv, st);
+    if (e == cudaSuccess)
+      e = p->D == 64 ? launch_tc_bwd(P, 64, 3, P.pq, P.pk, P.pv, P.pg, dq, dk, dv, st)
+                     : launch_f32_bwd(P, (float*)dq, (float*)dk, (float*)dv, st);
   }
   if (e == cudaSuccess && (P.target[1] || P.target[2])) {
     if (p->dtype == KDA_F32)

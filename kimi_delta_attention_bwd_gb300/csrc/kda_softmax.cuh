@@ -95,8 +95,10 @@ __device__ __forceinline__ bool saved(const SmxP& P) {
 }
 
 // Tensor-core kernels.  parts = 1: bf16 io; 3: fp32 io, its inputs as three bf16 arrays one behind the other
-// (launch_split), the backward at D = 64 only.  Rows of list l's tiles: tc_tile.
-constexpr int tc_block(int D, int parts, int l) { return D == 64 || (l == 0 && parts == 3) ? 64 : 128; }  // their blocks
+// (launch_split); their backward at D = 128 is launch_f32_bwd.  Rows of list l's tiles: tc_tile, of their blocks: tc_block.
+constexpr int tc_block(int D, int parts, int l) {
+  return D == 64 ? 64 : parts == 3 ? (l == 0 ? 64 : 32) : 128;
+}
 constexpr int tc_tile(int D, int parts, int l) { return l > 0 || (parts == 3 && D == 128) ? 128 : 256; }
 cudaError_t launch_tc_fwd(const SmxP& P, int D, int parts, const void* q, const void* k, const void* v, void* o,
                           float* lse, cudaStream_t st);
@@ -105,10 +107,7 @@ cudaError_t launch_tc_bwd(const SmxP& P, int D, int parts, const void* q, const 
 // Up to three fp32 arrays (their sizes multiples of 8) into their parts.
 cudaError_t launch_split(int n, const float* const* x, bf16* const* parts, const int64_t* values, cudaStream_t st);
 
-// The backward of fp32 io at D = 128, on the fp32 pipe: tiles of 64 rows.
-constexpr int F32_TILE = 64, F32_BLOCK = 64;
-cudaError_t launch_f32_bwd(const SmxP& P, const float* q, const float* k, const float* v, const float* dO, float* dq,
-                           float* dk, float* dv, cudaStream_t st);
+cudaError_t launch_f32_bwd(const SmxP& P, float* dq, float* dk, float* dv, cudaStream_t st);  // (of the parts in P)
 
 // Upper bound on the entries of list l: its tiles, and the pieces of those that are cut.
 inline int max_tiles(const SmxP& P, int l) {

@@ -1,311 +1,491 @@
-// Softmax attention, the backward of fp32 io at D = 128, on the fp32 pipe (the other
-// fp32 passes run on the tensor cores in three bf16 parts; here both own blocks in three
-// parts would fill shared memory).  Per document, query head h and its key head h / G:
+// Softmax attention, the backward of fp32 io at D = 128 on the 5th-generation tensor cores, every operand as three bf16
+// parts (the other passes: kda_softmax_tc.cu).  Per document, query head h and its key head h / G:
 //   p_ij = exp(scale q_i k_j - lse_i),  dv_j = sum_i p_ij dO_i
 //   ds_ij = p_ij (dO_i v_j - delta_i),  delta_i = o_i dO_i
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
-// Tiles of 16 R own rows by 64 of the other side, 256 threads with R x 4 pairs each;
-// operands of the pair products lie transposed in shared memory ([d][row]) so that a
-// thread's rows are one 16-byte load; the next block's values are on their way to
-// registers meanwhile.  dk and dv of a key tile are summed by one CTA over the queries
-// of its whole head group, dq by one CTA over the keys: no atomics, a fixed order.
-#include "kda_softmax.cuh"
+// Both own blocks of 128 rows would fill shared memory (96 KB each): one lies there, the other in tensor memory (192 of
+// its 512 columns), where a product can take its first operand from too.  That leaves room for a ring of blocks of 32
+// rows of the other side, and 128 columns for one result: dv and dk of a block take turns in it, and their sums over the
+// blocks are in registers, where they are rounded (the tensor pipe cuts its sums off).
+// Eight warps, a thread a row and half of a block's pairs, of a result's columns, and of an own row to tensor memory.
+// Bound by the tensor pipe: six products a product, and the first operand's reads (128 x 16 values for 32 columns: 32
+// cycles, so 16 of arithmetic).  4 x 1001 rows of 8 heads, every pair seen: 559 us with the forward (129); on the fp32
+// pipe, 64 x 64 pairs a CTA, 2105.  (16 warps would halve a thread's 128 sums of dk and dv and have too few registers for
+// them; eight spill 220 bytes, a few loads a block.)
+#include "kda_softmax_tc.cuh"
 
 namespace kda {
 namespace smx {
 namespace {
 
-constexpr int TM = 64, NT = 256;  // rows of the other side's blocks; threads
+constexpr int D = 128, XB = 32, EW = 8;                         // rows of the other side's blocks; warps of the pairs
+constexpr int OWN = BLK * D * 2 * 3, BYTES = XB * D * 2 * 3;    // a block of three parts, of either side
+constexpr int NA = 3, NB = 2, BLOCKS = OWN + NA * BYTES + NB * BYTES;
+constexpr int PART = XB / 2;                                    // columns of one part of a block's pairs as an operand
+constexpr uint32_t ID_S = idesc(BLK, XB, false), ID_O = idesc(BLK, D, true);
 
-__device__ __forceinline__ void ld4(const float* p, float* v) {
-  const float4 f = *reinterpret_cast<const float4*>(p);
-  v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-}
-__device__ __forceinline__ void st4(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-
-// A block of ROWS rows of x (ld elements apart) on its way to shared memory: rows from n on are zeros, so that a
-// neighbour's values never enter a product.
-template <int D, int ROWS>
-struct Block {
-  static constexpr int N = ROWS * D / 4 / NT;
-  float4 v[N];
-  __device__ __forceinline__ void load(const float* x, size_t ld, int n) {
-#pragma unroll
-    for (int k = 0; k < N; k++) {
-      const int i = threadIdx.x + k * NT, r = i % ROWS, d = i / ROWS * 4;
-      v[k] = r < n ? *reinterpret_cast<const float4*>(x + r * ld + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  }
-  // to tr[d][row], and to pl[row][d], where not null
-  __device__ __forceinline__ void store(float* tr, float* pl) const {
-#pragma unroll
-    for (int k = 0; k < N; k++) {
-      const int i = threadIdx.x + k * NT, r = i % ROWS, d = i / ROWS * 4;
-      if (tr) {
-        tr[d * ROWS + r] = v[k].x;
-        tr[(d + 1) * ROWS + r] = v[k].y;
-        tr[(d + 2) * ROWS + r] = v[k].z;
-        tr[(d + 3) * ROWS + r] = v[k].w;
-      }
-      if (pl) *reinterpret_cast<float4*>(pl + r * D + d) = v[k];
-    }
-  }
+struct Bars {
+  float stat[NA][2][XB];  // minus lse2 and minus delta of ring A's queries
+  uint64_t own, loaded, fullA[NA], emptyA[NA], fullB[NB], emptyB[NB], fullS[NA], s, dp, p, ds, taken, first, second, drain;
+  uint32_t tmem;
+  int dead;
 };
+constexpr int SMEM = BLOCKS + (int)sizeof(Bars);
+static_assert(SMEM <= 232448, "shared memory of a CTA");
 
-// c[i][j] = sum_d a[d][r0 + i] b[d][c0 + j]: a has 16 R rows, b TM
-template <int D, int R>
-__device__ __forceinline__ void pairs(const float* a, const float* b, int r0, int c0, float (&c)[R][4]) {
+// An own row's half (64 values, three parts `stride` values apart) to tensor memory; zeros behind the document's end.
+__device__ __forceinline__ void load_own(uint32_t to, const bf16* row, size_t stride, bool in) {
 #pragma unroll
-  for (int i = 0; i < R; i++)
+  for (int y = 0; y < 3; y++)
 #pragma unroll
-    for (int j = 0; j < 4; j++) c[i][j] = 0.f;
-#pragma unroll 1
-  for (int d0 = 0; d0 < D; d0 += 32) {  // (sums of 32, then their sum: a third of one long sum's rounding)
-    float u[R][4] = {};
-#pragma unroll 8
-    for (int d = d0; d < d0 + 32; d++) {
-      float x[R], y[4];
+    for (int c = 0; c < 2; c++) {
+      uint32_t w[16];
 #pragma unroll
-      for (int i = 0; i < R; i += 4) ld4(a + d * 16 * R + r0 + i, x + i);
-      ld4(b + d * TM + c0, y);
-#pragma unroll
-      for (int i = 0; i < R; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) u[i][j] = fmaf(x[i], y[j], u[i][j]);
+      for (int e = 0; e < 4; e++) {
+        const uint4 u = in ? *reinterpret_cast<const uint4*>(row + y * stride + 32 * c + 8 * e) : make_uint4(0, 0, 0, 0);
+        w[4 * e] = u.x, w[4 * e + 1] = u.y, w[4 * e + 2] = u.z, w[4 * e + 3] = u.w;
+      }
+      tm_st16(to + D / 2 * y + 16 * c, w);
     }
+  tm_wait_st();
+}
+// 16 pairs of a row as an operand's three parts
+__device__ __forceinline__ void put(float (&v)[16], uint32_t to) {
 #pragma unroll
-    for (int i = 0; i < R; i++)
+  for (int y = 0; y < 3; y++) {
+    uint32_t w[8];
+    next_part(v, w);
+    tm_st8(to + PART * y, w);
+  }
+  tm_wait_st();
+}
+// d = A B^T, A's three parts in tensor memory, B a block, K-major
+__device__ __forceinline__ void prod_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t me) {
+  using Q = Prod<3>;
 #pragma unroll
-      for (int j = 0; j < 4; j++) c[i][j] += u[i][j];
+  for (int i = 0; i < Q::N; i++)
+#pragma unroll
+    for (int s = 0; s < D / 16; s++)
+      mma_ts(d, a + D / 2 * Q::a(i) + 8 * s, desc_k<XB>(b + Q::b(i) * (XB * D * 2), s), ID_S, i > 0 || s > 0, me);
+}
+// d = pairs B over a block's rows
+__device__ __forceinline__ void apply(uint32_t d, uint32_t a, uint32_t b, uint32_t me) {
+  using Q = Prod<3>;
+#pragma unroll
+  for (int i = 0; i < Q::N; i++)
+#pragma unroll
+    for (int s = 0; s < XB / 16; s++)
+      mma_ts(d, a + PART * Q::a(i) + 8 * s, desc_mn<XB>(b + Q::b(i) * (XB * D * 2), s), ID_O, i > 0 || s > 0, me);
+}
+__device__ __forceinline__ void init(Bars& B) {
+  mma::mbar_init(&B.own, 1);
+  mma::mbar_init(&B.loaded, EW);
+  for (int i = 0; i < NA; i++) {
+    mma::mbar_init(&B.fullA[i], 1);
+    mma::mbar_init(&B.emptyA[i], 1);
+    mma::mbar_init(&B.fullS[i], 1);
+  }
+  for (int i = 0; i < NB; i++) {
+    mma::mbar_init(&B.fullB[i], 1);
+    mma::mbar_init(&B.emptyB[i], 1);
+  }
+  mma::mbar_init(&B.s, 1);
+  mma::mbar_init(&B.dp, 1);
+  mma::mbar_init(&B.p, EW);
+  mma::mbar_init(&B.ds, EW);
+  mma::mbar_init(&B.taken, EW);
+  mma::mbar_init(&B.first, 1);
+  mma::mbar_init(&B.second, 1);
+  mma::mbar_init(&B.drain, 1);
+  B.dead = 0;
+  mma::mbar_init_fence();
+}
+// (16 columns at a time: 128 sums a thread of dk and dv leave few registers)
+__device__ __forceinline__ void add(float (&sum)[64], uint32_t tm) {
+#pragma unroll
+  for (int c = 0; c < 64; c += 16) {
+    float v[16];
+    tm_ld16(tm + c, v);
+    tm_wait_ld(v);
+#pragma unroll
+    for (int e = 0; e < 16; e++) sum[c + e] += v[e];
   }
 }
-// c[i][64 m + 4 tx + e] += sum_n w[n][r0 + i] x[n][64 m + 4 tx + e]: w's rows are PP apart
-template <int R>
-constexpr int PP = 16 * R + 4;
-template <int D, int R>
-__device__ __forceinline__ void apply(const float* w, const float* x, int r0, int tx, float (&c)[R][D / 16]) {
-#pragma unroll 4
-  for (int n = 0; n < TM; n++) {
-    float a[R];
-#pragma unroll
-    for (int i = 0; i < R; i += 4) ld4(w + n * PP<R> + r0 + i, a + i);
-#pragma unroll
-    for (int m = 0; m < D / 64; m++) {
-      float y[4];
-      ld4(x + n * D + 64 * m + 4 * tx, y);
-#pragma unroll
-      for (int i = 0; i < R; i++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) c[i][4 * m + e] = fmaf(a[i], y[e], c[i][4 * m + e]);
-    }
-  }
-}
-template <int R>
-__device__ __forceinline__ void put_column(float* dst, const float (&v)[R]) {
-#pragma unroll
-  for (int i = 0; i < R; i += 4) st4(dst + i, v + i);
+// This warp's part of a step is in tensor memory, or taken from it.
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  tc::fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mma::mbar_arrive(bar);
 }
 
-// dk and dv of 16 R keys of one key head.  Threads: keys R ty .., queries 4 tx ..
-template <int D, int R>
-__global__ void __launch_bounds__(NT) smx_dkv_kernel(SmxP P, const float* __restrict__ q, const float* __restrict__ k,
-                                                    const float* __restrict__ v, const float* __restrict__ dO,
-                                                    float* __restrict__ dk, float* __restrict__ dv) {
-  constexpr int OWN = 16 * R;
-  extern __shared__ __align__(16) float sm[];
-  float *tK = sm, *tV = tK + D * OWN, *tQ = tV + D * OWN, *tG = tQ + D * TM, *sQ = tG + D * TM, *sG = sQ + D * TM;
-  float *sP = sG + D * TM, *sl = sP + TM * PP<R>, *sd = sl + TM;  // (the weights, then their gradients)
+// dk and dv of 128 keys of one key head, over the blocks of its group's queries; the pairs transposed, a key a lane.
+// Products in the order S'(x + 1), dv(x), dP'(x + 1), dk(x): while two run, the weights and gradients of the others form.
+__global__ void __launch_bounds__(EW * 32 + 64, 1)
+smx_f32_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mg, float* __restrict__ dk, float* __restrict__ dv) {
+  constexpr uint32_t cS = 0, cDP = XB, cP = 2 * XB, cDS = cP + 3 * PART, cO = cDS + 3 * PART, cV = cO + D;
+  static_assert(cV + 3 * (D / 2) <= 512, "tensor memory");
+  extern __shared__ __align__(1024) unsigned char sm[];
+  Bars& B = *reinterpret_cast<Bars*>(sm + BLOCKS);
+  if (mma::smem_u32(sm) & 1023) {  // (dynamic shared memory alone starts on such a boundary)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *P.err = KDA_ERR_DEVICE;
+    return;
+  }
+  unsigned char *ringA = sm + OWN, *ringB = ringA + NA * BYTES;  // q, dO
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (warp == EW) tc::tmem_alloc(&B.tmem, 512);
+  if (threadIdx.x == 32 * (EW + 1)) {
+    prefetch_map(&mq);
+    prefetch_map(&mk);
+    prefetch_map(&mg);
+  }
+  if (threadIdx.x == 0) init(B);
   pdl_wait();
   pdl_release();  // dq's CTAs may follow this grid's last ones: they wait for it at their end only
-  if (!saved(P)) return;
-  const int hk = blockIdx.x % P.Hkv, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   Tile t;
-  if (!tile_of(P, 2, blockIdx.x / P.Hkv, true, t)) return;
-  const int j0 = t.t * OWN, nk = min(OWN, t.Lk - j0);
-  {
-    const size_t at = ((size_t)(t.k0 + j0) * P.Hkv + hk) * D;
-    Block<D, OWN> b;
-    b.load(k + at, (size_t)P.Hkv * D, nk);
-    b.store(tK, nullptr);
-    b.load(v + at, (size_t)P.Hkv * D, nk);
-    b.store(tV, nullptr);
+  const int hk = blockIdx.x % P.Hkv;
+  const bool live = saved(P) && tile_of(P, 2, blockIdx.x / P.Hkv, true, t);
+  int j0 = 0, nk = 0, first = 0, per = 0;  // first query block, blocks a head
+  if (live) {
+    j0 = t.t * BLK;
+    nk = min(BLK, t.Lk - j0);
+    first = first_query(P.causal, j0, t.Lq, t.Lk) / XB;
+    per = max(0, (t.Lq + XB - 1) / XB - first);
   }
-  float ak[R][D / 16] = {}, av[R][D / 16] = {};
-  const int first = first_query(P.causal, j0, t.Lq, t.Lk) / TM, per = max(0, (t.Lq + TM - 1) / TM - first);
-  const size_t ld = (size_t)P.Hq * D;
-  Block<D, TM> bq, bg;
-  float nl = 0.f, nd = 0.f;
-  auto load = [&](int x) {  // block x of the group's heads' queries
-    const int y = t.j0 + x, h = hk * P.G + y / per, i0 = (first + y % per) * TM;
-    const size_t at = ((size_t)(t.q0 + i0) * P.Hq + h) * D;
-    bq.load(q + at, ld, t.Lq - i0);
-    bg.load(dO + at, ld, t.Lq - i0);
-    if (threadIdx.x < TM) {
-      const bool in = i0 + (int)threadIdx.x < t.Lq;
-      const size_t r = (size_t)h * P.Nq + t.q0 + i0 + threadIdx.x;
-      nl = in ? P.lse2[r] : 0.f;
-      nd = in ? P.delta[r] : 0.f;
+  const int n = live ? min(per * P.G, t.j1) - t.j0 : 0;
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = tm_base<512>(B.tmem);
+
+  if (warp == EW + 1) {  // copies, and the queries' row sums
+    if (lane == 0 && n > 0) {
+      mma::mbar_expect_tx(&B.own, OWN);
+      load_block<D, BLK, 3>(sm, &mk, hk, t.k0 + j0, P.Nk, &B.own);
     }
-  };
-  const int n = min(per * P.G, t.j1) - t.j0;
-  if (n > 0) load(0);
-  for (int x = 0; x < n; x++) {
-    const int i0 = (first + (t.j0 + x) % per) * TM;
-    __syncthreads();
-    bq.store(tQ, sQ);
-    bg.store(tG, sG);
-    if (threadIdx.x < TM) {
-      sl[threadIdx.x] = nl;
-      sd[threadIdx.x] = nd;
-    }
-    __syncthreads();
-    if (x + 1 < n) load(x + 1);
-    float s[R][4], dp[R][4];
-    pairs<D, R>(tK, tQ, R * ty, 4 * tx, s);
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int i = i0 + 4 * tx + j, lim = i < t.Lq ? keys_of(P.causal, i, t.Lq, t.Lk) : 0;
-      float p[R];
-#pragma unroll
-      for (int e = 0; e < R; e++) {
-        p[e] = j0 + R * ty + e < lim ? ex2(fmaf(s[e][j], P.scale2, -sl[4 * tx + j])) : 0.f;
-        s[e][j] = p[e];
+    __syncwarp();
+    for (int x = 0; x < n; x++) {
+      const int sa = x % NA, sb = x % NB, y = t.j0 + x, h = hk * P.G + y / per, i0 = (first + y % per) * XB, row = t.q0 + i0;
+      if (x >= NA && !wait(&B.emptyA[sa], (x / NA - 1) & 1, &B.dead)) break;
+      if (lane == 0) {
+        mma::mbar_expect_tx(&B.fullA[sa], BYTES);
+        load_block<D, XB, 3>(ringA + sa * BYTES, &mq, h, row, P.Nq, &B.fullA[sa]);
       }
-      put_column<R>(sP + (4 * tx + j) * PP<R> + R * ty, p);
+      const bool in = i0 + lane < t.Lq;
+      const size_t at = (size_t)h * P.Nq + row + lane;
+      B.stat[sa][0][lane] = in ? -P.lse2[at] : 0.f;
+      B.stat[sa][1][lane] = in ? -P.delta[at] : 0.f;
+      __syncwarp();
+      if (lane == 0) mma::mbar_arrive(&B.fullS[sa]);
+      if (x >= NB && !wait(&B.emptyB[sb], (x / NB - 1) & 1, &B.dead)) break;
+      if (lane == 0) {
+        mma::mbar_expect_tx(&B.fullB[sb], BYTES);
+        load_block<D, XB, 3>(ringB + sb * BYTES, &mg, h, row, P.Nq, &B.fullB[sb]);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-    apply<D, R>(sP, sG, R * ty, tx, av);
-    pairs<D, R>(tV, tG, R * ty, 4 * tx, dp);
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      float d[R];
-#pragma unroll
-      for (int e = 0; e < R; e++) d[e] = s[e][j] == 0.f ? 0.f : s[e][j] * (dp[e][j] - sd[4 * tx + j]);
-      put_column<R>(sP + (4 * tx + j) * PP<R> + R * ty, d);
+    // (a wait gives up after a second: by then every copy under way has landed)
+  } else if (warp == EW) {  // products
+    const uint32_t k0 = mma::smem_u32(sm), a0 = mma::smem_u32(ringA), b0 = mma::smem_u32(ringB);
+    const uint32_t me = elect();
+    // block x of queries (of their dO) has landed; rows behind its document's last are zeros
+    auto ready = [&](int x, unsigned char* block, uint64_t* full, int phase) -> bool {
+      const int left = t.Lq - (first + (t.j0 + x) % per) * XB;
+      if (!wait(full, phase & 1, &B.dead)) return false;
+      if (left < XB) zero_rows<D, XB, 3>(block, left);
+      return true;
+    };
+    auto readyA = [&](int x) { return ready(x, ringA + x % NA * BYTES, &B.fullA[x % NA], x / NA); };
+    auto readyB = [&](int x) { return ready(x, ringB + x % NB * BYTES, &B.fullB[x % NB], x / NB); };
+    auto logits = [&](int x) {
+      prod_ss<D, 3, BLK, XB>(tm + cS, k0, a0 + x % NA * BYTES, ID_S, me);
+      commit(&B.s, me);
+    };
+    auto grads = [&](int x) {
+      prod_ts(tm + cDP, tm + cV, b0 + x % NB * BYTES, me);
+      commit(&B.dp, me);
+    };
+    auto run = [&]() -> bool {
+      if (!wait(&B.own, 0, &B.dead) || !readyA(0)) return false;
+      logits(0);
+      if (!readyB(0) || !wait(&B.loaded, 0, &B.dead)) return false;
+      tc::fence_after();
+      grads(0);
+      for (int x = 0; x < n; x++) {
+        const bool more = x + 1 < n;
+        if (!wait(&B.p, x & 1, &B.dead)) return false;
+        tc::fence_after();
+        if (more) {
+          if (!readyA(x + 1)) return false;
+          logits(x + 1);
+        }
+        if (!wait(&B.ds, x & 1, &B.dead)) return false;  // (and dk of block x - 1 is taken)
+        tc::fence_after();
+        apply(tm + cO, tm + cP, b0 + x % NB * BYTES, me);
+        commit(&B.first, me);
+        commit(&B.emptyB[x % NB], me);
+        if (more) {
+          if (!readyB(x + 1)) return false;
+          grads(x + 1);
+        }
+        if (!wait(&B.taken, x & 1, &B.dead)) return false;
+        tc::fence_after();
+        apply(tm + cO, tm + cDS, a0 + x % NA * BYTES, me);
+        commit(&B.second, me);
+        commit(&B.emptyA[x % NA], me);
+      }
+      return true;
+    };
+    if (n > 0 && !run()) {
+      commit(&B.drain, me);
+      for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
     }
-    __syncwarp();
-    apply<D, R>(sP, sQ, R * ty, tx, ak);
-    __syncwarp();
+  } else if (warp < EW && live) {
+    const int half = warp / 4, r = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t out = tm + cO + 64 * half + lanes;
+    const int fq = first_query(P.causal, j0 + r, t.Lq, t.Lk), fq_last = first_query(P.causal, j0 + nk - 1, t.Lq, t.Lk);
+    const uint64_t sc = two(P.scale2, P.scale2);
+    float sv[64] = {}, sk[64] = {};  // dv and dk, columns 64 half ..
+    load_own(tm + cV + 32 * half + lanes, P.pv + ((size_t)(t.k0 + j0 + r) * P.Hkv + hk) * D + 64 * half,
+             (size_t)P.Nk * P.Hkv * D, r < nk);
+    arrive(&B.loaded);
+    bool ok = true;
+    for (int x = 0; x < n; x++) {
+      const int s = x % NA, i0 = (first + (t.j0 + x) % per) * XB;
+      const float *l2 = B.stat[s][0] + 16 * half, *dl = B.stat[s][1] + 16 * half;
+      const bool cut = i0 < fq_last || i0 + XB > t.Lq;
+      const int lo = fq - i0 - 16 * half, hi = t.Lq - i0 - 16 * half;
+      float a[16], g[16];
+      ok = wait(&B.fullS[s], (x / NA) & 1, &B.dead) && wait(&B.s, x & 1, &B.dead);
+      if (!ok) break;
+      tc::fence_after();
+      tm_ld16(tm + cS + 16 * half + lanes, a);
+      tm_wait_ld(a);
+      bwd_weights(a, l2, sc, cut, lo, hi);
+#pragma unroll
+      for (int e = 0; e < 16; e++) g[e] = a[e];
+      put(g, tm + cP + 8 * half + lanes);
+      arrive(&B.p);
+      ok = wait(&B.dp, x & 1, &B.dead);
+      if (!ok) break;
+      tc::fence_after();
+      tm_ld16(tm + cDP + 16 * half + lanes, g);
+      tm_wait_ld(g);
+      bwd_grads(a, g, dl, cut, lo, hi);
+      if (x > 0) {
+        ok = wait(&B.second, (x - 1) & 1, &B.dead);
+        if (!ok) break;
+        tc::fence_after();
+        add(sk, out);
+      }
+      put(a, tm + cDS + 8 * half + lanes);
+      arrive(&B.ds);
+      ok = wait(&B.first, x & 1, &B.dead);
+      if (!ok) break;
+      tc::fence_after();
+      add(sv, out);
+      arrive(&B.taken);
+    }
+    if (ok && n > 0) {
+      ok = wait(&B.second, (n - 1) & 1, &B.dead);
+      tc::fence_after();
+      if (ok) add(sk, out);
+    }
+    if (ok) {
+      const int w0 = r & ~31, c = 64 * half;  // (the CTA's own block is no longer read)
+      const bool whole = t.piece < 0;
+      const size_t at = ((size_t)(t.k0 + j0 + w0) * P.Hkv + hk) * D + c, ld = whole ? (size_t)P.Hkv * D : D;
+      const size_t pa = (((size_t)t.piece * P.Hkv + hk) * BLK + w0) * D + c;  // (a piece's place)
+      const size_t more = (size_t)P.pieces[2] * P.Hkv * BLK * D;
+      unsigned char* buf = sm + half * HALF + w0 * 128;
+      store_sums(buf, sv, 1.0f, whole ? dv + at : P.po[2] + more + pa, ld, nk - w0);
+      store_sums(buf, sk, whole ? P.scale : 1.0f, whole ? dk + at : P.po[2] + pa, ld, nk - w0);
+    }
+    tc::fence_before();
   }
-#pragma unroll
-  for (int i = 0; i < R; i++) {
-    const int r = R * ty + i;
-    if (r >= nk) continue;
-    const bool whole = t.piece < 0;
-    const size_t row = ((size_t)(t.k0 + j0 + r) * P.Hkv + hk) * D, pa = (((size_t)t.piece * P.Hkv + hk) * OWN + r) * D;
-    float* ok = whole ? dk + row : P.po[2] + pa;
-    float* ov = whole ? dv + row : P.po[2] + (size_t)P.pieces[2] * P.Hkv * OWN * D + pa;
-    const float f = whole ? P.scale : 1.0f;
-#pragma unroll
-    for (int c = 0; c < D / 64; c++) {
-      const float x[4] = {ak[i][4 * c] * f, ak[i][4 * c + 1] * f, ak[i][4 * c + 2] * f, ak[i][4 * c + 3] * f};
-      const float y[4] = {av[i][4 * c], av[i][4 * c + 1], av[i][4 * c + 2], av[i][4 * c + 3]};
-      st4(ok + 64 * c + 4 * tx, x);
-      st4(ov + 64 * c + 4 * tx, y);
-    }
+  __syncthreads();
+  if (threadIdx.x == 0 && B.dead) *P.err = KDA_ERR_DEVICE;
+  if (warp == EW) {
+    tc::fence_after();
+    tc::tmem_dealloc(tm, 512);
   }
 }
 
-// dq of 16 R queries of one head.  Threads: queries R ty .., keys 4 tx ..
-template <int D, int R>
-__global__ void __launch_bounds__(NT) smx_dq_kernel(SmxP P, const float* __restrict__ q, const float* __restrict__ k,
-                                                   const float* __restrict__ v, const float* __restrict__ dO,
-                                                   float* __restrict__ dq) {
-  constexpr int OWN = 16 * R;
-  extern __shared__ __align__(16) float sm[];
-  float *tQ = sm, *tG = tQ + D * OWN, *tK = tG + D * OWN, *tV = tK + D * TM, *sK = tV + D * TM, *sD = sK + D * TM;
+// dq of 128 queries of one head, over the blocks of keys.  S and dP are taken to registers at once, so that the next
+// block's products run while dS is formed and the block before's dq is added.
+__global__ void __launch_bounds__(EW * 32 + 64, 1)
+smx_f32_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, float* __restrict__ dq) {
+  constexpr uint32_t cS = 0, cDP = XB, cDS = 2 * XB, cDQ = cDS + 3 * PART, cG = cDQ + D;
+  static_assert(cG + 3 * (D / 2) <= 512, "tensor memory");
+  extern __shared__ __align__(1024) unsigned char sm[];
+  Bars& B = *reinterpret_cast<Bars*>(sm + BLOCKS);
   struct Last {  // what follows this grid follows dk and dv too
     __device__ ~Last() { pdl_wait(); }
   } last;
-  if (!saved(P)) return;
-  const int h = blockIdx.x % P.Hq, hk = h / P.G, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  if (mma::smem_u32(sm) & 1023) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *P.err = KDA_ERR_DEVICE;
+    return;
+  }
+  unsigned char *ringA = sm + OWN, *ringB = ringA + NA * BYTES;  // k, v
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (warp == EW) tc::tmem_alloc(&B.tmem, 512);
+  if (threadIdx.x == 32 * (EW + 1)) {
+    prefetch_map(&mq);
+    prefetch_map(&mk);
+    prefetch_map(&mv);
+  }
+  if (threadIdx.x == 0) init(B);
   Tile t;
-  if (!tile_of(P, 1, blockIdx.x / P.Hq, false, t)) return;
-  const int i0 = t.t * OWN, nq = min(OWN, t.Lq - i0);
-  const size_t qa = ((size_t)(t.q0 + i0) * P.Hq + h) * D;
-  {
-    Block<D, OWN> b;
-    b.load(q + qa, (size_t)P.Hq * D, nq);
-    b.store(tQ, nullptr);
-    b.load(dO + qa, (size_t)P.Hq * D, nq);
-    b.store(tG, nullptr);
+  const int h = blockIdx.x % P.Hq, hk = h / P.G;
+  const bool live = saved(P) && tile_of(P, 1, blockIdx.x / P.Hq, false, t);
+  int i0 = 0, nq = 0, n = 0, clean = 0;
+  if (live) {
+    i0 = t.t * BLK;
+    nq = min(BLK, t.Lq - i0);
+    n = min((keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk) + XB - 1) / XB, t.j1) - t.j0;
+    clean = keys_of(P.causal, i0, t.Lq, t.Lk) / XB;
   }
-  float acc[R][D / 16] = {}, l2[R], del[R];
-  int lim[R];
-#pragma unroll
-  for (int i = 0; i < R; i++) {
-    const int r = R * ty + i;
-    const size_t at = (size_t)h * P.Nq + t.q0 + i0 + r;
-    l2[i] = r < nq ? P.lse2[at] : 0.f;
-    del[i] = r < nq ? P.delta[at] : 0.f;
-    lim[i] = r < nq ? keys_of(P.causal, i0 + r, t.Lq, t.Lk) : 0;
-  }
-  const int nk = (int)min((int64_t)keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk), (int64_t)t.j1 * TM);
-  const size_t ld = (size_t)P.Hkv * D, at = ((size_t)t.k0 * P.Hkv + hk) * D;
-  Block<D, TM> bk, bv;
-  const int first = t.j0 * TM;
-  if (first < nk) {
-    bk.load(k + at + first * ld, ld, t.Lk - first);
-    bv.load(v + at + first * ld, ld, t.Lk - first);
-  }
-  for (int j0 = first; j0 < nk; j0 += TM) {
-    __syncthreads();
-    bk.store(tK, sK);
-    bv.store(tV, nullptr);
-    __syncthreads();
-    if (j0 + TM < nk) {
-      bk.load(k + at + (j0 + TM) * ld, ld, t.Lk - j0 - TM);
-      bv.load(v + at + (j0 + TM) * ld, ld, t.Lk - j0 - TM);
-    }
-    float s[R][4], dp[R][4];
-    pairs<D, R>(tQ, tK, R * ty, 4 * tx, s);
-    pairs<D, R>(tG, tV, R * ty, 4 * tx, dp);
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      float d[R];
-#pragma unroll
-      for (int i = 0; i < R; i++)
-        d[i] = j0 + 4 * tx + j < lim[i] ? ex2(fmaf(s[i][j], P.scale2, -l2[i])) * (dp[i][j] - del[i]) : 0.f;
-      put_column<R>(sD + (4 * tx + j) * PP<R> + R * ty, d);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = tm_base<512>(B.tmem);
+
+  if (warp == EW + 1) {  // copies
+    if (lane == 0 && n > 0) {
+      mma::mbar_expect_tx(&B.own, OWN);
+      load_block<D, BLK, 3>(sm, &mq, h, t.q0 + i0, P.Nq, &B.own);
     }
     __syncwarp();
-    apply<D, R>(sD, sK, R * ty, tx, acc);
-  }
-#pragma unroll
-  for (int i = 0; i < R; i++) {
-    const int r = R * ty + i;
-    if (r >= nq) continue;
-    const bool whole = t.piece < 0;
-    float* out = whole ? dq + qa + (size_t)r * P.Hq * D : P.po[1] + (((size_t)t.piece * P.Hq + h) * OWN + r) * D;
-    const float f = whole ? P.scale : 1.0f;
-#pragma unroll
-    for (int c = 0; c < D / 64; c++) {
-      const float x[4] = {acc[i][4 * c] * f, acc[i][4 * c + 1] * f, acc[i][4 * c + 2] * f, acc[i][4 * c + 3] * f};
-      st4(out + 64 * c + 4 * tx, x);
+    for (int x = 0; x < n; x++) {
+      const int sa = x % NA, sb = x % NB, row = t.k0 + (t.j0 + x) * XB;
+      if (x >= NA && !wait(&B.emptyA[sa], (x / NA - 1) & 1, &B.dead)) break;
+      if (lane == 0) {
+        mma::mbar_expect_tx(&B.fullA[sa], BYTES);
+        load_block<D, XB, 3>(ringA + sa * BYTES, &mk, hk, row, P.Nk, &B.fullA[sa]);
+      }
+      __syncwarp();
+      if (x >= NB && !wait(&B.emptyB[sb], (x / NB - 1) & 1, &B.dead)) break;
+      if (lane == 0) {
+        mma::mbar_expect_tx(&B.fullB[sb], BYTES);
+        load_block<D, XB, 3>(ringB + sb * BYTES, &mv, hk, row, P.Nk, &B.fullB[sb]);
+      }
+      __syncwarp();
     }
+  } else if (warp == EW) {  // products
+    const uint32_t q0 = mma::smem_u32(sm), a0 = mma::smem_u32(ringA), b0 = mma::smem_u32(ringB);
+    const uint32_t me = elect();
+    auto pairs = [&](int x) {
+      prod_ss<D, 3, BLK, XB>(tm + cS, q0, a0 + x % NA * BYTES, ID_S, me);
+      prod_ts(tm + cDP, tm + cG, b0 + x % NB * BYTES, me);
+      commit(&B.s, me);
+      commit(&B.emptyB[x % NB], me);
+    };
+    auto ready = [&](int x) -> bool {
+      const int left = t.Lk - (t.j0 + x) * XB;
+      if (!wait(&B.fullA[x % NA], (x / NA) & 1, &B.dead)) return false;
+      if (left < XB) zero_rows<D, XB, 3>(ringA + x % NA * BYTES, left);
+      return wait(&B.fullB[x % NB], (x / NB) & 1, &B.dead);
+    };
+    auto run = [&]() -> bool {
+      if (!wait(&B.own, 0, &B.dead) || !ready(0) || !wait(&B.loaded, 0, &B.dead)) return false;
+      tc::fence_after();
+      pairs(0);
+      for (int x = 0; x < n; x++) {
+        if (x + 1 < n) {
+          if (!ready(x + 1) || !wait(&B.taken, x & 1, &B.dead)) return false;
+          tc::fence_after();
+          pairs(x + 1);
+        }
+        if (!wait(&B.ds, x & 1, &B.dead)) return false;
+        tc::fence_after();
+        apply(tm + cDQ, tm + cDS, a0 + x % NA * BYTES, me);
+        commit(&B.first, me);
+        commit(&B.emptyA[x % NA], me);
+      }
+      return true;
+    };
+    if (n > 0 && !run()) {
+      commit(&B.drain, me);
+      for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
+    }
+  } else if (warp < EW && live) {
+    const int half = warp / 4, r = threadIdx.x & 127;
+    const bool in = r < nq;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t out = tm + cDQ + 64 * half + lanes;
+    const int lim = in ? keys_of(P.causal, i0 + r, t.Lq, t.Lk) : 0;
+    const size_t at = (size_t)h * P.Nq + t.q0 + i0 + r;
+    const float nl = in ? -P.lse2[at] : 0.f, nd = in ? -P.delta[at] : 0.f;
+    const uint64_t sc = two(P.scale2, P.scale2), l2 = two(nl, nl), dl = two(nd, nd);
+    float sum[64] = {};
+    load_own(tm + cG + 32 * half + lanes, P.pg + ((size_t)(t.q0 + i0 + r) * P.Hq + h) * D + 64 * half,
+             (size_t)P.Nq * P.Hq * D, in);
+    arrive(&B.loaded);
+    bool ok = true;
+    for (int x = 0; x < n; x++) {
+      ok = wait(&B.s, x & 1, &B.dead);
+      if (!ok) break;
+      tc::fence_after();
+      float a[16], g[16];
+      tm_ld16(tm + cS + 16 * half + lanes, a);
+      tm_ld16(tm + cDP + 16 * half + lanes, g);
+      tm_wait_ld(a);
+      tm_wait_ld(g);
+      arrive(&B.taken);
+      dq_grads(a, g, sc, l2, dl, t.j0 + x >= clean, lim - (t.j0 + x) * XB - 16 * half);
+      if (x > 0) {
+        ok = wait(&B.first, (x - 1) & 1, &B.dead);
+        if (!ok) break;
+        tc::fence_after();
+        add(sum, out);
+      }
+      put(a, tm + cDS + 8 * half + lanes);
+      arrive(&B.ds);
+    }
+    if (ok && n > 0) {
+      ok = wait(&B.first, (n - 1) & 1, &B.dead);
+      tc::fence_after();
+      if (ok) add(sum, out);
+    }
+    if (ok) {
+      const int w0 = r & ~31, c = 64 * half;
+      const bool whole = t.piece < 0;
+      const size_t to = ((size_t)(t.q0 + i0 + w0) * P.Hq + h) * D + c;
+      const size_t pa = (((size_t)t.piece * P.Hq + h) * BLK + w0) * D + c;  // (a piece's place)
+      store_sums(sm + half * HALF + w0 * 128, sum, whole ? P.scale : 1.0f, whole ? dq + to : P.po[1] + pa,
+                 whole ? (size_t)P.Hq * D : D, nq - w0);
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && B.dead) *P.err = KDA_ERR_DEVICE;
+  if (warp == EW) {
+    tc::fence_after();
+    tc::tmem_dealloc(tm, 512);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_f32_bwd(const SmxP& P, const float* q, const float* k, const float* v, const float* dO, float* dq,
-                           float* dk, float* dv, cudaStream_t st) {
-  constexpr int D = 128, R = F32_TILE / 16;
-  const size_t s1 = (2 * D * 16 * R + 4 * D * TM + TM * PP<R> + 2 * TM) * sizeof(float);
-  const size_t s2 = (2 * D * 16 * R + 3 * D * TM + TM * PP<R>) * sizeof(float);
-  const int64_t gk = (int64_t)max_tiles(P, 2) * P.Hkv, gq = (int64_t)max_tiles(P, 1) * P.Hq;
-  cudaError_t e = raise_smem<smx_dkv_kernel<D, R>>((int)s1);
-  if (e == cudaSuccess) e = raise_smem<smx_dq_kernel<D, R>>((int)s2);
+cudaError_t launch_f32_bwd(const SmxP& P, float* dq, float* dk, float* dv, cudaStream_t st) {
+  cudaError_t e = raise_smem<smx_f32_dkv_kernel>(SMEM);
+  if (e == cudaSuccess) e = raise_smem<smx_f32_dq_kernel>(SMEM);
   if (e != cudaSuccess) return e;
+  CUtensorMap mq, mk, xq, xg, xk, xv;  // own blocks of 128 rows, the other side's of 32
+  const int nq = 3 * P.Nq, nk = 3 * P.Nk;
+  if (!encode_head_rows(&mq, P.pq, nq, P.Hq, D, BLK) || !encode_head_rows(&mk, P.pk, nk, P.Hkv, D, BLK) ||
+      !encode_head_rows(&xq, P.pq, nq, P.Hq, D, XB) || !encode_head_rows(&xg, P.pg, nq, P.Hq, D, XB) ||
+      !encode_head_rows(&xk, P.pk, nk, P.Hkv, D, XB) || !encode_head_rows(&xv, P.pv, nk, P.Hkv, D, XB))
+    return cudaErrorInvalidValue;
+  const int64_t gk = (int64_t)max_tiles(P, 2) * P.Hkv, gq = (int64_t)max_tiles(P, 1) * P.Hq;
   prof_begin(K_SMX_DKV, st);
-  e = launch_pdl(smx_dkv_kernel<D, R>, dim3((unsigned)gk), dim3(NT), s1, st, P, q, k, v, dO, dk, dv);
+  e = launch_pdl(smx_f32_dkv_kernel, dim3((unsigned)gk), dim3(EW * 32 + 64), SMEM, st, P, xq, mk, xg, dk, dv);
   prof_end(K_SMX_DKV, st);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DQ, st);
-  e = launch_pdl(smx_dq_kernel<D, R>, dim3((unsigned)gq), dim3(NT), s2, st, P, q, k, v, dO, dq);
+  e = launch_pdl(smx_f32_dq_kernel, dim3((unsigned)gq), dim3(EW * 32 + 64), SMEM, st, P, mq, xk, xv, dq);
   prof_end(K_SMX_DQ, st);
   return e;
 }
