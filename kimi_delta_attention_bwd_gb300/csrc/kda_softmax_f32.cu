@@ -9,7 +9,7 @@
 // blocks are in registers, where they are rounded (the tensor pipe cuts its sums off).
 // Eight warps, a thread a row and half of a block's pairs, of a result's columns, and of an own row to tensor memory.
 // Bound by the tensor pipe: six products a product, and the first operand's reads (128 x 16 values for 32 columns: 32
-// cycles, so 16 of arithmetic).  4 x 1001 rows of 8 heads, every pair seen: 559 us with the forward (129); on the fp32
+// cycles, so 16 of arithmetic).  4 x 1001 rows of 8 heads, every pair seen: 559 us with the forward; on the fp32
 // pipe, 64 x 64 pairs a CTA, 2105.  (16 warps would halve a thread's 128 sums of dk and dv and have too few registers for
 // them; eight spill 220 bytes, a few loads a block.)
 #include "kda_softmax_tc.cuh"
@@ -111,13 +111,6 @@ __device__ __forceinline__ void add(float (&sum)[64], uint32_t tm) {
     for (int e = 0; e < 16; e++) sum[c + e] += v[e];
   }
 }
-// This warp's part of a step is in tensor memory, or taken from it.
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  tc::fence_before();
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mma::mbar_arrive(bar);
-}
-
 // dk and dv of 128 keys of one key head, over the blocks of its group's queries; the pairs transposed, a key a lane.
 // Products in the order S'(x + 1), dv(x), dP'(x + 1), dk(x): while two run, the weights and gradients of the others form.
 __global__ void __launch_bounds__(EW * 32 + 64, 1)
@@ -434,7 +427,8 @@ smx_f32_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       tm_wait_ld(a);
       tm_wait_ld(g);
       arrive(&B.taken);
-      dq_grads(a, g, sc, l2, dl, t.j0 + x >= clean, lim - (t.j0 + x) * XB - 16 * half);
+      dq_weights(a, sc, l2);
+      dq_grads(a, g, dl, t.j0 + x >= clean, lim - (t.j0 + x) * XB - 16 * half);
       if (x > 0) {
         ok = wait(&B.first, (x - 1) & 1, &B.dead);
         if (!ok) break;

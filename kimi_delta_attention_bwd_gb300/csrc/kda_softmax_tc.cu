@@ -468,17 +468,17 @@ __device__ __forceinline__ void put_parts(float (&v)[H][32], uint32_t to, uint32
     }
   }
 }
-// The same in dq, whose parts lie XB / 2 columns apart.
-template <int PARTS, bool TWICE, int XB>
-__device__ __forceinline__ void put_dq(float (&v)[2][32], uint32_t to) {
+// The same in dq, whose three parts lie XB / 2 columns apart, or second of two at `over`.
+template <int PARTS, bool TWICE, int XB, int H>
+__device__ __forceinline__ void put_dq(float (&v)[H][32], uint32_t to, uint32_t over) {
 #pragma unroll
   for (int y = 0; y < (TWICE ? 2 : PARTS); y++) {
 #pragma unroll
-    for (int c = 0; c < 2; c++) {
+    for (int c = 0; c < H; c++) {
       uint32_t w[16];
 #pragma unroll
       for (int e = 0; e < 16; e++) w[e] = rest(v[c][2 * e], v[c][2 * e + 1], y);
-      tm_st16(to + XB / 2 * y + 16 * c, w);
+      tm_st16((TWICE && y == 1 ? over : to + XB / 2 * y) + 16 * c, w);
     }
   }
 }
@@ -492,6 +492,9 @@ __device__ __forceinline__ void put_dq(float (&v)[2][32], uint32_t to) {
 // reads (q for dk and dv, k for dq), and B, of those that are free earlier (dO, v).
 // The other side's blocks have XB rows: 128, and eight warps for the pairs, at D = 128; at D = 64 half of both, and two
 // CTAs per SM.
+#ifndef EWQ64
+#define EWQ64 4
+#endif
 template <int D, int PARTS>
 struct Bwd {
   static_assert(PARTS == 1 || D == 64, "at D = 128 three parts of both own blocks leave no room for a ring: kda_softmax_f32.cu");
@@ -500,8 +503,10 @@ struct Bwd {
   static constexpr int NA = D == 64 && PARTS == 1 ? 5 : 3, NB = D == 64 && PARTS == 1 ? 4 : 2;
   static constexpr int BLOCKS = 2 * OWN + (NA + NB) * BYTES;
   // warps of the pairs: 64 of a row's pairs a thread; with three parts in dk and dv 32, and 32 columns of both sums
-  static constexpr int EW = XB / 16, EWK = PARTS == 3 ? 2 * EW : EW;
+  static constexpr int EW = D == 128 || PARTS == 3 ? XB / 16 : EWQ64, EWK = 8;
   static constexpr int COLS = D == 64 && PARTS == 1 ? 256 : 512, PER_SM = COLS == 256 ? 2 : 1;
+  // dq with bf16 io: q is an operand in tensor memory, and its place in shared memory has further blocks of ring A
+  static constexpr int QOWN = PARTS == 1 ? OWN : 2 * OWN, QA = NA + (2 * OWN - QOWN) / BYTES;
 };
 
 template <int XB>
@@ -513,7 +518,7 @@ struct BwdRest {  // (shared memory is full at D = 128: behind the blocks, whose
 };
 template <int D, int PARTS>
 constexpr int DKV_SMEM = Bwd<D, PARTS>::BLOCKS + (int)sizeof(BwdRest<Bwd<D, PARTS>::XB>);
-static_assert(2 * (DKV_SMEM<64, 1> + 1024) <= 233472 && DKV_SMEM<128, 1> <= 232448 && DKV_SMEM<64, 3> <= 232448,
+static_assert(Bwd<64, 1>::QA <= 7 && Bwd<128, 1>::QA <= 7 && 2 * (DKV_SMEM<64, 1> + 1024) <= 233472 && DKV_SMEM<128, 1> <= 232448 && DKV_SMEM<64, 3> <= 232448,
               "shared memory of an SM, of a CTA");
 
 template <int D, int PARTS>
@@ -522,7 +527,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
                   typename Io<PARTS>::T* __restrict__ dk, typename Io<PARTS>::T* __restrict__ dv) {
   using F = Bwd<D, PARTS>;
-  constexpr int XB = F::XB, EW = F::EWK, H = PARTS == 3 ? 1 : 2;
+  constexpr int XB = F::XB, EW = F::EWK, H = XB / 8 / EW;
   constexpr uint32_t cS = 0, cDP = XB, cDV = 2 * XB, cDK = 2 * XB + D, cX = 2 * XB + 2 * D;  // (X: third parts)
   extern __shared__ __align__(1024) unsigned char sm[];
   BwdRest<XB>& B = *reinterpret_cast<BwdRest<XB>*>(sm + F::BLOCKS);
@@ -739,7 +744,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       tc::fence_after();
     }
     if (ok) {
-      const int w0 = r & ~31, c = PARTS == 3 ? 32 * half : 64 * half;  // (the CTA's own blocks are no longer read)
+      const int w0 = r & ~31, c = PARTS == 3 ? 32 * half : 0;  // (the CTA's own blocks are no longer read)
       const size_t at = ((size_t)(t.k0 + j0 + w0) * P.Hkv + hk) * D + c, ld = (size_t)P.Hkv * D;
       unsigned char* buf = sm + half * HALF + w0 * 128;
       const size_t pa = (((size_t)t.piece * P.Hkv + hk) * BLK + w0) * D + c;  // (a piece's place)
@@ -752,12 +757,16 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
         const bool whole = t.piece < 0;
         store_sums(buf, sv, 1.0f, whole ? dv + at : P.po[2] + more + pa, whole ? ld : D, nk - w0);
         store_sums(buf, sk, whole ? P.scale : 1.0f, whole ? dk + at : P.po[2] + pa, whole ? ld : D, nk - w0);
-      } else if (t.piece >= 0) {
-        store_acc_f32(buf, tm + cDV + c + lanes, n > 0, P.po[2] + more + pa, D, nk - w0);
-        store_acc_f32(buf, tm + cDK + c + lanes, n > 0, P.po[2] + pa, D, nk - w0);
       } else {
-        store_acc(buf, tm + cDV + c + lanes, n > 0, 1.0f, dv + at, ld, nk - w0);
-        store_acc(buf, tm + cDK + c + lanes, n > 0, P.scale, dk + at, ld, nk - w0);
+        for (int y = half; y < 2 * (D / 64); y += EW / 4) {  // 64 columns: dv's, then dk's
+          const bool is_k = y >= D / 64;
+          const int cy = 64 * (is_k ? y - D / 64 : y);
+          const uint32_t from = tm + (is_k ? cDK : cDV) + cy + lanes;
+          if (t.piece >= 0)
+            store_acc_f32(buf, from, n > 0, P.po[2] + (is_k ? 0 : more) + pa + cy, D, nk - w0);
+          else
+            store_acc(buf, from, n > 0, is_k ? P.scale : 1.0f, (is_k ? dk : dv) + at + cy, ld, nk - w0);
+        }
       }
     }
     tc::fence_before();
@@ -772,10 +781,12 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
 
 // dq, per CTA (its grid starts behind dk and dv's last CTAs and needs nothing of theirs): 128 queries of one head over
 // the blocks of keys: S = q k^T, dP = dO v^T, dS = P (dP - delta), dq += dS k.
-// S and dP are taken to registers at once, so that the next block's products run while dS is formed; dS has two places
-// of its own.
+// S and dP are each taken to registers at once and formed anew for the next block meanwhile (one barrier for both left the
+// tensor pipe idle until both were taken: YYY).
+// (bf16) q is an operand in tensor memory: with both of S's from shared memory the copies and products of a block of 128
+// keep that busy for 1792 cycles, the tensor pipe for 1536.
 struct DqBars {
-  uint64_t own, fullA[5], emptyA[5], fullB[5], emptyB[5], s, taken, ds, used[2], drain;
+  uint64_t own, loaded, fullA[7], emptyA[7], fullB[4], emptyB[4], s, dp, takenS, takenP, ds, used[2], drain;
   uint32_t tmem;
   int dead;
 };
@@ -784,15 +795,16 @@ template <int D, int PARTS>
 __global__ void __launch_bounds__(Bwd<D, PARTS>::EW * 32 + 64, Bwd<D, PARTS>::PER_SM)
 smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
-                 typename Io<PARTS>::T* __restrict__ dq) {
+                 const bf16* __restrict__ q, typename Io<PARTS>::T* __restrict__ dq) {
   using F = Bwd<D, PARTS>;
-  constexpr int XB = F::XB, EW = F::EW;
+  constexpr int XB = F::XB, EW = F::EW, W = 4 * XB / EW, H = W / 32;  // (W: columns of a block's pairs a thread)
   constexpr uint32_t cS = 0, cDP = XB, cDQ = 2 * XB, nDQ = PARTS == 3 ? D : 0;         // (nDQ: columns to the other dq)
-  constexpr uint32_t cDS = 2 * XB + D + nDQ, nDS = XB / 2 * PARTS;                     // (nDS: of one dS, its parts)
+  constexpr uint32_t cDS = 2 * XB + D + nDQ, nDS = PARTS == 3 ? XB / 2 * PARTS : 0;    // (nDS: to the other dS)
+  constexpr uint32_t cQ = cDS + XB / 2;                                                 // (PARTS = 1)
   extern __shared__ unsigned char raw[];
   __shared__ DqBars B;
   unsigned char* sm = raw + ((1024 - (mma::smem_u32(raw) & 1023)) & 1023);
-  unsigned char *ringA = sm + 2 * F::OWN, *ringB = ringA + F::NA * F::BYTES;
+  unsigned char *ringA = sm + F::QOWN, *ringB = ringA + F::QA * F::BYTES;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == EW) tc::tmem_alloc(&B.tmem, F::COLS);
   if (threadIdx.x == 32 * (EW + 1)) {
@@ -803,7 +815,8 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   }
   if (threadIdx.x == 0) {
     mma::mbar_init(&B.own, 1);
-    for (int i = 0; i < F::NA; i++) {
+    mma::mbar_init(&B.loaded, EW);
+    for (int i = 0; i < F::QA; i++) {
       mma::mbar_init(&B.fullA[i], 1);
       mma::mbar_init(&B.emptyA[i], 1);
     }
@@ -812,7 +825,9 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       mma::mbar_init(&B.emptyB[i], 1);
     }
     mma::mbar_init(&B.s, 1);
-    mma::mbar_init(&B.taken, EW);
+    mma::mbar_init(&B.dp, 1);
+    mma::mbar_init(&B.takenS, EW);
+    mma::mbar_init(&B.takenP, EW);
     mma::mbar_init(&B.ds, EW);
     mma::mbar_init(&B.used[0], 1);
     mma::mbar_init(&B.used[1], 1);
@@ -824,7 +839,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   const int h = blockIdx.x % P.Hq, hk = h / P.G;
   const bool live = saved(P) && tile_of(P, 1, blockIdx.x / P.Hq, false, t);
   int i0 = 0, nq = 0, n = 0, clean = 0;
-  bool twice = false;  // dS in two parts, in its two places together
+  bool twice = false;  // dS in two parts, the second ones over S
   if (live) {
     i0 = t.t * BLK;
     nq = min(BLK, t.Lq - i0);
@@ -836,18 +851,18 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   __syncthreads();
   tc::fence_after();
   const uint32_t tm = tm_base<F::COLS>(B.tmem);
-  auto place = [](auto tw, int x) { return decltype(tw)::value ? 0 : x & 1; };  // of block x's dS
+  auto place = [](int x) { return PARTS == 3 ? x & 1 : 0; };  // of block x's dS
 
   if (warp == EW + 1) {  // copies
     if (lane == 0 && n > 0) {
-      mma::mbar_expect_tx(&B.own, 2 * F::OWN);
-      load_block<D, BLK, PARTS>(sm, &mq, h, t.q0 + i0, P.Nq, &B.own);
-      load_block<D, BLK, PARTS>(sm + F::OWN, &mg, h, t.q0 + i0, P.Nq, &B.own);
+      mma::mbar_expect_tx(&B.own, F::QOWN);
+      load_block<D, BLK, PARTS>(sm, &mg, h, t.q0 + i0, P.Nq, &B.own);
+      if (PARTS == 3) load_block<D, BLK, PARTS>(sm + F::OWN, &mq, h, t.q0 + i0, P.Nq, &B.own);
     }
     __syncwarp();
     for (int x = 0; x < n; x++) {
-      const int sa = x % F::NA, sb = x % F::NB;
-      if (x >= F::NA && !wait(&B.emptyA[sa], (x / F::NA - 1) & 1, &B.dead)) break;
+      const int sa = x % F::QA, sb = x % F::NB;
+      if (x >= F::QA && !wait(&B.emptyA[sa], (x / F::QA - 1) & 1, &B.dead)) break;
       if (lane == 0) {
         mma::mbar_expect_tx(&B.fullA[sa], F::BYTES);
         load_block<D, XB, PARTS>(ringA + sa * F::BYTES, &mk, hk, t.k0 + (t.j0 + x) * XB, P.Nk, &B.fullA[sa]);
@@ -861,46 +876,57 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       __syncwarp();
     }
   } else if (warp == EW) {  // products
-    const uint32_t q0 = mma::smem_u32(sm), g0 = q0 + F::OWN, a0 = mma::smem_u32(ringA), b0 = mma::smem_u32(ringB);
+    const uint32_t g0 = mma::smem_u32(sm), a0 = mma::smem_u32(ringA), b0 = mma::smem_u32(ringB);
     constexpr uint32_t id_s = idesc(BLK, XB, false), id_o = idesc(BLK, D, true);
     const uint32_t me = elect();
-    auto pairs = [&](int x) {
-      const uint32_t kb = a0 + x % F::NA * F::BYTES, vb = b0 + x % F::NB * F::BYTES;
-      prod_ss<D, PARTS, BLK, XB>(tm + cS, q0, kb, id_s, me);
-      prod_ss<D, PARTS, BLK, XB>(tm + cDP, g0, vb, id_s, me);
-      commit(&B.s, me);
-      commit(&B.emptyB[x % F::NB], me);
-    };
-    auto ready = [&](int x) -> bool {
+    auto logits = [&](int x) -> bool {
       const int left = t.Lk - (t.j0 + x) * XB;
-      if (!wait(&B.fullA[x % F::NA], (x / F::NA) & 1, &B.dead)) return false;
-      if (left < XB) zero_rows<D, XB, PARTS>(ringA + x % F::NA * F::BYTES, left);
-      return wait(&B.fullB[x % F::NB], (x / F::NB) & 1, &B.dead);
+      const uint32_t kb = a0 + x % F::QA * F::BYTES;
+      if (!wait(&B.fullA[x % F::QA], (x / F::QA) & 1, &B.dead)) return false;
+      if (left < XB) zero_rows<D, XB, PARTS>(ringA + x % F::QA * F::BYTES, left);
+      if (x > 0 && !wait(&B.takenS, (x - 1) & 1, &B.dead)) return false;
+      tc::fence_after();
+      if constexpr (PARTS == 3) {
+        prod_ss<D, PARTS, BLK, XB>(tm + cS, g0 + F::OWN, kb, id_s, me);
+      } else {
+#pragma unroll
+        for (int s = 0; s < D / 16; s++) mma_ts(tm + cS, tm + cQ + 8 * s, desc_k<XB>(kb, s), id_s, s > 0, me);
+      }
+      commit(&B.s, me);
+      return true;
+    };
+    auto grads = [&](int x) -> bool {
+      if (!wait(&B.fullB[x % F::NB], (x / F::NB) & 1, &B.dead)) return false;
+      if (x > 0 && !wait(&B.takenP, (x - 1) & 1, &B.dead)) return false;
+      tc::fence_after();
+      prod_ss<D, PARTS, BLK, XB>(tm + cDP, g0, b0 + x % F::NB * F::BYTES, id_s, me);
+      commit(&B.dp, me);
+      commit(&B.emptyB[x % F::NB], me);
+      return true;
     };
     auto run = [&](auto tw) -> bool {
-      if (!wait(&B.own, 0, &B.dead) || !ready(0)) return false;
-      pairs(0);
+      if (!wait(&B.own, 0, &B.dead) || (PARTS == 1 && !wait(&B.loaded, 0, &B.dead))) return false;
+      if (!logits(0) || !grads(0)) return false;
       for (int x = 0; x < n; x++) {
-        if (x + 1 < n) {
-          if (!ready(x + 1) || !wait(&B.taken, x & 1, &B.dead)) return false;
-          tc::fence_after();
-          pairs(x + 1);
-        }
+        auto next = [&]() { return x + 1 == n || (logits(x + 1) && grads(x + 1)); };
+        if (!decltype(tw)::value && !next()) return false;
         if (!wait(&B.ds, x & 1, &B.dead)) return false;
         tc::fence_after();
-        const uint32_t kb = a0 + x % F::NA * F::BYTES;
+        const uint32_t kb = a0 + x % F::QA * F::BYTES;
         using Q = Prod<PARTS>;
 #pragma unroll
         for (int y = 0; y < Q::N; y++)
 #pragma unroll
           for (int s = 0; s < XB / 16; s++)
-            mma_ts(tm + cDQ + nDQ * (x & 1), tm + cDS + nDS * place(tw, x) + XB / 2 * Q::a(y) + 8 * s,
+            mma_ts(tm + cDQ + nDQ * (x & 1), tm + cDS + nDS * place(x) + XB / 2 * Q::a(y) + 8 * s,
                    desc_mn<XB>(kb + Q::b(y) * (XB * D * 2), s), id_o, (PARTS == 1 && x > 0) || y > 0 || s > 0, me);
         if constexpr (decltype(tw)::value)
 #pragma unroll
-          for (int s = 0; s < XB / 16; s++) mma_ts(tm + cDQ, tm + cDS + XB / 2 + 8 * s, desc_mn<XB>(kb, s), id_o, true, me);
-        commit(&B.used[place(tw, x)], me);
-        commit(&B.emptyA[x % F::NA], me);
+          for (int s = 0; s < XB / 16; s++)
+            mma_ts(tm + cDQ, tm + cS + W * (s / (W / 16)) + 8 * (s % (W / 16)), desc_mn<XB>(kb, s), id_o, true, me);
+        commit(&B.used[place(x)], me);
+        commit(&B.emptyA[x % F::QA], me);
+        if (decltype(tw)::value && !next()) return false;
       }
       return true;
     };
@@ -912,53 +938,67 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
     const int half = warp / 4, r = threadIdx.x & 127;
     const bool in = r < nq;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tm + cS + 64 * half + lanes, td = tm + cDP + 64 * half + lanes;
+    const uint32_t ts = tm + cS + W * half + lanes, td = tm + cDP + W * half + lanes;
     const int lim = in ? keys_of(P.causal, i0 + r, t.Lq, t.Lk) : 0;
     const size_t at = (size_t)h * P.Nq + t.q0 + i0 + r;
     const float nl = in ? -P.lse2[at] : 0.f, nd = in ? -P.delta[at] : 0.f;
     const uint64_t sc = two(P.scale2, P.scale2), l2 = two(nl, nl), dl = two(nd, nd);
     float sum[PARTS == 3 ? 64 : 1] = {};  // (three parts) dq
+    if constexpr (PARTS == 1) {  // the row's q, W of its values a thread (zeros behind the document's end)
+      const bf16* row = q + ((size_t)(t.q0 + i0 + r) * P.Hq + h) * D + W * half;
+#pragma unroll
+      for (int c = 0; c < H; c++) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const uint4 u = in ? *reinterpret_cast<const uint4*>(row + 32 * c + 8 * e) : make_uint4(0, 0, 0, 0);
+          w[4 * e] = u.x, w[4 * e + 1] = u.y, w[4 * e + 2] = u.z, w[4 * e + 3] = u.w;
+        }
+        tm_st16(tm + cQ + W / 2 * half + 16 * c + lanes, w);
+      }
+      tm_wait_st();
+      arrive(&B.loaded);
+    }
     auto pairs = [&](auto tw) -> bool {
       constexpr bool TW = decltype(tw)::value;
       for (int x = 0; x < n; x++) {
         if (!wait(&B.s, x & 1, &B.dead)) return false;
         tc::fence_after();
-        float a[2][32], g[2][32];
+        float a[H][32], g[H][32];
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
-          tm_ld32(ts + 32 * c, a[c]);
-          tm_ld32(td + 32 * c, g[c]);
-        }
+        for (int c = 0; c < H; c++) tm_ld32(ts + 32 * c, a[c]);
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
-          tm_wait_ld(a[c]);
-          tm_wait_ld(g[c]);
-        }
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) mma::mbar_arrive(&B.taken);
-        const int left = lim - (t.j0 + x) * XB - 64 * half;
+        for (int c = 0; c < H; c++) tm_wait_ld(a[c]);
+        arrive(&B.takenS);
+#pragma unroll
+        for (int c = 0; c < H; c++) dq_weights(a[c], sc, l2);
+        if (!wait(&B.dp, x & 1, &B.dead)) return false;
+        tc::fence_after();
+#pragma unroll
+        for (int c = 0; c < H; c++) tm_ld32(td + 32 * c, g[c]);
+#pragma unroll
+        for (int c = 0; c < H; c++) tm_wait_ld(g[c]);
+        arrive(&B.takenP);
+        const int left = lim - (t.j0 + x) * XB - W * half;
         const bool cut = t.j0 + x >= clean;
 #pragma unroll
-        for (int c = 0; c < 2; c++) dq_grads(a[c], g[c], sc, l2, dl, cut, left - 32 * c);
-        if (x >= (TW ? 1 : 2)) {
-          if (!wait(&B.used[place(tw, x)], ((TW ? x : x / 2) - 1) & 1, &B.dead)) return false;
+        for (int c = 0; c < H; c++) dq_grads(a[c], g[c], dl, cut, left - 32 * c);
+        if (x >= (PARTS == 3 ? 2 : 1)) {
+          if (!wait(&B.used[place(x)], ((PARTS == 3 ? x / 2 : x) - 1) & 1, &B.dead)) return false;
           tc::fence_after();
           if constexpr (PARTS == 3) add_columns(sum, tm + cDQ + nDQ * (x & 1) + lanes);  // (block x - 2's)
         }
-        const uint32_t to = tm + cDS + nDS * place(tw, x) + 32 * half + lanes;
-        put_dq<PARTS, TW, XB>(a, to);
+        const uint32_t to = tm + cDS + nDS * place(x) + W / 2 * half + lanes;
+        put_dq<PARTS, TW, XB, H>(a, to, ts);
         tm_wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) mma::mbar_arrive(&B.ds);
+        arrive(&B.ds);
       }
-      if (n > 0 && !wait(&B.used[place(tw, n - 1)], (TW ? n - 1 : (n - 1) / 2) & 1, &B.dead)) return false;
+      if (n > 0 && !wait(&B.used[place(n - 1)], (PARTS == 3 ? (n - 1) / 2 : n - 1) & 1, &B.dead)) return false;
       tc::fence_after();
       return true;
     };
     const bool ok = with_parts<PARTS>(twice, pairs);
-    if (ok) {
+    if (ok && half < D / 64) {
       const int w0 = r & ~31, c = 64 * half;
       unsigned char* buf = sm + half * HALF + w0 * 128;
       const size_t to = ((size_t)(t.q0 + i0 + w0) * P.Hq + h) * D + c, ld = (size_t)P.Hq * D;
@@ -1008,7 +1048,8 @@ cudaError_t bwd(const SmxP& P, const void* q, const void* k, const void* v, cons
   prof_end(K_SMX_DKV, st);
   if (e != cudaSuccess) return e;
   prof_begin(K_SMX_DQ, st);
-  e = launch_pdl(smx_tc_dq_kernel<D, PARTS>, dim3((unsigned)gq), dim3(F::EW * 32 + 64), F::BLOCKS + 1024, st, P, mq, xk, xv, mg, (T*)dq);
+  e = launch_pdl(smx_tc_dq_kernel<D, PARTS>, dim3((unsigned)gq), dim3(F::EW * 32 + 64), F::BLOCKS + 1024, st, P, mq, xk,
+                 xv, mg, (const bf16*)q, (T*)dq);
   prof_end(K_SMX_DQ, st);
   return e;
 }

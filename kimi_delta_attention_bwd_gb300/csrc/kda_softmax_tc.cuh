@@ -148,6 +148,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead) 
   return ok;
 }
 
+// This warp's part of a step is in tensor memory, or taken from it.
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  tc::fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mma::mbar_arrive(bar);
+}
+
 // Logits of a row: those from `left` on are not seen.
 template <int N>
 __device__ __forceinline__ void mask(float (&v)[N], int left) {
@@ -351,17 +358,22 @@ __device__ __forceinline__ void bwd_grads(float (&p)[N], const float (&dp)[N], c
 }
 // The same of a query's row: its (negated) sums are scalars, its keys end at `left`.
 template <int N>
-__device__ __forceinline__ void dq_grads(float (&v)[N], const float (&dp)[N], uint64_t sc, uint64_t l2, uint64_t dl,
-                                         bool cut, int left) {
+__device__ __forceinline__ void dq_weights(float (&v)[N], uint64_t sc, uint64_t l2) {
 #pragma unroll
   for (int e = 0; e < N; e += 2) {
-    float a, b;
-    one(fma2(two(v[e], v[e + 1]), sc, l2), a, b);
-    one(mul2(two(ex2(a), ex2(b)), add2(two(dp[e], dp[e + 1]), dl)), v[e], v[e + 1]);
+    one(fma2(two(v[e], v[e + 1]), sc, l2), v[e], v[e + 1]);
+    v[e] = ex2(v[e]);
+    v[e + 1] = ex2(v[e + 1]);
   }
+}
+template <int N>
+__device__ __forceinline__ void dq_grads(float (&p)[N], const float (&dp)[N], uint64_t dl, bool cut, int left) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2)
+    one(mul2(two(p[e], p[e + 1]), add2(two(dp[e], dp[e + 1]), dl)), p[e], p[e + 1]);
   if (cut)
 #pragma unroll
-    for (int e = 0; e < N; e++) v[e] = e < left ? v[e] : 0.f;
+    for (int e = 0; e < N; e++) p[e] = e < left ? p[e] : 0.f;
 }
 template <int N>
 __device__ __forceinline__ void add_columns(float (&sum)[N], uint32_t tm) {
