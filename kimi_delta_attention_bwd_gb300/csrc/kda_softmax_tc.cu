@@ -488,22 +488,20 @@ __device__ __forceinline__ void put_dq(float (&v)[H][32], uint32_t to, uint32_t 
 // them, each half of the queries' columns; the row sums of the queries come through shared memory.  The products are
 // issued as dv, next S', dk, next dP': while two run, the other two's operand is formed.
 //
-// Both kernels keep two blocks of their own and two rings: A, of the blocks that a first product and then the last one
+// Both kernels keep two blocks of their own (dq with bf16 io one) and two rings: A, of the blocks that a first product and then the last one
 // reads (q for dk and dv, k for dq), and B, of those that are free earlier (dO, v).
 // The other side's blocks have XB rows: 128, and eight warps for the pairs, at D = 128; at D = 64 half of both, and two
 // CTAs per SM.
-#ifndef EWQ64
-#define EWQ64 4
-#endif
 template <int D, int PARTS>
 struct Bwd {
-  static_assert(PARTS == 1 || D == 64, "at D = 128 three parts of both own blocks leave no room for a ring: kda_softmax_f32.cu");
+  static_assert(PARTS == 1 || D == 64, "at D = 128 three parts of both own blocks leave no room: kda_softmax_f32.cu");
   static constexpr int XB = D == 64 ? 64 : 128;
   static constexpr int OWN = BLK * D * 2 * PARTS, BYTES = XB * D * 2 * PARTS;  // a block of either side
   static constexpr int NA = D == 64 && PARTS == 1 ? 5 : 3, NB = D == 64 && PARTS == 1 ? 4 : 2;
   static constexpr int BLOCKS = 2 * OWN + (NA + NB) * BYTES;
-  // warps of the pairs: 64 of a row's pairs a thread; with three parts in dk and dv 32, and 32 columns of both sums
-  static constexpr int EW = D == 128 || PARTS == 3 ? XB / 16 : EWQ64, EWK = 8;
+  // warps of the pairs: 64 of a row's pairs a thread, at D = 64 in dk and dv 32 (300M packed step: 93 us, 97 with 64); with
+  // three parts there also 32 columns of both sums.  (16 warps at D = 128: dk and dv the same, dq 6% slower.)
+  static constexpr int EW = XB / 16, EWK = 8;
   static constexpr int COLS = D == 64 && PARTS == 1 ? 256 : 512, PER_SM = COLS == 256 ? 2 : 1;
   // dq with bf16 io: q is an operand in tensor memory, and its place in shared memory has further blocks of ring A
   static constexpr int QOWN = PARTS == 1 ? OWN : 2 * OWN, QA = NA + (2 * OWN - QOWN) / BYTES;
@@ -782,9 +780,9 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
 // dq, per CTA (its grid starts behind dk and dv's last CTAs and needs nothing of theirs): 128 queries of one head over
 // the blocks of keys: S = q k^T, dP = dO v^T, dS = P (dP - delta), dq += dS k.
 // S and dP are each taken to registers at once and formed anew for the next block meanwhile (one barrier for both left the
-// tensor pipe idle until both were taken: YYY).
-// (bf16) q is an operand in tensor memory: with both of S's from shared memory the copies and products of a block of 128
-// keep that busy for 1792 cycles, the tensor pipe for 1536.
+// tensor pipe idle until both were taken: large heads 1085 us, so 1027).  (bf16) q is an operand in tensor memory: with both
+// of S's from shared memory the copies and products of a block of 128 keep that busy for 1792 cycles, the tensor pipe for
+// 1536 (300M packed step 65.5 us, 67.5 without; at D = 128 the same).
 struct DqBars {
   uint64_t own, loaded, fullA[7], emptyA[7], fullB[4], emptyB[4], s, dp, takenS, takenP, ds, used[2], drain;
   uint32_t tmem;
