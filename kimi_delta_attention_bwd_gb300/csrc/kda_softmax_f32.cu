@@ -137,7 +137,7 @@ smx_f32_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_
   pdl_release();  // dq's CTAs may follow this grid's last ones: they wait for it at their end only
   Tile t;
   const int hk = blockIdx.x % P.Hkv;
-  const bool live = saved(P) && tile_of(P, 2, blockIdx.x / P.Hkv, true, t);
+  const bool live = tile_of(P, 2, blockIdx.x / P.Hkv, true, t);
   int j0 = 0, nk = 0, first = 0, per = 0;  // first query block, blocks a head
   if (live) {
     j0 = t.t * BLK;
@@ -243,6 +243,7 @@ smx_f32_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_
     load_own(tm + cV + 32 * half + lanes, P.pv + ((size_t)(t.k0 + j0 + r) * P.Hkv + hk) * D + 64 * half,
              (size_t)P.Nk * P.Hkv * D, r < nk);
     arrive(&B.loaded);
+    const bool keep = saved(P);
     bool ok = true;
     for (int x = 0; x < n; x++) {
       const int s = x % NA, i0 = (first + (t.j0 + x) % per) * XB;
@@ -285,7 +286,7 @@ smx_f32_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_
       tc::fence_after();
       if (ok) add(sk, out);
     }
-    if (ok) {
+    if (ok && keep) {
       const int w0 = r & ~31, c = 64 * half;  // (the CTA's own block is no longer read)
       const bool whole = t.piece < 0;
       const size_t at = ((size_t)(t.k0 + j0 + w0) * P.Hkv + hk) * D + c, ld = whole ? (size_t)P.Hkv * D : D;
@@ -332,7 +333,7 @@ smx_f32_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   if (threadIdx.x == 0) init(B);
   Tile t;
   const int h = blockIdx.x % P.Hq, hk = h / P.G;
-  const bool live = saved(P) && tile_of(P, 1, blockIdx.x / P.Hq, false, t);
+  const bool live = tile_of(P, 1, blockIdx.x / P.Hq, false, t);
   int i0 = 0, nq = 0, n = 0, clean = 0;
   if (live) {
     i0 = t.t * BLK;
@@ -416,6 +417,7 @@ smx_f32_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     load_own(tm + cG + 32 * half + lanes, P.pg + ((size_t)(t.q0 + i0 + r) * P.Hq + h) * D + 64 * half,
              (size_t)P.Nq * P.Hq * D, in);
     arrive(&B.loaded);
+    const bool keep = saved(P);
     bool ok = true;
     for (int x = 0; x < n; x++) {
       ok = wait(&B.s, x & 1, &B.dead);
@@ -443,7 +445,7 @@ smx_f32_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       tc::fence_after();
       if (ok) add(sum, out);
     }
-    if (ok) {
+    if (ok && keep) {
       const int w0 = r & ~31, c = 64 * half;
       const bool whole = t.piece < 0;
       const size_t to = ((size_t)(t.q0 + i0 + w0) * P.Hq + h) * D + c;

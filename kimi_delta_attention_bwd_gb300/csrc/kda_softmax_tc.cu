@@ -567,7 +567,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   pdl_release();  // dq's CTAs may follow this grid's last ones: they wait for it at their end only
   Tile t;
   const int hk = blockIdx.x % P.Hkv;
-  const bool live = saved(P) && tile_of(P, 2, blockIdx.x / P.Hkv, true, t);
+  const bool live = tile_of(P, 2, blockIdx.x / P.Hkv, true, t);
   int j0 = 0, nk = 0, first = 0, per = 0;  // first query block, blocks a head
   if (live) {
     j0 = t.t * BLK;
@@ -736,12 +736,13 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       }
       return true;
     };
+    const bool keep = saved(P);
     bool ok = with_parts<PARTS>(twice, pairs);
     if (ok && n > 0) {
       ok = wait(&B.done, 0, &B.dead);
       tc::fence_after();
     }
-    if (ok) {
+    if (ok && keep) {
       const int w0 = r & ~31, c = PARTS == 3 ? 32 * half : 0;  // (the CTA's own blocks are no longer read)
       const size_t at = ((size_t)(t.k0 + j0 + w0) * P.Hkv + hk) * D + c, ld = (size_t)P.Hkv * D;
       unsigned char* buf = sm + half * HALF + w0 * 128;
@@ -835,7 +836,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   }
   Tile t;
   const int h = blockIdx.x % P.Hq, hk = h / P.G;
-  const bool live = saved(P) && tile_of(P, 1, blockIdx.x / P.Hq, false, t);
+  const bool live = tile_of(P, 1, blockIdx.x / P.Hq, false, t);
   int i0 = 0, nq = 0, n = 0, clean = 0;
   bool twice = false;  // dS in two parts, the second ones over S
   if (live) {
@@ -995,8 +996,9 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
       tc::fence_after();
       return true;
     };
+    const bool keep = saved(P);
     const bool ok = with_parts<PARTS>(twice, pairs);
-    if (ok && half < D / 64) {
+    if (ok && keep && half < D / 64) {
       const int w0 = r & ~31, c = 64 * half;
       unsigned char* buf = sm + half * HALF + w0 * 128;
       const size_t to = ((size_t)(t.q0 + i0 + w0) * P.Hq + h) * D + c, ld = (size_t)P.Hq * D;
