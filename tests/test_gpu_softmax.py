@@ -65,14 +65,14 @@ def run(x, causal=True, backward=True, host=False, scale=None):
     return got
 
 
-def limits(ans, dt, D, x):
+def limits(ans, dt, D, x, op=None):
     ref, mag, A = ans
     L = max(x["q"].shape[0] * x["q"].shape[1], x["k"].shape[0] * x["k"].shape[1]) + D
     if "dk" in ref:
         L *= x["q"].shape[2] // x["k"].shape[2]
     E = 2 * (D + 8) * 2.0 ** -23 * A + 2.0 ** -20
     R = ROUND[dt]
-    op = {"bf16": 2.0 ** -8, "f32": 0.0}[dt]
+    op = {"bf16": 2.0 ** -8, "f32": 0.0}[dt] if op is None else op
     lim = {}
     for n, r in ref.items():
         if n == "lse":
@@ -82,8 +82,8 @@ def limits(ans, dt, D, x):
     return lim
 
 
-def check(got, ans, dt, D, x):
-    for n, lim in limits(ans, dt, D, x).items():
+def check(got, ans, dt, D, x, op=None):
+    for n, lim in limits(ans, dt, D, x, op).items():
         r = ans[0][n]
         g = got[n].detach().double().cpu().numpy().reshape(r.shape)
         same = (g == r) & np.isinf(r)
@@ -159,6 +159,32 @@ def test_few_queries_on_many_keys(dt, D, lq, lk, rows, causal):
     """Tiles whose keys are cut into pieces and joined, whole ones beside them, and the backward after them."""
     x = make(40, lq, lk, 2, 1, D, dt, rows=rows)
     check(run(x, causal), oracle(x, causal), dt, D, x)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lq,lk", [([31], [31]), ([32, 33, 96], [32, 33, 96]), ([97, 1], [63, 65]), ([160], [33]),
+                                   ([224, 31], [320, 1])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_fp32_blocks(D, lq, lk, causal):
+    """Borders of the fp32 kernels' smaller blocks."""
+    x = make(43, lq, lk, 4, 2, D, "f32")
+    check(run(x, causal), oracle(x, causal), "f32", D, x)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lq,lk", [([50], [50]), ([1, 2, 40, 64], [1, 2, 40, 64]), ([200, 129, 256], [256, 130, 255])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_short_documents_take_operands_of_two_parts(D, lq, lk, causal):
+    """Few bf16 roundings do not average out: weights and their gradients are off by 2^-16 (two parts), and so is the o
+    of delta (its value and what rounding left); the outputs' own rounding remains."""
+    x = make(44, lq, lk, 4, 2, D, "bf16")
+    check(run(x, causal), oracle(x, causal), "bf16", D, x, op=2.0 ** -16)
+
+
+@pytest.mark.parametrize("n", [1023, 1024, 1025])
+def test_both_sides_of_the_small_problems_border(n):
+    x = make(45, [40, n - 40], [40, n - 40], 2, 1, 64, "bf16")
+    check(run(x), oracle(x), "bf16", 64, x)
 
 
 def test_pieces_with_values_that_are_not_finite():
@@ -266,6 +292,56 @@ def test_backward_on_another_stream_and_twice():
     for g in (first, second):
         for n in g:
             assert torch.equal(g[n], want[n]), n
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_two_streams_at_once(dt):
+    """Two problems' steps in flight at once, each on a stream of its own, again and again."""
+    xs = [make(46, [700, 0, 300], [700, 0, 300], 4, 2, 128, dt), make(47, [900], [900], 8, 8, 64, dt, rows=True)]
+    want = [run(x) for x in xs]
+    d = [{n: x[n].cuda() for n in ("q", "k", "v", "dO", "cu")} for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                o, lse, ctx = kda.kda_softmax_forward(d[i]["q"], d[i]["k"], d[i]["v"],
+                                                      cu_seqlens=None if xs[i]["rows"] else d[i]["cu"])
+                got.append((i, dict(o=o, lse=lse, **kda.kda_softmax_backward(ctx, d[i]["dO"]))))
+                del ctx
+    torch.cuda.synchronize()
+    for i, g in got:
+        for n in g:
+            assert torch.equal(g[n], want[i][n]), n
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_two_graphs_share_a_workspace(dt):
+    """A step of each of two problems, captured over one workspace and replayed in turn."""
+    xs = [make(48, [200, 100], [200, 100], 4, 2, 128, dt), make(49, [150], [150], 4, 4, 128, dt, rows=True)]
+    want = [run(x) for x in xs]
+    d = [{n: x[n].cuda() for n in ("q", "k", "v", "dO", "cu")} for x in xs]
+    kw = [dict(cu_seqlens=None if x["rows"] else y["cu"]) for x, y in zip(xs, d)]
+    size = max(kda.kda_softmax_forward(y["q"], y["k"], y["v"], **k)[2].workspace.numel() for y, k in zip(d, kw))
+    shared = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def step(i):
+        o, lse, ctx = kda.kda_softmax_forward(d[i]["q"], d[i]["k"], d[i]["v"], workspace=shared, **kw[i])
+        return dict(o=o, lse=lse, **kda.kda_softmax_backward(ctx, d[i]["dO"]))
+    graphs, outs = [], []
+    for i in range(2):
+        step(i)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(i))
+    for i in (0, 1, 1, 0):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        for n in outs[i]:
+            assert torch.equal(outs[i][n], want[i][n]), n
 
 
 def test_a_thread_s_first_call():
