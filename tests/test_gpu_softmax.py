@@ -431,6 +431,34 @@ def test_autograd_matches_the_calls_and_differences():
         assert torch.equal(t, u)
 
 
+def test_a_training_step_captured_into_a_graph():
+    """Positions, attention and their gradients through autograd, captured once and replayed on other values."""
+    xs = [make(50, [70, 1, 229], [70, 1, 229], 4, 2, 64, "bf16"), make(51, [100, 200, 0], [100, 200, 0], 4, 2, 64, "bf16")]
+    d = {n: xs[0][n].cuda() for n in ("q", "k", "v", "dO", "cu")}
+    freq = kda.rotary_frequencies(64)[0]
+
+    def step():
+        leaves = [d[n].detach().requires_grad_() for n in ("q", "k", "v")]
+        q, k = kda.rotary(leaves[0], leaves[1], freq, cu_seqlens=d["cu"])
+        o = kda.softmax_attention(q, k, leaves[2], cu_seqlens=d["cu"])
+        return [o.detach(), *torch.autograd.grad(o, leaves, d["dO"])]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for x in xs[::-1]:
+        for n in d:
+            d[n].copy_(x[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------- single tokens
 def decode_case(seed, lens, cap, Hq, Hkv, D, dt):
     g = torch.Generator().manual_seed(seed)
