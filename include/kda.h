@@ -500,7 +500,9 @@ KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, const void* q, 
 
 /* Backward of sum(o * dO): dq [B, T, Hq, D], dk, dv [B, Tk, Hkv, D] (dtype),
  * from the forward's inputs, its o and its workspace (another one is refused by
- * the device: KDA_ERR_WORKSPACE from kda_device_status).  dk and dv are summed over
+ * the device: KDA_ERR_WORKSPACE from kda_device_status).  The documents are those that
+ * the forward left in the workspace: cu_seqlens and cu_seqlens_k say only that there
+ * are offsets, the device memory they point to is not read and may be gone or hold others.  dk and dv are summed over
  * the heads of a group and over the queries by one CTA, or by a few whose sums are
  * added in order: no atomics.  The workspace may be used by several backwards, one
  * at a time (pieces' results and dO's parts lie in it). */

@@ -174,18 +174,18 @@ class _SoftmaxAttention(torch.autograd.Function):
                                          cu_seqlens_k=cu_seqlens_k, cu_seqlens_host=cu_seqlens_host,
                                          cu_seqlens_k_host=cu_seqlens_k_host,
                                          save_for_backward=recorded and any(fctx.needs_input_grad))
-        # (the workspace among them: freed by the backward, seen by hooks)
-        fctx.save_for_backward(q, k, v, o, cu_seqlens, cu_seqlens_k, sctx.workspace)
+        # (the workspace, which holds the documents' tiles, among them: freed by the backward, seen by hooks)
+        fctx.save_for_backward(q, k, v, o, sctx.workspace)
         fctx.rest = (sctx.problem, sctx.host, sctx.saved)
         return o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(fctx, dO):
-        q, k, v, o, cu_seqlens, cu_seqlens_k, workspace = fctx.saved_tensors
+        q, k, v, o, workspace = fctx.saved_tensors
         problem, host, saved = fctx.rest
-        g = kda_softmax_backward(SoftmaxContext(problem, q, k, v, o, cu_seqlens, cu_seqlens_k, host, workspace, saved),
-                                 _given(dO))
+        # (the library's backward reads no offsets on the device)
+        g = kda_softmax_backward(SoftmaxContext(problem, q, k, v, o, None, None, host, workspace, saved), _given(dO))
         return g["dq"], g["dk"], g["dv"], None, None, None, None, None, None, None
 
 

@@ -9,10 +9,12 @@ namespace smx {
 namespace {
 
 // ------------------------------------------------------------ tile tables
-// Block b builds list l0 + b: every document's tiles of queries (keys for list
+// Block l builds list l: every document's tiles of queries (keys for list
 // 2), by decreasing pairs, so that the longest tiles start first and the grid's
 // end is short ones (a counting sort; tiles of equal weight in any order, which no
-// result depends on).  The offsets are checked before any of them is used.
+// result depends on).  The offsets are checked before any of them is used.  A saving
+// forward builds the backward's lists too, so that a step has one launch of this kernel and
+// the backward reads no offsets: they may be gone or others by then.
 // Tiles with more than 1.5 times the load that `target` CTAs would have on average are
 // cut along the other side into pieces of about that load, which a further kernel joins:
 // a few queries against long prefixes, or few heads, would else leave most SMs idle
@@ -46,15 +48,14 @@ __device__ int incl_scan(int x, int* s_warp, int* total) {
   return r;
 }
 
-__global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P, int l0) {
+__global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P) {
   constexpr int NS = 1024;  // documents whose offsets shared memory holds
   __shared__ int s_bad, s_piece, s_join, s_warp[32], s_cnt[NB], s_off[3][NS + 1];
-  const int l = l0 + blockIdx.x, tid = threadIdx.x, n = P.n_docs, tile = P.tile[l];
+  const int l = blockIdx.x, tid = threadIdx.x, n = P.n_docs, tile = P.tile[l];
   const bool by_key = l == 2, near = n <= NS;
   pdl_wait();
   pdl_release();
   if (!P.list[l]) return;
-  const bool ok = l0 == 0 || (*P.wtag == P.tag && *P.err == KDA_OK);  // (block 0 may not write these before block 1 reads)
   const int32_t *cu = P.cu, *cuk = P.cuk;
   int32_t* pre = P.pre[l];
   if (near) {
@@ -73,13 +74,11 @@ __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P, int l0) {
   for (int i = tid; i < n; i += TT)
     if (cu[i + 1] < cu[i] || cuk[i + 1] < cuk[i]) s_bad = 1;
   __syncthreads();
-  if (tid == 0 && l0 == 0) {
+  if (tid == 0 && l == 0) {
     *P.err = s_bad ? KDA_ERR_BAD_SEQLENS : KDA_OK;
     *P.wtag = P.save && !s_bad ? P.tag : 0;
-  } else if (tid == 0 && s_bad && ok) {  // offsets that changed since the forward (else its words stay)
-    *P.err = KDA_ERR_BAD_SEQLENS;
   }
-  if (s_bad || !ok) {
+  if (s_bad) {
     if (tid == 0) P.counts[l] = 0;
     return;
   }
@@ -439,9 +438,9 @@ cudaError_t launch_join(const SmxP& P, void* o, float* lse, cudaStream_t st) {
   return e;
 }
 
-cudaError_t launch_table(const SmxP& P, int l0, int n, cudaStream_t st) {
+cudaError_t launch_table(const SmxP& P, cudaStream_t st) {
   prof_begin(K_SMX_TABLE, st);
-  const cudaError_t e = launch_pdl(smx_table_kernel, dim3(n), dim3(TT), 0, st, P, l0);
+  const cudaError_t e = launch_pdl(smx_table_kernel, dim3(P.save ? 3 : 1), dim3(TT), 0, st, P);
   prof_end(K_SMX_TABLE, st);
   return e;
 }
@@ -470,7 +469,7 @@ extern "C" KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, cons
   P.save = save_for_backward != 0;
   if (!workspace || workspace_bytes < layout(P, p->D, p->dtype, P.save, workspace)) return KDA_ERR_WORKSPACE;
   if ((uintptr_t)workspace % 256 != 0) return KDA_ERR_ALIGNMENT;
-  if (P.list[0] && launch_table(P, 0, 1, st) != cudaSuccess) return KDA_ERR_CUDA;
+  if ((P.list[0] || P.list[1] || P.list[2]) && launch_table(P, st) != cudaSuccess) return KDA_ERR_CUDA;
   cudaError_t e;
   if (p->dtype == KDA_F32) {
     const float* x[3] = {(const float*)q, (const float*)k, (const float*)v};
@@ -501,7 +500,6 @@ extern "C" KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, cons
     if (!a16(x)) return KDA_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < layout(P, p->D, p->dtype, true, workspace)) return KDA_ERR_WORKSPACE;
   if ((uintptr_t)workspace % 256 != 0) return KDA_ERR_ALIGNMENT;
-  if ((P.list[1] || P.list[2]) && launch_table(P, 1, 2, st) != cudaSuccess) return KDA_ERR_CUDA;
   cudaError_t e;
   if (p->dtype == KDA_F32)
     e = p->D == 64 ? launch_delta<64, float>(P, o, dO, st) : launch_delta<128, float>(P, o, dO, st);

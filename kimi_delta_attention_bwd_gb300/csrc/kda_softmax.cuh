@@ -52,7 +52,8 @@ __host__ __device__ inline int first_query(int causal, int j, int Lq, int Lk) {
   return i < 0 ? 0 : i > Lq ? Lq : i;
 }
 
-// Tile x of list l, the heavy ones first; false past the last.  by_key: the tiles are of keys.
+// Tile x of list l, the heavy ones first; false past the last.  by_key: the tiles are of keys.  The backward's lists are
+// the forward's: none is read from a workspace that another problem's forward filled.
 __device__ __forceinline__ bool tile_of(const SmxP& P, int l, int x, bool by_key, Tile& t) {
   t.j0 = 0;
   t.j1 = INT_MAX;
@@ -67,7 +68,8 @@ __device__ __forceinline__ bool tile_of(const SmxP& P, int l, int x, bool by_key
     t.Lk = P.Tk;
     return true;
   }
-  if (x >= P.counts[l]) return false;
+  const int tag = l > 0 ? *P.wtag : P.tag;
+  if (x >= P.counts[l] || tag != P.tag) return false;
   const int4 a = P.list[l][2 * (size_t)x], b = P.list[l][2 * (size_t)x + 1];
   t.q0 = a.x;
   t.Lq = a.y;

@@ -50,7 +50,7 @@ def kda_softmax_forward(q, k, v, scale: Optional[float] = None, causal: bool = T
                         out: Optional[torch.Tensor] = None):
     """Forward pass.  Returns (o, lse, ctx): lse [B, T, Hq] fp32, the rows'
     log-sums; ctx feeds kda_softmax_backward when save_for_backward is set, which
-    reads o too: leave it as it is until then.  scale: 1/sqrt(D) unless given
+    reads o too: leave it as it is until then (offsets on the device it reads no more).  scale: 1/sqrt(D) unless given
     (> 0).  out: optional preallocated o that shares no memory with the inputs."""
     _dims(q, "q", 4)
     _dims(k, "k", 4)

@@ -625,3 +625,93 @@ def test_a_hybrid_block_trains():
         # the differences' own error: fp32 noise of a sum of B T Hq D terms over 2 h, and a third derivative's h^2
         scale = float(g.norm() * step.norm())
         assert abs(num - want) <= 2e-2 * scale, (n, num, want, scale)
+
+
+# ---------------------------------------------------------------- what a backward takes from its forward
+def _offsets_of(n):
+    return torch.tensor([0] + list(np.cumsum(n)), dtype=torch.int32)
+
+
+# (whole tiles; tiles that the forward, or both passes, cut into pieces)
+BETWEEN = [([100, 0, 1, 199], [100, 0, 1, 199], [1, 198, 100, 1]), ([130, 0, 9, 161], [4000, 10, 9, 1150], [3, 200, 90, 7]),
+           ([3000, 1], [3000, 1], [1, 3000])]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("case", range(len(BETWEEN)))
+def test_offsets_overwritten_between_the_passes(dt, D, case):
+    """One buffer of offsets for every batch, the next batch's in it before this one's backward."""
+    lq, lk, after = BETWEEN[case]
+    x = make(60 + case, lq, lk, 2, 1, D, dt)
+    want = run(x)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO", "cu", "cu_k")}
+    kw = dict(cu_seqlens=d["cu"], cu_seqlens_k=None if x["same"] else d["cu_k"])
+    o, lse, ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"], **kw)
+    d["cu"].copy_(_offsets_of(after))
+    if not x["same"]:
+        d["cu_k"].copy_(d["cu_k"].flip(0).sub(d["cu_k"][-1]).neg())
+    got = dict(o=o, lse=lse, **kda.kda_softmax_backward(ctx, d["dO"]))
+    assert kda.kda_device_status(ctx.workspace) == 0
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("how", ["moved", "recomputed"])
+@pytest.mark.parametrize("own_keys", [False, True])
+def test_offsets_that_live_in_the_step_alone(how, own_keys):
+    """Saved tensors moved to the host, or formed again by a checkpoint, and offsets that the step made and dropped:
+    their memory holds others before the backward."""
+    from torch.utils.checkpoint import checkpoint
+    lq, lk = [100, 0, 1, 199], [100, 20, 31, 349] if own_keys else [100, 0, 1, 199]
+    x = make(64, lq, lk, 4, 2, 64, "bf16")
+    want = run(x)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO")}
+    leaves = [d[n].requires_grad_() for n in ("q", "k", "v")]
+
+    def step(q, k, v):
+        cu, cu_k = x["cu"].cuda(), x["cu_k"].cuda()
+        return kda.softmax_attention(q, k, v, cu_seqlens=cu, cu_seqlens_k=cu_k if own_keys else None)
+    if how == "moved":
+        with torch.autograd.graph.save_on_cpu():
+            o = step(*leaves)
+    else:
+        o = checkpoint(step, *leaves, use_reentrant=False)
+    others = [torch.tensor([0, 300, 300, 300, 300], dtype=torch.int32, device="cuda") for _ in range(64)]
+    for n, g in zip(("dq", "dk", "dv"), torch.autograd.grad(o, leaves, d["dO"])):
+        assert torch.equal(g, want[n]), n
+    assert torch.equal(o, want["o"]) and len(others) == 64
+
+
+@pytest.mark.parametrize("wanted", [0, 1, 2])
+def test_one_gradient_alone(wanted):
+    x = make(65, [70, 130], [70, 130], 4, 2, 64, "bf16")
+    want = run(x)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO", "cu")}
+    args = [d[n] for n in ("q", "k", "v")]
+    args[wanted].requires_grad_()
+    o = kda.softmax_attention(*args, cu_seqlens=d["cu"])
+    assert torch.equal(torch.autograd.grad(o, args[wanted], d["dO"])[0], want[("dq", "dk", "dv")[wanted]])
+
+
+def test_a_graph_s_backward_follows_its_own_forward_s_offsets():
+    """The two passes captured apart; the forward replayed on other offsets, the buffer overwritten, the backward
+    replayed."""
+    xs = [make(66, [150, 150], [150, 150], 4, 2, 64, "bf16"), make(67, [20, 280], [20, 280], 4, 2, 64, "bf16")]
+    want = [run(x) for x in xs]
+    d = {n: xs[0][n].cuda() for n in ("q", "k", "v", "dO", "cu")}
+    kda.kda_softmax_backward(kda.kda_softmax_forward(d["q"], d["k"], d["v"], cu_seqlens=d["cu"])[2], d["dO"])
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    with torch.cuda.graph(graphs[0]):
+        o, lse, ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"], cu_seqlens=d["cu"])
+    with torch.cuda.graph(graphs[1]):
+        got = dict(o=o, lse=lse, **kda.kda_softmax_backward(ctx, d["dO"]))
+    for x, w in zip(xs, want):
+        for n in d:
+            d[n].copy_(x[n])
+        graphs[0].replay()
+        d["cu"].copy_(torch.tensor([0, 77, 300], dtype=torch.int32))
+        graphs[1].replay()
+        for n in got:
+            assert torch.equal(got[n], w[n]), n
