@@ -51,6 +51,7 @@ __device__ int incl_scan(int x, int* s_warp, int* total) {
 __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P) {
   constexpr int NS = 1024;  // documents whose offsets shared memory holds
   __shared__ int s_bad, s_piece, s_join, s_warp[32], s_cnt[NB], s_off[3][NS + 1];
+  __shared__ unsigned long long s_blocks;
   const int l = blockIdx.x, tid = threadIdx.x, n = P.n_docs, tile = P.tile[l];
   const bool by_key = l == 2, near = n <= NS;
   pdl_wait();
@@ -91,38 +92,24 @@ __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P) {
     carry += total;
   }
   for (int b = tid; b < NB; b += TT) s_cnt[b] = 0;
-  if (tid == 0) s_piece = s_join = 0;
+  if (tid == 0) s_piece = s_join = 0, s_blocks = 0;
   __syncthreads();
   const int xb = P.xb[l], H = by_key ? P.Hkv : P.Hq;
-  struct Found {
-    int4 doc;
-    int t, nb;  // tile of the document; its blocks of the other side
-  };
-  auto find = [&](int x) -> Found {  // tile x in the documents' order
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= x) lo = mid;
-      else hi = mid - 1;
-    }
-    Found f;
-    f.t = x - pre[lo];
-    f.doc = make_int4(cu[lo], cu[lo + 1] - cu[lo], cuk[lo], cuk[lo + 1] - cuk[lo]);
-    f.nb = blocks_of(by_key, P.causal, f.t, tile, xb, P.G, f.doc.y, f.doc.w);
-    return f;
-  };
+  const Tiles tiles{cu, cuk, pre, n, tile, xb, P.G, P.causal, by_key};
   const bool may_cut = P.target[l] > 0;
-  int per = INT_MAX / 2;  // blocks a piece
+  int64_t per = 0;  // blocks a piece
   if (may_cut) {
-    int blocks = 0, total;
-    for (int x = tid; x < carry; x += TT) blocks += find(x).nb;
-    incl_scan(blocks, s_warp, &total);
-    per = max(512 / xb, (int)(((int64_t)total * H + P.target[l] - 1) / P.target[l]));
+    int64_t blocks = tiles.blocks(tid, carry, TT);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
+    if (tid % 32 == 0) atomicAdd(&s_blocks, (unsigned long long)blocks);
+    __syncthreads();
+    per = piece_blocks((int64_t)s_blocks, H, P.target[l], xb);
   }
-  auto pieces_of = [&](const Found& f) { return may_cut && f.nb > per + per / 2 ? (f.nb + per - 1) / per : 1; };
-  auto bucket = [&](const Found& f, int np) { return NB - 1 - min(NB - 1, f.nb / np); };
+  auto pieces_of = [&](const Tiles::Found& f) { return may_cut ? pieces_in(f.nb, per) : 1; };
+  auto bucket = [&](const Tiles::Found& f, int np) { return NB - 1 - min(NB - 1, f.nb / np); };
   for (int x = tid; x < carry; x += TT) {
-    const Found f = find(x);
+    const Tiles::Found f = tiles.find(x);
     const int np = pieces_of(f);
     atomicAdd(&s_cnt[bucket(f, np)], np);
   }
@@ -135,10 +122,10 @@ __global__ void __launch_bounds__(TT) smx_table_kernel(SmxP P) {
   }
   __syncthreads();
   for (int x = tid; x < carry; x += TT) {
-    const Found f = find(x);
+    const Tiles::Found f = tiles.find(x);
     const int np = pieces_of(f), at = atomicAdd(&s_cnt[bucket(f, np)], np);
     int first = -1;
-    if (np > 1) {  // (the room is the bound that the host forms from the same rule)
+    if (np > 1) {  // (there is room: piece_room)
       first = atomicAdd(&s_piece, np);
       const int j = atomicAdd(&s_join, 1), i0 = f.t * tile;
       P.joins[l][j] = by_key ? make_int4(f.doc.z + i0, min(tile, f.doc.w - i0), first, np)
@@ -283,9 +270,7 @@ bool worth_cutting(const SmxP& P, int l) {
     total += nb;
     most = nb > most ? nb : most;
   }
-  int64_t per = (total * P.B * (l == 2 ? P.Hkv : P.Hq) + P.target[l] - 1) / P.target[l];
-  if (per < 512 / P.xb[l]) per = 512 / P.xb[l];
-  return most > per + per / 2;
+  return pieces_in(most, piece_blocks(total * P.B, l == 2 ? P.Hkv : P.Hq, P.target[l], P.xb[l])) > 1;
 }
 
 bool offsets_ok(const int32_t* c, int n, int64_t end) {
@@ -349,8 +334,7 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
     if ((int64_t)max_tiles(P, l) * H <= 4 * wave && (int64_t)other * (l == 2 ? P.G : 1) > 1024 &&
         (!P.rows || P.B <= 1024)) {
       P.target[l] = wave;
-      // a tile of q > 1.5 average loads has ceil(q) pieces, at most 1.5 q, and all tiles' q sum to at most target / H
-      P.pieces[l] = (wave + H - 1) / H * 3 / 2 + 2;
+      P.pieces[l] = piece_room(wave, H);
       if (P.rows && !worth_cutting(P, l)) P.target[l] = P.pieces[l] = 0;
     }
   }

@@ -89,6 +89,46 @@ __host__ __device__ inline int blocks_of(bool by_key, int causal, int t, int til
   return (keys_of(causal, end - 1, Lq, Lk) + xb - 1) / xb;
 }
 
+// The tiles of a list in the documents' order: offsets, the documents' first tiles.
+struct Tiles {
+  const int32_t *cu, *cuk, *pre;
+  int n, tile, xb, G, causal;  // n: documents
+  bool by_key;
+  struct Found {
+    int4 doc;
+    int t, nb;  // tile of the document; its blocks of the other side
+  };
+  __host__ __device__ Found find(int x) const {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    Found f;
+    f.t = x - pre[lo];
+    f.doc = make_int4(cu[lo], cu[lo + 1] - cu[lo], cuk[lo], cuk[lo + 1] - cuk[lo]);
+    f.nb = blocks_of(by_key, causal, f.t, tile, xb, G, f.doc.y, f.doc.w);
+    return f;
+  }
+  // Blocks of tiles first, first + step, .. below end: 600 tiles of millions of blocks pass 32 bits.
+  __host__ __device__ int64_t blocks(int first, int end, int step) const {
+    int64_t sum = 0;
+    for (int x = first; x < end; x += step) sum += find(x).nb;
+    return sum;
+  }
+};
+// Blocks of a piece: the load that `target` CTAs have on average of a list's blocks with H heads, 512 rows at least.
+__host__ __device__ inline int64_t piece_blocks(int64_t blocks, int H, int target, int xb) {
+  const int64_t per = (blocks * H + target - 1) / target, least = 512 / xb;
+  return per > least ? per : least;
+}
+// Pieces of a tile of nb blocks: one up to 1.5 times that load.
+__host__ __device__ inline int pieces_in(int nb, int64_t per) { return nb > per + per / 2 ? (int)((nb + per - 1) / per) : 1; }
+// Room for the pieces of all cut tiles: a tile of q > 1.5 loads has ceil(q) pieces, at most 1.5 q, and all tiles' q sum to
+// at most target / H.
+__host__ __device__ inline int piece_room(int target, int H) { return (target + H - 1) / H * 3 / 2 + 2; }
+
 // The backward's kernels read only what a forward of the same problem saved.
 __device__ __forceinline__ bool saved(const SmxP& P) {
   if (*P.wtag == P.tag && *P.err == KDA_OK) return true;
