@@ -34,7 +34,8 @@ class SoftmaxContext:
     host: tuple
     workspace: torch.Tensor
     saved: bool
-    stream: Optional[int] = None  # the workspace's, where the forward allocated it
+    stream: Optional[int] = None  # the forward's
+    own: tuple = ()               # of what the backward reads, that the forward allocated there
 
 
 def _offsets(cu, name):
@@ -94,19 +95,22 @@ def kda_softmax_forward(q, k, v, scale: Optional[float] = None, causal: bool = T
         raise ValueError(f"scale must be positive, got {scale}")
     prob = _lib.make_softmax_problem(B, T, Tk, Hq, Hkv, D, io, scale, causal, cu_seqlens, cu_seqlens_k,
                                      cu_seqlens_host, cu_seqlens_k_host)
-    stream = None
+    stream, own = _lib._stream(), ()
     if workspace is None:
-        stream = _lib._stream()
         # (size 0 for a problem that the call below refuses with its own status)
         workspace = torch.empty(_lib.kda_softmax_workspace_size(prob, save_for_backward) or 1, dtype=torch.uint8,
                                 device=q.device)
+        own = (workspace,)
     else:
         _require(workspace=(workspace, workspace.shape, torch.uint8))
-    o = out if out is not None else torch.empty_like(q)
+    o = out
+    if o is None:
+        o = torch.empty_like(q)
+        own += (o,)
     lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
     _lib.kda_softmax_fwd(prob, q, k, v, o, lse, save_for_backward, workspace)
     return o, lse, SoftmaxContext(prob, q, k, v, o, cu_seqlens, cu_seqlens_k, (cu_seqlens_host, cu_seqlens_k_host),
-                                  workspace, bool(save_for_backward), stream)
+                                  workspace, bool(save_for_backward), stream, own)
 
 
 def kda_softmax_backward(ctx: SoftmaxContext, dO):
@@ -122,7 +126,8 @@ def kda_softmax_backward(ctx: SoftmaxContext, dO):
     g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(ctx.v)}
     if ctx.stream is not None and ctx.stream != _lib._stream():
         # a context dropped after this call must not give its memory to the forward's stream before the kernels end
-        ctx.workspace.record_stream(torch.cuda.current_stream())
+        for t in ctx.own:
+            t.record_stream(torch.cuda.current_stream())
     _lib.kda_softmax_bwd(ctx.problem, q, k, ctx.v, ctx.o, dO, g["dq"], g["dk"], g["dv"], ctx.workspace)
     return g
 

@@ -715,3 +715,27 @@ def test_a_graph_s_backward_follows_its_own_forward_s_offsets():
         graphs[1].replay()
         for n in got:
             assert torch.equal(got[n], w[n]), n
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_context_dropped_while_another_stream_s_backward_runs(given):
+    """What the forward allocated and the backward reads (workspace and o, or o alone) is not handed out on the forward's
+    stream before that backward has ended (only addresses are compared: nothing is written over it)."""
+    x = make(68, [300, 200], [300, 200], 4, 2, 64, "bf16")
+    want = run(x)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO", "cu")}
+    ws = kda.kda_softmax_forward(d["q"], d["k"], d["v"], cu_seqlens=d["cu"])[2].workspace if given else None
+    other = torch.cuda.Stream()
+    o, _, ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"], cu_seqlens=d["cu"], workspace=ws)
+    kept = [(t.data_ptr(), t.numel() * t.element_size()) for t in ((o,) if given else (o, ctx.workspace))]
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(100_000_000)  # about 50 ms: the backward waits behind it
+        got = kda.kda_softmax_backward(ctx, d["dO"])
+    del ctx, o, _
+    for at, size in kept:
+        blocks = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert all(not at - size < b.data_ptr() < at + size for b in blocks)
+    other.synchronize()
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
