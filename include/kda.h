@@ -500,7 +500,8 @@ KDA_API kda_status kda_softmax_fwd(const kda_softmax_problem* p, const void* q, 
 
 /* Backward of sum(o * dO): dq [B, T, Hq, D], dk, dv [B, Tk, Hkv, D] (dtype),
  * from the forward's inputs, its o and its workspace (another one is refused by
- * the device: KDA_ERR_WORKSPACE from kda_device_status).  The documents are those that
+ * the device: KDA_ERR_WORKSPACE from kda_device_status, and gradients of NaN, as after a
+ * forward that the device refused or ended with an error).  The documents are those that
  * the forward left in the workspace: cu_seqlens and cu_seqlens_k say only that there
  * are offsets, the device memory they point to is not read and may be gone or hold others.  dk and dv are summed over
  * the heads of a group and over the queries by one CTA, or by a few whose sums are

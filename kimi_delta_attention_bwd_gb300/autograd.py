@@ -192,7 +192,8 @@ class _SoftmaxAttention(torch.autograd.Function):
 def softmax_attention(q, k, v, scale: Optional[float] = None, causal: bool = True, cu_seqlens=None, cu_seqlens_k=None,
                       cu_seqlens_host=None, cu_seqlens_k_host=None):
     """Differentiable softmax attention: o from the layouts of
-    kda_softmax_forward; gradients to q, k and v through kda_softmax_backward."""
+    kda_softmax_forward; gradients to q, k and v through kda_softmax_backward
+    (NaN where offsets that only the device knows are wrong)."""
     return _SoftmaxAttention.apply(q, k, v, scale, causal, cu_seqlens, cu_seqlens_k, cu_seqlens_host,
                                    cu_seqlens_k_host, torch.is_grad_enabled())
 

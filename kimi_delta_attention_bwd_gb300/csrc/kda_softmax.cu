@@ -217,12 +217,25 @@ __global__ void __launch_bounds__(256) smx_join_grads_kernel(SmxP P, T* __restri
 // delta_i = sum_d o_i dO_i per row (token, head), D / 8 threads a row.  With bf16
 // io o is the stored output plus what its rounding left: delta is subtracted from
 // dO v, and a rounded o would put a further rounding's error into every gradient.
+// A backward that is refused (its workspace holds no forward of this problem) gets NaN gradients here: nothing after this
+// kernel writes any.
+template <typename T>
+__device__ void fill_nan(T* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+    stf(p + i, __int_as_float(0x7fffffff));
+}
 template <int D, typename T>
-__global__ void __launch_bounds__(256) smx_delta_kernel(SmxP P, const T* __restrict__ o, const T* __restrict__ dO) {
+__global__ void __launch_bounds__(256) smx_delta_kernel(SmxP P, const T* __restrict__ o, const T* __restrict__ dO,
+                                                       T* __restrict__ dq, T* __restrict__ dk, T* __restrict__ dv) {
   constexpr int TR = D / 8;
   pdl_wait();
   pdl_release();
-  if (!saved(P)) return;
+  if (!saved(P)) {
+    fill_nan(dq, (int64_t)P.Nq * P.Hq * D);
+    fill_nan(dk, (int64_t)P.Nk * P.Hkv * D);
+    fill_nan(dv, (int64_t)P.Nk * P.Hkv * D);
+    return;
+  }
   const int64_t row = (int64_t)blockIdx.x * (256 / TR) + threadIdx.x / TR;
   const bool in = row < (int64_t)P.Nq * P.Hq;
   float s = 0.f;
@@ -393,12 +406,12 @@ size_t layout(SmxP& P, int D, int dtype, bool bwd, void* base) {
 }
 
 template <int D, typename T>
-cudaError_t launch_delta(const SmxP& P, const void* o, const void* dO, cudaStream_t st) {
+cudaError_t launch_delta(const SmxP& P, const void* o, const void* dO, void* dq, void* dk, void* dv, cudaStream_t st) {
   const int64_t rows = (int64_t)P.Nq * P.Hq, per = 256 / (D / 8), grid = (rows + per - 1) / per;
   if (grid > 2147483647) return cudaErrorInvalidValue;
   prof_begin(K_SMX_DELTA, st);
   const cudaError_t e = launch_pdl(smx_delta_kernel<D, T>, dim3((unsigned)grid), dim3(256), 0, st, P, (const T*)o,
-                                   (const T*)dO);
+                                   (const T*)dO, (T*)dq, (T*)dk, (T*)dv);
   prof_end(K_SMX_DELTA, st);
   return e;
 }
@@ -486,9 +499,9 @@ extern "C" KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, cons
   if ((uintptr_t)workspace % 256 != 0) return KDA_ERR_ALIGNMENT;
   cudaError_t e;
   if (p->dtype == KDA_F32)
-    e = p->D == 64 ? launch_delta<64, float>(P, o, dO, st) : launch_delta<128, float>(P, o, dO, st);
+    e = p->D == 64 ? launch_delta<64, float>(P, o, dO, dq, dk, dv, st) : launch_delta<128, float>(P, o, dO, dq, dk, dv, st);
   else
-    e = p->D == 64 ? launch_delta<64, bf16>(P, o, dO, st) : launch_delta<128, bf16>(P, o, dO, st);
+    e = p->D == 64 ? launch_delta<64, bf16>(P, o, dO, dq, dk, dv, st) : launch_delta<128, bf16>(P, o, dO, dq, dk, dv, st);
   if (e != cudaSuccess) return KDA_ERR_CUDA;
   if (p->dtype == KDA_BF16) {
     e = launch_tc_bwd(P, p->D, 1, q, k, v, dO, dq, dk, dv, st);

@@ -115,7 +115,8 @@ def kda_softmax_forward(q, k, v, scale: Optional[float] = None, causal: bool = T
 
 def kda_softmax_backward(ctx: SoftmaxContext, dO):
     """Backward of sum(o * dO): a dict with dq, dk, dv in the io dtype.  Sums run
-    in a fixed order."""
+    in a fixed order.  NaN where the device refused the forward's offsets, or the
+    workspace (kda_device_status says which)."""
     if not ctx.saved:
         raise ValueError("the forward saved nothing: call kda_softmax_forward with save_for_backward=True")
     q, k = ctx.q, ctx.k

@@ -739,3 +739,30 @@ def test_a_context_dropped_while_another_stream_s_backward_runs(given):
     other.synchronize()
     for n in got:
         assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_refused_backward_s_gradients_are_not_numbers(dt, D):
+    """Offsets that the device refused, and workspaces that other problems' forwards saved: rows and packed, more and
+    fewer documents, with cut tiles and without."""
+    x = make(69, [30, 40], [30, 40], 4, 2, D, dt)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO", "cu")}
+    bad = torch.tensor([0, 80, 70], dtype=torch.int32, device="cuda")
+    leaves = [d[n].detach().requires_grad_() for n in ("q", "k", "v")]
+    o = kda.softmax_attention(*leaves, cu_seqlens=bad)
+    for g in torch.autograd.grad(o, leaves, d["dO"]):
+        assert torch.isnan(g).all()
+    y = make(70, [1] * 9 + [700, 1500], [1] * 9 + [700, 1500], 4, 2, D, dt)
+    e = {n: y[n].cuda() for n in ("q", "k", "v", "dO", "cu")}
+    short, long = (lambda: kda.kda_softmax_forward(d["q"], d["k"], d["v"], cu_seqlens=d["cu"])[2],
+                   lambda **kw: kda.kda_softmax_forward(e["q"], e["k"], e["v"], **kw)[2])
+    for ctx, other, dO in ((short(), long(cu_seqlens=e["cu"]), d["dO"]), (short(), long(), d["dO"]),
+                           (long(), long(cu_seqlens=e["cu"]), e["dO"]), (long(cu_seqlens=e["cu"]), long(), e["dO"]),
+                           (long(cu_seqlens=e["cu"]), long(cu_seqlens=e["cu"], causal=False), e["dO"])):
+        ws = torch.zeros(max(ctx.workspace.numel(), other.workspace.numel()), dtype=torch.uint8, device="cuda")
+        ws[:other.workspace.numel()] = other.workspace
+        ctx.workspace = ws
+        for n, g in kda.kda_softmax_backward(ctx, dO).items():
+            assert torch.isnan(g).all(), n
+        assert kda.kda_device_status(ws) == -5
