@@ -486,8 +486,10 @@ typedef struct kda_softmax_problem {
  * are exact zeros of a matrix product, so an infinity or NaN in a value also
  * reaches its document's queries up to 255 before it, never another document's.
  * Precision: logits, maxima, sums and o are accumulated in fp32.  With bf16 io the
- * weights (and, in the backward, their gradients) enter their products as bf16, in
- * two parts (2^-16) in short documents of small problems.  With fp32 io every operand
+ * weights (and, in the backward, their gradients) enter their products as bf16 (in the
+ * 2-norm o is then off by up to 1.3 times what rounding the exact one to bf16 gives, the
+ * gradients by up to 1.5 times), in two parts (2^-16) in documents of at most 64 rows on
+ * a kernel's own side (queries; keys for dk and dv) or 256 on the other.  With fp32 io every operand
  * enters as three bf16 parts (2^-24 together); values whose bf16 rounding is
  * finite (below 3.39e38).
  * The results of a call depend on its inputs alone and repeat to the bit.  A batch

@@ -332,9 +332,6 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   P.causal = p->causal;
   P.scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D);
   P.scale2 = P.scale * LOG2E;
-  // Two-part operands for its short documents: where the result's roundings are too few to average out.  In a large
-  // packed batch they do, and short documents' second products are seen (300M step, 16384 rows: 218 against 226 us).
-  P.few = (P.Nq < P.Nk ? P.Nq : P.Nk) <= 1024;
   const int parts = p->dtype == KDA_F32 ? 3 : 1;
   for (int l = 0; l < 3; l++) P.tile[l] = tc_tile(p->D, parts, l);
   // Cut tiles: where whole tiles would be fewer than four for each of 152 SMs, and some could have more than a few

@@ -15,7 +15,7 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct SmxP {
   int Nq, Nk, B, T, Tk, Hq, Hkv, G, n_docs, causal, rows;  // rows: documents are the rows of T queries, Tk keys
-  int save, tag, few;  // few: a small problem, whose short documents' operands take two parts
+  int save, tag;
   float scale, scale2;  // scale2 = scale log2(e): exponentials are powers of two
   const int32_t *cu, *cuk;
   int32_t *err, *wtag, *counts;  // counts[l]: entries of list l; counts[3 + l]: its cut tiles

@@ -10,9 +10,11 @@
 // Weights are rounded to bf16 (2^-8, the operand's type; o's error with that is that of one rounding of o times
 // sqrt(2)), but in a first block that a mask cuts they enter as two parts (2^-16): rows with few keys have theirs there,
 // and the backward's delta = o dO cancels against dO v in just those rows.  Documents
-// of few rows, or against few of the other side (FEW_ROWS, FEW), take two parts throughout, in the backward too, where
-// the whole problem is small (SmxP::few): a handful of roundings does not average out (up to 1.8 times the error of
-// weights that are multiplied in fp32 and a result rounded once; with two parts 1.5).
+// of few rows, or against few of the other side (FEW_ROWS, FEW), take two parts throughout, in the backward too: a handful
+// of roundings does not average out (up to 1.8 times the error of weights that are multiplied in fp32 and a result rounded
+// once; with two parts 1.5).  The rule looks at the document alone, whatever batch it stands in, and that costs batches of
+// short ones up to 12% (training steps of 64 rows of 256, 8 heads of 64: 101 us with one part, 113 with two; 100 documents
+// of 164, 16 heads on 4 of 128: 428 and 474; 256 documents of 64, 8 heads of 64: 156 and 159).
 #include "kda_softmax_tc.cuh"
 
 #include <type_traits>
@@ -113,7 +115,7 @@ smx_tc_fwd_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
   if (live) {
     i0 = t.t * (NT * BLK);
     nq = min(NT * BLK, t.Lq - i0);
-    twice = PARTS == 1 && P.few && (t.Lq <= FEW_ROWS || t.Lk <= FEW);
+    twice = PARTS == 1 && (t.Lq <= FEW_ROWS || t.Lk <= FEW);
 #pragma unroll
     for (int i = 0; i < NT; i++)
       if (i * BLK < nq) {
@@ -575,7 +577,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
     first = first_query(P.causal, j0, t.Lq, t.Lk) / XB;
     per = max(0, (t.Lq + XB - 1) / XB - first);
   }
-  const bool twice = PARTS == 1 && P.few && live && (t.Lk <= FEW_ROWS || t.Lq <= FEW);
+  const bool twice = PARTS == 1 && live && (t.Lk <= FEW_ROWS || t.Lq <= FEW);
   const int n = live ? min(per * P.G, t.j1) - t.j0 : 0;
   tc::fence_before();
   __syncthreads();
@@ -842,7 +844,7 @@ smx_tc_dq_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_co
   if (live) {
     i0 = t.t * BLK;
     nq = min(BLK, t.Lq - i0);
-    twice = PARTS == 1 && P.few && (t.Lq <= FEW_ROWS || t.Lk <= FEW);
+    twice = PARTS == 1 && (t.Lq <= FEW_ROWS || t.Lk <= FEW);
     n = min((keys_of(P.causal, i0 + nq - 1, t.Lq, t.Lk) + XB - 1) / XB, t.j1) - t.j0;
     clean = keys_of(P.causal, i0, t.Lq, t.Lk) / XB;
   }

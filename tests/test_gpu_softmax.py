@@ -766,3 +766,30 @@ def test_a_refused_backward_s_gradients_are_not_numbers(dt, D):
         for n, g in kda.kda_softmax_backward(ctx, dO).items():
             assert torch.isnan(g).all(), n
         assert kda.kda_device_status(ws) == -5
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,rows", [([50, 1, 64, 256, 200, 2, 40, 255] * 3, False), ([64] * 20, True), ([256] * 5, True)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_short_documents_of_large_problems_take_two_parts_too(D, lens, rows, causal):
+    """The operands' parts follow the document, not the batch that it stands in."""
+    assert sum(lens) > 1024
+    x = make(71, lens, lens, 4, 2, D, "bf16", rows=rows)
+    check(run(x, causal), oracle(x, causal), "bf16", D, x, op=2.0 ** -16)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_each_document_of_a_large_problem_is_near_its_rounding(D):
+    """The bound of test_bf16_outputs_are_near_their_rounding, for every document (of two tokens at least: one alone has
+    o = v and no gradients of q and k) by itself."""
+    lens = [2, 8, 33, 64, 65, 129, 200, 256, 257, 300, 700, 16, 100]
+    x = make(72, lens, lens, 8, 4, D, "bf16")
+    got, (ref, _, _) = run(x), oracle(x)
+    at = np.cumsum([0] + lens)
+    for n in ("o", "dq", "dk", "dv"):
+        g = got[n].double().cpu().numpy().reshape(ref[n].shape)
+        for a, b in zip(at[:-1], at[1:]):
+            r = ref[n][a:b]
+            rounded = torch.from_numpy(r).to(torch.bfloat16).double().numpy()
+            off = np.linalg.norm(g[a:b] - r) / np.linalg.norm(rounded - r)
+            assert off <= 1.5, (n, b - a, off)
