@@ -52,7 +52,8 @@ def kda_softmax_forward(q, k, v, scale: Optional[float] = None, causal: bool = T
     """Forward pass.  Returns (o, lse, ctx): lse [B, T, Hq] fp32, the rows'
     log-sums; ctx feeds kda_softmax_backward when save_for_backward is set, which
     reads o too: leave it as it is until then (offsets on the device it reads no more).  scale: 1/sqrt(D) unless given
-    (> 0).  out: optional preallocated o that shares no memory with the inputs."""
+    (> 0).  out: optional preallocated o that shares no memory with the inputs or
+    with a given workspace, which shares none with them either."""
     _dims(q, "q", 4)
     _dims(k, "k", 4)
     qs = q.shape
@@ -90,7 +91,9 @@ def kda_softmax_forward(q, k, v, scale: Optional[float] = None, causal: bool = T
     if not _all_well(*specs):
         _require(**dict(zip(names, specs)))
     if out is not None:
-        _apart("out", out, q=q, k=k, v=v)
+        _apart("out", out, q=q, k=k, v=v, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k)
+    if workspace is not None:
+        _apart("workspace", workspace, q=q, k=k, v=v, out=out, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k)
     if scale is not None and not scale > 0:
         raise ValueError(f"scale must be positive, got {scale}")
     prob = _lib.make_softmax_problem(B, T, Tk, Hq, Hkv, D, io, scale, causal, cu_seqlens, cu_seqlens_k,
@@ -141,7 +144,8 @@ def kda_softmax_decode_step(q, k, v, k_cache, v_cache, lengths, scale: Optional[
     them all and its own; lengths stays as it is (the layers of a model share it).
     A negative length takes no step (o = 0, a padded batch), and neither does one
     of cap or more (kda_device_status of a given workspace reports it).  out shares
-    no memory with the inputs, nor do the caches with each other or with k and v.
+    no memory with the inputs, nor do the caches with each other or with the other
+    inputs, nor a given workspace with any of them.
     Returns o [n, Hq, D]."""
     _dims(q, "q", 3)
     _dims(k_cache, "k_cache", 4)
@@ -162,15 +166,17 @@ def kda_softmax_decode_step(q, k, v, k_cache, v_cache, lengths, scale: Optional[
     # the caches share no memory with the other tensors or with each other (the named checks say which)
     kc, vc, size = k_cache.data_ptr(), v_cache.data_ptr(), k_cache.numel() * k_cache.element_size()
     near = kc < vc + size and vc < kc + size
-    for t in (q, k, v):
+    for t in (q, k, v, lengths):
         a = t.data_ptr()
         b = a + t.numel() * t.element_size()
         near = near or (a < kc + size and kc < b) or (a < vc + size and vc < b)
     if near:
-        _apart("k_cache", k_cache, q=q, k=k, v=v, v_cache=v_cache)
-        _apart("v_cache", v_cache, q=q, k=k, v=v)
+        _apart("k_cache", k_cache, q=q, k=k, v=v, lengths=lengths, v_cache=v_cache)
+        _apart("v_cache", v_cache, q=q, k=k, v=v, lengths=lengths)
     if out is not None:
-        _apart("out", out, q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache)
+        _apart("out", out, q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, lengths=lengths)
+    if workspace is not None:
+        _apart("workspace", workspace, q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, lengths=lengths, out=out)
     if scale is not None and not scale > 0:
         raise ValueError(f"scale must be positive, got {scale}")
     if workspace is None:

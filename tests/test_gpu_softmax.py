@@ -793,3 +793,49 @@ def test_each_document_of_a_large_problem_is_near_its_rounding(D):
             rounded = torch.from_numpy(r).to(torch.bfloat16).double().numpy()
             off = np.linalg.norm(g[a:b] - r) / np.linalg.norm(rounded - r)
             assert off <= 1.5, (n, b - a, off)
+
+
+def test_outputs_and_workspaces_that_overlap_are_refused():
+    from kimi_delta_attention_bwd_gb300 import _lib
+    x = make(73, [30, 40], [30, 40], 2, 2, 64, "f32")
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO")}
+    n = d["q"].numel()
+    both = torch.zeros(2 * n, dtype=torch.int32, device="cuda")
+    out = both[:n].view(torch.float32).view_as(d["q"])
+    for i in (0, n - 3):
+        both[i:i + 3] = x["cu"]
+        with pytest.raises(ValueError, match="out overlaps cu_seqlens"):
+            kda.kda_softmax_forward(d["q"], d["k"], d["v"], cu_seqlens=both[i:i + 3], out=out)
+    cu = both[n:n + 3]  # (right behind it: taken)
+    cu.copy_(x["cu"])
+    with pytest.raises(ValueError, match="out overlaps cu_seqlens_k"):
+        kda.kda_softmax_forward(d["q"], d["k"], d["v"], cu_seqlens=cu, cu_seqlens_k=both[:3], out=out)
+    o, _, ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"], cu_seqlens=cu, out=out)
+    assert o is out
+    size = ctx.workspace.numel()
+    ws = torch.zeros(size + 4 * n, dtype=torch.uint8, device="cuda")
+    inside = ws[size:].view(torch.float32).view_as(d["q"])
+    for name, kw in (("q", dict(q=inside)), ("k", dict(k=inside)), ("v", dict(v=inside)), ("out", dict(out=inside)),
+                     ("cu_seqlens", dict(cu_seqlens=ws[size - 12:size].view(torch.int32)))):
+        a = dict(q=d["q"], k=d["k"], v=d["v"], cu_seqlens=cu)
+        a.update(kw)
+        with pytest.raises(ValueError, match=f"workspace overlaps {name}"):
+            kda.kda_softmax_forward(**a, workspace=ws[:size + 256])
+    kda.kda_softmax_forward(inside, d["k"], d["v"], cu_seqlens=cu, workspace=ws[:size])
+
+    t = {m: u.cuda() for m, u in decode_case(74, [3, 7], 16, 2, 2, 64, "f32").items()}
+    step = lambda **kw: kda.kda_softmax_decode_step(*({**t, **kw}[m] for m in ("q", "k", "v", "k_cache", "v_cache", "lengths")),  # noqa: E731
+                                                    **{m: u for m, u in kw.items() if m in ("out", "workspace")})
+    size = _lib.kda_softmax_decode_workspace_size(2, 16, 2, 2, 64)
+    ws = torch.zeros(size + 4 * t["k_cache"].numel(), dtype=torch.uint8, device="cuda")
+    wide, small = ws[size:].view(torch.float32), t["k_cache"].view(-1)
+    for match, kw in (("workspace overlaps k_cache", dict(k_cache=wide.view_as(t["k_cache"]), workspace=ws[:size + 256])),
+                      ("workspace overlaps q", dict(q=wide[:256].view_as(t["q"]), workspace=ws[:size + 256])),
+                      ("workspace overlaps out", dict(out=wide[:256].view_as(t["q"]), workspace=ws[:size + 256])),
+                      ("workspace overlaps lengths", dict(lengths=wide[:2].view(torch.int32), workspace=ws[:size + 256])),
+                      ("out overlaps lengths", dict(out=wide[:256].view_as(t["q"]), lengths=wide[254:256].view(torch.int32))),
+                      ("k_cache overlaps lengths", dict(lengths=small[-2:].view(torch.int32))),
+                      ("v_cache overlaps lengths", dict(lengths=t["v_cache"].view(-1)[:2].view(torch.int32)))):
+        with pytest.raises(ValueError, match=match):
+            step(**kw)
+    step(q=wide[:256].view_as(t["q"]), workspace=ws[:size])
