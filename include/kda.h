@@ -456,7 +456,7 @@ KDA_API kda_status kda_layer_norm_bwd(int64_t n_rows, int D, int dtype, const vo
  *  B, T, Tk  : rows, queries per row, keys per row.
  *  D         : head dim of q, k, v and o: 64 or 128.
  *  dtype     : kda_dtype of q, k, v, o and their gradients.
- *  scale     : <= 0 selects 1/sqrt(D).
+ *  scale     : <= 0 selects 1/sqrt(D); finite.
  *  cu_seqlens, n_docs: DEVICE int32 [n_docs + 1] offsets of the documents'
  *              queries in the flattened B*T axis, or NULL: the rows.
  *  cu_seqlens_k: the same for their keys in the flattened B*Tk axis; NULL (only
@@ -532,7 +532,7 @@ KDA_API kda_status kda_softmax_decode(int n_seq, int cap, int Hq, int Hkv, int D
 /* Rotary positions of q [n_tok, Hq, D] and k [n_tok, Hkv, D] (Hkv = 0: q alone):
  * the first rot values of every head (even, <= D <= 1024) in pairs, value i with value
  * i + rot/2 (interleaved = 0) or 2 i with 2 i + 1 (interleaved = 1), each
- * turned by w = position * inv_freq[i] and multiplied by scale (<= 0: 1):
+ * turned by w = position * inv_freq[i] and multiplied by scale (<= 0: 1; finite):
  *   (a, b) -> scale (a cos w - b sin w, b cos w + a sin w);
  * inverse = 1 turns by -w (the gradients' way back, with the same scale).  The
  * other values pass.  inv_freq : [rot/2] fp32, taken as exact: the angle is

@@ -33,6 +33,8 @@ the flattened B*T tokens; states [n_docs, H, dk, dv] fp32.
 """
 from __future__ import annotations
 
+import ctypes
+import math
 from dataclasses import dataclass
 from typing import Optional
 
@@ -126,6 +128,13 @@ def _apart(name, out, may_be=(), /, **inputs):
             continue
         if other not in may_be or t.data_ptr() != a or t.shape != out.shape:
             raise ValueError(f"{name} overlaps {other}")
+
+
+def _positive(scale, name="scale"):
+    """A given factor is a positive fp32 number: the C interface takes one, and one that vanishes there would
+    select the default."""
+    if not 0.0 < ctypes.c_float(scale).value < math.inf:
+        raise ValueError(f"{name} must be positive and finite in fp32, got {scale}")
 
 
 def _gate_of(f, dt_bias, qshape):

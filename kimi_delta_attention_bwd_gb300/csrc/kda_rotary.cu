@@ -170,7 +170,7 @@ extern "C" KDA_API kda_status kda_rotary(int64_t n_tok, int64_t T, int Hq, int H
   if (n_tok <= 0 || n_tok > ((int64_t)1 << 31) - 1 || Hq <= 0 || Hkv < 0 || Hq > 4096 || Hkv > 4096)
     return KDA_ERR_INVALID_ARG;
   if (D <= 0 || D > 1024 || rot <= 0 || rot > D || rot % 2 != 0) return KDA_ERR_INVALID_ARG;
-  if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_INVALID_ARG;
+  if ((dtype != KDA_BF16 && dtype != KDA_F32) || !isfinite(scale)) return KDA_ERR_INVALID_ARG;
   if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1)) return KDA_ERR_INVALID_ARG;
   if (!inv_freq || !q || !q_out || (Hkv > 0 && (!k || !k_out))) return KDA_ERR_INVALID_ARG;
   if (positions && cu_seqlens) return KDA_ERR_INVALID_ARG;

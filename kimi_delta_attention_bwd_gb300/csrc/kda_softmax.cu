@@ -297,7 +297,7 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   if (!p) return KDA_ERR_INVALID_ARG;
   if (p->B <= 0 || p->T <= 0 || p->Tk <= 0 || p->Hq <= 0 || p->Hkv <= 0) return KDA_ERR_INVALID_ARG;
   if (p->dtype != KDA_BF16 && p->dtype != KDA_F32) return KDA_ERR_INVALID_ARG;
-  if (p->causal != 0 && p->causal != 1) return KDA_ERR_INVALID_ARG;
+  if ((p->causal != 0 && p->causal != 1) || !isfinite(p->scale)) return KDA_ERR_INVALID_ARG;
   if (p->Hq > 4096 || p->Hq % p->Hkv != 0) return KDA_ERR_INVALID_ARG;
   const int64_t nq = (int64_t)p->B * p->T, nk = (int64_t)p->B * p->Tk;
   // (tile counts times heads fit a grid, and a tile's last row an int)

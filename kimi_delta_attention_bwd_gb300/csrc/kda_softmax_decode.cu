@@ -543,7 +543,7 @@ extern "C" KDA_API kda_status kda_softmax_decode(int n_seq, int cap, int Hq, int
                                                  const void* q, const void* k, const void* v, void* k_cache,
                                                  void* v_cache, const int32_t* lengths, void* o, void* workspace,
                                                  size_t workspace_bytes, cudaStream_t st) {
-  if (!sizes_ok(n_seq, cap, Hq, Hkv, dtype)) return KDA_ERR_INVALID_ARG;
+  if (!sizes_ok(n_seq, cap, Hq, Hkv, dtype) || !isfinite(scale)) return KDA_ERR_INVALID_ARG;
   if (!q || !k || !v || !k_cache || !v_cache || !lengths || !o) return KDA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return KDA_ERR_UNSUPPORTED;
   for (const void* x : {q, k, v, (const void*)k_cache, (const void*)v_cache, (const void*)o})

@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from . import _all_well, _apart, _dims, _lib, _require
+from . import _all_well, _apart, _dims, _lib, _positive, _require
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, scaling: str = "none",
@@ -66,8 +66,7 @@ def _rotate(inverse, q, k, inv_freq, positions, cu_seqlens, interleaved, scale, 
     rot = 2 * inv_freq.numel()
     if not 0 < rot <= D:
         raise ValueError(f"inv_freq of {rot // 2} pairs for heads of {D} values")
-    if not scale > 0:
-        raise ValueError(f"scale must be positive, got {scale}")
+    _positive(scale)
     io, i32 = q.dtype, torch.int32
     specs, names = [(q, qs, io), (inv_freq, inv_freq.shape, torch.float32)], ["q", "inv_freq"]
     Hkv = 0

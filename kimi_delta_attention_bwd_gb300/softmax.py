@@ -17,7 +17,7 @@ from typing import Optional
 
 import torch
 
-from . import _all_well, _apart, _dims, _lib, _require
+from . import _all_well, _apart, _dims, _lib, _positive, _require
 from .linear import _host_offsets
 
 
@@ -94,8 +94,8 @@ def kda_softmax_forward(q, k, v, scale: Optional[float] = None, causal: bool = T
         _apart("out", out, q=q, k=k, v=v, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k)
     if workspace is not None:
         _apart("workspace", workspace, q=q, k=k, v=v, out=out, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k)
-    if scale is not None and not scale > 0:
-        raise ValueError(f"scale must be positive, got {scale}")
+    if scale is not None:
+        _positive(scale)
     prob = _lib.make_softmax_problem(B, T, Tk, Hq, Hkv, D, io, scale, causal, cu_seqlens, cu_seqlens_k,
                                      cu_seqlens_host, cu_seqlens_k_host)
     stream, own = _lib._stream(), ()
@@ -177,8 +177,8 @@ def kda_softmax_decode_step(q, k, v, k_cache, v_cache, lengths, scale: Optional[
         _apart("out", out, q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, lengths=lengths)
     if workspace is not None:
         _apart("workspace", workspace, q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, lengths=lengths, out=out)
-    if scale is not None and not scale > 0:
-        raise ValueError(f"scale must be positive, got {scale}")
+    if scale is not None:
+        _positive(scale)
     if workspace is None:
         workspace = torch.empty(_lib.kda_softmax_decode_workspace_size(n, cap, Hq, Hkv, D) or 1, dtype=torch.uint8,
                                 device=q.device)

@@ -251,3 +251,40 @@ def test_python_rotary_refusals():
         kda.kda_rotary(q, k[:, :3], f)
     with pytest.raises(ValueError, match="out_k without k"):
         kda.kda_rotary(q, None, f, out_k=k)
+
+
+@pytest.mark.parametrize("scale", [1e-46, 1e-300, 0.0, -1.0, 1e39, math.inf, math.nan])
+def test_scales_that_are_not_positive_fp32_numbers_are_refused(scale):
+    """Positive in 64 bits is not enough: what vanishes in fp32 would select the default."""
+    q, k, f = torch.zeros(1, 4, 4, 64, device="meta"), torch.zeros(1, 4, 2, 64, device="meta"), torch.zeros(32)
+    with pytest.raises(ValueError, match="scale must be positive"):
+        kda._positive(scale)
+    with pytest.raises(ValueError, match="scale must be positive"):
+        kda.kda_rotary(q, k, f, scale=scale)
+    for s in (1e-38, 1e-45, 0.125, 3e38):
+        kda._positive(s)
+
+
+def test_scales_that_are_not_finite_are_refused_by_the_c_entries():
+    lib = _lib.load()
+    P = ctypes.c_void_p
+    for scale in (math.inf, -math.inf, math.nan):
+        p = _prob()
+        p.scale = scale
+        assert _fwd(p) == -1 and _bwd(p) == -1
+        assert lib.kda_softmax_decode(2, 8, 4, 2, 64, 0, scale, *[P(FAKE)] * 8, 1 << 40, None) == -1
+        assert lib.kda_rotary(4, 4, 2, 1, 64, 64, 0, 0, 0, scale, P(FAKE), None, None, 0, *[P(FAKE)] * 2,
+                              *[P(2 * FAKE)] * 2, None) == -1
+
+
+def test_softmax_scales_are_checked(monkeypatch):
+    """The calls refuse before anything is launched (tensors on the host that the device checks let pass)."""
+    from kimi_delta_attention_bwd_gb300 import softmax
+    monkeypatch.setattr(softmax, "_all_well", lambda *a: True)
+    q, k = torch.zeros(1, 4, 4, 64), torch.zeros(1, 4, 2, 64)
+    for scale in (1e-46, math.inf, -1.0):
+        with pytest.raises(ValueError, match="scale must be positive"):
+            kda.kda_softmax_forward(q, k, k, scale=scale)
+        with pytest.raises(ValueError, match="scale must be positive"):
+            kda.kda_softmax_decode_step(q[0], k[0], k[0], torch.zeros(4, 9, 2, 64), torch.zeros(4, 9, 2, 64),
+                                        torch.zeros(4, dtype=torch.int32), scale=scale)
