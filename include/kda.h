@@ -538,7 +538,9 @@ KDA_API kda_status kda_softmax_decode(int n_seq, int cap, int Hq, int Hkv, int D
  * other values pass.  inv_freq : [rot/2] fp32, taken as exact: the angle is
  * right to about 1e-7 of a turn at any int32 position.  Positions: positions
  * [n_tok] int32, or places in documents (cu_seqlens [n_docs + 1] int32 over the
- * tokens), or (both NULL) places in rows of T tokens.  q_out and k_out are q and
+ * tokens), or (both NULL) places in rows of T tokens.  Offsets that are not
+ * 0 = c0 <= c1 <= ... = n_tok leave NaN in the turned values of some tokens
+ * (there is no workspace to report them in).  q_out and k_out are q and
  * k (in place, both) or share no memory with them. */
 KDA_API kda_status kda_rotary(int64_t n_tok, int64_t T, int Hq, int Hkv, int D, int rot, int dtype,
                    int interleaved, int inverse, float scale, const float* inv_freq, const int32_t* positions,

@@ -74,6 +74,16 @@ __device__ __forceinline__ int64_t position_of(const RotP& P, int64_t tok) {
   return tok - P.cu[lo];
 }
 
+// Whether this CTA sees offsets that are no documents of the tokens: the first looks at both ends, and 256 offsets at a time
+// are shared out, so that wrong ones show in some tokens at least and most CTAs have none to look at.  (All CTAs with the ends
+// to look at: 16384 tokens of 8 and 8 heads of 64 17.7 -> 18.8 us.)
+__device__ __forceinline__ bool bad_offsets(const RotP& P) {
+  int bad = blockIdx.x == 0 && (P.cu[0] != 0 || P.cu[P.n_docs] != P.n_tok);
+  for (int64_t i = (int64_t)blockIdx.x * RT + threadIdx.x; i < P.n_docs; i += (int64_t)gridDim.x * RT)
+    bad |= P.cu[i + 1] < P.cu[i];
+  return __syncthreads_or(bad);
+}
+
 // VEC: 16-byte vectors divide the rows and (half) the turned halves or (interleaved) the turned part.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(RT) rotary_kernel(RotP P, const T* q, const T* k, T* oq, T* ok) {
@@ -82,6 +92,7 @@ __global__ void __launch_bounds__(RT) rotary_kernel(RotP P, const T* q, const T*
   const int half = P.rot / 2, H = P.Hq + P.Hkv;
   const int64_t t0 = (int64_t)blockIdx.x * P.per;
   const int nt = (int)(P.n_tok - t0 < P.per ? P.n_tok - t0 : P.per);
+  const bool bad = P.cu && (int64_t)blockIdx.x * RT < P.n_docs && bad_offsets(P);
   for (int i = threadIdx.x; i < nt * half; i += RT) {
     const int t = i / half, f = i - t * half;
     const float w = P.freq[f];
@@ -90,7 +101,7 @@ __global__ void __launch_bounds__(RT) rotary_kernel(RotP P, const T* q, const T*
     const uint64_t turn = (uint64_t)position_of(P, t0 + t) * __double2ull_rn(x * 18446744073709551616.0);
     float s, c;
     sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // in half turns: 2^-31
-    if (!isfinite(w)) s = c = __int_as_float(0x7fffffff);
+    if (!isfinite(w) || bad) s = c = __int_as_float(0x7fffffff);
     cs[i] = make_float2(c * P.scale, (P.inverse ? -s : s) * P.scale);
   }
   __syncthreads();

@@ -119,7 +119,8 @@ def kda_rotary(q, k, inv_freq, positions=None, cu_seqlens=None, interleaved: boo
     be None) by their positions: returns (q', k').  inv_freq [rot/2] fp32
     (rotary_frequencies; rot <= D, the other values pass) is taken as exact.
     positions int32 [B, T] (or [n]); else places in the documents of cu_seqlens
-    (int32 [n_docs + 1] over the flattened tokens), else places in the rows.
+    (int32 [n_docs + 1] over the flattened tokens; offsets that are not ascending
+    from 0 to the tokens' number leave NaN in some tokens), else places in the rows.
     out_q and out_k may be q and k (in place, both), else they share no memory
     with the inputs."""
     return _rotate(False, q, k, inv_freq, positions, cu_seqlens, interleaved, scale, out_q, out_k)

@@ -133,3 +133,31 @@ def test_graph_replay():
     graph.replay()
     c, d = kda.kda_rotary(q, k, f, positions=pos)
     assert torch.equal(a, c) and torch.equal(b, d)
+
+
+@pytest.mark.parametrize("off", [[0, 80, 70], [1, 30, 70], [0, 30, 71], [0, 30, 69], [0, -5, 70], [0, 71, 70], [70, 0]])
+def test_wrong_offsets_show(off):
+    f, _ = kda.rotary_frequencies(32)
+    q, k = draw(17, 1, 70, 2, 64, dt="bf16"), draw(18, 1, 70, 1, 64, dt="bf16")
+    cu = torch.tensor(off, dtype=torch.int32, device="cuda")
+    for call in (kda.kda_rotary, kda.kda_rotary_backward):
+        a, b = call(q, k, f, cu_seqlens=cu)
+        nan = torch.isnan(a[:, :, 0, :32])
+        assert nan.any() and torch.equal(nan, torch.isnan(b[:, :, 0, :32]))
+        assert torch.equal(a[..., 32:], q[..., 32:]) and torch.equal(b[..., 32:], k[..., 32:])
+
+
+@pytest.mark.parametrize("n_docs,tokens", [(5000, 5000), (5000, 40), (40, 5000), (3, 1)])
+def test_one_wrong_offset_among_many_shows(n_docs, tokens):
+    """Wherever it stands: between documents that no token's own search comes to."""
+    f, _ = kda.rotary_frequencies(8)
+    q = draw(19, 1, tokens, 1, 8, dt="f32")
+    r = np.random.RandomState(20)
+    good = np.sort(r.randint(0, tokens + 1, n_docs + 1)).astype(np.int32)
+    good[0], good[-1] = 0, tokens
+    assert torch.isfinite(kda.kda_rotary(q, None, f, cu_seqlens=torch.from_numpy(good).cuda())[0]).all()
+    for at in {1, n_docs // 2, n_docs - 1}:
+        for wrong in (tokens + 1, -1):
+            cu = good.copy()
+            cu[at] = wrong
+            assert torch.isnan(kda.kda_rotary(q, None, f, cu_seqlens=torch.from_numpy(cu).cuda())[0]).any(), (at, wrong)
