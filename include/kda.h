@@ -517,7 +517,9 @@ KDA_API kda_status kda_softmax_bwd(const kda_softmax_problem* p, const void* q, 
  * k_cache, v_cache [n_seq, cap, Hkv, D] in dtype, lengths [n_seq] DEVICE int32: the
  * tokens in each cache before the step.  k and v are written to place
  * lengths[i] of sequence i's cache and the query sees places 0 .. lengths[i]; places
- * behind it are neither read nor written.  lengths[i] < 0: the sequence
+ * behind it are not written, and what they hold, NaN included, reaches no result; bf16
+ * blocks of 64 places may read up to 63 of them, so that writing them on another stream
+ * meanwhile is a race.  lengths[i] < 0: the sequence
  * takes no step (a padded batch): its cache is left alone and its o is 0.
  * lengths[i] >= cap: the same, and kda_device_status of the workspace reports
  * KDA_ERR_BAD_SEQLENS.  The lengths are not advanced (the layers of a model share them).

@@ -142,6 +142,8 @@ def kda_softmax_decode_step(q, k, v, k_cache, v_cache, lengths, scale: Optional[
     [n, cap, Hkv, D] (one dtype), lengths [n] int32 on the device: the tokens in
     each cache.  k and v are written behind them, in place, and the query sees
     them all and its own; lengths stays as it is (the layers of a model share it).
+    What places behind them hold reaches no result, but bf16 caches are read up to 63
+    places further: nothing else writes there meanwhile.
     A negative length takes no step (o = 0, a padded batch), and neither does one
     of cap or more (kda_device_status of a given workspace reports it).  out shares
     no memory with the inputs, nor do the caches with each other or with the other
