@@ -839,3 +839,59 @@ def test_outputs_and_workspaces_that_overlap_are_refused():
         with pytest.raises(ValueError, match=match):
             step(**kw)
     step(q=wide[:256].view_as(t["q"]), workspace=ws[:size])
+
+
+def test_a_hybrid_block_s_gradients_are_its_slopes():
+    """Norm, a linear-attention layer and a softmax-attention layer with rotary positions on packed documents: the
+    difference along each leaf's own gradient is the gradient's norm.  (The loss is a sum in 64 bits of 38400 terms of about
+    1 that are off by a few 2^-21 each, about 1e-4 together; h |g| is above 0.02 for every leaf, so that noise is below 0.5%
+    of the difference, and the h^2 of a third derivative, with h 0.2% of the leaf, smaller: 2% allows for both.  A gradient
+    of the wrong sign is off by 200%, one of another direction by 100%.)"""
+    torch.manual_seed(26)
+    B, T, Hq, Hkv, D = 1, 150, 4, 2, 64
+    cu = torch.tensor([0, 60, 61, 150], dtype=torch.int32, device="cuda")
+    f, _ = kda.rotary_frequencies(D)
+    x = torch.randn(B, T, Hq * D, device="cuda")
+    shapes = dict(w=(Hq * D,), wq=(Hq * D, Hq * D), wk=(Hq * D, Hkv * D), wv=(Hq * D, Hkv * D))
+    leaves = {n: (torch.randn(*s, device="cuda") / (Hq * D) ** 0.5).requires_grad_() for n, s in shapes.items()}
+    leaves["A"] = torch.linspace(-4.0, -1.0, Hq, device="cuda").requires_grad_()
+    up = torch.randn(B, T, Hq, D, device="cuda")
+
+    def block(p):
+        y = kda.layer_norm(x, 1 + p["w"])
+        h = y.view(B, T, Hq, D)
+        y = y + kda.linear_attention(h, h, h, p["A"], cu_seqlens=cu).reshape(B, T, Hq * D) * 0.1
+        q, k, v = ((y @ p[n]).view(B, T, -1, D) for n in ("wq", "wk", "wv"))
+        q, k = kda.rotary(q, k, f, cu_seqlens=cu)
+        return (kda.softmax_attention(q, k, v, cu_seqlens=cu).double() * up).sum()
+    names = list(leaves)
+    for n, g in zip(names, torch.autograd.grad(block(leaves), [leaves[n] for n in names])):
+        with torch.no_grad():
+            size = float(g.double().norm())
+            h = 2e-3 * float(leaves[n].norm())
+            assert h * size > 0.02, (n, h, size)
+            p, m = ({**leaves, n: leaves[n] + s * h / size * g} for s in (1, -1))
+            num = float(block(p) - block(m)) / (2 * h)
+        assert abs(num - size) <= 2e-2 * size, (n, num, size)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_linear_attention_s_backward_reads_no_offsets_either(dt):
+    """The forward's table holds its documents: offsets overwritten, or made and dropped by a checkpointed step."""
+    from torch.utils.checkpoint import checkpoint
+    g = torch.Generator().manual_seed(75)
+    off = torch.tensor([0, 700, 701, 1001], dtype=torch.int32)
+    q, k, v, dO = (torch.randn(1, 1001, 2, 64, generator=g).to(DT[dt]).cuda() for _ in range(4))
+    A = torch.tensor([-3.0, -1.0], device="cuda")
+    args = [t.requires_grad_() for t in (q, k, v, A)]
+    cu = off.cuda()
+    want = torch.autograd.grad(kda.linear_attention(*args, cu_seqlens=cu), args, dO)
+    _, _, ctx = kda.kda_linear_forward(*(t.detach() for t in args), cu_seqlens=cu)
+    cu.copy_(torch.tensor([0, 3, 500, 1001], dtype=torch.int32))
+    for a, b in zip(kda.kda_linear_backward(ctx, dO, want_dh0=False).values(), want):
+        assert torch.equal(a, b)
+    o = checkpoint(lambda *a: kda.linear_attention(*a, cu_seqlens=off.cuda()), *args, use_reentrant=False)
+    others = [torch.tensor([0, 3, 500, 1001], dtype=torch.int32, device="cuda") for _ in range(64)]
+    for a, b in zip(torch.autograd.grad(o, args, dO), want):
+        assert torch.equal(a, b)
+    assert len(others) == 64
