@@ -133,6 +133,8 @@ def _apart(name, out, may_be=(), /, **inputs):
 def _positive(scale, name="scale"):
     """A given factor is a positive fp32 number: the C interface takes one, and one that vanishes there would
     select the default."""
+    if 1e-30 < scale < 1e30:  # (for the calls whose time is the host's)
+        return
     if not 0.0 < ctypes.c_float(scale).value < math.inf:
         raise ValueError(f"{name} must be positive and finite in fp32, got {scale}")
 

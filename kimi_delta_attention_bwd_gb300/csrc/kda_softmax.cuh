@@ -1,6 +1,6 @@
-// Softmax attention with grouped heads: declarations shared by its kernels
-// (tables and entries: kda_softmax.cu, tensor cores: kda_softmax_tc.cu, fp32
-// pipe: kda_softmax_f32.cu).
+// Softmax attention with grouped heads: declarations shared by its kernels, all
+// on the tensor cores (tables and entries: kda_softmax.cu, forward and backward:
+// kda_softmax_tc.cu, the backward of fp32 io at D = 128: kda_softmax_f32.cu).
 #pragma once
 #include "kda_internal.cuh"
 #include "../../include/kda.h"

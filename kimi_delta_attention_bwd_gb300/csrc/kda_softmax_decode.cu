@@ -466,9 +466,12 @@ __global__ void __launch_bounds__(JW * 32) smx_join_kernel(DecP P, T* __restrict
   }
 }
 
-// Pieces of a sequence, none of fewer than 128 keys of a full cache: for one sequence a CTA for each of 152 SMs
-// (131072 places of 4 key heads: 49 us, with two 50, three 54); several sequences differ in length, and smaller
-// pieces even that out (16 of up to 16384 places: 68 us with four CTAs per SM, 71 with eight).
+// Pieces of a sequence, none of fewer than 128 keys of a full cache: for one sequence a CTA for each of 152 SMs, for several
+// four, since they differ in length and smaller pieces even that out.  Both sides, 16 heads on 4 of 128, one CTA an SM and four
+// (as graphs): one of 131072 places 51.7 and 60.3 us, a quarter full 22.4 and 28.6; two of 65536, full, 51.3 and 58.1, of
+// uneven lengths 47.7 and 46.1; four of 32768 54.6 and 57.8, uneven 48.4 and 40.2; 16 of 16384 89.5 and 101, uneven 73.9 and
+// 56.7; 64 of up to 8192 109 and 100.  Equal lengths lose up to 13% by the rule, uneven ones up to 30% by the other; lengths
+// are known on the device alone.
 int pieces(int n, int64_t units, int cap) {
   const int64_t want = ((n == 1 ? 1 : 4) * 152 + units - 1) / units, most = ((int64_t)cap + 127) / 128;
   const int64_t ns = want < most ? want : most;

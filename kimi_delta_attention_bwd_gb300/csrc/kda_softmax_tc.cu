@@ -1,4 +1,5 @@
-// Softmax attention for bf16 io on the 5th-generation tensor cores (tcgen05, accumulators in tensor memory).
+// Softmax attention on the 5th-generation tensor cores (tcgen05, accumulators in tensor memory): bf16 io, and fp32 io as
+// three bf16 parts of every value (kda_softmax_tc.cuh) but for its backward at D = 128 (kda_softmax_f32.cu).
 //
 // Forward, per CTA: 256 queries of one head as two tiles of 128 over the keys in blocks of 128.  One warp loads
 // (TMA, a ring of key and value blocks), one issues the products, and per tile four warps, a thread a row,
@@ -492,7 +493,8 @@ __device__ __forceinline__ void put_dq(float (&v)[H][32], uint32_t to, uint32_t 
 //
 // Both kernels keep two blocks of their own (dq with bf16 io one) and two rings: A, of the blocks that a first product and then the last one
 // reads (q for dk and dv, k for dq), and B, of those that are free earlier (dO, v).
-// The other side's blocks have XB rows: 128, and eight warps for the pairs, at D = 128; at D = 64 half of both, and two
+// The other side's blocks have XB rows: 128, and eight warps for the pairs, at D = 128; at D = 64 half of both (dk and dv
+// keep the eight), and two
 // CTAs per SM.
 template <int D, int PARTS>
 struct Bwd {
@@ -687,7 +689,7 @@ smx_tc_dkv_kernel(SmxP P, const __grid_constant__ CUtensorMap mq, const __grid_c
       commit(&B.drain, me);
       for (int it = 0; it < mma::WAIT_POLLS && !mma::mbar_try(&B.drain, 0); it++) {}
     }
-  } else if (warp < EW && live) {  // weights and their gradients: a thread a key, 64 of a block's queries
+  } else if (warp < EW && live) {  // weights and their gradients: a thread a key, 32 H of a block's queries
     const int half = warp / 4, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     constexpr int W = 32 * H;  // a thread's columns of a block's pairs
