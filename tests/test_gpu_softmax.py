@@ -895,3 +895,39 @@ def test_linear_attention_s_backward_reads_no_offsets_either(dt):
     for a, b in zip(torch.autograd.grad(o, args, dO), want):
         assert torch.equal(a, b)
     assert len(others) == 64
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lq,lk,rows,causal", [([3000], [40], True, False), ([2500], [100], True, True), ([1500] * 2, [130] * 2, True, False),
+                                               ([2000, 0, 700], [64, 5, 129], False, False), ([4000, 3], [1, 5], False, True)])
+def test_many_queries_on_few_keys(dt, D, lq, lk, rows, causal):
+    """Only the keys' tiles are cut: the forward's table launch has lists of the backward alone.  Two backwards of one
+    forward give the same bits."""
+    x = make(76, lq, lk, 4, 1, D, dt, rows=rows)
+    check(run(x, causal), oracle(x, causal), dt, D, x)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO", "cu", "cu_k")}
+    kw = {} if rows else dict(cu_seqlens=d["cu"], cu_seqlens_k=d["cu_k"])
+    ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"], causal=causal, **kw)[2]
+    one, two = kda.kda_softmax_backward(ctx, d["dO"]), kda.kda_softmax_backward(ctx, d["dO"])
+    for n in one:
+        assert torch.equal(one[n], two[n]), n
+
+
+@pytest.mark.parametrize("rows", [False, True])
+def test_a_forward_that_saves_nothing_takes_the_workspace(rows):
+    """A saving forward's workspace, used by one that does not save: the first one's backward is refused."""
+    x = make(77, [600, 600], [600, 600], 4, 2, 64, "bf16", rows=rows)
+    d = {n: x[n].cuda() for n in ("q", "k", "v", "dO", "cu")}
+    kw = {} if rows else dict(cu_seqlens=d["cu"])
+    ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"], **kw)[2]
+    kda.kda_softmax_forward(d["q"], d["k"], d["v"], save_for_backward=False, workspace=ctx.workspace, **kw)
+    for n, g in kda.kda_softmax_backward(ctx, d["dO"]).items():
+        assert torch.isnan(g).all(), n
+    assert kda.kda_device_status(ctx.workspace) == -5
+    # and a saving one serves again
+    _, _, ctx = kda.kda_softmax_forward(d["q"], d["k"], d["v"], workspace=ctx.workspace, **kw)
+    want = run(x)
+    for n, g in kda.kda_softmax_backward(ctx, d["dO"]).items():
+        assert torch.equal(g, want[n]), n
+    assert kda.kda_device_status(ctx.workspace) == 0
