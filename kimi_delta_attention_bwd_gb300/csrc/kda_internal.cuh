@@ -13,6 +13,9 @@
 namespace kda {
 
 constexpr int C = 64;          // chunk length (tokens)
+// SMs of a GB300.  Rules that workspaces or the order of sums follow go by it and not by the device: a size is asked for
+// without one, and a result's bits are the same on each.
+constexpr int SMS = 152;
 constexpr float L2_EPS = 1e-6f; // q/k L2-norm epsilon
 
 // Kernel ids for the per-kernel timing brackets.

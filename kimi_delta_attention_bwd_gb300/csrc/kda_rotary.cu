@@ -206,7 +206,7 @@ extern "C" KDA_API kda_status kda_rotary(int64_t n_tok, int64_t T, int Hq, int H
   P.freq = inv_freq;
   P.pos = positions;
   P.cu = cu_seqlens;
-  P.per = n_tok >= 8 * 152 ? 4 : 1;
+  P.per = n_tok >= 8 * SMS ? 4 : 1;
   const cudaError_t e = dtype == KDA_BF16 ? launch<bf16>(P, q, k, q_out, k_out, st)
                                           : launch<float>(P, q, k, q_out, k_out, st);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

@@ -337,7 +337,7 @@ kda_status check(const kda_softmax_problem* p, SmxP* out) {
   // Cut tiles: where whole tiles would be fewer than four for each of 152 SMs, and some could have more than a few
   // blocks; a CTA's load is the average of one CTA per SM (half of that, at D = 64 with its two CTAs, cut tiles of the
   // packed 300M step whose join took what it gave; twice as many pieces for either head dim lost 3 to 10%).
-  const int wave = 152;
+  const int wave = SMS;
   for (int l = 0; l < 3; l++) {
     const int H = l == 2 ? P.Hkv : P.Hq, other = l == 2 ? (P.rows ? P.T : P.Nq) : P.rows ? P.Tk : P.Nk;
     P.xb[l] = tc_block(p->D, parts, l);
@@ -416,7 +416,7 @@ cudaError_t launch_delta(const SmxP& P, const void* o, const void* dO, void* dq,
 template <int D, typename T>
 cudaError_t launch_join_grads(const SmxP& P, void* dq, void* dk, void* dv, cudaStream_t st) {
   prof_begin(K_SMX_JOIN_GRADS, st);
-  const cudaError_t e = launch_pdl(smx_join_grads_kernel<D, T>, dim3(4 * 152, P.target[2] ? 3 : 1), dim3(256), 0, st, P,
+  const cudaError_t e = launch_pdl(smx_join_grads_kernel<D, T>, dim3(4 * SMS, P.target[2] ? 3 : 1), dim3(256), 0, st, P,
                                    (T*)dq, (T*)dk, (T*)dv);
   prof_end(K_SMX_JOIN_GRADS, st);
   return e;
@@ -425,7 +425,7 @@ cudaError_t launch_join_grads(const SmxP& P, void* dq, void* dk, void* dv, cudaS
 template <int D, typename T>
 cudaError_t launch_join(const SmxP& P, void* o, float* lse, cudaStream_t st) {
   const int64_t most = (int64_t)(P.pieces[0] / 2) * P.Hq * (P.tile[0] / 8);  // (a cut tile has two pieces at least)
-  const int64_t grid = most < 8 * 152 ? most : 8 * 152;
+  const int64_t grid = most < 8 * SMS ? most : 8 * SMS;
   prof_begin(K_SMX_JOIN_ROWS, st);
   const cudaError_t e = launch_pdl(smx_join_rows_kernel<D, T>, dim3((unsigned)grid), dim3(256), 0, st, P, (T*)o, lse);
   prof_end(K_SMX_JOIN_ROWS, st);

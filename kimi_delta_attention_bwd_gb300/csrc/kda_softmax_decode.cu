@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(JW * 32) smx_join_kernel(DecP P, T* __restrict
 // 56.7; 64 of up to 8192 109 and 100.  Equal lengths lose up to 13% by the rule, uneven ones up to 30% by the other; lengths
 // are known on the device alone.
 int pieces(int n, int64_t units, int cap) {
-  const int64_t want = ((n == 1 ? 1 : 4) * 152 + units - 1) / units, most = ((int64_t)cap + 127) / 128;
+  const int64_t want = ((n == 1 ? 1 : 4) * SMS + units - 1) / units, most = ((int64_t)cap + 127) / 128;
   const int64_t ns = want < most ? want : most;
   return (int)(ns < 1 ? 1 : ns);
 }

@@ -31,7 +31,7 @@ int main() {
     const auto& own = by_key ? cuk : cu;
     for (int i = 0; i < n; i++) pre[i + 1] = pre[i] + (own[i + 1] - own[i] + tile - 1) / tile;
     const Tiles t{cu.data(), cuk.data(), pre.data(), n, tile, xb, Hq / Hkv, causal, by_key != 0};
-    const int H = by_key ? Hkv : Hq, target = 152;
+    const int H = by_key ? Hkv : Hq, target = kda::SMS;
     const int64_t blocks = t.blocks(0, pre[n], 1), per = piece_blocks(blocks, H, target, xb);
     int64_t pieces = 0, empty = 0, shares = 0;
     for (int s = 0; s < 1024; s++) shares += t.blocks(s, pre[n], 1024);  // (as the kernel's threads take them)
