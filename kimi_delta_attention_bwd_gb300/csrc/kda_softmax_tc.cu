@@ -494,8 +494,7 @@ __device__ __forceinline__ void put_dq(float (&v)[H][32], uint32_t to, uint32_t 
 // Both kernels keep two blocks of their own (dq with bf16 io one) and two rings: A, of the blocks that a first product and then the last one
 // reads (q for dk and dv, k for dq), and B, of those that are free earlier (dO, v).
 // The other side's blocks have XB rows: 128, and eight warps for the pairs, at D = 128; at D = 64 half of both (dk and dv
-// keep the eight), and two
-// CTAs per SM.
+// keep the eight), and two CTAs per SM.
 template <int D, int PARTS>
 struct Bwd {
   static_assert(PARTS == 1 || D == 64, "at D = 128 three parts of both own blocks leave no room: kda_softmax_f32.cu");
